@@ -87,7 +87,27 @@ enum {
   TFPA_ELANEMEM = -6     /* the page pool cannot hold the claim now: wait     */
 };
 
-typedef enum { TFPA_BF16 = 0, TFPA_FP8_E4M3 = 1 } tfpa_kv_dtype;
+typedef enum { TFPA_BF16 = 0, TFPA_FP8_E4M3 = 1, TFPA_FP4_E2M1 = 2 } tfpa_kv_dtype;
+
+/* A 4-bit cache (TFPA_FP4_E2M1): each value is an e2m1 code (0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 and their negatives) times the e4m3 scale of its 16 head dims
+ * times k_scale[g] / v_scale[g]: 72 bytes a row and kv head, K or V.  Where
+ * the layouts above say [256][128] elements, a page of one kv head is one
+ * block of TFPA_FP4_BLOCK bytes: two half-blocks of 128 positions, each
+ * [128][64] bytes of codes (byte i of a row: dim 2i in the low nibble, 2i + 1
+ * in the high one) and then [128][8] scale bytes.  So a pool is
+ * [num_pages][hkv][TFPA_FP4_BLOCK] bytes and a slab
+ * [hkv][slab_cap / 256][TFPA_FP4_BLOCK].
+ *   Store (tfpa_write_kv, tfpa_write_kv_rope, tfpa_decode_append): with x the
+ * value in float32 (a NaN counts as 0), each product and quotient rounded to
+ * float32, block scale = e4m3(max |x| / (6 k_scale[g])) and code =
+ * e2m1(x / (scale k_scale[g])), both rounded to nearest even and saturating;
+ * a block whose scale rounds to 0 holds zeros.  k_scale[g] = max |x| / 2688
+ * over a head's values uses the scales' whole range.  The stored form has no
+ * NaN and no infinity.
+ *   A save / restore image holds all rows' codes, [K, V][hkv][p1 - p0][64]
+ * bytes, and then all rows' scales, [K, V][hkv][p1 - p0][8]. */
+#define TFPA_FP4_BLOCK 18432
 
 /* One stream (a segment of the call). */
 typedef struct {
@@ -106,7 +126,7 @@ typedef struct {
   void* k_pool;                   /* DEVICE [num_pages][hkv][256][128], 1024-byte aligned;  */
   void* v_pool;                   /*   may be NULL when no segment is paged                 */
   int32_t num_pages;
-  const float* k_scale;           /* DEVICE float[hkv], fp8 only: value = e4m3 * scale      */
+  const float* k_scale;           /* DEVICE float[hkv], fp8: value = e4m3 * scale; fp4: see above */
   const float* v_scale;
   int32_t* err_flag;              /* optional DEVICE int32: OR-ed with 1 on a bad page id,
                                      4 on a rotary position outside the table */
@@ -244,11 +264,22 @@ int tfpa_row_splits(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
  * "What changes"): row r's K and V for every kv head go to position
  * row_pos[r] of segment row_seg[r], through its page table or slab.  bf16
  * caches copy the bits; fp8 caches store e4m3(RNE, saturating) of
- * float32(x) / scale[g].  row_seg/row_pos are HOST int32[rows]. */
+ * float32(x) / scale[g]; fp4 caches: see TFPA_FP4_BLOCK.  row_seg/row_pos are HOST int32[rows]. */
 int tfpa_write_kv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
                   const void* k_rows, const void* v_rows,
                   const int32_t* row_seg, const int32_t* row_pos, int32_t rows,
                   cudaStream_t stream);
+
+/* KV read: the stored K and V of row_pos[r] of segment row_seg[r], every kv
+ * head, as bf16 into k_rows / v_rows (DEVICE bf16 [rows][hkv][128], 16-byte
+ * aligned): the inverse of tfpa_write_kv.  bf16 caches copy the bits; fp8
+ * values are e4m3 * scale[g] and fp4 values (code * block scale) * scale[g],
+ * the product rounded to float32 and then to bf16.  A row on a page whose id
+ * is out of range is left unwritten and ORs 1 into cache->err_flag.  Errors
+ * as tfpa_write_kv. */
+int tfpa_read_kv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg, void* k_rows,
+                 void* v_rows, const int32_t* row_seg, const int32_t* row_pos, int32_t rows,
+                 cudaStream_t stream);
 
 /* Decode/verify split-K partials (Issue #1344, "Mechanism": the partial
  * kernels write pm/pl/po, then attn_merge).  For each row r < rows, head h
@@ -471,7 +502,7 @@ typedef struct {
   int32_t kind;          /* 0 write_kv, 1 decode partial, 2 merge, 3 prefill, 4 keep,
                             5 stage pages, 6 save, 7 restore, 8 verify (decode or tree
                             rows of runs with 49 or more query vectors per kv head, on
-                            tensor cores; items = tiles) */
+                            tensor cores; items = tiles), 9 read_kv */
   int32_t row0;          /* first row of the call this launch covers */
   int32_t rows;          /* rows it covers */
   int32_t runs;          /* row groups (segment, consecutive positions) */

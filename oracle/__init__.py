@@ -25,6 +25,8 @@ page title and section:
 Modules:
   e4m3       OCP FP8 E4M3 ("fn") decode table and round-to-nearest-even,
              saturating encoder.
+  fp4        the 4-bit cache: e2m1 codes under e4m3 block scales, its rows
+             and their addresses.
   kvcache    the physical cache (page pool or slab) and the KV row write.
   attention  one-pass softmax attention per (row, head), split partials and
              their log-sum-exp merge.
@@ -33,4 +35,4 @@ Parity status: every function is pinned by a ``-m "not gpu"`` test in
 ``tests/test_oracle_*.py``; none is "parity unpinned".
 """
 
-from . import e4m3, kvcache, attention  # noqa: F401
+from . import e4m3, fp4, kvcache, attention  # noqa: F401

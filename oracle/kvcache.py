@@ -22,7 +22,7 @@ from typing import List, Optional
 
 import numpy as np
 
-from . import e4m3
+from . import e4m3, fp4
 
 PAGE = 256
 
@@ -41,7 +41,7 @@ def bf16_to_f32(bits: np.ndarray) -> np.ndarray:
 @dataclass
 class Cache:
     """One layer's KV storage: page pools (may be None if unused) and scales."""
-    dtype: str                      # "bf16" or "fp8"
+    dtype: str                      # "bf16" or "fp8" ("fp4": see fp4.py)
     hkv: int
     d: int
     k_pool: Optional[np.ndarray]    # [num_pages][hkv][256][d]
@@ -102,6 +102,8 @@ def _rows_of(arr, page_table, g, n):
 
 def gather(cache: Cache, seg: Segment, g: int, n: int):
     """K and V of kv head ``g`` at positions 0..n-1, dequantised to float64."""
+    if cache.dtype == "fp4":
+        return fp4.gather(cache, seg, g, n)
     if seg.page_table is not None:
         k_raw = _rows_of(cache.k_pool, seg.page_table, g, n)
         v_raw = _rows_of(cache.v_pool, seg.page_table, g, n)

@@ -20,7 +20,9 @@ LIB_PATH = os.path.join(_PKG, "libtfpa.so")
 PAGE = 256
 HEAD_DIM = 128
 MAX_SPLITS = 32
-BF16, FP8_E4M3 = 0, 1
+BF16, FP8_E4M3, FP4_E2M1 = 0, 1, 2
+KV_DTYPES = {"bf16": BF16, "fp8": FP8_E4M3, "fp4": FP4_E2M1}
+FP4_BLOCK = 18432          # bytes of a page of one kv head of a 4-bit cache
 
 TFPA_OK, TFPA_EINVAL, TFPA_ERANGE, TFPA_ECAPACITY, TFPA_ECUDA, TFPA_EDEVICE = 0, -1, -2, -3, -4, -5
 TFPA_ELANEMEM = -6
@@ -34,7 +36,7 @@ EXPORTS = ("tfpa_pages_per_split", "tfpa_num_splits", "tfpa_write_kv", "tfpa_dec
            "tfpa_plan_destroy", "tfpa_plan_clear", "tfpa_plan_launches", "tfpa_plan_write_kv",
            "tfpa_plan_decode", "tfpa_plan_launch", "tfpa_plan_set_device", "tfpa_plan_dyn_bytes",
            "tfpa_plan_dyn_pack", "tfpa_plan_shape", "tfpa_plan_capture", "tfpa_plan_replay",
-           "tfpa_decode_append", "tfpa_plan_decode_append", "tfpa_row_splits")
+           "tfpa_decode_append", "tfpa_plan_decode_append", "tfpa_row_splits", "tfpa_read_kv")
 
 
 class TfpaError(RuntimeError):
@@ -75,7 +77,7 @@ class tfpa_launch_record(ctypes.Structure):
 
 HOOK = ctypes.CFUNCTYPE(None, ctypes.POINTER(tfpa_launch_record), ctypes.c_void_p)
 KINDS = {0: "write_kv", 1: "partial", 2: "merge", 3: "prefill", 4: "keep", 5: "stage",
-         6: "save", 7: "restore", 8: "verify"}
+         6: "save", 7: "restore", 8: "verify", 9: "read_kv"}
 
 _lib = None
 
@@ -95,6 +97,8 @@ def lib():
         L.tfpa_num_splits.restype = i32
         L.tfpa_write_kv.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, vp, vp, vp, vp, i32, vp]
         L.tfpa_write_kv.restype = ctypes.c_int
+        L.tfpa_read_kv.argtypes = L.tfpa_write_kv.argtypes
+        L.tfpa_read_kv.restype = ctypes.c_int
         L.tfpa_decode_partial.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, vp, vp, vp, i32,
                                           ctypes.c_float, P(tfpa_scratch), vp]
         L.tfpa_decode_partial.restype = ctypes.c_int
@@ -239,18 +243,18 @@ class _Cached:
 @dataclass(eq=False)
 class Cache(_Cached):
     """One layer's KV cache; holds the tensors so their memory stays alive."""
-    dtype: str                    # "bf16" or "fp8"
+    dtype: str                    # "bf16", "fp8" or "fp4"
     hq: int
     hkv: int
-    k_pool: object = None         # [num_pages][hkv][256][128] bf16 (or int16) / uint8
-    v_pool: object = None
-    k_scale: object = None        # float32 [hkv] (fp8)
+    k_pool: object = None         # [num_pages][hkv][256][128] bf16 (or int16) / uint8;
+    v_pool: object = None         #   fp4: uint8 [num_pages][hkv][FP4_BLOCK]
+    k_scale: object = None        # float32 [hkv] (fp8, fp4)
     v_scale: object = None
     err_flag: object = None       # int32 [1]
     num_pages: int = 0
 
     def _make_c(self) -> tfpa_cache:
-        return tfpa_cache(BF16 if self.dtype == "bf16" else FP8_E4M3, self.hq, self.hkv,
+        return tfpa_cache(KV_DTYPES.get(self.dtype, FP8_E4M3), self.hq, self.hkv,
                           HEAD_DIM, _ptr(self.k_pool), _ptr(self.v_pool), self.num_pages,
                           _ptr(self.k_scale), _ptr(self.v_scale), _ptr(self.err_flag))
 
@@ -350,6 +354,16 @@ def tfpa_write_kv(cache: Cache, segs: Sequence[Seg], k_rows, v_rows, row_seg, ro
     cc = cache.c()
     _check(lib().tfpa_write_kv(ctypes.byref(cc), cs, n, _ptr(k_rows), _ptr(v_rows), _ptr(rs),
                                _ptr(rp), len(rs), _stream(stream)), "tfpa_write_kv")
+
+
+def tfpa_read_kv(cache: Cache, segs: Sequence[Seg], k_rows, v_rows, row_seg, row_pos,
+                 stream=None) -> None:
+    """The rows' stored K and V as bf16 into k_rows / v_rows ([rows][hkv][128])."""
+    cs, n = _segs(segs)
+    rs, rp = _i32(row_seg), _i32(row_pos)
+    cc = cache.c()
+    _check(lib().tfpa_read_kv(ctypes.byref(cc), cs, n, _ptr(k_rows), _ptr(v_rows), _ptr(rs),
+                              _ptr(rp), len(rs), _stream(stream)), "tfpa_read_kv")
 
 
 def tfpa_decode_partial(cache: Cache, segs: Sequence[Seg], q, row_seg, row_pos, softmax_scale,

@@ -6,6 +6,7 @@
 // pinned host image sits behind NVLink-C2C, so the save is one kernel that
 // streams every (page, kv head) block straight to it.
 #include "common.cuh"
+#include "kvstore.cuh"
 #include "params.h"
 
 namespace tfpa {
@@ -42,6 +43,24 @@ __global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ CopyP
                                         row * p.row_bytes);
   uint4* img = reinterpret_cast<uint4*>(
       p.image + (((size_t)which * p.hkv + g) * (p.p1 - p.p0) + (lo - p.p0)) * p.row_bytes);
+  if (p.row_bytes == kFp4CodeBytes + kFp4ScaleBytes) {
+    // 4-bit rows: in each half-block the codes of the rows, then the scales;
+    // the image holds all planes' codes and then all planes' scales
+    const size_t n = p.p1 - p.p0, plane = (size_t)which * p.hkv + g;
+    uint8_t* base = static_cast<uint8_t*>(which ? p.v_base : p.k_base);
+    uint4* icodes = reinterpret_cast<uint4*>(p.image + (plane * n + (lo - p.p0)) * kFp4CodeBytes);
+    uint2* iscales = reinterpret_cast<uint2*>(p.image + 2 * p.hkv * n * kFp4CodeBytes) +
+                     plane * n + (lo - p.p0);
+    for (int i = threadIdx.x; i < (hi - lo) * 4; i += 256) {
+      uint4* d = reinterpret_cast<uint4*>(base + fp4_codes(row + (i >> 2))) + (i & 3);
+      if (p.restore) *d = icodes[i]; else icodes[i] = *d;
+    }
+    for (int i = threadIdx.x; i < hi - lo; i += 256) {
+      uint2* d = reinterpret_cast<uint2*>(base + fp4_scales(row + i));
+      if (p.restore) *d = iscales[i]; else iscales[i] = *d;
+    }
+    return;
+  }
   const uint4* src = p.restore ? img : dev;
   uint4* dst = p.restore ? dev : img;
   const int n = (hi - lo) * p.row_bytes / 16;

@@ -13,8 +13,8 @@
 //               of three 64 KB key chunks (bf16: a chunk is one stage;
 //               e4m3: two stages, read by consumer warps 0-3 and 4-7);
 //   warps 0..7  consumers: each takes an eighth of every chunk's keys, runs
-//               QK^T and PV on mma.sync m16n8k16 (bf16, or f16 for e4m3
-//               caches, whose bytes convert to f16 exactly) and an online
+//               QK^T and PV on mma.sync m16n8k16 (bf16, or f16 for e4m3 and
+//               4-bit caches, whose values convert to f16 exactly) and an online
 //               softmax reduced with warp shuffles; at the end of an item
 //               each warp stores its state (O, m, l) into tensor memory and
 //               goes straight on to the next item;
@@ -36,10 +36,11 @@
 namespace tfpa {
 namespace {
 
-// The ring holds three key chunks (64 KB of K and V each); a chunk arrives
-// as Cfg::kSub stages (see Cfg), at most kMaxStages in the ring.
+// The ring holds three key chunks (64 KB of K and V each; 4 bits: five of 36
+// KB); a chunk arrives as Cfg::kSub stages (see Cfg), at most kMaxStages in
+// the ring.
 constexpr int kRingBytes = 3 * 65536;
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 10;
 constexpr int kConsumerWarps = 8;
 constexpr int kCombineWarp0 = 8;      // warps 8..11
 constexpr int kCombineWarps = 4;
@@ -66,21 +67,25 @@ constexpr int kSmemBytes =
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 
-template <bool FP8>
+template <int KV>
 struct Cfg {
-  static constexpr int kChunk = FP8 ? 256 : 128;      // keys per chunk
+  static constexpr bool kF16 = KV != kKvBf16;          // f16 operands, kv head scales
+  static constexpr bool kFp4 = KV == kKvFp4;
+  static constexpr int kChunk = kF16 ? 256 : 128;      // keys per chunk
   // e4m3: a chunk in two stages of 128 keys (K 16 KB + V 16 KB), the first
   // read by consumer warps 0-3, the second by 4-7, so a stage is released
   // after half the warps' work (fp8 verify partial 174.2 -> 172.5 us);
-  // bf16: one stage of 128 keys (two stages measured 0.7 % slower).
-  static constexpr int kSub = FP8 ? 2 : 1;
-  static constexpr int kStages = 3 * kSub;
-  static constexpr int kStageBytes = 65536 / kSub;
+  // bf16: one stage of 128 keys (two stages measured 0.7 % slower);
+  // 4 bits: two stages, each a half-block of K and one of V.
+  static constexpr int kSub = kF16 ? 2 : 1;
+  static constexpr int kStages = kFp4 ? 10 : 3 * kSub;
+  static constexpr int kStageBytes = kFp4 ? 2 * kFp4HalfBytes : 65536 / kSub;
   static constexpr int kStageKeys = kChunk / kSub;     // 128 either way
   static constexpr int kSubWarps = kConsumerWarps / kSub;   // warps reading a stage
   static constexpr int kKeysPerWarp = kChunk / kConsumerWarps;
   static constexpr int kNT = kKeysPerWarp / 8;         // score n-tiles per warp
   static constexpr int kKS = kKeysPerWarp / 16;        // PV k-steps per warp
+  static_assert(kStages <= kMaxStages && kStages * kStageBytes <= kRingBytes, "ring");
 };
 
 // A work item: (run, kv head g, m-tile mt of 16 query vectors, split sigma).
@@ -146,7 +151,7 @@ __device__ __forceinline__ void item_keys(const DecodeParams& p, const DecodeDyn
 // KV write kernel stores them: lanes 0-15 a K row's 8-element slices, lanes
 // 16-31 a V row's.  Each lane then fences its stores against the TMA
 // loads that follow (async proxy), and the warp meets.
-template <bool FP8>
+template <int KV>
 __device__ void store_new_rows(const DecodeParams& p, const RunInfo& ru, int g, int k0, int k1,
                                int lane) {
   const bool is_v = lane >= 16;
@@ -167,7 +172,15 @@ __device__ void store_new_rows(const DecodeParams& p, const RunInfo& ru, int g, 
     const int row = ru.row0 + (key - ru.pos0);
     const uint4 in =
         *reinterpret_cast<const uint4*>(src_rows + ((size_t)row * p.hkv + g) * kHeadDim + t * 8);
-    if (FP8) {
+    if (KV == kKvFp4) {
+      float f[8];
+      unpack8(in, f);
+      uint8_t* b8 = static_cast<uint8_t*>(base);
+      uint32_t scale;
+      *reinterpret_cast<uint32_t*>(b8 + fp4_codes(dst_row) + t * 4) =
+          quant8_fp4(f, __ldg((is_v ? p.v_scale : p.k_scale) + g), 0xffffffffu, scale);
+      if (!(t & 1)) b8[fp4_scales(dst_row) + (t >> 1)] = (uint8_t)scale;
+    } else if (KV == kKvFp8) {
       float f[8];
       unpack8(in, f);
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + dst_row * kHeadDim + t * 8) =
@@ -181,14 +194,14 @@ __device__ void store_new_rows(const DecodeParams& p, const RunInfo& ru, int g, 
   __syncwarp();
 }
 
-template <bool FP8>
+template <int KV>
 __device__ __forceinline__ bool load_item(const DecodeParams& p, const RunInfo& ru, const Item& x,
                                           int klo, int khi, uint8_t* stage_mem, uint64_t* full,
                                           uint64_t* empty, int* stage_bad, uint32_t& stage);
 
 // Producer warp: lane 0 looks pages up and issues the TMA loads; with
 // append (APPEND), the whole warp first stores the new rows an item reads.
-template <bool FP8, bool APPEND>
+template <int KV, bool APPEND>
 __device__ void producer(const DecodeParams& p, const DecodeDyn& D, uint8_t* stage_mem,
                          uint64_t* full, uint64_t* empty, int* stage_bad) {
   const int lane = threadIdx.x & 31;
@@ -205,25 +218,25 @@ __device__ void producer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
     item_keys(p, D, x, klo, khi);
     if constexpr (APPEND) {
       const int k0 = max(klo, ru.pos0), k1 = min(khi, ru.pos0 + ru.nrows);
-      if (k0 < k1) store_new_rows<FP8>(p, ru, x.g, k0, k1, lane);
+      if (k0 < k1) store_new_rows<KV>(p, ru, x.g, k0, k1, lane);
       // the warp moves on item by item with lane 0, and leaves with it
-      ok = __shfl_sync(0xffffffffu, lane == 0 ? load_item<FP8>(p, ru, x, klo, khi, stage_mem,
+      ok = __shfl_sync(0xffffffffu, lane == 0 ? load_item<KV>(p, ru, x, klo, khi, stage_mem,
                                                                 full, empty, stage_bad, stage)
                                               : true,
                        0);
     } else {
-      ok = load_item<FP8>(p, ru, x, klo, khi, stage_mem, full, empty, stage_bad, stage);
+      ok = load_item<KV>(p, ru, x, klo, khi, stage_mem, full, empty, stage_bad, stage);
     }
   }
 }
 
 // Lane 0 of the producer warp: the TMA loads of one item's key chunks into
 // the ring, one page lookup per page.  False if a wait gave up.
-template <bool FP8>
+template <int KV>
 __device__ __forceinline__ bool load_item(const DecodeParams& p, const RunInfo& ru, const Item& x,
                                           int klo, int khi, uint8_t* stage_mem, uint64_t* full,
                                           uint64_t* empty, int* stage_bad, uint32_t& stage) {
-  using C = Cfg<FP8>;
+  using C = Cfg<KV>;
   {
     const CUtensorMap* mk = &p.maps[ru.src].k;
     const CUtensorMap* mv = &p.maps[ru.src].v;
@@ -255,7 +268,12 @@ __device__ __forceinline__ bool load_item(const DecodeParams& p, const RunInfo& 
         uint64_t* fb = &full[buf];
         uint8_t* sb = stage_mem + (size_t)buf * C::kStageBytes;
         mbar_arrive_expect_tx(fb, C::kStageBytes);
-        if (FP8) {
+        if (C::kFp4) {
+          const size_t off = (size_t)(y / kHalfRows) * kFp4HalfBytes;
+          bulk_load(sb, static_cast<const uint8_t*>(p.k_base[ru.src]) + off, kFp4HalfBytes, fb);
+          bulk_load(sb + kFp4HalfBytes, static_cast<const uint8_t*>(p.v_base[ru.src]) + off,
+                    kFp4HalfBytes, fb);
+        } else if (KV == kKvFp8) {
           tma_load_2d(sb, mk, 0, y, fb);
           tma_load_2d(sb + C::kStageBytes / 2, mv, 0, y, fb);
         } else {
@@ -272,17 +290,17 @@ __device__ __forceinline__ bool load_item(const DecodeParams& p, const RunInfo& 
 
 // Real head-dim index of C-fragment column n of PV n-tile nt (the V fragments
 // are loaded so a thread's sixteen n-tiles cover contiguous 16-byte chunks).
-template <bool FP8>
+template <int KV>
 __device__ __forceinline__ int out_col(int nt, int n) {
-  if (FP8) return 16 * n + nt;
+  if (KV != kKvBf16) return 16 * n + nt;
   return nt < 8 ? 8 * n + nt : 64 + 8 * n + (nt - 8);
 }
 
 // Query fragments of rows gq and gq+8 of an m-tile, the rows' causal limits,
 // their ancestor masks (all ones for causal rows) and their score multipliers
-// (f16 operands for e4m3 caches: each row is scaled by a power of two into
+// (f16 operands for e4m3 and 4-bit caches: each row is scaled by a power of two into
 // f16 range, exact for every element within 2^28 of the row's largest).
-template <bool FP8, bool GEN>
+template <int KV, bool GEN>
 __device__ __forceinline__ void load_q(const DecodeParams& p, const RunInfo& ru, const Item& x,
                                        int gq, int c, uint32_t (&qr)[2][16], int (&lim)[2],
                                        uint64_t (&anc)[2], float (&sc)[2]) {
@@ -301,7 +319,7 @@ __device__ __forceinline__ void load_q(const DecodeParams& p, const RunInfo& ru,
       if (GEN && p.anc) anc[hr] = __ldg(p.anc + ru.row0 + r);
       const uint4* qp =
           reinterpret_cast<const uint4*>(p.q + ((size_t)(ru.row0 + r) * p.hq + h) * kHeadDim);
-      if (FP8) {
+      if (KV != kKvBf16) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) v[m] = __ldg(qp + 4 * c + m);
       } else {
@@ -319,7 +337,7 @@ __device__ __forceinline__ void load_q(const DecodeParams& p, const RunInfo& ru,
       qr[hr][4 * m + 3] = v[m].w;
     }
     sc[hr] = p.scale_log2;
-    if (FP8) {
+    if (KV != kKvBf16) {
       float amax = 0.f;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
@@ -352,16 +370,25 @@ struct CombBars {
   uint64_t* done;        // the combiners finished the item (fold buffer free)
 };
 
+// The key, within its eight, of column n of a score n-tile.  4 bits: even
+// columns take keys 0-3 and odd ones 4-7, so that a quad's threads (columns
+// 2c, 2c + 1) read V rows c and c + 4: the four rows of one shared-memory
+// read are then consecutive (64 bytes each, no bank conflict).
+template <int KV>
+__device__ __forceinline__ int key_row(int n) {
+  return KV == kKvFp4 ? (n >> 1) | ((n & 1) << 2) : n;
+}
+
 // This warp's kKeysPerWarp keys, keys key_base.. at rows r0.. of the stage
 // at sb: scores, the causal or ancestor mask, the online softmax, and
 // O += P V.
-template <bool FP8, bool GEN>
+template <int KV, bool GEN>
 __device__ __forceinline__ void attend_block(uint32_t sb, int r0, int key_base, int seq_len,
                                              const uint32_t (&qr)[2][16], const int (&lim)[2],
                                              const float (&sc)[2], const uint64_t (&anc)[2],
                                              int tree_low, int gq, int c, float (&m_run)[2],
                                              float (&l_run)[2], float (&o)[16][4]) {
-  using C = Cfg<FP8>;
+  using C = Cfg<KV>;
   constexpr int kNT = C::kNT;             // score n-tiles
   constexpr int kKS = C::kKS;             // PV k-steps
   constexpr int kKeys = C::kKeysPerWarp;
@@ -370,9 +397,23 @@ __device__ __forceinline__ void attend_block(uint32_t sb, int r0, int key_base, 
 #pragma unroll
   for (int nt = 0; nt < kNT; ++nt) {
     s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-    const int kr = r0 + nt * 8 + gq;
+    const int kr = r0 + nt * 8 + key_row<KV>(gq);
     uint32_t kb[16];
-    if (FP8) {
+    if (C::kFp4) {
+      // dims 32 c .. 32 c + 31: 16 bytes of codes, two block scales
+      const uint4 w = lds128(sb + kr * kFp4CodeBytes + 16 * c);
+      const uint32_t s2 = e4m3x2_to_f16x2(
+          (uint16_t)lds16(sb + kFp4ScaleOff + kr * kFp4ScaleBytes + 2 * c));
+      const uint32_t sc0 = prmt(s2, s2, 0x1010), sc1 = prmt(s2, s2, 0x3232);
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t h[4];
+        e2m1x8_to_f16x8(ws[i], h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kb[4 * i + j] = hmul2(h[j], i < 2 ? sc0 : sc1);
+      }
+    } else if (KV == kKvFp8) {
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
         const uint4 w = lds128(swz128(sb, kr, 2 * c + ch));
@@ -398,7 +439,7 @@ __device__ __forceinline__ void attend_block(uint32_t sb, int r0, int key_base, 
     for (int ks = 0; ks < 8; ++ks) {
       const uint32_t a[4] = {qr[0][2 * ks], qr[1][2 * ks], qr[0][2 * ks + 1],
                              qr[1][2 * ks + 1]};
-      if (FP8)
+      if (C::kF16)
         mma_f16(s[nt], a, kb[2 * ks], kb[2 * ks + 1]);
       else
         mma_bf16(s[nt], a, kb[2 * ks], kb[2 * ks + 1]);
@@ -416,7 +457,7 @@ __device__ __forceinline__ void attend_block(uint32_t sb, int r0, int key_base, 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int hr = j >> 1;
-      const int key = key_base + nt * 8 + 2 * c + (j & 1);
+      const int key = key_base + nt * 8 + key_row<KV>(2 * c + (j & 1));
       bool vis = key <= lim[hr];
       if (tree_zone) {
         const int dd = lim[hr] - key;
@@ -466,7 +507,7 @@ __device__ __forceinline__ void attend_block(uint32_t sb, int r0, int key_base, 
 #pragma unroll
   for (int kk = 0; kk < kKS; ++kk) {
     uint32_t a[4];
-    if (FP8) {
+    if (C::kF16) {
       a[0] = pack_f16x2(s[2 * kk][0], s[2 * kk][1]);
       a[1] = pack_f16x2(s[2 * kk][2], s[2 * kk][3]);
       a[2] = pack_f16x2(s[2 * kk + 1][0], s[2 * kk + 1][1]);
@@ -479,7 +520,37 @@ __device__ __forceinline__ void attend_block(uint32_t sb, int r0, int key_base, 
     }
     const int kv0 = r0 + 16 * kk + 2 * c;    // rows kv0, kv0+1, kv0+8, kv0+9
     const int krow[4] = {kv0, kv0 + 1, kv0 + 8, kv0 + 9};
-    if (FP8) {
+    if (C::kFp4) {
+      // dims 16 gq .. 16 gq + 15 of the keys of k indices 2c, 2c + 1, 2c + 8,
+      // 2c + 9: 8 bytes of codes and one block scale each.  A byte of two
+      // keys' equal nibbles converts to a pair along the keys.
+      uint2 w[4];
+      uint32_t sb8[4];
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        const int row = r0 + 16 * kk + c + 4 * q4;       // key_row of that k index
+        w[q4] = lds64(vb + row * kFp4CodeBytes + 8 * gq);
+        sb8[q4] = lds8(vb + kFp4ScaleOff + row * kFp4ScaleBytes + gq);
+        if (key_base - r0 + row >= seq_len) sb8[q4] = 0;   // bytes there may be a NaN scale
+      }
+      const uint32_t s01 = e4m3x2_to_f16x2((uint16_t)(sb8[0] | (sb8[1] << 8)));
+      const uint32_t s23 = e4m3x2_to_f16x2((uint16_t)(sb8[2] | (sb8[3] << 8)));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t wa[4] = {i ? w[0].y : w[0].x, i ? w[1].y : w[1].x, i ? w[2].y : w[2].x,
+                                i ? w[3].y : w[3].x};
+        uint32_t lo01[4], hi01[4], lo23[4], hi23[4];
+        e2m1x8_to_f16x8((wa[0] & 0x0F0F0F0Fu) | ((wa[1] << 4) & 0xF0F0F0F0u), lo01);
+        e2m1x8_to_f16x8(((wa[0] >> 4) & 0x0F0F0F0Fu) | (wa[1] & 0xF0F0F0F0u), hi01);
+        e2m1x8_to_f16x8((wa[2] & 0x0F0F0F0Fu) | ((wa[3] << 4) & 0xF0F0F0F0u), lo23);
+        e2m1x8_to_f16x8(((wa[2] >> 4) & 0x0F0F0F0Fu) | (wa[3] & 0xF0F0F0F0u), hi23);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mma_f16(o[8 * i + 2 * j], a, hmul2(lo01[j], s01), hmul2(lo23[j], s23));
+          mma_f16(o[8 * i + 2 * j + 1], a, hmul2(hi01[j], s01), hmul2(hi23[j], s23));
+        }
+      }
+    } else if (KV == kKvFp8) {
       uint32_t w[4][4];
 #pragma unroll
       for (int q4 = 0; q4 < 4; ++q4) {
@@ -526,11 +597,11 @@ __device__ __forceinline__ void attend_block(uint32_t sb, int r0, int key_base, 
   }
 }
 
-template <bool FP8, bool GEN>
+template <int KV, bool GEN>
 __device__ void consumer(const DecodeParams& p, const DecodeDyn& D, uint8_t* stage_mem,
                          uint64_t* full, uint64_t* empty, const int* stage_bad, uint32_t tmem,
                          CombBars bars) {
-  using C = Cfg<FP8>;
+  using C = Cfg<KV>;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int gq = lane >> 2, c = lane & 3;
@@ -555,7 +626,7 @@ __device__ void consumer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
     // The chunk's 8 sub-blocks of kKeysPerWarp keys go to the 8 warps.
     const int sub0 = warp;
     if (x.run != q_run || x.g != q_g || x.mt != q_mt) {
-      load_q<FP8, GEN>(p, ru, x, gq, c, qr, lim, anc, sc);
+      load_q<KV, GEN>(p, ru, x, gq, c, qr, lim, anc, sc);
       maxlim = __reduce_max_sync(0xffffffffu, max(lim[0], lim[1]));
       if (GEN && p.anc) {
         const int mn = min(lim[0] >= 0 ? lim[0] : INT_MAX, lim[1] >= 0 ? lim[1] : INT_MAX);
@@ -583,7 +654,7 @@ __device__ void consumer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
       const int wk0 = sub0 * C::kKeysPerWarp;
       const int r0 = wk0 - (sub0 / C::kSubWarps) * C::kStageKeys;
       if (!stage_bad[buf] && k0 + wk0 <= maxlim)
-        attend_block<FP8, GEN>(sb, r0, k0 + wk0, ru.seq_len, qr, lim, sc, anc, tree_low, gq, c,
+        attend_block<KV, GEN>(sb, r0, k0 + wk0, ru.seq_len, qr, lim, sc, anc, tree_low, gq, c,
                                m_run, l_run, o);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[buf]);
@@ -727,7 +798,7 @@ __device__ __forceinline__ void merge_if_last(const DecodeParams& p, const RunIn
 // Each of pub, folded and done completes once per item (parity = item & 1);
 // a combiner waits for done of the previous item before publishing, so the
 // fold and (m, l) buffers are never overwritten while still being read.
-template <bool FP8, bool GEN, bool MERGE>
+template <int KV, bool GEN, bool MERGE>
 __device__ void combiner(const DecodeParams& p, const DecodeDyn& D, uint32_t tmem, float4* fold,
                          float* ml_buf, int* merge_flag, CombBars bars) {
   const int warp = threadIdx.x >> 5;
@@ -820,7 +891,7 @@ __device__ void combiner(const DecodeParams& p, const DecodeDyn& D, uint32_t tme
         }
         acc[u] = a;
       }
-      const float vs = FP8 ? __ldg(p.v_scale + x.g) : 1.f;
+      const float vs = KV != kKvBf16 ? __ldg(p.v_scale + x.g) : 1.f;
 #pragma unroll
       for (int hr = 0; hr < 2; ++hr) {
         const int qv = x.mt * 16 + gq + 8 * hr;
@@ -835,9 +906,9 @@ __device__ void combiner(const DecodeParams& p, const DecodeDyn& D, uint32_t tme
                              : make_float4(acc[0].x, acc[1].x, acc[2].x, acc[3].x);
         const float4 o1 = hr ? make_float4(acc[0].w, acc[1].w, acc[2].w, acc[3].w)
                              : make_float4(acc[0].y, acc[1].y, acc[2].y, acc[3].y);
-        *reinterpret_cast<float4*>(orow + out_col<FP8>(4 * q, 2 * c)) =
+        *reinterpret_cast<float4*>(orow + out_col<KV>(4 * q, 2 * c)) =
             make_float4(o0.x * vs, o0.y * vs, o0.z * vs, o0.w * vs);
-        *reinterpret_cast<float4*>(orow + out_col<FP8>(4 * q, 2 * c + 1)) =
+        *reinterpret_cast<float4*>(orow + out_col<KV>(4 * q, 2 * c + 1)) =
             make_float4(o1.x * vs, o1.y * vs, o1.z * vs, o1.w * vs);
         if (q == 0 && c == 0) {
           const int row = gq + 8 * hr;
@@ -862,7 +933,7 @@ __device__ void combiner(const DecodeParams& p, const DecodeDyn& D, uint32_t tme
 // DEV: the runs and CTA ranges are read from p.dyn (a plan in device mode).
 // MERGE: the combiners merge each finished group (p.arrive).
 // APPEND: the producer warp stores the rows' new K and V (p.k_rows).
-template <bool FP8, bool GEN, bool DEV, bool MERGE, bool APPEND>
+template <int KV, bool GEN, bool DEV, bool MERGE, bool APPEND>
 __global__ void __launch_bounds__(kThreads, 1) decode_partial_kernel(
     const __grid_constant__ DecodeParams p) {
   const DecodeDyn& D = DEV ? *p.dyn : p.d;
@@ -902,9 +973,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_kernel(
     }
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Cfg<FP8>::kStages; ++i) {
+    for (int i = 0; i < Cfg<KV>::kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], Cfg<FP8>::kSubWarps);
+      mbar_init(&empty[i], Cfg<KV>::kSubWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&cb.posted[i], kConsumerWarps);
@@ -915,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_kernel(
     mbar_init(cb.done, kCombineWarps);
     fence_mbar_init();
   }
-  if (warp == kProducerWarp && (threadIdx.x & 31) == 0) {
+  if (KV != kKvFp4 && warp == kProducerWarp && (threadIdx.x & 31) == 0) {
     for (int i = 0; i < p.nsrc; ++i) {
       tma_prefetch_desc(&p.maps[i].k);
       tma_prefetch_desc(&p.maps[i].v);
@@ -930,13 +1001,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_kernel(
   wait_prior_grid();
   if (warp < kCombineWarp0) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsumer));
-    consumer<FP8, GEN>(p, D, stage_mem, full, empty, stage_bad, tmem, cb);
+    consumer<KV, GEN>(p, D, stage_mem, full, empty, stage_bad, tmem, cb);
   } else if (warp < kProducerWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCombine));
-    combiner<FP8, GEN, MERGE>(p, D, tmem, fold, ml_buf, merge_flag, cb);
+    combiner<KV, GEN, MERGE>(p, D, tmem, fold, ml_buf, merge_flag, cb);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
-    if (warp == kProducerWarp) producer<FP8, APPEND>(p, D, stage_mem, full, empty, stage_bad);
+    if (warp == kProducerWarp) producer<KV, APPEND>(p, D, stage_mem, full, empty, stage_bad);
   }
   umma::fence_before_sync();
   __syncthreads();
@@ -985,59 +1056,60 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Merg
                                   p.lse ? p.lse + (size_t)row * p.hq + h : nullptr);
 }
 
-template <bool FP8, bool GEN, bool DEV, bool MERGE, bool APPEND>
+template <int KV, bool GEN, bool DEV, bool MERGE, bool APPEND>
 cudaError_t launch_partial(const DecodeParams& p, int grid, cudaStream_t s) {
   static PerDeviceOnce configured;
   cudaError_t e = configured.run([] {
     // The register split only works if the block launches with at least the
     // registers it hands out; otherwise setmaxnreg.inc would wait forever.
     cudaFuncAttributes attr;
-    cudaError_t r = cudaFuncGetAttributes(&attr, decode_partial_kernel<FP8, GEN, DEV, MERGE, APPEND>);
+    cudaError_t r = cudaFuncGetAttributes(&attr, decode_partial_kernel<KV, GEN, DEV, MERGE, APPEND>);
     if (r != cudaSuccess) return r;
     if (attr.numRegs * kThreads < 128 * (2 * kRegsConsumer + kRegsCombine + kRegsProducer))
       return cudaErrorInvalidValue;
-    return cudaFuncSetAttribute(decode_partial_kernel<FP8, GEN, DEV, MERGE, APPEND>,
+    return cudaFuncSetAttribute(decode_partial_kernel<KV, GEN, DEV, MERGE, APPEND>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   });
   if (e != cudaSuccess) return e;
   e =
-      launch_pdl(decode_partial_kernel<FP8, GEN, DEV, MERGE, APPEND>, dim3(grid), dim3(kThreads), kSmemBytes, s, p);
+      launch_pdl(decode_partial_kernel<KV, GEN, DEV, MERGE, APPEND>, dim3(grid), dim3(kThreads), kSmemBytes, s, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
-template <bool DEV>
-cudaError_t launch_partial_dev(const DecodeParams& p, bool fp8, int grid, cudaStream_t s) {
+template <int KV, bool DEV>
+cudaError_t launch_partial_dev(const DecodeParams& p, int grid, cudaStream_t s) {
   // Rows with ancestor masks take the general instantiation, so the plain
   // causal calls keep their own kernel's code.
-  if (p.anc)
-    return fp8 ? launch_partial<true, true, DEV, false, false>(p, grid, s)
-               : launch_partial<false, true, DEV, false, false>(p, grid, s);
-  if (p.k_rows)
-    return fp8 ? launch_partial<true, false, DEV, false, true>(p, grid, s)
-               : launch_partial<false, false, DEV, false, true>(p, grid, s);
-  return fp8 ? launch_partial<true, false, DEV, false, false>(p, grid, s)
-             : launch_partial<false, false, DEV, false, false>(p, grid, s);
+  if (p.anc) return launch_partial<KV, true, DEV, false, false>(p, grid, s);
+  if (p.k_rows) return launch_partial<KV, false, DEV, false, true>(p, grid, s);
+  return launch_partial<KV, false, DEV, false, false>(p, grid, s);
+}
+
+template <int KV>
+cudaError_t launch_partial_kv(const DecodeParams& p, int grid, cudaStream_t s) {
+  // The merge in the kernel is built for plain causal rows in parameter mode.
+  if (p.arrive) {
+    if (p.anc || p.dyn || !p.out) return cudaErrorInvalidValue;
+    return p.k_rows ? launch_partial<KV, false, false, true, true>(p, grid, s)
+                    : launch_partial<KV, false, false, true, false>(p, grid, s);
+  }
+  return p.dyn ? launch_partial_dev<KV, true>(p, grid, s)
+               : launch_partial_dev<KV, false>(p, grid, s);
 }
 
 }  // namespace
 
 // The launch shape comes from the parameters' own copy of the dynamic data
 // (p.d), which a device-mode plan keeps fixed from step to step.
-cudaError_t launch_decode_partial(const DecodeParams& p, bool fp8, int grid, cudaStream_t s) {
+cudaError_t launch_decode_partial(const DecodeParams& p, int kv, int grid, cudaStream_t s) {
   if (grid <= 0 || p.d.n_items == 0) return cudaSuccess;
-  // The merge in the kernel is built for plain causal rows in parameter mode.
   if (p.k_rows && p.anc) return cudaErrorInvalidValue;   // append has no tree rows
-  if (p.arrive) {
-    if (p.anc || p.dyn || !p.out) return cudaErrorInvalidValue;
-    if (p.k_rows)
-      return fp8 ? launch_partial<true, false, false, true, true>(p, grid, s)
-                 : launch_partial<false, false, false, true, true>(p, grid, s);
-    return fp8 ? launch_partial<true, false, false, true, false>(p, grid, s)
-               : launch_partial<false, false, false, true, false>(p, grid, s);
+  switch (kv) {
+    case kKvBf16: return launch_partial_kv<kKvBf16>(p, grid, s);
+    case kKvFp8: return launch_partial_kv<kKvFp8>(p, grid, s);
+    default: return launch_partial_kv<kKvFp4>(p, grid, s);
   }
-  return p.dyn ? launch_partial_dev<true>(p, fp8, grid, s)
-               : launch_partial_dev<false>(p, fp8, grid, s);
 }
 
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t s) {

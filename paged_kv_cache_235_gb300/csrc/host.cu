@@ -196,9 +196,10 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 int check_cache(const tfpa_cache* c) {
   if (!c) return TFPA_EINVAL;
-  if (c->dtype != TFPA_BF16 && c->dtype != TFPA_FP8_E4M3) return TFPA_EINVAL;
+  if (c->dtype != TFPA_BF16 && c->dtype != TFPA_FP8_E4M3 && c->dtype != TFPA_FP4_E2M1)
+    return TFPA_EINVAL;
   if (c->head_dim != kHeadDim || c->hkv < 1 || c->hq < 1 || c->hq % c->hkv) return TFPA_EINVAL;
-  if (c->dtype == TFPA_FP8_E4M3 && (!c->k_scale || !c->v_scale)) return TFPA_EINVAL;
+  if (c->dtype != TFPA_BF16 && (!c->k_scale || !c->v_scale)) return TFPA_EINVAL;
   if ((c->k_pool && !aligned(c->k_pool, 16)) || (c->v_pool && !aligned(c->v_pool, 16)))
     return TFPA_EINVAL;
   return TFPA_OK;
@@ -256,8 +257,16 @@ int build_runs(const tfpa_seg* segs, int32_t nseg, const int32_t* row_seg,
 // Runs of four or more m-tiles (16 query vectors each, so at least 49
 // vectors per kv head) are dense enough for the tensor cores: they take the
 // prefill kernel in verify mode, when a tile holds the group's heads.
-bool on_verify_path(const Run& r, int G) {
-  return G <= kVerifyVectors && (r.nrows * G + 15) / 16 >= 4;
+// A 4-bit cache's runs all take the decode partial kernel.
+bool on_verify_path(const Run& r, int G, int kv) {
+  return kv != kKvFp4 && G <= kVerifyVectors && (r.nrows * G + 15) / 16 >= 4;
+}
+
+// Stored bytes of one row of one kv head, K or V.
+int row_bytes_of(const tfpa_cache* c) {
+  return c->dtype == TFPA_BF16       ? 2 * kHeadDim
+         : c->dtype == TFPA_FP8_E4M3 ? kHeadDim
+                                     : kFp4CodeBytes + kFp4ScaleBytes;
 }
 
 int to_err(cudaError_t e) { return e == cudaSuccess ? TFPA_OK : TFPA_ECUDA; }
@@ -273,7 +282,7 @@ struct tfpa_plan {
   enum Kind : int { kDecode, kVerify, kMerge, kWrite };
   struct Entry {
     Kind kind;
-    bool fp8;
+    int kv;         // KvType
     int grid;
     size_t index;   // into the vector of its kind
   };
@@ -321,43 +330,43 @@ struct Sink {
     plan->dyn_used = k.dyn;
   }
   template <typename P>
-  int keep(tfpa_plan::Kind kind, std::vector<P>& v, const P& p, bool fp8, int grid) const {
+  int keep(tfpa_plan::Kind kind, std::vector<P>& v, const P& p, int kv, int grid) const {
     v.push_back(p);
-    plan->entries.push_back(tfpa_plan::Entry{kind, fp8, grid, v.size() - 1});
+    plan->entries.push_back(tfpa_plan::Entry{kind, kv, grid, v.size() - 1});
     return TFPA_OK;
   }
   // keep() for a launch with dynamic data: in device mode the launch takes
   // the next slot of the plan's device buffer.
   template <typename P>
-  int keep_dyn(tfpa_plan::Kind kind, std::vector<P>& v, const P& p, bool fp8, int grid) const {
+  int keep_dyn(tfpa_plan::Kind kind, std::vector<P>& v, const P& p, int kv, int grid) const {
     const size_t off = plan->dyn_used;
     if (plan->dyn_base) {
       const size_t end = (off + sizeof(p.d) + 15) & ~size_t(15);
       if (end > plan->dyn_cap) return TFPA_ECAPACITY;
       plan->dyn_used = end;
     }
-    keep(kind, v, p, fp8, grid);
+    keep(kind, v, p, kv, grid);
     v.back().dyn = plan->dyn_base
                        ? reinterpret_cast<decltype(p.dyn)>(plan->dyn_base + off)
                        : nullptr;
     return TFPA_OK;
   }
-  int decode(const DecodeParams& p, bool fp8, int grid) const {
-    if (plan) return keep_dyn(tfpa_plan::kDecode, plan->decode, p, fp8, grid);
-    return dry_run() ? TFPA_OK : to_err(launch_decode_partial(p, fp8, grid, stream));
+  int decode(const DecodeParams& p, int kv, int grid) const {
+    if (plan) return keep_dyn(tfpa_plan::kDecode, plan->decode, p, kv, grid);
+    return dry_run() ? TFPA_OK : to_err(launch_decode_partial(p, kv, grid, stream));
   }
-  int verify(const PrefillParams& p, bool fp8, int tiles) const {
+  int verify(const PrefillParams& p, int kv, int tiles) const {
     // the tensor-core verify launch's grid follows the streams' lengths
     if (device()) return TFPA_EINVAL;
-    if (plan) return keep(tfpa_plan::kVerify, plan->verify, p, fp8, tiles);
-    return dry_run() ? TFPA_OK : to_err(launch_verify(p, fp8, tiles, stream));
+    if (plan) return keep(tfpa_plan::kVerify, plan->verify, p, kv, tiles);
+    return dry_run() ? TFPA_OK : to_err(launch_verify(p, kv == kKvFp8, tiles, stream));
   }
   int merge(const MergeParams& p) const {
-    if (plan) return keep_dyn(tfpa_plan::kMerge, plan->merge, p, false, 0);
+    if (plan) return keep_dyn(tfpa_plan::kMerge, plan->merge, p, 0, 0);
     return dry_run() ? TFPA_OK : to_err(launch_merge(p, stream));
   }
   int write(const WriteParams& p) const {
-    if (plan) return keep_dyn(tfpa_plan::kWrite, plan->write, p, false, 0);
+    if (plan) return keep_dyn(tfpa_plan::kWrite, plan->write, p, 0, 0);
     return dry_run() ? TFPA_OK : to_err(launch_write_kv(p, stream));
   }
 };
@@ -471,8 +480,8 @@ int item_stages(const RunInfo& ri, int G, int mt, int sigma, int chunk) {
 // split.  An item's weight does not depend on its kv head, so each run's
 // (m-tile, split) prefix weights are computed once, and each CTA boundary is
 // found by a binary search in the block of the kv head that holds it.
-void plan_cta_ranges(DecodeParams& p, int nr, int G, bool fp8, int grid) {
-  const int chunk = fp8 ? 256 : 128;
+void plan_cta_ranges(DecodeParams& p, int nr, int G, int kv, int grid) {
+  const int chunk = kv == kKvBf16 ? 128 : 256;
   // The fixed cost, in key stages, was measured on the overcommitted pool
   // (17 streams of 1k-262k keys, e4m3): 0 -> 380 us, 1 -> 341 us, 2 -> 348 us,
   // 4 -> 377 us, 8 -> 444 us; uniform batches do not depend on it.
@@ -532,7 +541,7 @@ struct RopeArgs {
 };
 int write_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const void* k_rows,
                const void* v_rows, const int32_t* row_seg, const int32_t* row_pos, int32_t rows,
-               const RopeArgs& rope, const Sink& sink);
+               const RopeArgs& rope, const Sink& sink, bool read = false);
 
 // Partial (and optionally merge) launches over the call's rows.  With
 // `sliced`, each launch's partials start at scratch row 0 and are merged
@@ -562,10 +571,11 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
     if (tfpa_num_splits(segs[r.seg].seq_len) > sc->max_splits) return TFPA_ECAPACITY;
   if (rows == 0) return TFPA_OK;
   if ((e = check_device())) return e;
-  const bool fp8 = c->dtype == TFPA_FP8_E4M3;
+  const int kv = c->dtype;
+  const bool fp8 = kv == kKvFp8;
   const int G = c->hq / c->hkv;
   for (const Run& r : runs)
-    if (on_verify_path(r, G)) {
+    if (on_verify_path(r, G, kv)) {
       if ((e = check_tma_source(q))) return e;
       break;
     }
@@ -573,7 +583,7 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
     if (!k_rows || !v_rows || !aligned(k_rows, 16) || !aligned(v_rows, 16)) return TFPA_EINVAL;
     bool fuse = true;
     for (size_t i = 0; fuse && i < runs.size(); ++i) {
-      fuse = !on_verify_path(runs[i], G);   // the decode partial path
+      fuse = !on_verify_path(runs[i], G, kv);   // the decode partial path
       for (size_t j = 0; fuse && j < i; ++j) fuse = runs[j].seg != runs[i].seg;
     }
     if (!fuse) {
@@ -614,7 +624,7 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
       if (src < 0) break;
       const int32_t take = std::min(r.nrows - taken, sc->cap_rows - nrows);
       const tfpa_seg& g = segs[r.seg];
-      if (on_verify_path(r, G)) {
+      if (on_verify_path(r, G, kv)) {
         if (nv == 0) std::memset(&pv, 0, sizeof(pv));   // only launches that run are built
         RunInfo& info = pv.runs[nv++];
         fill_run(info, g, src, nrows, take, r.pos0 + taken);
@@ -651,7 +661,9 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
     bool fused = sliced && nv == 0 && sc->arrive && !anc && !sink.device();
     for (int r = 0; fused && r < nd; ++r) fused = p.d.runs[r].nsplit <= kFusedMergeMaxSplits;
     if (nd > 0) {
-      if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 128, p.maps, p.nsrc)))
+      if (kv == kKvFp4)
+        p.nsrc = 1 + ss.nslab;          // read through the bases below
+      else if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 128, p.maps, p.nsrc)))
         return e;
       p.q = static_cast<const __nv_bfloat16*>(q) + (size_t)base * hd;
       p.anc = anc ? anc + base : nullptr;   // the ancestor table shifts with the rows
@@ -663,8 +675,8 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
       const size_t rd = (size_t)c->hkv * kHeadDim;
       p.k_rows = k_rows ? static_cast<const __nv_bfloat16*>(k_rows) + (size_t)base * rd : nullptr;
       p.v_rows = v_rows ? static_cast<const __nv_bfloat16*>(v_rows) + (size_t)base * rd : nullptr;
-      if (k_rows) {
-        // where each source's rows go: the pool, then the slabs in source order
+      if (k_rows || kv == kKvFp4) {
+        // where each source's rows are: the pool, then the slabs in source order
         p.k_base[0] = c->k_pool;
         p.v_base[0] = c->v_pool;
         for (int i = 0; i < ss.nslab; ++i) {
@@ -687,9 +699,9 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
       // In device mode the grid is one CTA per SM whatever the work, so
       // that the launch can be replayed as the streams grow.
       const int grid = std::min(sink.device() ? nsm : std::min(items, nsm), kMaxDecodeGrid);
-      plan_cta_ranges(p, nd, G, fp8, grid);
+      plan_cta_ranges(p, nd, G, kv, grid);
       record(1, base, nrows, nd, items, grid, (int64_t)base * hd, 0);
-      if ((e = sink.decode(p, fp8, grid))) return e;
+      if ((e = sink.decode(p, kv, grid))) return e;
     }
     if (nv > 0) {
       if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 128, pv.maps, pv.nsrc))) return e;
@@ -717,7 +729,7 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
       pv.max_splits = sc->max_splits;
       pv.scale_log2 = scale * 1.4426950408889634f;
       record(8, base, nrows, nv, tiles, tiles, (int64_t)base * hd, 0);
-      if ((e = sink.verify(pv, fp8, tiles))) return e;
+      if ((e = sink.verify(pv, kv, tiles))) return e;
     }
     if (sliced && !fused) {
       mp.part_o = part_o;
@@ -766,7 +778,7 @@ extern "C" int tfpa_row_splits(const tfpa_cache* cache, const tfpa_seg* segs, in
   const int G = cache->hq / cache->hkv;
   for (const Run& r : runs) {
     const int32_t L = segs[r.seg].seq_len;
-    const int32_t n = on_verify_path(r, G) ? verify_num_splits(L) : tfpa_num_splits(L);
+    const int32_t n = on_verify_path(r, G, cache->dtype) ? verify_num_splits(L) : tfpa_num_splits(L);
     for (int32_t i = 0; i < r.nrows; ++i) nsplit[r.row0 + i] = n;
   }
   return TFPA_OK;
@@ -835,7 +847,7 @@ namespace {
 
 int write_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const void* k_rows,
                const void* v_rows, const int32_t* row_seg, const int32_t* row_pos, int32_t rows,
-               const RopeArgs& rope, const Sink& sink) {
+               const RopeArgs& rope, const Sink& sink, bool read) {
   int e;
   if ((e = check_cache(c)) || (e = check_segs(c, segs, nseg))) return e;
   if (rows > 0 && (!k_rows || !v_rows || !aligned(k_rows, 16) || !aligned(v_rows, 16)))
@@ -887,9 +899,13 @@ int write_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const vo
     p.d.rows = nrows;
     p.hkv = c->hkv;
     p.num_pages = c->num_pages;
-    p.fp8 = c->dtype == TFPA_FP8_E4M3;
-    record(0, base, nrows, nr, nrows * c->hkv, (nrows * c->hkv + 15) / 16, 0, 0);
-    if ((e = sink.write(p))) return e;
+    p.kv = c->dtype;
+    record(read ? 9 : 0, base, nrows, nr, nrows * c->hkv, (nrows * c->hkv + 15) / 16, 0, 0);
+    if (read)
+      e = dry_run() ? TFPA_OK : to_err(launch_read_kv(p, sink.stream));
+    else
+      e = sink.write(p);
+    if (e) return e;
   }
   return TFPA_OK;
 }
@@ -901,6 +917,15 @@ extern "C" int tfpa_write_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t 
                              const int32_t* row_pos, int32_t rows, cudaStream_t stream) {
   return write_impl(c, segs, nseg, k_rows, v_rows, row_seg, row_pos, rows,
                     RopeArgs{nullptr, nullptr, nullptr, 0}, Sink{stream, nullptr});
+}
+
+// The write's launches with the rows as the destination (const cast back by
+// the kernel: they are the caller's output).
+extern "C" int tfpa_read_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, void* k_rows,
+                            void* v_rows, const int32_t* row_seg, const int32_t* row_pos,
+                            int32_t rows, cudaStream_t stream) {
+  return write_impl(c, segs, nseg, k_rows, v_rows, row_seg, row_pos, rows,
+                    RopeArgs{nullptr, nullptr, nullptr, 0}, Sink{stream, nullptr}, true);
 }
 
 extern "C" int tfpa_write_kv_rope(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg,
@@ -1000,7 +1025,7 @@ namespace {
 uint64_t compute_shape(const tfpa_plan* plan) {
   uint64_t h = 14695981039346656037ull;
   for (const tfpa_plan::Entry& en : plan->entries) {
-    const int32_t head[3] = {(int32_t)en.kind, (int32_t)en.fp8, en.grid};
+    const int32_t head[3] = {(int32_t)en.kind, (int32_t)en.kv, en.grid};
     h = fnv1a(h, head, sizeof(head));
     switch (en.kind) {
       case tfpa_plan::kDecode: h = hash_static(h, plan->decode[en.index]); break;
@@ -1130,10 +1155,10 @@ extern "C" int tfpa_plan_launch(const tfpa_plan* plan, cudaStream_t stream) {
     cudaError_t r = cudaSuccess;
     switch (en.kind) {
       case tfpa_plan::kDecode:
-        r = launch_decode_partial(plan->decode[en.index], en.fp8, en.grid, stream);
+        r = launch_decode_partial(plan->decode[en.index], en.kv, en.grid, stream);
         break;
       case tfpa_plan::kVerify:
-        r = launch_verify(plan->verify[en.index], en.fp8, en.grid, stream);
+        r = launch_verify(plan->verify[en.index], en.kv == kKvFp8, en.grid, stream);
         break;
       case tfpa_plan::kMerge:
         r = launch_merge(plan->merge[en.index], stream);
@@ -1184,7 +1209,7 @@ extern "C" int tfpa_keep_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t n
   p.n = n;
   p.hkv = c->hkv;
   p.num_pages = c->num_pages;
-  p.row_bytes = c->dtype == TFPA_FP8_E4M3 ? kHeadDim : 2 * kHeadDim;
+  p.row_bytes = row_bytes_of(c);
   record(4, 0, n, 0, n * c->hkv, c->hkv, 0, 0);
   if (!dry_run())
     if ((e = to_err(launch_keep(p, stream)))) return e;
@@ -1233,7 +1258,7 @@ int copy_impl(const tfpa_cache* c, const tfpa_seg* seg, int32_t p0, int32_t p1, 
   p.page0 = p0 / kPage;
   p.hkv = c->hkv;
   p.num_pages = c->num_pages;
-  p.row_bytes = c->dtype == TFPA_FP8_E4M3 ? kHeadDim : 2 * kHeadDim;
+  p.row_bytes = row_bytes_of(c);
   p.restore = restore ? 1 : 0;
   const int npages = (p1 - 1) / kPage - p0 / kPage + 1;
   record(restore ? 7 : 6, p0, p1 - p0, 0, npages * c->hkv * 2, npages * c->hkv * 2, 0, 0);
@@ -1287,6 +1312,7 @@ extern "C" int tfpa_prefill(const tfpa_cache* c, const tfpa_seg* segs, int32_t n
   int e;
   if ((e = check_cache(c)) || (e = check_segs(c, segs, nseg))) return e;
   if (rows > 0 && (!q || !aligned(q, 16) || !out || !aligned(out, 16))) return TFPA_EINVAL;
+  if (c->dtype == TFPA_FP4_E2M1) return TFPA_EINVAL;
   if (max_rows_per_launch < 0 || !std::isfinite(scale) || !(scale > 0.f)) return TFPA_EINVAL;
   thread_local std::vector<Run> runs;   // reused by every call of this thread
   if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;

@@ -21,6 +21,20 @@ constexpr int kMaxSlabs = 15;       // slab streams per launch (+1 source for th
 constexpr int kMaxSources = kMaxSlabs + 1;
 constexpr int kMaxDecodeGrid = 256;  // CTAs of one decode partial launch, at most
 
+// Element type of a cache (the values of tfpa_kv_dtype).
+enum KvType : int { kKvBf16 = 0, kKvFp8 = 1, kKvFp4 = 2 };
+
+// A 4-bit cache: storage row R (pool: (page * hkv + g) * 256 + position %
+// 256; slab: g * slab_cap + position) lies in half-block R / 128, which
+// holds its 128 rows' codes ([128][64] bytes) and then their scales
+// ([128][8] bytes): one aligned run of 9,216 bytes that a single bulk copy
+// brings into shared memory.
+constexpr int kHalfRows = 128;
+constexpr int kFp4CodeBytes = 64;        // 128 e2m1 codes
+constexpr int kFp4ScaleBytes = 8;        // an e4m3 scale per 16 head dims
+constexpr int kFp4ScaleOff = kHalfRows * kFp4CodeBytes;
+constexpr int kFp4HalfBytes = kHalfRows * (kFp4CodeBytes + kFp4ScaleBytes);
+
 // TMA descriptors of one K/V source: the page pool (source 0) or a slab.
 struct KVMaps {
   CUtensorMap k;
@@ -72,6 +86,7 @@ struct DecodeParams {
   // go (pool: [num_pages][hkv][256][128], slab: [hkv][slab_cap][128]).
   const __nv_bfloat16* k_rows;
   const __nv_bfloat16* v_rows;
+  // A 4-bit cache is read through these bases too (bulk copies, no maps).
   void* k_base[kMaxSources];
   void* v_base[kMaxSources];
   // Merge in the partial kernel (arrive != nullptr): per (row, head) of a
@@ -148,7 +163,7 @@ struct WriteParams {
   int32_t rope_n;
   int32_t hkv;
   int32_t num_pages;
-  int32_t fp8;
+  int32_t kv;                 // KvType
 };
 
 // Keep: stored rows copied between positions of a stream (all kv heads).
@@ -171,7 +186,7 @@ struct KeepParams {
   int32_t n;
   int32_t hkv;
   int32_t num_pages;
-  int32_t row_bytes;          // 256 (bf16) or 128 (e4m3)
+  int32_t row_bytes;          // 256 (bf16), 128 (e4m3) or 72 (4 bits: codes and scales)
 };
 
 // Prefill: one work tile = (run, kv head g, query-head pair, 128 rows).
@@ -215,7 +230,8 @@ struct StageParams {
 };
 
 // Save / restore of a stream's stored rows [p0, p1) to / from an image laid
-// out [K, V][hkv][p1 - p0][row].
+// out [K, V][hkv][p1 - p0][row]; 4-bit rows: every row's codes, then every
+// row's scales, each in that order.
 struct CopyParams {
   const int32_t* page_table;  // nullptr => slab
   void* k_base;               // pool or slab
@@ -227,16 +243,18 @@ struct CopyParams {
   int32_t page0;              // first page of the range
   int32_t hkv;
   int32_t num_pages;
-  int32_t row_bytes;          // 256 (bf16) or 128 (e4m3)
+  int32_t row_bytes;          // 256 (bf16), 128 (e4m3) or 72 (4 bits)
   int32_t restore;            // 0: cache -> image, 1: image -> cache
 };
 
 // Launchers (defined next to their kernels).
 cudaError_t launch_write_kv(const WriteParams& p, cudaStream_t s);
+// The rows' stored K and V as bf16, into p.k_rows / p.v_rows.
+cudaError_t launch_read_kv(const WriteParams& p, cudaStream_t s);
 cudaError_t launch_keep(const KeepParams& p, cudaStream_t s);
 cudaError_t launch_stage(const StageParams& p, cudaStream_t s);
 cudaError_t launch_copy(const CopyParams& p, int npages, cudaStream_t s);
-cudaError_t launch_decode_partial(const DecodeParams& p, bool fp8, int grid, cudaStream_t s);
+cudaError_t launch_decode_partial(const DecodeParams& p, int kv, int grid, cudaStream_t s);
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t s);
 // Prefill launches a cluster of two CTAs per tile; verify one CTA per tile.
 cudaError_t launch_prefill(const PrefillParams& p, bool fp8, int tiles, cudaStream_t s);

@@ -1,12 +1,13 @@
-// KV write: new rows' K and V into their pages or slab, bf16 copy or e4m3
-// quantisation (TensorFold PR #1373, "What changes": the page-run layout the
+// KV write: new rows' K and V into their pages or slab, bf16 copy, e4m3 or
+// 4-bit quantisation (TensorFold PR #1373, "What changes": the page-run layout the
 // KV store kernels write), optionally with K rotated by its rotary position
 // first; and keep: stored rows copied between positions of a stream (the
 // PR #1373 review lists "rope stores and keep" among the paged store's
 // checks).
 //
 // Write: one 16-thread group per (row, kv head); each thread moves 8
-// elements (16 bytes of bf16 in; 16 bytes of bf16 or 8 bytes of e4m3 out).
+// elements (16 bytes of bf16 in; 16 bytes of bf16, 8 of e4m3 or 4 of e2m1
+// codes out, two threads sharing a block of 16 and its scale byte).
 // The page is looked up once per (row, head).  The rotation pairs element i
 // with i + 64 (rotate-half), so a thread also reads its partner's 8
 // elements; every product and sum is rounded on its own (no fused
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(256) write_kv_kernel(const __grid_constant__ W
                      : __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
     }
   }
-  if (!p.fp8) {
+  if (p.kv == kKvBf16) {
     __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(run.k_dst) + dst_row * kHeadDim + t * 8;
     __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(run.v_dst) + dst_row * kHeadDim + t * 8;
     *reinterpret_cast<uint4*>(kd) = p.rope_cos ? pack8_bf16(kf) : kv;
@@ -114,10 +115,88 @@ __global__ void __launch_bounds__(256) write_kv_kernel(const __grid_constant__ W
   }
   float vf[8];
   unpack8(vv, vf);
+  if (p.kv == kKvFp4) {
+    const unsigned lanes = 0xFFFFu << (threadIdx.x & 16);   // the row's 16 threads
+    uint8_t* kb = static_cast<uint8_t*>(run.k_dst);
+    uint8_t* vb = static_cast<uint8_t*>(run.v_dst);
+    const size_t codes = fp4_codes(dst_row) + t * 4, scales = fp4_scales(dst_row) + (t >> 1);
+    uint32_t ks, vs;
+    *reinterpret_cast<uint32_t*>(kb + codes) = quant8_fp4(kf, __ldg(p.k_scale + g), lanes, ks);
+    *reinterpret_cast<uint32_t*>(vb + codes) = quant8_fp4(vf, __ldg(p.v_scale + g), lanes, vs);
+    if (!(t & 1)) {
+      kb[scales] = (uint8_t)ks;
+      vb[scales] = (uint8_t)vs;
+    }
+    return;
+  }
   uint8_t* kd = static_cast<uint8_t*>(run.k_dst) + dst_row * kHeadDim + t * 8;
   uint8_t* vd = static_cast<uint8_t*>(run.v_dst) + dst_row * kHeadDim + t * 8;
   *reinterpret_cast<uint2*>(kd) = quant8(kf, __ldg(p.k_scale + g));
   *reinterpret_cast<uint2*>(vd) = quant8(vf, __ldg(p.v_scale + g));
+}
+
+// Read: the rows' stored K and V as bf16, the write kernel's thread mapping
+// run backwards (8 head dims a thread).  A bf16 row is copied; an e4m3 value
+// is code * scale and a 4-bit value (code * block scale, exact) * scale, the
+// product rounded to float32 and then to bf16.  Bound by launch latency for
+// a step's rows and by the bf16 output's bytes for a chunk's.
+__global__ void __launch_bounds__(256) read_kv_kernel(const __grid_constant__ WriteParams p) {
+  allow_next_grid();
+  wait_prior_grid();
+  const WriteDyn& D = p.d;
+  const int gid = blockIdx.x * 16 + (threadIdx.x >> 4);  // (row, head) pair
+  const int t = threadIdx.x & 15;                          // 8-element slice
+  if (gid >= D.rows * p.hkv) return;
+  const int row = gid / p.hkv;
+  const int g = gid - row * p.hkv;
+  int ri = 0;
+  while (ri + 1 < D.nruns && D.runs[ri + 1].row0 <= row) ++ri;
+  const WriteRun& run = D.runs[ri];
+  const int pos = run.pos0 + (row - run.row0);
+  size_t src_row;
+  if (run.page_table) {
+    const int pid = __ldg(run.page_table + (pos >> 8));
+    if ((unsigned)pid >= (unsigned)p.num_pages) {
+      if (t == 0) flag_error(p.err_flag, kErrBadPage);
+      return;
+    }
+    src_row = ((size_t)pid * p.hkv + g) * kPage + (pos & (kPage - 1));
+  } else {
+    src_row = (size_t)g * run.slab_cap + pos;
+  }
+  const size_t dst = ((size_t)row * p.hkv + g) * kHeadDim + t * 8;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const uint8_t* base = static_cast<const uint8_t*>(which ? run.v_dst : run.k_dst);
+    uint4* out = reinterpret_cast<uint4*>(
+        const_cast<__nv_bfloat16*>(which ? p.v_rows : p.k_rows) + dst);
+    if (p.kv == kKvBf16) {
+      *out = *reinterpret_cast<const uint4*>(base + (src_row * kHeadDim + t * 8) * 2);
+      continue;
+    }
+    const float sc = __ldg((which ? p.v_scale : p.k_scale) + g);
+    uint32_t h[4];                                       // eight f16
+    float block = 1.f;
+    if (p.kv == kKvFp8) {
+      const uint2 w = *reinterpret_cast<const uint2*>(base + src_row * kHeadDim + t * 8);
+      h[0] = e4m3x2_to_f16x2((uint16_t)(w.x & 0xFFFF));
+      h[1] = e4m3x2_to_f16x2((uint16_t)(w.x >> 16));
+      h[2] = e4m3x2_to_f16x2((uint16_t)(w.y & 0xFFFF));
+      h[3] = e4m3x2_to_f16x2((uint16_t)(w.y >> 16));
+    } else {
+      e2m1x8_to_f16x8(*reinterpret_cast<const uint32_t*>(base + fp4_codes(src_row) + t * 4), h);
+      const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)base[fp4_scales(src_row) + (t >> 1)]);
+      block = __low2float(*reinterpret_cast<const __half2*>(&s2));
+    }
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+      f[2 * i] = __fmul_rn(__fmul_rn(v.x, block), sc);
+      f[2 * i + 1] = __fmul_rn(__fmul_rn(v.y, block), sc);
+    }
+    *out = pack8_bf16(f);
+  }
 }
 
 // Keep: CTA g handles kv head g of every pair.  The pairs' source and
@@ -126,19 +205,24 @@ __global__ void __launch_bounds__(256) write_kv_kernel(const __grid_constant__ W
 // written, so chains of moves within a call (2 -> 1, 5 -> 2) copy the rows
 // as they were.  A pair whose source or destination page id is out of range
 // is skipped and flagged.
+// 4-bit rows (FP4) are five pieces: four of codes and the scales' 8 bytes.
 constexpr int kKeepThreads = 1024;
+template <bool FP4>
 __global__ void __launch_bounds__(kKeepThreads)
     keep_kernel(const __grid_constant__ KeepParams p) {
-  extern __shared__ uint4 stash[];                 // [n][K, V][row_bytes / 16]
+  extern __shared__ uint4 stash[];                 // [n][K, V][cpr]
   __shared__ uint4* src_row[kMaxKeep][2];
   __shared__ uint4* dst_row[kMaxKeep][2];
+  __shared__ uint2* src_scale[FP4 ? kMaxKeep : 1][2];
+  __shared__ uint2* dst_scale[FP4 ? kMaxKeep : 1][2];
   allow_next_grid();
   wait_prior_grid();
   const int g = blockIdx.x;
-  const int cpr = p.row_bytes / 16;               // 16-byte chunks per row
-  auto row_ptr = [&](const KeepPair& kp, int which, int pos) -> uint4* {
+  const int cpr = FP4 ? 5 : p.row_bytes / 16;     // pieces (16-byte chunks) per row
+  auto row_ptr = [&](const KeepPair& kp, int which, int pos, uint2*& scale) -> uint4* {
     uint8_t* base;
     size_t idx;
+    scale = nullptr;
     if (kp.page_table) {
       const int pid = __ldg(kp.page_table + (pos >> 8));
       if ((unsigned)pid >= (unsigned)p.num_pages) return nullptr;
@@ -148,18 +232,27 @@ __global__ void __launch_bounds__(kKeepThreads)
       base = static_cast<uint8_t*>(which ? kp.v_slab : kp.k_slab);
       idx = (size_t)g * kp.slab_cap + pos;
     }
+    if (FP4) {
+      scale = reinterpret_cast<uint2*>(base + fp4_scales(idx));
+      return reinterpret_cast<uint4*>(base + fp4_codes(idx));
+    }
     return reinterpret_cast<uint4*>(base + idx * p.row_bytes);
   };
   for (int i = threadIdx.x; i < 2 * p.n; i += blockDim.x) {
     const KeepPair& kp = p.pairs[i >> 1];
-    uint4* s = row_ptr(kp, i & 1, kp.src);
-    uint4* d = row_ptr(kp, i & 1, kp.dst);
+    uint2 *ss, *ds;
+    uint4* s = row_ptr(kp, i & 1, kp.src, ss);
+    uint4* d = row_ptr(kp, i & 1, kp.dst, ds);
     if (!s || !d) {
       flag_error(p.err_flag, kErrBadPage);
       s = d = nullptr;
     }
     src_row[i >> 1][i & 1] = s;
     dst_row[i >> 1][i & 1] = d;
+    if (FP4) {
+      src_scale[i >> 1][i & 1] = ss;
+      dst_scale[i >> 1][i & 1] = ds;
+    }
   }
   __syncthreads();
   // Each thread issues its (up to) kUnroll loads before any shared store, so
@@ -174,7 +267,15 @@ __global__ void __launch_bounds__(kKeepThreads)
       v[u] = make_uint4(0, 0, 0, 0);
       if (i < total) {
         const uint4* s = src_row[i / (2 * cpr)][(i / cpr) & 1];
-        if (s) v[u] = s[i % cpr];
+        if (FP4 && i % cpr == 4) {
+          if (s) {
+            const uint2 c = *src_scale[i / (2 * cpr)][(i / cpr) & 1];
+            v[u].x = c.x;
+            v[u].y = c.y;
+          }
+        } else if (s) {
+          v[u] = s[i % cpr];
+        }
       }
     }
 #pragma unroll
@@ -186,7 +287,11 @@ __global__ void __launch_bounds__(kKeepThreads)
   __syncthreads();
   for (int i = threadIdx.x; i < total; i += blockDim.x) {
     uint4* d = dst_row[i / (2 * cpr)][(i / cpr) & 1];
-    if (d) d[i % cpr] = stash[i];
+    if (FP4 && i % cpr == 4) {
+      if (d) *dst_scale[i / (2 * cpr)][(i / cpr) & 1] = make_uint2(stash[i].x, stash[i].y);
+    } else if (d) {
+      d[i % cpr] = stash[i];
+    }
   }
 }
 
@@ -198,18 +303,26 @@ cudaError_t launch_write_kv(const WriteParams& p, cudaStream_t s) {
                : launch_pdl(write_kv_kernel<false>, dim3(grid), dim3(256), 0, s, p);
 }
 
+cudaError_t launch_read_kv(const WriteParams& p, cudaStream_t s) {
+  const int grid = (p.d.rows * p.hkv + 15) / 16;
+  if (grid == 0) return cudaSuccess;
+  return launch_pdl(read_kv_kernel, dim3(grid), dim3(256), 0, s, p);
+}
+
 cudaError_t launch_keep(const KeepParams& p, cudaStream_t s) {
   if (p.n == 0) return cudaSuccess;
+  if (p.row_bytes == kFp4CodeBytes + kFp4ScaleBytes)     // at most 40 KB of pieces
+    return launch_pdl(keep_kernel<true>, dim3(p.hkv), dim3(kKeepThreads), p.n * 2 * 80, s, p);
   const int smem = p.n * 2 * p.row_bytes;
   static PerDeviceOnce configured;
   if (smem > 48 * 1024) {
     const cudaError_t e = configured.run([] {
-      return cudaFuncSetAttribute(keep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      return cudaFuncSetAttribute(keep_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   kMaxKeep * 2 * 256);
     });
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(keep_kernel, dim3(p.hkv), dim3(kKeepThreads), smem, s, p);
+  return launch_pdl(keep_kernel<false>, dim3(p.hkv), dim3(kKeepThreads), smem, s, p);
 }
 
 }  // namespace tfpa
