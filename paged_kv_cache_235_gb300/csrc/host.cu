@@ -359,7 +359,7 @@ struct Sink {
     // the tensor-core verify launch's grid follows the streams' lengths
     if (device()) return TFPA_EINVAL;
     if (plan) return keep(tfpa_plan::kVerify, plan->verify, p, kv, tiles);
-    return dry_run() ? TFPA_OK : to_err(launch_verify(p, kv == kKvFp8, tiles, stream));
+    return dry_run() ? TFPA_OK : to_err(launch_verify(p, kv, tiles, stream));
   }
   int merge(const MergeParams& p) const {
     if (plan) return keep_dyn(tfpa_plan::kMerge, plan->merge, p, 0, 0);
@@ -445,6 +445,19 @@ int fill_maps(const tfpa_cache* c, const tfpa_seg* segs, const SourceSet& ss, bo
   }
   nsrc = 1 + ss.nslab;
   return TFPA_OK;
+}
+
+// Where each source's rows are: the pool, then the slabs in source order.
+// Returns the number of sources.
+template <typename P>
+int32_t fill_bases(const tfpa_cache* c, const tfpa_seg* segs, const SourceSet& ss, P* k, P* v) {
+  k[0] = c->k_pool;
+  v[0] = c->v_pool;
+  for (int i = 0; i < ss.nslab; ++i) {
+    k[i + 1] = segs[ss.slab_seg[i]].k_slab;
+    v[i + 1] = segs[ss.slab_seg[i]].v_slab;
+  }
+  return 1 + ss.nslab;
 }
 
 void fill_run(RunInfo& ri, const tfpa_seg& g, int src, int row0, int nrows, int pos0) {
@@ -661,9 +674,8 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
     bool fused = sliced && nv == 0 && sc->arrive && !anc && !sink.device();
     for (int r = 0; fused && r < nd; ++r) fused = p.d.runs[r].nsplit <= kFusedMergeMaxSplits;
     if (nd > 0) {
-      if (kv == kKvFp4)
-        p.nsrc = 1 + ss.nslab;          // read through the bases below
-      else if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 128, p.maps, p.nsrc)))
+      if (kv != kKvFp4 &&
+          (e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 128, p.maps, p.nsrc)))
         return e;
       p.q = static_cast<const __nv_bfloat16*>(q) + (size_t)base * hd;
       p.anc = anc ? anc + base : nullptr;   // the ancestor table shifts with the rows
@@ -675,15 +687,7 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
       const size_t rd = (size_t)c->hkv * kHeadDim;
       p.k_rows = k_rows ? static_cast<const __nv_bfloat16*>(k_rows) + (size_t)base * rd : nullptr;
       p.v_rows = v_rows ? static_cast<const __nv_bfloat16*>(v_rows) + (size_t)base * rd : nullptr;
-      if (k_rows || kv == kKvFp4) {
-        // where each source's rows are: the pool, then the slabs in source order
-        p.k_base[0] = c->k_pool;
-        p.v_base[0] = c->v_pool;
-        for (int i = 0; i < ss.nslab; ++i) {
-          p.k_base[i + 1] = segs[ss.slab_seg[i]].k_slab;
-          p.v_base[i + 1] = segs[ss.slab_seg[i]].v_slab;
-        }
-      }
+      if (k_rows || kv == kKvFp4) p.nsrc = fill_bases(c, segs, ss, p.k_base, p.v_base);
       p.arrive = fused ? sc->arrive + (size_t)srow * c->hq : nullptr;
       p.out = fused ? static_cast<__nv_bfloat16*>(out) + (size_t)base * hd : nullptr;
       p.lse = fused && lse ? lse + (size_t)base * c->hq : nullptr;
@@ -1158,7 +1162,7 @@ extern "C" int tfpa_plan_launch(const tfpa_plan* plan, cudaStream_t stream) {
         r = launch_decode_partial(plan->decode[en.index], en.kv, en.grid, stream);
         break;
       case tfpa_plan::kVerify:
-        r = launch_verify(plan->verify[en.index], en.kv == kKvFp8, en.grid, stream);
+        r = launch_verify(plan->verify[en.index], en.kv, en.grid, stream);
         break;
       case tfpa_plan::kMerge:
         r = launch_merge(plan->merge[en.index], stream);
@@ -1312,13 +1316,13 @@ extern "C" int tfpa_prefill(const tfpa_cache* c, const tfpa_seg* segs, int32_t n
   int e;
   if ((e = check_cache(c)) || (e = check_segs(c, segs, nseg))) return e;
   if (rows > 0 && (!q || !aligned(q, 16) || !out || !aligned(out, 16))) return TFPA_EINVAL;
-  if (c->dtype == TFPA_FP4_E2M1) return TFPA_EINVAL;
   if (max_rows_per_launch < 0 || !std::isfinite(scale) || !(scale > 0.f)) return TFPA_EINVAL;
   thread_local std::vector<Run> runs;   // reused by every call of this thread
   if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;
   if (rows == 0) return TFPA_OK;
   if ((e = check_device()) || (e = check_tma_source(q))) return e;
-  const bool fp8 = c->dtype == TFPA_FP8_E4M3;
+  const int kv = c->dtype;
+  const bool fp8 = kv == kKvFp8;
   const int G = c->hq / c->hkv;
   const int npairs = (G + 1) / 2;
   const int32_t cap = max_rows_per_launch > 0 ? max_rows_per_launch : INT32_MAX;
@@ -1350,7 +1354,10 @@ extern "C" int tfpa_prefill(const tfpa_cache* c, const tfpa_seg* segs, int32_t n
         taken = 0;
       }
     }
-    if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 128, p.maps, p.nsrc))) return e;
+    if (kv == kKvFp4)
+      p.nsrc = fill_bases(c, segs, ss, p.k_base, p.v_base);
+    else if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 128, p.maps, p.nsrc)))
+      return e;
     if ((e = get_qmap(static_cast<const __nv_bfloat16*>(q) + (size_t)base * hd, c->hq, nrows, 1,
                       kPrefillTileRows,
                       &p.qmap)))
@@ -1373,7 +1380,7 @@ extern "C" int tfpa_prefill(const tfpa_cache* c, const tfpa_seg* segs, int32_t n
     // tiles), heaviest tiles first.
     record(3, base, nrows, nr, tiles, 2 * tiles, (int64_t)base * hd, (int64_t)base * hd);
     if (!dry_run())
-      if ((e = to_err(launch_prefill(p, fp8, tiles, stream)))) return e;
+      if ((e = to_err(launch_prefill(p, kv, tiles, stream)))) return e;
   }
   return TFPA_OK;
 }

@@ -218,6 +218,8 @@ struct PrefillParams {
   int32_t rows;
   int32_t max_splits;         // verify
   float scale_log2;
+  const void* k_base[kMaxSources];   // 4-bit caches: read by bulk copies, no maps
+  const void* v_base[kMaxSources];
 };
 
 // Page-table staging: ids written into a device page table on the stream.
@@ -257,7 +259,7 @@ cudaError_t launch_copy(const CopyParams& p, int npages, cudaStream_t s);
 cudaError_t launch_decode_partial(const DecodeParams& p, int kv, int grid, cudaStream_t s);
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t s);
 // Prefill launches a cluster of two CTAs per tile; verify one CTA per tile.
-cudaError_t launch_prefill(const PrefillParams& p, bool fp8, int tiles, cudaStream_t s);
-cudaError_t launch_verify(const PrefillParams& p, bool fp8, int tiles, cudaStream_t s);
+cudaError_t launch_prefill(const PrefillParams& p, int kv, int tiles, cudaStream_t s);
+cudaError_t launch_verify(const PrefillParams& p, int kv, int tiles, cudaStream_t s);
 
 }  // namespace tfpa

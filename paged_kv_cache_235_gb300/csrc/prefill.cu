@@ -28,10 +28,11 @@
 //               max/sum, P written back over S as bf16 (f16 for e4m3
 //               caches), O rescaled in TMEM only when the running max grows
 //               by more than 2^8.
-//   warps 12-15 (e4m3 caches only) converters: TMA lands e4m3 K/V tiles in
+//   warps 12-15 (e4m3 and 4-bit caches) converters: TMA lands e4m3 K/V tiles
+//               (4 bits: bulk copies land half-blocks of codes and scales) in
 //               a staging buffer; these warps write the exact f16 operand
 //               tiles (and zero V rows past the stream's end).
-// With an e4m3 cache the MMAs run in f16: each softmax thread first turns its
+// With an e4m3 or 4-bit cache the MMAs run in f16: each softmax thread first turns its
 // Q row into f16 scaled by a power of two (exact for every element within
 // 2^28 of the row's largest), and the K and V scales are applied to the
 // scores and to the output.  Verify tiles on an e4m3 cache instead split Q
@@ -63,10 +64,10 @@ namespace {
 
 constexpr int kTileRows = 128;
 constexpr int kTileKeys = 128;
-// bf16: warps 0-11.  e4m3: warps 0-15, warps 12-15 converting the staged
-// e4m3 tiles (one warp per SM sub-partition, beside the softmax warps).
-template <bool FP8>
-constexpr int threads_of() { return FP8 ? 512 : 384; }
+// bf16: warps 0-11.  F16 (e4m3, 4 bits): warps 0-15, warps 12-15 converting
+// the staged tiles (one warp per SM sub-partition, beside the softmax warps).
+template <bool F16>
+constexpr int threads_of() { return F16 ? 512 : 384; }
 constexpr int kConvWarp0 = 12;
 constexpr int kConvWarps = 4;
 constexpr int kOffQ = 0;                 // 2 heads x [128 rows][128] 16-bit = 64 KB
@@ -92,7 +93,7 @@ __device__ __forceinline__ int kstage8_off(int i) { return kOffK + i * 16384; }
 // stage n mod 3): K stage 2 is the unused second Q tile, V stage 2 follows
 // the prefill V ring.
 __device__ __forceinline__ int kstage16_off(int t) { return t < 2 ? kOffK + t * 32768 : kOffQ2; }
-template <bool FP8>
+template <bool F16>
 struct Layout {
   static constexpr int kOffBar = 229376;
   // Verify: the Q rows' scale factors (e4m3 caches; 128 floats) and slot
@@ -114,7 +115,7 @@ constexpr uint32_t kTmemCols = 512;
 // thread's staging loads at once (1.7 % on prompt chunks, 1 % on verify
 // tiles, against 56 / 200 / 200 / 56 with four at a time); it uses each
 // sub-partition's 16,384 registers exactly.
-template <bool FP8>
+template <bool F16>
 struct Regs;
 template <>
 struct Regs<true> {
@@ -124,9 +125,9 @@ template <>
 struct Regs<false> {
   static constexpr int kLow = 64, kHigh = 216, kConv = 0, kLaunch = 168;
 };
-template <bool FP8>
+template <bool F16>
 constexpr int regs_split() {
-  return 128 * (Regs<FP8>::kLow + 2 * Regs<FP8>::kHigh + Regs<FP8>::kConv);
+  return 128 * (Regs<F16>::kLow + 2 * Regs<F16>::kHigh + Regs<F16>::kConv);
 }
 static_assert(regs_split<true>() <= 512 * Regs<true>::kLaunch, "register split");
 static_assert(regs_split<false>() <= 384 * Regs<false>::kLaunch, "register split");
@@ -283,9 +284,10 @@ __device__ __forceinline__ int v_zero_from(const RunInfo& ru, int j, bool page_b
 }
 
 
-template <bool FP8, bool VERIFY>
+template <int KV, bool VERIFY>
 __device__ void producer(const PrefillParams& p, const RunInfo& ru, const Tile& x,
                          const TileGeom& gm, uint8_t* smem, const Bars& b) {
+  constexpr bool F16 = KV != kKvBf16;
   const CUtensorMap* mk = &p.maps[ru.src].k;
   const CUtensorMap* mv = &p.maps[ru.src].v;
   if (gm.nkt == 0) return;
@@ -336,13 +338,22 @@ __device__ void producer(const PrefillParams& p, const RunInfo& ru, const Tile& 
   // staging tile that the converters move on, K and V in their order.
   int staged_k = 0, staged_v = 0;       // e4m3: staging loads issued
   auto load = [&](bool is_v, int stage, uint32_t parity, int y) {
-    if (FP8) {
+    if (F16) {
       int& n = is_v ? staged_v : staged_k;
       uint64_t* empty = is_v ? b.v8_empty : b.k8_empty;
       uint64_t* full = is_v ? b.v8_full : b.k8_full;
       if (!mbar_wait_or_abort(empty, (n & 1) ^ 1, p.err_flag, b.abort)) return false;
-      mbar_arrive_expect_tx(full, 16384);
-      tma_load_2d(smem + stage8_off(is_v), is_v ? mv : mk, 0, y, full);
+      if (KV == kKvFp4) {
+        // a half-block: 128 rows' codes and scales in one copy
+        mbar_arrive_expect_tx(full, kFp4HalfBytes);
+        bulk_load(smem + stage8_off(is_v),
+                  static_cast<const uint8_t*>(is_v ? p.v_base[ru.src] : p.k_base[ru.src]) +
+                      (size_t)(y / kHalfRows) * kFp4HalfBytes,
+                  kFp4HalfBytes, full);
+      } else {
+        mbar_arrive_expect_tx(full, 16384);
+        tma_load_2d(smem + stage8_off(is_v), is_v ? mv : mk, 0, y, full);
+      }
       ++n;
       return true;
     }
@@ -364,7 +375,7 @@ __device__ void producer(const PrefillParams& p, const RunInfo& ru, const Tile& 
                   : (stage == 2 ? last_k2 : stage ? last_k1 : last_k0);
     w = (int)ph;
   };
-  if (VERIFY && FP8) {
+  if (VERIFY && F16) {
     // Step jj, slot hh: K into e4m3 stage 2 hh + (jj & 1), V into staging
     // tile 2 hh + (jj & 1), each at phase (jj >> 1) & 1; K of both slots,
     // then V of both.  last_k*, last_v*: each slot's last step loaded.
@@ -416,7 +427,7 @@ __device__ void producer(const PrefillParams& p, const RunInfo& ru, const Tile& 
   if (*b.abort) {
     // Let this CTA's loads in flight land before it exits.
     mbar_wait(b.q_full, 0, p.err_flag);
-    if (VERIFY && FP8) {
+    if (VERIFY && F16) {
       // each slot's last two steps loaded (buffers alternate by step)
       const int lasts[4] = {last_k0, last_k1, last_v0, last_v1};
 #pragma unroll
@@ -429,7 +440,7 @@ __device__ void producer(const PrefillParams& p, const RunInfo& ru, const Tile& 
           if (jj >= 0) mbar_wait(full + 2 * hh + (jj & 1), (uint32_t)((jj >> 1) & 1), p.err_flag);
         }
       }
-    } else if (FP8) {
+    } else if (F16) {
       if (staged_k > 0) mbar_wait(b.k8_full, (uint32_t)((staged_k - 1) & 1), p.err_flag);
       if (staged_v > 0) mbar_wait(b.v8_full, (uint32_t)((staged_v - 1) & 1), p.err_flag);
     } else {
@@ -483,11 +494,42 @@ __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, i
   }
 }
 
-// Warps 12-15 for e4m3 caches: staging -> f16 operand stages, in the order
+// The same for a staged half-block of a 4-bit cache (128 rows' codes, then
+// their scales): code * block scale, exact in f16.  A thread turns 32 head
+// dims of a row at a time.  Its lane fixes the row and which quarter of a
+// 64-column half it takes, the loop the half, so that eight neighbouring
+// lanes' 16-byte stores fall into eight different bank groups.
+__device__ __forceinline__ void convert_tile_fp4(const uint8_t* src, uint8_t* dst, int z0,
+                                                 int t) {
+  const uint32_t sb = smem_u32(src), db = smem_u32(dst);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int hf = k & 1, cc = t & 1;
+    const int row = (t >> 1) + 64 * (k >> 1), c = 2 * hf + cc;   // head dims 32 c .. + 31
+    const uint4 w = lds128(sb + row * kFp4CodeBytes + 16 * c);
+    uint32_t s8 = lds16(sb + kFp4ScaleOff + row * kFp4ScaleBytes + 2 * c);
+    if (row >= z0) s8 = 0;
+    const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)s8);
+    const uint32_t sc[2] = {prmt(s2, s2, 0x1010), prmt(s2, s2, 0x3232)};
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint32_t h[4];
+      e2m1x8_to_f16x8(ws[u], h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = hmul2(h[j], sc[u >> 1]);
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                       swz128(db + hf * 16384u, row, 4 * cc + u)),
+                   "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+    }
+  }
+}
+
+// Warps 12-15 for e4m3 and 4-bit caches: staging -> f16 operand stages, in the order
 // the producer fills the staging tiles.  Prefill: K and V of each key tile
 // through one staging tile each.  Verify: V only (K feeds 8-bit MMAs), slot
 // hh's step jj from staging tile 2 hh + (jj & 1).
-template <bool VERIFY>
+template <int KV, bool VERIFY>
 __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileGeom& gm,
                           uint8_t* smem, const Bars& b) {
   const int t = threadIdx.x - kConvWarp0 * 32;   // 0..127
@@ -500,7 +542,11 @@ __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileG
     uint64_t* full = is_v ? &b.v_full[s] : &b.k_full[s];
     if (!mbar_wait_or_abort(full8, ph8, p.err_flag, b.abort)) return false;
     if (!mbar_wait_or_abort(empty, ph ^ 1, p.err_flag, b.abort)) return false;
-    convert_tile(smem + src, smem + (is_v ? kOffV : kOffK) + s * 32768, is_v ? z0 : kTileKeys, t);
+    uint8_t* dst = smem + (is_v ? kOffV : kOffK) + s * 32768;
+    if (KV == kKvFp4)
+      convert_tile_fp4(smem + src, dst, is_v ? z0 : kTileKeys, t);
+    else
+      convert_tile(smem + src, dst, is_v ? z0 : kTileKeys, t);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
@@ -538,20 +584,21 @@ __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileG
   }
 }
 
-template <bool FP8, bool VERIFY>
+template <int KV, bool VERIFY>
 __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const TileGeom& gm,
                            uint8_t* smem, uint32_t tmem, const Bars& b) {
+  constexpr bool F16 = KV != kKvBf16;
   const int lane = threadIdx.x & 31;
   const bool leader = lane == 0;
-  constexpr uint32_t kIdescQK = umma::idesc_f16(128, 128, !FP8, false);
-  constexpr uint32_t kIdescPV = umma::idesc_f16(128, 128, !FP8, true);
+  constexpr uint32_t kIdescQK = umma::idesc_f16(128, 128, !F16, false);
+  constexpr uint32_t kIdescPV = umma::idesc_f16(128, 128, !F16, true);
   const uint32_t qb = smem_u32(smem + kOffQ);
   const uint32_t kb = smem_u32(smem + kOffK);
   const uint32_t vb = smem_u32(smem + kOffV);
 
   constexpr uint32_t kIdescQK8 = umma::idesc_e4m3(128, 128);
   auto issue_s = [&](int hh, int s) {     // S_hh = Q_hh K_s^T (verify: one Q tile)
-    if constexpr (VERIFY && FP8) {
+    if constexpr (VERIFY && F16) {
       // S_hh = Q_hi K^T + Q_lo K^T over e4m3 K stage s (K = 32 per MMA)
       const uint32_t k8 = smem_u32(smem + kstage8_off(s));
 #pragma unroll
@@ -591,12 +638,12 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
     // Slot hh, step jj.  bf16: K and V of tile n = 2 jj + hh in stage n mod
     // 3 at phase (n / 3) & 1.  e4m3: K in e4m3 stage 2 hh + (jj & 1) at phase
     // (jj >> 1) & 1, V in 16-bit stage hh at phase jj & 1.
-    auto kst = [&](int hh, int jj) { return FP8 ? 2 * hh + (jj & 1) : (2 * jj + hh) % 3; };
+    auto kst = [&](int hh, int jj) { return F16 ? 2 * hh + (jj & 1) : (2 * jj + hh) % 3; };
     auto kph = [&](int hh, int jj) {
-      return (uint32_t)(FP8 ? (jj >> 1) & 1 : ((2 * jj + hh) / 3) & 1);
+      return (uint32_t)(F16 ? (jj >> 1) & 1 : ((2 * jj + hh) / 3) & 1);
     };
-    auto vst = [&](int hh, int jj) { return FP8 ? hh : (2 * jj + hh) % 3; };
-    auto vph = [&](int hh, int jj) { return (uint32_t)(FP8 ? jj & 1 : ((2 * jj + hh) / 3) & 1); };
+    auto vst = [&](int hh, int jj) { return F16 ? hh : (2 * jj + hh) % 3; };
+    auto vph = [&](int hh, int jj) { return (uint32_t)(F16 ? jj & 1 : ((2 * jj + hh) / 3) & 1); };
     bool ok = mbar_wait_or_abort(b.q_ready, 0, p.err_flag, b.abort);
     for (int hh = 0; ok && hh < 2; ++hh) {
       if (slot_tiles<true>(gm, hh) == 0) continue;
@@ -619,7 +666,7 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
         const bool page_bad = hh ? pc1.bad(j) : pc0.bad(j);
         const int vs = vst(hh, jj);
         if (!(ok = mbar_wait_or_abort(&b.v_full[vs], vph(hh, jj), p.err_flag, b.abort))) break;
-        if (!FP8) {
+        if (!F16) {
           const int z0 = v_zero_from(ru, j, page_bad);
           if (z0 < kTileKeys) zero_v_rows(smem + kOffV + vs * 32768, z0, lane);
         }
@@ -678,7 +725,7 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
     const uint32_t ph1 = ((jj + 1) >> 1) & 1;
     const bool more = jj + 1 < gm.nkt;
     if (!(ok = mbar_wait_or_abort(&b.v_full[s], ph, p.err_flag, b.abort))) break;
-    if (!FP8) {   // the e4m3 converters zero these rows themselves
+    if (!F16) {   // the e4m3 converters zero these rows themselves
       const int z0 = v_zero_from(ru, j, page_bad);
       if (z0 < kTileKeys) zero_v_rows(smem + kOffV + s * 32768, z0, lane);
     }
@@ -833,10 +880,11 @@ __device__ __forceinline__ uint32_t part_ml(uint32_t smem_base, int hh, int r) {
   return smem_base + kOffQ + (hh * kTileRows + r) * 8;
 }
 
-template <bool FP8, bool VERIFY>
+template <int KV, bool VERIFY>
 __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Tile& x,
                              const TileGeom& gm, uint32_t rank, int hh, uint8_t* smem,
                              uint32_t tmem, const Bars& b) {
+  constexpr bool F16 = KV != kKvBf16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = 32 * (warp & 3) + lane;                 // row of the tile = TMEM lane
   const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
@@ -862,11 +910,11 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
       __brevll(tree && valid ? __ldg(p.anc + ru.row0 + gm.row_lo + rho) : ~0ull);
   float sl2 = p.scale_log2;
   bool ok = true;
-  if (FP8 && gm.nkt > 0) {
+  if (F16 && gm.nkt > 0) {
     // Prefill: each slot's warps turn their head's Q rows into f16.  Verify:
     // slot A's warps turn the one Q tile, publish each row's factor, and
     // slot B's take it once they see the tile ready.
-    float* down_s = reinterpret_cast<float*>(smem + Layout<FP8>::kOffDown);
+    float* down_s = reinterpret_cast<float*>(smem + Layout<F16>::kOffDown);
     if (!VERIFY || hh == 0) {
       ok = mbar_wait_or_abort(b.q_full, 0, p.err_flag, b.abort);
       if (ok) {
@@ -963,7 +1011,7 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
                     __uint_as_float(sv[(i0 + 1) >> 5][(i0 + 1) & 31])}, sc2, nb2);
       const f2 e = {fast_exp2(t.x), fast_exp2(t.y)};
       acc = fadd2(acc, e);
-      sv[k >> 5][k & 31] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+      sv[k >> 5][k & 31] = F16 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
     }
     const float rs = acc.x + acc.y;
     umma::tmem_st32(tS, sv[0]);
@@ -999,7 +1047,7 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
     // In half mode slot B's lanes are not slot A's: slot B's threads also
     // leave their O rows in shared memory (over the V stages, free once the
     // MMAs are done; 16-byte chunks permuted by vector against conflicts).
-    float2* ml_s = reinterpret_cast<float2*>(smem + Layout<FP8>::kOffMl);
+    float2* ml_s = reinterpret_cast<float2*>(smem + Layout<F16>::kOffMl);
     const uint32_t obuf = smem_u32(smem + kOffV) + (uint32_t)v * 512u;
     if (hh == 1) {
       if (mine) ml_s[v] = make_float2(m_run, l);
@@ -1031,7 +1079,7 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
     const float mx = fmaxf(m_run, mlb.x);
     const float a0 = m_run == -INFINITY ? 0.f : fast_exp2(m_run - mx);
     const float a1 = mlb.x == -INFINITY ? 0.f : fast_exp2(mlb.x - mx);
-    const float vs = FP8 ? __ldg(p.v_scale + x.g) : 1.f;
+    const float vs = F16 ? __ldg(p.v_scale + x.g) : 1.f;
     const float c0 = a0 * vs, c1 = a1 * vs;
     const int nb = slot_tiles<true>(gm, 1);
     const size_t slot =
@@ -1119,7 +1167,7 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
   const float a0 = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_all);
   const float a1 = ml1.x == -INFINITY ? 0.f : fast_exp2(ml1.x - m_all);
   const float l_all = __fmaf_rn(l, a0, __fmul_rn(ml1.y, a1));
-  const float inv = (l_all > 0.f ? 1.f / l_all : 0.f) * (FP8 ? __ldg(p.v_scale + x.g) : 1.f);
+  const float inv = (l_all > 0.f ? 1.f / l_all : 0.f) * (F16 ? __ldg(p.v_scale + x.g) : 1.f);
   const float c0 = a0 * inv, c1 = a1 * inv;
   const int h = x.g * p.group + 2 * x.hp + hh;
   const bool write = valid && (2 * x.hp + hh) < p.group;
@@ -1162,22 +1210,23 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
         l_all > 0.f ? (m_all + log2f(l_all)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <bool FP8, bool VERIFY>
-__global__ void __launch_bounds__(threads_of<FP8>(), 1)
+template <int KV, bool VERIFY>
+__global__ void __launch_bounds__(threads_of<KV != kKvBf16>(), 1)
     prefill_kernel(const __grid_constant__ PrefillParams p) {
+  constexpr bool F16 = KV != kKvBf16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Layout<FP8>::kOffBar);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Layout<F16>::kOffBar);
   Bars b;
   b.q_full = bars + 0;
-  b.q_ready = FP8 ? bars + 1 : bars + 0;
+  b.q_ready = F16 ? bars + 1 : bars + 0;
   // Verify with an e4m3 cache: four K stages (bars 2-5 full, 10-13 empty)
   // and four V staging tiles (24-27 full, 28-31 empty); no K staging.
   // Verify with a bf16 cache: rings of three, K full 24-26 and empty 27-29,
   // V full 2-4 and empty 5-7.
-  constexpr bool kDirectK = VERIFY && FP8;
-  constexpr bool kRing3 = VERIFY && !FP8;
+  constexpr bool kDirectK = VERIFY && F16;
+  constexpr bool kRing3 = VERIFY && !F16;
   b.k_full = kRing3 ? bars + 24 : bars + 2;
   b.k_empty = kDirectK ? bars + 10 : kRing3 ? bars + 27 : bars + 4;
   b.v_full = kRing3 ? bars + 2 : bars + 6;
@@ -1197,7 +1246,7 @@ __global__ void __launch_bounds__(threads_of<FP8>(), 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    const uint32_t stage_arrivals = FP8 ? kConvWarps : 1;   // the converters, or the producer
+    const uint32_t stage_arrivals = F16 ? kConvWarps : 1;   // the converters, or the producer
     mbar_init(b.q_full, 1);
     mbar_init(bars + 1, VERIFY ? 4 : 8);           // q_ready: the (slot A) softmax warps
     for (int i = 0; i < 2; ++i) {
@@ -1220,7 +1269,7 @@ __global__ void __launch_bounds__(threads_of<FP8>(), 1)
         mbar_init(&b.k_full[i], stage_arrivals);
         mbar_init(&b.k_empty[i], 1);
       }
-      if (FP8) {
+      if (F16) {
         mbar_init(b.k8_full, 1);
         mbar_init(b.k8_empty, kConvWarps);
         mbar_init(b.v8_full, 1);
@@ -1236,7 +1285,7 @@ __global__ void __launch_bounds__(threads_of<FP8>(), 1)
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&p.qmap);
-    for (int i = 0; i < p.nsrc; ++i) {
+    for (int i = 0; KV != kKvFp4 && i < p.nsrc; ++i) {
       tma_prefetch_desc(&p.maps[i].k);
       tma_prefetch_desc(&p.maps[i].v);
     }
@@ -1257,18 +1306,18 @@ __global__ void __launch_bounds__(threads_of<FP8>(), 1)
   const TileGeom gm = geom_of<VERIFY>(p, ru, x, rank);
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<FP8>::kLow));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<F16>::kLow));
     if (warp == 0) {
-      if (lane == 0) producer<FP8, VERIFY>(p, ru, x, gm, smem, b);
+      if (lane == 0) producer<KV, VERIFY>(p, ru, x, gm, smem, b);
     } else if (warp == 1) {
-      mma_issuer<FP8, VERIFY>(p, ru, gm, smem, tmem, b);
+      mma_issuer<KV, VERIFY>(p, ru, gm, smem, tmem, b);
     }
   } else if (warp < kConvWarp0) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<FP8>::kHigh));
-    softmax_role<FP8, VERIFY>(p, ru, x, gm, rank, (warp - 4) >> 2, smem, tmem, b);
-  } else if (FP8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<FP8>::kConv));
-    converter<VERIFY>(p, ru, gm, smem, b);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<F16>::kHigh));
+    softmax_role<KV, VERIFY>(p, ru, x, gm, rank, (warp - 4) >> 2, smem, tmem, b);
+  } else if (F16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<F16>::kConv));
+    converter<KV, VERIFY>(p, ru, gm, smem, b);
   }
   umma::fence_before_sync();
   __syncthreads();
@@ -1279,38 +1328,43 @@ __global__ void __launch_bounds__(threads_of<FP8>(), 1)
   }
 }
 
-template <bool FP8, bool VERIFY>
+template <int KV, bool VERIFY>
 cudaError_t launch(const PrefillParams& p, int tiles, cudaStream_t s) {
+  constexpr bool F16 = KV != kKvBf16;
   static PerDeviceOnce configured;
   const cudaError_t e = configured.run([] {
     // The register split only works if the block launches with at least the
     // registers it hands out; otherwise setmaxnreg.inc would wait forever.
     cudaFuncAttributes attr;
-    cudaError_t r = cudaFuncGetAttributes(&attr, prefill_kernel<FP8, VERIFY>);
+    cudaError_t r = cudaFuncGetAttributes(&attr, prefill_kernel<KV, VERIFY>);
     if (r != cudaSuccess) return r;
-    if (attr.numRegs * threads_of<FP8>() < regs_split<FP8>()) return cudaErrorInvalidValue;
-    return cudaFuncSetAttribute(prefill_kernel<FP8, VERIFY>,
+    if (attr.numRegs * threads_of<F16>() < regs_split<F16>()) return cudaErrorInvalidValue;
+    return cudaFuncSetAttribute(prefill_kernel<KV, VERIFY>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Layout<FP8>::kSmemBytes);
+                                Layout<F16>::kSmemBytes);
   });
   if (e != cudaSuccess) return e;
   if (VERIFY)
-    return launch_pdl(prefill_kernel<FP8, VERIFY>, dim3(tiles), dim3(threads_of<FP8>()),
-                      Layout<FP8>::kSmemBytes, s, p);
-  return launch_pdl_cluster(prefill_kernel<FP8, VERIFY>, dim3(2 * tiles),
-                            dim3(threads_of<FP8>()), Layout<FP8>::kSmemBytes, s, p, 2);
+    return launch_pdl(prefill_kernel<KV, VERIFY>, dim3(tiles), dim3(threads_of<F16>()),
+                      Layout<F16>::kSmemBytes, s, p);
+  return launch_pdl_cluster(prefill_kernel<KV, VERIFY>, dim3(2 * tiles),
+                            dim3(threads_of<F16>()), Layout<F16>::kSmemBytes, s, p, 2);
 }
 
 }  // namespace
 
-cudaError_t launch_prefill(const PrefillParams& p, bool fp8, int tiles, cudaStream_t s) {
+cudaError_t launch_prefill(const PrefillParams& p, int kv, int tiles, cudaStream_t s) {
   if (tiles <= 0) return cudaSuccess;
-  return fp8 ? launch<true, false>(p, tiles, s) : launch<false, false>(p, tiles, s);
+  switch (kv) {
+    case kKvBf16: return launch<kKvBf16, false>(p, tiles, s);
+    case kKvFp8: return launch<kKvFp8, false>(p, tiles, s);
+    default: return launch<kKvFp4, false>(p, tiles, s);
+  }
 }
 
-cudaError_t launch_verify(const PrefillParams& p, bool fp8, int tiles, cudaStream_t s) {
+cudaError_t launch_verify(const PrefillParams& p, int kv, int tiles, cudaStream_t s) {
   if (tiles <= 0) return cudaSuccess;
-  return fp8 ? launch<true, true>(p, tiles, s) : launch<false, true>(p, tiles, s);
+  return kv == kKvFp8 ? launch<kKvFp8, true>(p, tiles, s) : launch<kKvBf16, true>(p, tiles, s);
 }
 
 }  // namespace tfpa

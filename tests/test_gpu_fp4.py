@@ -413,3 +413,80 @@ def test_offsets_past_32_bits():
     ref, _, tol, _ = attend64(c.fill().cache, c.segs, q, [0], [599], SCALE)
     assert_within(f64(out), ref, tol, "far pages")
     assert bool((kp[num - 1] != 0).any()) and not bool((kp[num - 3] != 0).any())
+
+
+# ---------------------------------------------------------------- prompt chunks
+def prefill(c, q, rs, rp, max_rows=0, segs=None):
+    out = torch.full((len(rs), c.hq, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((len(rs), c.hq), float("nan"), device="cuda")
+    B.tfpa_prefill(c.gcache, segs or c.gsegs, dev_bf16(q), rs, rp, SCALE, out, lse, max_rows_per_launch=max_rows)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (3, 3), (5, 1)])
+@pytest.mark.parametrize("prefix,chunk", [(0, 1), (0, 128), (0, 129), (300, 257), (1000, 70), (127, 130), (513, 1)])
+def test_prompt_chunks(hq, hkv, prefix, chunk):
+    L = prefix + chunk
+    c = Fp4Case([L, L], [True, False], hq, hkv, seed=41).fill().upload()
+    rs, rp = last_rows([L, L], chunk)
+    q = c.q(len(rs))
+    out, lse = prefill(c, q, rs, rp)
+    check(c, q, rs, rp, out, lse, f"chunk {prefix}+{chunk}")
+    o2, l2 = prefill(c, q, rs, rp, max_rows=128)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_prompt_chunk_ignores_unwritten_rows():
+    c = Fp4Case([500], [True], seed=42).fill()
+    for g in range(2):
+        for w in ("k", "v"):
+            fp4.set_rows(c.cache, c.segs[0], w, g, np.arange(333, 500), np.full((167, 64), 0x7F, np.uint8),
+                         np.full((167, 8), 0x7F, np.uint8))
+    c.upload()
+    seg = [B.Seg(333, page_table=c.gsegs[0].page_table)]
+    q = c.q(200)
+    rs, rp = np.zeros(200, np.int32), np.arange(133, 333)
+    out, lse = prefill(c, q, rs, rp, segs=seg)
+    check(c, q, rs, rp, out, lse, "unwritten")
+
+
+def test_prompt_chunk_with_a_bad_page():
+    c = Fp4Case([700], [True], seed=43).fill().upload()
+    t = c.gsegs[0].page_table.clone()
+    t[1] = -1
+    q = c.q(130)
+    rs, rp = np.zeros(130, np.int32), np.arange(570, 700)
+    out, lse = prefill(c, q, rs, rp, segs=[B.Seg(700, page_table=t)])
+    assert int(c.err.item()) == 1 and torch.isfinite(out.float()).all()
+    c.err.zero_()
+    ref, _ = decode(c, q, rs, rp, segs=[B.Seg(700, page_table=t)], cap=130)
+    assert (out.float() - ref.float()).abs().max() < 0.05
+    c.err.zero_()
+
+
+def test_a_stream_served_in_four_bits():
+    """A prompt stored with its rotary positions in two chunks, each attended, then four tokens appended:
+    every output against the formula on the bytes the cache holds."""
+    from paged_kv_cache_235_gb300 import workloads as wl
+    c = Fp4Case([704], [True], seed=44).upload()
+    cos, sin = wl.rope_table(1e4, 1024)
+    cos, sin = dev(cos), dev(sin)
+    k, v = dev_bf16(c.k_bits[0].transpose(1, 0, 2)), dev_bf16(c.v_bits[0].transpose(1, 0, 2))
+    q = c.q(704)
+    t = c.gsegs[0].page_table
+    got = []
+    for a, b in ((0, 300), (300, 700)):
+        at = np.arange(a, b)
+        B.tfpa_write_kv_rope(c.gcache, [B.Seg(b, page_table=t)], k[a:b], v[a:b], np.zeros(b - a), at, cos, sin)
+        got.append(prefill(c, q[a:b], np.zeros(b - a), at, segs=[B.Seg(b, page_table=t)]))
+    sc = B.make_scratch(4, 8)
+    for p in range(700, 704):
+        out, lse = torch.empty(1, 8, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(1, 8, device="cuda")
+        B.tfpa_decode_append(c.gcache, [B.Seg(p + 1, page_table=t)], k[p:p + 1], v[p:p + 1], dev_bf16(q[p:p + 1]), [0], [p],
+                             SCALE, sc, out, lse)
+        got.append((out, lse))
+    torch.cuda.synchronize()
+    c.cache.k_pool, c.cache.v_pool = c.k_pool.cpu().numpy(), c.v_pool.cpu().numpy()
+    out, lse = torch.cat([o for o, _ in got]), torch.cat([x for _, x in got])
+    check(c, q, np.zeros(704, int), np.arange(704), out, lse, "served")
