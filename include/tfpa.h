@@ -494,6 +494,65 @@ int tfpa_prefill(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
                  int32_t rows, float softmax_scale, int32_t max_rows_per_launch,
                  void* out, float* lse, cudaStream_t stream);
 
+/* ---- Eviction by accumulated attention weight ------------------------------
+ * A long stream keeps the keys its rows attend to: their weights are summed
+ * up as the stream is served, and from time to time all but the keys of
+ * largest sum leave the cache, each kv head choosing its own.  None of the
+ * TensorFold sources has a counterpart to this.
+ *
+ * tfpa_key_mass adds the attention weights of the call's rows to the keys'
+ * sums.  For every segment s that has a row in the call, kv head g and key j
+ * < seq_len:
+ *   mass[s][g][j] = decay mass[s][g][j]
+ *                 + sum over the segment's rows r with row_pos[r] >= j and the
+ *                   query heads h of g of exp(softmax_scale q_rh.k_j - lse[r][h])
+ * so with lse as tfpa_decode or tfpa_prefill left it for the same rows and
+ * cache, a row adds 1 per query head in all.  The sum's order is fixed, so the
+ * bytes are too.
+ *   q    : DEVICE bf16 [rows][hq][128], 16-byte aligned (any memory the GPU
+ *          can read); lse: DEVICE float [rows][hq] (a row with lse = -inf adds
+ *          nothing).
+ *   mass : DEVICE float [nseg][hkv][mass_cap], planes by the segment's index
+ *          in the call; zero before a stream's first call.  Entries from
+ *          seq_len on, and segments without rows, are left as they are.
+ *          mass_cap >= seq_len of every segment used (TFPA_ECAPACITY).
+ *   decay: finite and >= 0; 0 does not read the old sums.
+ * K is read once (V not at all).  Keys of a page whose id is out of range keep
+ * their entries and OR 1 into cache->err_flag.  Rows may come in any order; a
+ * segment's rows count together however they are grouped. */
+int tfpa_key_mass(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg, const void* q,
+                  const float* lse, const int32_t* row_seg, const int32_t* row_pos, int32_t rows,
+                  float softmax_scale, float decay, float* mass, int32_t mass_cap,
+                  cudaStream_t stream);
+
+/* tfpa_evict_kv cuts every segment s of the call to keep[s] keys (HOST
+ * int32[nseg], 1 <= keep[s] <= seq_len, TFPA_ERANGE), for each kv head those
+ * that come first in this order: positions below `sink` and positions from
+ * next_pos[s] - recent on; then larger mass (a NaN counts as largest); then
+ * the lower slot.  The kept keys are packed into slots [0, keep[s]) in place:
+ * a kept key below keep[s] stays in its slot, and the evicted slots below
+ * keep[s], ascending, take the kept keys behind it, ascending (K and V rows,
+ * mass and key_pos; the stored bytes unchanged).  mass becomes 0 and key_pos
+ * -1 in [keep[s], seq_len).  The stream goes on with seq_len = keep[s]: its
+ * next row is stored at that slot, with its own rotary position.
+ *   key_pos : DEVICE int32 [nseg][hkv][mass_cap], the position that each
+ *             slot's key has in its stream; NULL: its slot.  Only read and
+ *             moved here: the caller writes a new row's entry.
+ *   next_pos: HOST int32[nseg], the position the stream's next row will have;
+ *             NULL: seq_len.
+ *   sink, recent >= 0, with sink + recent <= keep[s] where keep[s] < seq_len
+ *             (TFPA_EINVAL).
+ *   mass    : as tfpa_key_mass; mass_cap a multiple of 4.
+ *   moves   : DEVICE int32 [nseg][hkv][mass_cap + 4], 16-byte aligned, written:
+ *             [0] the number m of rows moved, and from [4] on m pairs (from
+ *             slot, to slot), for whoever keeps more per key than this cache.
+ * A pair on a page whose id is out of range leaves its K and V rows and ORs 1
+ * into cache->err_flag.  Two segments of a call must not share pages. */
+int tfpa_evict_kv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
+                  const int32_t* keep, const int32_t* next_pos, int32_t sink, int32_t recent,
+                  float* mass, int32_t* key_pos, int32_t mass_cap, int32_t* moves,
+                  cudaStream_t stream);
+
 /* Launch recording for host tests (PR #1355: "a launch-recording host test
  * where a 257-row chunk issues 3 slices").  With a hook installed every
  * launch is reported; with dry_run != 0 nothing is enqueued and no CUDA call
@@ -502,7 +561,8 @@ typedef struct {
   int32_t kind;          /* 0 write_kv, 1 decode partial, 2 merge, 3 prefill, 4 keep,
                             5 stage pages, 6 save, 7 restore, 8 verify (decode or tree
                             rows of runs with 49 or more query vectors per kv head, on
-                            tensor cores; items = tiles), 9 read_kv */
+                            tensor cores; items = tiles), 9 read_kv, 10 key_mass, 11 evict (choice),
+                            12 evict (moves) */
   int32_t row0;          /* first row of the call this launch covers */
   int32_t rows;          /* rows it covers */
   int32_t runs;          /* row groups (segment, consecutive positions) */

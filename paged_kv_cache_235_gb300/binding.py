@@ -36,7 +36,8 @@ EXPORTS = ("tfpa_pages_per_split", "tfpa_num_splits", "tfpa_write_kv", "tfpa_dec
            "tfpa_plan_destroy", "tfpa_plan_clear", "tfpa_plan_launches", "tfpa_plan_write_kv",
            "tfpa_plan_decode", "tfpa_plan_launch", "tfpa_plan_set_device", "tfpa_plan_dyn_bytes",
            "tfpa_plan_dyn_pack", "tfpa_plan_shape", "tfpa_plan_capture", "tfpa_plan_replay",
-           "tfpa_decode_append", "tfpa_plan_decode_append", "tfpa_row_splits", "tfpa_read_kv")
+           "tfpa_decode_append", "tfpa_plan_decode_append", "tfpa_row_splits", "tfpa_read_kv",
+           "tfpa_key_mass", "tfpa_evict_kv")
 
 
 class TfpaError(RuntimeError):
@@ -77,7 +78,8 @@ class tfpa_launch_record(ctypes.Structure):
 
 HOOK = ctypes.CFUNCTYPE(None, ctypes.POINTER(tfpa_launch_record), ctypes.c_void_p)
 KINDS = {0: "write_kv", 1: "partial", 2: "merge", 3: "prefill", 4: "keep", 5: "stage",
-         6: "save", 7: "restore", 8: "verify", 9: "read_kv"}
+         6: "save", 7: "restore", 8: "verify", 9: "read_kv", 10: "key_mass",
+         11: "evict", 12: "evict_move"}
 
 _lib = None
 
@@ -174,6 +176,12 @@ def lib():
         L.tfpa_plan_capture.restype = ctypes.c_int
         L.tfpa_plan_replay.argtypes = [vp, vp]
         L.tfpa_plan_replay.restype = ctypes.c_int
+        L.tfpa_key_mass.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, vp, vp, vp, vp, i32,
+                                    ctypes.c_float, ctypes.c_float, vp, i32, vp]
+        L.tfpa_key_mass.restype = ctypes.c_int
+        L.tfpa_evict_kv.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, vp, vp, i32, i32, vp, vp,
+                                    i32, vp, vp]
+        L.tfpa_evict_kv.restype = ctypes.c_int
         L.tfpa_set_launch_hook.argtypes = [HOOK, vp, ctypes.c_int]
         L.tfpa_set_launch_hook.restype = None
         L.tfpa_strerror.argtypes = [ctypes.c_int]
@@ -530,6 +538,44 @@ def tfpa_prefill(cache: Cache, segs: Sequence[Seg], q, row_seg, row_pos, softmax
     _check(lib().tfpa_prefill(ctypes.byref(cc), cs, n, _ptr(q), _ptr(rs), _ptr(rp), len(rs),
                               float(softmax_scale), int(max_rows_per_launch), _ptr(out),
                               _ptr(lse), _stream(stream)), "tfpa_prefill")
+
+
+def tfpa_key_mass(cache: Cache, segs: Sequence[Seg], q, lse, row_seg, row_pos, softmax_scale,
+                  mass, decay: float = 1.0, stream=None) -> None:
+    """Adds the rows' attention weights to ``mass`` (device float32 ``[nseg][hkv][cap]``);
+    ``lse`` is what tfpa_decode or tfpa_prefill left for the same rows."""
+    cs, n = _segs(segs)
+    rs, rp = _i32(row_seg), _i32(row_pos)
+    if mass.shape[0] != n or mass.shape[1] != cache.hkv or not mass.is_contiguous():
+        raise ValueError("mass must be a contiguous [nseg][hkv][cap] tensor")
+    _check(lib().tfpa_key_mass(ctypes.byref(cache.c()), cs, n, _ptr(q), _ptr(lse), _ptr(rs),
+                               _ptr(rp), len(rs), float(softmax_scale), float(decay), _ptr(mass),
+                               int(mass.shape[2]), _stream(stream)), "tfpa_key_mass")
+
+
+def make_moves(nseg: int, hkv: int, cap: int, device="cuda"):
+    """The ``moves`` buffer of tfpa_evict_kv: int32 ``[nseg][hkv][cap + 4]``."""
+    import torch
+    return torch.zeros(nseg, hkv, cap + 4, dtype=torch.int32, device=device)
+
+
+def tfpa_evict_kv(cache: Cache, segs: Sequence[Seg], keep, mass, moves, key_pos=None,
+                  next_pos=None, sink: int = 0, recent: int = 0, stream=None) -> None:
+    """Cuts every segment to its ``keep`` keys of largest ``mass``, in place (tfpa_evict_kv);
+    the caller goes on with seq_len = keep."""
+    cs, n = _segs(segs)
+    kp = _i32(keep)
+    nx = None if next_pos is None else _i32(next_pos)
+    cap = int(mass.shape[2])
+    for t, want in ((mass, (n, cache.hkv, cap)), (key_pos, (n, cache.hkv, cap)),
+                    (moves, (n, cache.hkv, cap + 4))):
+        if t is not None and (tuple(t.shape) != want or not t.is_contiguous()):
+            raise ValueError(f"expected a contiguous {list(want)} tensor")
+    if len(kp) != n or (nx is not None and len(nx) != n):
+        raise ValueError("keep and next_pos hold one value per segment")
+    _check(lib().tfpa_evict_kv(ctypes.byref(cache.c()), cs, n, _ptr(kp), _ptr(nx), int(sink),
+                               int(recent), _ptr(mass), _ptr(key_pos), cap, _ptr(moves),
+                               _stream(stream)), "tfpa_evict_kv")
 
 
 class Plan:

@@ -269,6 +269,16 @@ int row_bytes_of(const tfpa_cache* c) {
                                      : kFp4CodeBytes + kFp4ScaleBytes;
 }
 
+// A C entry's work; host memory that runs out is an error code, not an exception.
+template <typename F>
+int no_throw(F&& fn) {
+  try {
+    return fn();
+  } catch (const std::bad_alloc&) {
+    return TFPA_EINVAL;
+  }
+}
+
 int to_err(cudaError_t e) { return e == cudaSuccess ? TFPA_OK : TFPA_ECUDA; }
 
 }  // namespace
@@ -928,8 +938,10 @@ extern "C" int tfpa_write_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t 
 extern "C" int tfpa_read_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, void* k_rows,
                             void* v_rows, const int32_t* row_seg, const int32_t* row_pos,
                             int32_t rows, cudaStream_t stream) {
-  return write_impl(c, segs, nseg, k_rows, v_rows, row_seg, row_pos, rows,
-                    RopeArgs{nullptr, nullptr, nullptr, 0}, Sink{stream, nullptr}, true);
+  return no_throw([&] {
+    return write_impl(c, segs, nseg, k_rows, v_rows, row_seg, row_pos, rows,
+                      RopeArgs{nullptr, nullptr, nullptr, 0}, Sink{stream, nullptr}, true);
+  });
 }
 
 extern "C" int tfpa_write_kv_rope(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg,
@@ -1281,6 +1293,150 @@ extern "C" int tfpa_save_kv(const tfpa_cache* cache, const tfpa_seg* seg, int32_
 extern "C" int tfpa_restore_kv(const tfpa_cache* cache, const tfpa_seg* seg, int32_t p0,
                                int32_t p1, const void* image, cudaStream_t stream) {
   return copy_impl(cache, seg, p0, p1, image, true, stream);
+}
+
+// ------------------------------------------------------------ eviction
+namespace {
+constexpr int kMassKeys = 128;   // keys of a block of the weight kernel
+
+int mass_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const void* q,
+              const float* lse, const int32_t* row_seg, const int32_t* row_pos, int32_t rows,
+              float scale, float decay, float* mass, int32_t mass_cap, cudaStream_t stream) {
+  int e;
+  if ((e = check_cache(c)) || (e = check_segs(c, segs, nseg))) return e;
+  if (rows > 0 && (!q || !aligned(q, 16) || !lse || !aligned(lse, 4) || !mass ||
+                   !aligned(mass, 4)))
+    return TFPA_EINVAL;
+  if (!std::isfinite(scale) || !(scale > 0.f) || !std::isfinite(decay) || decay < 0.f)
+    return TFPA_EINVAL;
+  if (mass_cap < 1) return TFPA_EINVAL;
+  thread_local std::vector<Run> runs;   // reused by every call of this thread
+  if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;
+  for (const Run& r : runs)
+    if (segs[r.seg].seq_len > mass_cap) return TFPA_ECAPACITY;
+  if (rows == 0) return TFPA_OK;
+  if ((e = check_device())) return e;
+  // A segment's runs one after the other, in the call's order, so that one
+  // block sums all of its rows and the order of a sum is fixed.
+  std::stable_sort(runs.begin(), runs.end(),
+                   [](const Run& a, const Run& b) { return a.seg < b.seg; });
+  thread_local MassParams p;
+  size_t ri = 0;
+  int32_t last_seg = -1;                // the segment of the previous launch's last run
+  while (ri < runs.size()) {
+    std::memset(&p, 0, sizeof(p));
+    int32_t nrows = 0, nr = 0;
+    int64_t items = 0;
+    const int32_t first_row = runs[ri].row0;
+    while (ri < runs.size() && nr < kMaxRuns) {
+      const Run& r = runs[ri];
+      if (p.nsegs == 0 || p.segs[p.nsegs - 1].index != r.seg) {
+        const tfpa_seg& g = segs[r.seg];
+        const int64_t blocks = (int64_t)c->hkv * ((g.seq_len + kMassKeys - 1) / kMassKeys);
+        if (items + blocks > INT32_MAX) break;
+        MassSeg& m = p.segs[p.nsegs++];
+        m.page_table = g.page_table;
+        m.k_base = g.page_table ? c->k_pool : g.k_slab;
+        m.index = r.seg;
+        m.seq_len = g.seq_len;
+        m.slab_cap = g.slab_cap;
+        m.item0 = (int32_t)items;
+        m.run0 = nr;
+        m.decay = r.seg == last_seg ? 1.f : decay;
+        items += blocks;
+        last_seg = r.seg;
+      }
+      ++p.segs[p.nsegs - 1].nruns;
+      p.runs[nr++] = MassRun{r.row0, r.nrows, r.pos0};
+      nrows += r.nrows;
+      ++ri;
+    }
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.lse = lse;
+    p.mass = mass;
+    p.k_scale = c->k_scale;
+    p.err_flag = c->err_flag;
+    p.hq = c->hq;
+    p.hkv = c->hkv;
+    p.group = c->hq / c->hkv;
+    p.num_pages = c->num_pages;
+    p.mass_cap = mass_cap;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    record(10, first_row, nrows, nr, (int32_t)items, (int32_t)items, 0, 0);
+    if (!dry_run())
+      if ((e = to_err(launch_key_mass(p, c->dtype, (int)items, stream)))) return e;
+  }
+  return TFPA_OK;
+}
+
+}  // namespace
+
+extern "C" int tfpa_key_mass(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg,
+                             const void* q, const float* lse, const int32_t* row_seg,
+                             const int32_t* row_pos, int32_t rows, float scale, float decay,
+                             float* mass, int32_t mass_cap, cudaStream_t stream) {
+  return no_throw([&] {
+    return mass_impl(c, segs, nseg, q, lse, row_seg, row_pos, rows, scale, decay, mass, mass_cap,
+                     stream);
+  });
+}
+
+extern "C" int tfpa_evict_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg,
+                             const int32_t* keep, const int32_t* next_pos, int32_t sink,
+                             int32_t recent, float* mass, int32_t* key_pos, int32_t mass_cap,
+                             int32_t* moves, cudaStream_t stream) {
+  int e;
+  if ((e = check_cache(c)) || (e = check_segs(c, segs, nseg))) return e;
+  if (sink < 0 || recent < 0 || mass_cap < 4 || mass_cap % 4) return TFPA_EINVAL;
+  if (nseg > 0 && (!keep || !mass || !aligned(mass, 4) || !moves || !aligned(moves, 16) ||
+                   (key_pos && !aligned(key_pos, 4))))
+    return TFPA_EINVAL;
+  for (int32_t s = 0; s < nseg; ++s) {
+    if (keep[s] < 1 || keep[s] > segs[s].seq_len) return TFPA_ERANGE;
+    if (next_pos && next_pos[s] < 0) return TFPA_ERANGE;
+    if (segs[s].seq_len > mass_cap) return TFPA_ECAPACITY;
+    if (keep[s] < segs[s].seq_len && (int64_t)sink + recent > keep[s]) return TFPA_EINVAL;
+  }
+  if (nseg == 0) return TFPA_OK;
+  if ((e = check_device())) return e;
+  thread_local EvictParams p;
+  for (int32_t s0 = 0; s0 < nseg; s0 += kMaxEvictSegs) {
+    std::memset(&p, 0, sizeof(p));
+    p.nsegs = std::min<int32_t>(kMaxEvictSegs, nseg - s0);
+    int32_t most = 0;                   // pairs of one (segment, kv head), at most
+    for (int32_t i = 0; i < p.nsegs; ++i) {
+      const tfpa_seg& g = segs[s0 + i];
+      EvictSeg& v = p.segs[i];
+      v.page_table = g.page_table;
+      v.k_base = g.page_table ? c->k_pool : g.k_slab;
+      v.v_base = g.page_table ? c->v_pool : g.v_slab;
+      v.index = s0 + i;
+      v.seq_len = g.seq_len;
+      v.keep = keep[s0 + i];
+      v.next_pos = next_pos ? next_pos[s0 + i] : g.seq_len;
+      v.slab_cap = g.slab_cap;
+      most = std::max(most, std::min(v.keep, v.seq_len - v.keep));
+    }
+    p.mass = mass;
+    p.key_pos = key_pos;
+    p.moves = moves;
+    p.err_flag = c->err_flag;
+    p.hkv = c->hkv;
+    p.num_pages = c->num_pages;
+    p.mass_cap = mass_cap;
+    p.sink = sink;
+    p.recent = recent;
+    const int planes = p.nsegs * c->hkv;
+    record(11, s0, p.nsegs, 0, planes, planes, 0, 0);
+    if (!dry_run())
+      if ((e = to_err(launch_evict_select(p, stream)))) return e;
+    if (most == 0) continue;
+    p.grid_x = std::min((most + 7) / 8, 512);
+    record(12, s0, p.nsegs, 0, planes, p.grid_x * planes, 0, 0);
+    if (!dry_run())
+      if ((e = to_err(launch_evict_move(p, c->dtype, stream)))) return e;
+  }
+  return TFPA_OK;
 }
 
 extern "C" void tfpa_set_launch_hook(tfpa_launch_hook hook, void* user, int dry_run_flag) {

@@ -249,7 +249,69 @@ struct CopyParams {
   int32_t restore;            // 0: cache -> image, 1: image -> cache
 };
 
+// Accumulated attention weight: the segments of a launch, each with its runs.
+struct MassSeg {
+  const int32_t* page_table;  // nullptr => slab
+  const void* k_base;         // pool or slab
+  int32_t index;              // the segment's index in the call (its planes of mass)
+  int32_t seq_len;
+  int32_t slab_cap;
+  int32_t item0;              // first block of the segment
+  int32_t run0, nruns;
+  float decay;                // 1 when an earlier launch of the call has applied it
+  int32_t pad_;
+};
+struct MassRun {
+  int32_t row0;               // row of the call
+  int32_t nrows;
+  int32_t pos0;
+};
+struct MassParams {
+  MassSeg segs[kMaxRuns];
+  MassRun runs[kMaxRuns];
+  const __nv_bfloat16* q;     // [rows][hq][128]
+  const float* lse;           // [rows][hq]
+  float* mass;                // [nseg][hkv][mass_cap]
+  const float* k_scale;
+  int32_t* err_flag;
+  int32_t nsegs;
+  int32_t hq, hkv, group;
+  int32_t num_pages;
+  int32_t mass_cap;
+  float scale_log2;
+};
+
+// Eviction.
+constexpr int kMaxEvictSegs = 64;
+struct EvictSeg {
+  const int32_t* page_table;  // nullptr => slab
+  void* k_base;               // pool or slab
+  void* v_base;
+  int32_t index;              // the segment's index in the call
+  int32_t seq_len;
+  int32_t keep;
+  int32_t next_pos;
+  int32_t slab_cap;
+  int32_t pad_;
+};
+struct EvictParams {
+  EvictSeg segs[kMaxEvictSegs];
+  float* mass;                // [nseg][hkv][mass_cap]
+  int32_t* key_pos;           // the same, or nullptr (a slot's position is its index)
+  int32_t* moves;             // [nseg][hkv][mass_cap + 4]
+  int32_t* err_flag;
+  int32_t nsegs;
+  int32_t hkv;
+  int32_t num_pages;
+  int32_t mass_cap;
+  int32_t sink, recent;
+  int32_t grid_x;             // move blocks of one (segment, kv head)
+};
+
 // Launchers (defined next to their kernels).
+cudaError_t launch_key_mass(const MassParams& p, int kv, int grid, cudaStream_t s);
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s);
+cudaError_t launch_evict_move(const EvictParams& p, int kv, cudaStream_t s);
 cudaError_t launch_write_kv(const WriteParams& p, cudaStream_t s);
 // The rows' stored K and V as bf16, into p.k_rows / p.v_rows.
 cudaError_t launch_read_kv(const WriteParams& p, cudaStream_t s);
