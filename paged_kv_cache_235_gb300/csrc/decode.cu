@@ -36,11 +36,11 @@
 namespace tfpa {
 namespace {
 
-// The ring holds three key chunks (64 KB of K and V each; 4 bits: five of 36
-// KB); a chunk arrives as Cfg::kSub stages (see Cfg), at most kMaxStages in
-// the ring.
+// The ring holds three key chunks (64 KB of K and V each; 4 bits: four of 36
+// KB, see below); a chunk arrives as Cfg::kSub stages (see Cfg), at most
+// kMaxStages in the ring.
 constexpr int kRingBytes = 3 * 65536;
-constexpr int kMaxStages = 10;
+constexpr int kMaxStages = 6;
 constexpr int kConsumerWarps = 8;
 constexpr int kCombineWarp0 = 8;      // warps 8..11
 constexpr int kCombineWarps = 4;
@@ -69,18 +69,20 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 units
 
 template <int KV>
 struct Cfg {
+  static constexpr bool kFp4 = KV == kKvFp4 || KV == kKvFp4Wide;
   static constexpr bool kF16 = KV != kKvBf16;          // f16 operands, kv head scales
-  static constexpr bool kFp4 = KV == kKvFp4;
+  // query vectors of an m-tile (a work item's share of a run)
+  static constexpr int kVecs = KV == kKvFp4 ? 8 : 16;
   static constexpr int kChunk = kF16 ? 256 : 128;      // keys per chunk
   // e4m3: a chunk in two stages of 128 keys (K 16 KB + V 16 KB), the first
   // read by consumer warps 0-3, the second by 4-7, so a stage is released
   // after half the warps' work (fp8 verify partial 174.2 -> 172.5 us);
   // bf16: one stage of 128 keys (two stages measured 0.7 % slower);
-  // 4 bits: two stages, each a half-block of K and one of V.
-  static constexpr int kSub = kF16 ? 2 : 1;
-  static constexpr int kStages = kFp4 ? 10 : 3 * kSub;
-  static constexpr int kStageBytes = kFp4 ? 2 * kFp4HalfBytes : 65536 / kSub;
-  static constexpr int kStageKeys = kChunk / kSub;     // 128 either way
+  // 4 bits: one stage, a page's block of K and one of V.
+  static constexpr int kSub = KV == kKvFp8 ? 2 : 1;
+  static constexpr int kStages = KV == kKvFp4 ? 4 : kFp4 ? 5 : 3 * kSub;
+  static constexpr int kStageBytes = kFp4 ? 4 * kFp4HalfBytes : 65536 / kSub;
+  static constexpr int kStageKeys = kChunk / kSub;
   static constexpr int kSubWarps = kConsumerWarps / kSub;   // warps reading a stage
   static constexpr int kKeysPerWarp = kChunk / kConsumerWarps;
   static constexpr int kNT = kKeysPerWarp / 8;         // score n-tiles per warp
@@ -88,13 +90,15 @@ struct Cfg {
   static_assert(kStages <= kMaxStages && kStages * kStageBytes <= kRingBytes, "ring");
 };
 
-// A work item: (run, kv head g, m-tile mt of 16 query vectors, split sigma).
+// A work item: (run, kv head g, m-tile mt of 16 query vectors (4 bits: 8),
+// split sigma).
 struct Item {
   int run, g, mt, sigma;
 };
 
+template <int KV>
 __device__ __forceinline__ int mtiles_of(const RunInfo& ru, int group) {
-  return (ru.nrows * group + 15) >> 4;
+  return (ru.nrows * group + Cfg<KV>::kVecs - 1) / Cfg<KV>::kVecs;
 }
 
 // The run holding item `it`, by binary search over the runs' first items
@@ -111,19 +115,50 @@ __device__ __forceinline__ int run_of(const DecodeDyn& D, int it) {
 // Work item `it`; r is the run of an earlier item of this CTA (or of `it`)
 // and becomes `it`'s: a CTA walks its items in order, so the run only moves
 // forward.
+template <int KV>
 __device__ __forceinline__ Item item_of(const DecodeParams& p, const DecodeDyn& D, int it,
                                         int& r) {
   while (r + 1 < D.nruns && D.runs[r + 1].item0 <= it) ++r;
   const RunInfo& ru = D.runs[r];
   int local = it - ru.item0;
-  const int mgroups = mtiles_of(ru, p.group);
+  const int mgroups = mtiles_of<KV>(ru, p.group);
   Item x;
   x.run = r;
+  if (Cfg<KV>::kFp4) {
+    // the m-tiles of a split one after the other: the second finds the
+    // split's keys in L2
+    x.mt = local % mgroups;
+    local /= mgroups;
+    x.sigma = local % ru.nsplit;
+    x.g = local / ru.nsplit;
+    return x;
+  }
   x.sigma = local % ru.nsplit;
   local /= ru.nsplit;
   x.mt = local % mgroups;
   x.g = local / mgroups;
   return x;
+}
+
+// The work item after x (r: x's run, moved on with it), without the divisions
+// of item_of: a role that walks its items spends them once.
+template <int KV>
+__device__ __forceinline__ void next_item(const DecodeParams& p, const DecodeDyn& D, Item& x) {
+  const RunInfo& ru = D.runs[x.run];
+  if (Cfg<KV>::kFp4) {
+    if (++x.mt < mtiles_of<KV>(ru, p.group)) return;
+    x.mt = 0;
+    if (++x.sigma < ru.nsplit) return;
+    x.sigma = 0;
+  } else {
+    if (++x.sigma < ru.nsplit) return;
+    x.sigma = 0;
+    if (++x.mt < mtiles_of<KV>(ru, p.group)) return;
+    x.mt = 0;
+  }
+  if (++x.g < p.hkv) return;
+  x.g = 0;
+  ++x.run;
 }
 
 // Items [begin, end) of this CTA: a contiguous share balanced by work on the
@@ -136,11 +171,12 @@ __device__ __forceinline__ void cta_items(const DecodeDyn& D, int& begin, int& e
 
 // Key range [klo, khi) an item must read: its split's pages, cut at the
 // stream length and at the last position among the item's rows.
+template <int KV>
 __device__ __forceinline__ void item_keys(const DecodeParams& p, const DecodeDyn& D, const Item& x,
                                           int& klo, int& khi) {
   const RunInfo& ru = D.runs[x.run];
   const int nq = ru.nrows * p.group;
-  const int last_qv = min(16 * x.mt + 15, nq - 1);
+  const int last_qv = min(Cfg<KV>::kVecs * (x.mt + 1), nq) - 1;
   const int maxpos = ru.pos0 + last_qv / p.group;
   klo = x.sigma * ru.pps * kPage;
   khi = min(min(klo + ru.pps * kPage, ru.seq_len), maxpos + 1);
@@ -172,7 +208,7 @@ __device__ void store_new_rows(const DecodeParams& p, const RunInfo& ru, int g, 
     const int row = ru.row0 + (key - ru.pos0);
     const uint4 in =
         *reinterpret_cast<const uint4*>(src_rows + ((size_t)row * p.hkv + g) * kHeadDim + t * 8);
-    if (KV == kKvFp4) {
+    if (Cfg<KV>::kFp4) {
       float f[8];
       unpack8(in, f);
       uint8_t* b8 = static_cast<uint8_t*>(base);
@@ -212,10 +248,10 @@ __device__ void producer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
   uint32_t stage = 0;
   bool ok = true;
   for (int it = ib; ok && it < ie; ++it) {
-    const Item x = item_of(p, D, it, rh);
+    const Item x = item_of<KV>(p, D, it, rh);
     const RunInfo& ru = D.runs[x.run];
     int klo, khi;
-    item_keys(p, D, x, klo, khi);
+    item_keys<KV>(p, D, x, klo, khi);
     if constexpr (APPEND) {
       const int k0 = max(klo, ru.pos0), k1 = min(khi, ru.pos0 + ru.nrows);
       if (k0 < k1) store_new_rows<KV>(p, ru, x.g, k0, k1, lane);
@@ -261,18 +297,31 @@ __device__ __forceinline__ bool load_item(const DecodeParams& p, const RunInfo& 
         y = x.g * ru.slab_cap + k0;
       }
       for (int h = 0; h < C::kSub; ++h, ++stage, y += C::kStageKeys) {
-        const int buf = stage % C::kStages;
-        const uint32_t ph = (stage / C::kStages) & 1;
-        if (!mbar_wait(&empty[buf], ph ^ 1, p.err_flag)) return false;
+        int buf = stage % C::kStages;
+        uint32_t ph = (stage / C::kStages) & 1;
+        if (KV == kKvFp4) {
+          // two rings of two, pages of even and of odd index; `stage` counts
+          // each ring's loads in a half of its own
+          const int ring = page & 1;
+          const uint32_t n = ring ? stage >> 16 : stage & 0xFFFFu;
+          buf = 2 * ring + (n & 1);
+          ph = (n >> 1) & 1;
+          // the count modulo four is all that is needed
+          stage = ring ? (((n + 1) & 3u) << 16) | (stage & 0xFFFFu)
+                       : (stage & 0xFFFF0000u) | ((n + 1) & 3u);
+          --stage;                          // the loop's own increment
+        }
+        if (!mbar_wait<C::kFp4 ? 64 : 0>(&empty[buf], ph ^ 1, p.err_flag)) return false;
         stage_bad[buf] = bad;
         uint64_t* fb = &full[buf];
         uint8_t* sb = stage_mem + (size_t)buf * C::kStageBytes;
         mbar_arrive_expect_tx(fb, C::kStageBytes);
         if (C::kFp4) {
+          // a page's two half-blocks (a split starts on a page) are contiguous
+          constexpr uint32_t kBytes = C::kStageBytes / 2;
           const size_t off = (size_t)(y / kHalfRows) * kFp4HalfBytes;
-          bulk_load(sb, static_cast<const uint8_t*>(p.k_base[ru.src]) + off, kFp4HalfBytes, fb);
-          bulk_load(sb + kFp4HalfBytes, static_cast<const uint8_t*>(p.v_base[ru.src]) + off,
-                    kFp4HalfBytes, fb);
+          bulk_load(sb, static_cast<const uint8_t*>(p.k_base[ru.src]) + off, kBytes, fb);
+          bulk_load(sb + kBytes, static_cast<const uint8_t*>(p.v_base[ru.src]) + off, kBytes, fb);
         } else if (KV == kKvFp8) {
           tma_load_2d(sb, mk, 0, y, fb);
           tma_load_2d(sb + C::kStageBytes / 2, mv, 0, y, fb);
@@ -370,15 +419,6 @@ struct CombBars {
   uint64_t* done;        // the combiners finished the item (fold buffer free)
 };
 
-// The key, within its eight, of column n of a score n-tile.  4 bits: even
-// columns take keys 0-3 and odd ones 4-7, so that a quad's threads (columns
-// 2c, 2c + 1) read V rows c and c + 4: the four rows of one shared-memory
-// read are then consecutive (64 bytes each, no bank conflict).
-template <int KV>
-__device__ __forceinline__ int key_row(int n) {
-  return KV == kKvFp4 ? (n >> 1) | ((n & 1) << 2) : n;
-}
-
 // This warp's kKeysPerWarp keys, keys key_base.. at rows r0.. of the stage
 // at sb: scores, the causal or ancestor mask, the online softmax, and
 // O += P V.
@@ -397,23 +437,9 @@ __device__ __forceinline__ void attend_block(uint32_t sb, int r0, int key_base, 
 #pragma unroll
   for (int nt = 0; nt < kNT; ++nt) {
     s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-    const int kr = r0 + nt * 8 + key_row<KV>(gq);
+    const int kr = r0 + nt * 8 + gq;
     uint32_t kb[16];
-    if (C::kFp4) {
-      // dims 32 c .. 32 c + 31: 16 bytes of codes, two block scales
-      const uint4 w = lds128(sb + kr * kFp4CodeBytes + 16 * c);
-      const uint32_t s2 = e4m3x2_to_f16x2(
-          (uint16_t)lds16(sb + kFp4ScaleOff + kr * kFp4ScaleBytes + 2 * c));
-      const uint32_t sc0 = prmt(s2, s2, 0x1010), sc1 = prmt(s2, s2, 0x3232);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t h[4];
-        e2m1x8_to_f16x8(ws[i], h);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) kb[4 * i + j] = hmul2(h[j], i < 2 ? sc0 : sc1);
-      }
-    } else if (KV == kKvFp8) {
+    if (KV == kKvFp8) {
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
         const uint4 w = lds128(swz128(sb, kr, 2 * c + ch));
@@ -457,7 +483,7 @@ __device__ __forceinline__ void attend_block(uint32_t sb, int r0, int key_base, 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int hr = j >> 1;
-      const int key = key_base + nt * 8 + key_row<KV>(2 * c + (j & 1));
+      const int key = key_base + nt * 8 + 2 * c + (j & 1);
       bool vis = key <= lim[hr];
       if (tree_zone) {
         const int dd = lim[hr] - key;
@@ -520,37 +546,7 @@ __device__ __forceinline__ void attend_block(uint32_t sb, int r0, int key_base, 
     }
     const int kv0 = r0 + 16 * kk + 2 * c;    // rows kv0, kv0+1, kv0+8, kv0+9
     const int krow[4] = {kv0, kv0 + 1, kv0 + 8, kv0 + 9};
-    if (C::kFp4) {
-      // dims 16 gq .. 16 gq + 15 of the keys of k indices 2c, 2c + 1, 2c + 8,
-      // 2c + 9: 8 bytes of codes and one block scale each.  A byte of two
-      // keys' equal nibbles converts to a pair along the keys.
-      uint2 w[4];
-      uint32_t sb8[4];
-#pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) {
-        const int row = r0 + 16 * kk + c + 4 * q4;       // key_row of that k index
-        w[q4] = lds64(vb + row * kFp4CodeBytes + 8 * gq);
-        sb8[q4] = lds8(vb + kFp4ScaleOff + row * kFp4ScaleBytes + gq);
-        if (key_base - r0 + row >= seq_len) sb8[q4] = 0;   // bytes there may be a NaN scale
-      }
-      const uint32_t s01 = e4m3x2_to_f16x2((uint16_t)(sb8[0] | (sb8[1] << 8)));
-      const uint32_t s23 = e4m3x2_to_f16x2((uint16_t)(sb8[2] | (sb8[3] << 8)));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t wa[4] = {i ? w[0].y : w[0].x, i ? w[1].y : w[1].x, i ? w[2].y : w[2].x,
-                                i ? w[3].y : w[3].x};
-        uint32_t lo01[4], hi01[4], lo23[4], hi23[4];
-        e2m1x8_to_f16x8((wa[0] & 0x0F0F0F0Fu) | ((wa[1] << 4) & 0xF0F0F0F0u), lo01);
-        e2m1x8_to_f16x8(((wa[0] >> 4) & 0x0F0F0F0Fu) | (wa[1] & 0xF0F0F0F0u), hi01);
-        e2m1x8_to_f16x8((wa[2] & 0x0F0F0F0Fu) | ((wa[3] << 4) & 0xF0F0F0F0u), lo23);
-        e2m1x8_to_f16x8(((wa[2] >> 4) & 0x0F0F0F0Fu) | (wa[3] & 0xF0F0F0F0u), hi23);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          mma_f16(o[8 * i + 2 * j], a, hmul2(lo01[j], s01), hmul2(lo23[j], s23));
-          mma_f16(o[8 * i + 2 * j + 1], a, hmul2(hi01[j], s01), hmul2(hi23[j], s23));
-        }
-      }
-    } else if (KV == kKvFp8) {
+    if (KV == kKvFp8) {
       uint32_t w[4][4];
 #pragma unroll
       for (int q4 = 0; q4 < 4; ++q4) {
@@ -597,6 +593,175 @@ __device__ __forceinline__ void attend_block(uint32_t sb, int r0, int key_base, 
   }
 }
 
+// What a lane reads of its warp's 32 keys of a 4-bit stage (a page: K's two
+// half-blocks, then V's), as offsets from the stage: K codes and scales of the
+// key of column gq, V codes and scales of the first key of columns c.
+//   Columns of a score n-tile: even ones take its eight keys' 0-3, odd ones
+// 4-7, so that a quad's threads (columns 2c, 2c + 1) read V rows c and c + 4:
+// one read's four rows are then consecutive (64 bytes each, no bank
+// conflict).
+struct LaneFp4 {
+  uint32_t k, ks, v, vs;
+  __device__ __forceinline__ LaneFp4(int w8, int gq, int c) {
+    const uint32_t half = (uint32_t)(w8 >> 2) * kFp4HalfBytes;
+    const int r0 = (w8 & 3) * 32, kr = r0 + ((gq >> 1) | ((gq & 1) << 2)), vr = r0 + c;
+    constexpr uint32_t kV = 2 * kFp4HalfBytes;
+    k = half + kr * kFp4CodeBytes + 16 * c;
+    ks = half + kFp4ScaleOff + kr * kFp4ScaleBytes + 2 * c;
+    v = kV + half + vr * kFp4CodeBytes + 8 * gq;
+    vs = kV + half + kFp4ScaleOff + vr * kFp4ScaleBytes + gq;
+  }
+};
+
+// attend_block for a 4-bit cache, sixteen query vectors: this warp's 32 keys
+// from key_base on, in the stage at sb.  The score MMAs go round the four
+// n-tiles (a chain of eight dependent ones per n-tile otherwise), and the
+// running maximum is looked at with one vote: it moves only when some score
+// passes it by more than 2^8, which after a row's first block is rare.  A code
+// byte of two keys' equal nibbles converts to a V pair along the keys.
+template <bool GEN>
+__device__ __forceinline__ void attend_fp4_wide(uint32_t sb, const LaneFp4& at, int key_base,
+                                                int seq_len, const uint32_t (&qr)[2][16],
+                                                const int (&lim)[2], int minlim,
+                                                const float (&sc)[2], const uint64_t (&anc)[2],
+                                                int tree_low, int c, float (&m_run)[2],
+                                                float (&l_run)[2], float (&o)[16][4]) {
+  constexpr int kKeys = 32;
+  uint4 kw[4];
+  uint32_t ks[4];
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) {       // dims 32 c .. 32 c + 31 of a key
+    kw[nt] = lds128(sb + at.k + nt * 8 * kFp4CodeBytes);
+    ks[nt] = lds16(sb + at.ks + nt * 8 * kFp4ScaleBytes);
+  }
+  // ---- S = Q K^T
+  float s[4][4];
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) {
+    s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+    ks[nt] = e4m3x2_to_f16x2((uint16_t)ks[nt]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {          // code word i: k-steps 2 i and 2 i + 1
+    uint32_t h[4][4];
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      const uint32_t w = i == 0 ? kw[nt].x : i == 1 ? kw[nt].y : i == 2 ? kw[nt].z : kw[nt].w;
+      e2m1x8_to_f16x8(w, h[nt]);
+      const uint32_t s2 = prmt(ks[nt], ks[nt], i < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[nt][j] = hmul2(h[nt][j], s2);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int k = 2 * i + u;
+      const uint32_t a[4] = {qr[0][2 * k], qr[1][2 * k], qr[0][2 * k + 1], qr[1][2 * k + 1]};
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) mma_f16_free(s[nt], a, h[nt][2 * u], h[nt][2 * u + 1]);
+    }
+  }
+  // ---- V's codes, dims 16 gq .. 16 gq + 15 of a key
+  uint2 vw[2][4];
+  uint32_t vs[2][4];
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+    for (int q4 = 0; q4 < 4; ++q4) {
+      vw[kk][q4] = lds64(sb + at.v + (16 * kk + 4 * q4) * kFp4CodeBytes);
+      vs[kk][q4] = lds8(sb + at.vs + (16 * kk + 4 * q4) * kFp4ScaleBytes);
+    }
+  // ---- mask, running max, exponentials
+  const bool tree_zone = GEN && key_base + kKeys > tree_low;
+  if (key_base + kKeys - 1 > minlim || tree_zone) {
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int hr = j >> 1;
+        const int key = key_base + nt * 8 + c + 4 * (j & 1);
+        bool vis = key <= lim[hr];
+        if (tree_zone) {
+          const int dd = lim[hr] - key;
+          vis = vis && (dd > 63 || ((anc[hr] >> dd) & 1ull));
+        }
+        if (!vis) s[nt][j] = -INFINITY;
+      }
+  }
+  float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) {
+    mx[0] = fmax3(mx[0], s[nt][0], s[nt][1]);
+    mx[1] = fmax3(mx[1], s[nt][2], s[nt][3]);
+  }
+  mx[0] *= sc[0];                        // scales are positive
+  mx[1] *= sc[1];
+  if (__any_sync(0xffffffffu, mx[0] > m_run[0] + kRescaleThreshold ||
+                                  mx[1] > m_run[1] + kRescaleThreshold)) {
+    float alpha[2];
+#pragma unroll
+    for (int hr = 0; hr < 2; ++hr) {
+      mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
+      mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 2));
+      alpha[hr] = 1.f;
+      if (mx[hr] > m_run[hr] + kRescaleThreshold) {
+        alpha[hr] = fast_exp2(m_run[hr] - mx[hr]);
+        l_run[hr] *= alpha[hr];
+        m_run[hr] = mx[hr];
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < 16; ++nt) {
+      o[nt][0] *= alpha[0];
+      o[nt][1] *= alpha[0];
+      o[nt][2] *= alpha[1];
+      o[nt][3] *= alpha[1];
+    }
+  }
+  const float nb[2] = {m_run[0] == -INFINITY ? 0.f : -m_run[0],
+                       m_run[1] == -INFINITY ? 0.f : -m_run[1]};
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float e = fast_exp2(__fmaf_rn(s[nt][j], sc[j >> 1], nb[j >> 1]));
+      s[nt][j] = e;
+      l_run[j >> 1] += e;
+    }
+  // ---- O += P V.  Bytes past the stream's end may be a NaN scale.
+  if (key_base + kKeys > seq_len) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4)
+        if (key_base + 16 * kk + c + 4 * q4 >= seq_len) vs[kk][q4] = 0;
+  }
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    const uint32_t a[4] = {pack_f16x2(s[2 * kk][0], s[2 * kk][1]),
+                           pack_f16x2(s[2 * kk][2], s[2 * kk][3]),
+                           pack_f16x2(s[2 * kk + 1][0], s[2 * kk + 1][1]),
+                           pack_f16x2(s[2 * kk + 1][2], s[2 * kk + 1][3])};
+    const uint32_t s01 = e4m3x2_to_f16x2((uint16_t)(vs[kk][0] | (vs[kk][1] << 8)));
+    const uint32_t s23 = e4m3x2_to_f16x2((uint16_t)(vs[kk][2] | (vs[kk][3] << 8)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) w[q4] = i ? vw[kk][q4].y : vw[kk][q4].x;
+      uint32_t lo01[4], hi01[4], lo23[4], hi23[4];
+      e2m1x8_to_f16x8((w[0] & 0x0F0F0F0Fu) | ((w[1] << 4) & 0xF0F0F0F0u), lo01);
+      e2m1x8_to_f16x8(((w[0] >> 4) & 0x0F0F0F0Fu) | (w[1] & 0xF0F0F0F0u), hi01);
+      e2m1x8_to_f16x8((w[2] & 0x0F0F0F0Fu) | ((w[3] << 4) & 0xF0F0F0F0u), lo23);
+      e2m1x8_to_f16x8(((w[2] >> 4) & 0x0F0F0F0Fu) | (w[3] & 0xF0F0F0F0u), hi23);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mma_f16_free(o[8 * i + 2 * j], a, hmul2(lo01[j], s01), hmul2(lo23[j], s23));
+        mma_f16_free(o[8 * i + 2 * j + 1], a, hmul2(hi01[j], s01), hmul2(hi23[j], s23));
+      }
+    }
+  }
+}
+
 template <int KV, bool GEN>
 __device__ void consumer(const DecodeParams& p, const DecodeDyn& D, uint8_t* stage_mem,
                          uint64_t* full, uint64_t* empty, const int* stage_bad, uint32_t tmem,
@@ -615,19 +780,27 @@ __device__ void consumer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
   uint64_t anc[2] = {~0ull, ~0ull};
   float sc[2] = {0.f, 0.f};
   uint32_t qr[2][16];
-  int maxlim = -1;
+  int maxlim = -1, minlim = -1;
   int tree_low = INT_MAX;     // keys from here on may be hidden by an ancestor mask
 
+  Item x{};
   for (int it = ib; it < ie; ++it) {
-    const Item x = item_of(p, D, it, rh);
+    if (C::kFp4 && it > ib)
+      next_item<KV>(p, D, x);
+    else
+      x = item_of<KV>(p, D, it, rh);
     const RunInfo& ru = D.runs[x.run];
     int klo, khi;
-    item_keys(p, D, x, klo, khi);
+    item_keys<KV>(p, D, x, klo, khi);
     // The chunk's 8 sub-blocks of kKeysPerWarp keys go to the 8 warps.
     const int sub0 = warp;
     if (x.run != q_run || x.g != q_g || x.mt != q_mt) {
       load_q<KV, GEN>(p, ru, x, gq, c, qr, lim, anc, sc);
       maxlim = __reduce_max_sync(0xffffffffu, max(lim[0], lim[1]));
+      if (C::kFp4) {        // the least limit of a row that exists
+        const int mn = min(lim[0] >= 0 ? lim[0] : INT_MAX, lim[1] >= 0 ? lim[1] : INT_MAX);
+        minlim = (int)__reduce_min_sync(0xffffffffu, (unsigned)mn);
+      }
       if (GEN && p.anc) {
         const int mn = min(lim[0] >= 0 ? lim[0] : INT_MAX, lim[1] >= 0 ? lim[1] : INT_MAX);
         tree_low = (int)__reduce_min_sync(0xffffffffu, (unsigned)mn) - 63;
@@ -653,9 +826,14 @@ __device__ void consumer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
       const uint32_t sb = sbase + (uint32_t)buf * C::kStageBytes;
       const int wk0 = sub0 * C::kKeysPerWarp;
       const int r0 = wk0 - (sub0 / C::kSubWarps) * C::kStageKeys;
-      if (!stage_bad[buf] && k0 + wk0 <= maxlim)
-        attend_block<KV, GEN>(sb, r0, k0 + wk0, ru.seq_len, qr, lim, sc, anc, tree_low, gq, c,
-                               m_run, l_run, o);
+      if (!stage_bad[buf] && k0 + wk0 <= maxlim) {
+        if constexpr (C::kFp4)
+          attend_fp4_wide<GEN>(sb, LaneFp4(warp, gq, c), k0 + wk0, ru.seq_len, qr, lim, minlim,
+                               sc, anc, tree_low, c, m_run, l_run, o);
+        else
+          attend_block<KV, GEN>(sb, r0, k0 + wk0, ru.seq_len, qr, lim, sc, anc, tree_low, gq, c,
+                                 m_run, l_run, o);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[buf]);
     }
@@ -760,13 +938,14 @@ __device__ __forceinline__ void merge_vector(const float* part_o, const float* p
 // merges the group's query vectors, warp 8+q taking vectors q, q+4, ...
 // Every thread fences its partial stores before the count, and the merging
 // threads fence after it and load the partials through L2.
+template <int KV, int WARP0>
 __device__ __forceinline__ void merge_if_last(const DecodeParams& p, const RunInfo& ru,
                                               const Item& x, int nq, int* merge_flag) {
-  const int q = (threadIdx.x >> 5) - kCombineWarp0;
+  const int q = (threadIdx.x >> 5) - WARP0;
   __threadfence();
   named_bar_sync(1, 32 * kCombineWarps);
-  if (threadIdx.x == 32 * kCombineWarp0) {
-    const int qv0 = x.mt * 16;
+  if (threadIdx.x == 32 * WARP0) {
+    const int qv0 = x.mt * Cfg<KV>::kVecs;
     const int r0 = qv0 / p.group;
     uint32_t* ctr = p.arrive + (size_t)(ru.row0 + r0) * p.hq + x.g * p.group + (qv0 - r0 * p.group);
     const uint32_t old = atomicAdd(ctr, 1u);
@@ -777,8 +956,8 @@ __device__ __forceinline__ void merge_if_last(const DecodeParams& p, const RunIn
   named_bar_sync(1, 32 * kCombineWarps);
   if (!*merge_flag) return;
   __threadfence();
-  for (int j = q; j < 16; j += kCombineWarps) {
-    const int qv = x.mt * 16 + j;
+  for (int j = q; j < Cfg<KV>::kVecs; j += kCombineWarps) {
+    const int qv = x.mt * Cfg<KV>::kVecs + j;
     if (qv >= nq) break;
     const int r = qv / p.group;
     const size_t rh = (size_t)(ru.row0 + r) * p.hq + x.g * p.group + (qv - r * p.group);
@@ -809,14 +988,20 @@ __device__ void combiner(const DecodeParams& p, const DecodeDyn& D, uint32_t tme
   cta_items(D, ib, ie);
   int rh = ib < ie ? run_of(D, ib) : 0;   // run of the current item
   const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+  Item x{};
   for (int it = ib; it < ie; ++it) {
-    const Item x = item_of(p, D, it, rh);
+    if (Cfg<KV>::kFp4 && it > ib)
+      next_item<KV>(p, D, x);
+    else
+      x = item_of<KV>(p, D, it, rh);
     const RunInfo& ru = D.runs[x.run];
     const int nq = ru.nrows * p.group;
     const int rel = it - ib;
     const int b = rel & 1;
     const uint32_t par = (uint32_t)rel & 1u;
-    if (!mbar_wait(&bars.posted[b], (uint32_t)(rel >> 1) & 1u, p.err_flag)) return;
+    if (!mbar_wait<Cfg<KV>::kFp4 ? 128 : 0>(&bars.posted[b], (uint32_t)(rel >> 1) & 1u,
+                                            p.err_flag))
+      return;
     umma::fence_after_sync();
     const uint32_t tA = tl + (uint32_t)(b * kBufCols);          // consumer warp q
     const uint32_t tB = tA + kHalfCols;                          // consumer warp q + 4
@@ -926,7 +1111,7 @@ __device__ void combiner(const DecodeParams& p, const DecodeDyn& D, uint32_t tme
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bars.done);
-    if constexpr (MERGE) merge_if_last(p, ru, x, nq, merge_flag);
+    if constexpr (MERGE) merge_if_last<KV, kCombineWarp0>(p, ru, x, nq, merge_flag);
   }
 }
 
@@ -964,10 +1149,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_kernel(
     cta_items(D, ib, ie);
     if (ib < ie) {
       int r = run_of(D, ib);
-      const Item x = item_of(p, D, ib, r);
+      const Item x = item_of<KV>(p, D, ib, r);
       if (D.runs[x.run].page_table) {
         int klo, khi;
-        item_keys(p, D, x, klo, khi);
+        item_keys<KV>(p, D, x, klo, khi);
         prefetch_l2(D.runs[x.run].page_table + (klo >> 8));
       }
     }
@@ -986,7 +1171,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_kernel(
     mbar_init(cb.done, kCombineWarps);
     fence_mbar_init();
   }
-  if (KV != kKvFp4 && warp == kProducerWarp && (threadIdx.x & 31) == 0) {
+  if (!Cfg<KV>::kFp4 && warp == kProducerWarp && (threadIdx.x & 31) == 0) {
     for (int i = 0; i < p.nsrc; ++i) {
       tma_prefetch_desc(&p.maps[i].k);
       tma_prefetch_desc(&p.maps[i].v);
@@ -1012,6 +1197,495 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_kernel(
   umma::fence_before_sync();
   __syncthreads();
   if (warp == kCombineWarp0) {
+    umma::fence_after_sync();
+    umma::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- 4 bits
+// The same roles for a 4-bit cache, whose keys take half the time to arrive
+// and more work each: a key's K and V cost eight conversion and multiply
+// instructions a warp before any product, so the consumers, not the memory,
+// are what a kernel of the shape above waits for (8 consumer warps, two a
+// scheduler, each a chain of reads, conversions, MMAs, exponentials and MMAs:
+// 178 us for 8 streams of 65,536 keys and four rows, where the bytes need
+// 89).  So here sixteen consumer warps, four a scheduler, in two groups of
+// eight: a stage is a page, pages of even index belong to one group and of
+// odd index to the other, 32 keys a warp, and each group has a ring of two
+// stages of its own (a barrier's parity only tells phases apart for those who
+// wait for every one of them).  For their registers a work item has eight
+// query vectors (a decode row of up to eight heads a kv head), which halves a
+// warp's accumulators:
+//   S = Q K^T, vectors as the MMA's rows (half of them empty), so that S's
+//   fragment of vector gq is already P's fragment in
+//   O^T = V^T P^T, head dims as rows (16, all used) and vectors as columns.
+// The running maximum is looked at with one vote a block and moves only when
+// some score passes it by more than 2^8, which after a row's first block is
+// rare.
+constexpr int kWarps4 = 16;
+constexpr int kCombineWarp4 = 16;         // warps 16..19
+constexpr int kProducerWarp4 = 20;        // warps 21..23 only take part in the register split
+constexpr int kThreads4 = 24 * 32;
+constexpr int kRegsConsumer4 = 96, kRegsCombine4 = 72, kRegsProducer4 = 24;
+constexpr int kRegsLaunch4 = 80;
+static_assert(128 * (4 * kRegsConsumer4 + kRegsCombine4 + kRegsProducer4) <=
+                  kThreads4 * kRegsLaunch4, "register split");
+// TMEM: two buffers (item parity) of four states (consumer warps q, q + 4,
+// q + 8, q + 12 of lane quarter q) of 32 O columns.  (m, l) of every warp and
+// vector go through shared memory, two buffers likewise.
+constexpr int kBufCols4 = 256;
+constexpr int kStateCols4 = 64;
+constexpr int kRingBytes4 = Cfg<kKvFp4>::kStages * Cfg<kKvFp4>::kStageBytes;
+constexpr int kCombBytes4 = kCombineWarps * 8 * 32 * 16;   // [slot q][d m-tile][lane] float4
+constexpr int kMlFloats4 = kWarps4 * 8 * 2;                // [warp][vector](m, l), one buffer
+constexpr int kSmemBytes4 =
+    kRingBytes4 + kCombBytes4 + 2 * kMlFloats4 * 4 + kMaxStages * 4 + 8 + kNumBars * 8 + 1024;
+static_assert(kSmemBytes4 <= 232448, "shared memory");
+
+// 32 keys of one warp, from key_base on, in the stage at sb.  A code byte of
+// two keys' equal nibbles converts to a V pair along the keys; the low and the
+// high nibble of a byte are an O^T m-tile's rows gq and gq + 8.
+template <bool GEN>
+__device__ __forceinline__ void attend_fp4(uint32_t sb, const LaneFp4& at, int key_base,
+                                           int seq_len, const uint32_t (&qr)[16], int lim,
+                                           int minlim, float sc, uint64_t anc, int tree_low,
+                                           int c, float& m_run, float& l_run,
+                                           float (&o)[8][4]) {
+  constexpr int kKeys = 32;
+  // ---- S = Q K^T: lane (gq, c) holds dims 32 c .. 32 c + 31 of a key, a
+  // code word its dims 8 i .. + 7 of them.  The MMA's rows gq and gq + 8 both
+  // hold vector gq, with the word's pairs 0, 2 and 1, 3: of the product with
+  // the keys' pairs 0, 2 the first eight rows are kept, with 1, 3 the others,
+  // so that A is four registers as they stand.
+  float s[4][2];
+  const uint32_t ka = sb + at.k, ksa = sb + at.ks;
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) {
+    const uint4 kw = lds128(ka + nt * 8 * kFp4CodeBytes);
+    const uint32_t ks = e4m3x2_to_f16x2((uint16_t)lds16(ksa + nt * 8 * kFp4ScaleBytes));
+    float d0[4] = {}, d1[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = i == 0 ? kw.x : i == 1 ? kw.y : i == 2 ? kw.z : kw.w;
+      uint32_t h[4];
+      e2m1x8_to_f16x8(w, h);
+      const uint32_t s2 = prmt(ks, ks, i < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = hmul2(h[j], s2);
+      const uint32_t a[4] = {qr[4 * i], qr[4 * i + 1], qr[4 * i + 2], qr[4 * i + 3]};
+      mma_f16_free(d0, a, h[0], h[2]);
+      mma_f16_free(d1, a, h[1], h[3]);
+    }
+    s[nt][0] = d0[0] + d1[2];
+    s[nt][1] = d0[1] + d1[3];
+  }
+  // ---- mask, running max, exponentials
+  const bool tree_zone = GEN && key_base + kKeys > tree_low;
+  if (key_base + kKeys - 1 > minlim || tree_zone) {
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int key = key_base + nt * 8 + c + 4 * j;
+        bool vis = key <= lim;
+        if (tree_zone) {
+          const int dd = lim - key;
+          vis = vis && (dd > 63 || ((anc >> dd) & 1ull));
+        }
+        if (!vis) s[nt][j] = -INFINITY;
+      }
+  }
+  float mx = fmaxf(fmax3(fmax3(s[0][0], s[0][1], s[1][0]), s[1][1], s[2][0]),
+                   fmax3(s[2][1], s[3][0], s[3][1])) * sc;       // scales are positive
+  if (__any_sync(0xffffffffu, mx > m_run + kRescaleThreshold)) {
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    float alpha = 1.f;
+    if (mx > m_run + kRescaleThreshold) {
+      alpha = fast_exp2(m_run - mx);
+      l_run *= alpha;
+      m_run = mx;
+    }
+    // the factors of O^T's columns, vectors 2c and 2c + 1
+    const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c);
+    const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      o[mt][0] *= a0;
+      o[mt][1] *= a1;
+      o[mt][2] *= a0;
+      o[mt][3] *= a1;
+    }
+  }
+  const float nb = m_run == -INFINITY ? 0.f : -m_run;
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) s[nt][j] = fast_exp2(__fmaf_rn(s[nt][j], sc, nb));
+  l_run += ((s[0][0] + s[0][1]) + (s[1][0] + s[1][1])) +
+           ((s[2][0] + s[2][1]) + (s[3][0] + s[3][1]));
+  uint32_t pb[4];
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) pb[nt] = pack_f16x2(s[nt][0], s[nt][1]);
+  // ---- O^T += V^T P^T, 16 keys at a time: 16 dims (chunk gq) of the keys of
+  // k indices 2c, 2c + 1, 2c + 8, 2c + 9.  Bytes past the stream's end may be
+  // a NaN scale.
+  const uint32_t va = sb + at.v, vsa = sb + at.vs;
+  const bool tail = key_base + kKeys > seq_len;
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    uint2 vw[4];
+    uint32_t vs[4];
+#pragma unroll
+    for (int q4 = 0; q4 < 4; ++q4) {
+      vw[q4] = lds64(va + (16 * kk + 4 * q4) * kFp4CodeBytes);
+      vs[q4] = lds8(vsa + (16 * kk + 4 * q4) * kFp4ScaleBytes);
+    }
+    if (tail) {
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4)
+        if (key_base + 16 * kk + c + 4 * q4 >= seq_len) vs[q4] = 0;
+    }
+    const uint32_t s01 = e4m3x2_to_f16x2((uint16_t)(vs[0] | (vs[1] << 8)));
+    const uint32_t s23 = e4m3x2_to_f16x2((uint16_t)(vs[2] | (vs[3] << 8)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) w[q4] = i ? vw[q4].y : vw[q4].x;
+      uint32_t lo01[4], hi01[4], lo23[4], hi23[4];
+      e2m1x8_to_f16x8((w[0] & 0x0F0F0F0Fu) | ((w[1] << 4) & 0xF0F0F0F0u), lo01);
+      e2m1x8_to_f16x8(((w[0] >> 4) & 0x0F0F0F0Fu) | (w[1] & 0xF0F0F0F0u), hi01);
+      e2m1x8_to_f16x8((w[2] & 0x0F0F0F0Fu) | ((w[3] << 4) & 0xF0F0F0F0u), lo23);
+      e2m1x8_to_f16x8(((w[2] >> 4) & 0x0F0F0F0Fu) | (w[3] & 0xF0F0F0F0u), hi23);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a[4] = {hmul2(lo01[j], s01), hmul2(hi01[j], s01), hmul2(lo23[j], s23),
+                               hmul2(hi23[j], s23)};
+        mma_f16_free(o[4 * i + j], a, pb[2 * kk], pb[2 * kk + 1]);
+      }
+    }
+  }
+}
+
+// Vector gq of an m-tile as the lane's 16 A operand pairs, scaled by a power
+// of two into f16 range (exact for every element within 2^28 of the largest);
+// its causal limit (-1: no such vector), ancestor mask and score multiplier.
+template <bool GEN>
+__device__ __forceinline__ void load_q_fp4(const DecodeParams& p, const RunInfo& ru,
+                                           const Item& x, int gq, int c, uint32_t (&qr)[16],
+                                           int& lim, uint64_t& anc, float& sc) {
+  const int nq = ru.nrows * p.group;
+  const int qv = x.mt * Cfg<kKvFp4>::kVecs + gq;
+  lim = -1;
+  anc = ~0ull;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) qr[j] = 0u;
+  if (qv < nq) {
+    const int r = qv / p.group;
+    lim = ru.pos0 + r;
+    if (GEN && p.anc) anc = __ldg(p.anc + ru.row0 + r);
+    const uint4* qp = reinterpret_cast<const uint4*>(
+        p.q + ((size_t)(ru.row0 + r) * p.hq + x.g * p.group + (qv - r * p.group)) * kHeadDim);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const uint4 v = __ldg(qp + 4 * c + m);
+      qr[4 * m + 0] = v.x;
+      qr[4 * m + 1] = v.y;
+      qr[4 * m + 2] = v.z;
+      qr[4 * m + 3] = v.w;
+    }
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    amax = fmaxf(amax, fabsf(__uint_as_float(qr[j] << 16)));
+    amax = fmaxf(amax, fabsf(__uint_as_float(qr[j] & 0xFFFF0000u)));
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  int ex;
+  frexpf(amax, &ex);
+  ex = max(min(ex, 120), -100);
+  const float up = __int_as_float((127 + 14 - ex) << 23);
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    qr[j] = pack_f16x2(__uint_as_float(qr[j] << 16) * up,
+                       __uint_as_float(qr[j] & 0xFFFF0000u) * up);
+  sc = p.scale_log2 * __int_as_float((127 - 14 + ex) << 23) * __ldg(p.k_scale + x.g);
+}
+
+// Waits whose result and reconvergence the whole warp shares, for the
+// warp-wide (aligned) instructions that follow.
+// SLEEP: ns between looks, for a role that waits most of the time (its looks
+// take issue slots from the consumers).
+template <int SLEEP = 0>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err) {
+  return __all_sync(0xffffffffu, mbar_wait<SLEEP>(bar, parity, err));
+}
+
+template <bool GEN>
+__device__ void consumer_fp4(const DecodeParams& p, const DecodeDyn& D, uint8_t* stage_mem,
+                             uint64_t* full, uint64_t* empty, const int* stage_bad, uint32_t tmem,
+                             float* ml_buf, CombBars bars) {
+  using C = Cfg<kKvFp4>;
+  constexpr int KV = kKvFp4;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int gq = lane >> 2, c = lane & 3;
+  const LaneFp4 at(warp & 7, gq, c);
+  const int group = warp >> 3;                          // pages of this parity
+  const uint32_t ring = smem_u32(stage_mem) + (uint32_t)(2 * group) * C::kStageBytes;
+  full += 2 * group;
+  empty += 2 * group;
+  stage_bad += 2 * group;
+  uint32_t n = 0;                                       // stages of this group so far
+  int ib, ie;
+  cta_items(D, ib, ie);
+  if (ib >= ie) return;
+  int rh = run_of(D, ib);
+  Item x = item_of<KV>(p, D, ib, rh);
+  int q_run = -1, q_g = -1, q_mt = -1;     // the m-tile whose query is loaded
+  int lim = -1, maxlim = -1, minlim = -1;
+  uint64_t anc = ~0ull;
+  float sc = 0.f;
+  uint32_t qr[16];
+  int tree_low = INT_MAX;     // keys from here on may be hidden by an ancestor mask
+
+  for (int it = ib; it < ie; ++it, next_item<KV>(p, D, x)) {
+    const RunInfo& ru = D.runs[x.run];
+    int klo, khi;
+    item_keys<KV>(p, D, x, klo, khi);
+    if (x.run != q_run || x.g != q_g || x.mt != q_mt) {
+      load_q_fp4<GEN>(p, ru, x, gq, c, qr, lim, anc, sc);
+      maxlim = __reduce_max_sync(0xffffffffu, lim);
+      minlim = (int)__reduce_min_sync(0xffffffffu, (unsigned)(lim >= 0 ? lim : INT_MAX));
+      if (GEN && p.anc) tree_low = minlim - 63;
+      q_run = x.run;
+      q_g = x.g;
+      q_mt = x.mt;
+    }
+    float m_run = -INFINITY, l_run = 0.f;
+    float o[8][4];
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+    for (int k0 = klo + ((((klo >> 8) ^ group) & 1) ? kPage : 0); k0 < khi;
+         k0 += 2 * kPage, ++n) {
+      const int buf = n & 1;
+      if (!warp_wait(&full[buf], (n >> 1) & 1, p.err_flag)) return;
+      const int key_base = k0 + (warp & 7) * 32;
+      if (!stage_bad[buf] && key_base <= maxlim)
+        attend_fp4<GEN>(ring + (uint32_t)buf * C::kStageBytes, at, key_base, ru.seq_len, qr, lim,
+                        minlim, sc, anc, tree_low, c, m_run, l_run, o);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[buf]);
+    }
+    // ---- hand the state to the combiners, as the other consumers do
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+    const int rel = it - ib;
+    const int b = rel & 1;
+    if (rel >= 2 &&
+        !warp_wait(&bars.tmem_free[b], (uint32_t)((rel >> 1) - 1) & 1u, p.err_flag))
+      return;
+    if (c == 0)
+      *reinterpret_cast<float2*>(ml_buf + b * kMlFloats4 + (warp * 8 + gq) * 2) =
+          make_float2(m_run, l_run);
+    __syncwarp();
+    umma::fence_after_sync();
+    {
+      uint32_t ov[32];
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ov[4 * mt + j] = __float_as_uint(o[mt][j]);
+      }
+      umma::tmem_st32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) +
+                          (uint32_t)(b * kBufCols4 + (warp >> 2) * kStateCols4), ov);
+    }
+    umma::tmem_st_wait();
+    umma::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.posted[b]);
+  }
+}
+
+// Combiner warp 16+q, for every item of the CTA: (1) folds the four states of
+// its lane quarter, each rescaled to the sixteen warps' common max, into fold
+// slot q; (2) adds the four slots in order for m-tiles 2q and 2q + 1 and
+// writes that part of the partial.  O^T element j of m-tile mt is head dim
+// 16 gq + 2 mt + (j >> 1) of vector 2c + (j & 1), so slot q's part is dims
+// 16 gq + 4q .. + 3.  Each of folded and done completes once per item; a
+// combiner waits for done of the item before, so the fold buffer is never
+// overwritten while still being read.
+template <bool MERGE>
+__device__ void combiner_fp4(const DecodeParams& p, const DecodeDyn& D, uint32_t tmem,
+                             float4* fold, const float* ml_buf, int* merge_flag, CombBars bars) {
+  constexpr int KV = kKvFp4;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int q = warp - kCombineWarp4;
+  const int gq = lane >> 2, c = lane & 3;
+  int ib, ie;
+  cta_items(D, ib, ie);
+  if (ib >= ie) return;
+  int rh = run_of(D, ib);
+  Item x = item_of<KV>(p, D, ib, rh);
+  const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+  for (int it = ib; it < ie; ++it, next_item<KV>(p, D, x)) {
+    const RunInfo& ru = D.runs[x.run];
+    const int nq = ru.nrows * p.group;
+    const int rel = it - ib;
+    const int b = rel & 1;
+    const uint32_t par = (uint32_t)rel & 1u;
+    if (!warp_wait<128>(&bars.posted[b], (uint32_t)(rel >> 1) & 1u, p.err_flag)) return;
+    umma::fence_after_sync();
+    const uint32_t t0 = tl + (uint32_t)(b * kBufCols4);
+    const float* ml = ml_buf + b * kMlFloats4;
+    // vectors 2c and 2c + 1: the largest m of the sixteen warps, this
+    // quarter's four factors, and (combiner q < 2) vector 2c + q's sum
+    float M[2] = {-INFINITY, -INFINITY}, a[4][2];
+#pragma unroll
+    for (int w = 0; w < kWarps4; ++w) {
+      const float4 t = *reinterpret_cast<const float4*>(ml + (w * 8 + 2 * c) * 2);
+      M[0] = fmaxf(M[0], t.x);
+      M[1] = fmaxf(M[1], t.z);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 t = *reinterpret_cast<const float4*>(ml + ((q + 4 * k) * 8 + 2 * c) * 2);
+      a[k][0] = t.x == -INFINITY ? 0.f : fast_exp2(t.x - M[0]);
+      a[k][1] = t.z == -INFINITY ? 0.f : fast_exp2(t.z - M[1]);
+    }
+    const float Mq = q & 1 ? M[1] : M[0];
+    float L = 0.f;
+    if (q < 2) {
+#pragma unroll
+      for (int w = 0; w < kWarps4; ++w) {
+        const float2 t = *reinterpret_cast<const float2*>(ml + (w * 8 + 2 * c + q) * 2);
+        L += (t.x == -INFINITY ? 0.f : fast_exp2(t.x - Mq)) * t.y;
+      }
+    }
+    if (rel > 0 && !warp_wait(bars.done, par ^ 1u, p.err_flag)) return;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float acc[16];
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        uint32_t v[2][16];
+        umma::tmem_ld16(t0 + k * kStateCols4 + 16 * half, v[0]);
+        umma::tmem_ld16(t0 + (k + 1) * kStateCols4 + 16 * half, v[1]);
+        umma::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float f = __uint_as_float(v[0][i]);
+          acc[i] = k == 0 ? __fmul_rn(a[0][i & 1], f) : __fmaf_rn(a[k][i & 1], f, acc[i]);
+          acc[i] = __fmaf_rn(a[k + 1][i & 1], __uint_as_float(v[1][i]), acc[i]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        fold[(q * 8 + 4 * half + u) * 32 + lane] =
+            make_float4(acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
+    }
+    umma::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&bars.tmem_free[b]);
+      mbar_arrive(bars.folded);
+    }
+    if (!warp_wait(bars.folded, par, p.err_flag)) return;
+    {
+      float4 acc[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int mt = 2 * q + u;
+        acc[u] = fold[mt * 32 + lane];
+#pragma unroll
+        for (int sl = 1; sl < kCombineWarps; ++sl) {
+          const float4 t = fold[(sl * 8 + mt) * 32 + lane];
+          acc[u].x += t.x;
+          acc[u].y += t.y;
+          acc[u].z += t.z;
+          acc[u].w += t.w;
+        }
+      }
+      const float vs = __ldg(p.v_scale + x.g);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int qv = x.mt * Cfg<KV>::kVecs + 2 * c + e;
+        if (qv >= nq) continue;
+        const int r = qv / p.group;
+        const int h = x.g * p.group + (qv - r * p.group);
+        const size_t pslot = ((size_t)(ru.row0 + r) * p.hq + h) * p.max_splits + x.sigma;
+        *reinterpret_cast<float4*>(p.part_o + pslot * kHeadDim + 16 * gq + 4 * q) =
+            e ? make_float4(acc[0].y * vs, acc[0].w * vs, acc[1].y * vs, acc[1].w * vs)
+              : make_float4(acc[0].x * vs, acc[0].z * vs, acc[1].x * vs, acc[1].z * vs);
+        if (q == e && gq == 0)
+          *reinterpret_cast<float2*>(p.part_ml + pslot * 2) = make_float2(Mq, L);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars.done);
+    if constexpr (MERGE) merge_if_last<KV, kCombineWarp4>(p, ru, x, nq, merge_flag);
+  }
+}
+
+template <bool GEN, bool DEV, bool MERGE, bool APPEND>
+__global__ void __launch_bounds__(kThreads4, 1) decode_fp4_kernel(
+    const __grid_constant__ DecodeParams p) {
+  constexpr int KV = kKvFp4;
+  const DecodeDyn& D = DEV ? *p.dyn : p.d;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* stage_mem = smem;
+  float4* fold = reinterpret_cast<float4*>(smem + kRingBytes4);
+  float* ml_buf = reinterpret_cast<float*>(smem + kRingBytes4 + kCombBytes4);
+  int* stage_bad = reinterpret_cast<int*>(ml_buf + 2 * kMlFloats4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stage_bad + kMaxStages);
+  int* merge_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(
+      (reinterpret_cast<uintptr_t>(merge_flag + 1) + 7) & ~uintptr_t(7));
+  uint64_t* full = bars;
+  uint64_t* empty = bars + kMaxStages;
+  uint64_t* cbar = bars + 2 * kMaxStages;
+  CombBars cb{cbar, cbar + 2, cbar + 4, cbar + 5, cbar + 6};
+
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Cfg<KV>::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps4 / 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&cb.posted[i], kWarps4);
+      mbar_init(&cb.tmem_free[i], kCombineWarps);
+    }
+    mbar_init(cb.folded, kCombineWarps);
+    mbar_init(cb.done, kCombineWarps);
+    fence_mbar_init();
+  }
+  if (warp == kCombineWarp4) umma::tmem_alloc(tmem_slot, kTmemCols);
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  allow_next_grid();
+  wait_prior_grid();
+  if (warp < kCombineWarp4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsumer4));
+    consumer_fp4<GEN>(p, D, stage_mem, full, empty, stage_bad, tmem, ml_buf, cb);
+  } else if (warp < kProducerWarp4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCombine4));
+    combiner_fp4<MERGE>(p, D, tmem, fold, ml_buf, merge_flag, cb);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer4));
+    if (warp == kProducerWarp4) producer<KV, APPEND>(p, D, stage_mem, full, empty, stage_bad);
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  if (warp == kCombineWarp4) {
     umma::fence_after_sync();
     umma::tmem_dealloc(tmem, kTmemCols);
   }
@@ -1056,6 +1730,24 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Merg
                                   p.lse ? p.lse + (size_t)row * p.hq + h : nullptr);
 }
 
+template <bool GEN, bool DEV, bool MERGE, bool APPEND>
+cudaError_t launch_fp4(const DecodeParams& p, int grid, cudaStream_t s) {
+  constexpr auto kernel = decode_fp4_kernel<GEN, DEV, MERGE, APPEND>;
+  static PerDeviceOnce configured;
+  const cudaError_t e = configured.run([] {
+    // as below: never launch a split that waits for registers for ever
+    cudaFuncAttributes attr;
+    cudaError_t r = cudaFuncGetAttributes(&attr, kernel);
+    if (r != cudaSuccess) return r;
+    if (attr.numRegs * kThreads4 < 128 * (4 * kRegsConsumer4 + kRegsCombine4 + kRegsProducer4))
+      return cudaErrorInvalidValue;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes4);
+  });
+  if (e != cudaSuccess) return e;
+  const cudaError_t r = launch_pdl(kernel, dim3(grid), dim3(kThreads4), kSmemBytes4, s, p);
+  return r != cudaSuccess ? r : cudaGetLastError();
+}
+
 template <int KV, bool GEN, bool DEV, bool MERGE, bool APPEND>
 cudaError_t launch_partial(const DecodeParams& p, int grid, cudaStream_t s) {
   static PerDeviceOnce configured;
@@ -1077,13 +1769,22 @@ cudaError_t launch_partial(const DecodeParams& p, int grid, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// The instantiation of a cache type and a call's variants.
+template <int KV, bool GEN, bool DEV, bool MERGE, bool APPEND>
+cudaError_t launch_variant(const DecodeParams& p, int grid, cudaStream_t s) {
+  if constexpr (KV == kKvFp4)
+    return launch_fp4<GEN, DEV, MERGE, APPEND>(p, grid, s);
+  else
+    return launch_partial<KV, GEN, DEV, MERGE, APPEND>(p, grid, s);
+}
+
 template <int KV, bool DEV>
 cudaError_t launch_partial_dev(const DecodeParams& p, int grid, cudaStream_t s) {
   // Rows with ancestor masks take the general instantiation, so the plain
   // causal calls keep their own kernel's code.
-  if (p.anc) return launch_partial<KV, true, DEV, false, false>(p, grid, s);
-  if (p.k_rows) return launch_partial<KV, false, DEV, false, true>(p, grid, s);
-  return launch_partial<KV, false, DEV, false, false>(p, grid, s);
+  if (p.anc) return launch_variant<KV, true, DEV, false, false>(p, grid, s);
+  if (p.k_rows) return launch_variant<KV, false, DEV, false, true>(p, grid, s);
+  return launch_variant<KV, false, DEV, false, false>(p, grid, s);
 }
 
 template <int KV>
@@ -1091,8 +1792,8 @@ cudaError_t launch_partial_kv(const DecodeParams& p, int grid, cudaStream_t s) {
   // The merge in the kernel is built for plain causal rows in parameter mode.
   if (p.arrive) {
     if (p.anc || p.dyn || !p.out) return cudaErrorInvalidValue;
-    return p.k_rows ? launch_partial<KV, false, false, true, true>(p, grid, s)
-                    : launch_partial<KV, false, false, true, false>(p, grid, s);
+    return p.k_rows ? launch_variant<KV, false, false, true, true>(p, grid, s)
+                    : launch_variant<KV, false, false, true, false>(p, grid, s);
   }
   return p.dyn ? launch_partial_dev<KV, true>(p, grid, s)
                : launch_partial_dev<KV, false>(p, grid, s);
@@ -1108,7 +1809,8 @@ cudaError_t launch_decode_partial(const DecodeParams& p, int kv, int grid, cudaS
   switch (kv) {
     case kKvBf16: return launch_partial_kv<kKvBf16>(p, grid, s);
     case kKvFp8: return launch_partial_kv<kKvFp8>(p, grid, s);
-    default: return launch_partial_kv<kKvFp4>(p, grid, s);
+    case kKvFp4: return launch_partial_kv<kKvFp4>(p, grid, s);
+    default: return launch_partial_kv<kKvFp4Wide>(p, grid, s);
   }
 }
 

@@ -279,6 +279,12 @@ int no_throw(F&& fn) {
   }
 }
 
+// Runs of more than eight query vectors per kv head over a 4-bit cache take
+// the decode kernel of 16-vector items, the others that of eight (8 streams of
+// 65,536 keys: 16 vectors 178 us in one item, 264 us as two of eight; four
+// vectors WIDE_NARROW).
+bool on_wide_path(const Run& r, int G, int kv) { return kv == kKvFp4 && r.nrows * G > 8; }
+
 int to_err(cudaError_t e) { return e == cudaSuccess ? TFPA_OK : TFPA_ECUDA; }
 
 }  // namespace
@@ -420,6 +426,28 @@ int32_t verify_num_splits(int32_t seq_len) {
   return (np + pps - 1) / pps;
 }
 
+// Splits of a run of a 4-bit cache.  An item's end (sixteen warps' states
+// handed over and folded) costs as much as about 500 of its keys, and a key
+// arrives in half an e4m3 key's time, so the items are longer than the other
+// types': at least four pages (two where fewer than eight kv heads make few
+// items), and at most 16 (32) splits a stream.  A function of the stream's
+// length and the cache's kv heads only; never more than tfpa_num_splits.
+int32_t fp4_pages_per_split(int32_t seq_len, int32_t hkv) {
+  const int32_t np = pages_of(std::max(seq_len, 1));
+  if (np <= 8) return 1;
+  if (np <= 16) return 2;
+  return hkv >= 8 ? std::max<int32_t>(4, (np + 15) / 16) : std::max<int32_t>(2, (np + 31) / 32);
+}
+int32_t fp4_num_splits(int32_t seq_len, int32_t hkv) {
+  const int32_t np = pages_of(std::max(seq_len, 1));
+  const int32_t pps = fp4_pages_per_split(seq_len, hkv);
+  return (np + pps - 1) / pps;
+}
+// Splits of a run that the decode partial kernel takes.
+int32_t decode_num_splits(int kv, int32_t seq_len, int32_t hkv) {
+  return kv == kKvFp4 ? fp4_num_splits(seq_len, hkv) : tfpa_num_splits(seq_len);
+}
+
 // K/V sources of one launch: source 0 is the pool, 1.. are slab streams.
 struct SourceSet {
   int slab_seg[kMaxSlabs];
@@ -484,12 +512,15 @@ void fill_run(RunInfo& ri, const tfpa_seg& g, int src, int row0, int nrows, int 
   ri.pad_ = 0;
 }
 
+// Query vectors of a decode work item (an m-tile of the decode kernels).
+int item_vectors(int kv) { return kv == kKvFp4 ? 8 : 16; }
+
 // Key stages of decode work item (m-tile mt, split sigma) of a run: its
 // split's keys, cut at the stream's end and at the last position of the
 // item's rows (the kernel's item key range, in units of the kernel's chunk).
-int item_stages(const RunInfo& ri, int G, int mt, int sigma, int chunk) {
+int item_stages(const RunInfo& ri, int G, int mt, int sigma, int chunk, int vecs) {
   const int nq = ri.nrows * G;
-  const int last_qv = std::min(16 * mt + 15, nq - 1);
+  const int last_qv = std::min(vecs * (mt + 1), nq) - 1;
   const int maxpos = ri.pos0 + last_qv / G;
   const int klo = sigma * ri.pps * kPage;
   const int khi = std::min(std::min(klo + ri.pps * kPage, ri.seq_len), maxpos + 1);
@@ -505,6 +536,7 @@ int item_stages(const RunInfo& ri, int G, int mt, int sigma, int chunk) {
 // found by a binary search in the block of the kv head that holds it.
 void plan_cta_ranges(DecodeParams& p, int nr, int G, int kv, int grid) {
   const int chunk = kv == kKvBf16 ? 128 : 256;
+  const int vecs = item_vectors(kv);
   // The fixed cost, in key stages, was measured on the overcommitted pool
   // (17 streams of 1k-262k keys, e4m3): 0 -> 380 us, 1 -> 341 us, 2 -> 348 us,
   // 4 -> 377 us, 8 -> 444 us; uniform batches do not depend on it.
@@ -515,15 +547,18 @@ void plan_cta_ranges(DecodeParams& p, int nr, int G, int kv, int grid) {
   int64_t total = 0;
   for (int r = 0; r < nr; ++r) {
     const RunInfo& ri = p.d.runs[r];
-    const int mtiles = (ri.nrows * G + 15) / 16;
+    const int mtiles = (ri.nrows * G + vecs - 1) / vecs;
     blk[r] = (int32_t)cum.size();
     int64_t sum = 0;
     cum.push_back(0);
-    for (int mt = 0; mt < mtiles; ++mt)
-      for (int sg = 0; sg < ri.nsplit; ++sg) {
-        sum += item_stages(ri, G, mt, sg, chunk) + kItemCost;
-        cum.push_back(sum);
-      }
+    // splits fastest, or (4 bits) a split's m-tiles
+    const bool by_split = kv == kKvFp4 || kv == kKvFp4Wide;
+    const int n = mtiles * ri.nsplit, inner = by_split ? mtiles : ri.nsplit;
+    for (int i = 0; i < n; ++i) {
+      const int a = i / inner, b = i - a * inner;
+      sum += item_stages(ri, G, by_split ? b : a, by_split ? a : b, chunk, vecs) + kItemCost;
+      cum.push_back(sum);
+    }
     total += sum * p.hkv;
   }
   blk[nr] = (int32_t)cum.size();
@@ -624,8 +659,8 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
   int32_t taken = 0;  // rows of runs[ri] already launched
   // Launch parameters are large (kernel arguments by value): each host
   // thread builds them in its own buffers.
-  thread_local DecodeParams p;
-  thread_local PrefillParams pv;   // the tensor-core verify launch of the same rows
+  thread_local DecodeParams pd[2];   // [1]: a 4-bit cache's runs of more than eight vectors
+  thread_local PrefillParams pv;     // the tensor-core verify launch of the same rows
   thread_local MergeParams mp;
   // Runs of four or more m-tiles (16 query vectors each, so at least 49
   // vectors per kv head) are dense enough for the tensor cores: they go to
@@ -639,8 +674,8 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
   while (ri < runs.size()) {
     SourceSet ss;
     const int32_t base = runs[ri].row0 + taken;  // first call row of this launch
-    int32_t nrows = 0, items = 0, tiles = 0;
-    int nr = 0, nd = 0, nv = 0;  // runs of the slice: all, decode, verify
+    int32_t nrows = 0, items[2] = {0, 0}, tiles = 0;
+    int nr = 0, nd[2] = {0, 0}, nv = 0;  // runs of the slice: all, decode, verify
     while (ri < runs.size() && nr < kMaxRuns && nrows < sc->cap_rows) {
       const Run& r = runs[ri];
       const int src = ss.add(segs, r.seg);
@@ -657,11 +692,19 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
         tiles += c->hkv * ((take + vrows - 1) / vrows) * info.nsplit;
         mp.d.runs[nr] = MergeRun{nrows, take, info.nsplit, 0};
       } else {
-        if (nd == 0) std::memset(&p, 0, sizeof(p));
-        RunInfo& info = p.d.runs[nd++];
+        // decided on the call's whole run, like the verify path
+        const int w = on_wide_path(r, G, kv) ? 1 : 0;
+        DecodeParams& p = pd[w];
+        if (nd[w] == 0) std::memset(&p, 0, sizeof(p));
+        RunInfo& info = p.d.runs[nd[w]++];
         fill_run(info, g, src, nrows, take, r.pos0 + taken);
-        info.item0 = items;
-        items += c->hkv * ((take * G + 15) / 16) * info.nsplit;
+        if (kv == kKvFp4) {
+          info.pps = fp4_pages_per_split(g.seq_len, c->hkv);
+          info.nsplit = fp4_num_splits(g.seq_len, c->hkv);
+        }
+        info.item0 = items[w];
+        const int vecs = item_vectors(w ? kKvFp4Wide : kv);
+        items[w] += c->hkv * ((take * G + vecs - 1) / vecs) * info.nsplit;
         mp.d.runs[nr] = MergeRun{nrows, take, info.nsplit, 0};
       }
       ++nr;
@@ -682,8 +725,13 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
     // its last split, reading every split's partial: cheap for a few splits,
     // slower than a separate grid-wide merge for many.
     bool fused = sliced && nv == 0 && sc->arrive && !anc && !sink.device();
-    for (int r = 0; fused && r < nd; ++r) fused = p.d.runs[r].nsplit <= kFusedMergeMaxSplits;
-    if (nd > 0) {
+    for (int w = 0; w < 2; ++w)
+      for (int r = 0; fused && r < nd[w]; ++r)
+        fused = pd[w].d.runs[r].nsplit <= kFusedMergeMaxSplits;
+    for (int w = 0; w < 2; ++w) {
+      if (nd[w] == 0) continue;
+      DecodeParams& p = pd[w];
+      const int wkv = w ? kKvFp4Wide : kv;
       if (kv != kKvFp4 &&
           (e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 128, p.maps, p.nsrc)))
         return e;
@@ -701,8 +749,8 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
       p.arrive = fused ? sc->arrive + (size_t)srow * c->hq : nullptr;
       p.out = fused ? static_cast<__nv_bfloat16*>(out) + (size_t)base * hd : nullptr;
       p.lse = fused && lse ? lse + (size_t)base * c->hq : nullptr;
-      p.d.nruns = nd;
-      p.d.n_items = items;
+      p.d.nruns = nd[w];
+      p.d.n_items = items[w];
       p.hq = c->hq;
       p.hkv = c->hkv;
       p.group = G;
@@ -712,10 +760,10 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
       p.scale_log2 = scale * 1.4426950408889634f;
       // In device mode the grid is one CTA per SM whatever the work, so
       // that the launch can be replayed as the streams grow.
-      const int grid = std::min(sink.device() ? nsm : std::min(items, nsm), kMaxDecodeGrid);
-      plan_cta_ranges(p, nd, G, kv, grid);
-      record(1, base, nrows, nd, items, grid, (int64_t)base * hd, 0);
-      if ((e = sink.decode(p, kv, grid))) return e;
+      const int grid = std::min(sink.device() ? nsm : std::min(items[w], nsm), kMaxDecodeGrid);
+      plan_cta_ranges(p, nd[w], G, wkv, grid);
+      record(1, base, nrows, nd[w], items[w], grid, (int64_t)base * hd, 0);
+      if ((e = sink.decode(p, wkv, grid))) return e;
     }
     if (nv > 0) {
       if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 128, pv.maps, pv.nsrc))) return e;
@@ -792,7 +840,9 @@ extern "C" int tfpa_row_splits(const tfpa_cache* cache, const tfpa_seg* segs, in
   const int G = cache->hq / cache->hkv;
   for (const Run& r : runs) {
     const int32_t L = segs[r.seg].seq_len;
-    const int32_t n = on_verify_path(r, G, cache->dtype) ? verify_num_splits(L) : tfpa_num_splits(L);
+    const int32_t n = on_verify_path(r, G, cache->dtype)
+                          ? verify_num_splits(L)
+                          : decode_num_splits(cache->dtype, L, cache->hkv);
     for (int32_t i = 0; i < r.nrows; ++i) nsplit[r.row0 + i] = n;
   }
   return TFPA_OK;

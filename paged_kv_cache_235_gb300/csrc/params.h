@@ -23,6 +23,9 @@ constexpr int kMaxDecodeGrid = 256;  // CTAs of one decode partial launch, at mo
 
 // Element type of a cache (the values of tfpa_kv_dtype).
 enum KvType : int { kKvBf16 = 0, kKvFp8 = 1, kKvFp4 = 2 };
+// A decode partial launch over a 4-bit cache whose runs have more than eight
+// query vectors per kv head.
+constexpr int kKvFp4Wide = 3;
 
 // A 4-bit cache: storage row R (pool: (page * hkv + g) * 256 + position %
 // 256; slab: g * slab_cap + position) lies in half-block R / 128, which
