@@ -1347,7 +1347,7 @@ extern "C" int tfpa_restore_kv(const tfpa_cache* cache, const tfpa_seg* seg, int
 
 // ------------------------------------------------------------ eviction
 namespace {
-constexpr int kMassKeys = 128;   // keys of a block of the weight kernel
+constexpr int kMassKeys = 128;   // keys of a tile of the weight kernel
 
 int mass_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const void* q,
               const float* lse, const int32_t* row_seg, const int32_t* row_pos, int32_t rows,
@@ -1370,6 +1370,9 @@ int mass_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const voi
   // block sums all of its rows and the order of a sum is fixed.
   std::stable_sort(runs.begin(), runs.end(),
                    [](const Run& a, const Run& b) { return a.seg < b.seg; });
+  const int kv = c->dtype;
+  const int nsm = sm_count();
+  if (nsm < 1) return TFPA_ECUDA;
   thread_local MassParams p;
   size_t ri = 0;
   int32_t last_seg = -1;                // the segment of the previous launch's last run
@@ -1377,6 +1380,7 @@ int mass_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const voi
     std::memset(&p, 0, sizeof(p));
     int32_t nrows = 0, nr = 0;
     int64_t items = 0;
+    SourceSet ss;
     const int32_t first_row = runs[ri].row0;
     while (ri < runs.size() && nr < kMaxRuns) {
       const Run& r = runs[ri];
@@ -1384,6 +1388,8 @@ int mass_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const voi
         const tfpa_seg& g = segs[r.seg];
         const int64_t blocks = (int64_t)c->hkv * ((g.seq_len + kMassKeys - 1) / kMassKeys);
         if (items + blocks > INT32_MAX) break;
+        const int src = ss.add(segs, r.seg);
+        if (src < 0) break;
         MassSeg& m = p.segs[p.nsegs++];
         m.page_table = g.page_table;
         m.k_base = g.page_table ? c->k_pool : g.k_slab;
@@ -1393,6 +1399,7 @@ int mass_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const voi
         m.item0 = (int32_t)items;
         m.run0 = nr;
         m.decay = r.seg == last_seg ? 1.f : decay;
+        m.src = src;
         items += blocks;
         last_seg = r.seg;
       }
@@ -1412,9 +1419,24 @@ int mass_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const voi
     p.num_pages = c->num_pages;
     p.mass_cap = mass_cap;
     p.scale_log2 = scale * 1.4426950408889634f;
-    record(10, first_row, nrows, nr, (int32_t)items, (int32_t)items, 0, 0);
+    p.tiles = (int32_t)items;
+    if (kv != kKvFp4) {
+      const bool fp8 = kv == kKvFp8;
+      const int inner = fp8 ? 128 : 64;
+      if (ss.pool && (e = get_map(c->k_pool, (uint64_t)c->num_pages * c->hkv * kPage, fp8, inner,
+                                  kMassKeys, &p.maps[0])))
+        return e;
+      for (int i = 0; i < ss.nslab; ++i) {
+        const tfpa_seg& g = segs[ss.slab_seg[i]];
+        if ((e = get_map(g.k_slab, (uint64_t)c->hkv * g.slab_cap, fp8, inner, kMassKeys,
+                         &p.maps[i + 1])))
+          return e;
+      }
+    }
+    const int grid = (int)std::min<int64_t>(items, nsm);
+    record(10, first_row, nrows, nr, (int32_t)items, grid, 0, 0);
     if (!dry_run())
-      if ((e = to_err(launch_key_mass(p, c->dtype, (int)items, stream)))) return e;
+      if ((e = to_err(launch_key_mass(p, kv, grid, stream)))) return e;
   }
   return TFPA_OK;
 }

@@ -6,266 +6,404 @@
 // the weights that the rows' attention (which left lse) gave the key.  K is
 // read once and V not at all.
 //
-// A block of four warps takes 128 keys of one (segment, kv head), 32 a warp.
-// A warp turns its keys into the A fragments of mma.sync m16n8k16 (keys x
-// head dims) straight from global memory, every load issued before the first
-// use, and keeps them while the segment's query vectors pass by, eight at a
-// time, as B fragments from shared memory.  So a key's weights lie in four
-// neighbouring lanes' registers, their sum needs two shuffles at the very
-// end, and one thread owns a key's entry: no atomics, and a fixed order.
-// e4m3 and 4-bit keys go through f16 (exact), with each query vector scaled
-// into f16 range by a power of two.
+// Keys are the rows of the products and query vectors their columns:
+//   D [128 keys][N vectors] = K Q^T (tcgen05, one MMA chain a key tile),
+// so that a key is a TMEM lane and its weights one thread's columns: the
+// thread sums them in a fixed order and owns the key's entry; no shuffles, no
+// atomics.  Persistent CTAs, each an equal run of the call's key tiles
+// (segment, kv head, 128 keys), so mostly of one (segment, kv head), whose
+// query vectors it stages once as the B operand (up to 256; more go in
+// passes over the same keys).
+//   warp 0       producer: key tiles into a ring, by TMA (bf16: the operand
+//                itself; e4m3: staging) or bulk copies (4 bits: staging)
+//   warp 1       TMEM owner and MMA issuer, two D buffers
+//   warps 4-11   epilogue: two groups of four, tiles in turn
+//   warps 12-19  (e4m3, 4 bits) converters: staged tiles -> f16 operand tiles
+// e4m3 and 4-bit keys are exact in f16; their query vectors are scaled into
+// f16 range by a power of two each.
+#include <climits>
+
 #include "common.cuh"
-#include "kvstore.cuh"
+#include "convert.cuh"
 #include "params.h"
+#include "tcgen05.cuh"
 
 namespace tfpa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kKeys = 32 * kWarps;       // keys of a block
-constexpr int kVec = 64;                 // query vectors staged at once
-constexpr int kQStride = 320;            // bytes: eight rows' 64-byte reads fall in all banks
-
-// Byte offset, within a staged query vector, of head dim d (a multiple of
-// 8).  Lane c of a quad holds 32 of a key's head dims, 16 bytes of the
-// cache's row at a time; its j-th 16 bytes of the query sit at 64 j + 16 c.
+constexpr int kTile = 128;               // keys of a tile
+constexpr int kVec = 256;                // query vectors of a pass, at most
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+constexpr int kConvWarp0 = 12, kConvWarps = 8;
 template <int KV>
-__device__ __forceinline__ int q_off(int d) {
-  if (KV == kKvBf16) return d * 2;
-  if (KV == kKvFp8) {
-    const int id = d >> 4;
-    return (2 * (id >> 2) + ((d >> 3) & 1)) * 64 + (id & 3) * 16;
-  }
-  return ((d & 31) >> 3) * 64 + (d >> 5) * 16;
-}
-
-// Lane (gq, c)'s 32 head dims of one stored row, as 16 operand pairs.
-template <int KV>
-struct RawRow {
-  uint4 w[KV == kKvBf16 ? 4 : KV == kKvFp8 ? 2 : 1];
-  uint16_t s;
-  __device__ __forceinline__ void load(const uint8_t* base, size_t row, int c) {
-    if (KV == kKvFp4) {
-      w[0] = __ldg(reinterpret_cast<const uint4*>(base + fp4_codes(row)) + c);
-      s = __ldg(reinterpret_cast<const uint16_t*>(base + fp4_scales(row)) + c);
-    } else {
-      constexpr int n = KV == kKvBf16 ? 4 : 2;
-      const uint4* p = reinterpret_cast<const uint4*>(base + row * (n * 64)) + c;
-#pragma unroll
-      for (int j = 0; j < n; ++j) w[j] = __ldg(p + 4 * j);
-    }
-  }
-  __device__ __forceinline__ void pairs(uint32_t (&r)[16]) const {
-    if (KV == kKvBf16) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        r[4 * j] = w[j].x;
-        r[4 * j + 1] = w[j].y;
-        r[4 * j + 2] = w[j].z;
-        r[4 * j + 3] = w[j].w;
-      }
-    } else if (KV == kKvFp8) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          r[8 * j + 2 * i] = e4m3x2_to_f16x2((uint16_t)(v[i] & 0xFFFF));
-          r[8 * j + 2 * i + 1] = e4m3x2_to_f16x2((uint16_t)(v[i] >> 16));
-        }
-      }
-    } else {
-      const uint32_t s2 = e4m3x2_to_f16x2(s);
-      const uint32_t sc[2] = {prmt(s2, s2, 0x1010), prmt(s2, s2, 0x3232)};
-      const uint32_t v[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t h[4];
-        e2m1x8_to_f16x8(v[i], h);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) r[4 * i + j] = hmul2(h[j], sc[i >> 1]);
-      }
-    }
-  }
+struct MassCfg {
+  static constexpr bool kF16 = KV != kKvBf16;
+  static constexpr int kThreads = kF16 ? 640 : 384;
+  static constexpr int kStageBytes =
+      KV == kKvBf16 ? 32768 : KV == kKvFp8 ? 16384 : kFp4HalfBytes;
+  static constexpr int kStages = KV == kKvBf16 ? 4 : KV == kKvFp8 ? 5 : 9;
+  static constexpr int kOps = kF16 ? 2 : 0;              // f16 operand tiles
+  static constexpr int kOffQ = 0;                        // 64 KB
+  static constexpr int kOffOp = 65536;
+  static constexpr int kOffStage = kOffOp + kOps * 32768;
+  static constexpr int kOffTab = (kOffStage + kStages * kStageBytes + 1023) & ~1023;
+  static constexpr int kOffLim = kOffTab + kVec * 8;
+  static constexpr int kOffBar = kOffLim + kVec * 4;
+  static constexpr int kBars = 2 * kStages + 2 * 2 + 2 * 2 + 1;
+  static constexpr int kSmem = kOffBar + kBars * 8 + 32 + 1024;
+  static_assert(kSmem <= 232448, "shared memory");
 };
 
+struct MassBars {
+  uint64_t *full, *empty;        // [kStages]: the ring
+  uint64_t *op_full, *op_empty;  // [2]: f16 operand tiles
+  uint64_t *d_full, *d_empty;    // [2]: D buffers
+  uint64_t* drain;
+  uint32_t* tmem_slot;
+  volatile int* abort;
+  int* span;                     // [2][2], by pass parity: its rows' least, largest position
+};
+
+// Vector v of segment sg: its run and row.
+__device__ __forceinline__ void find_vector(const MassParams& p, const MassSeg& sg, int v,
+                                            int& row, int& pos, int& head) {
+  int r = sg.run0;
+  while (v >= p.runs[r].nrows * p.group) v -= p.runs[r++].nrows * p.group;
+  const int k = v / p.group;
+  row = p.runs[r].row0 + k;
+  pos = p.runs[r].pos0 + k;
+  head = v - k * p.group;
+}
+
+// Query vectors [v0, v0 + nv) as the B operand ([n rows][2 halves of 64],
+// 128B swizzle; rows from nv on zero) with each one's score factor, -lse and
+// position; all threads, 16 a vector.
 template <int KV>
-__global__ void __launch_bounds__(32 * kWarps) key_mass_kernel(
-    const __grid_constant__ MassParams p) {
-  __shared__ __align__(16) uint8_t q_s[kVec * kQStride];
-  __shared__ float sc_s[kVec], lse_s[kVec];
-  __shared__ int lim_s[kVec];
+__device__ void stage_q(const MassParams& p, const MassSeg& sg, int g, int v0, int nv, int n,
+                        uint8_t* smem, int* span) {
+  using C = MassCfg<KV>;
+  const uint32_t qb = smem_u32(smem + C::kOffQ);
+  float2* tab = reinterpret_cast<float2*>(smem + C::kOffTab);
+  int* lims = reinterpret_cast<int*>(smem + C::kOffLim);
+  const int t = threadIdx.x & 15;
+  for (int i = threadIdx.x >> 4; i < n; i += C::kThreads / 16) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    int lim = -1;
+    float sc = 0.f, neg = -INFINITY;
+    if (i < nv) {
+      int row, head;
+      find_vector(p, sg, v0 + i, row, lim, head);
+      const size_t rh = (size_t)row * p.hq + g * p.group + head;
+      w = __ldg(reinterpret_cast<const uint4*>(p.q + rh * kHeadDim) + t);
+      sc = p.scale_log2;
+      // a row without keys has lse -inf and gives no weight
+      const float lse = __ldg(p.lse + rh);
+      neg = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+    }
+    if (C::kF16) {
+      // f16, the vector's largest magnitude brought into [2^13, 2^14):
+      // exact for every element within 2^28 of it
+      uint32_t e[4] = {w.x, w.y, w.z, w.w};
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        amax = fmaxf(amax, fabsf(__uint_as_float(e[j] << 16)));
+        amax = fmaxf(amax, fabsf(__uint_as_float(e[j] & 0xFFFF0000u)));
+      }
+      const unsigned lanes = 0xFFFFu << (threadIdx.x & 16);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, o));
+      int ex;
+      frexpf(amax, &ex);
+      ex = max(min(ex, 120), -100);
+      const float up = __int_as_float((127 + 14 - ex) << 23);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        e[j] = pack_f16x2(__uint_as_float(e[j] << 16) * up,
+                          __uint_as_float(e[j] & 0xFFFF0000u) * up);
+      w = make_uint4(e[0], e[1], e[2], e[3]);
+      sc *= __int_as_float((127 - 14 + ex) << 23) * __ldg(p.k_scale + g);
+    }
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                     swz128(qb + (uint32_t)(t >> 3) * (uint32_t)n * 128u, i, t & 7)),
+                 "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+    if (t == 0) {
+      tab[i] = make_float2(sc, neg);
+      lims[i] = lim;
+      if (i < nv) {
+        atomicMin(&span[0], lim);
+        atomicMax(&span[1], lim);
+      }
+    }
+  }
+  fence_proxy_async_smem();
+}
+
+template <int KV>
+__global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
+    key_mass_kernel(const __grid_constant__ MassParams p) {
+  using C = MassCfg<KV>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  MassBars b;
+  b.full = bars;
+  b.empty = bars + C::kStages;
+  b.op_full = bars + 2 * C::kStages;
+  b.op_empty = b.op_full + 2;
+  b.d_full = b.op_full + 4;
+  b.d_empty = b.op_full + 6;
+  b.drain = b.op_full + 8;
+  b.tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
+  b.abort = reinterpret_cast<volatile int*>(b.tmem_slot + 1);
+  b.span = reinterpret_cast<int*>(b.tmem_slot + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&b.full[i], 1);
+      mbar_init(&b.empty[i], C::kF16 ? kConvWarps : 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b.op_full[i], kConvWarps);
+      mbar_init(&b.op_empty[i], 1);
+      mbar_init(&b.d_full[i], 1);
+      mbar_init(&b.d_empty[i], kEpiWarps / 2);
+    }
+    mbar_init(b.drain, 1);
+    *b.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) umma::tmem_alloc(b.tmem_slot, 512);
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tmem = *b.tmem_slot;
   allow_next_grid();
   wait_prior_grid();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gq = lane >> 2, c = lane & 3;
-  int si = 0;
-  while (si + 1 < p.nsegs && p.segs[si + 1].item0 <= (int)blockIdx.x) ++si;
-  const MassSeg& sg = p.segs[si];
-  const int tiles = (sg.seq_len + kKeys - 1) / kKeys;
-  const int local = blockIdx.x - sg.item0;
-  const int g = local / tiles;
-  const int key0 = (local - g * tiles) * kKeys;
-  size_t row0;                                            // storage row of key0
-  if (sg.page_table) {
-    const int pid = __ldg(sg.page_table + (key0 >> 8));
-    if ((unsigned)pid >= (unsigned)p.num_pages) {         // its keys keep their entries
-      if (threadIdx.x == 0) flag_error(p.err_flag, kErrBadPage);
-      return;
-    }
-    row0 = ((size_t)pid * p.hkv + g) * kPage + (key0 & (kPage - 1));
-  } else {
-    row0 = (size_t)g * sg.slab_cap + key0;
-  }
-  // ---- this warp's 32 keys as A fragments: m-tile t holds keys 16 t + gq
-  // and 16 t + 8 + gq of the warp
-  const int wkey = key0 + 32 * warp;
-  uint32_t a[2][2][16];
-  if (wkey < sg.seq_len) {
-    RawRow<KV> raw[2][2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr)
-        raw[t][hr].load(static_cast<const uint8_t*>(sg.k_base),
-                        row0 + 32 * warp + 16 * t + 8 * hr + gq, c);
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr) raw[t][hr].pairs(a[t][hr]);
-  }
-  float acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-  const float ks = KV == kKvBf16 ? 1.f : __ldg(p.k_scale + g);
-  const int G = p.group;
-  for (int ri = sg.run0; ri < sg.run0 + sg.nruns; ++ri) {
-    const MassRun ru = p.runs[ri];
-    if (ru.pos0 + ru.nrows - 1 < key0) continue;          // no row of it sees the block's keys
-    const int nq = ru.nrows * G;
-    for (int v0 = 0; v0 < nq; v0 += kVec) {
-      const int nv = min(kVec, nq - v0);
-      __syncthreads();                                    // the previous vectors are done with
-      // four threads a vector, 32 head dims each
-      for (int i = threadIdx.x >> 2; i < ((nv + 7) & ~7); i += 8 * kWarps) {
-        const int part = threadIdx.x & 3;
-        const int v = v0 + i;
-        uint4 w[4];
-        int lim = -1;
-        float sc = 0.f, l2 = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = make_uint4(0, 0, 0, 0);
-        if (i < nv) {
-          const int r = v / G;
-          const int h = g * G + (v - r * G);
-          const size_t rh = (size_t)(ru.row0 + r) * p.hq + h;
-          const uint4* qp = reinterpret_cast<const uint4*>(p.q + rh * kHeadDim) + 4 * part;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = __ldg(qp + j);
-          lim = ru.pos0 + r;
-          sc = p.scale_log2 * ks;
-          const float lse = __ldg(p.lse + rh);
-          // a row without keys has lse -inf and gives no weight
-          l2 = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
-        }
-        if (KV != kKvBf16) {
-          // f16, the vector's largest magnitude brought into [2^13, 2^14):
-          // exact for every element within 2^28 of it
-          float amax = 0.f;
-          uint32_t* e = reinterpret_cast<uint32_t*>(w);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            amax = fmaxf(amax, fabsf(__uint_as_float(e[j] << 16)));
-            amax = fmaxf(amax, fabsf(__uint_as_float(e[j] & 0xFFFF0000u)));
-          }
-          const unsigned quad = 0xFu << (lane & 28);      // a vector's four threads
-          amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
-          amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
-          int ex;
-          frexpf(amax, &ex);
-          ex = max(min(ex, 120), -100);
-          const float up = __int_as_float((127 + 14 - ex) << 23);
-          sc *= __int_as_float((127 - 14 + ex) << 23);
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            e[j] = pack_f16x2(__uint_as_float(e[j] << 16) * up,
-                              __uint_as_float(e[j] & 0xFFFF0000u) * up);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(q_s + i * kQStride + q_off<KV>(32 * part + 8 * j)) = w[j];
-        if (part == 0) {
-          sc_s[i] = sc;
-          lse_s[i] = l2;
-          lim_s[i] = lim;
-        }
+
+  const int t0 = (int)((int64_t)p.tiles * blockIdx.x / gridDim.x);
+  const int t1 = (int)((int64_t)p.tiles * (blockIdx.x + 1) / gridDim.x);
+  const float2* tab = reinterpret_cast<const float2*>(smem + C::kOffTab);
+  const int* lims = reinterpret_cast<const int*>(smem + C::kOffLim);
+  uint32_t cnt = 0;                      // tiles multiplied so far (every role's count)
+  int si = 0, pass = 0;
+  for (int t = t0; t < t1;) {
+    while (si + 1 < p.nsegs && p.segs[si + 1].item0 <= t) ++si;
+    const MassSeg& sg = p.segs[si];
+    const int tiles = (sg.seq_len + kTile - 1) / kTile;
+    const int local = t - sg.item0;
+    const int g = local / tiles, kt0 = local - g * tiles;
+    const int nt = min(t1 - t, tiles - kt0);
+    int total = 0;                       // the segment's query vectors
+    for (int r = sg.run0; r < sg.run0 + sg.nruns; ++r) total += p.runs[r].nrows * p.group;
+    for (int v0 = 0; v0 < total; v0 += kVec, ++pass) {
+      const int nv = min(kVec, total - v0);
+      const int n = (nv + 15) & ~15;     // the MMA's N
+      int* span = b.span + 2 * (pass & 1);   // the other one may still be read
+      if (threadIdx.x == 0) {
+        span[0] = INT_MAX;
+        span[1] = -1;
       }
+      __syncthreads();                   // every role is done with the pass before
+      if (*b.abort) goto out;
+      stage_q<KV>(p, sg, g, v0, nv, n, smem, span);
       __syncthreads();
-      if (wkey >= sg.seq_len) continue;
-      for (int n0 = 0; n0 < nv; n0 += 8) {
-        uint32_t b[16];
-        const uint32_t qa = smem_u32(q_s) + (n0 + gq) * kQStride + 16 * c;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 t = lds128(qa + 64 * j);
-          b[4 * j] = t.x;
-          b[4 * j + 1] = t.y;
-          b[4 * j + 2] = t.z;
-          b[4 * j + 3] = t.w;
-        }
-        float d[2][4] = {};
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const uint32_t af[4] = {a[t][0][2 * k], a[t][1][2 * k], a[t][0][2 * k + 1],
-                                    a[t][1][2 * k + 1]};
-            if (KV == kKvBf16)
-              mma_bf16(d[t], af, b[2 * k], b[2 * k + 1]);
-            else
-              mma_f16(d[t], af, b[2 * k], b[2 * k + 1]);
-          }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {                     // vectors n0 + 2 c + e
-          const int v = n0 + 2 * c + e;
-          const float sc = sc_s[v], l2 = lse_s[v];
-          const int lim = lim_s[v];
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int hr = 0; hr < 2; ++hr) {
-              const float w = fast_exp2(__fmaf_rn(d[t][2 * hr + e], sc, -l2));
-              acc[t][hr] += wkey + 16 * t + 8 * hr + gq <= lim ? w : 0.f;
+      const int minlim = span[0], maxlim = span[1];
+      // tiles past the last row's position get no weight
+      const int mt = max(0, min(nt, maxlim / kTile + 1 - kt0));
+      if (warp == 0) {
+        if (lane == 0) {
+          int page_at = -1, pid = 0;
+          for (int i = 0; i < mt; ++i) {
+            const int key0 = (kt0 + i) * kTile;
+            int row;
+            if (sg.page_table) {
+              const int page = key0 >> 8;
+              if (page != page_at) {
+                page_at = page;
+                pid = __ldg(sg.page_table + page);
+                if ((unsigned)pid >= (unsigned)p.num_pages) {
+                  flag_error(p.err_flag, kErrBadPage);
+                  pid = 0;
+                }
+              }
+              row = (pid * p.hkv + g) * kPage + (key0 & (kPage - 1));
+            } else {
+              row = g * sg.slab_cap + key0;
             }
+            const uint32_t st = cnt + i;
+            const int s = st % C::kStages;
+            if (!mbar_wait_or_abort(&b.empty[s], ((st / C::kStages) & 1) ^ 1, p.err_flag, b.abort))
+              break;
+            uint8_t* dst = smem + C::kOffStage + s * C::kStageBytes;
+            mbar_arrive_expect_tx(&b.full[s], C::kStageBytes);
+            if (KV == kKvBf16) {
+              tma_load_2d(dst, &p.maps[sg.src], 0, row, &b.full[s]);
+              tma_load_2d(dst + 16384, &p.maps[sg.src], 64, row, &b.full[s]);
+            } else if (KV == kKvFp8) {
+              tma_load_2d(dst, &p.maps[sg.src], 0, row, &b.full[s]);
+            } else {
+              bulk_load(dst, static_cast<const uint8_t*>(sg.k_base) +
+                                 (size_t)(row / kHalfRows) * kFp4HalfBytes,
+                        kFp4HalfBytes, &b.full[s]);
+            }
+          }
+        }
+        __syncwarp();
+      } else if (warp == 1) {
+        const uint32_t idesc = umma::idesc_f16(128, 16, !C::kF16, false) + ((uint32_t)(n - 16) >> 3 << 17);
+        const uint32_t qb = smem_u32(smem + C::kOffQ);
+        for (int i = 0; i < mt; ++i) {
+          const uint32_t st = cnt + i;
+          const int s = C::kF16 ? st & 1 : st % C::kStages;
+          uint64_t* ready = C::kF16 ? &b.op_full[s] : &b.full[s];
+          const uint32_t ph = C::kF16 ? (st >> 1) & 1 : (st / C::kStages) & 1;
+          const int d = st & 1;
+          if (!mbar_wait_or_abort(ready, ph, p.err_flag, b.abort)) break;
+          if (!mbar_wait_or_abort(&b.d_empty[d], ((st >> 1) & 1) ^ 1, p.err_flag, b.abort)) break;
+          __syncwarp();
+          umma::fence_after_sync();
+          if (lane == 0) {
+            const uint32_t kb =
+                smem_u32(smem + (C::kF16 ? C::kOffOp + s * 32768 : C::kOffStage + s * 32768));
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              const uint64_t ad =
+                  umma::smem_desc_sw128(kb + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024);
+              const uint64_t bd = umma::smem_desc_sw128(
+                  qb + (ks >> 2) * (uint32_t)n * 128u + (ks & 3) * 32, 16, 1024);
+              umma::mma_ss(tmem + d * 256, ad, bd, idesc, ks > 0 ? 1u : 0u);
+            }
+            umma::commit(C::kF16 ? &b.op_empty[s] : &b.empty[s]);
+            umma::commit(&b.d_full[d]);
+          }
+          __syncwarp();
+        }
+      } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
+        const int grp = (warp - kEpiWarp0) >> 2;
+        const float decay = v0 == 0 ? sg.decay : 1.f;
+        float* plane = p.mass + (size_t)(sg.index * p.hkv + g) * p.mass_cap;
+        const uint32_t td = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + grp * 256;
+        for (int i = 0; i < nt; ++i) {
+          const uint32_t st = cnt + i;
+          // tiles that are multiplied go to the group whose D buffer they
+          // take; the others only decay
+          if ((int)(st & 1) != grp) continue;
+          const int key = (kt0 + i) * kTile + 32 * (warp & 3) + lane;
+          bool live = key < sg.seq_len;
+          if (live && sg.page_table) {
+            // a bad page's keys keep their entries
+            const int pid = __ldg(sg.page_table + (key >> 8));
+            if ((unsigned)pid >= (unsigned)p.num_pages) {
+              flag_error(p.err_flag, kErrBadPage);
+              live = false;
+            }
+          }
+          // decay 0 does not read the old entry
+          const float old = live && decay != 0.f ? plane[key] * decay : 0.f;
+          float sum = 0.f;
+          if (i < mt) {
+            if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&b.d_full[grp], (st >> 1) & 1,
+                                                             p.err_flag, b.abort)))
+              break;
+            umma::fence_after_sync();
+            const bool masked = (kt0 + i + 1) * kTile - 1 > minlim;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int c0 = 0; c0 < n; c0 += 16) {
+              uint32_t v[16];
+              umma::tmem_ld16(td + c0, v);
+              umma::tmem_ld_wait();
+              if (masked) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const float2 f = tab[c0 + j];
+                  const float w = fast_exp2(__fmaf_rn(__uint_as_float(v[j]), f.x, f.y));
+                  acc[j & 3] += key <= lims[c0 + j] ? w : 0.f;
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                  const float4 f = *reinterpret_cast<const float4*>(tab + c0 + j);
+                  acc[j & 3] += fast_exp2(__fmaf_rn(__uint_as_float(v[j]), f.x, f.y));
+                  acc[(j + 1) & 3] += fast_exp2(__fmaf_rn(__uint_as_float(v[j + 1]), f.z, f.w));
+                }
+              }
+            }
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.d_empty[grp]);
+            sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          }
+          if (live && (i < mt || decay != 1.f)) plane[key] = old + sum;
+        }
+      } else if (C::kF16 && warp >= kConvWarp0) {
+        const int ct = threadIdx.x - kConvWarp0 * 32;
+        for (int i = 0; i < mt; ++i) {
+          const uint32_t st = cnt + i;
+          const int s = st % C::kStages, o = st & 1;
+          if (!mbar_wait_or_abort(&b.full[s], (st / C::kStages) & 1, p.err_flag, b.abort)) break;
+          if (!mbar_wait_or_abort(&b.op_empty[o], ((st >> 1) & 1) ^ 1, p.err_flag, b.abort)) break;
+          __syncwarp();
+          const uint8_t* src = smem + C::kOffStage + s * C::kStageBytes;
+          uint8_t* dst = smem + C::kOffOp + o * 32768;
+          if (KV == kKvFp4)
+            convert_tile_fp4<32 * kConvWarps>(src, dst, kTile, ct);
+          else
+            convert_tile<32 * kConvWarps>(src, dst, kTile, ct);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&b.empty[s]);
+            mbar_arrive(&b.op_full[o]);
+          }
         }
       }
+      cnt += mt;
     }
+    t += nt;
   }
-  if (wkey >= sg.seq_len) return;
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      float s = acc[t][hr];
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      const int key = wkey + 16 * t + 8 * hr + gq;
-      if (c == 0 && key < sg.seq_len) {
-        float* m = p.mass + (size_t)(sg.index * p.hkv + g) * p.mass_cap + key;
-        // decay 0 does not read the old entry
-        *m = sg.decay == 0.f ? s : __fmaf_rn(*m, sg.decay, s);
-      }
+out:
+  umma::fence_before_sync();
+  __syncthreads();
+  if (*b.abort) {
+    // a wait gave up: let the MMAs and the loads in flight end
+    if (warp == 1 && lane == 0) {
+      umma::commit(b.drain);
+      mbar_wait(b.drain, 0, p.err_flag);
     }
+    if (threadIdx.x == 0) {
+      const uint64_t since = global_timer_ns();
+      while (global_timer_ns() - since < 1000000) {}     // 1 ms: far longer than any copy takes
+    }
+    __syncthreads();
+  }
+  if (warp == 1) {
+    umma::fence_after_sync();
+    umma::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int KV>
+cudaError_t launch(const MassParams& p, int grid, cudaStream_t s) {
+  static PerDeviceOnce configured;
+  const cudaError_t e = configured.run([] {
+    return cudaFuncSetAttribute(key_mass_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                MassCfg<KV>::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(key_mass_kernel<KV>, dim3(grid), dim3(MassCfg<KV>::kThreads),
+                    MassCfg<KV>::kSmem, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_key_mass(const MassParams& p, int kv, int grid, cudaStream_t s) {
   if (grid <= 0) return cudaSuccess;
-  const dim3 b(32 * kWarps);
   switch (kv) {
-    case kKvBf16: return launch_pdl(key_mass_kernel<kKvBf16>, dim3(grid), b, 0, s, p);
-    case kKvFp8: return launch_pdl(key_mass_kernel<kKvFp8>, dim3(grid), b, 0, s, p);
-    default: return launch_pdl(key_mass_kernel<kKvFp4>, dim3(grid), b, 0, s, p);
+    case kKvBf16: return launch<kKvBf16>(p, grid, s);
+    case kKvFp8: return launch<kKvFp8>(p, grid, s);
+    default: return launch<kKvFp4>(p, grid, s);
   }
 }
 

@@ -259,10 +259,10 @@ struct MassSeg {
   int32_t index;              // the segment's index in the call (its planes of mass)
   int32_t seq_len;
   int32_t slab_cap;
-  int32_t item0;              // first block of the segment
+  int32_t item0;              // first key tile of the segment
   int32_t run0, nruns;
   float decay;                // 1 when an earlier launch of the call has applied it
-  int32_t pad_;
+  int32_t src;                // index into maps[]
 };
 struct MassRun {
   int32_t row0;               // row of the call
@@ -270,6 +270,7 @@ struct MassRun {
   int32_t pos0;
 };
 struct MassParams {
+  CUtensorMap maps[kMaxSources];   // K of each source (bf16, e4m3)
   MassSeg segs[kMaxRuns];
   MassRun runs[kMaxRuns];
   const __nv_bfloat16* q;     // [rows][hq][128]
@@ -278,6 +279,7 @@ struct MassParams {
   const float* k_scale;
   int32_t* err_flag;
   int32_t nsegs;
+  int32_t tiles;              // key tiles: hkv * ceil(seq_len / 128) of every segment
   int32_t hq, hkv, group;
   int32_t num_pages;
   int32_t mass_cap;
