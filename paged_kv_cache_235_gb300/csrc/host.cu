@@ -1420,6 +1420,14 @@ int mass_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const voi
     p.mass_cap = mass_cap;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.tiles = (int32_t)items;
+    p.dbufs = 4;
+    for (int i = 0; i < p.nsegs; ++i) {
+      int64_t vecs = 0;
+      for (int r = 0; r < p.segs[i].nruns; ++r)
+        vecs += (int64_t)p.runs[p.segs[i].run0 + r].nrows * (c->hq / c->hkv);
+      if (vecs > INT32_MAX) return TFPA_EINVAL;
+      if (vecs > 128) p.dbufs = 2;
+    }
     if (kv != kKvFp4) {
       const bool fp8 = kv == kKvFp8;
       const int inner = fp8 ? 128 : 64;

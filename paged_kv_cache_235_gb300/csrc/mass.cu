@@ -16,11 +16,17 @@
 // passes over the same keys).
 //   warp 0       producer: key tiles into a ring, by TMA (bf16: the operand
 //                itself; e4m3: staging) or bulk copies (4 bits: staging)
-//   warp 1       TMEM owner and MMA issuer, two D buffers
+//   warp 1       TMEM owner and MMA issuer, two or four D buffers
 //   warps 4-11   epilogue: two groups of four, tiles in turn
-//   warps 12-19  (e4m3, 4 bits) converters: staged tiles -> f16 operand tiles
-// e4m3 and 4-bit keys are exact in f16; their query vectors are scaled into
-// f16 range by a power of two each.
+//   warps 12-19  (e4m3, 4 bits) converters: staged tiles -> f16 operand tiles,
+//                two groups of four, tiles in turn
+// e4m3 and 4-bit keys are exact in f16; a pass's query vectors are scaled into
+// f16 range by one power of two (exact for every element within 2^30 of the
+// pass's largest), so that all of its scores have one factor and a column's
+// only constant is its -lse.  Those constants come from shared memory, and a
+// read that gives all lanes one value costs as much of its bandwidth as one
+// that gives each its own: the epilogue takes two key tiles at a time, each
+// constant read once for both.
 #include <climits>
 
 #include "common.cuh"
@@ -47,21 +53,22 @@ struct MassCfg {
   static constexpr int kOffOp = 65536;
   static constexpr int kOffStage = kOffOp + kOps * 32768;
   static constexpr int kOffTab = (kOffStage + kStages * kStageBytes + 1023) & ~1023;
-  static constexpr int kOffLim = kOffTab + kVec * 8;
+  static constexpr int kOffLim = kOffTab + kVec * 4;
   static constexpr int kOffBar = kOffLim + kVec * 4;
-  static constexpr int kBars = 2 * kStages + 2 * 2 + 2 * 2 + 1;
-  static constexpr int kSmem = kOffBar + kBars * 8 + 32 + 1024;
+  static constexpr int kBars = 2 * kStages + 2 * 2 + 2 * 4 + 1;
+  static constexpr int kSmem = kOffBar + kBars * 8 + 64 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
 struct MassBars {
   uint64_t *full, *empty;        // [kStages]: the ring
   uint64_t *op_full, *op_empty;  // [2]: f16 operand tiles
-  uint64_t *d_full, *d_empty;    // [2]: D buffers
+  uint64_t *d_full, *d_empty;    // [4]: D buffers
   uint64_t* drain;
   uint32_t* tmem_slot;
   volatile int* abort;
-  int* span;                     // [2][2], by pass parity: its rows' least, largest position
+  int* amax;                     // [2], by pass parity: largest |q| of the pass (its bits)
+  int* stop;                     // [2], by pass parity: a wait has given up
 };
 
 // Vector v of segment sg: its run and row.
@@ -75,68 +82,133 @@ __device__ __forceinline__ void find_vector(const MassParams& p, const MassSeg& 
   head = v - k * p.group;
 }
 
-// Query vectors [v0, v0 + nv) as the B operand ([n rows][2 halves of 64],
-// 128B swizzle; rows from nv on zero) with each one's score factor, -lse and
-// position; all threads, 16 a vector.
-template <int KV>
-__device__ void stage_q(const MassParams& p, const MassSeg& sg, int g, int v0, int nv, int n,
-                        uint8_t* smem, int* span) {
-  using C = MassCfg<KV>;
-  const uint32_t qb = smem_u32(smem + C::kOffQ);
-  float2* tab = reinterpret_cast<float2*>(smem + C::kOffTab);
-  int* lims = reinterpret_cast<int*>(smem + C::kOffLim);
-  const int t = threadIdx.x & 15;
-  for (int i = threadIdx.x >> 4; i < n; i += C::kThreads / 16) {
-    uint4 w = make_uint4(0, 0, 0, 0);
-    int lim = -1;
-    float sc = 0.f, neg = -INFINITY;
-    if (i < nv) {
-      int row, head;
-      find_vector(p, sg, v0 + i, row, lim, head);
-      const size_t rh = (size_t)row * p.hq + g * p.group + head;
-      w = __ldg(reinterpret_cast<const uint4*>(p.q + rh * kHeadDim) + t);
-      sc = p.scale_log2;
-      // a row without keys has lse -inf and gives no weight
-      const float lse = __ldg(p.lse + rh);
-      neg = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+// Least and largest position of the rows of vectors [v0, v0 + nv).
+__device__ __forceinline__ void pass_span(const MassParams& p, const MassSeg& sg, int v0, int nv,
+                                          int& lo, int& hi) {
+  lo = INT_MAX;
+  hi = -1;
+  int at = 0;                            // first vector of run r
+  for (int r = sg.run0; r < sg.run0 + sg.nruns; ++r) {
+    const int n = p.runs[r].nrows * p.group;
+    const int a = max(v0, at) - at, z = min(v0 + nv, at + n) - at;
+    if (a < z) {
+      lo = min(lo, p.runs[r].pos0 + a / p.group);
+      hi = max(hi, p.runs[r].pos0 + (z - 1) / p.group);
     }
-    if (C::kF16) {
-      // f16, the vector's largest magnitude brought into [2^13, 2^14):
-      // exact for every element within 2^28 of it
-      uint32_t e[4] = {w.x, w.y, w.z, w.w};
-      float amax = 0.f;
+    at += n;
+  }
+}
+
+// Query vectors [v0, v0 + nv) as the B operand ([n rows][2 halves of 64],
+// 128B swizzle; rows from nv on zero) with each one's -lse and position; all
+// warps but the producer's, 16 threads a vector.  Returns the scores' factor.
+template <int KV>
+__device__ float stage_q(const MassParams& p, const MassSeg& sg, int g, int v0, int nv, int n,
+                         uint8_t* smem, int* amax_s) {
+  using C = MassCfg<KV>;
+  constexpr int kStep = (C::kThreads - 32) / 16;
+  const uint32_t qb = smem_u32(smem + C::kOffQ);
+  float* negs = reinterpret_cast<float*>(smem + C::kOffTab);
+  int* lims = reinterpret_cast<int*>(smem + C::kOffLim);
+  const int t = threadIdx.x & 15, i0 = (threadIdx.x - 32) >> 4;
+  auto load = [&](int i, int& lim, size_t& rh) {
+    int row, head;
+    find_vector(p, sg, v0 + i, row, lim, head);
+    rh = (size_t)row * p.hq + g * p.group + head;
+    return __ldg(reinterpret_cast<const uint4*>(p.q + rh * kHeadDim) + t);
+  };
+  float up = 1.f, sc = p.scale_log2;
+  if (C::kF16) {
+    // the pass's largest magnitude goes to [2^13, 2^14)
+    float amax = 0.f;
+    for (int i = i0; i < nv; i += kStep) {
+      int lim;
+      size_t rh;
+      const uint4 w = load(i, lim, rh);
+      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         amax = fmaxf(amax, fabsf(__uint_as_float(e[j] << 16)));
         amax = fmaxf(amax, fabsf(__uint_as_float(e[j] & 0xFFFF0000u)));
       }
-      const unsigned lanes = 0xFFFFu << (threadIdx.x & 16);
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, o));
-      int ex;
-      frexpf(amax, &ex);
-      ex = max(min(ex, 120), -100);
-      const float up = __int_as_float((127 + 14 - ex) << 23);
+    }
+    __syncwarp();
+    const int most = __reduce_max_sync(0xffffffffu, __float_as_int(amax));   // not negative
+    if ((threadIdx.x & 31) == 0) atomicMax(amax_s, most);
+    __syncwarp();
+    named_bar_sync(2, C::kThreads - 32);
+    int ex;
+    frexpf(__int_as_float(*amax_s), &ex);
+    ex = max(min(ex, 120), -100);
+    up = __int_as_float((127 + 14 - ex) << 23);
+    sc = p.scale_log2 * __int_as_float((127 - 14 + ex) << 23) * __ldg(p.k_scale + g);
+  }
+  for (int i = i0; i < n; i += kStep) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    int lim = -1;
+    float neg = -INFINITY;
+    if (i < nv) {
+      size_t rh;
+      w = load(i, lim, rh);
+      // a row without keys has lse -inf and gives no weight
+      const float lse = __ldg(p.lse + rh);
+      neg = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+    }
+    if (C::kF16) {
+      uint32_t e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         e[j] = pack_f16x2(__uint_as_float(e[j] << 16) * up,
                           __uint_as_float(e[j] & 0xFFFF0000u) * up);
       w = make_uint4(e[0], e[1], e[2], e[3]);
-      sc *= __int_as_float((127 - 14 + ex) << 23) * __ldg(p.k_scale + g);
     }
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
                      swz128(qb + (uint32_t)(t >> 3) * (uint32_t)n * 128u, i, t & 7)),
                  "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
     if (t == 0) {
-      tab[i] = make_float2(sc, neg);
+      negs[i] = neg;
       lims[i] = lim;
-      if (i < nv) {
-        atomicMin(&span[0], lim);
-        atomicMax(&span[1], lim);
-      }
     }
   }
   fence_proxy_async_smem();
+  return sc;
+}
+
+// Adds the weights of columns [0, n) (n a multiple of 16) of one or two D
+// tiles, of the keys key0 and key1.
+template <bool TWO, bool MASKED>
+__device__ __forceinline__ void add_columns(uint32_t d0, uint32_t d1, int n, const float* negs,
+                                            const int* lims, float sc, int key0, int key1,
+                                            float& sum0, float& sum1) {
+  float a[2][4] = {};
+  for (int c0 = 0; c0 < n; c0 += 16) {
+    uint32_t v[2][16];
+    umma::tmem_ld16(d0 + c0, v[0]);
+    if (TWO) umma::tmem_ld16(d1 + c0, v[1]);
+    float4 f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = *reinterpret_cast<const float4*>(negs + c0 + 4 * j);
+    umma::tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float neg = j % 4 == 0 ? f[j / 4].x : j % 4 == 1 ? f[j / 4].y
+                        : j % 4 == 2 ? f[j / 4].z : f[j / 4].w;
+      const int lim = MASKED ? lims[c0 + j] : 0;
+#pragma unroll
+      for (int u = 0; u < (TWO ? 2 : 1); ++u) {
+        const float w = fast_exp2(__fmaf_rn(__uint_as_float(v[u][j]), sc, neg));
+        a[u][j & 3] += !MASKED || (u ? key1 : key0) <= lim ? w : 0.f;
+      }
+    }
+  }
+  sum0 = (a[0][0] + a[0][1]) + (a[0][2] + a[0][3]);
+  if (TWO) sum1 = (a[1][0] + a[1][1]) + (a[1][2] + a[1][3]);
+}
+
+// A wait of the whole warp, which goes on as one.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int32_t* err,
+                                         volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, err, abort));
 }
 
 template <int KV>
@@ -153,20 +225,23 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
   b.op_full = bars + 2 * C::kStages;
   b.op_empty = b.op_full + 2;
   b.d_full = b.op_full + 4;
-  b.d_empty = b.op_full + 6;
-  b.drain = b.op_full + 8;
+  b.d_empty = b.op_full + 8;
+  b.drain = b.op_full + 12;
   b.tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
   b.abort = reinterpret_cast<volatile int*>(b.tmem_slot + 1);
-  b.span = reinterpret_cast<int*>(b.tmem_slot + 2);
+  b.amax = reinterpret_cast<int*>(b.tmem_slot + 2);
+  b.stop = b.amax + 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&b.full[i], 1);
-      mbar_init(&b.empty[i], C::kF16 ? kConvWarps : 1);
+      mbar_init(&b.empty[i], C::kF16 ? kConvWarps / 2 : 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&b.op_full[i], kConvWarps);
+      mbar_init(&b.op_full[i], kConvWarps / 2);
       mbar_init(&b.op_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&b.d_full[i], 1);
       mbar_init(&b.d_empty[i], kEpiWarps / 2);
     }
@@ -184,8 +259,11 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
 
   const int t0 = (int)((int64_t)p.tiles * blockIdx.x / gridDim.x);
   const int t1 = (int)((int64_t)p.tiles * (blockIdx.x + 1) / gridDim.x);
-  const float2* tab = reinterpret_cast<const float2*>(smem + C::kOffTab);
+  const float* negs = reinterpret_cast<const float*>(smem + C::kOffTab);
   const int* lims = reinterpret_cast<const int*>(smem + C::kOffLim);
+  // D buffers: four of 128 columns where the launch's passes are that narrow,
+  // so that the epilogue can take two tiles at a time, else two of 256
+  const int nb = p.dbufs, lnb = nb == 4 ? 2 : 1, dcols = 512 >> lnb;
   uint32_t cnt = 0;                      // tiles multiplied so far (every role's count)
   int si = 0, pass = 0;
   for (int t = t0; t < t1;) {
@@ -200,18 +278,27 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
     for (int v0 = 0; v0 < total; v0 += kVec, ++pass) {
       const int nv = min(kVec, total - v0);
       const int n = (nv + 15) & ~15;     // the MMA's N
-      int* span = b.span + 2 * (pass & 1);   // the other one may still be read
-      if (threadIdx.x == 0) {
-        span[0] = INT_MAX;
-        span[1] = -1;
-      }
-      __syncthreads();                   // every role is done with the pass before
-      if (*b.abort) goto out;
-      stage_q<KV>(p, sg, g, v0, nv, n, smem, span);
-      __syncthreads();
-      const int minlim = span[0], maxlim = span[1];
+      int minlim, maxlim;
+      pass_span(p, sg, v0, nv, minlim, maxlim);
       // tiles past the last row's position get no weight
       const int mt = max(0, min(nt, maxlim / kTile + 1 - kt0));
+      // the producer runs ahead of the passes; the others stage each one's
+      // vectors once all of them are done with the last
+      float sc = 0.f;
+      if (warp != 0) {
+        // one thread's look at the flag decides for all (the other parity's
+        // words may still be read)
+        if (threadIdx.x == 32) {
+          b.amax[pass & 1] = 0;
+          b.stop[pass & 1] = *b.abort;
+        }
+        __syncwarp();
+        named_bar_sync(2, C::kThreads - 32);
+        if (b.stop[pass & 1]) goto out;
+        sc = stage_q<KV>(p, sg, g, v0, nv, n, smem, b.amax + (pass & 1));
+        __syncwarp();
+        named_bar_sync(2, C::kThreads - 32);
+      }
       if (warp == 0) {
         if (lane == 0) {
           int page_at = -1, pid = 0;
@@ -235,7 +322,7 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
             const uint32_t st = cnt + i;
             const int s = st % C::kStages;
             if (!mbar_wait_or_abort(&b.empty[s], ((st / C::kStages) & 1) ^ 1, p.err_flag, b.abort))
-              break;
+              goto out;
             uint8_t* dst = smem + C::kOffStage + s * C::kStageBytes;
             mbar_arrive_expect_tx(&b.full[s], C::kStageBytes);
             if (KV == kKvBf16) {
@@ -259,10 +346,10 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
           const int s = C::kF16 ? st & 1 : st % C::kStages;
           uint64_t* ready = C::kF16 ? &b.op_full[s] : &b.full[s];
           const uint32_t ph = C::kF16 ? (st >> 1) & 1 : (st / C::kStages) & 1;
-          const int d = st & 1;
-          if (!mbar_wait_or_abort(ready, ph, p.err_flag, b.abort)) break;
-          if (!mbar_wait_or_abort(&b.d_empty[d], ((st >> 1) & 1) ^ 1, p.err_flag, b.abort)) break;
-          __syncwarp();
+          const int d = st & (nb - 1);
+          if (!wait_all(ready, ph, p.err_flag, b.abort) ||
+              !wait_all(&b.d_empty[d], ((st >> lnb) & 1) ^ 1, p.err_flag, b.abort))
+            break;
           umma::fence_after_sync();
           if (lane == 0) {
             const uint32_t kb =
@@ -273,7 +360,7 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
                   umma::smem_desc_sw128(kb + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024);
               const uint64_t bd = umma::smem_desc_sw128(
                   qb + (ks >> 2) * (uint32_t)n * 128u + (ks & 3) * 32, 16, 1024);
-              umma::mma_ss(tmem + d * 256, ad, bd, idesc, ks > 0 ? 1u : 0u);
+              umma::mma_ss(tmem + d * dcols, ad, bd, idesc, ks > 0 ? 1u : 0u);
             }
             umma::commit(C::kF16 ? &b.op_empty[s] : &b.empty[s]);
             umma::commit(&b.d_full[d]);
@@ -284,73 +371,82 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
         const int grp = (warp - kEpiWarp0) >> 2;
         const float decay = v0 == 0 ? sg.decay : 1.f;
         float* plane = p.mass + (size_t)(sg.index * p.hkv + g) * p.mass_cap;
-        const uint32_t td = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + grp * 256;
-        for (int i = 0; i < nt; ++i) {
-          const uint32_t st = cnt + i;
-          // tiles that are multiplied go to the group whose D buffer they
-          // take; the others only decay
-          if ((int)(st & 1) != grp) continue;
-          const int key = (kt0 + i) * kTile + 32 * (warp & 3) + lane;
-          bool live = key < sg.seq_len;
+        const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const int lane_key = 32 * (warp & 3) + lane;
+        // A tile's entry of this lane: its old value, decayed (decay 0 does
+        // not read it); whether it is written (a bad page's are not).
+        auto entry = [&](int i, bool& live) {
+          const int key = (kt0 + i) * kTile + lane_key;
+          live = key < sg.seq_len;
           if (live && sg.page_table) {
-            // a bad page's keys keep their entries
             const int pid = __ldg(sg.page_table + (key >> 8));
             if ((unsigned)pid >= (unsigned)p.num_pages) {
               flag_error(p.err_flag, kErrBadPage);
               live = false;
             }
           }
-          // decay 0 does not read the old entry
-          const float old = live && decay != 0.f ? plane[key] * decay : 0.f;
-          float sum = 0.f;
-          if (i < mt) {
-            if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&b.d_full[grp], (st >> 1) & 1,
-                                                             p.err_flag, b.abort)))
-              break;
-            umma::fence_after_sync();
-            const bool masked = (kt0 + i + 1) * kTile - 1 > minlim;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int c0 = 0; c0 < n; c0 += 16) {
-              uint32_t v[16];
-              umma::tmem_ld16(td + c0, v);
-              umma::tmem_ld_wait();
-              if (masked) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const float2 f = tab[c0 + j];
-                  const float w = fast_exp2(__fmaf_rn(__uint_as_float(v[j]), f.x, f.y));
-                  acc[j & 3] += key <= lims[c0 + j] ? w : 0.f;
-                }
-              } else {
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                  const float4 f = *reinterpret_cast<const float4*>(tab + c0 + j);
-                  acc[j & 3] += fast_exp2(__fmaf_rn(__uint_as_float(v[j]), f.x, f.y));
-                  acc[(j + 1) & 3] += fast_exp2(__fmaf_rn(__uint_as_float(v[j + 1]), f.z, f.w));
-                }
-              }
-            }
-            umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&b.d_empty[grp]);
-            sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          return live && decay != 0.f ? plane[key] * decay : 0.f;
+        };
+        // Tiles that are multiplied: D buffers 0, 1 go to one group and 2, 3
+        // to the other, two tiles at a time (two buffers: one each).
+        for (int i = 0; i < mt;) {
+          const uint32_t st = cnt + i;
+          const bool two = nb == 4 && !(st & 1) && i + 1 < mt;
+          if ((int)((nb == 4 ? st >> 1 : st) & 1) != grp) {
+            i += two ? 2 : 1;
+            continue;
           }
-          if (live && (i < mt || decay != 1.f)) plane[key] = old + sum;
+          bool live0, live1 = false;
+          const float old0 = entry(i, live0), old1 = two ? entry(i + 1, live1) : 0.f;
+          const int d = st & (nb - 1);
+          const int key = (kt0 + i) * kTile + lane_key;
+          if (!wait_all(&b.d_full[d], (st >> lnb) & 1, p.err_flag, b.abort)) break;
+          if (two && !wait_all(&b.d_full[d + 1], (st >> lnb) & 1, p.err_flag, b.abort)) break;
+          umma::fence_after_sync();
+          float s0 = 0.f, s1 = 0.f;
+          const uint32_t td = tq + d * dcols;
+          const bool masked = (kt0 + i + (two ? 2 : 1)) * kTile - 1 > minlim;
+          if (two && masked)
+            add_columns<true, true>(td, td + dcols, n, negs, lims, sc, key, key + kTile, s0, s1);
+          else if (two)
+            add_columns<true, false>(td, td + dcols, n, negs, lims, sc, key, key + kTile, s0, s1);
+          else if (masked)
+            add_columns<false, true>(td, td, n, negs, lims, sc, key, key, s0, s1);
+          else
+            add_columns<false, false>(td, td, n, negs, lims, sc, key, key, s0, s1);
+          umma::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&b.d_empty[d]);
+            if (two) mbar_arrive(&b.d_empty[d + 1]);
+          }
+          if (live0) plane[key] = old0 + s0;
+          if (live1) plane[key + kTile] = old1 + s1;
+          i += two ? 2 : 1;
+        }
+        // the others only decay
+        for (int i = mt; decay != 1.f && i < nt; ++i) {
+          if ((i & 1) != grp) continue;
+          bool live;
+          const float old = entry(i, live);
+          if (live) plane[(kt0 + i) * kTile + lane_key] = old;
         }
       } else if (C::kF16 && warp >= kConvWarp0) {
-        const int ct = threadIdx.x - kConvWarp0 * 32;
-        for (int i = 0; i < mt; ++i) {
+        constexpr int kGroup = 16 * kConvWarps;          // threads of a group
+        const int o = (warp - kConvWarp0) / (kConvWarps / 2);   // its tiles' parity and operand
+        const int ct = (threadIdx.x - kConvWarp0 * 32) % kGroup;
+        for (int i = (cnt & 1) ^ o; i < mt; i += 2) {
           const uint32_t st = cnt + i;
-          const int s = st % C::kStages, o = st & 1;
-          if (!mbar_wait_or_abort(&b.full[s], (st / C::kStages) & 1, p.err_flag, b.abort)) break;
-          if (!mbar_wait_or_abort(&b.op_empty[o], ((st >> 1) & 1) ^ 1, p.err_flag, b.abort)) break;
-          __syncwarp();
+          const int s = st % C::kStages;
+          if (!wait_all(&b.full[s], (st / C::kStages) & 1, p.err_flag, b.abort) ||
+              !wait_all(&b.op_empty[o], ((st >> 1) & 1) ^ 1, p.err_flag, b.abort))
+            break;
           const uint8_t* src = smem + C::kOffStage + s * C::kStageBytes;
           uint8_t* dst = smem + C::kOffOp + o * 32768;
           if (KV == kKvFp4)
-            convert_tile_fp4<32 * kConvWarps>(src, dst, kTile, ct);
+            convert_tile_fp4<kGroup>(src, dst, kTile, ct);
           else
-            convert_tile<32 * kConvWarps>(src, dst, kTile, ct);
+            convert_tile<kGroup>(src, dst, kTile, ct);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -364,14 +460,19 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
     t += nt;
   }
 out:
-  umma::fence_before_sync();
-  __syncthreads();
-  if (*b.abort) {
-    // a wait gave up: let the MMAs and the loads in flight end
-    if (warp == 1 && lane == 0) {
+  __syncwarp();
+  if (warp == 1) {
+    // every MMA and every arrival asked of them has happened
+    if (lane == 0) {
       umma::commit(b.drain);
       mbar_wait(b.drain, 0, p.err_flag);
     }
+    __syncwarp();
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  if (*b.abort) {
+    // a wait gave up: let the loads in flight end
     if (threadIdx.x == 0) {
       const uint64_t since = global_timer_ns();
       while (global_timer_ns() - since < 1000000) {}     // 1 ms: far longer than any copy takes

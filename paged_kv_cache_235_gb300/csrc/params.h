@@ -279,6 +279,7 @@ struct MassParams {
   const float* k_scale;
   int32_t* err_flag;
   int32_t nsegs;
+  int32_t dbufs;              // 4 if no segment has more than 128 query vectors, else 2
   int32_t tiles;              // key tiles: hkv * ceil(seq_len / 128) of every segment
   int32_t hq, hkv, group;
   int32_t num_pages;
