@@ -542,7 +542,8 @@ int tfpa_key_mass(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg, c
  *             NULL: seq_len.
  *   sink, recent >= 0, with sink + recent <= keep[s] where keep[s] < seq_len
  *             (TFPA_EINVAL).
- *   mass    : as tfpa_key_mass; mass_cap a multiple of 4.
+ *   mass    : as tfpa_key_mass, 16-byte aligned like key_pos; mass_cap a
+ *             multiple of 4.
  *   moves   : DEVICE int32 [nseg][hkv][mass_cap + 4], 16-byte aligned, written:
  *             [0] the number m of rows moved, and from [4] on m pairs (from
  *             slot, to slot), for whoever keeps more per key than this cache.

@@ -1468,8 +1468,8 @@ extern "C" int tfpa_evict_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t 
   int e;
   if ((e = check_cache(c)) || (e = check_segs(c, segs, nseg))) return e;
   if (sink < 0 || recent < 0 || mass_cap < 4 || mass_cap % 4) return TFPA_EINVAL;
-  if (nseg > 0 && (!keep || !mass || !aligned(mass, 4) || !moves || !aligned(moves, 16) ||
-                   (key_pos && !aligned(key_pos, 4))))
+  if (nseg > 0 && (!keep || !mass || !aligned(mass, 16) || !moves || !aligned(moves, 16) ||
+                   (key_pos && !aligned(key_pos, 16))))
     return TFPA_EINVAL;
   for (int32_t s = 0; s < nseg; ++s) {
     if (keep[s] < 1 || keep[s] > segs[s].seq_len) return TFPA_ERANGE;
@@ -1479,11 +1479,14 @@ extern "C" int tfpa_evict_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t 
   }
   if (nseg == 0) return TFPA_OK;
   if ((e = check_device())) return e;
+  const int nsm = sm_count();
+  if (nsm < 1) return TFPA_ECUDA;
   thread_local EvictParams p;
   for (int32_t s0 = 0; s0 < nseg; s0 += kMaxEvictSegs) {
     std::memset(&p, 0, sizeof(p));
     p.nsegs = std::min<int32_t>(kMaxEvictSegs, nseg - s0);
     int32_t most = 0;                   // pairs of one (segment, kv head), at most
+    int32_t longest = 0;
     for (int32_t i = 0; i < p.nsegs; ++i) {
       const tfpa_seg& g = segs[s0 + i];
       EvictSeg& v = p.segs[i];
@@ -1496,6 +1499,7 @@ extern "C" int tfpa_evict_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t 
       v.next_pos = next_pos ? next_pos[s0 + i] : g.seq_len;
       v.slab_cap = g.slab_cap;
       most = std::max(most, std::min(v.keep, v.seq_len - v.keep));
+      if (v.keep < v.seq_len) longest = std::max(longest, v.seq_len);
     }
     p.mass = mass;
     p.key_pos = key_pos;
@@ -1507,11 +1511,21 @@ extern "C" int tfpa_evict_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t 
     p.sink = sink;
     p.recent = recent;
     const int planes = p.nsegs * c->hkv;
+    // Blocks of one (segment, kv head): more while the GPU holds them (one a
+    // SM) and each has 4,096 slots, a step of its threads.
+    p.cluster = 1;
+    while (p.cluster < 8 && (int64_t)planes * p.cluster * 2 <= nsm &&
+           longest / (p.cluster * 2) >= 4096)
+      p.cluster *= 2;
+    while (p.cluster < 8 && select_chunk(longest, p.cluster) > kSelectKeys) p.cluster *= 2;
+    p.key_slots = std::min(select_chunk(longest, p.cluster), kSelectKeys);
     record(11, s0, p.nsegs, 0, planes, planes, 0, 0);
     if (!dry_run())
       if ((e = to_err(launch_evict_select(p, stream)))) return e;
     if (most == 0) continue;
-    p.grid_x = std::min((most + 7) / 8, 512);
+    // 32 pairs a block and round; several blocks' worth of rounds where there
+    // are many, so that planes of few pairs leave early
+    p.grid_x = std::min((most + 31) / 32, std::max(1, 64 * nsm / planes));
     record(12, s0, p.nsegs, 0, planes, p.grid_x * planes, 0, 0);
     if (!dry_run())
       if ((e = to_err(launch_evict_move(p, c->dtype, stream)))) return e;

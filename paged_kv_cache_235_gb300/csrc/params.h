@@ -289,6 +289,11 @@ struct MassParams {
 
 // Eviction.
 constexpr int kMaxEvictSegs = 64;
+constexpr int32_t kSelectKeys = 49152;   // order keys that a select block's shared memory holds
+// Slots of one of `blocks` select blocks (whole runs of 128).
+__host__ __device__ inline int32_t select_chunk(int32_t seq_len, int32_t blocks) {
+  return (int32_t)((((int64_t)seq_len + blocks - 1) / blocks + 127) & ~(int64_t)127);
+}
 struct EvictSeg {
   const int32_t* page_table;  // nullptr => slab
   void* k_base;               // pool or slab
@@ -312,6 +317,8 @@ struct EvictParams {
   int32_t mass_cap;
   int32_t sink, recent;
   int32_t grid_x;             // move blocks of one (segment, kv head)
+  int32_t cluster;            // select blocks of one (segment, kv head)
+  int32_t key_slots;          // keys that one of them can keep in shared memory
 };
 
 // Launchers (defined next to their kernels).
