@@ -238,18 +238,16 @@ int build_runs(const tfpa_seg* segs, int32_t nseg, const int32_t* row_seg,
                const int32_t* row_pos, int32_t rows, std::vector<Run>& out) {
   out.clear();
   if (rows < 0 || (rows > 0 && (!row_seg || !row_pos))) return TFPA_EINVAL;
-  for (int32_t r = 0; r < rows; ++r) {
+  for (int32_t r = 0; r < rows;) {
     const int32_t s = row_seg[r], p = row_pos[r];
     if (s < 0 || s >= nseg) return TFPA_ERANGE;
     if (p < 0 || p >= segs[s].seq_len) return TFPA_ERANGE;
-    if (!out.empty()) {
-      Run& b = out.back();
-      if (b.seg == s && b.pos0 + b.nrows == p) {
-        ++b.nrows;
-        continue;
-      }
-    }
-    out.push_back(Run{s, r, 1, p});
+    // the rows that go on from this one, within the segment
+    const int32_t most = std::min(rows - r, segs[s].seq_len - p);
+    int32_t n = 1;
+    while (n < most && row_seg[r + n] == s && row_pos[r + n] == p + n) ++n;
+    out.push_back(Run{s, r, n, p});
+    r += n;
   }
   return TFPA_OK;
 }
