@@ -592,7 +592,7 @@ def tfpa_evict_kv(cache: Cache, segs: Sequence[Seg], keep, mass, moves, key_pos=
     cap = int(mass.shape[2])
     for t, want in ((mass, (n, cache.hkv, cap)), (key_pos, (n, cache.hkv, cap)),
                     (moves, (n, cache.hkv, cap + 4))):
-        if t is not None and (tuple(t.shape) != want or not t.is_contiguous()):
+        if t is not None and (t.shape != want or not t.is_contiguous()):
             raise ValueError(f"expected a contiguous {list(want)} tensor")
     if len(kp) != n or (nx is not None and len(nx) != n):
         raise ValueError("keep and next_pos hold one value per segment")

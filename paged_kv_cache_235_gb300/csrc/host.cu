@@ -245,6 +245,12 @@ int build_runs(const tfpa_seg* segs, int32_t nseg, const int32_t* row_seg,
     // the rows that go on from this one, within the segment
     const int32_t most = std::min(rows - r, segs[s].seq_len - p);
     int32_t n = 1;
+    for (; n + 16 <= most; n += 16) {     // blocks without an exit, which the compiler vectorises
+      int32_t differ = 0;
+      for (int32_t i = 0; i < 16; ++i)
+        differ |= (row_seg[r + n + i] ^ s) | (row_pos[r + n + i] ^ (p + n + i));
+      if (differ) break;
+    }
     while (n < most && row_seg[r + n] == s && row_pos[r + n] == p + n) ++n;
     out.push_back(Run{s, r, n, p});
     r += n;
@@ -918,12 +924,12 @@ int write_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const vo
     if (!rope.sin || rope.n < 1 || !aligned(rope.cos, 16) || !aligned(rope.sin, 16) ||
         (rope.pos && !aligned(rope.pos, 4)))
       return TFPA_EINVAL;
-    if (!rope.pos)
-      for (int32_t r = 0; r < rows; ++r)
-        if (row_pos && row_pos[r] >= rope.n) return TFPA_ERANGE;
   }
   thread_local std::vector<Run> runs;   // reused by every call of this thread
   if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;
+  if (rope.cos && !rope.pos)
+    for (const Run& r : runs)
+      if (r.pos0 + r.nrows > rope.n) return TFPA_ERANGE;
   if (rows == 0) return TFPA_OK;
   if ((e = check_device())) return e;
   const size_t rd = (size_t)c->hkv * kHeadDim;

@@ -44,7 +44,25 @@ __device__ __forceinline__ uint32_t quant8_fp4(float (&x)[8], float g, unsigned 
   scale = s;
   const float step = __fmul_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw(s, __NV_E4M3))), g);
   if (!(step > 0.f)) return 0u;
-  uint32_t out = 0;
+  // A code only depends on which side of seven borders the quotient falls.
+  // x times the reciprocal is off by at most 2^-22 of it (two roundings, a
+  // subnormal reciprocal aside), so where that much more and that much less
+  // give the same codes, the quotient does too; else (a border that near:
+  // about one block of 10^5) the quotients are formed.
+  const float r = __frcp_rn(step);
+  uint32_t out = 0, other = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = __fmul_rn(x[2 * i], r), b = __fmul_rn(x[2 * i + 1], r);
+    constexpr float kMore = 1.f + 0x1p-21f, kLess = 1.f - 0x1p-21f;
+    out |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(__fmul_rn(a, kLess), __fmul_rn(b, kLess)),
+                                              __NV_E2M1, cudaRoundNearest) << (8 * i);
+    other |= (uint32_t)__nv_cvt_float2_to_fp4x2(
+                 make_float2(__fmul_rn(a, kMore), __fmul_rn(b, kMore)), __NV_E2M1,
+                 cudaRoundNearest) << (8 * i);
+  }
+  if (out == other && step >= 0x1p-100f && step <= 0x1p100f) return out;
+  out = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = make_float2(__fdiv_rn(x[2 * i], step), __fdiv_rn(x[2 * i + 1], step));

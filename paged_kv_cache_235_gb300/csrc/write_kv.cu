@@ -64,9 +64,23 @@ __global__ void __launch_bounds__(256) write_kv_kernel(const __grid_constant__ W
   const WriteRun& run = D.runs[ri];
   const int pos = run.pos0 + (row - run.row0);
 
+  // Everything the row is made of is on its way before the first use, the
+  // destination's page id among it.
+  const int pid = run.page_table ? __ldg(run.page_table + (pos >> 8)) : 0;
+  const size_t src_row = ((size_t)row * p.hkv + g) * kHeadDim;
+  const size_t src = src_row + t * 8;
+  const uint4 kv = *reinterpret_cast<const uint4*>(p.k_rows + src);
+  const uint4 vv = *reinterpret_cast<const uint4*>(p.v_rows + src);
+  const bool second = t >= 8;                // elements 64.. of the head
+  const int i0 = (t & 7) * 8;                // index within the half
+  uint4 ov = make_uint4(0, 0, 0, 0);         // the rotation's partners
+  int rpos = pos;
+  if (p.rope_cos) {
+    ov = *reinterpret_cast<const uint4*>(p.k_rows + src_row + (second ? i0 : 64 + i0));
+    if (p.rope_pos) rpos = __ldg(p.rope_pos + row);
+  }
   size_t dst_row;  // element index of the destination row
   if (run.page_table) {
-    const int pid = __ldg(run.page_table + (pos >> 8));
     if ((unsigned)pid >= (unsigned)p.num_pages) {
       if (t == 0) flag_error(p.err_flag, kErrBadPage);
       return;
@@ -75,24 +89,16 @@ __global__ void __launch_bounds__(256) write_kv_kernel(const __grid_constant__ W
   } else {
     dst_row = (size_t)g * run.slab_cap + pos;
   }
-  const size_t src_row = ((size_t)row * p.hkv + g) * kHeadDim;
-  const size_t src = src_row + t * 8;
-  const uint4 kv = *reinterpret_cast<const uint4*>(p.k_rows + src);
-  const uint4 vv = *reinterpret_cast<const uint4*>(p.v_rows + src);
 
   float kf[8];
   unpack8(kv, kf);
   if (p.rope_cos) {
-    const int rpos = p.rope_pos ? __ldg(p.rope_pos + row) : pos;
     if ((unsigned)rpos >= (unsigned)p.rope_n) {
       if (t == 0) flag_error(p.err_flag, kErrRopeRange);
       return;
     }
-    const bool second = t >= 8;                // elements 64.. of the head
-    const int i0 = (t & 7) * 8;                // index within the half
     float other[8];
-    unpack8(*reinterpret_cast<const uint4*>(p.k_rows + src_row + (second ? i0 : 64 + i0)),
-            other);
+    unpack8(ov, other);
     const float4* cp = reinterpret_cast<const float4*>(p.rope_cos + (size_t)rpos * 64 + i0);
     const float4* sp = reinterpret_cast<const float4*>(p.rope_sin + (size_t)rpos * 64 + i0);
     const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
