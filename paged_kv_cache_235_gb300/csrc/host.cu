@@ -261,9 +261,12 @@ int build_runs(const tfpa_seg* segs, int32_t nseg, const int32_t* row_seg,
 // Runs of four or more m-tiles (16 query vectors each, so at least 49
 // vectors per kv head) are dense enough for the tensor cores: they take the
 // prefill kernel in verify mode, when a tile holds the group's heads.
-// A 4-bit cache's runs all take the decode partial kernel.
+// Over a 4-bit cache, whose decode kernel spends most of its time on turning
+// codes into operands, already runs of two or more (more than 16 vectors).
+constexpr int kFp4VerifyVectors = 16;
 bool on_verify_path(const Run& r, int G, int kv) {
-  return kv != kKvFp4 && G <= kVerifyVectors && (r.nrows * G + 15) / 16 >= 4;
+  if (kv == kKvFp4) return G <= kVerifyVectors && r.nrows * G > kFp4VerifyVectors;
+  return G <= kVerifyVectors && (r.nrows * G + 15) / 16 >= 4;
 }
 
 // Stored bytes of one row of one kv head, K or V.
@@ -770,7 +773,10 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
       if ((e = sink.decode(p, wkv, grid))) return e;
     }
     if (nv > 0) {
-      if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 128, pv.maps, pv.nsrc))) return e;
+      if (kv == kKvFp4)
+        pv.nsrc = fill_bases(c, segs, ss, pv.k_base, pv.v_base);
+      else if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 128, pv.maps, pv.nsrc)))
+        return e;
       // The kernel loads a verify tile's Q as two boxes of 64 query vectors
       // when G divides 64 (so that a tile of at most 64 vectors can hold
       // them twice, one copy per MMA slot), else as one box.

@@ -48,6 +48,8 @@
 // bf16: rings of three K and V stages over the slots' common tile order.
 // e4m3: two e4m3 K stages per slot (8-bit S MMAs), two V staging tiles per
 // slot, one f16 V stage per slot.
+// 4 bits: three staged half-blocks each of K and V over the slots' common
+// order, one f16 stage each per slot.
 // TMEM (512 columns): S_A [0,128) O_A [128,256) S_B [256,384) O_B [384,512).
 // CTA 1's partial lands in CTA 0's shared memory once CTA 0's MMAs are done:
 // O (float32 [2 heads][128 rows][128], 16-byte chunks permuted by row against
@@ -89,6 +91,13 @@ __device__ __forceinline__ int vstage8_off(int i) {
   return i < 2 ? kOffK8 + i * 16384 : kOffQ2 + (i - 2) * 16384;
 }
 __device__ __forceinline__ int kstage8_off(int i) { return kOffK + i * 16384; }
+// Verify, 4 bits: K and V both go through the converters, one f16 stage each
+// per slot (the prefill rings), from three staged half-blocks each over the
+// CTA's tiles in the slots' common order (tile n = 2 step + slot in stage n
+// mod 3): K's over the second Q tile, V's over the prefill staging pair.
+__device__ __forceinline__ int stage4_off(bool is_v, int i) {
+  return (is_v ? kOffK8 : kOffQ2) + i * kFp4HalfBytes;
+}
 // Verify, bf16: a ring of three 16-bit stages each for K and V over the
 // CTA's key tiles in the slots' common order (tile n = 2 step + slot in
 // stage n mod 3): K stage 2 is the unused second Q tile, V stage 2 follows
@@ -148,9 +157,9 @@ struct Bars {
   uint64_t* v_full;      // [2] (verify, bf16: [3])
   uint64_t* v_empty;     // [2] (verify, bf16: [3])
   uint64_t* k8_full;     // prefill, e4m3: the staging tile landed / free
-  uint64_t* k8_empty;
-  uint64_t* v8_full;     // (verify, e4m3: [4])
-  uint64_t* v8_empty;    // (verify, e4m3: [4])
+  uint64_t* k8_empty;    // (verify, 4 bits: [3])
+  uint64_t* v8_full;     // (verify, e4m3: [4], 4 bits: [3])
+  uint64_t* v8_empty;    // (verify, e4m3: [4], 4 bits: [3])
   uint64_t* s_full;      // [2] per head: S in TMEM
   uint64_t* p_ready;     // [2] per head: P in TMEM, O corrected
   uint64_t* o_final;
@@ -376,7 +385,31 @@ __device__ void producer(const PrefillParams& p, const RunInfo& ru, const Tile& 
                   : (stage == 2 ? last_k2 : stage ? last_k1 : last_k0);
     w = (int)ph;
   };
-  if (VERIFY && F16) {
+  if constexpr (VERIFY && KV == kKvFp4) {
+    // Step jj, slot hh: tile n = 2 jj + hh into staging n mod 3 at phase (n /
+    // 3) & 1; K of both slots, then V of both.  last_k0, last_v0: tiles
+    // loaded.
+    bool ok = true;
+    last_k0 = last_v0 = 0;
+    for (int jj = 0; ok && jj < slot_tiles<true>(gm, 0); ++jj) {
+      for (int kv = 0; ok && kv < 2; ++kv)
+        for (int hh = 0; ok && hh < 2; ++hh) {
+          if (jj >= slot_tiles<true>(gm, hh)) continue;
+          const int n = 2 * jj + hh, i = n % 3;
+          uint64_t* empty = kv ? b.v8_empty + i : b.k8_empty + i;
+          uint64_t* full = kv ? b.v8_full + i : b.k8_full + i;
+          const int y = row_of(slot_tile<true>(gm, jj, hh));
+          if (!(ok = mbar_wait_or_abort(empty, (uint32_t)((n / 3) & 1) ^ 1, p.err_flag, b.abort)))
+            break;
+          mbar_arrive_expect_tx(full, kFp4HalfBytes);
+          bulk_load(smem + stage4_off(kv == 1, i),
+                    static_cast<const uint8_t*>(kv ? p.v_base[ru.src] : p.k_base[ru.src]) +
+                        (size_t)(y / kHalfRows) * kFp4HalfBytes,
+                    kFp4HalfBytes, full);
+          ++(kv ? last_v0 : last_k0);
+        }
+    }
+  } else if (VERIFY && F16) {
     // Step jj, slot hh: K into e4m3 stage 2 hh + (jj & 1), V into staging
     // tile 2 hh + (jj & 1), each at phase (jj >> 1) & 1; K of both slots,
     // then V of both.  last_k*, last_v*: each slot's last step loaded.
@@ -428,7 +461,14 @@ __device__ void producer(const PrefillParams& p, const RunInfo& ru, const Tile& 
   if (*b.abort) {
     // Let this CTA's loads in flight land before it exits.
     mbar_wait(b.q_full, 0, p.err_flag);
-    if (VERIFY && F16) {
+    if constexpr (VERIFY && KV == kKvFp4) {
+      // the last three tiles loaded, in their order, are n - 1, n - 2, n - 3
+      for (int u = 0; u < 2; ++u) {
+        const int loaded = u ? last_v0 : last_k0;
+        for (int n = max(0, loaded - 3); n < loaded; ++n)
+          mbar_wait((u ? b.v8_full : b.k8_full) + n % 3, (uint32_t)((n / 3) & 1), p.err_flag);
+      }
+    } else if (VERIFY && F16) {
       // each slot's last two steps loaded (buffers alternate by step)
       const int lasts[4] = {last_k0, last_k1, last_v0, last_v1};
 #pragma unroll
@@ -499,7 +539,26 @@ __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileG
     }
     return true;
   };
-  if (VERIFY) {
+  if constexpr (VERIFY && KV == kKvFp4) {
+    PageCheck pc0(p, ru, gm, gm.kt0, slot_tiles<true>(gm, 0), 2);
+    PageCheck pc1(p, ru, gm, gm.kt0 + 1, slot_tiles<true>(gm, 1), 2);
+    bool ok = true;
+    for (int jj = 0; ok && jj < slot_tiles<true>(gm, 0); ++jj) {
+      for (int kv = 0; ok && kv < 2; ++kv)
+        for (int hh = 0; ok && hh < 2; ++hh) {
+          if (jj >= slot_tiles<true>(gm, hh)) continue;
+          const int n = 2 * jj + hh, i = n % 3;
+          int z0 = kTileKeys;
+          if (kv) {
+            const int j = slot_tile<true>(gm, jj, hh);
+            z0 = v_zero_from(ru, j, hh ? pc1.bad(j) : pc0.bad(j));
+          }
+          ok = convert(kv == 1, hh, jj & 1, z0, stage4_off(kv == 1, i), (uint32_t)((n / 3) & 1),
+                       (kv ? b.v8_full : b.k8_full) + i, (kv ? b.v8_empty : b.k8_empty) + i);
+        }
+    }
+    return;
+  } else if (VERIFY) {
     PageCheck pc0(p, ru, gm, gm.kt0, slot_tiles<true>(gm, 0), 2);
     PageCheck pc1(p, ru, gm, gm.kt0 + 1, slot_tiles<true>(gm, 1), 2);
     bool ok = true;
@@ -542,7 +601,7 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
 
   constexpr uint32_t kIdescQK8 = umma::idesc_e4m3(128, 128);
   auto issue_s = [&](int hh, int s) {     // S_hh = Q_hh K_s^T (verify: one Q tile)
-    if constexpr (VERIFY && F16) {
+    if constexpr (VERIFY && KV == kKvFp8) {
       // S_hh = Q_hi K^T + Q_lo K^T over e4m3 K stage s (K = 32 per MMA)
       const uint32_t k8 = smem_u32(smem + kstage8_off(s));
 #pragma unroll
@@ -558,7 +617,8 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
       for (int ks = 0; ks < 8; ++ks) {
         const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
         const uint64_t a = umma::smem_desc_sw128(qb + (VERIFY ? 0 : hh * 32768) + off, 16, 1024);
-        const uint32_t k16 = VERIFY ? smem_u32(smem + kstage16_off(s)) : kb + s * 32768;
+        const uint32_t k16 =
+            VERIFY && !F16 ? smem_u32(smem + kstage16_off(s)) : kb + s * 32768;
         const uint64_t bd = umma::smem_desc_sw128(k16 + off, 16, 1024);
         umma::mma_ss(tmem + col_s(hh), a, bd, kIdescQK, ks > 0 ? 1u : 0u);
       }
@@ -582,9 +642,12 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
     // Slot hh, step jj.  bf16: K and V of tile n = 2 jj + hh in stage n mod
     // 3 at phase (n / 3) & 1.  e4m3: K in e4m3 stage 2 hh + (jj & 1) at phase
     // (jj >> 1) & 1, V in 16-bit stage hh at phase jj & 1.
-    auto kst = [&](int hh, int jj) { return F16 ? 2 * hh + (jj & 1) : (2 * jj + hh) % 3; };
+    // 4 bits: K and V both in the slot's one 16-bit stage at phase jj & 1.
+    auto kst = [&](int hh, int jj) {
+      return KV == kKvFp4 ? hh : F16 ? 2 * hh + (jj & 1) : (2 * jj + hh) % 3;
+    };
     auto kph = [&](int hh, int jj) {
-      return (uint32_t)(F16 ? (jj >> 1) & 1 : ((2 * jj + hh) / 3) & 1);
+      return (uint32_t)(KV == kKvFp4 ? jj & 1 : F16 ? (jj >> 1) & 1 : ((2 * jj + hh) / 3) & 1);
     };
     auto vst = [&](int hh, int jj) { return F16 ? hh : (2 * jj + hh) % 3; };
     auto vph = [&](int hh, int jj) { return (uint32_t)(F16 ? jj & 1 : ((2 * jj + hh) / 3) & 1); };
@@ -856,14 +919,15 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
   bool ok = true;
   if (F16 && gm.nkt > 0) {
     // Prefill: each slot's warps turn their head's Q rows into f16.  Verify:
-    // slot A's warps turn the one Q tile, publish each row's factor, and
+    // slot A's warps turn the one Q tile (e4m3: into two e4m3 tiles), publish each row's factor, and
     // slot B's take it once they see the tile ready.
     float* down_s = reinterpret_cast<float*>(smem + Layout<F16>::kOffDown);
     if (!VERIFY || hh == 0) {
       ok = mbar_wait_or_abort(b.q_full, 0, p.err_flag, b.abort);
       if (ok) {
-        const float down = VERIFY ? q_row_to_e4m3_pair(smem + kOffQ, r)
-                                  : q_row_to_f16(smem + kOffQ + hh * 32768, r);
+        const float down = VERIFY && KV == kKvFp8
+                               ? q_row_to_e4m3_pair(smem + kOffQ, r)
+                               : q_row_to_f16(smem + kOffQ + (VERIFY ? 0 : hh * 32768), r);
         sl2 = p.scale_log2 * down * __ldg(p.k_scale + x.g);
         if (VERIFY) down_s[r] = down;
         fence_proxy_async_smem();
@@ -1169,16 +1233,19 @@ __global__ void __launch_bounds__(threads_of<KV != kKvBf16>(), 1)
   // and four V staging tiles (24-27 full, 28-31 empty); no K staging.
   // Verify with a bf16 cache: rings of three, K full 24-26 and empty 27-29,
   // V full 2-4 and empty 5-7.
-  constexpr bool kDirectK = VERIFY && F16;
+  // Verify with a 4-bit cache: operand stages as in prefill, three staged
+  // half-blocks each of K (full 10-12, empty 25-27) and V (28-30, 22-24).
+  constexpr bool kDirectK = VERIFY && KV == kKvFp8;
+  constexpr bool kStaged3 = VERIFY && KV == kKvFp4;
   constexpr bool kRing3 = VERIFY && !F16;
   b.k_full = kRing3 ? bars + 24 : bars + 2;
   b.k_empty = kDirectK ? bars + 10 : kRing3 ? bars + 27 : bars + 4;
   b.v_full = kRing3 ? bars + 2 : bars + 6;
   b.v_empty = kRing3 ? bars + 5 : bars + 8;
   b.k8_full = bars + 10;
-  b.k8_empty = bars + 11;
-  b.v8_full = kDirectK ? bars + 24 : bars + 12;
-  b.v8_empty = kDirectK ? bars + 28 : bars + 13;
+  b.k8_empty = kStaged3 ? bars + 25 : bars + 11;
+  b.v8_full = kStaged3 ? bars + 28 : kDirectK ? bars + 24 : bars + 12;
+  b.v8_empty = kStaged3 ? bars + 22 : kDirectK ? bars + 28 : bars + 13;
   b.s_full = bars + 14;
   b.p_ready = bars + 16;
   b.o_final = bars + 18;
@@ -1213,17 +1280,19 @@ __global__ void __launch_bounds__(threads_of<KV != kKvBf16>(), 1)
         mbar_init(&b.k_full[i], stage_arrivals);
         mbar_init(&b.k_empty[i], 1);
       }
-      if (F16) {
-        mbar_init(b.k8_full, 1);
-        mbar_init(b.k8_empty, kConvWarps);
-        mbar_init(b.v8_full, 1);
-        mbar_init(b.v8_empty, kConvWarps);
+      for (int i = 0; F16 && i < (kStaged3 ? 3 : 1); ++i) {
+        mbar_init(b.k8_full + i, 1);
+        mbar_init(b.k8_empty + i, kConvWarps);
+        mbar_init(b.v8_full + i, 1);
+        mbar_init(b.v8_empty + i, kConvWarps);
       }
     }
     mbar_init(b.o_final, 1);
     mbar_init(b.drain, 1);
-    mbar_init(b.peer_ready, 256);                  // every softmax thread of CTA 1
-    mbar_init(b.dst_free, 1);
+    if (!VERIFY) {
+      mbar_init(b.peer_ready, 256);                // every softmax thread of CTA 1
+      mbar_init(b.dst_free, 1);
+    }
     *b.abort = 0;
     fence_mbar_init();
   }
@@ -1308,7 +1377,11 @@ cudaError_t launch_prefill(const PrefillParams& p, int kv, int tiles, cudaStream
 
 cudaError_t launch_verify(const PrefillParams& p, int kv, int tiles, cudaStream_t s) {
   if (tiles <= 0) return cudaSuccess;
-  return kv == kKvFp8 ? launch<kKvFp8, true>(p, tiles, s) : launch<kKvBf16, true>(p, tiles, s);
+  switch (kv) {
+    case kKvBf16: return launch<kKvBf16, true>(p, tiles, s);
+    case kKvFp8: return launch<kKvFp8, true>(p, tiles, s);
+    default: return launch<kKvFp4, true>(p, tiles, s);
+  }
 }
 
 }  // namespace tfpa
