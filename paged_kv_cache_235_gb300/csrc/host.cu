@@ -288,8 +288,8 @@ int no_throw(F&& fn) {
 
 // Runs of more than eight query vectors per kv head over a 4-bit cache take
 // the decode kernel of 16-vector items, the others that of eight (8 streams of
-// 65,536 keys: 16 vectors 178 us in one item, 264 us as two of eight; four
-// vectors WIDE_NARROW).
+// 65,536 keys: 16 vectors 167 us in one item, 264 us as two of eight; four
+// vectors 134 us in an item of eight, 166 us in one of 16).
 bool on_wide_path(const Run& r, int G, int kv) { return kv == kKvFp4 && r.nrows * G > 8; }
 
 int to_err(cudaError_t e) { return e == cudaSuccess ? TFPA_OK : TFPA_ECUDA; }
@@ -423,13 +423,15 @@ namespace {
 // 331 with 9 of 29, 263 / 325 with 7 of 37 and 295 / 348 with 6 of 43.
 // Other batches fill the waves differently.  Never more splits than the
 // decode path's, so a scratch sized for decode holds them.
-int32_t verify_pages_per_split(int32_t seq_len) {
+// Over a 4-bit cache at least 16 pages: 16-node trees of 32,761 keys 218 us
+// with six splits of 24 (384 tiles, 2.53 waves), 183 us with seven of 19.
+int32_t verify_pages_per_split(int32_t seq_len, int kv) {
   const int32_t np = pages_of(std::max(seq_len, 1));
-  return std::max<int32_t>(24, (np + 6) / 7);
+  return std::max<int32_t>(kv == kKvFp4 ? 16 : 24, (np + 6) / 7);
 }
-int32_t verify_num_splits(int32_t seq_len) {
+int32_t verify_num_splits(int32_t seq_len, int kv) {
   const int32_t np = pages_of(std::max(seq_len, 1));
-  const int32_t pps = verify_pages_per_split(seq_len);
+  const int32_t pps = verify_pages_per_split(seq_len, kv);
   return (np + pps - 1) / pps;
 }
 
@@ -693,8 +695,8 @@ int decode_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
         if (nv == 0) std::memset(&pv, 0, sizeof(pv));   // only launches that run are built
         RunInfo& info = pv.runs[nv++];
         fill_run(info, g, src, nrows, take, r.pos0 + taken);
-        info.pps = verify_pages_per_split(g.seq_len);
-        info.nsplit = verify_num_splits(g.seq_len);
+        info.pps = verify_pages_per_split(g.seq_len, kv);
+        info.nsplit = verify_num_splits(g.seq_len, kv);
         info.item0 = tiles;
         tiles += c->hkv * ((take + vrows - 1) / vrows) * info.nsplit;
         mp.d.runs[nr] = MergeRun{nrows, take, info.nsplit, 0};
@@ -851,7 +853,7 @@ extern "C" int tfpa_row_splits(const tfpa_cache* cache, const tfpa_seg* segs, in
   for (const Run& r : runs) {
     const int32_t L = segs[r.seg].seq_len;
     const int32_t n = on_verify_path(r, G, cache->dtype)
-                          ? verify_num_splits(L)
+                          ? verify_num_splits(L, cache->dtype)
                           : decode_num_splits(cache->dtype, L, cache->hkv);
     for (int32_t i = 0; i < r.nrows; ++i) nsplit[r.row0 + i] = n;
   }
