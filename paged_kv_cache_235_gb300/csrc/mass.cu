@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
           const uint8_t* src = smem + C::kOffStage + s * C::kStageBytes;
           uint8_t* dst = smem + C::kOffOp + o * 32768;
           if (KV == kKvFp4)
-            convert_tile_fp4<kGroup>(src, dst, kTile, ct);
+            convert_tile_fp4<kGroup, 1>(src, dst, kTile, ct);
           else
             convert_tile<kGroup>(src, dst, kTile, ct);
           fence_proxy_async_smem();

@@ -528,7 +528,7 @@ __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileG
     if (!mbar_wait_or_abort(empty, ph ^ 1, p.err_flag, b.abort)) return false;
     uint8_t* dst = smem + (is_v ? kOffV : kOffK) + s * 32768;
     if (KV == kKvFp4)
-      convert_tile_fp4<kConvWarps * 32>(smem + src, dst, is_v ? z0 : kTileKeys, t);
+      convert_tile_fp4<kConvWarps * 32, 4>(smem + src, dst, is_v ? z0 : kTileKeys, t);
     else
       convert_tile<kConvWarps * 32>(smem + src, dst, is_v ? z0 : kTileKeys, t);
     fence_proxy_async_smem();
@@ -542,20 +542,62 @@ __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileG
   if constexpr (VERIFY && KV == kKvFp4) {
     PageCheck pc0(p, ru, gm, gm.kt0, slot_tiles<true>(gm, 0), 2);
     PageCheck pc1(p, ru, gm, gm.kt0 + 1, slot_tiles<true>(gm, 1), 2);
-    bool ok = true;
-    for (int jj = 0; ok && jj < slot_tiles<true>(gm, 0); ++jj) {
-      for (int kv = 0; ok && kv < 2; ++kv)
-        for (int hh = 0; ok && hh < 2; ++hh) {
-          if (jj >= slot_tiles<true>(gm, hh)) continue;
-          const int n = 2 * jj + hh, i = n % 3;
-          int z0 = kTileKeys;
-          if (kv) {
-            const int j = slot_tile<true>(gm, jj, hh);
-            z0 = v_zero_from(ru, j, hh ? pc1.bad(j) : pc0.bad(j));
-          }
-          ok = convert(kv == 1, hh, jj & 1, z0, stage4_off(kv == 1, i), (uint32_t)((n / 3) & 1),
-                       (kv ? b.v8_full : b.k8_full) + i, (kv ? b.v8_empty : b.k8_empty) + i);
+    // The step's two K tiles, then its two V tiles: both staged tiles are read
+    // (and freed) before the first is written, so that one look at the four
+    // barriers and one read's latency serve both.
+    const int n0 = slot_tiles<true>(gm, 0), n1 = slot_tiles<true>(gm, 1);
+    int i0 = 0, par0 = 0;                // tile 2 jj: its stage and the stage's phase
+    for (int jj = 0; jj < n0; ++jj) {
+      const bool two = jj < n1;
+      const int i1 = i0 == 2 ? 0 : i0 + 1, par1 = i0 == 2 ? par0 ^ 1 : par0;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint64_t* full8 = kv ? b.v8_full : b.k8_full;
+        uint64_t* empty8 = kv ? b.v8_empty : b.k8_empty;
+        uint64_t* full = kv ? b.v_full : b.k_full;
+        uint64_t* empty = kv ? b.v_empty : b.k_empty;
+        int z0[2] = {kTileKeys, kTileKeys};
+        if (kv) {
+          const int j = slot_tile<true>(gm, jj, 0);
+          z0[0] = v_zero_from(ru, j, pc0.bad(j));
+          if (two) z0[1] = v_zero_from(ru, j + 1, pc1.bad(j + 1));
         }
+        const uint32_t ph = (uint32_t)(jj & 1) ^ 1;
+        const bool r0 = mbar_try_wait(full8 + i0, par0), r1 = mbar_try_wait(full8 + i1, par1);
+        const bool r2 = mbar_try_wait(empty, ph), r3 = mbar_try_wait(empty + 1, ph);
+        if (!(r0 && r2 && (!two || (r1 && r3)))) {
+          if (!mbar_wait_or_abort(full8 + i0, par0, p.err_flag, b.abort) ||
+              !mbar_wait_or_abort(empty, ph, p.err_flag, b.abort))
+            return;
+          if (two && (!mbar_wait_or_abort(full8 + i1, par1, p.err_flag, b.abort) ||
+                      !mbar_wait_or_abort(empty + 1, ph, p.err_flag, b.abort)))
+            return;
+        }
+        __syncwarp();
+        uint8_t* dst = smem + (kv ? kOffV : kOffK);
+        Fp4Tile<kConvWarps * 32> a, c;
+        a.read(smem + stage4_off(kv == 1, i0), z0[0], t);
+        if (two) c.read(smem + stage4_off(kv == 1, i1), z0[1], t);
+        a.write(dst, t);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(empty8 + i0);
+          mbar_arrive(full);
+        }
+        if (two) {
+          c.write(dst + 32768, t);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(empty8 + i1);
+            mbar_arrive(full + 1);
+          }
+        }
+      }
+      // two tiles on: stage + 2 mod 3
+      par0 ^= i0 >= 1;
+      i0 = i0 == 0 ? 2 : i0 - 1;
     }
     return;
   } else if (VERIFY) {
