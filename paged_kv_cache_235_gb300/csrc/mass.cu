@@ -111,21 +111,33 @@ __device__ float stage_q(const MassParams& p, const MassSeg& sg, int g, int v0, 
   float* negs = reinterpret_cast<float*>(smem + C::kOffTab);
   int* lims = reinterpret_cast<int*>(smem + C::kOffLim);
   const int t = threadIdx.x & 15, i0 = (threadIdx.x - 32) >> 4;
-  auto load = [&](int i, int& lim, size_t& rh) {
-    int row, head;
-    find_vector(p, sg, v0 + i, row, lim, head);
-    rh = (size_t)row * p.hq + g * p.group + head;
-    return __ldg(reinterpret_cast<const uint4*>(p.q + rh * kHeadDim) + t);
+  // A thread's vectors i0, i0 + kStep, ...: all of a batch's loads at once.
+  constexpr int kMost = (kVec + kStep - 1) / kStep, kBatch = C::kF16 ? kMost : 4;
+  uint4 w[kBatch];
+  int lim[kBatch];
+  float neg[kBatch];
+  auto load_batch = [&](int i) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u, i += kStep) {
+      w[u] = make_uint4(0, 0, 0, 0);
+      lim[u] = -1;
+      neg[u] = INFINITY;
+      if (i >= nv) continue;
+      int row, head;
+      find_vector(p, sg, v0 + i, row, lim[u], head);
+      const size_t rh = (size_t)row * p.hq + g * p.group + head;
+      w[u] = __ldg(reinterpret_cast<const uint4*>(p.q + rh * kHeadDim) + t);
+      neg[u] = __ldg(p.lse + rh);
+    }
   };
   float up = 1.f, sc = p.scale_log2;
   if (C::kF16) {
     // the pass's largest magnitude goes to [2^13, 2^14)
+    load_batch(i0);
     float amax = 0.f;
-    for (int i = i0; i < nv; i += kStep) {
-      int lim;
-      size_t rh;
-      const uint4 w = load(i, lim, rh);
-      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const uint32_t e[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         amax = fmaxf(amax, fabsf(__uint_as_float(e[j] << 16)));
@@ -143,31 +155,27 @@ __device__ float stage_q(const MassParams& p, const MassSeg& sg, int g, int v0, 
     up = __int_as_float((127 + 14 - ex) << 23);
     sc = p.scale_log2 * __int_as_float((127 - 14 + ex) << 23) * __ldg(p.k_scale + g);
   }
-  for (int i = i0; i < n; i += kStep) {
-    uint4 w = make_uint4(0, 0, 0, 0);
-    int lim = -1;
-    float neg = -INFINITY;
-    if (i < nv) {
-      size_t rh;
-      w = load(i, lim, rh);
-      // a row without keys has lse -inf and gives no weight
-      const float lse = __ldg(p.lse + rh);
-      neg = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
-    }
-    if (C::kF16) {
-      uint32_t e[4] = {w.x, w.y, w.z, w.w};
+  for (int ib = i0; ib < n; ib += kBatch * kStep) {
+    if (!C::kF16) load_batch(ib);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        e[j] = pack_f16x2(__uint_as_float(e[j] << 16) * up,
-                          __uint_as_float(e[j] & 0xFFFF0000u) * up);
-      w = make_uint4(e[0], e[1], e[2], e[3]);
-    }
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                     swz128(qb + (uint32_t)(t >> 3) * (uint32_t)n * 128u, i, t & 7)),
-                 "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
-    if (t == 0) {
-      negs[i] = neg;
-      lims[i] = lim;
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = ib + u * kStep;
+      if (i >= n) break;
+      uint32_t e[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      if (C::kF16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          e[j] = pack_f16x2(__uint_as_float(e[j] << 16) * up,
+                            __uint_as_float(e[j] & 0xFFFF0000u) * up);
+      }
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                       swz128(qb + (uint32_t)(t >> 3) * (uint32_t)n * 128u, i, t & 7)),
+                   "r"(e[0]), "r"(e[1]), "r"(e[2]), "r"(e[3]) : "memory");
+      if (t == 0) {
+        // a row without keys has lse -inf and gives no weight
+        negs[i] = i >= nv || neg[u] == -INFINITY ? -INFINITY : -neg[u] * 1.4426950408889634f;
+        lims[i] = lim[u];
+      }
     }
   }
   fence_proxy_async_smem();
@@ -175,11 +183,12 @@ __device__ float stage_q(const MassParams& p, const MassSeg& sg, int g, int v0, 
 }
 
 // Adds the weights of columns [0, n) (n a multiple of 16) of one or two D
-// tiles, of the keys key0 and key1.
+// tiles, of the keys key0 and key1; the D buffers are handed back (empty) as
+// soon as their last columns are in registers.
 template <bool TWO, bool MASKED>
 __device__ __forceinline__ void add_columns(uint32_t d0, uint32_t d1, int n, const float* negs,
                                             const int* lims, float sc, int key0, int key1,
-                                            float& sum0, float& sum1) {
+                                            uint64_t* empty, float& sum0, float& sum1) {
   float a[2][4] = {};
   for (int c0 = 0; c0 < n; c0 += 16) {
     uint32_t v[2][16];
@@ -189,6 +198,14 @@ __device__ __forceinline__ void add_columns(uint32_t d0, uint32_t d1, int n, con
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[j] = *reinterpret_cast<const float4*>(negs + c0 + 4 * j);
     umma::tmem_ld_wait();
+    if (c0 + 16 == n) {
+      umma::fence_before_sync();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) {
+        mbar_arrive(empty);
+        if (TWO) mbar_arrive(empty + 1);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const float neg = j % 4 == 0 ? f[j / 4].x : j % 4 == 1 ? f[j / 4].y
@@ -204,6 +221,12 @@ __device__ __forceinline__ void add_columns(uint32_t d0, uint32_t d1, int n, con
   sum0 = (a[0][0] + a[0][1]) + (a[0][2] + a[0][3]);
   if (TWO) sum1 = (a[1][0] + a[1][1]) + (a[1][2] + a[1][3]);
 }
+
+// Keeps a value in its register (not read again from where it came).
+__device__ __forceinline__ void hold(int& x) { asm volatile("" : "+r"(x)); }
+__device__ __forceinline__ void hold(float& x) { asm volatile("" : "+f"(x)); }
+template <typename T>
+__device__ __forceinline__ void hold(T*& x) { asm volatile("" : "+l"(x)); }
 
 // A wait of the whole warp, which goes on as one.
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int32_t* err,
@@ -302,14 +325,21 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
       if (warp == 0) {
         if (lane == 0) {
           int page_at = -1, pid = 0;
+          const int32_t* table = sg.page_table;
+          const void* base = sg.k_base;
+          int slab_cap = sg.slab_cap, src = sg.src;
+          hold(table);
+          hold(base);
+          hold(slab_cap);
+          hold(src);
           for (int i = 0; i < mt; ++i) {
             const int key0 = (kt0 + i) * kTile;
             int row;
-            if (sg.page_table) {
+            if (table) {
               const int page = key0 >> 8;
               if (page != page_at) {
                 page_at = page;
-                pid = __ldg(sg.page_table + page);
+                pid = __ldg(table + page);
                 if ((unsigned)pid >= (unsigned)p.num_pages) {
                   flag_error(p.err_flag, kErrBadPage);
                   pid = 0;
@@ -317,7 +347,7 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
               }
               row = (pid * p.hkv + g) * kPage + (key0 & (kPage - 1));
             } else {
-              row = g * sg.slab_cap + key0;
+              row = g * slab_cap + key0;
             }
             const uint32_t st = cnt + i;
             const int s = st % C::kStages;
@@ -326,12 +356,12 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
             uint8_t* dst = smem + C::kOffStage + s * C::kStageBytes;
             mbar_arrive_expect_tx(&b.full[s], C::kStageBytes);
             if (KV == kKvBf16) {
-              tma_load_2d(dst, &p.maps[sg.src], 0, row, &b.full[s]);
-              tma_load_2d(dst + 16384, &p.maps[sg.src], 64, row, &b.full[s]);
+              tma_load_2d(dst, &p.maps[src], 0, row, &b.full[s]);
+              tma_load_2d(dst + 16384, &p.maps[src], 64, row, &b.full[s]);
             } else if (KV == kKvFp8) {
-              tma_load_2d(dst, &p.maps[sg.src], 0, row, &b.full[s]);
+              tma_load_2d(dst, &p.maps[src], 0, row, &b.full[s]);
             } else {
-              bulk_load(dst, static_cast<const uint8_t*>(sg.k_base) +
+              bulk_load(dst, static_cast<const uint8_t*>(base) +
                                  (size_t)(row / kHalfRows) * kFp4HalfBytes,
                         kFp4HalfBytes, &b.full[s]);
             }
@@ -369,35 +399,42 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
         }
       } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
         const int grp = (warp - kEpiWarp0) >> 2;
-        const float decay = v0 == 0 ? sg.decay : 1.f;
+        float decay = v0 == 0 ? sg.decay : 1.f;
+        hold(decay);
         float* plane = p.mass + (size_t)(sg.index * p.hkv + g) * p.mass_cap;
+        hold(plane);
         const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const int lane_key = 32 * (warp & 3) + lane;
-        // A tile's entry of this lane: its old value, decayed (decay 0 does
-        // not read it); whether it is written (a bad page's are not).
-        auto entry = [&](int i, bool& live) {
+        // A tile's entry of this lane, loaded before the tile's scores are waited
+        // for (decay 0 reads none), and whether it is written (a bad page's is
+        // not).  What a step needs of the segment is held in registers: an
+        // indexed read of the launch's parameters costs hundreds of cycles.
+        const int32_t* table = sg.page_table;
+        int seq_len = sg.seq_len;
+        hold(table);
+        hold(seq_len);
+        auto old_of = [&](int i) {
           const int key = (kt0 + i) * kTile + lane_key;
-          live = key < sg.seq_len;
-          if (live && sg.page_table) {
-            const int pid = __ldg(sg.page_table + (key >> 8));
-            if ((unsigned)pid >= (unsigned)p.num_pages) {
-              flag_error(p.err_flag, kErrBadPage);
-              live = false;
-            }
+          return decay != 0.f && key < seq_len ? plane[key] : 0.f;
+        };
+        auto live_of = [&](int i) {
+          const int key = (kt0 + i) * kTile + lane_key;
+          if (key >= seq_len) return false;
+          if (table && (unsigned)__ldg(table + (key >> 8)) >= (unsigned)p.num_pages) {
+            flag_error(p.err_flag, kErrBadPage);
+            return false;
           }
-          return live && decay != 0.f ? plane[key] * decay : 0.f;
+          return true;
         };
         // Tiles that are multiplied: D buffers 0, 1 go to one group and 2, 3
         // to the other, two tiles at a time (two buffers: one each).
-        for (int i = 0; i < mt;) {
-          const uint32_t st = cnt + i;
-          const bool two = nb == 4 && !(st & 1) && i + 1 < mt;
-          if ((int)((nb == 4 ? st >> 1 : st) & 1) != grp) {
-            i += two ? 2 : 1;
-            continue;
-          }
-          bool live0, live1 = false;
-          const float old0 = entry(i, live0), old1 = two ? entry(i + 1, live1) : 0.f;
+        const uint32_t end = cnt + mt, width = nb >> 1;
+        for (uint32_t at = (cnt & ~(uint32_t)(nb - 1)) + width * grp; at < end; at += nb) {
+          const uint32_t st = max(at, cnt), stop = min(at + width, end);
+          if (st >= stop) continue;
+          const int i = st - cnt;
+          const bool two = stop - st == 2;
+          const float old0 = old_of(i), old1 = two ? old_of(i + 1) : 0.f;
           const int d = st & (nb - 1);
           const int key = (kt0 + i) * kTile + lane_key;
           if (!wait_all(&b.d_full[d], (st >> lnb) & 1, p.err_flag, b.abort)) break;
@@ -407,29 +444,21 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
           const uint32_t td = tq + d * dcols;
           const bool masked = (kt0 + i + (two ? 2 : 1)) * kTile - 1 > minlim;
           if (two && masked)
-            add_columns<true, true>(td, td + dcols, n, negs, lims, sc, key, key + kTile, s0, s1);
+            add_columns<true, true>(td, td + dcols, n, negs, lims, sc, key, key + kTile, &b.d_empty[d], s0, s1);
           else if (two)
-            add_columns<true, false>(td, td + dcols, n, negs, lims, sc, key, key + kTile, s0, s1);
+            add_columns<true, false>(td, td + dcols, n, negs, lims, sc, key, key + kTile, &b.d_empty[d], s0, s1);
           else if (masked)
-            add_columns<false, true>(td, td, n, negs, lims, sc, key, key, s0, s1);
+            add_columns<false, true>(td, td, n, negs, lims, sc, key, key, &b.d_empty[d], s0, s1);
           else
-            add_columns<false, false>(td, td, n, negs, lims, sc, key, key, s0, s1);
-          umma::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&b.d_empty[d]);
-            if (two) mbar_arrive(&b.d_empty[d + 1]);
-          }
-          if (live0) plane[key] = old0 + s0;
-          if (live1) plane[key + kTile] = old1 + s1;
-          i += two ? 2 : 1;
+            add_columns<false, false>(td, td, n, negs, lims, sc, key, key, &b.d_empty[d], s0, s1);
+          if (live_of(i)) plane[key] = __fmaf_rn(old0, decay, s0);
+          if (two && live_of(i + 1)) plane[key + kTile] = __fmaf_rn(old1, decay, s1);
         }
         // the others only decay
         for (int i = mt; decay != 1.f && i < nt; ++i) {
           if ((i & 1) != grp) continue;
-          bool live;
-          const float old = entry(i, live);
-          if (live) plane[(kt0 + i) * kTile + lane_key] = old;
+          const float old = old_of(i);
+          if (live_of(i)) plane[(kt0 + i) * kTile + lane_key] = old * decay;
         }
       } else if (C::kF16 && warp >= kConvWarp0) {
         constexpr int kGroup = 16 * kConvWarps;          // threads of a group
