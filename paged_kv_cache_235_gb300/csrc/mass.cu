@@ -371,17 +371,17 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
       } else if (warp == 1) {
         const uint32_t idesc = umma::idesc_f16(128, 16, !C::kF16, false) + ((uint32_t)(n - 16) >> 3 << 17);
         const uint32_t qb = smem_u32(smem + C::kOffQ);
-        for (int i = 0; i < mt; ++i) {
-          const uint32_t st = cnt + i;
-          const int s = C::kF16 ? st & 1 : st % C::kStages;
-          uint64_t* ready = C::kF16 ? &b.op_full[s] : &b.full[s];
-          const uint32_t ph = C::kF16 ? (st >> 1) & 1 : (st / C::kStages) & 1;
-          const int d = st & (nb - 1);
-          if (!wait_all(ready, ph, p.err_flag, b.abort) ||
-              !wait_all(&b.d_empty[d], ((st >> lnb) & 1) ^ 1, p.err_flag, b.abort))
-            break;
-          umma::fence_after_sync();
-          if (lane == 0) {
+        if (umma::elect_one()) {
+          for (int i = 0; i < mt; ++i) {
+            const uint32_t st = cnt + i;
+            const int s = C::kF16 ? st & 1 : st % C::kStages;
+            uint64_t* ready = C::kF16 ? &b.op_full[s] : &b.full[s];
+            const uint32_t ph = C::kF16 ? (st >> 1) & 1 : (st / C::kStages) & 1;
+            const int d = st & (nb - 1);
+            if (!mbar_wait_or_abort(ready, ph, p.err_flag, b.abort) ||
+                !mbar_wait_or_abort(&b.d_empty[d], ((st >> lnb) & 1) ^ 1, p.err_flag, b.abort))
+              break;
+            umma::fence_after_sync();
             const uint32_t kb =
                 smem_u32(smem + (C::kF16 ? C::kOffOp + s * 32768 : C::kOffStage + s * 32768));
 #pragma unroll
@@ -395,8 +395,8 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
             umma::commit(C::kF16 ? &b.op_empty[s] : &b.empty[s]);
             umma::commit(&b.d_full[d]);
           }
-          __syncwarp();
         }
+        __syncwarp();
       } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
         const int grp = (warp - kEpiWarp0) >> 2;
         float decay = v0 == 0 ? sg.decay : 1.f;
@@ -492,7 +492,7 @@ out:
   __syncwarp();
   if (warp == 1) {
     // every MMA and every arrival asked of them has happened
-    if (lane == 0) {
+    if (umma::elect_one()) {
       umma::commit(b.drain);
       mbar_wait(b.drain, 0, p.err_flag);
     }

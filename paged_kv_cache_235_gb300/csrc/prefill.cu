@@ -634,7 +634,6 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
                            uint8_t* smem, uint32_t tmem, const Bars& b) {
   constexpr bool F16 = KV != kKvBf16;
   const int lane = threadIdx.x & 31;
-  const bool leader = lane == 0;
   constexpr uint32_t kIdescQK = umma::idesc_f16(128, 128, !F16, false);
   constexpr uint32_t kIdescPV = umma::idesc_f16(128, 128, !F16, true);
   const uint32_t qb = smem_u32(smem + kOffQ);
@@ -676,7 +675,7 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
   };
 
   if (gm.nkt == 0) {                  // no keys in this half: nothing to wait for
-    if (leader) mbar_arrive(b.o_final);
+    if (umma::elect_one()) mbar_arrive(b.o_final);
     __syncwarp();
     return;
   }
@@ -698,7 +697,7 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
       if (slot_tiles<true>(gm, hh) == 0) continue;
       if (!(ok = mbar_wait_or_abort(&b.k_full[kst(hh, 0)], 0, p.err_flag, b.abort))) break;
       umma::fence_after_sync();
-      if (leader) {
+      if (umma::elect_one()) {
         issue_s(hh, kst(hh, 0));
         umma::commit(&b.s_full[hh]);
         umma::commit(&b.k_empty[kst(hh, 0)]);
@@ -721,7 +720,7 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
         }
         if (!(ok = mbar_wait_or_abort(&b.p_ready[hh], jj & 1, p.err_flag, b.abort))) break;
         umma::fence_after_sync();
-        if (leader) {
+        if (umma::elect_one()) {
           issue_pv(hh, vs, jj > 0);
           umma::commit(&b.v_empty[vs]);
         }
@@ -731,7 +730,7 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
           if (!(ok = mbar_wait_or_abort(&b.k_full[ks], kph(hh, jj + 1), p.err_flag, b.abort)))
             break;
           umma::fence_after_sync();
-          if (leader) {
+          if (umma::elect_one()) {
             issue_s(hh, ks);
             umma::commit(&b.s_full[hh]);
             umma::commit(&b.k_empty[ks]);
@@ -740,7 +739,7 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
         }
       }
     }
-    if (leader) {
+    if (umma::elect_one()) {
       if (ok) {
         umma::commit(b.o_final);
       } else {
@@ -755,7 +754,7 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
             mbar_wait_or_abort(&b.k_full[0], 0, p.err_flag, b.abort);
   if (ok) {
     umma::fence_after_sync();
-    if (leader) {
+    if (umma::elect_one()) {
       issue_s(0, 0);
       umma::commit(&b.s_full[0]);
       issue_s(1, 0);
@@ -781,11 +780,11 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
     // head A
     if (!(ok = mbar_wait_or_abort(&b.p_ready[0], jj & 1, p.err_flag, b.abort))) break;
     umma::fence_after_sync();
-    if (leader) issue_pv(0, s, jj > 0);
+    if (umma::elect_one()) issue_pv(0, s, jj > 0);
     if (more) {
       if (!(ok = mbar_wait_or_abort(&b.k_full[s1], ph1, p.err_flag, b.abort))) break;
       umma::fence_after_sync();
-      if (leader) {
+      if (umma::elect_one()) {
         issue_s(0, s1);
         umma::commit(&b.s_full[0]);
       }
@@ -793,7 +792,7 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
     // head B
     if (!(ok = mbar_wait_or_abort(&b.p_ready[1], jj & 1, p.err_flag, b.abort))) break;
     umma::fence_after_sync();
-    if (leader) {
+    if (umma::elect_one()) {
       issue_pv(1, s, jj > 0);
       if (more) {
         issue_s(1, s1);
@@ -804,7 +803,7 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
     }
     __syncwarp();
   }
-  if (leader) {
+  if (umma::elect_one()) {
     if (ok) {
       umma::commit(b.o_final);
     } else {

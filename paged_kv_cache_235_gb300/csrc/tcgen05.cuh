@@ -106,6 +106,18 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
       ::"r"(smem_u32(bar)) : "memory");
 }
 
+// The one thread of a converged warp that issues (the same at every call).
+// Under it the instructions above are issued far faster than under a
+// comparison of lane numbers, where the attention-weight kernel's eight MMAs
+// and two commits took 1,050 cycles a key tile: prompt chunk of 4,096 rows
+// over 32,768 keys 1729 -> 1380 us (bf16), 1751 -> 1453 us (4 bits).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(e));
+  return e != 0;
+}
+
 // ---------------------------------------------------------------- TMEM <-> regs
 // Each thread of the warp reads 32 consecutive 32-bit columns of its lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
