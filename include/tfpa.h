@@ -8,7 +8,9 @@
  * arithmetic, so a stream's output is the same bytes paged or not, batched or
  * alone (PR #1373, "What changes"; Issue #1344, "Conclusion").
  *
- * Layouts (all row-major, element = bf16 or one e4m3 byte):
+ * Layouts (all row-major, element = bf16 or one e4m3 byte; a 4-bit cache holds
+ * blocks of codes and scales in place of [256][128] elements, see
+ * TFPA_FP4_BLOCK):
  *   pool  K, V : [num_pages][hkv][256][128]   key j of kv head g of a paged
  *                stream is pool[PT[j/256]][g][j%256]  (PR #2011, review
  *                "Is paged output the same as windowed output?": base
@@ -46,6 +48,8 @@
  * reads; results are the host's once the stream has passed the call.  A
  * slice with rows for the tensor-core verify path and tfpa_prefill load q
  * by TMA from device memory only: host memory there returns TFPA_EINVAL.
+ * The K/V rows that tfpa_read_kv writes and the q and lse that tfpa_key_mass
+ * reads may be host memory too; mass, key_pos and moves are device memory.
  * Memory that is not page-locked is not supported (and not checked).
  *
  * Threads.  Calls may be made from several host threads at once, on any
@@ -244,7 +248,9 @@ int tfpa_restore_kv(const tfpa_cache* cache, const tfpa_seg* seg, int32_t p0, in
 
 /* Split policy, a function of a stream's own length only (so a stream's
  * partials never depend on its batch): pages_per_split = 1 for npages <= 16,
- * else max(2, ceil(npages / 32)); nsplit = ceil(npages / pages_per_split). */
+ * else max(2, ceil(npages / 32)); nsplit = ceil(npages / pages_per_split).
+ * A 4-bit cache has longer splits, never more of them (tfpa_row_splits gives
+ * each row's): tfpa_num_splits is what a scratch is sized by for every type. */
 int32_t tfpa_pages_per_split(int32_t seq_len);
 int32_t tfpa_num_splits(int32_t seq_len);
 
@@ -254,7 +260,11 @@ int32_t tfpa_num_splits(int32_t seq_len);
  * run of at least 49 query vectors per kv head (ceil(nrows * G / 16) >= 4,
  * G = hq / hkv <= 128) takes the tensor-core verify path, whose splits are
  * at least 24 pages and at most 7 a stream; every other row has
- * tfpa_num_splits(seq_len).  Host only (no GPU work): nsplit is HOST
+ * tfpa_num_splits(seq_len).  Over a 4-bit cache the verify path takes runs
+ * of 17 or more query vectors per kv head, in splits of at least 16 pages;
+ * the other rows' splits are 1 page for npages <= 8, 2 pages for npages <=
+ * 16, else max(4, ceil(npages / 16)) pages, or max(2, ceil(npages / 32)) for
+ * fewer than eight kv heads.  Host only (no GPU work): nsplit is HOST
  * int32[rows].  TFPA_EINVAL / TFPA_ERANGE as tfpa_decode. */
 int tfpa_row_splits(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
                     const int32_t* row_seg, const int32_t* row_pos, int32_t rows,
@@ -264,7 +274,10 @@ int tfpa_row_splits(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
  * "What changes"): row r's K and V for every kv head go to position
  * row_pos[r] of segment row_seg[r], through its page table or slab.  bf16
  * caches copy the bits; fp8 caches store e4m3(RNE, saturating) of
- * float32(x) / scale[g]; fp4 caches: see TFPA_FP4_BLOCK.  row_seg/row_pos are HOST int32[rows]. */
+ * float32(x) / scale[g]; fp4 caches: see TFPA_FP4_BLOCK.  row_seg/row_pos are
+ * HOST int32[rows].  A position of a segment may be named once in a call (two
+ * rows that name one leave a mixture of both, which over a 4-bit cache can be
+ * neither's values). */
 int tfpa_write_kv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
                   const void* k_rows, const void* v_rows,
                   const int32_t* row_seg, const int32_t* row_pos, int32_t rows,
@@ -285,7 +298,8 @@ int tfpa_read_kv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg, vo
  * kernels write pm/pl/po, then attn_merge).  For each row r < rows, head h
  * and split s < nsplit[r]: (m, l, o) at scratch row r, where nsplit[r] is
  * what tfpa_row_splits gives for the same rows (tfpa_num_splits(seq_len),
- * or fewer for rows of a run on the tensor-core verify path).
+ * or fewer for rows of a run on the tensor-core verify path and for a 4-bit
+ * cache).
  * Requires rows <= scratch->cap_rows (TFPA_ECAPACITY otherwise). */
 int tfpa_decode_partial(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
                         const void* q, const int32_t* row_seg, const int32_t* row_pos,
@@ -436,8 +450,8 @@ int tfpa_plan_launch(const tfpa_plan* plan, cudaStream_t stream);
  *   empty plan (after create or clear), else TFPA_EINVAL.  The plan keeps the
  *   pointer; tfpa_plan_clear keeps the mode.  A planning call whose slots do
  *   not fit returns TFPA_ECAPACITY; rows that would take the tensor-core
- *   verify path (a stream with 4 or more 16-vector m-tiles, whose grid
- *   follows the lengths) return TFPA_EINVAL.
+ *   verify path (a run of 49 or more query vectors per kv head, 17 or more
+ *   over a 4-bit cache, whose grid follows the lengths) return TFPA_EINVAL.
  * tfpa_plan_dyn_bytes: bytes of the buffer the planned launches use (about
  *   4 KB per decode launch, 2.6 KB per write, 2 KB per merge).
  * tfpa_plan_dyn_pack(plan, host, bytes): writes those bytes, the data of
@@ -488,7 +502,7 @@ int tfpa_plan_replay(const tfpa_plan* plan, cudaStream_t stream);
  * softmax on tcgen05/TMEM tiles (PR #2011, "hpattn_p256_kernel": page size a
  * constant 256, one page lookup per key tile).  max_rows_per_launch > 0 runs
  * the rows in slices of that many (a slice's result is the same bytes as one
- * launch); 0 = one launch.  bf16 and fp8 caches. */
+ * launch); 0 = one launch.  Every cache type. */
 int tfpa_prefill(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
                  const void* q, const int32_t* row_seg, const int32_t* row_pos,
                  int32_t rows, float softmax_scale, int32_t max_rows_per_launch,
@@ -561,9 +575,9 @@ int tfpa_evict_kv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
 typedef struct {
   int32_t kind;          /* 0 write_kv, 1 decode partial, 2 merge, 3 prefill, 4 keep,
                             5 stage pages, 6 save, 7 restore, 8 verify (decode or tree
-                            rows of runs with 49 or more query vectors per kv head, on
-                            tensor cores; items = tiles), 9 read_kv, 10 key_mass, 11 evict (choice),
-                            12 evict (moves) */
+                            rows of runs with 49 or more query vectors per kv head, 17
+                            over a 4-bit cache, on tensor cores; items = tiles),
+                            9 read_kv, 10 key_mass, 11 evict (choice), 12 evict (moves) */
   int32_t row0;          /* first row of the call this launch covers */
   int32_t rows;          /* rows it covers */
   int32_t runs;          /* row groups (segment, consecutive positions) */

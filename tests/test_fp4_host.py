@@ -65,3 +65,28 @@ def test_slab_capacity_is_in_positions():
     with B.record_launches(), pytest.raises(B.TfpaError) as e:
         CALLS["decode"](_cache(), [bad])
     assert e.value.code == B.TFPA_EINVAL
+
+
+def test_runs_of_each_length_take_their_launches():
+    """One decode call: up to 8 query vectors per kv head, up to 16, and more go to three kernels."""
+    rs = np.repeat([0, 1, 2], [2, 4, 5])
+    rp = np.concatenate([np.arange(998, 1000), np.arange(996, 1000), np.arange(995, 1000)])
+    with B.record_launches() as rec:
+        B.tfpa_decode(_cache(8, 2), [_seg() for _ in range(3)], FAKE, rs, rp, 0.1, B.Scratch(FAKE, FAKE, 64), FAKE, stream=0)
+    kinds = [(r["kind"], r["runs"]) for r in rec]
+    assert kinds[:2] == [("partial", 1)] * 2 and kinds[2:] == [("verify", 1), ("merge", 3)]
+
+
+@pytest.mark.parametrize("rows,ok", [(1, True), (4, True), (5, False), (16, False)])
+def test_device_mode_takes_the_decode_path_only(rows, ok):
+    with B.record_launches():
+        plan = B.Plan()
+        assert B.lib().tfpa_plan_set_device(plan._p, FAKE, 1 << 16) == B.TFPA_OK
+        args = (_cache(8, 2), [_seg()], FAKE, [0] * rows, list(range(1000 - rows, 1000)), 0.1, B.Scratch(FAKE, FAKE, 64), FAKE)
+        if ok:
+            plan.decode(*args)
+            assert len(plan) == 2
+        else:
+            with pytest.raises(B.TfpaError) as e:
+                plan.decode(*args)
+            assert e.value.code == B.TFPA_EINVAL and len(plan) == 0

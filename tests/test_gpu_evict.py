@@ -428,3 +428,75 @@ def test_captured_and_replayed():
     torch.cuda.synchronize()
     assert torch.equal(mass, mass2) and torch.equal(mv[..., 0], mv2[..., 0])
     assert torch.equal(a.k_pool, b.k_pool) and torch.equal(a.v_pool, b.v_pool)
+
+
+# ---------------------------------------------------------------- many streams, long ones, other memory
+def test_mass_of_many_slabs_and_pages():
+    """More slab streams and more runs than a launch holds."""
+    L = [40 + 7 * i for i in range(80)]
+    c = make("fp4", L, [i % 3 == 0 for i in range(80)], 4, 2, seed=81)
+    order = np.random.default_rng(1).permutation(80)
+    check_mass(c, order, [L[s] - 1 for s in order], 0.5, "many")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp4"])
+def test_mass_reads_pinned_host_rows(kv):
+    c = make(kv, [500], [True], seed=82)
+    q, lse = dev_bf16(c.q(3)), torch.randn(3, 8, device="cuda").abs() + 4
+    m = [torch.zeros(1, 2, 512, device="cuda") for _ in range(2)]
+    args = (np.zeros(3, int), np.arange(497, 500), SCALE)
+    B.tfpa_key_mass(c.gcache, c.gsegs, q, lse, *args, m[0])
+    B.tfpa_key_mass(c.gcache, c.gsegs, q.cpu().pin_memory(), lse.cpu().pin_memory(), *args, m[1])
+    torch.cuda.synchronize()
+    assert torch.equal(*m) and (m[0][..., :500] > 0).all()
+
+
+def test_mass_of_rows_without_keys_and_bad_rows():
+    """lse of -inf gives nothing; +inf gives nothing; a NaN reaches only its own heads' keys."""
+    c = make("bf16", [300], [True], 8, 2, seed=83)
+    q, lse = c.q(2), np.full((2, 8), 3.0, np.float32)
+    lse[0, :4], lse[1, 1] = -np.inf, np.inf
+    m = run_mass(c, q, lse, [0, 0], [298, 299], np.zeros((1, 2, 304), np.float32), 1.0)
+    one = lse.copy()
+    one[0, :], one[1, 1] = -np.inf, -np.inf
+    want = run_mass(c, q, one, [0, 0], [298, 299], np.zeros((1, 2, 304), np.float32), 1.0)
+    assert torch.equal(m[0, 0], want[0, 0]) and torch.isfinite(m).all()
+    lse[0, 7] = np.nan
+    m2 = run_mass(c, q, lse, [0, 0], [298, 299], np.zeros((1, 2, 304), np.float32), 1.0)
+    assert torch.equal(m2[0, 0], m[0, 0]) and torch.isnan(m2[0, 1, :299]).all()
+    assert (m2[0, :, 300:] == 0).all()
+
+
+def test_evict_of_many_segments_and_heads():
+    """More segments than a launch holds, and more kv heads than a cluster's CTAs."""
+    L = [3 + 5 * i for i in range(140)]
+    c = F.Fp4Case(L, [i % 2 == 0 for i in range(140)], 12, 12, seed=84).upload()
+    check_evict(c, np.array([max(1, n * 2 // 3) for n in L], np.int32), masses(c, 3), sink=1)
+
+
+@pytest.mark.parametrize("share", [0.1, 0.6])
+def test_evict_of_a_stream_beyond_shared_memory(share):
+    """More keys than a cluster holds: the choice reads the weights again."""
+    L = 420001
+    c = F.Fp4Case([L], [True], 1, 1, seed=85).upload()
+    check_evict(c, np.array([int(L * share)], np.int32), masses(c, 4), recent=100)
+
+
+def test_two_streams_evict_at_once():
+    """Different caches on different streams: each its own answer."""
+    cs = [F.Fp4Case([9000, 700], [True, False], 2, 2, seed=86 + i).upload() for i in range(2)]
+    ms = [masses(c, i) for i, c in enumerate(cs)]
+    keep = np.array([4000, 300], np.int32)
+    dm = [dev(m) for m in ms]
+    mv = [B.make_moves(2, 2, m.shape[2]) for m in ms]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for c, m, w, s in zip(cs, dm, mv, streams):
+        B.tfpa_evict_kv(c.gcache, c.gsegs, keep, m, w, stream=s)
+    torch.cuda.synchronize()
+    for c, m, d in zip(cs, ms, dm):
+        p0 = np.broadcast_to(np.arange(m.shape[2], dtype=np.int32), m.shape)
+        want, _, moves = evict64(c, keep, m, p0, np.array(c.lengths), 0, 0)
+        assert np.array_equal(d.cpu().numpy(), want)
+        move_rows(c, moves)
+        same_cache(c)

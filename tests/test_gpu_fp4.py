@@ -490,3 +490,118 @@ def test_a_stream_served_in_four_bits():
     c.cache.k_pool, c.cache.v_pool = c.k_pool.cpu().numpy(), c.v_pool.cpu().numpy()
     out, lse = torch.cat([o for o, _ in got]), torch.cat([x for _, x in got])
     check(c, q, np.zeros(704, int), np.arange(704), out, lse, "served")
+
+
+# ---------------------------------------------------------------- calls that mix and overlap
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (8, 2), (5, 1), (8, 1)])
+def test_one_call_of_short_and_long_runs(hq, hkv):
+    """Runs for all three kernels in one call: the bytes of each run alone, and the formula."""
+    L, R = [900, 1300, 4500, 700, 333], [1, 2, 30, 4, 9]
+    c = Fp4Case(L, [True, False, True, True, False], hq, hkv, seed=71).fill().upload()
+    rs = np.concatenate([np.full(r, s) for s, r in enumerate(R)])
+    rp = np.concatenate([np.arange(n - r, n) for n, r in zip(L, R)])
+    q = c.q(len(rs))
+    out, lse = decode(c, q, rs, rp)
+    check(c, q, rs, rp, out, lse, f"{hq}/{hkv}")
+    for s in range(len(L)):
+        at = np.flatnonzero(rs == s)
+        o1, l1 = decode(c, q[at], rs[at], rp[at])
+        assert torch.equal(o1, out[at[0]: at[-1] + 1]) and torch.equal(l1, lse[at[0]: at[-1] + 1])
+
+
+def test_halves_of_a_mixed_call():
+    """tfpa_decode_partial and tfpa_merge with each row's own split count: the bytes of tfpa_decode."""
+    L, R = [9000, 2500, 4000], [1, 5, 20]
+    c = Fp4Case(L, [True, True, False], 16, 4, seed=72).fill().upload()
+    rs = np.concatenate([np.full(r, s) for s, r in enumerate(R)])
+    rp = np.concatenate([np.arange(n - r, n) for n, r in zip(L, R)])
+    q = c.q(len(rs))
+    out, lse = decode(c, q, rs, rp)
+    check(c, q, rs, rp, out, lse)
+    sc = B.make_scratch(64, 16, fused_merge=False)
+    ns = B.tfpa_row_splits(c.gcache, c.gsegs, rs, rp)
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+    B.tfpa_decode_partial(c.gcache, c.gsegs, dev_bf16(q), rs, rp, SCALE, sc)
+    B.tfpa_merge(sc, 16, ns, o2, l2)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_long_run_with_a_bad_page():
+    """Verify rows: the keys of a page outside the pool take no part, on either kind of tile."""
+    c = Fp4Case([1500], [True], 8, 2, seed=73).fill().upload()
+    t = c.gsegs[0].page_table.clone()
+    t[2] = -7
+    rs, rp = np.zeros(20, int), np.arange(1480, 1500)
+    q = c.q(20)
+    out, lse = decode(c, q, rs, rp, segs=[B.Seg(1500, page_table=t)])
+    assert int(c.err.item()) == 1
+    c.err.zero_()
+    qd, keep = f64(dev_bf16(q)), np.r_[0:512, 768:1500]
+    for g in range(2):
+        K, V = kvcache.gather(c.cache, c.segs[0], g, 1500)
+        for r in range(20):
+            vis = keep[keep <= rp[r]]
+            for h in range(4 * g, 4 * g + 4):
+                x = SCALE * (K[vis] @ qd[r, h])
+                w = np.exp(x - x.max())
+                ref = w @ V[vis] / w.sum()
+                tol = 2.0 ** -9 * (w @ np.abs(V[vis]) / w.sum()) + 2.0 ** -8 * np.abs(ref) + 1e-6
+                assert (np.abs(f64(out[r, h]) - ref) <= tol).all()
+
+
+def test_another_stream_and_two_threads():
+    """Calls on streams of their own from two threads at once: the bytes of the same calls one by one."""
+    import threading
+    jobs = []
+    for i in range(2):
+        c = Fp4Case([3000 + 100 * i, 800], [True, False], 8, 2, seed=74 + i).fill().upload()
+        rs = np.concatenate([np.zeros(1 + 19 * i, int), np.ones(2, int)])
+        rp = np.concatenate([np.arange(c.lengths[0] - 1 - 19 * i, c.lengths[0]), [798, 799]])
+        q = c.q(len(rs))
+        jobs.append((c, rs, rp, dev_bf16(q), decode(c, q, rs, rp)))
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            c, rs, rp, q, _ = jobs[i]
+            stream = torch.cuda.Stream()
+            out = torch.full((len(rs), 8, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+            lse = torch.full((len(rs), 8), float("nan"), device="cuda")
+            sc = B.make_scratch(64, 8)
+            torch.cuda.synchronize()
+            for _ in range(20):
+                B.tfpa_decode(c.gcache, c.gsegs, q, rs, rp, SCALE, sc, out, lse, stream=stream)
+            stream.synchronize()
+            got[i] = (out, lse)
+        except Exception as e:                                # shown by the assertion below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    for i in range(2):
+        assert torch.equal(got[i][0], jobs[i][4][0]) and torch.equal(got[i][1], jobs[i][4][1])
+
+
+def test_pinned_host_rows():
+    """Read-back into pinned host memory; decode's q there (short runs), refused for verify tiles."""
+    c = Fp4Case([600], [True], 8, 2, seed=76).fill().upload()
+    rp = np.array([599, 0, 256])
+    k, v = (torch.empty(3, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kh, vh = (torch.empty(3, 2, 128, dtype=torch.bfloat16).pin_memory() for _ in range(2))
+    B.tfpa_read_kv(c.gcache, c.gsegs, k, v, np.zeros(3), rp)
+    B.tfpa_read_kv(c.gcache, c.gsegs, kh, vh, np.zeros(3), rp)
+    torch.cuda.synchronize()
+    assert torch.equal(k.cpu(), kh) and torch.equal(v.cpu(), vh)
+    q = c.q(5)
+    out, lse = decode(c, q, np.zeros(5, int), np.arange(595, 600))
+    qh = dev_bf16(q).cpu().pin_memory()
+    o2, sc = torch.empty_like(out), B.make_scratch(16, 8)
+    with pytest.raises(B.TfpaError):
+        B.tfpa_decode(c.gcache, c.gsegs, qh, np.zeros(5, int), np.arange(595, 600), SCALE, sc, o2)
+    o1, _ = decode(c, q[:4], np.zeros(4, int), np.arange(595, 599))
+    B.tfpa_decode(c.gcache, c.gsegs, qh[:4], np.zeros(4, int), np.arange(595, 599), SCALE, sc, o2[:4])
+    torch.cuda.synchronize()
+    assert torch.equal(o1, o2[:4])
