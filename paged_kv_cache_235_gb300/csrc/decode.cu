@@ -1216,9 +1216,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_kernel(
 // wait for every one of them).  For their registers a work item has eight
 // query vectors (a decode row of up to eight heads a kv head), which halves a
 // warp's accumulators:
-//   S = Q K^T, vectors as the MMA's rows (half of them empty), so that S's
-//   fragment of vector gq is already P's fragment in
-//   O^T = V^T P^T, head dims as rows (16, all used) and vectors as columns.
+//   S^T = K Q^T, keys as the MMA's rows and vectors as its columns, then
+//   O^T = V^T P^T, head dims as rows and vectors as columns: all 16 rows used
+//   in both, S^T's fragments turned into P^T's by one 8 x 8 transposition a
+//   tile (8 streams of 65,536 keys 123 us; with vectors as S's rows, half of
+//   them empty and no transposition, 131 us).
 // The running maximum is looked at with one vote a block and moves only when
 // some score passes it by more than 2^8, which after a row's first block is
 // rare.
@@ -1247,37 +1249,50 @@ static_assert(kSmemBytes4 <= 232448, "shared memory");
 // high nibble of a byte are an O^T m-tile's rows gq and gq + 8.
 template <bool GEN>
 __device__ __forceinline__ void attend_fp4(uint32_t sb, const LaneFp4& at, int key_base,
-                                           int seq_len, const uint32_t (&qr)[16], int lim,
-                                           int minlim, float sc, uint64_t anc, int tree_low,
-                                           int c, float& m_run, float& l_run,
+                                           int seq_len, const uint32_t (&qr)[16],
+                                           const int (&lim)[2], int minlim, const float (&sc)[2],
+                                           const uint64_t (&anc)[2], int tree_low, int gq, int c,
+                                           float (&m_run)[2], float (&l_run)[2],
                                            float (&o)[8][4]) {
   constexpr int kKeys = 32;
-  // ---- S = Q K^T: lane (gq, c) holds dims 32 c .. 32 c + 31 of a key, a
-  // code word its dims 8 i .. + 7 of them.  The MMA's rows gq and gq + 8 both
-  // hold vector gq, with the word's pairs 0, 2 and 1, 3: of the product with
-  // the keys' pairs 0, 2 the first eight rows are kept, with 1, 3 the others,
-  // so that A is four registers as they stand.
-  float s[4][2];
+  // ---- S^T = K Q^T: lane (gq, c) holds dims 32 c .. 32 c + 31 of a key, a
+  // code word its dims 8 i .. + 7 of them; two n-tiles of eight keys are an
+  // MMA's rows gq and gq + 8.
+  float s[4][2];                 // [n-tile][vectors 2c, 2c + 1] of key row gq
   const uint32_t ka = sb + at.k, ksa = sb + at.ks;
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt) {
-    const uint4 kw = lds128(ka + nt * 8 * kFp4CodeBytes);
-    const uint32_t ks = e4m3x2_to_f16x2((uint16_t)lds16(ksa + nt * 8 * kFp4ScaleBytes));
-    float d0[4] = {}, d1[4] = {};
+  for (int t = 0; t < 2; ++t) {
+    uint4 kw[2];
+    uint32_t ks[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      kw[u] = lds128(ka + (2 * t + u) * 8 * kFp4CodeBytes);
+      ks[u] = lds16(ksa + (2 * t + u) * 8 * kFp4ScaleBytes);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) ks[u] = e4m3x2_to_f16x2((uint16_t)ks[u]);
+    float d[4] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t w = i == 0 ? kw.x : i == 1 ? kw.y : i == 2 ? kw.z : kw.w;
-      uint32_t h[4];
-      e2m1x8_to_f16x8(w, h);
-      const uint32_t s2 = prmt(ks, ks, i < 2 ? 0x1010 : 0x3232);
+      uint32_t h[2][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = hmul2(h[j], s2);
-      const uint32_t a[4] = {qr[4 * i], qr[4 * i + 1], qr[4 * i + 2], qr[4 * i + 3]};
-      mma_f16_free(d0, a, h[0], h[2]);
-      mma_f16_free(d1, a, h[1], h[3]);
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t w = i == 0 ? kw[u].x : i == 1 ? kw[u].y : i == 2 ? kw[u].z : kw[u].w;
+        e2m1x8_to_f16x8(w, h[u]);
+        const uint32_t s2 = prmt(ks[u], ks[u], i < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[u][j] = hmul2(h[u][j], s2);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t a[4] = {h[0][2 * k], h[1][2 * k], h[0][2 * k + 1], h[1][2 * k + 1]};
+        mma_f16_free(d, a, qr[4 * i + 2 * k], qr[4 * i + 2 * k + 1]);
+      }
     }
-    s[nt][0] = d0[0] + d1[2];
-    s[nt][1] = d0[1] + d1[3];
+    s[2 * t][0] = d[0];
+    s[2 * t][1] = d[1];
+    s[2 * t + 1][0] = d[2];
+    s[2 * t + 1][1] = d[3];
   }
   // ---- mask, running max, exponentials
   const bool tree_zone = GEN && key_base + kKeys > tree_low;
@@ -1286,47 +1301,54 @@ __device__ __forceinline__ void attend_fp4(uint32_t sb, const LaneFp4& at, int k
     for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int key = key_base + nt * 8 + c + 4 * j;
-        bool vis = key <= lim;
+        const int key = key_base + nt * 8 + ((gq >> 1) | ((gq & 1) << 2));
+        bool vis = key <= lim[j];
         if (tree_zone) {
-          const int dd = lim - key;
-          vis = vis && (dd > 63 || ((anc >> dd) & 1ull));
+          const int dd = lim[j] - key;
+          vis = vis && (dd > 63 || ((anc[j] >> dd) & 1ull));
         }
         if (!vis) s[nt][j] = -INFINITY;
       }
   }
-  float mx = fmaxf(fmax3(fmax3(s[0][0], s[0][1], s[1][0]), s[1][1], s[2][0]),
-                   fmax3(s[2][1], s[3][0], s[3][1])) * sc;       // scales are positive
-  if (__any_sync(0xffffffffu, mx > m_run + kRescaleThreshold)) {
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    float alpha = 1.f;
-    if (mx > m_run + kRescaleThreshold) {
-      alpha = fast_exp2(m_run - mx);
-      l_run *= alpha;
-      m_run = mx;
+  float mx[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)            // scales are positive
+    mx[j] = fmaxf(fmax3(s[0][j], s[1][j], s[2][j]), s[3][j]) * sc[j];
+  if (__any_sync(0xffffffffu, mx[0] > m_run[0] + kRescaleThreshold ||
+                                  mx[1] > m_run[1] + kRescaleThreshold)) {
+    float alpha[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 4));
+      mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 8));
+      mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
+      alpha[j] = 1.f;
+      if (mx[j] > m_run[j] + kRescaleThreshold) {
+        alpha[j] = fast_exp2(m_run[j] - mx[j]);
+        l_run[j] *= alpha[j];
+        m_run[j] = mx[j];
+      }
     }
-    // the factors of O^T's columns, vectors 2c and 2c + 1
-    const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c);
-    const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
-      o[mt][0] *= a0;
-      o[mt][1] *= a1;
-      o[mt][2] *= a0;
-      o[mt][3] *= a1;
+      o[mt][0] *= alpha[0];
+      o[mt][1] *= alpha[1];
+      o[mt][2] *= alpha[0];
+      o[mt][3] *= alpha[1];
     }
   }
-  const float nb = m_run == -INFINITY ? 0.f : -m_run;
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt)
+  for (int j = 0; j < 2; ++j) {
+    const float nb = m_run[j] == -INFINITY ? 0.f : -m_run[j];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) s[nt][j] = fast_exp2(__fmaf_rn(s[nt][j], sc, nb));
-  l_run += ((s[0][0] + s[0][1]) + (s[1][0] + s[1][1])) +
-           ((s[2][0] + s[2][1]) + (s[3][0] + s[3][1]));
+    for (int nt = 0; nt < 4; ++nt) s[nt][j] = fast_exp2(__fmaf_rn(s[nt][j], sc[j], nb));
+    l_run[j] += (s[0][j] + s[1][j]) + (s[2][j] + s[3][j]);
+  }
+  // P^T's fragments: keys 2c, 2c + 1 of an n-tile (its keys c and c + 4) and
+  // vector gq
   uint32_t pb[4];
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt) pb[nt] = pack_f16x2(s[nt][0], s[nt][1]);
+  for (int nt = 0; nt < 4; ++nt) pb[nt] = transpose8x8(pack_f16x2(s[nt][0], s[nt][1]));
   // ---- O^T += V^T P^T, 16 keys at a time: 16 dims (chunk gq) of the keys of
   // k indices 2c, 2c + 1, 2c + 8, 2c + 9.  Bytes past the stream's end may be
   // a NaN scale.
@@ -1415,6 +1437,13 @@ __device__ __forceinline__ void load_q_fp4(const DecodeParams& p, const RunInfo&
   sc = p.scale_log2 * __int_as_float((127 - 14 + ex) << 23) * __ldg(p.k_scale + x.g);
 }
 
+// The values of vectors 2c and 2c + 1 from the lanes that hold vector gq's.
+template <typename T>
+__device__ __forceinline__ void of_columns(T x, int c, T (&y)[2]) {
+  y[0] = __shfl_sync(0xffffffffu, x, 8 * c);
+  y[1] = __shfl_sync(0xffffffffu, x, 8 * c + 4);
+}
+
 // Waits whose result and reconvergence the whole warp shares, for the
 // warp-wide (aligned) instructions that follow.
 // SLEEP: ns between looks, for a role that waits most of the time (its looks
@@ -1447,9 +1476,9 @@ __device__ void consumer_fp4(const DecodeParams& p, const DecodeDyn& D, uint8_t*
   int rh = run_of(D, ib);
   Item x = item_of<KV>(p, D, ib, rh);
   int q_run = -1, q_g = -1, q_mt = -1;     // the m-tile whose query is loaded
-  int lim = -1, maxlim = -1, minlim = -1;
-  uint64_t anc = ~0ull;
-  float sc = 0.f;
+  int lim[2] = {-1, -1}, maxlim = -1, minlim = -1;   // of vectors 2c, 2c + 1
+  uint64_t anc[2] = {~0ull, ~0ull};
+  float sc[2] = {0.f, 0.f};
   uint32_t qr[16];
   int tree_low = INT_MAX;     // keys from here on may be hidden by an ancestor mask
 
@@ -1458,15 +1487,21 @@ __device__ void consumer_fp4(const DecodeParams& p, const DecodeDyn& D, uint8_t*
     int klo, khi;
     item_keys<KV>(p, D, x, klo, khi);
     if (x.run != q_run || x.g != q_g || x.mt != q_mt) {
-      load_q_fp4<GEN>(p, ru, x, gq, c, qr, lim, anc, sc);
-      maxlim = __reduce_max_sync(0xffffffffu, lim);
-      minlim = (int)__reduce_min_sync(0xffffffffu, (unsigned)(lim >= 0 ? lim : INT_MAX));
+      int lim1;
+      uint64_t anc1;
+      float sc1;
+      load_q_fp4<GEN>(p, ru, x, gq, c, qr, lim1, anc1, sc1);
+      maxlim = __reduce_max_sync(0xffffffffu, lim1);
+      minlim = (int)__reduce_min_sync(0xffffffffu, (unsigned)(lim1 >= 0 ? lim1 : INT_MAX));
+      of_columns(lim1, c, lim);
+      of_columns(sc1, c, sc);
+      if (GEN) of_columns(anc1, c, anc);
       if (GEN && p.anc) tree_low = minlim - 63;
       q_run = x.run;
       q_g = x.g;
       q_mt = x.mt;
     }
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     float o[8][4];
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
@@ -1474,28 +1509,30 @@ __device__ void consumer_fp4(const DecodeParams& p, const DecodeDyn& D, uint8_t*
          k0 += 2 * kPage, ++n) {
       const int buf = n & 1;
       // the next stage's barrier is looked at before this one's keys, off the
-      // path of the wait (8 streams of 65,536 keys 134 -> 131 us)
+      // path of the wait (8 streams of 65,536 keys 134 -> 131 us at the time)
       if (!__all_sync(0xffffffffu, ready) && !warp_wait(&full[buf], (n >> 1) & 1, p.err_flag))
         return;
       ready = mbar_test_wait(&full[buf ^ 1], ((n + 1) >> 1) & 1);
       const int key_base = k0 + (warp & 7) * 32;
       if (!stage_bad[buf] && key_base <= maxlim)
         attend_fp4<GEN>(ring + (uint32_t)buf * C::kStageBytes, at, key_base, ru.seq_len, qr, lim,
-                        minlim, sc, anc, tree_low, c, m_run, l_run, o);
+                        minlim, sc, anc, tree_low, gq, c, m_run, l_run, o);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[buf]);
     }
     // ---- hand the state to the combiners, as the other consumers do
-    l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
-    l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int k = 4; k < 32; k *= 2) l_run[j] += __shfl_xor_sync(0xffffffffu, l_run[j], k);
     const int rel = it - ib;
     const int b = rel & 1;
     if (rel >= 2 &&
         !warp_wait(&bars.tmem_free[b], (uint32_t)((rel >> 1) - 1) & 1u, p.err_flag))
       return;
-    if (c == 0)
-      *reinterpret_cast<float2*>(ml_buf + b * kMlFloats4 + (warp * 8 + gq) * 2) =
-          make_float2(m_run, l_run);
+    if (gq == 0)
+      *reinterpret_cast<float4*>(ml_buf + b * kMlFloats4 + (warp * 8 + 2 * c) * 2) =
+          make_float4(m_run[0], l_run[0], m_run[1], l_run[1]);
     __syncwarp();
     umma::fence_after_sync();
     {
