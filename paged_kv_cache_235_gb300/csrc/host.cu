@@ -262,7 +262,8 @@ int build_runs(const tfpa_seg* segs, int32_t nseg, const int32_t* row_seg,
 // vectors per kv head) are dense enough for the tensor cores: they take the
 // prefill kernel in verify mode, when a tile holds the group's heads.
 // Over a 4-bit cache, whose decode kernel spends most of its time on turning
-// codes into operands, already runs of two or more (more than 16 vectors).
+// codes into operands, already runs of two or more (more than 16 vectors: 8
+// streams of 65,536 keys, 20 vectors, 265 us on tiles and 330 us as items).
 constexpr int kFp4VerifyVectors = 16;
 bool on_verify_path(const Run& r, int G, int kv) {
   if (kv == kKvFp4) return G <= kVerifyVectors && r.nrows * G > kFp4VerifyVectors;
@@ -288,8 +289,8 @@ int no_throw(F&& fn) {
 
 // Runs of more than eight query vectors per kv head over a 4-bit cache take
 // the decode kernel of 16-vector items, the others that of eight (8 streams of
-// 65,536 keys: 16 vectors 167 us in one item, 264 us as two of eight; four
-// vectors 134 us in an item of eight, 166 us in one of 16).
+// 65,536 keys: 16 vectors 167 us in one item, 240 us as two of eight; eight
+// vectors 123 us in an item of eight, 165 us in one of 16).
 bool on_wide_path(const Run& r, int G, int kv) { return kv == kKvFp4 && r.nrows * G > 8; }
 
 int to_err(cudaError_t e) { return e == cudaSuccess ? TFPA_OK : TFPA_ECUDA; }
@@ -1399,7 +1400,10 @@ int mass_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const voi
       if (p.nsegs == 0 || p.segs[p.nsegs - 1].index != r.seg) {
         const tfpa_seg& g = segs[r.seg];
         const int64_t blocks = (int64_t)c->hkv * ((g.seq_len + kMassKeys - 1) / kMassKeys);
-        if (items + blocks > INT32_MAX) break;
+        if (items + blocks > INT32_MAX) {
+          if (nr == 0) return TFPA_ECAPACITY;   // more tiles than one launch can number
+          break;
+        }
         const int src = ss.add(segs, r.seg);
         if (src < 0) break;
         MassSeg& m = p.segs[p.nsegs++];

@@ -99,3 +99,12 @@ def test_evict_launches():
     with B.record_launches() as rec:
         _evict(keep=[100] * 100, segs=segs)
     assert [(r["kind"], r["row0"], r["rows"]) for r in rec] == [("evict", 0, 64), ("evict_move", 0, 64), ("evict", 64, 36), ("evict_move", 64, 36)]
+
+
+def test_mass_of_more_tiles_than_a_launch_numbers():
+    """A segment whose tiles pass 32 bits is refused; the launches before it are what they were."""
+    L, hkv = 2 ** 31 - 257, 256
+    with B.record_launches() as rec, pytest.raises(B.TfpaError) as e:
+        B.tfpa_key_mass(_cache(hq=hkv, hkv=hkv), [B.Seg(L, page_table=3 * FAKE)], FAKE, FAKE, [0], [5], 0.088,
+                        Plane(1, hkv, L), stream=0)
+    assert e.value.code == B.TFPA_ECAPACITY and rec == []
