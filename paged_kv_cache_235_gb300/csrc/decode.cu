@@ -598,18 +598,26 @@ __device__ __forceinline__ void attend_block(uint32_t sb, int r0, int key_base, 
 // key of column gq, V codes and scales of the first key of columns c.
 //   Columns of a score n-tile: even ones take its eight keys' 0-3, odd ones
 // 4-7, so that a quad's threads (columns 2c, 2c + 1) read V rows c and c + 4:
-// one read's four rows are then consecutive (64 bytes each, no bank
-// conflict).
+// one read's four rows are then consecutive.  CROSS: rows c and 4 + (c ^ 1),
+// so that the K rows of columns 2c and 2c + 1, 64 bytes each, lie in different
+// halves of the banks as well; a second pair of V addresses to hold (16-vector
+// items 167 -> 161 us for 8 streams of 65,536 keys and four rows; eight-vector
+// items, which have no registers to spare, 123 -> 125 us for one row).
+template <bool CROSS>
 struct LaneFp4 {
   uint32_t k, ks, v, vs;
   __device__ __forceinline__ LaneFp4(int w8, int gq, int c) {
     const uint32_t half = (uint32_t)(w8 >> 2) * kFp4HalfBytes;
-    const int r0 = (w8 & 3) * 32, kr = r0 + ((gq >> 1) | ((gq & 1) << 2)), vr = r0 + c;
+    const int r0 = (w8 & 3) * 32, kr = r0 + key_of(gq), vr = r0 + c;
     constexpr uint32_t kV = 2 * kFp4HalfBytes;
     k = half + kr * kFp4CodeBytes + 16 * c;
     ks = half + kFp4ScaleOff + kr * kFp4ScaleBytes + 2 * c;
     v = kV + half + vr * kFp4CodeBytes + 8 * gq;
     vs = kV + half + kFp4ScaleOff + vr * kFp4ScaleBytes + gq;
+  }
+  // The key of an n-tile's column i.
+  static __device__ __forceinline__ int key_of(int i) {
+    return i & 1 ? 4 + (CROSS ? (i >> 1) ^ 1 : i >> 1) : i >> 1;
   }
 };
 
@@ -620,7 +628,7 @@ struct LaneFp4 {
 // passes it by more than 2^8, which after a row's first block is rare.  A code
 // byte of two keys' equal nibbles converts to a V pair along the keys.
 template <bool GEN>
-__device__ __forceinline__ void attend_fp4_wide(uint32_t sb, const LaneFp4& at, int key_base,
+__device__ __forceinline__ void attend_fp4_wide(uint32_t sb, const LaneFp4<true>& at, int key_base,
                                                 int seq_len, const uint32_t (&qr)[2][16],
                                                 const int (&lim)[2], int minlim,
                                                 const float (&sc)[2], const uint64_t (&anc)[2],
@@ -661,14 +669,17 @@ __device__ __forceinline__ void attend_fp4_wide(uint32_t sb, const LaneFp4& at, 
     }
   }
   // ---- V's codes, dims 16 gq .. 16 gq + 15 of a key
+  const uint32_t va = sb + at.v, vsa = sb + at.vs;
+  const int cross = 1 - 2 * (c & 1);      // rows to c ^ 1
+  const uint32_t va1 = va + cross * kFp4CodeBytes, vsa1 = vsa + cross * kFp4ScaleBytes;
   uint2 vw[2][4];
   uint32_t vs[2][4];
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
     for (int q4 = 0; q4 < 4; ++q4) {
-      vw[kk][q4] = lds64(sb + at.v + (16 * kk + 4 * q4) * kFp4CodeBytes);
-      vs[kk][q4] = lds8(sb + at.vs + (16 * kk + 4 * q4) * kFp4ScaleBytes);
+      vw[kk][q4] = lds64((q4 & 1 ? va1 : va) + (16 * kk + 4 * q4) * kFp4CodeBytes);
+      vs[kk][q4] = lds8((q4 & 1 ? vsa1 : vsa) + (16 * kk + 4 * q4) * kFp4ScaleBytes);
     }
   // ---- mask, running max, exponentials
   const bool tree_zone = GEN && key_base + kKeys > tree_low;
@@ -678,7 +689,7 @@ __device__ __forceinline__ void attend_fp4_wide(uint32_t sb, const LaneFp4& at, 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int hr = j >> 1;
-        const int key = key_base + nt * 8 + c + 4 * (j & 1);
+        const int key = key_base + nt * 8 + at.key_of(2 * c + (j & 1));
         bool vis = key <= lim[hr];
         if (tree_zone) {
           const int dd = lim[hr] - key;
@@ -733,7 +744,8 @@ __device__ __forceinline__ void attend_fp4_wide(uint32_t sb, const LaneFp4& at, 
     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
       for (int q4 = 0; q4 < 4; ++q4)
-        if (key_base + 16 * kk + c + 4 * q4 >= seq_len) vs[kk][q4] = 0;
+        if (key_base + 16 * kk + 8 * (q4 >> 1) + at.key_of(2 * c + (q4 & 1)) >= seq_len)
+          vs[kk][q4] = 0;
   }
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) {
@@ -828,7 +840,7 @@ __device__ void consumer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
       const int r0 = wk0 - (sub0 / C::kSubWarps) * C::kStageKeys;
       if (!stage_bad[buf] && k0 + wk0 <= maxlim) {
         if constexpr (C::kFp4)
-          attend_fp4_wide<GEN>(sb, LaneFp4(warp, gq, c), k0 + wk0, ru.seq_len, qr, lim, minlim,
+          attend_fp4_wide<GEN>(sb, LaneFp4<true>(warp, gq, c), k0 + wk0, ru.seq_len, qr, lim, minlim,
                                sc, anc, tree_low, c, m_run, l_run, o);
         else
           attend_block<KV, GEN>(sb, r0, k0 + wk0, ru.seq_len, qr, lim, sc, anc, tree_low, gq, c,
@@ -1248,7 +1260,7 @@ static_assert(kSmemBytes4 <= 232448, "shared memory");
 // two keys' equal nibbles converts to a V pair along the keys; the low and the
 // high nibble of a byte are an O^T m-tile's rows gq and gq + 8.
 template <bool GEN>
-__device__ __forceinline__ void attend_fp4(uint32_t sb, const LaneFp4& at, int key_base,
+__device__ __forceinline__ void attend_fp4(uint32_t sb, const LaneFp4<false>& at, int key_base,
                                            int seq_len, const uint32_t (&qr)[16],
                                            const int (&lim)[2], int minlim, const float (&sc)[2],
                                            const uint64_t (&anc)[2], int tree_low, int gq, int c,
@@ -1301,7 +1313,7 @@ __device__ __forceinline__ void attend_fp4(uint32_t sb, const LaneFp4& at, int k
     for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int key = key_base + nt * 8 + ((gq >> 1) | ((gq & 1) << 2));
+        const int key = key_base + nt * 8 + at.key_of(gq);
         bool vis = key <= lim[j];
         if (tree_zone) {
           const int dd = lim[j] - key;
@@ -1462,7 +1474,7 @@ __device__ void consumer_fp4(const DecodeParams& p, const DecodeDyn& D, uint8_t*
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int gq = lane >> 2, c = lane & 3;
-  const LaneFp4 at(warp & 7, gq, c);
+  const LaneFp4<false> at(warp & 7, gq, c);
   const int group = warp >> 3;                          // pages of this parity
   const uint32_t ring = smem_u32(stage_mem) + (uint32_t)(2 * group) * C::kStageBytes;
   full += 2 * group;
