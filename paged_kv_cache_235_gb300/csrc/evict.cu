@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(
   h0 += hb;
   m0 += mb;
   if (tid == 0 && rank == 0) moves[0] = (int32_t)all;
+  uint8_t* list = reinterpret_cast<uint8_t*>(sh.hist) + 256 * (tid >> 5);   // 32 warps x 256 bytes
   {
     uint32_t at_eq = eq_at;
     for (int j0 = w0; j0 < w1; j0 += 128) {
@@ -290,18 +291,35 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(
       // both ranks in one scan (a run has at most 128 of each)
       uint32_t sum;
       const uint32_t r = warp_prefix(__popc(holes) | (uint32_t)__popc(movers) << 16, sum);
-      uint32_t rh = h0 + (r & 0xFFFFu), rm = m0 + (r >> 16);
+      // each list in rank order in the warp's part of shared memory (the slots'
+      // offsets in the run), then written by consecutive lanes
+      uint32_t rh = r & 0xFFFFu, rm = r >> 16;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        if (holes >> u & 1u) moves[4 + 2 * rh++ + 1] = j + u;
-        if (movers >> u & 1u) moves[4 + 2 * rm++] = j + u;
-        if (gone >> u & 1u) {           // a mover's slot is emptied when it moves
-          mass[j + u] = 0.f;
-          if (pos) pos[j + u] = -1;
+        if (holes >> u & 1u) list[rh++] = (uint8_t)(4 * lane + u);
+        if (movers >> u & 1u) list[128 + rm++] = (uint8_t)(4 * lane + u);
+      }
+      __syncwarp();
+      const uint32_t nholes = sum & 0xFFFFu, nmovers = sum >> 16;
+      for (uint32_t i = lane; i < nholes; i += 32) moves[4 + 2 * (h0 + i) + 1] = j0 + list[i];
+      for (uint32_t i = lane; i < nmovers; i += 32) moves[4 + 2 * (m0 + i)] = j0 + list[128 + i];
+      __syncwarp();
+      h0 += nholes;
+      m0 += nmovers;
+      // the evicted slots behind the cut (a mover's is emptied when it moves);
+      // the lane's other slots are written back as they are
+      if (gone) {
+        float4 m = *reinterpret_cast<const float4*>(mass + j);
+        m = make_float4(gone & 1u ? 0.f : m.x, gone & 2u ? 0.f : m.y, gone & 4u ? 0.f : m.z,
+                        gone & 8u ? 0.f : m.w);
+        *reinterpret_cast<float4*>(mass + j) = m;
+        if (pos) {
+          int4 a = *reinterpret_cast<const int4*>(pos + j);
+          a = make_int4(gone & 1u ? -1 : a.x, gone & 2u ? -1 : a.y, gone & 4u ? -1 : a.z,
+                        gone & 8u ? -1 : a.w);
+          *reinterpret_cast<int4*>(pos + j) = a;
         }
       }
-      h0 += sum & 0xFFFFu;
-      m0 += sum >> 16;
     }
   }
   sync();                               // no block leaves while another reads its counts
@@ -309,35 +327,30 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(
 
 constexpr int kMoveWarps = 8;
 
-// Lane t of 16's part of a stored row.
+// Lane t's part of a stored row: 16 bytes, as many lanes as the row has (4
+// bits: of its codes; lane 0 takes the scales too).  Rows are read and written
+// once, and the loads and stores say so (8 streams of 32,768 to 65,536 bf16
+// keys 201 -> 193 us, the choice with it).
 template <int KV>
-struct MoveRow;
-template <>
-struct MoveRow<kKvBf16> {
+struct MoveRow {
+  static constexpr int kLanes = KV == kKvBf16 ? 16 : KV == kKvFp8 ? 8 : 4;
   uint4 v;
-  __device__ void load(const uint8_t* b, size_t r, int t) {
-    v = reinterpret_cast<const uint4*>(b)[r * 16 + t];
+  uint2 scales;
+  __device__ __forceinline__ void load(const uint8_t* b, size_t r, int t) {
+    if (KV == kKvFp4) {
+      v = __ldcs(reinterpret_cast<const uint4*>(b + fp4_codes(r)) + t);
+      if (t == 0) scales = __ldcs(reinterpret_cast<const uint2*>(b + fp4_scales(r)));
+    } else {
+      v = __ldcs(reinterpret_cast<const uint4*>(b) + r * kLanes + t);
+    }
   }
-  __device__ void store(uint8_t* b, size_t r, int t) { reinterpret_cast<uint4*>(b)[r * 16 + t] = v; }
-};
-template <>
-struct MoveRow<kKvFp8> {
-  uint2 v;
-  __device__ void load(const uint8_t* b, size_t r, int t) {
-    v = reinterpret_cast<const uint2*>(b)[r * 16 + t];
-  }
-  __device__ void store(uint8_t* b, size_t r, int t) { reinterpret_cast<uint2*>(b)[r * 16 + t] = v; }
-};
-template <>
-struct MoveRow<kKvFp4> {
-  uint32_t v, s;                        // codes; lanes 0 and 1: four scales
-  __device__ void load(const uint8_t* b, size_t r, int t) {
-    v = reinterpret_cast<const uint32_t*>(b + fp4_codes(r))[t];
-    if (t < 2) s = reinterpret_cast<const uint32_t*>(b + fp4_scales(r))[t];
-  }
-  __device__ void store(uint8_t* b, size_t r, int t) {
-    reinterpret_cast<uint32_t*>(b + fp4_codes(r))[t] = v;
-    if (t < 2) reinterpret_cast<uint32_t*>(b + fp4_scales(r))[t] = s;
+  __device__ __forceinline__ void store(uint8_t* b, size_t r, int t) const {
+    if (KV == kKvFp4) {
+      __stcs(reinterpret_cast<uint4*>(b + fp4_codes(r)) + t, v);
+      if (t == 0) __stcs(reinterpret_cast<uint2*>(b + fp4_scales(r)), scales);
+    } else {
+      __stcs(reinterpret_cast<uint4*>(b) + r * kLanes + t, v);
+    }
   }
 };
 
@@ -358,8 +371,10 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(
   float* mass = p.mass + at * p.mass_cap;
   int32_t* pos = p.key_pos ? p.key_pos + at * p.mass_cap : nullptr;
   const int count = moves[0];
-  const bool is_v = lane >= 16;
-  const int t = lane & 15;
+  // a pair takes 2 kLanes lanes, K's and V's; a warp kPairs pairs at a time
+  constexpr int kPairs = 16 / Row::kLanes;
+  const int sub = lane / (2 * Row::kLanes), t = lane % Row::kLanes;
+  const bool is_v = lane / Row::kLanes & 1;
   uint8_t* base = static_cast<uint8_t*>(is_v ? sg.v_base : sg.k_base);
   auto row_of = [&](int slot, bool& ok) -> size_t {
     if (!sg.page_table) return (size_t)g * sg.slab_cap + slot;
@@ -369,7 +384,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(
   };
   // A warp takes pairs in batches, every one's row on its way before the
   // first is stored.
-  constexpr int kBatch = KV == kKvBf16 ? 4 : 8;
+  constexpr int kSteps = 4, kBatch = kSteps * kPairs;
   for (int i0 = (bx * kMoveWarps + (threadIdx.x >> 5)) * kBatch; i0 < count;
        i0 += p.grid_x * kMoveWarps * kBatch) {
     if (lane < kBatch && i0 + lane < count) {   // weights and positions: a lane a pair
@@ -381,23 +396,24 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(
         pos[m.x] = -1;
       }
     }
-    Row row[kBatch];
-    size_t dst[kBatch];
-    bool ok[kBatch];
+    Row row[kSteps];
+    size_t dst[kSteps];
+    bool ok[kSteps];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      ok[u] = i0 + u < count;
+    for (int u = 0; u < kSteps; ++u) {
+      const int i = i0 + u * kPairs + sub;
+      ok[u] = i < count;
       if (!ok[u]) continue;
-      const int2 m = *reinterpret_cast<const int2*>(moves + 4 + 2 * (i0 + u));
+      const int2 m = *reinterpret_cast<const int2*>(moves + 4 + 2 * i);
       const size_t src = row_of(m.x, ok[u]);
       dst[u] = row_of(m.y, ok[u]);
       if (ok[u])
         row[u].load(base, src, t);
-      else if (lane == 0)
+      else if (t == 0)
         flag_error(p.err_flag, kErrBadPage);
     }
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u)
+    for (int u = 0; u < kSteps; ++u)
       if (ok[u]) row[u].store(base, dst[u], t);
   }
 }

@@ -1539,8 +1539,9 @@ extern "C" int tfpa_evict_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t 
     if (!dry_run())
       if ((e = to_err(launch_evict_select(p, stream)))) return e;
     if (most == 0) continue;
-    // 32 pairs a block and round; several blocks' worth of rounds where there
-    // are many, so that planes of few pairs leave early
+    // 32 pairs a block and round (64 and 128 of the narrower types); several
+    // blocks' worth of rounds where there are many, so that planes of few pairs
+    // leave early
     p.grid_x = std::min((most + 31) / 32, std::max(1, 64 * nsm / planes));
     record(12, s0, p.nsegs, 0, planes, p.grid_x * planes, 0, 0);
     if (!dry_run())
