@@ -289,7 +289,7 @@ int no_throw(F&& fn) {
 
 // Runs of more than eight query vectors per kv head over a 4-bit cache take
 // the decode kernel of 16-vector items, the others that of eight (8 streams of
-// 65,536 keys: 16 vectors 167 us in one item, 240 us as two of eight; eight
+// 65,536 keys: 16 vectors 161 us in one item, 240 us as two of eight; eight
 // vectors 123 us in an item of eight, 165 us in one of 16).
 bool on_wide_path(const Run& r, int G, int kv) { return kv == kKvFp4 && r.nrows * G > 8; }
 
