@@ -47,7 +47,11 @@ struct MassCfg {
   static constexpr int kThreads = kF16 ? 640 : 384;
   static constexpr int kStageBytes =
       KV == kKvBf16 ? 32768 : KV == kKvFp8 ? 16384 : kFp4HalfBytes;
-  static constexpr int kStages = KV == kKvBf16 ? 4 : KV == kKvFp8 ? 5 : 9;
+  // An even number: the converter groups take tiles in turn, and a stage has to
+  // be the same group's every time (a barrier's parity only tells phases apart
+  // for those who wait for every one of them).
+  static constexpr int kStages = KV == kKvFp4 ? 8 : 4;
+  static_assert(kStages % 2 == 0, "a stage belongs to one converter group");
   static constexpr int kOps = kF16 ? 2 : 0;              // f16 operand tiles
   static constexpr int kOffQ = 0;                        // 64 KB
   static constexpr int kOffOp = 65536;
