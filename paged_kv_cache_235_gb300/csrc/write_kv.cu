@@ -12,6 +12,10 @@
 // with i + 64 (rotate-half), so a thread also reads its partner's 8
 // elements; every product and sum is rounded on its own (no fused
 // multiply-add), so the stored code is a function of the inputs alone.
+// Measured over a 4-bit cache: 4,096 rows of 8 kv heads with their rotation 12
+// us, one row of 8 streams 4.3 us (a launch and one chain of memory latencies);
+// the chunk is bound by the same chain, its loads all on their way before the
+// page id is looked at.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -145,7 +149,8 @@ __global__ void __launch_bounds__(256) write_kv_kernel(const __grid_constant__ W
 // run backwards (8 head dims a thread).  A bf16 row is copied; an e4m3 value
 // is code * scale and a 4-bit value (code * block scale, exact) * scale, the
 // product rounded to float32 and then to bf16.  Bound by launch latency for
-// a step's rows and by the bf16 output's bytes for a chunk's.
+// a step's rows (4.5 us) and by the bf16 output's bytes for a chunk's (4,096 rows
+// of 8 kv heads of a 4-bit cache 7.5 us, 2.9 TB/s out of L2).
 __global__ void __launch_bounds__(256) read_kv_kernel(const __grid_constant__ WriteParams p) {
   allow_next_grid();
   wait_prior_grid();
