@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(256) write_kv_kernel(const __grid_constant__ W
 // is code * scale and a 4-bit value (code * block scale, exact) * scale, the
 // product rounded to float32 and then to bf16.  Bound by launch latency for
 // a step's rows (4.5 us) and by the bf16 output's bytes for a chunk's (4,096 rows
-// of 8 kv heads of a 4-bit cache 7.5 us, 2.9 TB/s out of L2).
+// of 8 kv heads of a 4-bit cache 7.5 us, 2.9 TB/s).
 __global__ void __launch_bounds__(256) read_kv_kernel(const __grid_constant__ WriteParams p) {
   allow_next_grid();
   wait_prior_grid();
