@@ -320,20 +320,25 @@ cudaError_t launch_read_kv(const WriteParams& p, cudaStream_t s) {
   return launch_pdl(read_kv_kernel, dim3(grid), dim3(256), 0, s, p);
 }
 
+// Shared memory for the most pairs that a call may have is asked for once,
+// whatever this call's number: the kernel's own tables (8 KB, 16 KB of a 4-bit
+// cache's) count towards the 48 KB that a launch gets without asking, so a
+// test of the pieces alone would not know when they pass it.
+template <bool FP4>
+cudaError_t launch_keep_rows(const KeepParams& p, int pair_bytes, cudaStream_t s) {
+  static PerDeviceOnce configured;
+  const cudaError_t e = configured.run([] {
+    return cudaFuncSetAttribute(keep_kernel<FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kMaxKeep * 2 * (FP4 ? 80 : 256));
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(keep_kernel<FP4>, dim3(p.hkv), dim3(kKeepThreads), p.n * pair_bytes, s, p);
+}
+
 cudaError_t launch_keep(const KeepParams& p, cudaStream_t s) {
   if (p.n == 0) return cudaSuccess;
-  if (p.row_bytes == kFp4CodeBytes + kFp4ScaleBytes)     // at most 40 KB of pieces
-    return launch_pdl(keep_kernel<true>, dim3(p.hkv), dim3(kKeepThreads), p.n * 2 * 80, s, p);
-  const int smem = p.n * 2 * p.row_bytes;
-  static PerDeviceOnce configured;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = configured.run([] {
-      return cudaFuncSetAttribute(keep_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  kMaxKeep * 2 * 256);
-    });
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(keep_kernel<false>, dim3(p.hkv), dim3(kKeepThreads), smem, s, p);
+  return p.row_bytes == kFp4CodeBytes + kFp4ScaleBytes ? launch_keep_rows<true>(p, 2 * 80, s)
+                                                       : launch_keep_rows<false>(p, 2 * p.row_bytes, s);
 }
 
 }  // namespace tfpa
