@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
         named_bar_sync(2, C::kThreads - 32);
       }
       if (warp == 0) {
+        bool ok = true;
         if (lane == 0) {
           int page_at = -1, pid = 0;
           const int32_t* table = sg.page_table;
@@ -360,8 +361,8 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
             }
             const uint32_t st = cnt + i;
             const int s = st % C::kStages;
-            if (!mbar_wait_or_abort(&b.empty[s], ((st / C::kStages) & 1) ^ 1, p.err_flag, b.abort))
-              goto out;
+            ok = mbar_wait_or_abort(&b.empty[s], ((st / C::kStages) & 1) ^ 1, p.err_flag, b.abort);
+            if (!ok) break;
             uint8_t* dst = smem + C::kOffStage + s * C::kStageBytes;
             mbar_arrive_expect_tx(&b.full[s], C::kStageBytes);
             if (KV == kKvBf16) {
@@ -376,7 +377,9 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
             }
           }
         }
-        __syncwarp();
+        // the warp leaves with lane 0: alone, it would wait in the block's
+        // last barrier for lanes that wait for it here
+        if (!__shfl_sync(0xffffffffu, ok, 0)) goto out;
       } else if (warp == 1) {
         const uint32_t idesc = umma::idesc_f16(128, 16, !C::kF16, false) + ((uint32_t)(n - 16) >> 3 << 17);
         const uint32_t qb = smem_u32(smem + C::kOffQ);
