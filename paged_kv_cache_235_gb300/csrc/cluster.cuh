@@ -97,4 +97,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 
+// The whole warp's wait, as warp_wait.
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, int32_t* err) {
+  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, err));
+}
+
 }  // namespace tfpa

@@ -159,6 +159,19 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parit
   return true;
 }
 
+// The same waits made by a whole converged warp, which goes on or gives up as
+// one.  Lanes on their own can disagree when the time runs out, and then
+// those that leave wait at the block's next barrier for those that stay,
+// which wait for them at the next warp-wide instruction.
+template <int SLEEP = 0>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err) {
+  return __all_sync(0xffffffffu, mbar_wait<SLEEP>(bar, parity, err));
+}
+__device__ __forceinline__ bool warp_wait_or_abort(uint64_t* bar, uint32_t parity, int32_t* err,
+                                                   volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, err, abort));
+}
+
 // 3D tiled load (x innermost).
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y,
                                             int z, uint64_t* bar) {

@@ -1456,15 +1456,6 @@ __device__ __forceinline__ void of_columns(T x, int c, T (&y)[2]) {
   y[1] = __shfl_sync(0xffffffffu, x, 8 * c + 4);
 }
 
-// Waits whose result and reconvergence the whole warp shares, for the
-// warp-wide (aligned) instructions that follow.
-// SLEEP: ns between looks, for a role that waits most of the time (its looks
-// take issue slots from the consumers).
-template <int SLEEP = 0>
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err) {
-  return __all_sync(0xffffffffu, mbar_wait<SLEEP>(bar, parity, err));
-}
-
 template <bool GEN>
 __device__ void consumer_fp4(const DecodeParams& p, const DecodeDyn& D, uint8_t* stage_mem,
                              uint64_t* full, uint64_t* empty, const int* stage_bad, uint32_t tmem,

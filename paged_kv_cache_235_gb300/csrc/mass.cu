@@ -237,12 +237,6 @@ __device__ __forceinline__ void hold(float& x) { asm volatile("" : "+f"(x)); }
 template <typename T>
 __device__ __forceinline__ void hold(T*& x) { asm volatile("" : "+l"(x)); }
 
-// A wait of the whole warp, which goes on as one.
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int32_t* err,
-                                         volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, err, abort));
-}
-
 template <int KV>
 __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
     key_mass_kernel(const __grid_constant__ MassParams p) {
@@ -449,8 +443,9 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
           const float old0 = old_of(i), old1 = two ? old_of(i + 1) : 0.f;
           const int d = st & (nb - 1);
           const int key = (kt0 + i) * kTile + lane_key;
-          if (!wait_all(&b.d_full[d], (st >> lnb) & 1, p.err_flag, b.abort)) break;
-          if (two && !wait_all(&b.d_full[d + 1], (st >> lnb) & 1, p.err_flag, b.abort)) break;
+          if (!warp_wait_or_abort(&b.d_full[d], (st >> lnb) & 1, p.err_flag, b.abort)) break;
+          if (two && !warp_wait_or_abort(&b.d_full[d + 1], (st >> lnb) & 1, p.err_flag, b.abort))
+            break;
           umma::fence_after_sync();
           float s0 = 0.f, s1 = 0.f;
           const uint32_t td = tq + d * dcols;
@@ -479,8 +474,8 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
         for (int i = (cnt & 1) ^ o; i < mt; i += 2) {
           const uint32_t st = cnt + i;
           const int s = st % C::kStages;
-          if (!wait_all(&b.full[s], (st / C::kStages) & 1, p.err_flag, b.abort) ||
-              !wait_all(&b.op_empty[o], ((st >> 1) & 1) ^ 1, p.err_flag, b.abort))
+          if (!warp_wait_or_abort(&b.full[s], (st / C::kStages) & 1, p.err_flag, b.abort) ||
+              !warp_wait_or_abort(&b.op_empty[o], ((st >> 1) & 1) ^ 1, p.err_flag, b.abort))
             break;
           const uint8_t* src = smem + C::kOffStage + s * C::kStageBytes;
           uint8_t* dst = smem + C::kOffOp + o * 32768;

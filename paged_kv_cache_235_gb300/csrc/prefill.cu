@@ -152,6 +152,13 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 units
 __device__ __forceinline__ uint32_t col_s(int hh) { return hh ? 256u : 0u; }
 __device__ __forceinline__ uint32_t col_o(int hh) { return hh ? 384u : 128u; }
 
+// Waits give up after a time limit, and every thread has to reach the block's
+// last barrier all the same.  A wait answers for its own lane, and lanes can
+// disagree when the time runs out.  So either one thread waits for its warp,
+// or the warp votes, or no lane leaves on its answer: it goes on in step with
+// its warp over bytes that are not there, and what it would hand on (an
+// arrival, an MMA) it does not.  *abort is set by then, and the rest of the
+// block gives up as well.
 struct Bars {
   uint64_t* q_full;      // Q tiles landed (TMA)
   uint64_t* q_ready;     // Q operand ready for the MMA (e4m3 caches: after conversion)
@@ -515,7 +522,9 @@ __device__ __forceinline__ void zero_v_rows(uint8_t* vtile, int z0, int lane) {
 // Warps 12-15 for e4m3 and 4-bit caches: staging -> f16 operand stages, in the order
 // the producer fills the staging tiles.  Prefill: K and V of each key tile
 // through one staging tile each.  Verify: V only (K feeds 8-bit MMAs), slot
-// hh's step jj from staging tile 2 hh + (jj & 1).
+// hh's step jj from staging tile 2 hh + (jj & 1).  A lane whose wait gave up
+// converts what is there, and nobody is told (see Bars): a vote after each
+// wait cost an e4m3 prompt chunk 1.3 %, the flag read beside it nothing.
 template <int KV, bool VERIFY>
 __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileGeom& gm,
                           uint8_t* smem, const Bars& b) {
@@ -527,8 +536,9 @@ __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileG
                      uint64_t* full8, uint64_t* empty8) {
     uint64_t* empty = is_v ? &b.v_empty[s] : &b.k_empty[s];
     uint64_t* full = is_v ? &b.v_full[s] : &b.k_full[s];
-    if (!mbar_wait_or_abort(full8, ph8, p.err_flag, b.abort)) return false;
-    if (!mbar_wait_or_abort(empty, ph ^ 1, p.err_flag, b.abort)) return false;
+    mbar_wait_or_abort(full8, ph8, p.err_flag, b.abort);
+    mbar_wait_or_abort(empty, ph ^ 1, p.err_flag, b.abort);
+    const int gave_up = *b.abort;
     uint8_t* dst = smem + (is_v ? kOffV : kOffK) + s * 32768;
     if (KV == kKvFp4)
       convert_tile_fp4<kConvWarps * 32, 4>(smem + src, dst, is_v ? z0 : kTileKeys, t);
@@ -536,11 +546,10 @@ __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileG
       convert_tile<kConvWarps * 32>(smem + src, dst, is_v ? z0 : kTileKeys, t);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) {
+    if (lane == 0 && !gave_up) {
       mbar_arrive(empty8);
       mbar_arrive(full);
     }
-    return true;
   };
   if constexpr (VERIFY && KV == kKvFp4) {
     PageCheck pc0(p, ru, gm, gm.kt0, slot_tiles<true>(gm, 0), 2);
@@ -569,13 +578,14 @@ __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileG
         const bool r0 = mbar_try_wait(full8 + i0, par0), r1 = mbar_try_wait(full8 + i1, par1);
         const bool r2 = mbar_try_wait(empty, ph), r3 = mbar_try_wait(empty + 1, ph);
         if (!(r0 && r2 && (!two || (r1 && r3)))) {
-          if (!mbar_wait_or_abort(full8 + i0, par0, p.err_flag, b.abort) ||
-              !mbar_wait_or_abort(empty, ph, p.err_flag, b.abort))
-            return;
-          if (two && (!mbar_wait_or_abort(full8 + i1, par1, p.err_flag, b.abort) ||
-                      !mbar_wait_or_abort(empty + 1, ph, p.err_flag, b.abort)))
-            return;
+          mbar_wait_or_abort(full8 + i0, par0, p.err_flag, b.abort);
+          mbar_wait_or_abort(empty, ph, p.err_flag, b.abort);
+          if (two) {
+            mbar_wait_or_abort(full8 + i1, par1, p.err_flag, b.abort);
+            mbar_wait_or_abort(empty + 1, ph, p.err_flag, b.abort);
+          }
         }
+        const int gave_up = *b.abort;
         __syncwarp();
         uint8_t* dst = smem + (kv ? kOffV : kOffK);
         Fp4Tile<kConvWarps * 32> a, c;
@@ -584,7 +594,7 @@ __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileG
         a.write(dst, t);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0 && !gave_up) {
           mbar_arrive(empty8 + i0);
           mbar_arrive(full);
         }
@@ -592,7 +602,7 @@ __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileG
           c.write(dst + 32768, t);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
+          if (lane == 0 && !gave_up) {
             mbar_arrive(empty8 + i1);
             mbar_arrive(full + 1);
           }
@@ -606,15 +616,14 @@ __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileG
   } else if (VERIFY) {
     PageCheck pc0(p, ru, gm, gm.kt0, slot_tiles<true>(gm, 0), 2);
     PageCheck pc1(p, ru, gm, gm.kt0 + 1, slot_tiles<true>(gm, 1), 2);
-    bool ok = true;
-    for (int jj = 0; ok && jj < slot_tiles<true>(gm, 0); ++jj) {
-      for (int hh = 0; ok && hh < 2; ++hh) {
+    for (int jj = 0; jj < slot_tiles<true>(gm, 0); ++jj) {
+      for (int hh = 0; hh < 2; ++hh) {
         if (jj >= slot_tiles<true>(gm, hh)) continue;
         const int j = slot_tile<true>(gm, jj, hh);
         const int z0 = v_zero_from(ru, j, hh ? pc1.bad(j) : pc0.bad(j));
         const int i = 2 * hh + (jj & 1);
-        ok = convert(true, hh, jj & 1, z0, vstage8_off(i), (uint32_t)((jj >> 1) & 1),
-                     b.v8_full + i, b.v8_empty + i);
+        convert(true, hh, jj & 1, z0, vstage8_off(i), (uint32_t)((jj >> 1) & 1),
+                b.v8_full + i, b.v8_empty + i);
       }
     }
     return;
@@ -627,8 +636,8 @@ __device__ void converter(const PrefillParams& p, const RunInfo& ru, const TileG
     const uint32_t ph = (jj >> 1) & 1;
     // one staging tile each for K and V: its jj-th fill is phase jj & 1
     const uint32_t ph8 = (uint32_t)(jj & 1);
-    if (!convert(false, s, ph, z0, stage8_off(false), ph8, b.k8_full, b.k8_empty)) return;
-    if (!convert(true, s, ph, z0, stage8_off(true), ph8, b.v8_full, b.v8_empty)) return;
+    convert(false, s, ph, z0, stage8_off(false), ph8, b.k8_full, b.k8_empty);
+    convert(true, s, ph, z0, stage8_off(true), ph8, b.v8_full, b.v8_empty);
   }
 }
 
@@ -643,6 +652,11 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
   const uint32_t kb = smem_u32(smem + kOffK);
   const uint32_t vb = smem_u32(smem + kOffV);
 
+  // A bf16 prompt's descriptors are formed from here on each time: kept over
+  // the one thread's loop, those of every stage and k-step spill.
+  auto fresh = [](uint32_t& x) {
+    if (!VERIFY && !F16) asm volatile("" : "+r"(x));
+  };
   constexpr uint32_t kIdescQK8 = umma::idesc_e4m3(128, 128);
   auto issue_s = [&](int hh, int s) {     // S_hh = Q_hh K_s^T (verify: one Q tile)
     if constexpr (VERIFY && KV == kKvFp8) {
@@ -657,21 +671,25 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
           umma::mma_ss_f8(tmem + col_s(hh), a, bd, kIdescQK8, (q | ks) ? 1u : 0u);
         }
     } else {
+      uint32_t q16 = qb + (VERIFY ? 0 : hh * 32768);
+      uint32_t k16 = VERIFY && !F16 ? smem_u32(smem + kstage16_off(s)) : kb + s * 32768;
+      fresh(q16);
+      fresh(k16);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
         const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-        const uint64_t a = umma::smem_desc_sw128(qb + (VERIFY ? 0 : hh * 32768) + off, 16, 1024);
-        const uint32_t k16 =
-            VERIFY && !F16 ? smem_u32(smem + kstage16_off(s)) : kb + s * 32768;
+        const uint64_t a = umma::smem_desc_sw128(q16 + off, 16, 1024);
         const uint64_t bd = umma::smem_desc_sw128(k16 + off, 16, 1024);
         umma::mma_ss(tmem + col_s(hh), a, bd, kIdescQK, ks > 0 ? 1u : 0u);
       }
     }
   };
   auto issue_pv = [&](int hh, int s, bool acc) {   // O_hh (+)= P_hh V_s
+    uint32_t v16 = vb + s * 32768;
+    fresh(v16);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
-      const uint64_t bd = umma::smem_desc_sw128(vb + s * 32768 + kk * 2048, 16384, 1024);
+      const uint64_t bd = umma::smem_desc_sw128(v16 + kk * 2048, 16384, 1024);
       umma::mma_ts(tmem + col_o(hh), tmem + col_s(hh) + kk * 8, bd, kIdescPV,
                    (acc || kk > 0) ? 1u : 0u);
     }
@@ -683,64 +701,67 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
     return;
   }
   if (VERIFY) {
-    // Slot hh, step jj.  bf16: K and V of tile n = 2 jj + hh in stage n mod
-    // 3 at phase (n / 3) & 1.  e4m3: K in e4m3 stage 2 hh + (jj & 1) at phase
-    // (jj >> 1) & 1, V in 16-bit stage hh at phase jj & 1.
+    // One thread waits and issues (a tile's waits by the whole warp, which
+    // then meets for each issue: 16-node trees over a 4-bit cache 159 us against
+    // 157); only V rows to be zeroed bring the warp together.
+    // Step n: tile n, slot hh = n & 1, the slot's step jj = n / 2.  bf16: K
+    // and V in stage n mod 3 at phase (n / 3) & 1.  e4m3: K in e4m3 stage 2 hh
+    // + (jj & 1) at phase (jj >> 1) & 1, V in 16-bit stage hh at phase jj & 1.
     // 4 bits: K and V both in the slot's one 16-bit stage at phase jj & 1.
-    auto kst = [&](int hh, int jj) {
-      return KV == kKvFp4 ? hh : F16 ? 2 * hh + (jj & 1) : (2 * jj + hh) % 3;
+    auto wait = [&](uint64_t* bar, uint32_t ph) {
+      return mbar_wait_or_abort(bar, ph, p.err_flag, b.abort);
     };
-    auto kph = [&](int hh, int jj) {
-      return (uint32_t)(KV == kKvFp4 ? jj & 1 : F16 ? (jj >> 1) & 1 : ((2 * jj + hh) / 3) & 1);
+    auto kst = [&](int n) {
+      return KV == kKvFp4 ? n & 1 : F16 ? 2 * (n & 1) + ((n >> 1) & 1) : n % 3;
     };
-    auto vst = [&](int hh, int jj) { return F16 ? hh : (2 * jj + hh) % 3; };
-    auto vph = [&](int hh, int jj) { return (uint32_t)(F16 ? jj & 1 : ((2 * jj + hh) / 3) & 1); };
-    bool ok = mbar_wait_or_abort(b.q_ready, 0, p.err_flag, b.abort);
-    for (int hh = 0; ok && hh < 2; ++hh) {
-      if (slot_tiles<true>(gm, hh) == 0) continue;
-      if (!(ok = mbar_wait_or_abort(&b.k_full[kst(hh, 0)], 0, p.err_flag, b.abort))) break;
+    auto kph = [&](int n) {
+      return (uint32_t)(KV == kKvFp4 ? (n >> 1) & 1 : F16 ? (n >> 2) & 1 : (n / 3) & 1);
+    };
+    auto vst = [&](int n) { return F16 ? n & 1 : n % 3; };
+    auto vph = [&](int n) { return (uint32_t)(F16 ? (n >> 1) & 1 : (n / 3) & 1); };
+    const int steps = gm.nkt;
+    auto score = [&](int n) {
+      if (!wait(&b.k_full[kst(n)], kph(n))) return false;
       umma::fence_after_sync();
+      issue_s(n & 1, kst(n));
+      umma::commit(&b.s_full[n & 1]);
+      umma::commit(&b.k_empty[kst(n)]);
+      return true;
+    };
+    auto step = [&](int n, bool v_there) {
+      const int vs = vst(n);
+      if (!v_there && !wait(&b.v_full[vs], vph(n))) return false;
+      if (!wait(&b.p_ready[n & 1], (n >> 1) & 1)) return false;
+      umma::fence_after_sync();
+      issue_pv(n & 1, vs, n > 1);
+      umma::commit(&b.v_empty[vs]);
+      return n + 2 >= steps || score(n + 2);
+    };
+    PageCheck pc(p, ru, gm, gm.kt0, steps, 1);
+    int n = 0;
+    bool ok = true;
+    while (ok && n < steps) {
+      int z0 = kTileKeys;
       if (umma::elect_one()) {
-        issue_s(hh, kst(hh, 0));
-        umma::commit(&b.s_full[hh]);
-        umma::commit(&b.k_empty[kst(hh, 0)]);
-      }
-      __syncwarp();
-    }
-    PageCheck pc0(p, ru, gm, gm.kt0, slot_tiles<true>(gm, 0), 2);
-    PageCheck pc1(p, ru, gm, gm.kt0 + 1, slot_tiles<true>(gm, 1), 2);
-    for (int jj = 0; ok && jj < slot_tiles<true>(gm, 0); ++jj) {
-      for (int hh = 0; ok && hh < 2; ++hh) {
-        const int n = slot_tiles<true>(gm, hh);
-        if (jj >= n) continue;
-        const int j = slot_tile<true>(gm, jj, hh);
-        const bool page_bad = hh ? pc1.bad(j) : pc0.bad(j);
-        const int vs = vst(hh, jj);
-        if (!(ok = mbar_wait_or_abort(&b.v_full[vs], vph(hh, jj), p.err_flag, b.abort))) break;
-        if (!F16) {
-          const int z0 = v_zero_from(ru, j, page_bad);
-          if (z0 < kTileKeys) zero_v_rows(smem + kOffV + vs * 32768, z0, lane);
-        }
-        if (!(ok = mbar_wait_or_abort(&b.p_ready[hh], jj & 1, p.err_flag, b.abort))) break;
-        umma::fence_after_sync();
-        if (umma::elect_one()) {
-          issue_pv(hh, vs, jj > 0);
-          umma::commit(&b.v_empty[vs]);
-        }
-        __syncwarp();
-        if (jj + 1 < n) {
-          const int ks = kst(hh, jj + 1);
-          if (!(ok = mbar_wait_or_abort(&b.k_full[ks], kph(hh, jj + 1), p.err_flag, b.abort)))
-            break;
-          umma::fence_after_sync();
-          if (umma::elect_one()) {
-            issue_s(hh, ks);
-            umma::commit(&b.s_full[hh]);
-            umma::commit(&b.k_empty[ks]);
+        if (n == 0) ok = wait(b.q_ready, 0) && score(0) && (steps < 2 || score(1));
+        for (; ok && n < steps; ++n) {
+          if (!F16) {                   // the converters zero these rows themselves
+            z0 = v_zero_from(ru, gm.kt0 + n, pc.bad(gm.kt0 + n));
+            if (z0 < kTileKeys) break;
           }
-          __syncwarp();
+          ok = step(n, false);
         }
       }
+      ok = __all_sync(0xffffffffu, ok);
+      if (F16 || !ok) break;
+      n = (int)__reduce_max_sync(0xffffffffu, (unsigned)n);     // the thread's
+      z0 = (int)__reduce_min_sync(0xffffffffu, (unsigned)z0);
+      if (n == steps) break;
+      if (!(ok = warp_wait_or_abort(&b.v_full[vst(n)], vph(n), p.err_flag, b.abort))) break;
+      zero_v_rows(smem + kOffV + vst(n) * 32768, z0, lane);
+      if (umma::elect_one()) ok = step(n, true);
+      ok = __all_sync(0xffffffffu, ok);
+      ++n;
     }
     if (umma::elect_one()) {
       if (ok) {
@@ -753,11 +774,15 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
     __syncwarp();
     return;
   }
-  bool ok = mbar_wait_or_abort(b.q_ready, 0, p.err_flag, b.abort) &&
-            mbar_wait_or_abort(&b.k_full[0], 0, p.err_flag, b.abort);
-  if (ok) {
+  if constexpr (F16) {
+    // e4m3 and 4 bits: every lane waits, the elected one issues if its own waits
+    // ended well, and no lane leaves before the others (see Bars).  Chunk of 4,096
+    // rows over 32,768 keys: e4m3 1,405 us, 4 bits 1,430; a step at a time in one
+    // thread 1,450 and 1,489; a vote after each wait 1,417 and 1,458.
+    bool live = mbar_wait_or_abort(b.q_ready, 0, p.err_flag, b.abort) &&
+                mbar_wait_or_abort(&b.k_full[0], 0, p.err_flag, b.abort);
     umma::fence_after_sync();
-    if (umma::elect_one()) {
+    if (umma::elect_one() && live) {
       issue_s(0, 0);
       umma::commit(&b.s_full[0]);
       issue_s(1, 0);
@@ -765,37 +790,83 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
       umma::commit(&b.k_empty[0]);
     }
     __syncwarp();
-  }
-  PageCheck pc(p, ru, gm, gm.kt0, gm.nkt, 1);
-  for (int jj = 0; ok && jj < gm.nkt; ++jj) {
-    const int j = gm.kt0 + jj;
-    const bool page_bad = pc.bad(j);
-    const int s = jj & 1;
-    const uint32_t ph = (jj >> 1) & 1;
-    const int s1 = (jj + 1) & 1;
-    const uint32_t ph1 = ((jj + 1) >> 1) & 1;
-    const bool more = jj + 1 < gm.nkt;
-    if (!(ok = mbar_wait_or_abort(&b.v_full[s], ph, p.err_flag, b.abort))) break;
-    if (!F16) {   // the e4m3 converters zero these rows themselves
-      const int z0 = v_zero_from(ru, j, page_bad);
-      if (z0 < kTileKeys) zero_v_rows(smem + kOffV + s * 32768, z0, lane);
-    }
-    // head A
-    if (!(ok = mbar_wait_or_abort(&b.p_ready[0], jj & 1, p.err_flag, b.abort))) break;
-    umma::fence_after_sync();
-    if (umma::elect_one()) issue_pv(0, s, jj > 0);
-    if (more) {
-      if (!(ok = mbar_wait_or_abort(&b.k_full[s1], ph1, p.err_flag, b.abort))) break;
+    for (int jj = 0; jj < gm.nkt; ++jj) {
+      const int s = jj & 1;
+      const uint32_t ph = (jj >> 1) & 1;
+      const int s1 = (jj + 1) & 1;
+      const uint32_t ph1 = ((jj + 1) >> 1) & 1;
+      const bool more = jj + 1 < gm.nkt;
+      live = live && mbar_wait_or_abort(&b.v_full[s], ph, p.err_flag, b.abort);
+      // head A
+      live = live && mbar_wait_or_abort(&b.p_ready[0], jj & 1, p.err_flag, b.abort);
       umma::fence_after_sync();
-      if (umma::elect_one()) {
+      if (umma::elect_one() && live) issue_pv(0, s, jj > 0);
+      if (more) {
+        live = live && mbar_wait_or_abort(&b.k_full[s1], ph1, p.err_flag, b.abort);
+        umma::fence_after_sync();
+        if (umma::elect_one() && live) {
+          issue_s(0, s1);
+          umma::commit(&b.s_full[0]);
+        }
+      }
+      // head B
+      live = live && mbar_wait_or_abort(&b.p_ready[1], jj & 1, p.err_flag, b.abort);
+      umma::fence_after_sync();
+      if (umma::elect_one() && live) {
+        issue_pv(1, s, jj > 0);
+        if (more) {
+          issue_s(1, s1);
+          umma::commit(&b.s_full[1]);
+          umma::commit(&b.k_empty[s1]);
+        }
+        umma::commit(&b.v_empty[s]);
+      }
+      __syncwarp();
+    }
+    if (umma::elect_one()) {
+      if (live) {
+        umma::commit(b.o_final);
+      } else {
+        umma::commit(b.drain);          // let issued MMAs finish before TMEM is freed
+        mbar_wait(b.drain, 0, p.err_flag);
+      }
+    }
+    __syncwarp();
+  } else {
+    // bf16: a step at a time in one thread, which waits and issues, and a vote
+    // after it; V rows to be zeroed are the whole warp's.  Chunk of 4,096 rows over
+    // 32,768 keys: 1,313 us, with every lane waiting 1,364 us.
+    auto wait = [&](uint64_t* bar, uint32_t ph) {
+      return mbar_wait_or_abort(bar, ph, p.err_flag, b.abort);
+    };
+    bool ok = true;
+    if (umma::elect_one()) {
+      ok = wait(b.q_ready, 0) && wait(&b.k_full[0], 0);
+      if (ok) {
+        umma::fence_after_sync();
+        issue_s(0, 0);
+        umma::commit(&b.s_full[0]);
+        issue_s(1, 0);
+        umma::commit(&b.s_full[1]);
+        umma::commit(&b.k_empty[0]);
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    auto step = [&](int jj) {
+      const int s = jj & 1, s1 = s ^ 1;
+      const uint32_t ph1 = ((jj + 1) >> 1) & 1;
+      const bool more = jj + 1 < gm.nkt;
+      if (!wait(&b.v_full[s], (jj >> 1) & 1) || !wait(&b.p_ready[0], jj & 1)) return false;
+      umma::fence_after_sync();
+      issue_pv(0, s, jj > 0);
+      if (more) {
+        if (!wait(&b.k_full[s1], ph1)) return false;
+        umma::fence_after_sync();
         issue_s(0, s1);
         umma::commit(&b.s_full[0]);
       }
-    }
-    // head B
-    if (!(ok = mbar_wait_or_abort(&b.p_ready[1], jj & 1, p.err_flag, b.abort))) break;
-    umma::fence_after_sync();
-    if (umma::elect_one()) {
+      if (!wait(&b.p_ready[1], jj & 1)) return false;
+      umma::fence_after_sync();
       issue_pv(1, s, jj > 0);
       if (more) {
         issue_s(1, s1);
@@ -803,18 +874,30 @@ __device__ void mma_issuer(const PrefillParams& p, const RunInfo& ru, const Tile
         umma::commit(&b.k_empty[s1]);
       }
       umma::commit(&b.v_empty[s]);
+      return true;
+    };
+    PageCheck pc(p, ru, gm, gm.kt0, gm.nkt, 1);
+    for (int jj = 0; ok && jj < gm.nkt; ++jj) {
+      const int j = gm.kt0 + jj;
+      const int z0 = v_zero_from(ru, j, pc.bad(j));
+      if (z0 < kTileKeys) {
+        if (!(ok = warp_wait_or_abort(&b.v_full[jj & 1], (jj >> 1) & 1, p.err_flag, b.abort)))
+          break;
+        zero_v_rows(smem + kOffV + (jj & 1) * 32768, z0, lane);
+      }
+      if (umma::elect_one()) ok = step(jj);
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (umma::elect_one()) {
+      if (ok) {
+        umma::commit(b.o_final);
+      } else {
+        umma::commit(b.drain);          // let issued MMAs finish before TMEM is freed
+        mbar_wait(b.drain, 0, p.err_flag);
+      }
     }
     __syncwarp();
   }
-  if (umma::elect_one()) {
-    if (ok) {
-      umma::commit(b.o_final);
-    } else {
-      umma::commit(b.drain);          // let issued MMAs finish before TMEM is freed
-      mbar_wait(b.drain, 0, p.err_flag);
-    }
-  }
-  __syncwarp();
 }
 
 // e4m3 caches: turn this thread's Q row (bf16, in the operand tile) into f16
@@ -967,7 +1050,7 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
     // slot B's take it once they see the tile ready.
     float* down_s = reinterpret_cast<float*>(smem + Layout<F16>::kOffDown);
     if (!VERIFY || hh == 0) {
-      ok = mbar_wait_or_abort(b.q_full, 0, p.err_flag, b.abort);
+      ok = warp_wait_or_abort(b.q_full, 0, p.err_flag, b.abort);
       if (ok) {
         const float down = VERIFY && KV == kKvFp8
                                ? q_row_to_e4m3_pair(smem + kOffQ, r)
@@ -979,7 +1062,7 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
         if (lane == 0) mbar_arrive(b.q_ready);
       }
     } else {
-      ok = mbar_wait_or_abort(b.q_ready, 0, p.err_flag, b.abort);
+      ok = warp_wait_or_abort(b.q_ready, 0, p.err_flag, b.abort);
       if (ok) sl2 = p.scale_log2 * down_s[r] * __ldg(p.k_scale + x.g);
     }
   }
@@ -994,9 +1077,11 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
   for (int jj = 0; ok && jj < nt; ++jj) {
     const int j = slot_tile<VERIFY>(gm, jj, hh);
     const bool page_bad = pc.bad(j);
-    if (!(ok = mbar_wait_or_abort(&b.s_full[hh], jj & 1, p.err_flag, b.abort))) break;
+    // Asked of the whole warp in the vote on the maxima below (a vote of its
+    // own here: 1.5 % of an e4m3 chunk's time)
+    const bool there = mbar_wait_or_abort(&b.s_full[hh], jj & 1, p.err_flag, b.abort);
     if (idle) {
-      __syncwarp();
+      if (!(ok = __all_sync(0xffffffffu, there))) break;
       if (lane == 0) mbar_arrive(&b.p_ready[hh]);
       continue;
     }
@@ -1068,7 +1153,9 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
     const float rs = acc.x + acc.y;
     umma::tmem_st32(tS, sv[0]);
     umma::tmem_st32(tS + 32, sv[1]);
-    if (jj > 0 && __any_sync(0xffffffffu, resc)) {     // O *= alpha in TMEM
+    if (__any_sync(0xffffffffu, (jj > 0 && resc) || !there)) {
+      if (!(ok = __all_sync(0xffffffffu, there))) break;
+      // O *= alpha in TMEM
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
@@ -1085,7 +1172,7 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
     __syncwarp();
     if (lane == 0) mbar_arrive(&b.p_ready[hh]);
   }
-  if (ok) ok = mbar_wait_or_abort(b.o_final, 0, p.err_flag, b.abort);
+  if (ok) ok = warp_wait_or_abort(b.o_final, 0, p.err_flag, b.abort);
   if (ok) umma::fence_after_sync();
 
   if (VERIFY) {
@@ -1104,9 +1191,8 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
     if (hh == 1) {
       if (mine) ml_s[v] = make_float2(m_run, l);
       // tcgen05.ld is warp-wide: the condition is the same for every lane
-      // (mine and nt are per warp), and only the stores follow `valid`
-      const bool wok = __all_sync(0xffffffffu, ok);
-      if (half && mine && nt > 0 && wok) {
+      // (mine, nt and ok are per warp), and only the stores follow `valid`
+      if (half && mine && nt > 0 && ok) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
@@ -1126,7 +1212,7 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
     }
     __syncwarp();
     named_bar_sync(1, 256);
-    if (hh == 1 || !__all_sync(0xffffffffu, ok)) return;
+    if (hh == 1 || !ok) return;
     const float2 mlb = ml_s[v];
     const float mx = fmaxf(m_run, mlb.x);
     const float a0 = m_run == -INFINITY ? 0.f : fast_exp2(m_run - mx);
@@ -1188,7 +1274,7 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
     // Store (m, l, O) into CTA 0 once its rings are free; arrive on its
     // barrier whatever happened, so that it never waits out the time limit
     // on this CTA's account.
-    const bool free = mbar_wait_cluster(b.dst_free, 0, p.err_flag);
+    const bool free = warp_wait_cluster(b.dst_free, 0, p.err_flag);
     if (ok && free) {
       const uint32_t orow = mapa_shared(part_o_row(sbase, hh, r), 0);
 #pragma unroll
@@ -1210,7 +1296,7 @@ __device__ void softmax_role(const PrefillParams& p, const RunInfo& ru, const Ti
   // CTA 0: its MMAs are done (or it gave up), so CTA 1 may store into the
   // rings.  Then merge CTA 1's half into this one, normalise, write.
   if (threadIdx.x == 128) mbar_arrive_remote(mapa_shared(smem_u32(b.dst_free), 1));
-  const bool peer = mbar_wait_cluster(b.peer_ready, 0, p.err_flag);
+  const bool peer = warp_wait_cluster(b.peer_ready, 0, p.err_flag);
   if (!ok || !peer) return;
   float2 ml1;
   asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(ml1.x), "=f"(ml1.y)

@@ -70,3 +70,38 @@ def test_no_thread_leaves_its_role_alone(name):
         src = strip(f.read())
     bad = [(line, s) for line, s, h in statements(src) if re.search(r"\bgoto\b", s) and alone(s, h)]
     assert not bad, bad
+
+
+# functions, and functions' local ones, that one thread runs
+ONE_THREAD = {"prefill.cu": r"\bproducer\(|auto wait = ", "mass.cu": None}
+WAIT = re.compile(r"\bmbar_wait\w*\s*(<[^;()]*>)?\(")
+LEAVES = re.compile(r"\b(return|break|goto|continue)\b")
+
+
+def lane_by_lane(text):
+    """Does every lane take its own answer and none leaves on it?  Either it is dropped (a bare call: *abort is read
+    afterwards), or kept in `live` or `there`, on which nothing leaves but by a vote."""
+    text = re.sub(r"^(else )?if \(.*\) (?=mbar_wait)", "", text)
+    return bool(re.match(r"(mbar_wait|(bool )?live = |const bool there = )", text))
+
+
+@pytest.mark.parametrize("name", sorted(ONE_THREAD))
+def test_a_warp_waits_as_one(name):
+    """mbar_wait and its like give each lane an answer of its own: for one thread, or for lanes that stay together
+    whatever it is.  Elsewhere a warp's wait is warp_wait."""
+    with open(os.path.join(CSRC, name)) as f:
+        src = strip(f.read())
+    seen, bad = 0, []
+    for line, s, h in statements(src):
+        if WAIT.search(s):
+            seen += 1
+            one = ONE_THREAD[name] and any(re.search(ONE_THREAD[name], x) for x in h)
+            if not (one or alone(s, h) or lane_by_lane(s)):
+                bad.append((line, s))
+        # no lane leaves, and no loop ends, on its own answer
+        at = re.sub(r"__(all|any)_sync\([^;]*\)", "", s)
+        if re.search(r"\b(live|there)\b", at) and (LEAVES.search(at) or re.match(r"(for|while)\b", at)):
+            bad.append((line, s))
+        if re.search(r"\b(live|there|gave_up)\b", " ".join(h[-1:])) and LEAVES.search(s) and "_sync" not in h[-1]:
+            bad.append((line, s))
+    assert seen and not bad, bad
