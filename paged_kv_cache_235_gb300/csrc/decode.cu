@@ -794,6 +794,7 @@ __device__ void consumer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
   uint32_t qr[2][16];
   int maxlim = -1, minlim = -1;
   int tree_low = INT_MAX;     // keys from here on may be hidden by an ancestor mask
+  bool ready = false;         // 4 bits: the next chunk's stage was seen to be full
 
   Item x{};
   for (int it = ib; it < ie; ++it) {
@@ -834,7 +835,14 @@ __device__ void consumer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
       const uint32_t st = chunk * C::kSub + sub0 / C::kSubWarps;
       const int buf = st % C::kStages;
       const uint32_t ph = (st / C::kStages) & 1;
-      if (!mbar_wait(&full[buf], ph, p.err_flag)) return;
+      if (C::kFp4) {
+        // as in the kernel of eight-vector items: looked at a chunk ahead, so
+        // that the warp's agreement is all that is left on the path
+        if (!__all_sync(0xffffffffu, ready) && !warp_wait(&full[buf], ph, p.err_flag)) return;
+        ready = mbar_test_wait(&full[(st + 1) % C::kStages], ((st + 1) / C::kStages) & 1);
+      } else if (!warp_wait(&full[buf], ph, p.err_flag)) {
+        return;
+      }
       const uint32_t sb = sbase + (uint32_t)buf * C::kStageBytes;
       const int wk0 = sub0 * C::kKeysPerWarp;
       const int r0 = wk0 - (sub0 / C::kSubWarps) * C::kStageKeys;
@@ -861,7 +869,7 @@ __device__ void consumer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
     const int rel = it - ib;
     const int b = rel & 1;
     if (rel >= 2 &&
-        !mbar_wait(&bars.tmem_free[b], (uint32_t)((rel >> 1) - 1) & 1u, p.err_flag))
+        !warp_wait(&bars.tmem_free[b], (uint32_t)((rel >> 1) - 1) & 1u, p.err_flag))
       return;
     umma::fence_after_sync();
     const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16) +
@@ -950,13 +958,16 @@ __device__ __forceinline__ void merge_vector(const float* part_o, const float* p
 // merges the group's query vectors, warp 8+q taking vectors q, q+4, ...
 // Every thread fences its partial stores before the count, and the merging
 // threads fence after it and load the partials through L2.
+// ok: no wait of this warp has given up; a warp without takes part in the
+// two barriers, which count on all four, and in nothing else.
 template <int KV, int WARP0>
 __device__ __forceinline__ void merge_if_last(const DecodeParams& p, const RunInfo& ru,
-                                              const Item& x, int nq, int* merge_flag) {
+                                              const Item& x, int nq, int* merge_flag, bool ok) {
   const int q = (threadIdx.x >> 5) - WARP0;
   __threadfence();
   named_bar_sync(1, 32 * kCombineWarps);
-  if (threadIdx.x == 32 * WARP0) {
+  if (threadIdx.x == 32 * WARP0 && !ok) *merge_flag = 0;
+  if (threadIdx.x == 32 * WARP0 && ok) {
     const int qv0 = x.mt * Cfg<KV>::kVecs;
     const int r0 = qv0 / p.group;
     uint32_t* ctr = p.arrive + (size_t)(ru.row0 + r0) * p.hq + x.g * p.group + (qv0 - r0 * p.group);
@@ -966,7 +977,7 @@ __device__ __forceinline__ void merge_if_last(const DecodeParams& p, const RunIn
     *merge_flag = last;
   }
   named_bar_sync(1, 32 * kCombineWarps);
-  if (!*merge_flag) return;
+  if (!*merge_flag || !ok) return;
   __threadfence();
   for (int j = q; j < Cfg<KV>::kVecs; j += kCombineWarps) {
     const int qv = x.mt * Cfg<KV>::kVecs + j;
@@ -1000,20 +1011,13 @@ __device__ void combiner(const DecodeParams& p, const DecodeDyn& D, uint32_t tme
   cta_items(D, ib, ie);
   int rh = ib < ie ? run_of(D, ib) : 0;   // run of the current item
   const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
-  Item x{};
-  for (int it = ib; it < ie; ++it) {
-    if (Cfg<KV>::kFp4 && it > ib)
-      next_item<KV>(p, D, x);
-    else
-      x = item_of<KV>(p, D, it, rh);
-    const RunInfo& ru = D.runs[x.run];
-    const int nq = ru.nrows * p.group;
-    const int rel = it - ib;
+  // One item; false if a wait gave up.
+  auto fold_item = [&](const Item& x, const RunInfo& ru, int nq, int rel) {
     const int b = rel & 1;
     const uint32_t par = (uint32_t)rel & 1u;
-    if (!mbar_wait<Cfg<KV>::kFp4 ? 128 : 0>(&bars.posted[b], (uint32_t)(rel >> 1) & 1u,
+    if (!warp_wait<Cfg<KV>::kFp4 ? 128 : 0>(&bars.posted[b], (uint32_t)(rel >> 1) & 1u,
                                             p.err_flag))
-      return;
+      return false;
     umma::fence_after_sync();
     const uint32_t tA = tl + (uint32_t)(b * kBufCols);          // consumer warp q
     const uint32_t tB = tA + kHalfCols;                          // consumer warp q + 4
@@ -1021,7 +1025,7 @@ __device__ void combiner(const DecodeParams& p, const DecodeDyn& D, uint32_t tme
     umma::tmem_ld4(tA + 64, mlA);
     umma::tmem_ld4(tB + 64, mlB);
     umma::tmem_ld_wait();
-    if (rel > 0 && !mbar_wait(bars.done, par ^ 1u, p.err_flag)) return;
+    if (rel > 0 && !warp_wait(bars.done, par ^ 1u, p.err_flag)) return false;
     if (c == 0) {
 #pragma unroll
       for (int hr = 0; hr < 2; ++hr) {
@@ -1034,7 +1038,7 @@ __device__ void combiner(const DecodeParams& p, const DecodeDyn& D, uint32_t tme
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bars.pub);
-    if (!mbar_wait(bars.pub, par, p.err_flag)) return;
+    if (!warp_wait(bars.pub, par, p.err_flag)) return false;
     float M[2], aA[2], aB[2];
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
@@ -1070,7 +1074,7 @@ __device__ void combiner(const DecodeParams& p, const DecodeDyn& D, uint32_t tme
       mbar_arrive(&bars.tmem_free[b]);
       mbar_arrive(bars.folded);
     }
-    if (!mbar_wait(bars.folded, par, p.err_flag)) return;
+    if (!warp_wait(bars.folded, par, p.err_flag)) return false;
     // final: n-tiles 4q..4q+3 of this lane's fragment, summed over the slots
     {
       float4 acc[4];
@@ -1123,7 +1127,22 @@ __device__ void combiner(const DecodeParams& p, const DecodeDyn& D, uint32_t tme
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bars.done);
-    if constexpr (MERGE) merge_if_last<KV, kCombineWarp0>(p, ru, x, nq, merge_flag);
+    return true;
+  };
+  Item x{};
+  bool ok = true;
+  for (int it = ib; it < ie; ++it) {
+    if (Cfg<KV>::kFp4 && it > ib)
+      next_item<KV>(p, D, x);
+    else
+      x = item_of<KV>(p, D, it, rh);
+    const RunInfo& ru = D.runs[x.run];
+    const int nq = ru.nrows * p.group;
+    ok = ok && fold_item(x, ru, nq, it - ib);
+    if constexpr (MERGE)
+      merge_if_last<KV, kCombineWarp0>(p, ru, x, nq, merge_flag, ok);
+    else if (!ok)
+      return;
   }
 }
 
@@ -1577,13 +1596,11 @@ __device__ void combiner_fp4(const DecodeParams& p, const DecodeDyn& D, uint32_t
   int rh = run_of(D, ib);
   Item x = item_of<KV>(p, D, ib, rh);
   const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
-  for (int it = ib; it < ie; ++it, next_item<KV>(p, D, x)) {
-    const RunInfo& ru = D.runs[x.run];
-    const int nq = ru.nrows * p.group;
-    const int rel = it - ib;
+  // One item; false if a wait gave up.
+  auto fold_item = [&](const Item& x, const RunInfo& ru, int nq, int rel) {
     const int b = rel & 1;
     const uint32_t par = (uint32_t)rel & 1u;
-    if (!warp_wait<128>(&bars.posted[b], (uint32_t)(rel >> 1) & 1u, p.err_flag)) return;
+    if (!warp_wait<128>(&bars.posted[b], (uint32_t)(rel >> 1) & 1u, p.err_flag)) return false;
     umma::fence_after_sync();
     const uint32_t t0 = tl + (uint32_t)(b * kBufCols4);
     const float* ml = ml_buf + b * kMlFloats4;
@@ -1611,7 +1628,7 @@ __device__ void combiner_fp4(const DecodeParams& p, const DecodeDyn& D, uint32_t
         L += (t.x == -INFINITY ? 0.f : fast_exp2(t.x - Mq)) * t.y;
       }
     }
-    if (rel > 0 && !warp_wait(bars.done, par ^ 1u, p.err_flag)) return;
+    if (rel > 0 && !warp_wait(bars.done, par ^ 1u, p.err_flag)) return false;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       float acc[16];
@@ -1639,7 +1656,7 @@ __device__ void combiner_fp4(const DecodeParams& p, const DecodeDyn& D, uint32_t
       mbar_arrive(&bars.tmem_free[b]);
       mbar_arrive(bars.folded);
     }
-    if (!warp_wait(bars.folded, par, p.err_flag)) return;
+    if (!warp_wait(bars.folded, par, p.err_flag)) return false;
     {
       float4 acc[2];
 #pragma unroll
@@ -1672,7 +1689,17 @@ __device__ void combiner_fp4(const DecodeParams& p, const DecodeDyn& D, uint32_t
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bars.done);
-    if constexpr (MERGE) merge_if_last<KV, kCombineWarp4>(p, ru, x, nq, merge_flag);
+    return true;
+  };
+  bool ok = true;
+  for (int it = ib; it < ie; ++it, next_item<KV>(p, D, x)) {
+    const RunInfo& ru = D.runs[x.run];
+    const int nq = ru.nrows * p.group;
+    ok = ok && fold_item(x, ru, nq, it - ib);
+    if constexpr (MERGE)
+      merge_if_last<KV, kCombineWarp4>(p, ru, x, nq, merge_flag, ok);
+    else if (!ok)
+      return;
   }
 }
 

@@ -73,7 +73,7 @@ def test_no_thread_leaves_its_role_alone(name):
 
 
 # functions, and functions' local ones, that one thread runs
-ONE_THREAD = {"prefill.cu": r"\bproducer\(|auto wait = ", "mass.cu": None}
+ONE_THREAD = {"prefill.cu": r"\bproducer\(|auto wait = ", "decode.cu": r"\bload_item\(", "mass.cu": None}
 WAIT = re.compile(r"\bmbar_wait\w*\s*(<[^;()]*>)?\(")
 LEAVES = re.compile(r"\b(return|break|goto|continue)\b")
 
