@@ -550,10 +550,11 @@ int tfpa_key_mass(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg, c
  * -1 in [keep[s], seq_len).  The stream goes on with seq_len = keep[s]: its
  * next row is stored at that slot, with its own rotary position.
  *   key_pos : DEVICE int32 [nseg][hkv][mass_cap], the position that each
- *             slot's key has in its stream; NULL: its slot.  Only read and
- *             moved here: the caller writes a new row's entry.
- *   next_pos: HOST int32[nseg], the position the stream's next row will have;
- *             NULL: seq_len.
+ *             slot's key has in its stream, all different; NULL: its slot.  Only
+ *             read and moved here: the caller writes a new row's entry.
+ *   next_pos: HOST int32[nseg], the position the stream's next row will have,
+ *             at least seq_len (TFPA_ERANGE); NULL: seq_len without key_pos,
+ *             else one past the largest position among the kv head's slots.
  *   sink, recent >= 0, with sink + recent <= keep[s] where keep[s] < seq_len
  *             (TFPA_EINVAL).
  *   mass    : as tfpa_key_mass, 16-byte aligned like key_pos; mass_cap a

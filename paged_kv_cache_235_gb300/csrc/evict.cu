@@ -123,7 +123,22 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(
   const int chunk = select_chunk(L, nb);
   const int lo = min(L, rank * chunk), hi = min(L, lo + chunk);
   const bool kept = chunk <= p.key_slots;
-  const int guard_from = sg.next_pos - p.recent;
+  int next_pos = sg.next_pos;
+  if (next_pos == kNextPosHeld) {       // the largest position that a slot holds, plus one
+    int most = -1;
+    for (int j = lo + tid; j < hi; j += kSelThreads) most = max(most, pos[j]);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) sh.warp_s[tid >> 5] = (uint32_t)most;
+    __syncthreads();
+    most = __reduce_max_sync(0xffffffffu, (int)sh.warp_s[lane]);
+    if (tid == 0) sh.count[0] = (uint32_t)most;
+    sync();
+    for (int r = 0; CLUSTER && r < nb; ++r)
+      most = max(most, (int)ld_cluster_u32(mapa_shared(smem_u32(&sh.count[0]), r)));
+    sync();                             // read, before count or warp_s is written again
+    next_pos = most + 1;
+  }
+  const int guard_from = next_pos - p.recent;
   // Keys of slots j .. j + 3 (j a multiple of 4; 0, which no key is, from hi
   // on).  mass_cap is a multiple of 4, so the reads stay within the plane.
   auto make_keys = [&](int j) {

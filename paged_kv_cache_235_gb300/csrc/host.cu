@@ -1489,7 +1489,8 @@ extern "C" int tfpa_evict_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t 
     return TFPA_EINVAL;
   for (int32_t s = 0; s < nseg; ++s) {
     if (keep[s] < 1 || keep[s] > segs[s].seq_len) return TFPA_ERANGE;
-    if (next_pos && next_pos[s] < 0) return TFPA_ERANGE;
+    // seq_len keys at positions of their own, all below the next
+    if (next_pos && next_pos[s] < segs[s].seq_len) return TFPA_ERANGE;
     if (segs[s].seq_len > mass_cap) return TFPA_ECAPACITY;
     if (keep[s] < segs[s].seq_len && (int64_t)sink + recent > keep[s]) return TFPA_EINVAL;
   }
@@ -1512,7 +1513,7 @@ extern "C" int tfpa_evict_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t 
       v.index = s0 + i;
       v.seq_len = g.seq_len;
       v.keep = keep[s0 + i];
-      v.next_pos = next_pos ? next_pos[s0 + i] : g.seq_len;
+      v.next_pos = next_pos ? next_pos[s0 + i] : key_pos ? kNextPosHeld : g.seq_len;
       v.slab_cap = g.slab_cap;
       most = std::max(most, std::min(v.keep, v.seq_len - v.keep));
       if (v.keep < v.seq_len) longest = std::max(longest, v.seq_len);

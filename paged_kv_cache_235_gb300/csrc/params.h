@@ -294,6 +294,7 @@ constexpr int32_t kSelectKeys = 49152;   // order keys that a select block's sha
 __host__ __device__ inline int32_t select_chunk(int32_t seq_len, int32_t blocks) {
   return (int32_t)((((int64_t)seq_len + blocks - 1) / blocks + 127) & ~(int64_t)127);
 }
+constexpr int32_t kNextPosHeld = -1;     // next_pos: one past the largest key_pos held
 struct EvictSeg {
   const int32_t* page_table;  // nullptr => slab
   void* k_base;               // pool or slab
