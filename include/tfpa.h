@@ -551,7 +551,9 @@ int tfpa_key_mass(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg, c
  * next row is stored at that slot, with its own rotary position.
  *   key_pos : DEVICE int32 [nseg][hkv][mass_cap], the position that each
  *             slot's key has in its stream, all different; NULL: its slot.  Only
- *             read and moved here: the caller writes a new row's entry.
+ *             read and moved here: the caller writes a new row's entry.  A
+ *             negative entry is no position: neither among the first nor among
+ *             the last ones.
  *   next_pos: HOST int32[nseg], the position the stream's next row will have,
  *             at least seq_len (TFPA_ERANGE); NULL: seq_len without key_pos,
  *             else one past the largest position among the kv head's slots.

@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(
     int4 at = make_int4(j, j + 1, j + 2, j + 3);
     if (pos) at = *reinterpret_cast<const int4*>(pos + j);
     auto one = [&](float x, int a, int i) {
-      return i < hi ? order_key(x, a < p.sink || a >= guard_from) : 0u;
+      // (a negative position, a slot whose entry is not written, is neither)
+      return i < hi ? order_key(x, a >= 0 && (a < p.sink || a >= guard_from)) : 0u;
     };
     return make_uint4(one(m.x, at.x, j), one(m.y, at.y, j + 1), one(m.z, at.z, j + 2),
                       one(m.w, at.w, j + 3));

@@ -1,5 +1,5 @@
 """Eviction with positions of the slots' own: which keys count as the first and the last ones when the call gives
-no next_pos.  Against a sort in 64 bits."""
+no next_pos, and when a slot's position has not been written.  Against a sort in 64 bits."""
 
 import numpy as np
 import pytest
@@ -15,7 +15,7 @@ pytestmark = pytest.mark.gpu
 def want(mass, pos, L, n, sink, recent):
     """Slots that fill the first n, of one kv head; the last positions are those up to the largest that is held."""
     m, p = mass[:L].astype(np.float64), pos[:L]
-    guard = (p < sink) | (p >= p.max() + 1 - recent)
+    guard = ((p >= 0) & (p < sink)) | (p >= p.max() + 1 - recent)
     stays = np.zeros(L, bool)
     stays[np.lexsort((np.arange(L), -m, ~guard))[:n]] = True
     take = np.arange(n)
@@ -51,3 +51,16 @@ def test_a_later_cut_without_next_pos(lengths):
             pos[s, g, :L] = rng.permutation(np.sort(rng.choice(4 * L, L, replace=False)))
     keep = np.array([max(4, L // 2) for L in lengths], np.int32)
     check(c, keep, mass, pos, sink=2, recent=2)
+
+
+@pytest.mark.parametrize("sink,recent", [(4, 0), (4, 16), (0, 1)])
+def test_slots_without_a_position_are_not_protected(sink, recent):
+    """-1: a row whose entry the caller has not written yet.  Its weight alone decides."""
+    c = Fp4Case([500], [True], 4, 2, seed=96).upload()
+    mass = masses(c, 6)
+    pos = np.broadcast_to(np.arange(mass.shape[2], dtype=np.int32), mass.shape).copy()
+    pos[:, :, 200:230] = -1
+    mass[:, :, 200:215] = 0                                      # goes
+    mass[:, :, 215:230] = 1e6                                    # stays
+    gp = check(c, np.array([250], np.int32), mass, pos, sink, recent)
+    assert (np.count_nonzero(gp[0, :, :250] == -1, axis=1) == 15).all()
