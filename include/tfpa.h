@@ -564,8 +564,9 @@ int tfpa_key_mass(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg, c
  *   moves   : DEVICE int32 [nseg][hkv][mass_cap + 4], 16-byte aligned, written:
  *             [0] the number m of rows moved, and from [4] on m pairs (from
  *             slot, to slot), for whoever keeps more per key than this cache.
- * A pair on a page whose id is out of range leaves its K and V rows and ORs 1
- * into cache->err_flag.  Two segments of a call must not share pages, and a
+ * A pair on a page whose id is out of range leaves both slots' K and V rows,
+ * mass and key_pos as they are and ORs 1 into cache->err_flag (moves lists it).
+ * Two segments of a call must not share pages, and a
  * stream that goes on reading a page must not share it with one that is cut. */
 int tfpa_evict_kv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
                   const int32_t* keep, const int32_t* next_pos, int32_t sink, int32_t recent,

@@ -376,7 +376,8 @@ struct MoveRow {
 };
 
 // Blocks: grid_x per (segment, kv head).  A pair on a page whose id is
-// out of range is skipped and flagged.
+// out of range is skipped and flagged: its rows stay, and its weights and
+// positions with them.
 template <int KV>
 __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(
     const __grid_constant__ EvictParams p) {
@@ -397,10 +398,14 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(
   const int sub = lane / (2 * Row::kLanes), t = lane % Row::kLanes;
   const bool is_v = lane / Row::kLanes & 1;
   uint8_t* base = static_cast<uint8_t*>(is_v ? sg.v_base : sg.k_base);
-  auto row_of = [&](int slot, bool& ok) -> size_t {
-    if (!sg.page_table) return (size_t)g * sg.slab_cap + slot;
+  auto page_of = [&](int slot, bool& ok) {
     const int pid = __ldg(sg.page_table + (slot >> 8));
     ok = ok && (unsigned)pid < (unsigned)p.num_pages;
+    return pid;
+  };
+  auto row_of = [&](int slot, bool& ok) -> size_t {
+    if (!sg.page_table) return (size_t)g * sg.slab_cap + slot;
+    const int pid = page_of(slot, ok);
     return ((size_t)pid * p.hkv + g) * kPage + (slot & (kPage - 1));
   };
   // A warp takes pairs in batches, every one's row on its way before the
@@ -410,11 +415,18 @@ __global__ void __launch_bounds__(32 * kMoveWarps) move_kernel(
        i0 += p.grid_x * kMoveWarps * kBatch) {
     if (lane < kBatch && i0 + lane < count) {   // weights and positions: a lane a pair
       const int2 m = *reinterpret_cast<const int2*>(moves + 4 + 2 * (i0 + lane));
-      mass[m.y] = mass[m.x];
-      mass[m.x] = 0.f;
-      if (pos) {
-        pos[m.y] = pos[m.x];
-        pos[m.x] = -1;
+      bool ok = true;
+      if (sg.page_table) {
+        page_of(m.x, ok);
+        page_of(m.y, ok);
+      }
+      if (ok) {
+        mass[m.y] = mass[m.x];
+        mass[m.x] = 0.f;
+        if (pos) {
+          pos[m.y] = pos[m.x];
+          pos[m.x] = -1;
+        }
       }
     }
     Row row[kSteps];
