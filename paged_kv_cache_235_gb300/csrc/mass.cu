@@ -109,8 +109,11 @@ __device__ __forceinline__ void pass_span(const MassParams& p, const MassSeg& sg
 }
 
 // Query vectors [v0, v0 + nv) as the B operand ([n rows][2 halves of 64],
-// 128B swizzle; rows from nv on zero) with each one's -lse and position; all
-// warps but the producer's, 16 threads a vector.  Returns the scores' factor.
+// 128B swizzle) with each one's -lse and position; all warps but the
+// producer's, 16 threads a vector.  Rows from nv on repeat the first vector
+// with -lse = -inf: a weight of 0 by any key that gives the first one a finite
+// weight or 0, an infinite key among them, where zeros would give a NaN.  Returns the
+// scores' factor.
 template <int KV>
 __device__ float stage_q(const MassParams& p, const MassSeg& sg, int g, int v0, int nv, int n,
                          uint8_t* smem, int* amax_s) {
@@ -131,12 +134,13 @@ __device__ float stage_q(const MassParams& p, const MassSeg& sg, int g, int v0, 
       w[u] = make_uint4(0, 0, 0, 0);
       lim[u] = -1;
       neg[u] = INFINITY;
-      if (i >= nv) continue;
-      int row, head;
-      find_vector(p, sg, v0 + i, row, lim[u], head);
+      if (i >= n) continue;
+      int row, head, pos;
+      find_vector(p, sg, i < nv ? v0 + i : v0, row, pos, head);
       const size_t rh = (size_t)row * p.hq + g * p.group + head;
       w[u] = __ldg(reinterpret_cast<const uint4*>(p.q + rh * kHeadDim) + t);
       neg[u] = __ldg(p.lse + rh);
+      if (i < nv) lim[u] = pos;
     }
   };
   float up = 1.f, sc = p.scale_log2;
