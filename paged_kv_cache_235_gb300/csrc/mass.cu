@@ -78,6 +78,7 @@ struct MassBars {
   volatile int* abort;
   int* amax;                     // [2], by pass parity: largest |q| of the pass (its bits)
   int* stop;                     // [2], by pass parity: a wait has given up
+  int* none;                     // [2], by pass parity: a row of the pass saw no key
 };
 
 // Vector v of segment sg: its run and row.
@@ -112,11 +113,12 @@ __device__ __forceinline__ void pass_span(const MassParams& p, const MassSeg& sg
 // 128B swizzle) with each one's -lse and position; all warps but the
 // producer's, 16 threads a vector.  Rows from nv on repeat the first vector
 // with -lse = -inf: a weight of 0 by any key that gives the first one a finite
-// weight or 0, an infinite key among them, where zeros would give a NaN.  Returns the
-// scores' factor.
+// weight or 0, an infinite key among them, where zeros would give a NaN.  A row
+// that saw no key (lse -inf) becomes zeros, whatever its q holds, and *none_s
+// says that there is one.  Returns the scores' factor.
 template <int KV>
 __device__ float stage_q(const MassParams& p, const MassSeg& sg, int g, int v0, int nv, int n,
-                         uint8_t* smem, int* amax_s) {
+                         uint8_t* smem, int* amax_s, int* none_s) {
   using C = MassCfg<KV>;
   constexpr int kStep = (C::kThreads - 32) / 16;
   const uint32_t qb = smem_u32(smem + C::kOffQ);
@@ -141,6 +143,20 @@ __device__ float stage_q(const MassParams& p, const MassSeg& sg, int g, int v0, 
       w[u] = __ldg(reinterpret_cast<const uint4*>(p.q + rh * kHeadDim) + t);
       neg[u] = __ldg(p.lse + rh);
       if (i < nv) lim[u] = pos;
+    }
+    // all loads are on their way by now
+    i -= kBatch * kStep;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u, i += kStep) {
+      if (neg[u] == -INFINITY) {
+        w[u] = make_uint4(0, 0, 0, 0);
+        lim[u] = -1;
+        *none_s = 1;
+      }
+      if (t == 0 && i < n) {
+        negs[i] = lim[u] < 0 ? -INFINITY : -neg[u] * 1.4426950408889634f;
+        lims[i] = lim[u];
+      }
     }
   };
   float up = 1.f, sc = p.scale_log2;
@@ -184,11 +200,6 @@ __device__ float stage_q(const MassParams& p, const MassSeg& sg, int g, int v0, 
       asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
                        swz128(qb + (uint32_t)(t >> 3) * (uint32_t)n * 128u, i, t & 7)),
                    "r"(e[0]), "r"(e[1]), "r"(e[2]), "r"(e[3]) : "memory");
-      if (t == 0) {
-        // a row without keys has lse -inf and gives no weight
-        negs[i] = i >= nv || neg[u] == -INFINITY ? -INFINITY : -neg[u] * 1.4426950408889634f;
-        lims[i] = lim[u];
-      }
     }
   }
   fence_proxy_async_smem();
@@ -261,6 +272,7 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
   b.abort = reinterpret_cast<volatile int*>(b.tmem_slot + 1);
   b.amax = reinterpret_cast<int*>(b.tmem_slot + 2);
   b.stop = b.amax + 2;
+  b.none = b.stop + 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -320,14 +332,18 @@ __global__ void __launch_bounds__(MassCfg<KV>::kThreads, 1)
         // words may still be read)
         if (threadIdx.x == 32) {
           b.amax[pass & 1] = 0;
+          b.none[pass & 1] = 0;
           b.stop[pass & 1] = *b.abort;
         }
         __syncwarp();
         named_bar_sync(2, C::kThreads - 32);
         if (b.stop[pass & 1]) goto out;
-        sc = stage_q<KV>(p, sg, g, v0, nv, n, smem, b.amax + (pass & 1));
+        sc = stage_q<KV>(p, sg, g, v0, nv, n, smem, b.amax + (pass & 1), b.none + (pass & 1));
         __syncwarp();
         named_bar_sync(2, C::kThreads - 32);
+        // a row that saw no key: every tile's limits are looked at, as a key
+        // that is not finite has no finite product with its zeros
+        if (b.none[pass & 1]) minlim = -1;
       }
       if (warp == 0) {
         bool ok = true;

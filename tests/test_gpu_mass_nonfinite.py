@@ -37,3 +37,21 @@ def test_mass_of_an_infinite_key(hq, hkv, rows):
     ref, tol = mass64(c, q, lse, rs, rp, np.zeros((1, hkv, 304), np.float32), 0.0, 304)
     ref[0, :, key] = 0
     F.assert_within(m, ref, tol + 1e-300, "other keys")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("bits", [0x7FC0, 0x7F80, 0x7E00])
+@pytest.mark.parametrize("none", [0, 1])
+def test_mass_of_rows_that_saw_no_key_whatever_their_query_holds(kv, bits, none):
+    """lse = -inf adds nothing: the same bytes with a query of NaN, of infinity or of 2^125 in that row as with
+    zeros, for the call's other rows too."""
+    c = make(kv, [400], [True], 8, 2, seed=92)
+    q, lse = c.q(3), np.full((3, 8), 4.0, np.float32)
+    lse[none] = -np.inf
+    rs, rp = np.zeros(3, int), np.array([397, 398, 399])
+    old = np.ones((1, 2, 400), np.float32)
+    q[none] = 0
+    want = run_mass(c, q, lse, rs, rp, old, 0.5)
+    q[none] = bits
+    got = run_mass(c, q, lse, rs, rp, old, 0.5)
+    assert torch.isfinite(want).all() and torch.equal(got, want)
