@@ -525,7 +525,9 @@ int tfpa_prefill(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
  * bytes are too.
  *   q    : DEVICE bf16 [rows][hq][128], 16-byte aligned (any memory the GPU
  *          can read); lse: DEVICE float [rows][hq] (a row with lse = -inf adds
- *          nothing).
+ *          nothing, whatever its q holds).  Over an e4m3 or 4-bit cache up to
+ *          256 query vectors of a kv head are taken in f16 under one power of
+ *          two: exact within 2^30 of their largest finite element.
  *   mass : DEVICE float [nseg][hkv][mass_cap], planes by the segment's index
  *          in the call; zero before a stream's first call.  Entries from
  *          seq_len on, and segments without rows, are left as they are.

@@ -163,23 +163,40 @@ __device__ float stage_q(const MassParams& p, const MassSeg& sg, int g, int v0, 
   if (C::kF16) {
     // the pass's largest magnitude goes to [2^13, 2^14)
     load_batch(i0);
-    float amax = 0.f;
+    // The largest of the batch's magnitudes up to `top` (a NaN is none), over
+    // all threads, in *amax_s.
+    auto largest = [&](float top) {
+      float amax = 0.f;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const uint32_t e[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      for (int u = 0; u < kBatch; ++u) {
+        const uint32_t e[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        amax = fmaxf(amax, fabsf(__uint_as_float(e[j] << 16)));
-        amax = fmaxf(amax, fabsf(__uint_as_float(e[j] & 0xFFFF0000u)));
+        for (int j = 0; j < 4; ++j) {
+          const float lo = fabsf(__uint_as_float(e[j] << 16));
+          const float hi = fabsf(__uint_as_float(e[j] & 0xFFFF0000u));
+          amax = fmaxf(amax, top == INFINITY || lo <= top ? lo : 0.f);
+          amax = fmaxf(amax, top == INFINITY || hi <= top ? hi : 0.f);
+        }
       }
+      __syncwarp();
+      const int most = __reduce_max_sync(0xffffffffu, __float_as_int(amax));   // not negative
+      if ((threadIdx.x & 31) == 0) atomicMax(amax_s, most);
+      __syncwarp();
+      named_bar_sync(2, C::kThreads - 32);
+      return __int_as_float(*amax_s);
+    };
+    float amax = largest(INFINITY);
+    if (amax == INFINITY) {
+      // an infinity stays one in f16 and sets no other row's scale: the
+      // largest finite magnitude instead, in the same word
+      named_bar_sync(2, C::kThreads - 32);
+      if (threadIdx.x == 32) *amax_s = 0;
+      __syncwarp();
+      named_bar_sync(2, C::kThreads - 32);
+      amax = largest(__uint_as_float(0x7F7F0000u));     // bf16's largest number
     }
-    __syncwarp();
-    const int most = __reduce_max_sync(0xffffffffu, __float_as_int(amax));   // not negative
-    if ((threadIdx.x & 31) == 0) atomicMax(amax_s, most);
-    __syncwarp();
-    named_bar_sync(2, C::kThreads - 32);
     int ex;
-    frexpf(__int_as_float(*amax_s), &ex);
+    frexpf(amax, &ex);
     ex = max(min(ex, 120), -100);
     up = __int_as_float((127 + 14 - ex) << 23);
     sc = p.scale_log2 * __int_as_float((127 - 14 + ex) << 23) * __ldg(p.k_scale + g);

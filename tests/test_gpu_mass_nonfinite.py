@@ -55,3 +55,18 @@ def test_mass_of_rows_that_saw_no_key_whatever_their_query_holds(kv, bits, none)
     q[none] = bits
     got = run_mass(c, q, lse, rs, rp, old, 0.5)
     assert torch.isfinite(want).all() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("bits", [0x7FC0, 0x7F80])
+def test_mass_of_a_query_that_is_not_finite_stays_with_its_keys(kv, bits):
+    """A row at position 100 whose query is not finite spoils keys 0 to 100 at most: the keys behind it keep the
+    later row's weights."""
+    c = make(kv, [400], [True], 8, 2, seed=93)
+    q, lse = c.q(2, 8.0), np.full((2, 8), 30.0, np.float32)
+    rs, rp = np.zeros(2, int), np.array([100, 399])
+    old = np.zeros((1, 2, 400), np.float32)
+    q[0, :, 3] = bits
+    got = run_mass(c, q, lse, rs, rp, old, 0.0).cpu().numpy().astype(np.float64)
+    ref, tol = mass64(c, q[1:], lse[1:], rs[1:], rp[1:], old, 0.0, 400)
+    F.assert_within(got[..., 101:], ref[..., 101:], tol[..., 101:] + F32_MIN_NORMAL, "keys behind the row")
