@@ -1375,8 +1375,13 @@ int mass_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const voi
   if (mass_cap < 1) return TFPA_EINVAL;
   thread_local std::vector<Run> runs;   // reused by every call of this thread
   if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;
+  // what a launch could not number is refused before the first one
+  auto blocks_of = [&](int32_t s) {
+    return (int64_t)c->hkv * (((int64_t)segs[s].seq_len + kMassKeys - 1) / kMassKeys);
+  };
   for (const Run& r : runs)
-    if (segs[r.seg].seq_len > mass_cap) return TFPA_ECAPACITY;
+    if (segs[r.seg].seq_len > mass_cap || blocks_of(r.seg) > INT32_MAX) return TFPA_ECAPACITY;
+  if ((int64_t)rows * (c->hq / c->hkv) > INT32_MAX) return TFPA_EINVAL;
   if (rows == 0) return TFPA_OK;
   if ((e = check_device())) return e;
   // A segment's runs one after the other, in the call's order, so that one
@@ -1399,11 +1404,8 @@ int mass_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const voi
       const Run& r = runs[ri];
       if (p.nsegs == 0 || p.segs[p.nsegs - 1].index != r.seg) {
         const tfpa_seg& g = segs[r.seg];
-        const int64_t blocks = (int64_t)c->hkv * ((g.seq_len + kMassKeys - 1) / kMassKeys);
-        if (items + blocks > INT32_MAX) {
-          if (nr == 0) return TFPA_ECAPACITY;   // more tiles than one launch can number
-          break;
-        }
+        const int64_t blocks = blocks_of(r.seg);
+        if (items + blocks > INT32_MAX) break;  // the next launch's
         const int src = ss.add(segs, r.seg);
         if (src < 0) break;
         MassSeg& m = p.segs[p.nsegs++];
@@ -1441,7 +1443,6 @@ int mass_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const voi
       int64_t vecs = 0;
       for (int r = 0; r < p.segs[i].nruns; ++r)
         vecs += (int64_t)p.runs[p.segs[i].run0 + r].nrows * (c->hq / c->hkv);
-      if (vecs > INT32_MAX) return TFPA_EINVAL;
       if (vecs > 128) p.dbufs = 2;
     }
     if (kv != kKvFp4) {
