@@ -190,7 +190,7 @@ int check_tma_source(const void* q) {
                                                                               : TFPA_EINVAL;
 }
 
-int32_t pages_of(int32_t L) { return (L + kPage - 1) / kPage; }
+int32_t pages_of(int32_t L) { return L / kPage + (L % kPage != 0); }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -222,7 +222,8 @@ int check_segs(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg) {
     } else {
       if (!g.k_slab || !g.v_slab) return TFPA_EINVAL;
       if (!aligned(g.k_slab, 16) || !aligned(g.v_slab, 16)) return TFPA_EINVAL;
-      if (g.slab_cap % kPage || g.slab_cap < pages_of(g.seq_len) * kPage) return TFPA_EINVAL;
+      // (a multiple of the page, so it holds the stream's last page whole)
+      if (g.slab_cap % kPage || g.slab_cap < g.seq_len) return TFPA_EINVAL;
       if ((int64_t)c->hkv * g.slab_cap > INT32_MAX) return TFPA_EINVAL;
     }
   }
