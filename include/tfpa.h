@@ -88,7 +88,8 @@ enum {
   TFPA_ECAPACITY = -3,   /* scratch too small for the requested rows/splits */
   TFPA_ECUDA = -4,       /* a CUDA runtime/driver call or a launch failed    */
   TFPA_EDEVICE = -5,     /* current device is not sm_100-family (tcgen05)    */
-  TFPA_ELANEMEM = -6     /* the page pool cannot hold the claim now: wait     */
+  TFPA_ELANEMEM = -6,    /* the page pool cannot hold the claim now: wait     */
+  TFPA_ENOMEM = -7       /* host memory ran out inside the call               */
 };
 
 typedef enum { TFPA_BF16 = 0, TFPA_FP8_E4M3 = 1, TFPA_FP4_E2M1 = 2 } tfpa_kv_dtype;
@@ -208,7 +209,7 @@ int tfpa_keep_kv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
  * be contiguous, so only the free count decides); a released page may be
  * claimed again.  Thread-safe.  No CUDA call. */
 typedef struct tfpa_pool tfpa_pool;
-tfpa_pool* tfpa_pool_create(int32_t num_pages);      /* NULL if num_pages < 1       */
+tfpa_pool* tfpa_pool_create(int32_t num_pages);      /* NULL if num_pages < 1 or out of memory */
 void tfpa_pool_destroy(tfpa_pool* pool);
 int32_t tfpa_pool_free(const tfpa_pool* pool);        /* pages free now              */
 int tfpa_pool_fits(const tfpa_pool* pool, int32_t npages);  /* 1 if npages <= pool size */

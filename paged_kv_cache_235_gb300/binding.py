@@ -25,7 +25,7 @@ KV_DTYPES = {"bf16": BF16, "fp8": FP8_E4M3, "fp4": FP4_E2M1}
 FP4_BLOCK = 18432          # bytes of a page of one kv head of a 4-bit cache
 
 TFPA_OK, TFPA_EINVAL, TFPA_ERANGE, TFPA_ECAPACITY, TFPA_ECUDA, TFPA_EDEVICE = 0, -1, -2, -3, -4, -5
-TFPA_ELANEMEM = -6
+TFPA_ELANEMEM, TFPA_ENOMEM = -6, -7
 
 EXPORTS = ("tfpa_pages_per_split", "tfpa_num_splits", "tfpa_write_kv", "tfpa_decode_partial",
            "tfpa_merge", "tfpa_decode", "tfpa_prefill", "tfpa_set_launch_hook",

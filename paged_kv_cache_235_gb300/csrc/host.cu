@@ -278,13 +278,14 @@ int row_bytes_of(const tfpa_cache* c) {
                                      : kFp4CodeBytes + kFp4ScaleBytes;
 }
 
-// A C entry's work; host memory that runs out is an error code, not an exception.
+// A C entry's work; host memory that runs out (for a call's row groups, a
+// plan's launches, a map) is an error code, not an exception.
 template <typename F>
 int no_throw(F&& fn) {
   try {
     return fn();
   } catch (const std::bad_alloc&) {
-    return TFPA_EINVAL;
+    return TFPA_ENOMEM;
   }
 }
 
@@ -829,16 +830,20 @@ extern "C" int tfpa_decode_partial(const tfpa_cache* cache, const tfpa_seg* segs
                                    const void* q, const int32_t* row_seg, const int32_t* row_pos,
                                    int32_t rows, float softmax_scale, const tfpa_scratch* scratch,
                                    cudaStream_t stream) {
-  return decode_impl(cache, segs, nseg, q, row_seg, row_pos, nullptr, rows, softmax_scale,
-                     scratch, nullptr, nullptr, Sink{stream, nullptr}, false);
+  return no_throw([&] {
+    return decode_impl(cache, segs, nseg, q, row_seg, row_pos, nullptr, rows, softmax_scale,
+                       scratch, nullptr, nullptr, Sink{stream, nullptr}, false);
+  });
 }
 
 extern "C" int tfpa_decode(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
                            const void* q, const int32_t* row_seg, const int32_t* row_pos,
                            int32_t rows, float softmax_scale, const tfpa_scratch* scratch,
                            void* out, float* lse, cudaStream_t stream) {
-  return decode_impl(cache, segs, nseg, q, row_seg, row_pos, nullptr, rows, softmax_scale,
-                     scratch, out, lse, Sink{stream, nullptr}, true);
+  return no_throw([&] {
+    return decode_impl(cache, segs, nseg, q, row_seg, row_pos, nullptr, rows, softmax_scale,
+                       scratch, out, lse, Sink{stream, nullptr}, true);
+  });
 }
 
 extern "C" int tfpa_row_splits(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
@@ -848,7 +853,8 @@ extern "C" int tfpa_row_splits(const tfpa_cache* cache, const tfpa_seg* segs, in
   if ((e = check_cache(cache)) || (e = check_segs(cache, segs, nseg))) return e;
   if (rows > 0 && !nsplit) return TFPA_EINVAL;
   thread_local std::vector<Run> runs;
-  if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;
+  if ((e = no_throw([&] { return build_runs(segs, nseg, row_seg, row_pos, rows, runs); })))
+    return e;
   // the same choice of kernel as decode_impl: runs of four or more m-tiles
   // take the tensor-core verify path and its splits
   const int G = cache->hq / cache->hkv;
@@ -868,8 +874,10 @@ extern "C" int tfpa_decode_tree(const tfpa_cache* cache, const tfpa_seg* segs, i
                                 const tfpa_scratch* scratch, void* out, float* lse,
                                 cudaStream_t stream) {
   if (rows > 0 && !row_anc) return TFPA_EINVAL;
-  return decode_impl(cache, segs, nseg, q, row_seg, row_pos, row_anc, rows, softmax_scale,
-                     scratch, out, lse, Sink{stream, nullptr}, true);
+  return no_throw([&] {
+    return decode_impl(cache, segs, nseg, q, row_seg, row_pos, row_anc, rows, softmax_scale,
+                       scratch, out, lse, Sink{stream, nullptr}, true);
+  });
 }
 
 extern "C" int tfpa_decode_append(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
@@ -878,8 +886,10 @@ extern "C" int tfpa_decode_append(const tfpa_cache* cache, const tfpa_seg* segs,
                                   float softmax_scale, const tfpa_scratch* scratch, void* out,
                                   float* lse, cudaStream_t stream) {
   if (rows > 0 && (!k_rows || !v_rows)) return TFPA_EINVAL;
-  return decode_impl(cache, segs, nseg, q, row_seg, row_pos, nullptr, rows, softmax_scale,
-                     scratch, out, lse, Sink{stream, nullptr}, true, k_rows, v_rows);
+  return no_throw([&] {
+    return decode_impl(cache, segs, nseg, q, row_seg, row_pos, nullptr, rows, softmax_scale,
+                       scratch, out, lse, Sink{stream, nullptr}, true, k_rows, v_rows);
+  });
 }
 
 extern "C" int tfpa_merge(const tfpa_scratch* sc, int32_t hq, int32_t rows,
@@ -993,8 +1003,10 @@ int write_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const vo
 extern "C" int tfpa_write_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg,
                              const void* k_rows, const void* v_rows, const int32_t* row_seg,
                              const int32_t* row_pos, int32_t rows, cudaStream_t stream) {
-  return write_impl(c, segs, nseg, k_rows, v_rows, row_seg, row_pos, rows,
-                    RopeArgs{nullptr, nullptr, nullptr, 0}, Sink{stream, nullptr});
+  return no_throw([&] {
+    return write_impl(c, segs, nseg, k_rows, v_rows, row_seg, row_pos, rows,
+                      RopeArgs{nullptr, nullptr, nullptr, 0}, Sink{stream, nullptr});
+  });
 }
 
 // The write's launches with the rows as the destination (const cast back by
@@ -1015,8 +1027,10 @@ extern "C" int tfpa_write_kv_rope(const tfpa_cache* c, const tfpa_seg* segs, int
                                   const float* rope_sin, int32_t rope_n, int32_t rows,
                                   cudaStream_t stream) {
   if (!rope_cos) return TFPA_EINVAL;
-  return write_impl(c, segs, nseg, k_rows, v_rows, row_seg, row_pos, rows,
-                    RopeArgs{rope_pos, rope_cos, rope_sin, rope_n}, Sink{stream, nullptr});
+  return no_throw([&] {
+    return write_impl(c, segs, nseg, k_rows, v_rows, row_seg, row_pos, rows,
+                      RopeArgs{rope_pos, rope_cos, rope_sin, rope_n}, Sink{stream, nullptr});
+  });
 }
 
 // ------------------------------------------------------------ plans
@@ -1182,12 +1196,7 @@ int plan_call(tfpa_plan* plan, F&& fn) {
   if (!plan) return TFPA_EINVAL;
   const Sink sink{nullptr, plan};
   const Sink::Mark m = sink.mark();
-  int e;
-  try {
-    e = fn(sink);
-  } catch (const std::bad_alloc&) {
-    e = TFPA_EINVAL;
-  }
+  const int e = no_throw([&] { return fn(sink); });
   if (e != TFPA_OK)
     sink.rollback(m);   // the plan, and so its shape, as before the call
   else
@@ -1568,6 +1577,7 @@ extern "C" const char* tfpa_strerror(int code) {
     case TFPA_ECUDA: return "CUDA call or launch failed";
     case TFPA_EDEVICE: return "current device is not sm_100-family";
     case TFPA_ELANEMEM: return "the page pool cannot hold the claim now (wait for releases)";
+    case TFPA_ENOMEM: return "host memory ran out inside the call";
     default: return "unknown error";
   }
 }
@@ -1577,12 +1587,10 @@ extern "C" const char* tfpa_version(void) { return "tfpa 0.1 (sm_103a)"; }
 // ------------------------------------------------------------ prefill
 namespace {
 constexpr int kPrefillTileRows = 128;
-}
 
-extern "C" int tfpa_prefill(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg,
-                            const void* q, const int32_t* row_seg, const int32_t* row_pos,
-                            int32_t rows, float scale, int32_t max_rows_per_launch, void* out,
-                            float* lse, cudaStream_t stream) {
+int prefill_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const void* q,
+                 const int32_t* row_seg, const int32_t* row_pos, int32_t rows, float scale,
+                 int32_t max_rows_per_launch, void* out, float* lse, cudaStream_t stream) {
   int e;
   if ((e = check_cache(c)) || (e = check_segs(c, segs, nseg))) return e;
   if (rows > 0 && (!q || !aligned(q, 16) || !out || !aligned(out, 16))) return TFPA_EINVAL;
@@ -1653,4 +1661,15 @@ extern "C" int tfpa_prefill(const tfpa_cache* c, const tfpa_seg* segs, int32_t n
       if ((e = to_err(launch_prefill(p, kv, tiles, stream)))) return e;
   }
   return TFPA_OK;
+}
+}  // namespace
+
+extern "C" int tfpa_prefill(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg,
+                            const void* q, const int32_t* row_seg, const int32_t* row_pos,
+                            int32_t rows, float scale, int32_t max_rows_per_launch, void* out,
+                            float* lse, cudaStream_t stream) {
+  return no_throw([&] {
+    return prefill_impl(c, segs, nseg, q, row_seg, row_pos, rows, scale, max_rows_per_launch, out,
+                        lse, stream);
+  });
 }

@@ -9,6 +9,7 @@
 // claimed.  One mutex per pool.
 #include <algorithm>
 #include <mutex>
+#include <new>
 #include <set>
 #include <vector>
 
@@ -25,9 +26,14 @@ extern "C" tfpa_pool* tfpa_pool_create(int32_t num_pages) {
   if (num_pages < 1) return nullptr;
   tfpa_pool* p = new (std::nothrow) tfpa_pool;
   if (!p) return nullptr;
-  p->n = num_pages;
-  p->claimed.assign(num_pages, 0);
-  for (int32_t i = 0; i < num_pages; ++i) p->free_ids.insert(p->free_ids.end(), i);
+  try {
+    p->n = num_pages;
+    p->claimed.assign(num_pages, 0);
+    for (int32_t i = 0; i < num_pages; ++i) p->free_ids.insert(p->free_ids.end(), i);
+  } catch (const std::bad_alloc&) {
+    delete p;
+    return nullptr;
+  }
   return p;
 }
 
@@ -59,16 +65,22 @@ extern "C" int tfpa_pool_claim(tfpa_pool* pool, int32_t npages, int32_t* pages_o
 
 extern "C" int tfpa_pool_release(tfpa_pool* pool, const int32_t* pages, int32_t n) {
   if (!pool || n < 0 || (n > 0 && !pages)) return TFPA_EINVAL;
+  if (n > pool->n) return TFPA_EINVAL;          // a page twice, or one that is not the pool's
   std::lock_guard<std::mutex> lock(pool->mu);
-  std::vector<int32_t> v(pages, pages + n);
+  std::vector<int32_t> v;
+  std::set<int32_t> back;                       // the pages' nodes, made before anything is released
+  try {
+    v.assign(pages, pages + n);
+    back.insert(v.begin(), v.end());
+  } catch (const std::bad_alloc&) {
+    return TFPA_ENOMEM;
+  }
   std::sort(v.begin(), v.end());
   for (int32_t i = 0; i < n; ++i) {
     if (v[i] < 0 || v[i] >= pool->n || !pool->claimed[v[i]]) return TFPA_EINVAL;
     if (i > 0 && v[i] == v[i - 1]) return TFPA_EINVAL;
   }
-  for (int32_t id : v) {
-    pool->claimed[id] = 0;
-    pool->free_ids.insert(id);
-  }
+  for (int32_t id : v) pool->claimed[id] = 0;
+  pool->free_ids.merge(back);
   return TFPA_OK;
 }
