@@ -163,3 +163,34 @@ def test_mass_of_dozens_of_tiles_a_cta(kv, rows, decay):
     m2 = old.clone()
     B.tfpa_key_mass(c.cache, c.segs, q, lse, rs, rp, X.SCALE, m2, decay=decay)
     assert torch.equal(m, m2) and int(c.err.item()) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+def test_more_heads_a_kv_head_than_a_tile_holds(kv):
+    """160 query heads on one kv head: ten m-tiles a split, a row's own."""
+    L = [3001 + 517 * i for i in range(12)]
+    c = _case(kv, L, hq=160, hkv=1, seed=150)
+    rs, rp = X.last_rows(L, [1] * 12)
+    assert max(_items(c, rs, rp)) > 4 * 152
+    q = c.q(12)
+    out, lse = _decode(c, q, rs, rp)
+    ref, rl, tol, lt = X.attend(c, q, rs, rp)
+    if kv == "bf16":                             # the weights are rounded to bf16 there: 2^-8 of each, not 2^-11
+        tol = 8 * tol
+    X.assert_within(out, ref, tol, "out")
+    X.assert_within(lse, rl, lt, "lse")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+def test_mass_of_more_heads_than_a_pass_holds(kv):
+    """300 query heads on one kv head, three rows: passes of 256 vectors that begin inside a row."""
+    L = [20001, 3000]
+    c = _case(kv, L, hq=300, hkv=1, seed=151)
+    rs, rp = X.last_rows(L, [3, 2])
+    q = c.q(5)
+    lse = torch.randn(5, 300, generator=c.g, device="cuda").abs() + 8
+    m = torch.zeros(2, 1, 20001, device="cuda")
+    B.tfpa_key_mass(c.cache, c.segs, q, lse, rs, rp, X.SCALE, m, decay=0.0)
+    torch.cuda.synchronize()
+    ref, tol = X.mass(c, q, lse, rs, rp, torch.zeros_like(m), 0.0)
+    X.assert_within(m, ref, tol, kv)
