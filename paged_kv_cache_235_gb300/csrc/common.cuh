@@ -172,6 +172,16 @@ __device__ __forceinline__ bool warp_wait_or_abort(uint64_t* bar, uint32_t parit
   return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, err, abort));
 }
 
+// For the whole block, after a wait of its own gave up: loads that are still
+// on their way end before the block and its shared memory do.
+__device__ __forceinline__ void let_copies_land() {
+  if (threadIdx.x == 0) {
+    const uint64_t since = global_timer_ns();
+    while (global_timer_ns() - since < 1000000) {}       // 1 ms: far longer than any copy takes
+  }
+  __syncthreads();
+}
+
 // 3D tiled load (x innermost).
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y,
                                             int z, uint64_t* bar) {

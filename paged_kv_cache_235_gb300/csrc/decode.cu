@@ -63,7 +63,7 @@ constexpr int kCombBytes = kCombineWarps * 16 * 32 * 16;
 constexpr int kMlBytes = kConsumerWarps * 16 * 2 * 4;
 constexpr int kNumBars = 2 * kMaxStages + 7;
 constexpr int kSmemBytes =
-    kRingBytes + kCombBytes + kMlBytes + kMaxStages * 4 + 8 + kNumBars * 8 + 1024;
+    kRingBytes + kCombBytes + kMlBytes + kMaxStages * 4 + 16 + kNumBars * 8 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 
@@ -239,7 +239,7 @@ __device__ __forceinline__ bool load_item(const DecodeParams& p, const RunInfo& 
 // append (APPEND), the whole warp first stores the new rows an item reads.
 template <int KV, bool APPEND>
 __device__ void producer(const DecodeParams& p, const DecodeDyn& D, uint8_t* stage_mem,
-                         uint64_t* full, uint64_t* empty, int* stage_bad) {
+                         uint64_t* full, uint64_t* empty, int* stage_bad, int* lost) {
   const int lane = threadIdx.x & 31;
   if (!APPEND && lane != 0) return;
   int ib, ie;
@@ -264,6 +264,7 @@ __device__ void producer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
       ok = load_item<KV>(p, ru, x, klo, khi, stage_mem, full, empty, stage_bad, stage);
     }
   }
+  if (!ok) *lost = 1;
 }
 
 // Lane 0 of the producer warp: the TMA loads of one item's key chunks into
@@ -417,6 +418,7 @@ struct CombBars {
   uint64_t* pub;         // the combiners published their pairs' (m, l)
   uint64_t* folded;      // the combiners wrote their folds
   uint64_t* done;        // the combiners finished the item (fold buffer free)
+  int* lost;             // a wait of a role gave up
 };
 
 // This warp's kKeysPerWarp keys, keys key_base.. at rows r0.. of the stage
@@ -838,9 +840,13 @@ __device__ void consumer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
       if (C::kFp4) {
         // as in the kernel of eight-vector items: looked at a chunk ahead, so
         // that the warp's agreement is all that is left on the path
-        if (!__all_sync(0xffffffffu, ready) && !warp_wait(&full[buf], ph, p.err_flag)) return;
+        if (!__all_sync(0xffffffffu, ready) && !warp_wait(&full[buf], ph, p.err_flag)) {
+          *bars.lost = 1;
+          return;
+        }
         ready = mbar_test_wait(&full[(st + 1) % C::kStages], ((st + 1) / C::kStages) & 1);
       } else if (!warp_wait(&full[buf], ph, p.err_flag)) {
+        *bars.lost = 1;
         return;
       }
       const uint32_t sb = sbase + (uint32_t)buf * C::kStageBytes;
@@ -869,8 +875,10 @@ __device__ void consumer(const DecodeParams& p, const DecodeDyn& D, uint8_t* sta
     const int rel = it - ib;
     const int b = rel & 1;
     if (rel >= 2 &&
-        !warp_wait(&bars.tmem_free[b], (uint32_t)((rel >> 1) - 1) & 1u, p.err_flag))
+        !warp_wait(&bars.tmem_free[b], (uint32_t)((rel >> 1) - 1) & 1u, p.err_flag)) {
+      *bars.lost = 1;
       return;
+    }
     umma::fence_after_sync();
     const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16) +
                         (uint32_t)(b * kBufCols + (warp >> 2) * kHalfCols);
@@ -1138,7 +1146,10 @@ __device__ void combiner(const DecodeParams& p, const DecodeDyn& D, uint32_t tme
       x = item_of<KV>(p, D, it, rh);
     const RunInfo& ru = D.runs[x.run];
     const int nq = ru.nrows * p.group;
-    ok = ok && fold_item(x, ru, nq, it - ib);
+    if (ok && !fold_item(x, ru, nq, it - ib)) {
+      ok = false;
+      *bars.lost = 1;
+    }
     if constexpr (MERGE)
       merge_if_last<KV, kCombineWarp0>(p, ru, x, nq, merge_flag, ok);
     else if (!ok)
@@ -1163,11 +1174,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_kernel(
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stage_bad + kMaxStages);
   int* merge_flag = reinterpret_cast<int*>(tmem_slot + 1);
   uint64_t* bars = reinterpret_cast<uint64_t*>(
-      (reinterpret_cast<uintptr_t>(merge_flag + 1) + 7) & ~uintptr_t(7));
+      (reinterpret_cast<uintptr_t>(merge_flag + 2) + 7) & ~uintptr_t(7));
   uint64_t* full = bars;
   uint64_t* empty = bars + kMaxStages;
   uint64_t* cbar = bars + 2 * kMaxStages;
-  CombBars cb{cbar, cbar + 2, cbar + 4, cbar + 5, cbar + 6};
+  CombBars cb{cbar, cbar + 2, cbar + 4, cbar + 5, cbar + 6, merge_flag + 1};
 
   const int warp = threadIdx.x >> 5;
   // With the launch data in the parameters, the producer's first page id is
@@ -1200,6 +1211,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_kernel(
     mbar_init(cb.pub, kCombineWarps);
     mbar_init(cb.folded, kCombineWarps);
     mbar_init(cb.done, kCombineWarps);
+    *cb.lost = 0;
     fence_mbar_init();
   }
   if (!Cfg<KV>::kFp4 && warp == kProducerWarp && (threadIdx.x & 31) == 0) {
@@ -1223,10 +1235,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_kernel(
     combiner<KV, GEN, MERGE>(p, D, tmem, fold, ml_buf, merge_flag, cb);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
-    if (warp == kProducerWarp) producer<KV, APPEND>(p, D, stage_mem, full, empty, stage_bad);
+    if (warp == kProducerWarp)
+      producer<KV, APPEND>(p, D, stage_mem, full, empty, stage_bad, cb.lost);
   }
   umma::fence_before_sync();
   __syncthreads();
+  if (*cb.lost) let_copies_land();
   if (warp == kCombineWarp0) {
     umma::fence_after_sync();
     umma::tmem_dealloc(tmem, kTmemCols);
@@ -1272,7 +1286,7 @@ constexpr int kRingBytes4 = Cfg<kKvFp4>::kStages * Cfg<kKvFp4>::kStageBytes;
 constexpr int kCombBytes4 = kCombineWarps * 8 * 32 * 16;   // [slot q][d m-tile][lane] float4
 constexpr int kMlFloats4 = kWarps4 * 8 * 2;                // [warp][vector](m, l), one buffer
 constexpr int kSmemBytes4 =
-    kRingBytes4 + kCombBytes4 + 2 * kMlFloats4 * 4 + kMaxStages * 4 + 8 + kNumBars * 8 + 1024;
+    kRingBytes4 + kCombBytes4 + 2 * kMlFloats4 * 4 + kMaxStages * 4 + 16 + kNumBars * 8 + 1024;
 static_assert(kSmemBytes4 <= 232448, "shared memory");
 
 // 32 keys of one warp, from key_base on, in the stage at sb.  A code byte of
@@ -1532,8 +1546,10 @@ __device__ void consumer_fp4(const DecodeParams& p, const DecodeDyn& D, uint8_t*
       const int buf = n & 1;
       // the next stage's barrier is looked at before this one's keys, off the
       // path of the wait (8 streams of 65,536 keys 134 -> 131 us at the time)
-      if (!__all_sync(0xffffffffu, ready) && !warp_wait(&full[buf], (n >> 1) & 1, p.err_flag))
+      if (!__all_sync(0xffffffffu, ready) && !warp_wait(&full[buf], (n >> 1) & 1, p.err_flag)) {
+        *bars.lost = 1;
         return;
+      }
       ready = mbar_test_wait(&full[buf ^ 1], ((n + 1) >> 1) & 1);
       const int key_base = k0 + (warp & 7) * 32;
       if (!stage_bad[buf] && key_base <= maxlim)
@@ -1550,8 +1566,10 @@ __device__ void consumer_fp4(const DecodeParams& p, const DecodeDyn& D, uint8_t*
     const int rel = it - ib;
     const int b = rel & 1;
     if (rel >= 2 &&
-        !warp_wait(&bars.tmem_free[b], (uint32_t)((rel >> 1) - 1) & 1u, p.err_flag))
+        !warp_wait(&bars.tmem_free[b], (uint32_t)((rel >> 1) - 1) & 1u, p.err_flag)) {
+      *bars.lost = 1;
       return;
+    }
     if (gq == 0)
       *reinterpret_cast<float4*>(ml_buf + b * kMlFloats4 + (warp * 8 + 2 * c) * 2) =
           make_float4(m_run[0], l_run[0], m_run[1], l_run[1]);
@@ -1695,7 +1713,10 @@ __device__ void combiner_fp4(const DecodeParams& p, const DecodeDyn& D, uint32_t
   for (int it = ib; it < ie; ++it, next_item<KV>(p, D, x)) {
     const RunInfo& ru = D.runs[x.run];
     const int nq = ru.nrows * p.group;
-    ok = ok && fold_item(x, ru, nq, it - ib);
+    if (ok && !fold_item(x, ru, nq, it - ib)) {
+      ok = false;
+      *bars.lost = 1;
+    }
     if constexpr (MERGE)
       merge_if_last<KV, kCombineWarp4>(p, ru, x, nq, merge_flag, ok);
     else if (!ok)
@@ -1718,11 +1739,11 @@ __global__ void __launch_bounds__(kThreads4, 1) decode_fp4_kernel(
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stage_bad + kMaxStages);
   int* merge_flag = reinterpret_cast<int*>(tmem_slot + 1);
   uint64_t* bars = reinterpret_cast<uint64_t*>(
-      (reinterpret_cast<uintptr_t>(merge_flag + 1) + 7) & ~uintptr_t(7));
+      (reinterpret_cast<uintptr_t>(merge_flag + 2) + 7) & ~uintptr_t(7));
   uint64_t* full = bars;
   uint64_t* empty = bars + kMaxStages;
   uint64_t* cbar = bars + 2 * kMaxStages;
-  CombBars cb{cbar, cbar + 2, cbar + 4, cbar + 5, cbar + 6};
+  CombBars cb{cbar, cbar + 2, cbar + 4, cbar + 5, cbar + 6, merge_flag + 1};
 
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -1736,6 +1757,7 @@ __global__ void __launch_bounds__(kThreads4, 1) decode_fp4_kernel(
     }
     mbar_init(cb.folded, kCombineWarps);
     mbar_init(cb.done, kCombineWarps);
+    *cb.lost = 0;
     fence_mbar_init();
   }
   if (warp == kCombineWarp4) umma::tmem_alloc(tmem_slot, kTmemCols);
@@ -1753,10 +1775,12 @@ __global__ void __launch_bounds__(kThreads4, 1) decode_fp4_kernel(
     combiner_fp4<MERGE>(p, D, tmem, fold, ml_buf, merge_flag, cb);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer4));
-    if (warp == kProducerWarp4) producer<KV, APPEND>(p, D, stage_mem, full, empty, stage_bad);
+    if (warp == kProducerWarp4)
+      producer<KV, APPEND>(p, D, stage_mem, full, empty, stage_bad, cb.lost);
   }
   umma::fence_before_sync();
   __syncthreads();
+  if (*cb.lost) let_copies_land();
   if (warp == kCombineWarp4) {
     umma::fence_after_sync();
     umma::tmem_dealloc(tmem, kTmemCols);

@@ -544,14 +544,7 @@ out:
   }
   umma::fence_before_sync();
   __syncthreads();
-  if (*b.abort) {
-    // a wait gave up: let the loads in flight end
-    if (threadIdx.x == 0) {
-      const uint64_t since = global_timer_ns();
-      while (global_timer_ns() - since < 1000000) {}     // 1 ms: far longer than any copy takes
-    }
-    __syncthreads();
-  }
+  if (*b.abort) let_copies_land();
   if (warp == 1) {
     umma::fence_after_sync();
     umma::tmem_dealloc(tmem, 512);

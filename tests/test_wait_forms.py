@@ -105,3 +105,14 @@ def test_a_warp_waits_as_one(name):
         if re.search(r"\b(live|there|gave_up)\b", " ".join(h[-1:])) and LEAVES.search(s) and "_sync" not in h[-1]:
             bad.append((line, s))
     assert seen and not bad, bad
+
+
+@pytest.mark.parametrize("name,lands", [("decode.cu", r"\*cb\.lost\) let_copies_land\(\)"), ("mass.cu", r"\*b\.abort\) let_copies_land\(\)"),
+                                        ("prefill.cu", r"if \(\*b\.abort\) { mbar_wait\(b\.q_full")])
+def test_loads_in_flight_land_before_a_block_ends(name, lands):
+    """A kernel that loads into its shared memory asynchronously waits for that after a wait gave up: every such kernel
+    of the file, or (prefill.cu) the producer that issued the loads."""
+    with open(os.path.join(CSRC, name)) as f:
+        src = " ".join(strip(f.read()).split())
+    kernels = len(re.findall(r"__global__ void __launch_bounds__\([^;{]*?(decode_partial|decode_fp4|key_mass)_kernel\(", src)) or 1
+    assert len(re.findall(lands, src)) == kernels
