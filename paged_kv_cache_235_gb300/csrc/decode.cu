@@ -15,7 +15,8 @@
 //   warps 0..7  consumers: each takes an eighth of every chunk's keys, runs
 //               QK^T and PV on mma.sync m16n8k16 (bf16, or f16 for e4m3 and
 //               4-bit caches, whose values convert to f16 exactly) and an online
-//               softmax reduced with warp shuffles; at the end of an item
+//               softmax reduced with warp shuffles (its weights rounded to the
+//               operands' 16 bits, its sums not); at the end of an item
 //               each warp stores its state (O, m, l) into tensor memory and
 //               goes straight on to the next item;
 //   warps 8..11 combiners: warp 8+q reads the states of consumer warps q and
@@ -1268,7 +1269,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_kernel(
 //   them empty and no transposition, 131 us).
 // The running maximum is looked at with one vote a block and moves only when
 // some score passes it by more than 2^8, which after a row's first block is
-// rare.
+// rare.  The weights are rounded to f16 (2^-11 of each) to be an operand; the
+// sums l add them before that, in float32.
 constexpr int kWarps4 = 16;
 constexpr int kCombineWarp4 = 16;         // warps 16..19
 constexpr int kProducerWarp4 = 20;        // warps 21..23 only take part in the register split

@@ -551,7 +551,9 @@ void plan_cta_ranges(DecodeParams& p, int nr, int G, int kv, int grid) {
   const int vecs = item_vectors(kv);
   // The fixed cost, in key stages, was measured on the overcommitted pool
   // (17 streams of 1k-262k keys, e4m3): 0 -> 380 us, 1 -> 341 us, 2 -> 348 us,
-  // 4 -> 377 us, 8 -> 444 us; uniform batches do not depend on it.
+  // 4 -> 377 us, 8 -> 444 us; uniform batches do not depend on it.  A 4-bit
+  // item's end is nearer two stages (fp4_pages_per_split); others than 1 have
+  // not been measured there.
   constexpr int64_t kItemCost = 1;
   thread_local std::vector<int64_t> cum;     // per run: 0, w0, w0 + w1, ...
   int32_t blk[kMaxRuns + 1];                 // run r's prefix weights: cum[blk[r] .. blk[r + 1]]

@@ -25,9 +25,11 @@
 //               overlaps head B's MMAs and the other way round.
 //   warps 4-7   softmax of head A, warps 8-11 of head B: one thread per row
 //               (TMEM lane), causal mask on the diagonal tiles, online
-//               max/sum, P written back over S as bf16 (f16 for e4m3
-//               caches), O rescaled in TMEM only when the running max grows
-//               by more than 2^8.
+//               max/sum, P written back over S as bf16 (f16 for e4m3 and
+//               4-bit caches), O rescaled in TMEM only when the running max
+//               grows by more than 2^8.  Rounding P to 16 bits (2^-8 of a
+//               weight in bf16, 2^-11 in f16) is what the tensor cores' 16-bit
+//               operands cost; the row sums add the weights before it.
 //   warps 12-15 (e4m3 and 4-bit caches) converters: TMA lands e4m3 K/V tiles
 //               (4 bits: bulk copies land half-blocks of codes and scales) in
 //               a staging buffer; these warps write the exact f16 operand
@@ -50,9 +52,9 @@
 // slot, one f16 V stage per slot.
 // 4 bits: three staged half-blocks each of K and V over the slots' common
 // order, one f16 stage each per slot (16-node trees of 8 streams of 32,761 keys
-// 160 us, 25 % of HBM: a slot's softmax, P V and next scores in a row, beside
+// 155 us, 29 % of HBM: a slot's softmax, P V and next scores in a row, beside
 // four tile conversions a step; prompt chunk of 4,096 rows over 32,768 keys
-// 1,451 us, 75 % of the measured tensor rate).
+// 1,431 us, 76 % of the measured tensor rate).
 // TMEM (512 columns): S_A [0,128) O_A [128,256) S_B [256,384) O_B [384,512).
 // CTA 1's partial lands in CTA 0's shared memory once CTA 0's MMAs are done:
 // O (float32 [2 heads][128 rows][128], 16-byte chunks permuted by row against
