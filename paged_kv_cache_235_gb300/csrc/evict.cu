@@ -17,7 +17,9 @@
 // the slots are gone through in order, a thread four of them: holes and movers
 // are counted (of the keys equal to the threshold the first slots stay; where
 // not all of them do, they are counted first), numbered and written.  What
-// bounds it is the instructions a key costs, so every step takes four keys.
+// bounds it is the chain of three passes and the numbering, each ended by
+// barriers of the block or the cluster (8 streams of 16,384 to 32,768 keys: 26 us,
+// issue slots 47 % busy, DRAM 6 %); four keys a step shorten its links.
 // A run's lists are put in rank order in shared memory and written by
 // consecutive lanes (a lane writing its own slots' numbers spread each store
 // over four times the sectors: 14 -> 7 us of the choice's 46).
