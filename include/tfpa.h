@@ -576,6 +576,145 @@ int tfpa_evict_kv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
                   float* mass, int32_t* key_pos, int32_t mass_cap, int32_t* moves,
                   cudaStream_t stream);
 
+/* ---- From the projection to attention over a part of a long stream ----------
+ * A decode step of a long stream: tfpa_write_qkv turns the projection's rows
+ * into q and stored K / V, tfpa_key_bounds brings the bounds of the blocks they
+ * fell into up to date, tfpa_select_blocks chooses for each row and kv head the
+ * blocks worth reading, and tfpa_decode_blocks attends to them.  None of the
+ * TensorFold sources has a counterpart to this.  Every call can be captured
+ * in a graph (lengths and positions are kept as they were then). */
+
+/* Rotary tables: cos and sin of position t and frequency f_i, i < rot_dim / 2,
+ * times attn_scale, with f_i = base^(-2 i / rot_dim) radians a position, and
+ * for a context stretched `factor` times beyond orig_len positions
+ *   TFPA_ROPE_LINEAR  f_i / factor
+ *   TFPA_ROPE_BASE    base * factor^(rot_dim / (rot_dim - 2)) in base's place
+ *   TFPA_ROPE_BANDS   f_i u + f_i / factor (1 - u), where
+ *                     u = (turns_i - low) / (high - low), cut to [0, 1], and
+ *                     turns_i = orig_len f_i / 2 pi
+ *   TFPA_ROPE_RAMP    the same with u = 1 - (i - a) / max(b - a, 0.001), cut to
+ *                     [0, 1]; dim(n) = rot_dim ln(orig_len / (2 pi n)) /
+ *                     (2 ln base), a = max(floor(dim(high)), 0),
+ *                     b = min(ceil(dim(low)), rot_dim - 1)
+ * The frequencies are formed in 64 bits and the angle modulo one turn to 2^-64
+ * of a turn, so far positions lose nothing. */
+enum {
+  TFPA_ROPE_NONE = 0,
+  TFPA_ROPE_LINEAR = 1,
+  TFPA_ROPE_BASE = 2,
+  TFPA_ROPE_BANDS = 3,
+  TFPA_ROPE_RAMP = 4
+};
+typedef struct {
+  double base;                    /* > 1                                                   */
+  double factor;                  /* >= 1 (not read for TFPA_ROPE_NONE)                    */
+  double low, high;               /* TFPA_ROPE_BANDS, _RAMP: 0 < low < high                */
+  double attn_scale;              /* > 0; 1: none                                          */
+  int32_t rot_dim;                /* a multiple of 16, at most 128                         */
+  int32_t scaling;
+  int32_t orig_len;               /* TFPA_ROPE_BANDS, _RAMP: >= 1                          */
+} tfpa_rope_spec;
+/* Writes the rows of positions first .. first + n - 1 to cos and sin (DEVICE
+ * float [n][rot_dim / 2], 16-byte aligned).  TFPA_ERANGE unless 0 <= first and
+ * first + n <= 2^31.  With rot_dim = 128 they are the tables of
+ * tfpa_write_kv_rope too. */
+int tfpa_rope_table(const tfpa_rope_spec* spec, int64_t first, int32_t n, float* cos, float* sin,
+                    cudaStream_t stream);
+
+/* A projection's rows.  Row r's q, k and v lie at their pointers plus r times
+ * their strides (so all three may point into one fused projection's output);
+ * heads are [128] one after the other.  For every q head (k head)
+ *   with q_weight (k_weight): y = x (1 / sqrt(mean x^2 + eps)) w; the squares
+ *     are added in pairs of neighbours, then pairs of those sums, and so on;
+ *   with rope_cos: the first rot_dim dims rotated by row t of the table, t the
+ *     row's rotary position (rope_pos, or NULL: row_pos): each pair (a, b)
+ *     becomes (a c - b s, b c + a s), where a pair is dims i and
+ *     i + rot_dim / 2, or with `interleaved` dims 2 i and 2 i + 1;
+ * each product, sum, quotient and root rounded to float32 (no fused multiply-
+ * add).  q is rounded to bf16 into q_out (DEVICE bf16 [rows][hq][128]); K and V
+ * are stored as tfpa_write_kv stores them (K unrounded before a quantised
+ * store).  q and q_out may both be NULL (K and V only), and q_out may be q
+ * itself when q_stride is hq * 128; else q_out shares no memory with an input
+ * (TFPA_EINVAL).
+ * A rotary position outside the table leaves the row's q_out, K and V unwritten
+ * and ORs 4 into cache->err_flag (without rope_pos it is TFPA_ERANGE); a page
+ * id out of range leaves its K and V unwritten and ORs 1. */
+typedef struct {
+  const void* q;                  /* DEVICE bf16, 16-byte aligned like k and v             */
+  const void* k;
+  const void* v;
+  int64_t q_stride;               /* elements between rows: a multiple of 8, >= heads * 128 */
+  int64_t k_stride;
+  int64_t v_stride;
+  const float* q_weight;          /* DEVICE float[128], 16-byte aligned; NULL: not normed  */
+  const float* k_weight;
+  const float* rope_cos;          /* DEVICE float[rope_n][rot_dim / 2], 16-byte aligned;   */
+  const float* rope_sin;          /*   NULL: not rotated                                   */
+  const int32_t* rope_pos;        /* DEVICE int32[rows], or NULL                           */
+  int32_t rope_n;
+  int32_t rot_dim;                /* a multiple of 16, at most 128                         */
+  int32_t interleaved;
+  float eps;                      /* > 0 with a weight                                     */
+} tfpa_qkv;
+int tfpa_write_qkv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
+                   const tfpa_qkv* in, const int32_t* row_seg, const int32_t* row_pos,
+                   int32_t rows, void* q_out, cudaStream_t stream);
+
+/* Bounds of the keys.  A stream's positions are cut into blocks of `block`
+ * positions (64, 128 or 256, counted from position 0).  For each block and kv
+ * head the smallest and then the largest stored K of every head dim is kept,
+ * as the stored value without k_scale (exact in bf16 for every cache type; a
+ * NaN counts as 0).  Bounds go with the pages: streams that share a page share
+ * its bounds. */
+typedef struct {
+  int32_t block;
+  void* pool;                     /* DEVICE bf16 [num_pages][hkv][256 / block][2][128],    */
+                                  /*   16-byte aligned; may be NULL without paged segments */
+  void* const* slabs;             /* HOST [nseg]: a slab segment's DEVICE bf16             */
+                                  /*   [hkv][slab_cap / block][2][128]; NULL without slabs */
+} tfpa_bounds;
+
+/* Takes the bounds of every block that holds one of the call's rows anew, from
+ * the keys stored at its positions below seq_len (so a block whose rows were
+ * overwritten, or that a cut left in part, is right again after a call with
+ * one of its rows).  A block on a page whose id is out of range is left as it
+ * is and ORs 1 into cache->err_flag.  After tfpa_evict_kv a stream's keys have
+ * moved: call with all of its rows. */
+int tfpa_key_bounds(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
+                    const tfpa_bounds* bounds, const int32_t* row_seg, const int32_t* row_pos,
+                    int32_t rows, cudaStream_t stream);
+
+/* For each row and kv head the nsel blocks to attend to, of the blocks up to
+ * the row's own: the first `sink`, the last `recent` (the row's own the last of
+ * them), then those of largest
+ *   score = sum over the kv head's query heads h and dims d of
+ *           max(q_hd, 0) largest_d + min(q_hd, 0) smallest_d,
+ * which no sum of the heads' scores with a key of the block exceeds; ties go to
+ * the lower block, and a score that is not a number (an infinite bound under a
+ * zero of q) counts as largest.  The choice is that of exact arithmetic: scores
+ * too near the border for float32 are taken in 64 bits.
+ *   q      : DEVICE bf16 [rows][hq][128], 16-byte aligned (as tfpa_decode's)
+ *   blocks : DEVICE int32 [rows][hkv][nsel], written: block numbers ascending,
+ *            -1 behind the last where there are fewer than nsel.
+ * A block on a page whose id is out of range is not chosen and ORs 1 into
+ * cache->err_flag.  sink, recent >= 0, sink + recent <= nsel (TFPA_EINVAL).  At
+ * most 18,432 blocks up to a row (TFPA_ECAPACITY). */
+int tfpa_select_blocks(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
+                       const tfpa_bounds* bounds, const void* q, const int32_t* row_seg,
+                       const int32_t* row_pos, int32_t rows, int32_t nsel, int32_t sink,
+                       int32_t recent, int32_t* blocks, cudaStream_t stream);
+
+/* Attention of each row over its own blocks: tfpa_decode whose row r and kv
+ * head g see the keys of the blocks blocks[r][g][0..nsel) (DEVICE int32, as
+ * tfpa_select_blocks leaves them) up to row_pos[r].  Entries may come in any
+ * order; a negative one, and one past the row's own block, is passed over; a
+ * block that is named twice counts twice.  A row that sees no key gets out = 0
+ * and lse = -inf.  No scratch.  A page id out of range: as tfpa_decode. */
+int tfpa_decode_blocks(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
+                       const void* q, const int32_t* row_seg, const int32_t* row_pos,
+                       int32_t rows, int32_t block, int32_t nsel, const int32_t* blocks,
+                       float softmax_scale, void* out, float* lse, cudaStream_t stream);
+
 /* Launch recording for host tests (PR #1355: "a launch-recording host test
  * where a 257-row chunk issues 3 slices").  With a hook installed every
  * launch is reported; with dry_run != 0 nothing is enqueued and no CUDA call
@@ -585,7 +724,9 @@ typedef struct {
                             5 stage pages, 6 save, 7 restore, 8 verify (decode or tree
                             rows of runs with 49 or more query vectors per kv head, 17
                             over a 4-bit cache, on tensor cores; items = tiles),
-                            9 read_kv, 10 key_mass, 11 evict (choice), 12 evict (moves) */
+                            9 read_kv, 10 key_mass, 11 evict (choice), 12 evict (moves),
+                            13 rope_table, 14 write_qkv, 15 key_bounds, 16 select_blocks,
+                            17 decode_blocks */
   int32_t row0;          /* first row of the call this launch covers */
   int32_t rows;          /* rows it covers */
   int32_t runs;          /* row groups (segment, consecutive positions) */

@@ -37,7 +37,9 @@ EXPORTS = ("tfpa_pages_per_split", "tfpa_num_splits", "tfpa_write_kv", "tfpa_dec
            "tfpa_plan_decode", "tfpa_plan_launch", "tfpa_plan_set_device", "tfpa_plan_dyn_bytes",
            "tfpa_plan_dyn_pack", "tfpa_plan_shape", "tfpa_plan_capture", "tfpa_plan_replay",
            "tfpa_decode_append", "tfpa_plan_decode_append", "tfpa_row_splits", "tfpa_read_kv",
-           "tfpa_key_mass", "tfpa_evict_kv")
+           "tfpa_key_mass", "tfpa_evict_kv", "tfpa_rope_table", "tfpa_write_qkv",
+           "tfpa_key_bounds", "tfpa_select_blocks", "tfpa_decode_blocks")
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 
 
 class TfpaError(RuntimeError):
@@ -70,6 +72,27 @@ class tfpa_copy(ctypes.Structure):
     _fields_ = [("dst", ctypes.c_void_p), ("src", ctypes.c_void_p), ("bytes", ctypes.c_size_t)]
 
 
+class tfpa_rope_spec(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("attn_scale", ctypes.c_double),
+                ("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("orig_len", ctypes.c_int32)]
+
+
+class tfpa_qkv(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("rope_cos", ctypes.c_void_p),
+                ("rope_sin", ctypes.c_void_p), ("rope_pos", ctypes.c_void_p),
+                ("rope_n", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class tfpa_bounds(ctypes.Structure):
+    _fields_ = [("block", ctypes.c_int32), ("pool", ctypes.c_void_p), ("slabs", ctypes.c_void_p)]
+
+
 class tfpa_launch_record(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("row0", ctypes.c_int32), ("rows", ctypes.c_int32),
                 ("runs", ctypes.c_int32), ("items", ctypes.c_int32), ("grid", ctypes.c_int32),
@@ -79,7 +102,8 @@ class tfpa_launch_record(ctypes.Structure):
 HOOK = ctypes.CFUNCTYPE(None, ctypes.POINTER(tfpa_launch_record), ctypes.c_void_p)
 KINDS = {0: "write_kv", 1: "partial", 2: "merge", 3: "prefill", 4: "keep", 5: "stage",
          6: "save", 7: "restore", 8: "verify", 9: "read_kv", 10: "key_mass",
-         11: "evict", 12: "evict_move"}
+         11: "evict", 12: "evict_move", 13: "rope_table", 14: "write_qkv", 15: "key_bounds",
+         16: "select_blocks", 17: "decode_blocks"}
 
 _lib = None
 _addressof, _c_char = ctypes.addressof, ctypes.c_char
@@ -183,6 +207,20 @@ def lib():
         L.tfpa_evict_kv.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, vp, vp, i32, i32, vp, vp,
                                     i32, vp, vp]
         L.tfpa_evict_kv.restype = ctypes.c_int
+        L.tfpa_rope_table.argtypes = [P(tfpa_rope_spec), ctypes.c_int64, i32, vp, vp, vp]
+        L.tfpa_rope_table.restype = ctypes.c_int
+        L.tfpa_write_qkv.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, P(tfpa_qkv), vp, vp, i32,
+                                     vp, vp]
+        L.tfpa_write_qkv.restype = ctypes.c_int
+        L.tfpa_key_bounds.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, P(tfpa_bounds), vp, vp,
+                                      i32, vp]
+        L.tfpa_key_bounds.restype = ctypes.c_int
+        L.tfpa_select_blocks.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, P(tfpa_bounds), vp, vp,
+                                         vp, i32, i32, i32, i32, vp, vp]
+        L.tfpa_select_blocks.restype = ctypes.c_int
+        L.tfpa_decode_blocks.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, vp, vp, vp, i32, i32,
+                                         i32, vp, ctypes.c_float, vp, vp, vp]
+        L.tfpa_decode_blocks.restype = ctypes.c_int
         L.tfpa_set_launch_hook.argtypes = [HOOK, vp, ctypes.c_int]
         L.tfpa_set_launch_hook.restype = None
         L.tfpa_strerror.argtypes = [ctypes.c_int]
@@ -599,6 +637,141 @@ def tfpa_evict_kv(cache: Cache, segs: Sequence[Seg], keep, mass, moves, key_pos=
     _check(lib().tfpa_evict_kv(ctypes.byref(cache.c()), cs, n, _ptr(kp), _ptr(nx), int(sink),
                                int(recent), _ptr(mass), _ptr(key_pos), cap, _ptr(moves),
                                _stream(stream)), "tfpa_evict_kv")
+
+
+@dataclass(eq=False)
+class RopeSpec(_Cached):
+    """Rotary frequencies (tfpa_rope_spec): ``scaling`` is "none", or how a context stretched
+    ``factor`` times gets its frequencies ("linear", "base", "bands", "ramp")."""
+    base: float
+    rot_dim: int = HEAD_DIM
+    scaling: str = "none"
+    factor: float = 1.0
+    orig_len: int = 0
+    low: float = 0.0
+    high: float = 0.0
+    attn_scale: float = 1.0
+
+    def _make_c(self) -> tfpa_rope_spec:
+        return tfpa_rope_spec(self.base, self.factor, self.low, self.high, self.attn_scale,
+                              self.rot_dim, ROPE_SCALINGS.get(self.scaling, -1), self.orig_len)
+
+
+def tfpa_rope_table(spec: RopeSpec, first: int, cos, sin, stream=None) -> None:
+    """Rows of positions first.. of the tables ``cos`` and ``sin`` (device float32
+    ``[n][rot_dim / 2]``), as many as they have."""
+    want = (cos.shape[0], spec.rot_dim // 2)
+    for t in (cos, sin):
+        if tuple(t.shape) != want or not t.is_contiguous():
+            raise ValueError(f"expected contiguous {list(want)} tables")
+    _check(lib().tfpa_rope_table(ctypes.byref(spec.c()), int(first), int(want[0]), _ptr(cos),
+                                 _ptr(sin), _stream(stream)), "tfpa_rope_table")
+
+
+def _heads(t, rows: int, heads: int, what: str) -> int:
+    """The row stride of ``[rows][heads][128]`` rows whose heads lie one after the other."""
+    if tuple(t.shape) != (rows, heads, HEAD_DIM) or t.stride(2) != 1 or (
+            heads > 1 and t.stride(1) != HEAD_DIM):
+        raise ValueError(f"{what} must be [rows][heads][{HEAD_DIM}] with heads one after the other")
+    return t.stride(0) if rows > 1 else heads * HEAD_DIM
+
+
+def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, row_pos,
+                   q_weight=None, k_weight=None, eps: float = 1e-6, rope_cos=None, rope_sin=None,
+                   rope_pos=None, interleaved: bool = False, stream=None) -> None:
+    """A projection's rows: q and k heads normed (with a weight, device float32 ``[128]``) and
+    rotated (with ``rope_cos`` / ``rope_sin``, device float32 ``[n][rot_dim / 2]``), q into
+    ``q_out``, K and V into the cache.  ``q``, ``k`` and ``v`` are ``[rows][heads][128]`` views,
+    e.g. of one fused projection's output; q and q_out may both be None."""
+    cs, n = _segs(segs)
+    rs, rp = _i32(row_seg), _i32(row_pos)
+    rows = len(rs)
+    half = 0
+    if rope_cos is not None:
+        half = rope_cos.shape[1]
+        if tuple(rope_sin.shape) != tuple(rope_cos.shape) or not (
+                rope_cos.is_contiguous() and rope_sin.is_contiguous()):
+            raise ValueError("rope_cos and rope_sin must be contiguous tables of one shape")
+    if q_out is not None and (tuple(q_out.shape) != (rows, cache.hq, HEAD_DIM)
+                              or not q_out.is_contiguous()):
+        raise ValueError("q_out must be contiguous [rows][hq][128]")
+    a = tfpa_qkv(_ptr(q), _ptr(k), _ptr(v),
+                 0 if q is None else _heads(q, rows, cache.hq, "q"),
+                 _heads(k, rows, cache.hkv, "k"), _heads(v, rows, cache.hkv, "v"),
+                 _ptr(q_weight), _ptr(k_weight), _ptr(rope_cos), _ptr(rope_sin), _ptr(rope_pos),
+                 0 if rope_cos is None else rope_cos.shape[0], 2 * half, int(bool(interleaved)),
+                 float(eps))
+    _check(lib().tfpa_write_qkv(ctypes.byref(cache.c()), cs, n, ctypes.byref(a), _ptr(rs),
+                                _ptr(rp), rows, _ptr(q_out), _stream(stream)), "tfpa_write_qkv")
+
+
+@dataclass(eq=False)
+class Bounds(_Cached):
+    """Block bounds of a cache's keys (tfpa_bounds): ``pool`` goes with the page pool, and
+    ``slabs`` holds one tensor per segment of a call (None for a paged one)."""
+    block: int
+    pool: object = None               # bf16 [num_pages][hkv][256 / block][2][128]
+    slabs: Optional[Sequence] = None  # bf16 [hkv][slab_cap / block][2][128] each
+
+    def _make_c(self) -> tfpa_bounds:
+        arr = None
+        if self.slabs is not None:
+            arr = (ctypes.c_void_p * max(1, len(self.slabs)))(*[_ptr(s) for s in self.slabs])
+            object.__setattr__(self, "_arr", arr)
+        return tfpa_bounds(self.block, _ptr(self.pool),
+                           None if arr is None else ctypes.addressof(arr))
+
+    def of(self, nseg: int) -> tfpa_bounds:
+        if self.slabs is not None and len(self.slabs) != nseg:
+            raise ValueError("slabs holds one entry per segment")
+        return self.c()
+
+
+def make_bounds(num_pages: int, hkv: int, block: int, device="cuda") -> Bounds:
+    """Bounds for a pool of num_pages pages, in blocks of ``block`` positions."""
+    import torch
+    return Bounds(block, torch.zeros(num_pages, hkv, PAGE // block, 2, HEAD_DIM,
+                                     dtype=torch.bfloat16, device=device))
+
+
+def tfpa_key_bounds(cache: Cache, segs: Sequence[Seg], bounds: Bounds, row_seg, row_pos,
+                    stream=None) -> None:
+    """The bounds of every block that holds one of the rows, taken anew from the stored keys."""
+    cs, n = _segs(segs)
+    rs, rp = _i32(row_seg), _i32(row_pos)
+    _check(lib().tfpa_key_bounds(ctypes.byref(cache.c()), cs, n, ctypes.byref(bounds.of(n)),
+                                 _ptr(rs), _ptr(rp), len(rs), _stream(stream)), "tfpa_key_bounds")
+
+
+def _list_shape(blocks, rows: int, hkv: int) -> int:
+    if len(blocks.shape) != 3 or tuple(blocks.shape[:2]) != (rows, hkv) or not blocks.is_contiguous():
+        raise ValueError("blocks must be contiguous [rows][hkv][nsel]")
+    return int(blocks.shape[2])
+
+
+def tfpa_select_blocks(cache: Cache, segs: Sequence[Seg], bounds: Bounds, q, row_seg, row_pos,
+                       blocks, sink: int = 0, recent: int = 1, stream=None) -> None:
+    """Each row's and kv head's blocks of largest bound into ``blocks`` (device int32
+    ``[rows][hkv][nsel]``), the first ``sink`` and the last ``recent`` among them."""
+    cs, n = _segs(segs)
+    rs, rp = _i32(row_seg), _i32(row_pos)
+    nsel = _list_shape(blocks, len(rs), cache.hkv)
+    _check(lib().tfpa_select_blocks(ctypes.byref(cache.c()), cs, n, ctypes.byref(bounds.of(n)),
+                                    _ptr(q), _ptr(rs), _ptr(rp), len(rs), nsel, int(sink),
+                                    int(recent), _ptr(blocks), _stream(stream)),
+           "tfpa_select_blocks")
+
+
+def tfpa_decode_blocks(cache: Cache, segs: Sequence[Seg], q, row_seg, row_pos, blocks, block: int,
+                       softmax_scale, out, lse=None, stream=None) -> None:
+    """Attention of each row over its own blocks (``blocks`` as tfpa_select_blocks leaves it)."""
+    cs, n = _segs(segs)
+    rs, rp = _i32(row_seg), _i32(row_pos)
+    nsel = _list_shape(blocks, len(rs), cache.hkv)
+    _check(lib().tfpa_decode_blocks(ctypes.byref(cache.c()), cs, n, _ptr(q), _ptr(rs), _ptr(rp),
+                                    len(rs), int(block), nsel, _ptr(blocks),
+                                    float(softmax_scale), _ptr(out), _ptr(lse),
+                                    _stream(stream)), "tfpa_decode_blocks")
 
 
 class Plan:

@@ -1564,6 +1564,425 @@ extern "C" int tfpa_evict_kv(const tfpa_cache* c, const tfpa_seg* segs, int32_t 
   return TFPA_OK;
 }
 
+// ------------------------------------------------------------ rotary tables
+namespace {
+constexpr double kTwoPi = 6.283185307179586476925;
+constexpr int64_t kMaxRopePos = int64_t(1) << 31;
+
+// A frequency (radians a position, at most 1) as a fraction of a turn, times
+// 2^64 and rounded: its 53 bits times 1 / 2 pi to 128 bits.
+uint64_t turns_of(double f) {
+  int ex;
+  const uint64_t mant = (uint64_t)std::ldexp(std::frexp(f, &ex), 53);   // f = mant 2^(ex - 53)
+  typedef unsigned __int128 u128;
+  const u128 hi = 0x28be60db9391054aull, lo = 0x7f09d5f47d4d3770ull;    // 2^128 / 2 pi
+  const u128 prod = mant * hi + ((mant * lo) >> 64);
+  const int shift = 53 - ex;
+  return shift >= 127 ? 0 : (uint64_t)((prod + ((u128)1 << (shift - 1))) >> shift);
+}
+
+// The frequencies (radians a position) of a table's columns.
+int rope_freqs(const tfpa_rope_spec* r, double* freq) {
+  if (!r || r->rot_dim < 16 || r->rot_dim > kHeadDim || r->rot_dim % 16) return TFPA_EINVAL;
+  if (!std::isfinite(r->base) || !(r->base > 1.0) || !std::isfinite(r->attn_scale) ||
+      !(r->attn_scale > 0.0))
+    return TFPA_EINVAL;
+  const int n = r->rot_dim / 2;
+  const double d = r->rot_dim, f = r->factor;
+  if (r->scaling < TFPA_ROPE_NONE || r->scaling > TFPA_ROPE_RAMP) return TFPA_EINVAL;
+  if (r->scaling != TFPA_ROPE_NONE && (!std::isfinite(f) || !(f >= 1.0))) return TFPA_EINVAL;
+  const bool parts = r->scaling == TFPA_ROPE_BANDS || r->scaling == TFPA_ROPE_RAMP;
+  if (parts && (r->orig_len < 1 || !std::isfinite(r->low) || !std::isfinite(r->high) ||
+                !(r->low > 0.0) || !(r->high > r->low)))
+    return TFPA_EINVAL;
+  const double base =
+      r->scaling == TFPA_ROPE_BASE ? r->base * std::pow(f, d / (d - 2.0)) : r->base;
+  if (!std::isfinite(base)) return TFPA_EINVAL;
+  // TFPA_ROPE_RAMP: the dims that turn `high` and `low` times in orig_len positions
+  double first = 0.0, end = 0.0;
+  if (r->scaling == TFPA_ROPE_RAMP) {
+    const auto where = [&](double turns) {
+      return d * std::log(r->orig_len / (kTwoPi * turns)) / (2.0 * std::log(r->base));
+    };
+    first = std::max(std::floor(where(r->high)), 0.0);
+    end = std::min(std::ceil(where(r->low)), d - 1.0);
+  }
+  for (int i = 0; i < n; ++i) {
+    double w = std::pow(base, -2.0 * i / d);
+    double keep = 1.0;                       // share of the frequency that is not stretched
+    switch (r->scaling) {
+      case TFPA_ROPE_LINEAR: keep = 0.0; break;
+      case TFPA_ROPE_BANDS:
+        keep = (r->orig_len * w / kTwoPi - r->low) / (r->high - r->low);
+        break;
+      case TFPA_ROPE_RAMP: keep = 1.0 - (i - first) / std::max(end - first, 0.001); break;
+      default: break;
+    }
+    keep = std::min(1.0, std::max(0.0, keep));
+    if (r->scaling == TFPA_ROPE_LINEAR || parts) w = w * keep + w / f * (1.0 - keep);
+    freq[i] = w;
+  }
+  return TFPA_OK;
+}
+}  // namespace
+
+extern "C" int tfpa_rope_table(const tfpa_rope_spec* spec, int64_t first, int32_t n, float* cos,
+                               float* sin, cudaStream_t stream) {
+  double freq[kHeadDim / 2];
+  int e;
+  if ((e = rope_freqs(spec, freq))) return e;
+  if (n < 0 || (n > 0 && (!cos || !sin || !aligned(cos, 16) || !aligned(sin, 16))))
+    return TFPA_EINVAL;
+  if (first < 0 || first + (int64_t)n > kMaxRopePos || first > kMaxRopePos) return TFPA_ERANGE;
+  if (n == 0) return TFPA_OK;
+  if ((e = check_device())) return e;
+  TableParams p{};
+  p.cos = cos;
+  p.sin = sin;
+  p.half = spec->rot_dim / 2;
+  for (int i = 0; i < p.half; ++i) p.turns[i] = turns_of(freq[i]);
+  p.first = first;
+  p.n = n;
+  p.attn_scale = (float)spec->attn_scale;
+  record(13, 0, n, 0, n, 0, 0, 0);
+  return dry_run() ? TFPA_OK : to_err(launch_rope_table(p, stream));
+}
+
+// ------------------------------------------------------------ a projection's rows
+namespace {
+
+// Do [a, a + na) and [b, b + nb) share a byte?
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uint64_t)nb && y < x + (uint64_t)na;
+}
+
+int qkv_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const tfpa_qkv* in,
+             const int32_t* row_seg, const int32_t* row_pos, int32_t rows, void* q_out,
+             cudaStream_t stream) {
+  int e;
+  if ((e = check_cache(c)) || (e = check_segs(c, segs, nseg))) return e;
+  if (!in || !q_out != !in->q) return TFPA_EINVAL;
+  const int64_t hd = kHeadDim;
+  const int q_heads = in->q ? c->hq : 0;
+  if (rows > 0) {
+    const auto bad = [&](const void* p, int64_t stride, int64_t heads) {
+      return !p || !aligned(p, 16) || stride % 8 || stride < heads * hd || stride > INT32_MAX;
+    };
+    if ((in->q && (bad(in->q, in->q_stride, c->hq) || !aligned(q_out, 16))) ||
+        bad(in->k, in->k_stride, c->hkv) || bad(in->v, in->v_stride, c->hkv))
+      return TFPA_EINVAL;
+  }
+  if ((in->q_weight && !aligned(in->q_weight, 16)) || (in->k_weight && !aligned(in->k_weight, 16)))
+    return TFPA_EINVAL;
+  if ((in->q_weight || in->k_weight) && (!std::isfinite(in->eps) || !(in->eps > 0.f)))
+    return TFPA_EINVAL;
+  if (in->rope_cos &&
+      (!in->rope_sin || in->rope_n < 1 || !aligned(in->rope_cos, 16) ||
+       !aligned(in->rope_sin, 16) || (in->rope_pos && !aligned(in->rope_pos, 4)) ||
+       in->rot_dim < 16 || in->rot_dim > kHeadDim || in->rot_dim % 16))
+    return TFPA_EINVAL;
+  if ((int64_t)rows * (q_heads + c->hkv) > INT32_MAX - 16) return TFPA_EINVAL;
+  if (in->q && rows > 0) {
+    // q_out may be q itself, row for row; else it shares no memory with an input
+    const int64_t out_bytes = (int64_t)rows * c->hq * hd * 2;
+    const auto shares = [&](const void* p, int64_t stride, int64_t heads) {
+      return overlap(q_out, out_bytes, p, ((rows - 1) * stride + heads * hd) * 2);
+    };
+    const bool in_place = q_out == in->q && in->q_stride == c->hq * hd;
+    if ((!in_place && shares(in->q, in->q_stride, c->hq)) ||
+        shares(in->k, in->k_stride, c->hkv) || shares(in->v, in->v_stride, c->hkv))
+      return TFPA_EINVAL;
+  }
+  thread_local std::vector<Run> runs;   // reused by every call of this thread
+  if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;
+  if (in->rope_cos && !in->rope_pos)
+    for (const Run& r : runs)
+      if (r.pos0 + r.nrows > in->rope_n) return TFPA_ERANGE;
+  if (rows == 0) return TFPA_OK;
+  if ((e = check_device())) return e;
+  thread_local QkvParams p;
+  size_t ri = 0;
+  while (ri < runs.size()) {
+    std::memset(&p, 0, sizeof(p));
+    const int32_t base = runs[ri].row0;
+    int nr = 0;
+    int32_t nrows = 0;
+    while (ri < runs.size() && nr < kMaxRuns) {
+      const Run& r = runs[ri++];
+      const tfpa_seg& g = segs[r.seg];
+      WriteRun& w = p.runs[nr++];
+      w.page_table = g.page_table;
+      w.k_dst = g.page_table ? c->k_pool : g.k_slab;
+      w.v_dst = g.page_table ? c->v_pool : g.v_slab;
+      w.row0 = r.row0 - base;
+      w.nrows = r.nrows;
+      w.pos0 = r.pos0;
+      w.slab_cap = g.slab_cap;
+      w.seq_len = g.seq_len;
+      nrows = r.row0 + r.nrows - base;
+    }
+    if (in->q) {
+      p.q = static_cast<const __nv_bfloat16*>(in->q) + base * in->q_stride;
+      p.q_out = static_cast<__nv_bfloat16*>(q_out) + (int64_t)base * c->hq * hd;
+    }
+    p.k = static_cast<const __nv_bfloat16*>(in->k) + base * in->k_stride;
+    p.v = static_cast<const __nv_bfloat16*>(in->v) + base * in->v_stride;
+    p.q_stride = in->q_stride;
+    p.k_stride = in->k_stride;
+    p.v_stride = in->v_stride;
+    p.q_weight = in->q_weight;
+    p.k_weight = in->k_weight;
+    p.eps = in->eps;
+    p.rope_cos = in->rope_cos;
+    p.rope_sin = in->rope_sin;
+    p.rope_pos = in->rope_cos && in->rope_pos ? in->rope_pos + base : nullptr;
+    p.rope_n = in->rope_n;
+    p.rot_dim = in->rot_dim;
+    p.interleaved = in->interleaved;
+    p.k_scale = c->k_scale;
+    p.v_scale = c->v_scale;
+    p.err_flag = c->err_flag;
+    p.nruns = nr;
+    p.rows = nrows;
+    p.q_heads = q_heads;
+    p.hkv = c->hkv;
+    p.num_pages = c->num_pages;
+    p.kv = c->dtype;
+    const int32_t heads = nrows * (q_heads + c->hkv);
+    record(14, base, nrows, nr, heads, (heads + 15) / 16, in->q ? base * in->q_stride : 0,
+           in->q ? (int64_t)base * c->hq * hd : 0);
+    if (!dry_run())
+      if ((e = to_err(launch_write_qkv(p, stream)))) return e;
+  }
+  return TFPA_OK;
+}
+
+}  // namespace
+
+extern "C" int tfpa_write_qkv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
+                              const tfpa_qkv* in, const int32_t* row_seg, const int32_t* row_pos,
+                              int32_t rows, void* q_out, cudaStream_t stream) {
+  return no_throw([&] {
+    return qkv_impl(cache, segs, nseg, in, row_seg, row_pos, rows, q_out, stream);
+  });
+}
+
+// ------------------------------------------------------------ attention over selected blocks
+namespace {
+
+bool is_block(int32_t block) { return block == 64 || block == 128 || block == 256; }
+
+// The bounds of the segments that a call's runs use.
+int check_bounds(const tfpa_bounds* b, const tfpa_seg* segs, const std::vector<Run>& runs) {
+  if (!b || !is_block(b->block)) return TFPA_EINVAL;
+  for (const Run& r : runs) {
+    const void* at = segs[r.seg].page_table ? b->pool : b->slabs ? b->slabs[r.seg] : nullptr;
+    if (!at || !aligned(at, 16)) return TFPA_EINVAL;
+  }
+  return TFPA_OK;
+}
+
+void* bounds_of(const tfpa_bounds* b, const tfpa_seg* segs, int32_t seg) {
+  return segs[seg].page_table ? b->pool : b->slabs[seg];
+}
+
+int bounds_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const tfpa_bounds* b,
+                const int32_t* row_seg, const int32_t* row_pos, int32_t rows,
+                cudaStream_t stream) {
+  int e;
+  if ((e = check_cache(c)) || (e = check_segs(c, segs, nseg))) return e;
+  thread_local std::vector<Run> runs;   // reused by every call of this thread
+  if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;
+  if ((e = check_bounds(b, segs, runs))) return e;
+  if (rows == 0) return TFPA_OK;
+  int64_t all = 0;
+  for (const Run& r : runs)
+    all += (int64_t)c->hkv * ((r.pos0 + r.nrows - 1) / b->block - r.pos0 / b->block + 1);
+  if (all > INT32_MAX) return TFPA_EINVAL;
+  if ((e = check_device())) return e;
+  thread_local BoundsParams p;
+  size_t ri = 0;
+  while (ri < runs.size()) {
+    std::memset(&p, 0, sizeof(p));
+    const int32_t base = runs[ri].row0;
+    int nr = 0;
+    int32_t nrows = 0, items = 0;
+    while (ri < runs.size() && nr < kMaxRuns) {
+      const Run& r = runs[ri++];
+      const tfpa_seg& g = segs[r.seg];
+      BoundsRun& w = p.runs[nr++];
+      w.page_table = g.page_table;
+      w.k_base = g.page_table ? c->k_pool : g.k_slab;
+      w.bounds = bounds_of(b, segs, r.seg);
+      w.seq_len = g.seq_len;
+      w.slab_cap = g.slab_cap;
+      w.block0 = r.pos0 / b->block;
+      w.item0 = items;
+      items += (r.pos0 + r.nrows - 1) / b->block - w.block0 + 1;
+      nrows = r.row0 + r.nrows - base;
+    }
+    p.err_flag = c->err_flag;
+    p.nruns = nr;
+    p.items = items;
+    p.hkv = c->hkv;
+    p.num_pages = c->num_pages;
+    p.block = b->block;
+    record(15, base, nrows, nr, items * c->hkv, items * c->hkv, 0, 0);
+    if (!dry_run())
+      if ((e = to_err(launch_key_bounds(p, c->dtype, stream)))) return e;
+  }
+  return TFPA_OK;
+}
+
+int select_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const tfpa_bounds* b,
+                const void* q, const int32_t* row_seg, const int32_t* row_pos, int32_t rows,
+                int32_t nsel, int32_t sink, int32_t recent, int32_t* blocks,
+                cudaStream_t stream) {
+  int e;
+  if ((e = check_cache(c)) || (e = check_segs(c, segs, nseg))) return e;
+  if (rows > 0 && (!q || !aligned(q, 16) || !blocks || !aligned(blocks, 4))) return TFPA_EINVAL;
+  if (nsel < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > nsel) return TFPA_EINVAL;
+  thread_local std::vector<Run> runs;   // reused by every call of this thread
+  if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;
+  if ((e = check_bounds(b, segs, runs))) return e;
+  if ((int64_t)rows * c->hkv > INT32_MAX) return TFPA_EINVAL;
+  for (const Run& r : runs)
+    if ((r.pos0 + r.nrows - 1) / b->block + 1 > kSelectBlocks) return TFPA_ECAPACITY;
+  if (rows == 0) return TFPA_OK;
+  if ((e = check_device())) return e;
+  thread_local SelectParams p;
+  size_t ri = 0;
+  while (ri < runs.size()) {
+    std::memset(&p, 0, sizeof(p));
+    const int32_t base = runs[ri].row0;
+    int nr = 0;
+    int32_t nrows = 0;
+    while (ri < runs.size() && nr < kMaxRuns) {
+      const Run& r = runs[ri++];
+      const tfpa_seg& g = segs[r.seg];
+      SelRun& w = p.runs[nr++];
+      w.page_table = g.page_table;
+      w.bounds = bounds_of(b, segs, r.seg);
+      w.row0 = r.row0 - base;
+      w.nrows = r.nrows;
+      w.pos0 = r.pos0;
+      w.slab_cap = g.slab_cap;
+      p.cap = std::max(p.cap, (r.pos0 + r.nrows - 1) / b->block + 1);
+      nrows = r.row0 + r.nrows - base;
+    }
+    p.q = static_cast<const __nv_bfloat16*>(q) + (int64_t)base * c->hq * kHeadDim;
+    p.blocks = blocks + (int64_t)base * c->hkv * nsel;
+    p.err_flag = c->err_flag;
+    p.nruns = nr;
+    p.rows = nrows;
+    p.hq = c->hq;
+    p.hkv = c->hkv;
+    p.group = c->hq / c->hkv;
+    p.num_pages = c->num_pages;
+    p.block = b->block;
+    p.nsel = nsel;
+    p.sink = sink;
+    p.recent = recent;
+    record(16, base, nrows, nr, nrows * c->hkv, nrows * c->hkv, (int64_t)base * c->hq * kHeadDim,
+           (int64_t)base * c->hkv * nsel);
+    if (!dry_run())
+      if ((e = to_err(launch_select_blocks(p, stream)))) return e;
+  }
+  return TFPA_OK;
+}
+
+int blocks_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const void* q,
+                const int32_t* row_seg, const int32_t* row_pos, int32_t rows, int32_t block,
+                int32_t nsel, const int32_t* blocks, float scale, void* out, float* lse,
+                cudaStream_t stream) {
+  int e;
+  if ((e = check_cache(c)) || (e = check_segs(c, segs, nseg))) return e;
+  if (rows > 0 && (!q || !aligned(q, 16) || !blocks || !aligned(blocks, 4) || !out ||
+                   !aligned(out, 16) || (lse && !aligned(lse, 4))))
+    return TFPA_EINVAL;
+  if (!is_block(block) || nsel < 1 || !std::isfinite(scale) || !(scale > 0.f))
+    return TFPA_EINVAL;
+  if ((int64_t)rows * c->hq > INT32_MAX) return TFPA_EINVAL;
+  thread_local std::vector<Run> runs;   // reused by every call of this thread
+  if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;
+  if (rows == 0) return TFPA_OK;
+  if ((e = check_device())) return e;
+  thread_local BlocksParams p;
+  size_t ri = 0;
+  while (ri < runs.size()) {
+    std::memset(&p, 0, sizeof(p));
+    const int32_t base = runs[ri].row0;
+    int nr = 0;
+    int32_t nrows = 0;
+    while (ri < runs.size() && nr < kMaxRuns) {
+      const Run& r = runs[ri++];
+      const tfpa_seg& g = segs[r.seg];
+      BlocksRun& w = p.runs[nr++];
+      w.page_table = g.page_table;
+      w.k_base = g.page_table ? c->k_pool : g.k_slab;
+      w.v_base = g.page_table ? c->v_pool : g.v_slab;
+      w.row0 = r.row0 - base;
+      w.nrows = r.nrows;
+      w.pos0 = r.pos0;
+      w.slab_cap = g.slab_cap;
+      nrows = r.row0 + r.nrows - base;
+    }
+    const int64_t hd = (int64_t)c->hq * kHeadDim;
+    p.q = static_cast<const __nv_bfloat16*>(q) + base * hd;
+    p.blocks = blocks + (int64_t)base * c->hkv * nsel;
+    p.out = static_cast<__nv_bfloat16*>(out) + base * hd;
+    p.lse = lse ? lse + (int64_t)base * c->hq : nullptr;
+    p.k_scale = c->k_scale;
+    p.v_scale = c->v_scale;
+    p.err_flag = c->err_flag;
+    p.nruns = nr;
+    p.rows = nrows;
+    p.hq = c->hq;
+    p.hkv = c->hkv;
+    p.group = c->hq / c->hkv;
+    p.num_pages = c->num_pages;
+    p.block = block;
+    p.nsel = nsel;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    record(17, base, nrows, nr, nrows * c->hkv, nrows * c->hq, base * hd, base * hd);
+    if (!dry_run())
+      if ((e = to_err(launch_decode_blocks(p, c->dtype, stream)))) return e;
+  }
+  return TFPA_OK;
+}
+
+}  // namespace
+
+extern "C" int tfpa_key_bounds(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
+                               const tfpa_bounds* bounds, const int32_t* row_seg,
+                               const int32_t* row_pos, int32_t rows, cudaStream_t stream) {
+  return no_throw(
+      [&] { return bounds_impl(cache, segs, nseg, bounds, row_seg, row_pos, rows, stream); });
+}
+
+extern "C" int tfpa_select_blocks(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
+                                  const tfpa_bounds* bounds, const void* q,
+                                  const int32_t* row_seg, const int32_t* row_pos, int32_t rows,
+                                  int32_t nsel, int32_t sink, int32_t recent, int32_t* blocks,
+                                  cudaStream_t stream) {
+  return no_throw([&] {
+    return select_impl(cache, segs, nseg, bounds, q, row_seg, row_pos, rows, nsel, sink, recent,
+                       blocks, stream);
+  });
+}
+
+extern "C" int tfpa_decode_blocks(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
+                                  const void* q, const int32_t* row_seg, const int32_t* row_pos,
+                                  int32_t rows, int32_t block, int32_t nsel,
+                                  const int32_t* blocks, float softmax_scale, void* out,
+                                  float* lse, cudaStream_t stream) {
+  return no_throw([&] {
+    return blocks_impl(cache, segs, nseg, q, row_seg, row_pos, rows, block, nsel, blocks,
+                       softmax_scale, out, lse, stream);
+  });
+}
+
 extern "C" void tfpa_set_launch_hook(tfpa_launch_hook hook, void* user, int dry_run_flag) {
   g_hook_user.store(user, std::memory_order_relaxed);
   g_hook_dry.store(hook ? dry_run_flag : 0, std::memory_order_relaxed);

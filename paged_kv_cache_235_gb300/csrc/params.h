@@ -322,7 +322,116 @@ struct EvictParams {
   int32_t key_slots;          // keys that one of them can keep in shared memory
 };
 
+// Rotary tables.
+struct TableParams {
+  float* cos;                 // [n][half]
+  float* sin;
+  uint64_t turns[kHeadDim / 2];   // each frequency as a fraction of a turn, times 2^64
+  int64_t first;              // position of the first row
+  int32_t n;
+  int32_t half;               // frequencies: rot_dim / 2
+  float attn_scale;
+};
+
+// A projection's rows: norm, rotation, q out, K and V stored.
+struct QkvParams {
+  WriteRun runs[kMaxRuns];
+  const __nv_bfloat16* q;     // rows of this launch, row strides in elements
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int64_t q_stride, k_stride, v_stride;
+  __nv_bfloat16* q_out;       // [rows][q_heads][128]
+  const float* q_weight;      // [128], or nullptr: not normed
+  const float* k_weight;
+  const float* rope_cos;      // [rope_n][rot_dim / 2], or nullptr: not rotated
+  const float* rope_sin;
+  const int32_t* rope_pos;    // rows of this launch, or nullptr: the storage positions
+  const float* k_scale;
+  const float* v_scale;
+  int32_t* err_flag;
+  float eps;
+  int32_t rope_n, rot_dim, interleaved;
+  int32_t nruns;
+  int32_t rows;
+  int32_t q_heads;            // 0: no q
+  int32_t hkv;
+  int32_t num_pages;
+  int32_t kv;                 // KvType
+};
+
+// Bounds of the blocks of a launch: each run is consecutive blocks of a stream.
+struct BoundsRun {
+  const int32_t* page_table;  // nullptr => slab
+  const void* k_base;         // pool or slab
+  void* bounds;               // the pool's or the slab's
+  int32_t seq_len;
+  int32_t slab_cap;
+  int32_t block0;             // first block
+  int32_t item0;              // blocks of the runs before
+};
+struct BoundsParams {
+  BoundsRun runs[kMaxRuns];
+  int32_t* err_flag;
+  int32_t nruns;
+  int32_t items;              // blocks of all runs
+  int32_t hkv;
+  int32_t num_pages;
+  int32_t block;
+};
+
+// Selection and attention over selected blocks.
+constexpr int32_t kSelectBlocks = 18432;   // blocks whose keys a CTA's shared memory holds
+struct SelRun {
+  const int32_t* page_table;  // nullptr => slab
+  const void* bounds;
+  int32_t row0, nrows, pos0;
+  int32_t slab_cap;
+};
+struct SelectParams {
+  SelRun runs[kMaxRuns];
+  const __nv_bfloat16* q;     // rows of this launch: [rows][hq][128]
+  int32_t* blocks;            // [rows][hkv][nsel]
+  int32_t* err_flag;
+  int32_t nruns;
+  int32_t rows;
+  int32_t hq, hkv, group;
+  int32_t num_pages;
+  int32_t block;
+  int32_t nsel;
+  int32_t sink, recent;
+  int32_t cap;                // blocks of the longest row
+};
+struct BlocksRun {
+  const int32_t* page_table;  // nullptr => slab
+  const void* k_base;
+  const void* v_base;
+  int32_t row0, nrows, pos0;
+  int32_t slab_cap;
+};
+struct BlocksParams {
+  BlocksRun runs[kMaxRuns];
+  const __nv_bfloat16* q;     // rows of this launch: [rows][hq][128]
+  const int32_t* blocks;      // [rows][hkv][nsel]
+  __nv_bfloat16* out;         // [rows][hq][128]
+  float* lse;                 // [rows][hq] or nullptr
+  const float* k_scale;
+  const float* v_scale;
+  int32_t* err_flag;
+  int32_t nruns;
+  int32_t rows;
+  int32_t hq, hkv, group;
+  int32_t num_pages;
+  int32_t block;
+  int32_t nsel;
+  float scale_log2;
+};
+
 // Launchers (defined next to their kernels).
+cudaError_t launch_rope_table(const TableParams& p, cudaStream_t s);
+cudaError_t launch_write_qkv(const QkvParams& p, cudaStream_t s);
+cudaError_t launch_key_bounds(const BoundsParams& p, int kv, cudaStream_t s);
+cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t s);
+cudaError_t launch_decode_blocks(const BlocksParams& p, int kv, cudaStream_t s);
 cudaError_t launch_key_mass(const MassParams& p, int kv, int grid, cudaStream_t s);
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s);
 cudaError_t launch_evict_move(const EvictParams& p, int kv, cudaStream_t s);
