@@ -1,0 +1,564 @@
+// Attention of each row over its own blocks of keys (tfpa_decode_blocks).
+//
+// A work item is a row, a kv head and up to 8 or 16 of its query heads; its
+// list of blocks is cut into equal parts, one CTA each, and the item's CTAs are
+// a cluster: their parts' states (running maximum, sum, unnormalised output)
+// meet in distributed shared memory, so there is one launch, no scratch and no
+// merge kernel.  The parts follow from the list's length alone, so a row's bytes
+// do not depend on its batch.
+// Per CTA:
+//   warp 4      producer: a lane a list entry looks the entry and its page up
+//               (the chain of two loads runs once a 32 entries), then blocks
+//               stream in as stages of 64 keys, K and V (TMA tiles with 128B
+//               swizzle; a 4-bit cache's codes and scales as bulk copies);
+//   warps 0..3  consumers: 16 keys of every stage each.  Both products have the
+//               keys' side as the MMA's 16 rows and the query vectors as its 8
+//               columns (with the vectors as rows, 4 query heads would leave 12
+//               of 16 rows empty): S^T = K Q^T, weights transposed in registers,
+//               O^T = V^T P^T.  Each warp keeps its own softmax state.
+// What bounds it is the stream of K and V out of memory; the ring's stages keep
+// it going while the consumers' chain of score, exponential and output runs.
+#include "cluster.cuh"
+#include "common.cuh"
+#include "kvstore.cuh"
+#include "params.h"
+
+namespace tfpa {
+namespace {
+
+constexpr int kConsumers = 4;
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kStageKeys = 64;
+constexpr float kRescaleThreshold = 8.0f;   // log2 units
+
+template <int KV>
+struct Cfg {
+  static constexpr bool kF16 = KV != kKvBf16;          // f16 operands, kv head scales
+  static constexpr int kHalfStage =                    // K of 64 keys, or V
+      kStageKeys * (KV == kKvBf16 ? 256 : KV == kKvFp8 ? 128 : kFp4CodeBytes + kFp4ScaleBytes);
+  static constexpr int kStageBytes = 2 * kHalfStage;
+  static constexpr int kStages = KV == kKvBf16 ? 3 : KV == kKvFp8 ? 4 : 6;
+  static constexpr int kRing = kStages * kStageBytes;
+};
+
+struct Shared {
+  uint64_t full[8], empty[8];
+  int key0[8];                 // first key of a stage; -1: the list's end
+  int lost;                    // a wait gave up
+  float m[kConsumers][16], l[kConsumers][16];
+  float part_m[16], part_l[16];   // the CTA's part, read by the cluster
+};
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+// The key (of 16) in row i of a score tile.  4 bits: a lane's V rows are those
+// of columns 2c and 2c + 1 of the weights; rows c and 4 + (c ^ 1) lie next to
+// each other over the lanes, and neighbouring K rows, 64 bytes each, in
+// different halves of the banks.
+template <int KV>
+__device__ __forceinline__ int key_of(int i) {
+  if (KV != kKvFp4) return i;
+  return (i & 8) + (i & 1 ? 4 + (((i >> 1) & 3) ^ 1) : (i >> 1) & 3);
+}
+
+// Head dim of row i (0..15) of output tile t.
+template <int KV>
+__device__ __forceinline__ int dim_of(int t, int i) {
+  if (KV == kKvBf16) return 16 * t + i;
+  if (KV == kKvFp8) return 16 * t + 2 * (i & 7) + (i >> 3);
+  return 16 * (i & 7) + 2 * t + (i >> 3);
+}
+
+// K rows `row` of the stage as operand registers: the 32 dims that this lane
+// (column c of its quad) holds of a row, in the order of load_q.
+template <int KV>
+__device__ __forceinline__ void load_k(uint32_t sb, int row, int c, uint32_t (&k)[16]) {
+  if (KV == kKvBf16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 w = lds128(swz128(sb + (i >> 1) * 8192, row, 2 * c + (i & 1)));
+      k[4 * i] = w.x;
+      k[4 * i + 1] = w.y;
+      k[4 * i + 2] = w.z;
+      k[4 * i + 3] = w.w;
+    }
+  } else if (KV == kKvFp8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 w = lds128(swz128(sb, row, 2 * c + i));
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        k[8 * i + 2 * j] = e4m3x2_to_f16x2((uint16_t)(ws[j] & 0xFFFF));
+        k[8 * i + 2 * j + 1] = e4m3x2_to_f16x2((uint16_t)(ws[j] >> 16));
+      }
+    }
+  } else {
+    const uint4 w = lds128(sb + row * kFp4CodeBytes + 16 * c);
+    const uint32_t s2 = e4m3x2_to_f16x2(
+        (uint16_t)lds16(sb + kStageKeys * kFp4CodeBytes + row * kFp4ScaleBytes + 2 * c));
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t h[4];
+      e2m1x8_to_f16x8(ws[j], h);
+      const uint32_t s = prmt(s2, s2, j < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) k[4 * j + u] = hmul2(h[u], s);
+    }
+  }
+}
+
+// Query vector `h` (nullptr: none) as this lane's 32 dims in operand registers,
+// and the factor of its scores.  f16 operands: scaled by a power of two into
+// f16 range, exact for every element within 2^28 of the vector's largest.
+template <int KV>
+__device__ __forceinline__ void load_q(const __nv_bfloat16* h, int c, float scale,
+                                       uint32_t (&q)[16], float& factor) {
+  const uint4* qp = reinterpret_cast<const uint4*>(h);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = KV == kKvBf16 ? (i >> 1) * 8 + 2 * c + (i & 1) : 4 * c + i;
+    const uint4 w = h ? __ldg(qp + at) : make_uint4(0, 0, 0, 0);
+    q[4 * i] = w.x;
+    q[4 * i + 1] = w.y;
+    q[4 * i + 2] = w.z;
+    q[4 * i + 3] = w.w;
+  }
+  factor = scale;
+  if (!Cfg<KV>::kF16) return;
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    amax = fmaxf(amax, fabsf(__uint_as_float(q[j] << 16)));
+    amax = fmaxf(amax, fabsf(__uint_as_float(q[j] & 0xFFFF0000u)));
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  int ex;
+  frexpf(amax, &ex);
+  ex = max(min(ex, 120), -100);
+  const float up = __int_as_float((127 + 14 - ex) << 23);
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    q[j] = pack_f16x2(__uint_as_float(q[j] << 16) * up,
+                      __uint_as_float(q[j] & 0xFFFF0000u) * up);
+  factor = scale * __int_as_float((127 - 14 + ex) << 23);
+}
+
+// O^T += V^T P^T over 16 keys at rows r0.. of the stage (V at sb).  keep:
+// masks of a lane's keys (columns 2c, 2c + 1 and 2c + 8, 2c + 9), which zero
+// what lies behind the row's position (a weight of 0 would not: 0 NaN = NaN).
+template <int KV, int NT>
+__device__ __forceinline__ void add_pv(uint32_t sb, int r0, int lane, const uint32_t (&pb)[NT][2],
+                                       uint32_t keep0, uint32_t keep1, float (&o)[NT][8][4]) {
+  const int gq = lane >> 2, c = lane & 3;
+  auto mma = [&](int t, const uint32_t (&a)[4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (Cfg<KV>::kF16)
+        mma_f16_free(o[n][t], a, pb[n][0], pb[n][1]);
+      else
+        mma_bf16(o[n][t], a, pb[n][0], pb[n][1]);
+    }
+  };
+  if (KV == kKvBf16) {
+    // matrices: keys 0-7 and 8-15 (lane bit 4) of two chunks of 8 dims (bit 3)
+    const int row = r0 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      uint32_t a[4];
+      ldmatrix_x4_trans(a, swz128(sb + (t >> 2) * 8192, row, (2 * t & 7) + ((lane >> 3) & 1)));
+      a[0] &= keep0;
+      a[1] &= keep0;
+      a[2] &= keep1;
+      a[3] &= keep1;
+      mma(t, a);
+    }
+  } else if (KV == kKvFp8) {
+    // a 16-bit column holds dims 2i and 2i + 1: rows i and i + 8 of a tile
+    const int row = r0 + (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+    for (int t = 0; t < 8; t += 2) {
+      uint32_t w[4];
+      ldmatrix_x4_trans(w, swz128(sb, row, t + (lane >> 4)));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t x = prmt(w[2 * u] & keep0, 0, 0x3120), y = prmt(w[2 * u + 1] & keep1, 0, 0x3120);
+        const uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)(x & 0xFFFF)),
+                               e4m3x2_to_f16x2((uint16_t)(x >> 16)),
+                               e4m3x2_to_f16x2((uint16_t)(y & 0xFFFF)),
+                               e4m3x2_to_f16x2((uint16_t)(y >> 16))};
+        mma(t + u, a);
+      }
+    }
+  } else {
+    // dims 16 gq .. 16 gq + 15 of four keys: one scale each
+    uint2 w[4];
+    uint32_t s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = r0 + key_of<KV>(2 * c + (i & 1) + 8 * (i >> 1));
+      w[i] = lds64(sb + row * kFp4CodeBytes + 8 * gq);
+      s[i] = lds8(sb + kStageKeys * kFp4CodeBytes + row * kFp4ScaleBytes + gq);
+    }
+    const uint32_t s01 = e4m3x2_to_f16x2((uint16_t)((s[0] | (s[1] << 8)) & prmt(keep0, 0, 0x4420)));
+    const uint32_t s23 = e4m3x2_to_f16x2((uint16_t)((s[2] | (s[3] << 8)) & prmt(keep1, 0, 0x4420)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // a byte of two keys' equal nibbles converts to a pair along the keys
+      uint32_t f[2][2][4];                 // [keys 0-7, 8-15][even, odd dims][pair]
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t A = i ? w[2 * k].y : w[2 * k].x, B = i ? w[2 * k + 1].y : w[2 * k + 1].x;
+        e2m1x8_to_f16x8((A & 0x0F0F0F0Fu) | ((B & 0x0F0F0F0Fu) << 4), f[k][0]);
+        e2m1x8_to_f16x8(((A >> 4) & 0x0F0F0F0Fu) | (B & 0xF0F0F0F0u), f[k][1]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a[4] = {hmul2(f[0][0][j], s01), hmul2(f[0][1][j], s01),
+                               hmul2(f[1][0][j], s23), hmul2(f[1][1][j], s23)};
+        mma(4 * i + j, a);
+      }
+    }
+  }
+}
+
+// The producer warp.  False if a wait gave up.
+template <int KV>
+__device__ bool produce(const BlocksParams& p, const BlocksRun& run, const int32_t* list, int i0,
+                        int i1, int pos, int g, uint8_t* ring, Shared& sh) {
+  using C = Cfg<KV>;
+  const int lane = threadIdx.x & 31;
+  uint32_t stage = 0;
+  for (int base = i0; base < i1; base += 32) {
+    // a lane an entry: the block, and the storage row of its first key
+    int b = -1, row0 = 0;
+    if (base + lane < i1) b = __ldg(list + base + lane);
+    if (b >= 0 && (int64_t)b * p.block > pos) b = -1;
+    if (b >= 0) {
+      const int key0 = b * p.block;
+      if (run.page_table) {
+        const int pid = __ldg(run.page_table + (key0 >> 8));
+        if ((unsigned)pid < (unsigned)p.num_pages) {
+          row0 = (pid * p.hkv + g) * kPage + (key0 & (kPage - 1));
+        } else {
+          flag_error(p.err_flag, kErrBadPage);
+          b = -1;
+        }
+      } else {
+        row0 = g * run.slab_cap + key0;
+      }
+    }
+    uint32_t todo = __ballot_sync(0xffffffffu, b >= 0);
+    while (todo) {
+      const int l = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int key0 = __shfl_sync(0xffffffffu, b, l) * p.block;
+      const int r0 = __shfl_sync(0xffffffffu, row0, l);
+      const int n = min(p.block, pos - key0 + 1);
+      for (int k = 0; k < n; k += kStageKeys, ++stage) {
+        const int buf = stage % C::kStages;
+        if (!warp_wait(&sh.empty[buf], ((stage / C::kStages) & 1) ^ 1, p.err_flag)) return false;
+        if (lane == 0) {
+          uint64_t* fb = &sh.full[buf];
+          uint8_t* sk = ring + (size_t)buf * C::kStageBytes;
+          uint8_t* sv = sk + C::kHalfStage;
+          const int y = r0 + k;
+          sh.key0[buf] = key0 + k;
+          mbar_arrive_expect_tx(fb, C::kStageBytes);
+          if (KV == kKvFp4) {
+            const size_t codes = fp4_codes(y), scales = fp4_scales(y);
+            constexpr uint32_t kCodes = kStageKeys * kFp4CodeBytes;
+            constexpr uint32_t kScales = kStageKeys * kFp4ScaleBytes;
+            const uint8_t* kb = static_cast<const uint8_t*>(run.k_base);
+            const uint8_t* vb = static_cast<const uint8_t*>(run.v_base);
+            bulk_load(sk, kb + codes, kCodes, fb);
+            bulk_load(sk + kCodes, kb + scales, kScales, fb);
+            bulk_load(sv, vb + codes, kCodes, fb);
+            bulk_load(sv + kCodes, vb + scales, kScales, fb);
+          } else {
+            const KVMaps& m = p.maps[run.src];
+            tma_load_2d(sk, &m.k, 0, y, fb);
+            if (KV == kKvBf16) tma_load_2d(sk + 8192, &m.k, 64, y, fb);
+            tma_load_2d(sv, &m.v, 0, y, fb);
+            if (KV == kKvBf16) tma_load_2d(sv + 8192, &m.v, 64, y, fb);
+          }
+        }
+      }
+    }
+  }
+  const int buf = stage % C::kStages;
+  if (!warp_wait(&sh.empty[buf], ((stage / C::kStages) & 1) ^ 1, p.err_flag)) return false;
+  if (lane == 0) {
+    sh.key0[buf] = -1;
+    mbar_arrive(&sh.full[buf]);
+  }
+  return true;
+}
+
+template <int KV, int NT>
+__global__ void __launch_bounds__(kThreads)
+    decode_blocks_kernel(const __grid_constant__ BlocksParams p) {
+  using C = Cfg<KV>;
+  constexpr int kVecs = 8 * NT;
+  __shared__ Shared sh;
+  extern __shared__ uint8_t ring_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(ring_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], kConsumers);
+    }
+    sh.lost = 0;
+    fence_mbar_init();
+  }
+  allow_next_grid();
+  __syncthreads();
+  wait_prior_grid();
+  // ---- the item, and this CTA's part of its list
+  const int part = blockIdx.x % p.parts;
+  int item = blockIdx.x / p.parts;
+  const int qtiles = (p.group + kVecs - 1) / kVecs;
+  const int qt = item % qtiles;
+  item /= qtiles;
+  const int row = item / p.hkv, g = item % p.hkv;
+  int ri = 0;
+  while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
+  const BlocksRun& run = p.runs[ri];
+  const int pos = run.pos0 + (row - run.row0);
+  const int32_t* list = p.blocks + ((size_t)row * p.hkv + g) * p.nsel;
+  const int i0 = (int)((int64_t)p.nsel * part / p.parts);
+  const int i1 = (int)((int64_t)p.nsel * (part + 1) / p.parts);
+  const int vecs = min(kVecs, p.group - qt * kVecs);     // query vectors of this item
+  const size_t head0 = (size_t)row * p.hq + (size_t)g * p.group + qt * kVecs;
+
+  const int gq = lane >> 2, c = lane & 3;
+  float o[NT][8][4], m[NT][2], l[NT][2];
+  if (warp == kConsumers) {
+    if (!produce<KV>(p, run, list, i0, i1, pos, g, ring, sh)) sh.lost = 1;
+  } else {
+    uint32_t q[NT][16];
+    float sc[NT][2];
+    const float scale = C::kF16 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int v = 8 * n + gq;
+      float f;
+      load_q<KV>(v < vecs ? p.q + (head0 + v) * kHeadDim : nullptr, c, scale, q[n], f);
+      // the factors of the vectors in this lane's columns, 2c and 2c + 1
+      sc[n][0] = __shfl_sync(0xffffffffu, f, 8 * c);
+      sc[n][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.f;
+    }
+    const int r0 = 16 * warp;
+    for (uint32_t stage = 0;; ++stage) {
+      const int buf = stage % C::kStages;
+      if (!warp_wait(&sh.full[buf], (stage / C::kStages) & 1, p.err_flag)) {
+        sh.lost = 1;
+        break;
+      }
+      const int first = sh.key0[buf];
+      if (first < 0) break;
+      const int key0 = first + r0;
+      if (key0 <= pos) {
+        const uint32_t sk = smem_u32(ring + (size_t)buf * C::kStageBytes);
+        // ---- S^T = K Q^T: keys key_of(gq), key_of(gq + 8); vectors 2c, 2c + 1
+        float s[NT][4];
+        {
+          uint32_t ka[16], kb[16];
+          load_k<KV>(sk, r0 + key_of<KV>(gq), c, ka);
+          load_k<KV>(sk, r0 + key_of<KV>(gq + 8), c, kb);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t a[4] = {ka[2 * ks], kb[2 * ks], ka[2 * ks + 1], kb[2 * ks + 1]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (C::kF16)
+                mma_f16_free(s[n], a, q[n][2 * ks], q[n][2 * ks + 1]);
+              else
+                mma_bf16(s[n], a, q[n][2 * ks], q[n][2 * ks + 1]);
+            }
+          }
+        }
+        const bool see0 = key0 + key_of<KV>(gq) <= pos, see1 = key0 + key_of<KV>(gq + 8) <= pos;
+        // ---- online softmax over the tile's keys, a column a vector
+        uint32_t pb[NT][2];
+        bool resc = false;
+        float al[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s[n][e] = see0 ? s[n][e] * sc[n][e] : -INFINITY;
+            s[n][2 + e] = see1 ? s[n][2 + e] * sc[n][e] : -INFINITY;
+            float mx = fmaxf(s[n][e], s[n][2 + e]);
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            al[n][e] = 1.f;
+            if (mx > m[n][e] + kRescaleThreshold) {      // the maximum moves by 2^8 at least
+              al[n][e] = fast_exp2(m[n][e] - mx);
+              l[n][e] *= al[n][e];
+              m[n][e] = mx;
+              resc = true;
+            }
+            const float base = m[n][e] == -INFINITY ? 0.f : m[n][e];
+            s[n][e] = fast_exp2(s[n][e] - base);
+            s[n][2 + e] = fast_exp2(s[n][2 + e] - base);
+            l[n][e] += s[n][e] + s[n][2 + e];
+          }
+          // weights rounded to the operands' 16 bits; the sums are not
+          const uint32_t w0 = C::kF16 ? pack_f16x2(s[n][0], s[n][1]) : pack_bf16x2(s[n][0], s[n][1]);
+          const uint32_t w1 = C::kF16 ? pack_f16x2(s[n][2], s[n][3]) : pack_bf16x2(s[n][2], s[n][3]);
+          pb[n][0] = transpose8x8(w0);
+          pb[n][1] = transpose8x8(w1);
+        }
+        if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[n][t][j] *= al[n][j & 1];
+        }
+        // ---- O^T += V^T P^T
+        auto mask = [&](int i) {
+          return (key0 + key_of<KV>(2 * c + i) <= pos ? 0xFFFFu : 0u) |
+                 (key0 + key_of<KV>(2 * c + 1 + i) <= pos ? 0xFFFF0000u : 0u);
+        };
+        add_pv<KV, NT>(sk + C::kHalfStage, r0, lane, pb, mask(0), mask(8), o);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[buf]);
+    }
+    // ---- this warp's state
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+        if (gq == 0) {
+          sh.m[warp][8 * n + 2 * c + e] = m[n][e];
+          sh.l[warp][8 * n + 2 * c + e] = l[n][e];
+        }
+      }
+  }
+  __syncthreads();
+  if (sh.lost) let_copies_land();
+  // ---- the warps' states, folded: [warp][vector][dim] in the ring, which every
+  // load has left, then [vector][dim] behind them
+  float* fold = reinterpret_cast<float*>(ring);
+  float* mine = fold + kConsumers * kVecs * kHeadDim;
+  if (warp < kConsumers) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          fold[(warp * kVecs + 8 * n + 2 * c + (j & 1)) * kHeadDim +
+               dim_of<KV>(t, gq + 8 * (j >> 1))] = o[n][t][j];
+  }
+  __syncthreads();
+  for (int i = tid; i < vecs * (kHeadDim / 4); i += kThreads) {
+    const int v = i / (kHeadDim / 4), d = i % (kHeadDim / 4) * 4;
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, sh.m[w][v]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kConsumers; ++w) {
+      const float a = sh.m[w][v] == -INFINITY ? 0.f : fast_exp2(sh.m[w][v] - M);
+      const float4 x = *reinterpret_cast<const float4*>(fold + (w * kVecs + v) * kHeadDim + d);
+      L = fmaf(a, sh.l[w][v], L);
+      acc.x = fmaf(a, x.x, acc.x);
+      acc.y = fmaf(a, x.y, acc.y);
+      acc.z = fmaf(a, x.z, acc.z);
+      acc.w = fmaf(a, x.w, acc.w);
+    }
+    *reinterpret_cast<float4*>(mine + v * kHeadDim + d) = acc;
+    if (d == 0) {
+      sh.part_m[v] = M;
+      sh.part_l[v] = L;
+    }
+  }
+  // ---- the parts, in the cluster's shared memory: each CTA finishes its share
+  // of the item's elements
+  const float vs = C::kF16 ? __ldg(p.v_scale + g) : 1.f;
+  __syncwarp();
+  if (p.parts > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  for (int i = part * kThreads + tid; i < vecs * (kHeadDim / 4); i += p.parts * kThreads) {
+    const int v = i / (kHeadDim / 4), d = i % (kHeadDim / 4) * 4;
+    float M = -INFINITY, L = 0.f;
+    const uint32_t pm = smem_u32(&sh.part_m[v]), pl = smem_u32(&sh.part_l[v]);
+    for (int r = 0; r < p.parts; ++r)
+      M = fmaxf(M, __uint_as_float(ld_cluster_u32(mapa_shared(pm, r))));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < p.parts; ++r) {
+      const float mr = __uint_as_float(ld_cluster_u32(mapa_shared(pm, r)));
+      const float a = mr == -INFINITY ? 0.f : fast_exp2(mr - M);
+      L = fmaf(a, __uint_as_float(ld_cluster_u32(mapa_shared(pl, r))), L);
+      const float4 x = ld_cluster_f4(mapa_shared(smem_u32(mine + v * kHeadDim + d), r));
+      acc.x = fmaf(a, x.x, acc.x);
+      acc.y = fmaf(a, x.y, acc.y);
+      acc.z = fmaf(a, x.z, acc.z);
+      acc.w = fmaf(a, x.w, acc.w);
+    }
+    const float f = L == 0.f ? 0.f : vs / L;         // no key: zeros
+    uint2 w;
+    w.x = pack_bf16x2(acc.x * f, acc.y * f);
+    w.y = pack_bf16x2(acc.z * f, acc.w * f);
+    *reinterpret_cast<uint2*>(p.out + (head0 + v) * kHeadDim + d) = w;
+    if (d == 0 && p.lse)
+      p.lse[head0 + v] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  }
+  __syncwarp();
+  if (p.parts > 1) cluster_sync();                   // read, before a CTA's memory goes
+}
+
+template <int KV, int NT>
+cudaError_t launch(const BlocksParams& p, cudaStream_t s) {
+  constexpr int kSmem = Cfg<KV>::kRing + 1024;
+  static_assert((kConsumers + 1) * 8 * NT * kHeadDim * 4 <= Cfg<KV>::kRing, "fold buffers");
+  static PerDeviceOnce configured;
+  const cudaError_t e = configured.run([] {
+    return cudaFuncSetAttribute(decode_blocks_kernel<KV, NT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  const int qtiles = (p.group + 8 * NT - 1) / (8 * NT);
+  const dim3 grid(p.rows * p.hkv * qtiles * p.parts);
+  return launch_pdl_cluster(decode_blocks_kernel<KV, NT>, grid, dim3(kThreads), kSmem, s, p,
+                            p.parts);
+}
+
+template <int KV>
+cudaError_t launch_of(const BlocksParams& p, cudaStream_t s) {
+  return p.group <= 8 ? launch<KV, 1>(p, s) : launch<KV, 2>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_blocks(const BlocksParams& p, int kv, cudaStream_t s) {
+  switch (kv) {
+    case kKvBf16: return launch_of<kKvBf16>(p, s);
+    case kKvFp8: return launch_of<kKvFp8>(p, s);
+    default: return launch_of<kKvFp4>(p, s);
+  }
+}
+
+}  // namespace tfpa

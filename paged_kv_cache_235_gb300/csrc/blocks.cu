@@ -424,86 +424,6 @@ __global__ void __launch_bounds__(kSelThreads)
   for (uint32_t i = filled + tid; i < (uint32_t)p.nsel; i += kSelThreads) out[i] = -1;
 }
 
-// ---------------------------------------------------------------- attention
-constexpr int kAttThreads = 128;
-
-// One CTA a (row, query head): a warp a key, four head dims a lane.
-template <int KV>
-__global__ void __launch_bounds__(kAttThreads)
-    decode_blocks_kernel(const __grid_constant__ BlocksParams p) {
-  __shared__ float sm[4], sl[4], so[4][kHeadDim];
-  allow_next_grid();
-  wait_prior_grid();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x / p.hq, h = blockIdx.x % p.hq, g = h / p.group;
-  int ri = 0;
-  while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
-  const BlocksRun& run = p.runs[ri];
-  const int pos = run.pos0 + (row - run.row0);
-  const int32_t* list = p.blocks + ((size_t)row * p.hkv + g) * p.nsel;
-  const __nv_bfloat16* qp = p.q + ((size_t)row * p.hq + h) * kHeadDim + lane * 4;
-  float q[4], o[4] = {0.f, 0.f, 0.f, 0.f};
-  const float sk = KV == kKvBf16 ? 1.f : __ldg(p.k_scale + g);
-  const float sv = KV == kKvBf16 ? 1.f : __ldg(p.v_scale + g);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = __bfloat162float(qp[i]);
-  float m = -INFINITY, l = 0.f;
-  for (int i = 0; i < p.nsel; ++i) {
-    const int b = __ldg(list + i);
-    if (b < 0 || (int64_t)b * p.block > pos) continue;
-    const int key0 = b * p.block;
-    size_t row0;
-    if (run.page_table) {
-      const int pid = __ldg(run.page_table + (key0 >> 8));
-      if ((unsigned)pid >= (unsigned)p.num_pages) {
-        if (threadIdx.x == 0) flag_error(p.err_flag, kErrBadPage);
-        continue;
-      }
-      row0 = ((size_t)pid * p.hkv + g) * kPage + (key0 & (kPage - 1));
-    } else {
-      row0 = (size_t)g * run.slab_cap + key0;
-    }
-    const int n = min(p.block, pos - key0 + 1);
-    for (int r = warp; r < n; r += 4) {
-      float x[8];
-      load8<KV>(run.k_base, row0 + r, lane >> 1, x);
-      float s = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s = fmaf(q[j], lane & 1 ? x[4 + j] : x[j], s);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      s *= p.scale_log2 * sk;
-      load8<KV>(run.v_base, row0 + r, lane >> 1, x);
-      const float mn = fmaxf(m, s);
-      const float a = m == mn ? 1.f : fast_exp2(m - mn), e = fast_exp2(s - (mn == -INFINITY ? 0.f : mn));
-      l = l * a + e;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = o[j] * a + e * (lane & 1 ? x[4 + j] : x[j]);
-      m = mn;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) so[warp][lane * 4 + j] = o[j];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  __syncthreads();
-  float M = -INFINITY, L = 0.f, acc = 0.f;
-  for (int w = 0; w < 4; ++w) M = fmaxf(M, sm[w]);
-  const float base = M == -INFINITY ? 0.f : M;
-  for (int w = 0; w < 4; ++w) {
-    const float a = fast_exp2(sm[w] - base);
-    L += sl[w] * a;
-    acc += so[w][threadIdx.x] * a;
-  }
-  const size_t at = (size_t)row * p.hq + h;
-  static_cast<__nv_bfloat16*>(p.out)[at * kHeadDim + threadIdx.x] =
-      __float2bfloat16_rn(L > 0.f || L != L ? acc / L * sv : 0.f);
-  if (p.lse && threadIdx.x == 0)
-    p.lse[at] = L > 0.f || L != L ? 0.6931471805599453f * (M + log2f(L)) : -INFINITY;
-}
-
 }  // namespace
 
 cudaError_t launch_key_bounds(const BoundsParams& p, int kv, cudaStream_t s) {
@@ -524,15 +444,6 @@ cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   return launch_pdl(select_blocks_kernel, dim3(p.rows * p.hkv), dim3(kSelThreads),
                     (size_t)p.cap * 12, s, p);
-}
-
-cudaError_t launch_decode_blocks(const BlocksParams& p, int kv, cudaStream_t s) {
-  const dim3 grid(p.rows * p.hq), block(kAttThreads);
-  switch (kv) {
-    case kKvBf16: return launch_pdl(decode_blocks_kernel<kKvBf16>, grid, block, 0, s, p);
-    case kKvFp8: return launch_pdl(decode_blocks_kernel<kKvFp8>, grid, block, 0, s, p);
-    default: return launch_pdl(decode_blocks_kernel<kKvFp4>, grid, block, 0, s, p);
-  }
 }
 
 }  // namespace tfpa

@@ -1892,6 +1892,13 @@ int select_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const t
   return TFPA_OK;
 }
 
+// CTAs that share a row's list: one for every four stages of 64 keys, up to a
+// cluster of eight.  A function of the list's length only, so a row's bytes do
+// not depend on its batch.
+int32_t block_parts(int32_t block, int32_t nsel) {
+  return (int32_t)std::min<int64_t>(8, ((int64_t)nsel * (block / 64) + 3) / 4);
+}
+
 int blocks_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const void* q,
                 const int32_t* row_seg, const int32_t* row_pos, int32_t rows, int32_t block,
                 int32_t nsel, const int32_t* blocks, float scale, void* out, float* lse,
@@ -1903,9 +1910,12 @@ int blocks_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
     return TFPA_EINVAL;
   if (!is_block(block) || nsel < 1 || !std::isfinite(scale) || !(scale > 0.f))
     return TFPA_EINVAL;
-  if ((int64_t)rows * c->hq > INT32_MAX) return TFPA_EINVAL;
   thread_local std::vector<Run> runs;   // reused by every call of this thread
   if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;
+  const int32_t parts = block_parts(block, nsel);
+  const int G = c->hq / c->hkv;
+  const int64_t qtiles = G <= 8 ? 1 : (G + 15) / 16;
+  if ((int64_t)rows * c->hkv * qtiles * parts > INT32_MAX) return TFPA_EINVAL;
   if (rows == 0) return TFPA_OK;
   if ((e = check_device())) return e;
   thread_local BlocksParams p;
@@ -1915,10 +1925,14 @@ int blocks_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
     const int32_t base = runs[ri].row0;
     int nr = 0;
     int32_t nrows = 0;
+    SourceSet ss;
     while (ri < runs.size() && nr < kMaxRuns) {
+      const int src = ss.add(segs, runs[ri].seg);
+      if (src < 0) break;
       const Run& r = runs[ri++];
       const tfpa_seg& g = segs[r.seg];
       BlocksRun& w = p.runs[nr++];
+      w.src = src;
       w.page_table = g.page_table;
       w.k_base = g.page_table ? c->k_pool : g.k_slab;
       w.v_base = g.page_table ? c->v_pool : g.v_slab;
@@ -1940,12 +1954,19 @@ int blocks_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
     p.rows = nrows;
     p.hq = c->hq;
     p.hkv = c->hkv;
-    p.group = c->hq / c->hkv;
+    p.group = G;
     p.num_pages = c->num_pages;
     p.block = block;
     p.nsel = nsel;
+    p.parts = parts;
     p.scale_log2 = scale * 1.4426950408889634f;
-    record(17, base, nrows, nr, nrows * c->hkv, nrows * c->hq, base * hd, base * hd);
+    if (c->dtype != TFPA_FP4_E2M1) {
+      const bool fp8 = c->dtype == TFPA_FP8_E4M3;
+      int32_t nsrc;
+      if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 64, p.maps, nsrc))) return e;
+    }
+    const int32_t items = (int32_t)(nrows * c->hkv * qtiles);
+    record(17, base, nrows, nr, items, items * parts, base * hd, base * hd);
     if (!dry_run())
       if ((e = to_err(launch_decode_blocks(p, c->dtype, stream)))) return e;
   }

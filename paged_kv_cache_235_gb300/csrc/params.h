@@ -407,8 +407,11 @@ struct BlocksRun {
   const void* v_base;
   int32_t row0, nrows, pos0;
   int32_t slab_cap;
+  int32_t src;                // index into maps[]
+  int32_t pad_;
 };
 struct BlocksParams {
+  KVMaps maps[kMaxSources];   // boxes of 64 rows (bf16, e4m3)
   BlocksRun runs[kMaxRuns];
   const __nv_bfloat16* q;     // rows of this launch: [rows][hq][128]
   const int32_t* blocks;      // [rows][hkv][nsel]
@@ -423,6 +426,7 @@ struct BlocksParams {
   int32_t num_pages;
   int32_t block;
   int32_t nsel;
+  int32_t parts;              // CTAs (a cluster) of a row, kv head and query tile
   float scale_log2;
 };
 
