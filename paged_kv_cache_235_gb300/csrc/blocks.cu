@@ -12,6 +12,7 @@
 // are bf16 numbers, so no bound is rounded, and the scale, common to all
 // blocks, does not change their order.
 #include "blocks.cuh"
+#include "cluster.cuh"
 #include "common.cuh"
 #include "kvstore.cuh"
 #include "params.h"
@@ -92,8 +93,20 @@ __global__ void __launch_bounds__(kBoundThreads)
 }
 
 // ---------------------------------------------------------------- selection
-constexpr int kSelThreads = 512;
+// A cluster of one to eight CTAs takes a kv head and up to four consecutive rows
+// of a stream.  Its CTAs share the blocks: a warp reads eight blocks' bounds at a
+// time (16 bytes a lane, so the reads of a page are one run), forms all rows'
+// scores from them and leaves them in the shared memory of the CTA that chooses
+// for the row (rank r for row r).  What bounds that part is the read of the
+// bounds, once for the rows together.
+// The choice: the scores' leading bits that all of them share are passed over,
+// a histogram of the next 11 finds the bin of the border, and few keys in it are
+// ranked one against all (else 11 bits more).  Barriers and their latencies are
+// what it costs, not work.
+constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kBins = 2048;
 constexpr int kNear = 64;                    // near candidates ranked one against all
 constexpr uint32_t kTaken = 0xFFFFFFFFu;     // order key of a block that is in whatever its score
 constexpr uint32_t kAbsent = 0u;             // and of one that is not
@@ -106,6 +119,7 @@ __device__ __forceinline__ uint32_t order32(float s) {
 __device__ __forceinline__ float value32(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
+__device__ __forceinline__ bool is_score(uint32_t k) { return k != kTaken && k != kAbsent; }
 // The same of a float64 score; a NaN above every number.
 __device__ __forceinline__ uint64_t order64(double s) {
   if (s != s) return ~0ull;
@@ -114,17 +128,24 @@ __device__ __forceinline__ uint64_t order64(double s) {
 }
 
 struct SelShared {
-  double q64[256];           // sum_h min(q, 0) (0..127), sum_h max(q, 0) (128..255)
-  uint32_t hist[256];
+  union {
+    uint32_t hist[kBins];
+    double q64[256];         // sum_h min(q, 0) (0..127), sum_h max(q, 0) (128..255), for exact
+  };                         // scores, between two uses of the histogram
+  uint32_t most[kMaxCluster * kSelWarps];   // largest |bound| (bf16 bits; ~0: a score was no
+                                            // number), of every warp of the cluster
   uint32_t warp_s[kSelWarps];
-  uint32_t digit, above, count, forced, free_blocks;
-  uint32_t most;             // largest |bound|, as bits
-  float q1;                  // sum_d |q64|
-  int nonfinite;
+  uint32_t warp_lo[kSelWarps], warp_hi[kSelWarps];
+  uint32_t pick[3];
+  uint32_t count;
+  uint32_t border;
   int near_i[kNear];
   uint64_t near_k[kNear];
 };
+constexpr size_t kSelectSmem = (size_t)kSelectBlocks * 12;
+static_assert(sizeof(SelShared) + kSelectSmem <= 232448, "shared memory");
 
+// Exclusive prefix sum of x over the block's threads; total: the sum.
 __device__ __forceinline__ uint32_t sel_prefix(uint32_t x, uint32_t* warp_s, uint32_t& total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t inc = x;
@@ -133,41 +154,31 @@ __device__ __forceinline__ uint32_t sel_prefix(uint32_t x, uint32_t* warp_s, uin
     const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
-  __syncthreads();
+  __syncthreads();                       // warp_s of the previous call is read
   if (lane == 31) warp_s[warp] = inc;
   __syncthreads();
-  const uint32_t w = lane < kSelWarps ? warp_s[lane] : 0;
-  uint32_t winc = w;
+  uint32_t before = 0;
+  total = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, winc, o);
-    if (lane >= o) winc += y;
+  for (int w = 0; w < kSelWarps; ++w) {
+    const uint32_t v = warp_s[w];
+    before += w < warp ? v : 0u;
+    total += v;
   }
-  total = __shfl_sync(0xffffffffu, winc, 31);
-  return __shfl_sync(0xffffffffu, winc - w, warp) + inc - x;
+  return before + inc - x;
 }
 
-// Sum over the block's threads.
-__device__ __forceinline__ uint32_t sel_sum(uint32_t x, uint32_t* warp_s) {
-  uint32_t total;
-  sel_prefix(x, warp_s, total);
-  return total;
-}
-
-// This lane's 16 bytes of block b's bounds (lanes 0-15 the smallest, 16-31
-// the largest), or nullptr on a page out of range.
-__device__ __forceinline__ const uint4* bound_ptr(const SelectParams& p, const SelRun& run, int g,
-                                                  int b, int lane) {
+// Index (in blocks' bounds) of block b, or -1 on a page out of range.
+__device__ __forceinline__ int bound_at(const SelectParams& p, const SelRun& run, int g, int b) {
   const int per_page = kPage / p.block;
-  size_t at;
-  if (run.page_table) {
-    const int pid = __ldg(run.page_table + b / per_page);
-    if ((unsigned)pid >= (unsigned)p.num_pages) return nullptr;
-    at = ((size_t)pid * p.hkv + g) * per_page + b % per_page;
-  } else {
-    at = (size_t)g * (run.slab_cap / p.block) + b;
-  }
-  return static_cast<const uint4*>(run.bounds) + at * 32 + lane;
+  if (!run.page_table) return g * (run.slab_cap / p.block) + b;
+  const int pid = __ldg(run.page_table + b / per_page);
+  if ((unsigned)pid >= (unsigned)p.num_pages) return -1;
+  return (pid * p.hkv + g) * per_page + b % per_page;
+}
+// This lane's 16 bytes of it: lanes 0-15 the smallest, 16-31 the largest.
+__device__ __forceinline__ uint4 bound_load(const SelRun& run, int at, int lane) {
+  return __ldg(static_cast<const uint4*>(run.bounds) + (size_t)at * 32 + lane);
 }
 
 // The score of a block from the whole warp's bounds, in 64 bits.  Every block's
@@ -183,168 +194,183 @@ __device__ __forceinline__ double score64(const SelShared& sh, const uint4& w, i
   return s;
 }
 
-// One CTA a (row, kv head).
-__global__ void __launch_bounds__(kSelThreads)
-    select_blocks_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ SelShared sh;
-  extern __shared__ uint64_t dyn[];          // [cap] exact keys, then [cap] keys
-  allow_next_grid();
-  wait_prior_grid();
+// Sums over the warp's lanes of eight values a lane: lane l gets value l / 4's.
+__device__ __forceinline__ float reduce8(const float (&v)[8], int lane) {
+  float a[4], b[2], c;
+  const bool u4 = lane & 16, u3 = lane & 8, u2 = lane & 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    a[j] = (u4 ? v[j + 4] : v[j]) + __shfl_xor_sync(0xffffffffu, u4 ? v[j] : v[j + 4], 16);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    b[j] = (u3 ? a[j + 2] : a[j]) + __shfl_xor_sync(0xffffffffu, u3 ? a[j] : a[j + 2], 8);
+  c = (u2 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, u2 ? b[0] : b[1], 4);
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  return c + __shfl_xor_sync(0xffffffffu, c, 1);
+}
+
+// The rows' blocks from the keys in this CTA's shared memory: the want-th
+// largest, what is near it, and the list.
+__device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bfloat16* q, int g,
+                       int n, int ranks, float q1, uint32_t* key32, uint64_t* key64,
+                       SelShared& sh, int32_t* out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = blockIdx.x / p.hkv, g = blockIdx.x % p.hkv;
-  int ri = 0;
-  while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
-  const SelRun& run = p.runs[ri];
-  const int pos = run.pos0 + (row - run.row0);
-  const int last = pos / p.block, n = last + 1;
-  int32_t* out = p.blocks + ((size_t)row * p.hkv + g) * p.nsel;
-  uint64_t* key64 = dyn;
-  uint32_t* key32 = reinterpret_cast<uint32_t*>(dyn + p.cap);
-  auto forced = [&](int b) { return b < p.sink || b > last - p.recent; };
-
-  // ---- the query heads' positive and negative parts, summed
-  if (tid == 0) {
-    sh.most = 0;
-    sh.nonfinite = 0;
-    sh.q1 = 0.f;
-  }
-  __syncthreads();
-  if (tid < 256) {
-    const int d = tid & 127;
-    const __nv_bfloat16* q = p.q + ((size_t)row * p.hq + (size_t)g * p.group) * kHeadDim + d;
-    double s = 0.0;
-    for (int h = 0; h < p.group; ++h) {
-      const float x = __bfloat162float(q[(size_t)h * kHeadDim]);
-      s += tid < 128 ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x);
-    }
-    sh.q64[tid] = s;
-    float a = fabsf((float)s);
-#pragma unroll
-    for (int d2 = 16; d2; d2 >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d2);
-    if (lane == 0) atomicAdd(&sh.q1, a);     // only a bound hangs on the order
-  }
-  __syncthreads();
-  float qf[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) qf[i] = (float)sh.q64[lane * 8 + i];
-
-  // ---- every visible block's score in float32
-  float most = 0.f;
-  int nonfinite = 0;
-  for (int b = warp; b < n; b += kSelWarps) {
-    const uint4* at = bound_ptr(p, run, g, b, lane);
-    uint32_t key = kAbsent;
-    if (!at) {
-      if (lane == 0) flag_error(p.err_flag, kErrBadPage);
-    } else if (forced(b)) {
-      key = kTaken;
-    } else {
-      float x[8];
-      unpack8(__ldg(at), x);
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s = fmaf(qf[i], x[i], s);
-        most = fmaxf(most, fabsf(x[i]));
-      }
-#pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      if (!(fabsf(s) < INFINITY)) {
-        nonfinite = 1;
-        s = 0.f;
-      }
-      key = order32(s);
-    }
-    if (lane == 0) key32[b] = key;
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-  if (lane == 0) atomicMax(&sh.most, __float_as_uint(most));
-  if (nonfinite) sh.nonfinite = 1;
-  __syncthreads();
-  uint32_t nforced = 0, nfree = 0;
+  // ---- how many are free to choose from, and their range
+  uint32_t counts = 0, kmin = 0xFFFFFFFFu, kmax = 0;     // counts: taken << 16 | free (18,432 at most)
   for (int b = tid; b < n; b += kSelThreads) {
-    nforced += key32[b] == kTaken;
-    nfree += key32[b] != kTaken && key32[b] != kAbsent;
+    const uint32_t k = key32[b];
+    if (k == kTaken) {
+      counts += 0x10000u;
+    } else if (k != kAbsent) {
+      ++counts;
+      kmin = min(kmin, k);
+      kmax = max(kmax, k);
+    }
   }
-  nforced = sel_sum(nforced, sh.warp_s);
-  nfree = sel_sum(nfree, sh.warp_s);
-  const uint32_t want = min(nfree, p.nsel > (int)nforced ? p.nsel - nforced : 0u);
-
-  if (want == nfree) {                       // all of them
-    for (int b = tid; b < n; b += kSelThreads)
-      if (key32[b] != kAbsent) key32[b] = kTaken;
-  } else if (want == 0) {
-    for (int b = tid; b < n; b += kSelThreads)
-      if (key32[b] != kTaken) key32[b] = kAbsent;
-  } else {
-    // ---- the want-th largest key, a digit of 8 bits at a time
-    uint32_t prefix = 0, rest = want;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelThreads) sh.hist[i] = 0;
-      __syncthreads();
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  counts = __reduce_add_sync(0xffffffffu, counts);
+  if (lane == 0) {
+    sh.warp_lo[warp] = kmin;
+    sh.warp_hi[warp] = kmax;
+    sh.warp_s[warp] = counts;
+  }
+  if (tid == 0) sh.count = 0;
+  for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+  __syncthreads();
+  uint32_t ntaken = 0, nfree = 0, most = 0;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) {
+    kmin = min(kmin, sh.warp_lo[w]);
+    kmax = max(kmax, sh.warp_hi[w]);
+    ntaken += sh.warp_s[w] >> 16;
+    nfree += sh.warp_s[w] & 0xFFFFu;
+  }
+  const uint32_t want = min(nfree, p.nsel > (int)ntaken ? p.nsel - ntaken : 0u);
+  uint32_t in_from = 0;                  // keys from here on are in, but for near ones
+  float low = 0.f, top = 0.f;
+  bool all = false;                      // every score is near
+  if (want == 0) {
+    in_from = kTaken;
+  } else if (want < nfree) {
+    for (int i = 0; i < ranks * kSelWarps; ++i) most = max(most, sh.most[i]);
+    // ---- the want-th largest key
+    const uint32_t differ = kmin ^ kmax;
+    int shift = differ ? 32 - __clz(differ) : 0;         // bits that are not the same in all
+    uint32_t prefix = shift == 32 ? 0u : kmin >> shift << shift;
+    uint32_t rest = want;
+    while (shift > 0) {
+      const int bits = min(shift, 11);
+      const uint32_t high = shift == 32 ? 0u : ~0u << shift;
+      shift -= bits;
       for (int b = tid; b < n; b += kSelThreads) {
         const uint32_t k = key32[b];
-        if (k == kTaken || k == kAbsent) continue;
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-          atomicAdd(&sh.hist[(k >> shift) & 255], 1u);
+        if (is_score(k) && (k & high) == prefix)
+          atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1)], 1u);
       }
       __syncthreads();
-      if (tid == 0) {
-        uint32_t seen = 0;
-        int d = 255;
-        while (seen + sh.hist[d] < rest) seen += sh.hist[d--];
-        sh.digit = d;
-        sh.above = seen;
-      }
-      __syncthreads();
-      prefix |= sh.digit << shift;
-      rest -= sh.above;
-    }
-    // ---- who is in, who is out, and who is too near to tell.  A float32 score
-    // is off by at most e: its 14 roundings of 2^-24 each, the sums' own parts
-    // among them, weigh sum |q| |bound| (twice that for good measure).  The
-    // exact want-th largest is within e of the one found, so a score beyond it
-    // by more than 2 e is decided.
-    const float e = 0x1p-19f * sh.q1 * __uint_as_float(sh.most) + 1e-40f;
-    const float at = value32(prefix);
-    const bool all = sh.nonfinite || !(e < INFINITY);
-    const float top = at + 2.125f * e, low = at - 2.125f * e;
-    uint32_t in = 0, near = 0;
-    for (int b = tid; b < n; b += kSelThreads) {
-      const uint32_t k = key32[b];
-      if (k == kTaken || k == kAbsent) continue;
-      const float s = value32(k);
-      if (all || (s >= low && s <= top))
-        ++near;
-      else if (s > top)
-        ++in;
-    }
-    in = sel_sum(in, sh.warp_s);
-    near = sel_sum(near, sh.warp_s);
-    const uint32_t need = want - in;         // of the near ones
-    if (tid == 0) sh.count = 0;
-    __syncthreads();
-    if (near == need || near <= kNear) {
-      for (int b = tid; b < n; b += kSelThreads) {
-        const uint32_t k = key32[b];
-        if (k == kTaken || k == kAbsent) continue;
-        const float s = value32(k);
-        if (all || (s >= low && s <= top)) {
-          if (near == need) {
-            key32[b] = kTaken;
-          } else {
-            sh.near_i[atomicAdd(&sh.count, 1u)] = b;
-            key32[b] = kAbsent;
+      // thread t: the eight bins from 2047 - 8 t down
+      uint32_t c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += c[i] = sh.hist[kBins - 1 - 8 * tid - i];
+      uint32_t total, above = sel_prefix(sum, sh.warp_s, total);
+      if (above < rest && rest <= above + sum) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (above < rest && rest <= above + c[i]) {
+            sh.pick[0] = kBins - 1 - 8 * tid - i;
+            sh.pick[1] = rest - above;
+            sh.pick[2] = c[i];
           }
-        } else {
-          key32[b] = s > top ? kTaken : kAbsent;
+          above += c[i];
         }
       }
       __syncthreads();
-      if (near != need) {
+      prefix |= sh.pick[0] << shift;
+      rest = sh.pick[1];
+      const uint32_t same = sh.pick[2];
+      if (shift > 0 && same <= kNear) {
+        // few share the leading bits: the rest-th largest of them directly
+        const uint32_t lead = ~0u << shift;
+        for (int b = tid; b < n; b += kSelThreads) {
+          const uint32_t k = key32[b];
+          if (is_score(k) && (k & lead) == prefix) sh.near_k[atomicAdd(&sh.count, 1u)] = k;
+        }
+        __syncthreads();
+        if (tid < (int)same) {
+          const uint32_t k = (uint32_t)sh.near_k[tid];
+          uint32_t more = 0, equal = 0;
+          for (uint32_t i = 0; i < same; ++i) {
+            more += (uint32_t)sh.near_k[i] > k;
+            equal += (uint32_t)sh.near_k[i] == k;
+          }
+          if (more < rest && rest <= more + equal) sh.border = k;
+        }
+        __syncthreads();
+        prefix = sh.border;
+        break;
+      }
+      if (shift > 0) {
+        for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+        __syncthreads();
+      }
+    }
+    // ---- who is in, who is out, and who is too near to tell.  A float32 score is
+    // off by its roundings' sum |q| |bound|: the sums over G heads (all of one
+    // sign), 8 products and sums of a lane, 5 of the reduction, 2^-24 each; e is
+    // twice that.  The exact want-th largest is within e of the one found, so a
+    // score beyond it by more than 2 e is decided.
+    const float e = (float)(16 + p.group) * 0x1p-23f * q1 * __uint_as_float(most << 16) + 1e-40f;
+    const float at = value32(prefix);
+    all = most >= 0x7F80u || !(e < INFINITY);
+    top = at + 2.125f * e;
+    low = at - 2.125f * e;
+    uint32_t both = 0;                   // in << 16 | near
+    for (int b = tid; b < n; b += kSelThreads) {
+      const uint32_t k = key32[b];
+      if (!is_score(k)) continue;
+      const float s = value32(k);
+      both += all || (s >= low && s <= top) ? 1u : s > top ? 0x10000u : 0u;
+    }
+    uint32_t total;
+    sel_prefix(both, sh.warp_s, total);
+    const uint32_t near = total & 0xFFFFu, need = want - (total >> 16);
+    if (near == need) {
+      in_from = all ? 1u : order32(low);
+      all = false;
+    } else {
+      // ---- the near ones' exact scores
+      auto is_near = [&](uint32_t k) {
+        if (!is_score(k)) return false;
+        const float s = value32(k);
+        return all || (s >= low && s <= top);
+      };
+      if (tid < 128) {
+        double down = 0.0, up = 0.0;
+        for (int h = 0; h < p.group; ++h) {
+          const float x = __bfloat162float(q[(size_t)h * kHeadDim + tid]);
+          down += x > 0.f ? 0.f : x;
+          up += x < 0.f ? 0.f : x;
+        }
+        sh.q64[tid] = down;
+        sh.q64[128 + tid] = up;
+      }
+      if (tid == 0) sh.count = 0;
+      __syncthreads();
+      if (near <= kNear) {
+        for (int b = tid; b < n; b += kSelThreads) {
+          const uint32_t k = key32[b];
+          if (is_near(k)) {
+            sh.near_i[atomicAdd(&sh.count, 1u)] = b;
+            key32[b] = kAbsent;
+          } else if (is_score(k)) {
+            key32[b] = value32(k) > top ? kTaken : kAbsent;
+          }
+        }
+        __syncthreads();
         for (uint32_t i = warp; i < near; i += kSelWarps) {
-          const double s = score64(sh, __ldg(bound_ptr(p, run, g, sh.near_i[i], lane)), lane);
+          const uint4 w = bound_load(run, bound_at(p, run, g, sh.near_i[i]), lane);
+          const double s = score64(sh, w, lane);
           if (lane == 0) sh.near_k[i] = order64(s);
         }
         __syncthreads();
@@ -356,72 +382,242 @@ __global__ void __launch_bounds__(kSelThreads)
             before += sh.near_k[i] > k || (sh.near_k[i] == k && sh.near_i[i] < b);
           if (before < need) key32[b] = kTaken;
         }
-      }
-    } else {
-      // ---- many near ones (equal blocks, scores that are not numbers): their
-      // exact keys, and the need-th largest among them
-      for (int b = warp; b < n; b += kSelWarps) {
-        const uint32_t k = key32[b];
-        const float s = value32(k);
-        const bool is_near = k != kTaken && k != kAbsent && (all || (s >= low && s <= top));
-        uint64_t x = 0;
-        if (is_near) {
-          x = order64(score64(sh, __ldg(bound_ptr(p, run, g, b, lane)), lane));
-          if (x == 0) x = 1;                 // 0 marks a block that is not near
+      } else {
+        // many (equal blocks, scores that are no numbers): the need-th largest of
+        // their exact keys, 8 bits at a time
+        for (int b = warp; b < n; b += kSelWarps) {
+          const uint32_t k = key32[b];
+          const bool mine = is_near(k);
+          uint64_t x = 0;                // 0 marks a block that is not near
+          if (mine) {
+            const uint4 w = bound_load(run, bound_at(p, run, g, b), lane);
+            x = max(order64(score64(sh, w, lane)), (uint64_t)1);
+          }
+          __syncwarp();
+          if (lane == 0) {
+            key64[b] = x;
+            if (!mine && is_score(k)) key32[b] = value32(k) > top ? kTaken : kAbsent;
+          }
         }
-        __syncwarp();
-        if (lane == 0) {
-          key64[b] = x;
-          if (!is_near) key32[b] = k == kTaken || (k != kAbsent && s > top) ? kTaken : kAbsent;
+        uint64_t prefix64 = 0;
+        uint32_t left = need;
+        for (int shift64 = 56; shift64 >= 0; shift64 -= 8) {
+          __syncthreads();
+          sh.hist[tid] = 0;
+          __syncthreads();
+          for (int b = tid; b < n; b += kSelThreads) {
+            const uint64_t k = key64[b];
+            if (k && (shift64 == 56 || (k >> (shift64 + 8)) == (prefix64 >> (shift64 + 8))))
+              atomicAdd(&sh.hist[(k >> shift64) & 255], 1u);
+          }
+          __syncthreads();
+          const uint32_t c = sh.hist[255 - tid];
+          uint32_t sum;
+          const uint32_t above = sel_prefix(c, sh.warp_s, sum);
+          if (above < left && left <= above + c) {
+            sh.pick[0] = 255 - tid;
+            sh.pick[1] = left - above;
+          }
+          __syncthreads();
+          prefix64 |= (uint64_t)sh.pick[0] << shift64;
+          left = sh.pick[1];
+        }
+        // those above the need-th, and of the ones equal to it the first `left`
+        uint32_t seen = 0;
+        for (int b0 = 0; b0 < n; b0 += kSelThreads) {
+          const int b = b0 + tid;
+          const uint64_t k = b < n ? key64[b] : 0;
+          uint32_t sum;
+          const uint32_t before = seen + sel_prefix(k == prefix64, sh.warp_s, sum);
+          if (k) key32[b] = k > prefix64 || (k == prefix64 && before < left) ? kTaken : kAbsent;
+          seen += sum;
         }
       }
-      __syncthreads();
-      uint64_t prefix64 = 0;
-      uint32_t left = need;
-      for (int shift = 56; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelThreads) sh.hist[i] = 0;
-        __syncthreads();
-        for (int b = tid; b < n; b += kSelThreads) {
-          const uint64_t k = key64[b];
-          if (k && (shift == 56 || (k >> (shift + 8)) == (prefix64 >> (shift + 8))))
-            atomicAdd(&sh.hist[(k >> shift) & 255], 1u);
-        }
-        __syncthreads();
-        if (tid == 0) {
-          uint32_t seen = 0;
-          int d = 255;
-          while (seen + sh.hist[d] < left) seen += sh.hist[d--];
-          sh.digit = d;
-          sh.above = seen;
-        }
-        __syncthreads();
-        prefix64 |= (uint64_t)sh.digit << shift;
-        left -= sh.above;
-      }
-      // those above the need-th, and of the ones equal to it the first `left`
-      uint32_t seen = 0;
-      for (int b0 = 0; b0 < n; b0 += kSelThreads) {
-        const int b = b0 + tid;
-        const uint64_t k = b < n ? key64[b] : 0;
-        uint32_t total;
-        const uint32_t before = seen + sel_prefix(k == prefix64, sh.warp_s, total);
-        if (k) key32[b] = k > prefix64 || (k == prefix64 && before < left) ? kTaken : kAbsent;
-        seen += total;
-      }
+      in_from = kTaken;                  // the keys say it all now
     }
   }
+  // ---- the chosen blocks, ascending: a thread takes consecutive ones.  (Every key
+  // but kAbsent is at least 1.)
+  in_from = max(in_from, 1u);
   __syncthreads();
-  // ---- the chosen blocks, ascending
-  uint32_t filled = 0;
-  for (int b0 = 0; b0 < n; b0 += kSelThreads) {
-    const int b = b0 + tid;
-    const bool in = b < n && key32[b] == kTaken;
-    uint32_t total;
-    const uint32_t before = filled + sel_prefix(in, sh.warp_s, total);
-    if (in) out[before] = b;
-    filled += total;
+  const int per = (n + kSelThreads - 1) / kSelThreads;
+  const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
+  uint32_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += key32[b] >= in_from;
+  uint32_t total, at = sel_prefix(mine, sh.warp_s, total);
+  for (int b = b0; b < b1; ++b)
+    if (key32[b] >= in_from) out[at++] = b;
+  for (uint32_t i = total + tid; i < (uint32_t)p.nsel; i += kSelThreads) out[i] = -1;
+}
+
+// R: rows of a cluster at most.  The grid: clusters of p.cluster CTAs, one for
+// each (row group, kv head).
+template <int R>
+__global__ void __launch_bounds__(kSelThreads)
+    select_blocks_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ SelShared sh;
+  extern __shared__ uint64_t dyn[];          // [cap] exact keys, then [cap] keys
+  uint64_t* key64 = dyn;
+  uint32_t* key32 = reinterpret_cast<uint32_t*>(dyn + p.cap);
+  const int nc = p.cluster;
+  if (nc > 1) cluster_arrive();              // every CTA has to run before its memory is written
+  allow_next_grid();
+  wait_prior_grid();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = nc > 1 ? (int)cluster_ctarank() : 0;
+  const int item = blockIdx.x / nc, g = item % p.hkv, group = item / p.hkv;
+  int ri = 0;
+  while (ri + 1 < p.nruns && p.runs[ri + 1].group0 <= group) ++ri;
+  const SelRun& run = p.runs[ri];
+  const int in_run = (group - run.group0) * R;           // first row of the group, in its run
+  const int rows = min(R, run.nrows - in_run);
+  const int row0 = run.row0 + in_run, pos0 = run.pos0 + in_run;
+  const int n = (pos0 + rows - 1) / p.block + 1;         // blocks that its last row sees
+  const bool every = n <= p.nsel;                        // every block is in: no scores
+  const bool waits = nc > 1;
+  float qf[R][8];
+  if (every) {
+    if (rank < rows) {
+      const int last = (pos0 + rank) / p.block;
+      for (int b = tid; b <= last; b += kSelThreads) {
+        const bool there = bound_at(p, run, g, b) >= 0;
+        if (!there) flag_error(p.err_flag, kErrBadPage);
+        key32[b] = there ? kTaken : kAbsent;
+      }
+    }
+  } else {
+    // ---- the query heads' negative (lanes 0-15) and positive parts, summed
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) qf[r][i] = 0.f;
+      if (r >= rows) continue;
+      const uint4* qp = reinterpret_cast<const uint4*>(
+          p.q + ((size_t)(row0 + r) * p.hq + (size_t)g * p.group) * kHeadDim) + (lane & 15);
+#pragma unroll 4
+      for (int h = 0; h < p.group; ++h) {
+        float x[8];
+        unpack8(__ldg(qp + h * 16), x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          qf[r][i] += lane < 16 ? (x[i] > 0.f ? 0.f : x[i]) : (x[i] < 0.f ? 0.f : x[i]);
+      }
+    }
+    // ---- this CTA's blocks, eight a warp and step
+    const int chunk = ((n + nc - 1) / nc + 7) & ~7;
+    const int lo = min(n, rank * chunk), hi = min(n, lo + chunk);
+    uint32_t most = 0;
+    bool nonfinite = false, may_write = !waits;
+    auto find = [&](int b) { return b < hi ? bound_at(p, run, g, b) : -1; };
+    int b0 = lo + warp * 8;
+    int at = find(b0 + (lane & 7));
+    for (; b0 < hi; b0 += kSelWarps * 8) {
+      uint4 w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int a = __shfl_sync(0xffffffffu, at, j);
+        w[j] = a >= 0 ? bound_load(run, a, lane) : make_uint4(0, 0, 0, 0);
+      }
+      const int here = __shfl_sync(0xffffffffu, at, lane >> 2);   // the block this lane answers for
+      at = find(b0 + kSelWarps * 8 + (lane & 7));
+      float s[R][8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float x[8];
+        unpack8(w[j], x);
+        most = __vmaxu2(most, w[j].x & 0x7FFF7FFFu);
+        most = __vmaxu2(most, w[j].y & 0x7FFF7FFFu);
+        most = __vmaxu2(most, w[j].z & 0x7FFF7FFFu);
+        most = __vmaxu2(most, w[j].w & 0x7FFF7FFFu);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          s[r][j] = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[r][j] = fmaf(qf[r][i], x[i], s[r][j]);
+        }
+      }
+      const int b = b0 + (lane >> 2);
+      float mine = 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float v = reduce8(s[r], lane);
+        if ((lane & 3) == r) mine = v;
+      }
+      const int r = lane & 3;                            // and the row
+      if (!may_write) {
+        __syncwarp();
+        cluster_wait();
+        may_write = true;
+      }
+      if (r < rows && b < hi) {
+        const int last = (pos0 + r) / p.block;
+        if (b <= last) {
+          uint32_t key;
+          if (here < 0) {
+            key = kAbsent;
+            flag_error(p.err_flag, kErrBadPage);
+          } else if (b < p.sink || b > last - p.recent) {
+            key = kTaken;
+          } else {
+            const bool number = fabsf(mine) < INFINITY;
+            nonfinite |= !number;
+            key = order32(number ? mine : 0.f);
+          }
+          if (waits)
+            st_cluster_u32(mapa_shared(smem_u32(key32 + b), r), key);
+          else
+            key32[b] = key;
+        }
+      }
+    }
+    __syncwarp();
+    if (!may_write) cluster_wait();
+    most = max(most & 0xFFFFu, most >> 16);
+    most = __reduce_max_sync(0xffffffffu, nonfinite ? 0xFFFFu : most);
+    if (lane < rows) {
+      uint32_t* slot = &sh.most[rank * kSelWarps + warp];
+      if (waits)
+        st_cluster_u32(mapa_shared(smem_u32(slot), lane), most);
+      else
+        *slot = most;
+    }
   }
-  for (uint32_t i = filled + tid; i < (uint32_t)p.nsel; i += kSelThreads) out[i] = -1;
+  __syncwarp();
+  if (waits) {
+    if (every) cluster_wait();
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  if (rank >= rows) return;
+  // ---- this CTA's row
+  float q1 = 0.f;
+  if (!every) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r == rank) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q1 += fabsf(qf[r][i]);
+      }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) q1 += __shfl_xor_sync(0xffffffffu, q1, d);
+  }
+  const int row = row0 + rank;
+  choose(p, run, p.q + ((size_t)row * p.hq + (size_t)g * p.group) * kHeadDim, g,
+         (pos0 + rank) / p.block + 1, nc, q1, key32, key64, sh,
+         p.blocks + ((size_t)row * p.hkv + g) * p.nsel);
+}
+
+template <int R>
+cudaError_t launch_select(const SelectParams& p, cudaStream_t s) {
+  static PerDeviceOnce configured;
+  const cudaError_t e = configured.run([] {
+    return cudaFuncSetAttribute(select_blocks_kernel<R>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectSmem);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl_cluster(select_blocks_kernel<R>, dim3(p.groups * p.hkv * p.cluster),
+                            dim3(kSelThreads), (size_t)p.cap * 12, s, p, p.cluster);
 }
 
 }  // namespace
@@ -436,14 +632,9 @@ cudaError_t launch_key_bounds(const BoundsParams& p, int kv, cudaStream_t s) {
 }
 
 cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t s) {
-  static PerDeviceOnce configured;
-  const cudaError_t e = configured.run([] {
-    return cudaFuncSetAttribute(select_blocks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kSelectBlocks * 12);
-  });
-  if (e != cudaSuccess) return e;
-  return launch_pdl(select_blocks_kernel, dim3(p.rows * p.hkv), dim3(kSelThreads),
-                    (size_t)p.cap * 12, s, p);
+  return p.rows_per == 1   ? launch_select<1>(p, s)
+         : p.rows_per == 2 ? launch_select<2>(p, s)
+                           : launch_select<4>(p, s);
 }
 
 }  // namespace tfpa

@@ -1846,22 +1846,25 @@ int select_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const t
   thread_local std::vector<Run> runs;   // reused by every call of this thread
   if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;
   if ((e = check_bounds(b, segs, runs))) return e;
-  if ((int64_t)rows * c->hkv > INT32_MAX) return TFPA_EINVAL;
+  if ((int64_t)rows * c->hkv * 8 > INT32_MAX) return TFPA_EINVAL;
   for (const Run& r : runs)
     if ((r.pos0 + r.nrows - 1) / b->block + 1 > kSelectBlocks) return TFPA_ECAPACITY;
   if (rows == 0) return TFPA_OK;
   if ((e = check_device())) return e;
+  const int nsm = sm_count();
+  if (nsm < 1) return TFPA_ECUDA;
   thread_local SelectParams p;
   size_t ri = 0;
   while (ri < runs.size()) {
     std::memset(&p, 0, sizeof(p));
     const int32_t base = runs[ri].row0;
     int nr = 0;
-    int32_t nrows = 0;
+    int32_t nrows = 0, longest = 1;
     while (ri < runs.size() && nr < kMaxRuns) {
       const Run& r = runs[ri++];
       const tfpa_seg& g = segs[r.seg];
       SelRun& w = p.runs[nr++];
+      longest = std::max(longest, r.nrows);
       w.page_table = g.page_table;
       w.bounds = bounds_of(b, segs, r.seg);
       w.row0 = r.row0 - base;
@@ -1884,8 +1887,20 @@ int select_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const t
     p.nsel = nsel;
     p.sink = sink;
     p.recent = recent;
-    record(16, base, nrows, nr, nrows * c->hkv, nrows * c->hkv, (int64_t)base * c->hq * kHeadDim,
-           (int64_t)base * c->hkv * nsel);
+    // Up to four rows of a run share the reads of the bounds; a cluster has a CTA
+    // for each of them to choose in.  More CTAs while the GPU holds them (four a
+    // SM) and each has 64 blocks, eight a warp.
+    p.rows_per = longest >= 3 ? 4 : longest;
+    for (int i = 0; i < nr; ++i) {
+      p.runs[i].group0 = p.groups;
+      p.groups += (p.runs[i].nrows + p.rows_per - 1) / p.rows_per;
+    }
+    p.cluster = p.rows_per;
+    while (p.cluster < 8 && (int64_t)p.groups * c->hkv * p.cluster * 2 <= 4 * nsm &&
+           p.cap / (p.cluster * 2) >= 64)
+      p.cluster *= 2;
+    record(16, base, nrows, nr, p.groups * c->hkv, p.groups * c->hkv * p.cluster,
+           (int64_t)base * c->hq * kHeadDim, (int64_t)base * c->hkv * nsel);
     if (!dry_run())
       if ((e = to_err(launch_select_blocks(p, stream)))) return e;
   }

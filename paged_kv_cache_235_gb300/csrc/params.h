@@ -386,6 +386,8 @@ struct SelRun {
   const void* bounds;
   int32_t row0, nrows, pos0;
   int32_t slab_cap;
+  int32_t group0;             // row groups of the runs before
+  int32_t pad_;
 };
 struct SelectParams {
   SelRun runs[kMaxRuns];
@@ -400,6 +402,9 @@ struct SelectParams {
   int32_t nsel;
   int32_t sink, recent;
   int32_t cap;                // blocks of the longest row
+  int32_t rows_per;           // rows of a group: 1, 2 or 4
+  int32_t groups;
+  int32_t cluster;            // CTAs of a (group, kv head)
 };
 struct BlocksRun {
   const int32_t* page_table;  // nullptr => slab
