@@ -709,7 +709,8 @@ int tfpa_select_blocks(const tfpa_cache* cache, const tfpa_seg* segs, int32_t ns
  * tfpa_select_blocks leaves them) up to row_pos[r].  Entries may come in any
  * order; a negative one, and one past the row's own block, is passed over; a
  * block that is named twice counts twice.  A row that sees no key gets out = 0
- * and lse = -inf.  No scratch.  A page id out of range: as tfpa_decode. */
+ * and lse = -inf.  No scratch.  1 <= nsel <= 2^24.  A page id out of range: as
+ * tfpa_decode. */
 int tfpa_decode_blocks(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
                        const void* q, const int32_t* row_seg, const int32_t* row_pos,
                        int32_t rows, int32_t block, int32_t nsel, const int32_t* blocks,

@@ -9,6 +9,7 @@ Loading fails loudly if the library has not been built.
 import contextlib
 import ctypes
 import os
+import struct
 from dataclasses import dataclass, field
 from typing import List, Optional, Sequence
 
@@ -209,7 +210,7 @@ def lib():
         L.tfpa_evict_kv.restype = ctypes.c_int
         L.tfpa_rope_table.argtypes = [P(tfpa_rope_spec), ctypes.c_int64, i32, vp, vp, vp]
         L.tfpa_rope_table.restype = ctypes.c_int
-        L.tfpa_write_qkv.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, P(tfpa_qkv), vp, vp, i32,
+        L.tfpa_write_qkv.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, vp, vp, vp, i32,
                                      vp, vp]
         L.tfpa_write_qkv.restype = ctypes.c_int
         L.tfpa_key_bounds.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, P(tfpa_bounds), vp, vp,
@@ -258,9 +259,10 @@ def _ptr(x) -> Optional[int]:
         return x
     if t is np.ndarray:
         return _np_ptr(x)
-    if isinstance(x, int):
+    try:
+        return x.data_ptr()
+    except AttributeError:
         return int(x)
-    return x.data_ptr()
 
 
 _current_stream = None
@@ -670,10 +672,15 @@ def tfpa_rope_table(spec: RopeSpec, first: int, cos, sin, stream=None) -> None:
 
 def _heads(t, rows: int, heads: int, what: str) -> int:
     """The row stride of ``[rows][heads][128]`` rows whose heads lie one after the other."""
-    if tuple(t.shape) != (rows, heads, HEAD_DIM) or t.stride(2) != 1 or (
-            heads > 1 and t.stride(1) != HEAD_DIM):
+    s = t.stride()
+    if t.shape != (rows, heads, HEAD_DIM) or s[2] != 1 or (heads > 1 and s[1] != HEAD_DIM):
         raise ValueError(f"{what} must be [rows][heads][{HEAD_DIM}] with heads one after the other")
-    return t.stride(0) if rows > 1 else heads * HEAD_DIM
+    return s[0] if rows > 1 else heads * HEAD_DIM
+
+
+# tfpa_qkv, packed in a fifth of the time that its ctypes structure takes to fill
+_pack_qkv = struct.Struct("@3P3q5P3if").pack
+assert struct.calcsize("@3P3q5P3if") == ctypes.sizeof(tfpa_qkv)
 
 
 def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, row_pos,
@@ -686,23 +693,22 @@ def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, r
     cs, n = _segs(segs)
     rs, rp = _i32(row_seg), _i32(row_pos)
     rows = len(rs)
-    half = 0
+    table = half = 0
     if rope_cos is not None:
-        half = rope_cos.shape[1]
-        if tuple(rope_sin.shape) != tuple(rope_cos.shape) or not (
-                rope_cos.is_contiguous() and rope_sin.is_contiguous()):
+        table, half = rope_cos.shape
+        if rope_sin.shape != (table, half) or not (rope_cos.is_contiguous()
+                                                   and rope_sin.is_contiguous()):
             raise ValueError("rope_cos and rope_sin must be contiguous tables of one shape")
-    if q_out is not None and (tuple(q_out.shape) != (rows, cache.hq, HEAD_DIM)
-                              or not q_out.is_contiguous()):
+    hq, hkv = cache.hq, cache.hkv
+    if q_out is not None and (q_out.shape != (rows, hq, HEAD_DIM) or not q_out.is_contiguous()):
         raise ValueError("q_out must be contiguous [rows][hq][128]")
-    a = tfpa_qkv(_ptr(q), _ptr(k), _ptr(v),
-                 0 if q is None else _heads(q, rows, cache.hq, "q"),
-                 _heads(k, rows, cache.hkv, "k"), _heads(v, rows, cache.hkv, "v"),
-                 _ptr(q_weight), _ptr(k_weight), _ptr(rope_cos), _ptr(rope_sin), _ptr(rope_pos),
-                 0 if rope_cos is None else rope_cos.shape[0], 2 * half, int(bool(interleaved)),
-                 float(eps))
-    _check(lib().tfpa_write_qkv(ctypes.byref(cache.c()), cs, n, ctypes.byref(a), _ptr(rs),
-                                _ptr(rp), rows, _ptr(q_out), _stream(stream)), "tfpa_write_qkv")
+    a = _pack_qkv(_ptr(q) or 0, _ptr(k) or 0, _ptr(v) or 0,
+                  0 if q is None else _heads(q, rows, hq, "q"), _heads(k, rows, hkv, "k"),
+                  _heads(v, rows, hkv, "v"), _ptr(q_weight) or 0, _ptr(k_weight) or 0,
+                  _ptr(rope_cos) or 0, _ptr(rope_sin) or 0, _ptr(rope_pos) or 0, table, 2 * half,
+                  1 if interleaved else 0, eps)
+    _check(lib().tfpa_write_qkv(ctypes.byref(cache.c()), cs, n, a, _ptr(rs), _ptr(rp), rows,
+                                _ptr(q_out), _stream(stream)), "tfpa_write_qkv")
 
 
 @dataclass(eq=False)
@@ -744,9 +750,10 @@ def tfpa_key_bounds(cache: Cache, segs: Sequence[Seg], bounds: Bounds, row_seg, 
 
 
 def _list_shape(blocks, rows: int, hkv: int) -> int:
-    if len(blocks.shape) != 3 or tuple(blocks.shape[:2]) != (rows, hkv) or not blocks.is_contiguous():
+    shape = blocks.shape
+    if len(shape) != 3 or shape[0] != rows or shape[1] != hkv or not blocks.is_contiguous():
         raise ValueError("blocks must be contiguous [rows][hkv][nsel]")
-    return int(blocks.shape[2])
+    return shape[2]
 
 
 def tfpa_select_blocks(cache: Cache, segs: Sequence[Seg], bounds: Bounds, q, row_seg, row_pos,

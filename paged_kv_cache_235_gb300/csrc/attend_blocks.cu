@@ -9,9 +9,11 @@
 // Per CTA:
 //   warp 4      producer: a lane a list entry looks the entry and its page up
 //               (the chain of two loads runs once a 32 entries), then blocks
-//               stream in as stages of 64 keys, K and V (TMA tiles with 128B
-//               swizzle; a 4-bit cache's codes and scales as bulk copies);
-//   warps 0..3  consumers: 16 keys of every stage each.  Both products have the
+//               stream in as stages of 64 keys (bf16: 32), K and V (TMA tiles
+//               with 128B swizzle; a 4-bit cache's codes and scales as bulk
+//               copies);
+//   warps 0..3  consumers: 16 keys of a stage each (bf16: two warps a stage, the
+//               pairs in turn).  Both products have the
 //               keys' side as the MMA's 16 rows and the query vectors as its 8
 //               columns (with the vectors as rows, 4 query heads would leave 12
 //               of 16 rows empty): S^T = K Q^T, weights transposed in registers,
@@ -28,16 +30,19 @@ namespace {
 
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kStageKeys = 64;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 
 template <int KV>
 struct Cfg {
   static constexpr bool kF16 = KV != kKvBf16;          // f16 operands, kv head scales
+  static constexpr int kStageKeys = KV == kKvBf16 ? 32 : 64;
+  static constexpr int kStageWarps = kStageKeys / 16;  // consumer warps that read a stage
+  static constexpr int kGroups = kConsumers / kStageWarps;   // and groups of them, in turn
   static constexpr int kHalfStage =                    // K of 64 keys, or V
       kStageKeys * (KV == kKvBf16 ? 256 : KV == kKvFp8 ? 128 : kFp4CodeBytes + kFp4ScaleBytes);
   static constexpr int kStageBytes = 2 * kHalfStage;
-  static constexpr int kStages = KV == kKvBf16 ? 3 : KV == kKvFp8 ? 4 : 6;
+  // four CTAs of eight vectors a SM: a batch's clusters of eight then run at once
+  static constexpr int kStages = KV == kKvFp4 ? 5 : 3;
   static constexpr int kRing = kStages * kStageBytes;
 };
 
@@ -79,7 +84,7 @@ __device__ __forceinline__ void load_k(uint32_t sb, int row, int c, uint32_t (&k
   if (KV == kKvBf16) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 w = lds128(swz128(sb + (i >> 1) * 8192, row, 2 * c + (i & 1)));
+      const uint4 w = lds128(swz128(sb + (i >> 1) * (Cfg<KV>::kHalfStage / 2), row, 2 * c + (i & 1)));
       k[4 * i] = w.x;
       k[4 * i + 1] = w.y;
       k[4 * i + 2] = w.z;
@@ -99,7 +104,7 @@ __device__ __forceinline__ void load_k(uint32_t sb, int row, int c, uint32_t (&k
   } else {
     const uint4 w = lds128(sb + row * kFp4CodeBytes + 16 * c);
     const uint32_t s2 = e4m3x2_to_f16x2(
-        (uint16_t)lds16(sb + kStageKeys * kFp4CodeBytes + row * kFp4ScaleBytes + 2 * c));
+        (uint16_t)lds16(sb + Cfg<KV>::kStageKeys * kFp4CodeBytes + row * kFp4ScaleBytes + 2 * c));
     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -171,7 +176,8 @@ __device__ __forceinline__ void add_pv(uint32_t sb, int r0, int lane, const uint
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
       uint32_t a[4];
-      ldmatrix_x4_trans(a, swz128(sb + (t >> 2) * 8192, row, (2 * t & 7) + ((lane >> 3) & 1)));
+      ldmatrix_x4_trans(a, swz128(sb + (t >> 2) * (Cfg<KV>::kHalfStage / 2), row,
+                                  (2 * t & 7) + ((lane >> 3) & 1)));
       a[0] &= keep0;
       a[1] &= keep0;
       a[2] &= keep1;
@@ -203,7 +209,7 @@ __device__ __forceinline__ void add_pv(uint32_t sb, int r0, int lane, const uint
     for (int i = 0; i < 4; ++i) {
       const int row = r0 + key_of<KV>(2 * c + (i & 1) + 8 * (i >> 1));
       w[i] = lds64(sb + row * kFp4CodeBytes + 8 * gq);
-      s[i] = lds8(sb + kStageKeys * kFp4CodeBytes + row * kFp4ScaleBytes + gq);
+      s[i] = lds8(sb + Cfg<KV>::kStageKeys * kFp4CodeBytes + row * kFp4ScaleBytes + gq);
     }
     const uint32_t s01 = e4m3x2_to_f16x2((uint16_t)((s[0] | (s[1] << 8)) & prmt(keep0, 0, 0x4420)));
     const uint32_t s23 = e4m3x2_to_f16x2((uint16_t)((s[2] | (s[3] << 8)) & prmt(keep1, 0, 0x4420)));
@@ -227,14 +233,16 @@ __device__ __forceinline__ void add_pv(uint32_t sb, int r0, int lane, const uint
   }
 }
 
-// The producer warp.  False if a wait gave up.
+// The producer warp: units [u0, u1) of the list, 64 keys each (a block of `per`
+// units an entry).  False if a wait gave up.
 template <int KV>
-__device__ bool produce(const BlocksParams& p, const BlocksRun& run, const int32_t* list, int i0,
-                        int i1, int pos, int g, uint8_t* ring, Shared& sh) {
+__device__ bool produce(const BlocksParams& p, const BlocksRun& run, const int32_t* list, int u0,
+                        int u1, int per, int pos, int g, uint8_t* ring, Shared& sh) {
   using C = Cfg<KV>;
   const int lane = threadIdx.x & 31;
+  const int i1 = (u1 + per - 1) / per;
   uint32_t stage = 0;
-  for (int base = i0; base < i1; base += 32) {
+  for (int base = u0 / per; base < i1; base += 32) {
     // a lane an entry: the block, and the storage row of its first key
     int b = -1, row0 = 0;
     if (base + lane < i1) b = __ldg(list + base + lane);
@@ -259,8 +267,9 @@ __device__ bool produce(const BlocksParams& p, const BlocksRun& run, const int32
       todo &= todo - 1;
       const int key0 = __shfl_sync(0xffffffffu, b, l) * p.block;
       const int r0 = __shfl_sync(0xffffffffu, row0, l);
-      const int n = min(p.block, pos - key0 + 1);
-      for (int k = 0; k < n; k += kStageKeys, ++stage) {
+      const int first = (base + l) * per;                // the entry's first unit
+      const int n = min(64 * (u1 - first), min(p.block, pos - key0 + 1));
+      for (int k = 64 * max(0, u0 - first); k < n; k += C::kStageKeys, ++stage) {
         const int buf = stage % C::kStages;
         if (!warp_wait(&sh.empty[buf], ((stage / C::kStages) & 1) ^ 1, p.err_flag)) return false;
         if (lane == 0) {
@@ -272,8 +281,8 @@ __device__ bool produce(const BlocksParams& p, const BlocksRun& run, const int32
           mbar_arrive_expect_tx(fb, C::kStageBytes);
           if (KV == kKvFp4) {
             const size_t codes = fp4_codes(y), scales = fp4_scales(y);
-            constexpr uint32_t kCodes = kStageKeys * kFp4CodeBytes;
-            constexpr uint32_t kScales = kStageKeys * kFp4ScaleBytes;
+            constexpr uint32_t kCodes = C::kStageKeys * kFp4CodeBytes;
+            constexpr uint32_t kScales = C::kStageKeys * kFp4ScaleBytes;
             const uint8_t* kb = static_cast<const uint8_t*>(run.k_base);
             const uint8_t* vb = static_cast<const uint8_t*>(run.v_base);
             bulk_load(sk, kb + codes, kCodes, fb);
@@ -283,9 +292,9 @@ __device__ bool produce(const BlocksParams& p, const BlocksRun& run, const int32
           } else {
             const KVMaps& m = p.maps[run.src];
             tma_load_2d(sk, &m.k, 0, y, fb);
-            if (KV == kKvBf16) tma_load_2d(sk + 8192, &m.k, 64, y, fb);
+            if (KV == kKvBf16) tma_load_2d(sk + C::kHalfStage / 2, &m.k, 64, y, fb);
             tma_load_2d(sv, &m.v, 0, y, fb);
-            if (KV == kKvBf16) tma_load_2d(sv + 8192, &m.v, 64, y, fb);
+            if (KV == kKvBf16) tma_load_2d(sv + C::kHalfStage / 2, &m.v, 64, y, fb);
           }
         }
       }
@@ -333,15 +342,16 @@ __global__ void __launch_bounds__(kThreads)
   const BlocksRun& run = p.runs[ri];
   const int pos = run.pos0 + (row - run.row0);
   const int32_t* list = p.blocks + ((size_t)row * p.hkv + g) * p.nsel;
-  const int i0 = (int)((int64_t)p.nsel * part / p.parts);
-  const int i1 = (int)((int64_t)p.nsel * (part + 1) / p.parts);
+  const int per = p.block / 64;
+  const int u0 = (int)((int64_t)p.nsel * per * part / p.parts);
+  const int u1 = (int)((int64_t)p.nsel * per * (part + 1) / p.parts);
   const int vecs = min(kVecs, p.group - qt * kVecs);     // query vectors of this item
   const size_t head0 = (size_t)row * p.hq + (size_t)g * p.group + qt * kVecs;
 
   const int gq = lane >> 2, c = lane & 3;
   float o[NT][8][4], m[NT][2], l[NT][2];
   if (warp == kConsumers) {
-    if (!produce<KV>(p, run, list, i0, i1, pos, g, ring, sh)) sh.lost = 1;
+    if (!produce<KV>(p, run, list, u0, u1, per, pos, g, ring, sh)) sh.lost = 1;
   } else {
     uint32_t q[NT][16];
     float sc[NT][2];
@@ -359,7 +369,10 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int t = 0; t < 8; ++t) o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.f;
     }
-    const int r0 = 16 * warp;
+    const int r0 = 16 * (warp % C::kStageWarps);
+    // Every warp passes every stage, also those that are the other group's: the
+    // parity of a phase tells it from the next one only, so a warp must not be
+    // two loads of a stage ahead of what it has seen.
     for (uint32_t stage = 0;; ++stage) {
       const int buf = stage % C::kStages;
       if (!warp_wait(&sh.full[buf], (stage / C::kStages) & 1, p.err_flag)) {
@@ -369,7 +382,7 @@ __global__ void __launch_bounds__(kThreads)
       const int first = sh.key0[buf];
       if (first < 0) break;
       const int key0 = first + r0;
-      if (key0 <= pos) {
+      if (stage % C::kGroups == (uint32_t)(warp / C::kStageWarps) && key0 <= pos) {
         const uint32_t sk = smem_u32(ring + (size_t)buf * C::kStageBytes);
         // ---- S^T = K Q^T: keys key_of(gq), key_of(gq + 8); vectors 2c, 2c + 1
         float s[NT][4];

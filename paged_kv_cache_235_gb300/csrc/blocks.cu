@@ -56,40 +56,54 @@ __global__ void __launch_bounds__(kBoundThreads)
     at = (size_t)g * (run.slab_cap / p.block) + block;
   }
   const int t = threadIdx.x & 15;
-  float lo[8], hi[8];
+  // lowest and highest so far, two dims a word: bf16 (a bf16 cache) or f16, which
+  // hold every stored value
+  uint32_t lo[4], hi[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo[i] = INFINITY;
-    hi[i] = -INFINITY;
+  for (int i = 0; i < 4; ++i) {
+    lo[i] = KV == kKvBf16 ? 0x7F807F80u : 0x7C007C00u;
+    hi[i] = lo[i] | 0x80008000u;
   }
-  for (int r = threadIdx.x >> 4; r < n; r += kBoundThreads / 16) {
-    float x[8];
-    load8<KV>(run.k_base, row0 + r, t, x);
+  constexpr int kRows = kBoundThreads / 16;          // rows at a time
+  constexpr int kStep = 8;                           // and of those, loads in flight
+  for (int r0 = threadIdx.x >> 4; r0 < n; r0 += kRows * kStep) {
+    Raw8<KV> raw[kStep];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = x[i] != x[i] ? 0.f : x[i];
-      lo[i] = fminf(lo[i], v);
-      hi[i] = fmaxf(hi[i], v);
+    for (int u = 0; u < kStep; ++u)
+      if (r0 + u * kRows < n) raw[u].load(run.k_base, row0 + r0 + u * kRows, t);
+#pragma unroll
+    for (int u = 0; u < kStep; ++u) {
+      if (r0 + u * kRows >= n) break;
+      uint32_t x[4];
+      raw[u].words(x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] &= number_mask<KV>(x[i]);               // a NaN counts as 0
+        lo[i] = min2<KV>(lo[i], x[i]);
+        hi[i] = max2<KV>(hi[i], x[i]);
+      }
     }
   }
-  auto pack = [](const float (&v)[8]) {      // exact: see above
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                      pack_bf16x2(v[6], v[7]));
-  };
-  part[0][threadIdx.x] = pack(lo);
-  part[1][threadIdx.x] = pack(hi);
+  part[0][threadIdx.x] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  part[1][threadIdx.x] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   __syncthreads();
   if (threadIdx.x >= 32) return;
   const int which = threadIdx.x >> 4;        // lanes 0-15 the smallest, 16-31 the largest
-  float m[8];
-  unpack8(part[which][t], m);
-  for (int r = 1; r < kBoundThreads / 16; ++r) {
-    float x[8];
-    unpack8(part[which][r * 16 + t], x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = which ? fmaxf(m[i], x[i]) : fminf(m[i], x[i]);
+  uint4 m = part[which][t];
+  for (int r = 1; r < kRows; ++r) {
+    const uint4 x = part[which][r * 16 + t];
+    m.x = which ? max2<KV>(m.x, x.x) : min2<KV>(m.x, x.x);
+    m.y = which ? max2<KV>(m.y, x.y) : min2<KV>(m.y, x.y);
+    m.z = which ? max2<KV>(m.z, x.z) : min2<KV>(m.z, x.z);
+    m.w = which ? max2<KV>(m.w, x.w) : min2<KV>(m.w, x.w);
   }
-  reinterpret_cast<uint4*>(run.bounds)[(at * 2 + which) * 16 + t] = pack(m);
+  if (KV != kKvBf16) {                       // f16 to bf16: at most six bits, exact
+    m.x = bf16x2_of_f16x2(m.x);
+    m.y = bf16x2_of_f16x2(m.y);
+    m.z = bf16x2_of_f16x2(m.z);
+    m.w = bf16x2_of_f16x2(m.w);
+  }
+  reinterpret_cast<uint4*>(run.bounds)[(at * 2 + which) * 16 + t] = m;
 }
 
 // ---------------------------------------------------------------- selection
@@ -453,7 +467,7 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
 // R: rows of a cluster at most.  The grid: clusters of p.cluster CTAs, one for
 // each (row group, kv head).
 template <int R>
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, R == 1 ? 4 : 2)
     select_blocks_kernel(const __grid_constant__ SelectParams p) {
   __shared__ SelShared sh;
   extern __shared__ uint64_t dyn[];          // [cap] exact keys, then [cap] keys

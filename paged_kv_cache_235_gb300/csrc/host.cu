@@ -1644,6 +1644,7 @@ extern "C" int tfpa_rope_table(const tfpa_rope_spec* spec, int64_t first, int32_
   p.first = first;
   p.n = n;
   p.attn_scale = (float)spec->attn_scale;
+  p.steps = n >= 32768 ? 8 : 1;     // the threads of 8 a row still cover the GPU twice
   record(13, 0, n, 0, n, 0, 0, 0);
   return dry_run() ? TFPA_OK : to_err(launch_rope_table(p, stream));
 }
@@ -1656,6 +1657,10 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + (uint64_t)nb && y < x + (uint64_t)na;
 }
+
+// From this many heads on a thread group takes several: one a group then no
+// longer has all of them on the GPU at once.
+constexpr int32_t kWideHeads = 8192;
 
 int qkv_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const tfpa_qkv* in,
              const int32_t* row_seg, const int32_t* row_pos, int32_t rows, void* q_out,
@@ -1750,6 +1755,7 @@ int qkv_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const tfpa
     p.num_pages = c->num_pages;
     p.kv = c->dtype;
     const int32_t heads = nrows * (q_heads + c->hkv);
+    p.wide = heads >= kWideHeads;
     record(14, base, nrows, nr, heads, (heads + 15) / 16, in->q ? base * in->q_stride : 0,
            in->q ? (int64_t)base * c->hq * hd : 0);
     if (!dry_run())
@@ -1907,12 +1913,14 @@ int select_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const t
   return TFPA_OK;
 }
 
-// CTAs that share a row's list: one for every four stages of 64 keys, up to a
-// cluster of eight.  A function of the list's length only, so a row's bytes do
-// not depend on its batch.
+// CTAs that share a row's list: one for every 128 keys, up to a cluster of
+// eight.  A function of the list's length only, so a row's bytes do not depend on
+// its batch.
 int32_t block_parts(int32_t block, int32_t nsel) {
-  return (int32_t)std::min<int64_t>(8, ((int64_t)nsel * (block / 64) + 3) / 4);
+  return (int32_t)std::min<int64_t>(8, ((int64_t)nsel * (block / 64) + 1) / 2);
 }
+
+constexpr int32_t kMaxListed = 1 << 24;   // entries of a list, at most
 
 int blocks_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const void* q,
                 const int32_t* row_seg, const int32_t* row_pos, int32_t rows, int32_t block,
@@ -1923,7 +1931,8 @@ int blocks_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
   if (rows > 0 && (!q || !aligned(q, 16) || !blocks || !aligned(blocks, 4) || !out ||
                    !aligned(out, 16) || (lse && !aligned(lse, 4))))
     return TFPA_EINVAL;
-  if (!is_block(block) || nsel < 1 || !std::isfinite(scale) || !(scale > 0.f))
+  if (!is_block(block) || nsel < 1 || nsel > kMaxListed || !std::isfinite(scale) ||
+      !(scale > 0.f))
     return TFPA_EINVAL;
   thread_local std::vector<Run> runs;   // reused by every call of this thread
   if ((e = build_runs(segs, nseg, row_seg, row_pos, rows, runs))) return e;
@@ -1978,7 +1987,7 @@ int blocks_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
     if (c->dtype != TFPA_FP4_E2M1) {
       const bool fp8 = c->dtype == TFPA_FP8_E4M3;
       int32_t nsrc;
-      if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, 64, p.maps, nsrc))) return e;
+      if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, fp8 ? 64 : 32, p.maps, nsrc))) return e;
     }
     const int32_t items = (int32_t)(nrows * c->hkv * qtiles);
     record(17, base, nrows, nr, items, items * parts, base * hd, base * hd);

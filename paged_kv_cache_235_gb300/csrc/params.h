@@ -330,6 +330,7 @@ struct TableParams {
   int64_t first;              // position of the first row
   int32_t n;
   int32_t half;               // frequencies: rot_dim / 2
+  int32_t steps;              // rows a thread takes
   float attn_scale;
 };
 
@@ -357,6 +358,7 @@ struct QkvParams {
   int32_t hkv;
   int32_t num_pages;
   int32_t kv;                 // KvType
+  int32_t wide;               // four heads a thread group instead of one
 };
 
 // Bounds of the blocks of a launch: each run is consecutive blocks of a stream.
@@ -416,7 +418,7 @@ struct BlocksRun {
   int32_t pad_;
 };
 struct BlocksParams {
-  KVMaps maps[kMaxSources];   // boxes of 64 rows (bf16, e4m3)
+  KVMaps maps[kMaxSources];   // boxes of a stage's keys: 32 rows (bf16) or 64 (e4m3)
   BlocksRun runs[kMaxRuns];
   const __nv_bfloat16* q;     // rows of this launch: [rows][hq][128]
   const int32_t* blocks;      // [rows][hkv][nsel]

@@ -9,8 +9,10 @@
 // taken to within an eighth of a turn of a quarter turn (its top bits) and
 // only then rounded to float32.  Bound by the stores, 8 bytes an entry.
 //
-// Rows.  One 16-thread group per (row, head) as in the KV write kernel, a
-// q head or a kv head's K and V; a thread holds 8 head dims.  The mean
+// Rows.  A 16-thread group takes a q head, or a kv head's K and V, of a row,
+// and where there are rows enough four q heads or two kv heads: their loads are
+// then in flight together and share the row's angles and the weights.  A thread
+// holds 8 head dims.  The mean
 // square is added up pair by pair (a thread's 8, then lanes 1, 2, 4, 8
 // apart), and every product, sum, quotient and root is rounded to float32 on
 // its own, so that the stored codes are a function of the inputs alone.
@@ -24,34 +26,59 @@ namespace tfpa {
 
 namespace {
 constexpr int kTableThreads = 256;
-}
 
+// sin and cos of |x| <= pi / 4 by their Taylor polynomials, cut where the next
+// term is below 2^-29 (x^11 / 11! and x^12 / 12!); with the few roundings of the
+// last steps both are within 1.5 2^-24 of the value at 1.
+__device__ __forceinline__ void sin_cos(float x, float& sn, float& cs) {
+  const float y = x * x;
+  float a = fmaf(y, 1.f / 362880.f, -1.f / 5040.f);
+  a = fmaf(y, a, 1.f / 120.f);
+  a = fmaf(y, a, -1.f / 6.f);
+  sn = fmaf(x * y, a, x);
+  float b = fmaf(y, -1.f / 3628800.f, 1.f / 40320.f);
+  b = fmaf(y, b, -1.f / 720.f);
+  b = fmaf(y, b, 1.f / 24.f);
+  b = fmaf(y, b, -0.5f);
+  cs = fmaf(y, b, 1.f);
+}
+}  // namespace
+
+// A thread keeps four frequencies and takes p.steps rows of them (indexing the
+// launch parameters by lane costs a pass through the constant cache each).
 __global__ void __launch_bounds__(kTableThreads)
     rope_table_kernel(const __grid_constant__ TableParams p) {
   allow_next_grid();
   wait_prior_grid();
-  const int quads = p.half / 4;                    // four frequencies a thread
-  const int64_t i = (int64_t)blockIdx.x * kTableThreads + threadIdx.x;
-  if (i >= (int64_t)p.n * quads) return;
-  const int64_t row = i / quads;
-  const int f0 = (int)(i - row * quads) * 4;
-  const uint64_t t = (uint64_t)(p.first + row);
-  float c[4], s[4];
+  const int quads = p.half / 4, rows = kTableThreads / quads;
+  const int r = threadIdx.x / quads, f0 = (threadIdx.x - r * quads) * 4;
+  if (r >= rows) return;
+  uint64_t f[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint64_t turn = t * p.turns[f0 + j];
-    // the nearest quarter turn, and what is left of it in half turns
-    const uint32_t quarter = (uint32_t)((turn + (1ull << 61)) >> 62);
-    const float x = (float)(int64_t)(turn - ((uint64_t)quarter << 62)) * 0x1p-63f;
-    float sn, cs;
-    sincospif(x, &sn, &cs);
-    const float a = quarter & 1 ? sn : cs, b = quarter & 1 ? cs : sn;
-    c[j] = p.attn_scale * (quarter == 1 || quarter == 2 ? -a : a);
-    s[j] = p.attn_scale * (quarter >= 2 ? -b : b);
+  for (int j = 0; j < 4; ++j) f[j] = p.turns[f0 + j];
+  int64_t row = (int64_t)blockIdx.x * rows * p.steps + r;
+  for (int i = 0; i < p.steps && row < p.n; ++i, row += rows) {
+    const uint64_t t = (uint64_t)(p.first + row);
+    float c[4], s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t turn = t * f[j];
+      // the nearest quarter turn, and what is left of it (at most an eighth) in
+      // radians; the low word counts where the angle itself is small
+      const uint32_t quarter = ((uint32_t)(turn >> 32) + (1u << 29)) >> 30;
+      const uint64_t left = turn - ((uint64_t)quarter << 62);
+      const float x = fmaf((float)(int32_t)(left >> 32), 0x1p32f, (float)(uint32_t)left) *
+                      (float)(6.283185307179586 * 0x1p-64);
+      float sn, cs;
+      sin_cos(x, sn, cs);
+      const float u = quarter & 1 ? sn : cs, v = quarter & 1 ? cs : sn;
+      c[j] = p.attn_scale * (quarter == 1 || quarter == 2 ? -u : u);
+      s[j] = p.attn_scale * (quarter & 2 ? -v : v);
+    }
+    const size_t at = (size_t)row * p.half + f0;
+    *reinterpret_cast<float4*>(p.cos + at) = make_float4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<float4*>(p.sin + at) = make_float4(s[0], s[1], s[2], s[3]);
   }
-  const size_t at = (size_t)row * p.half + f0;
-  *reinterpret_cast<float4*>(p.cos + at) = make_float4(c[0], c[1], c[2], c[3]);
-  *reinterpret_cast<float4*>(p.sin + at) = make_float4(s[0], s[1], s[2], s[3]);
 }
 
 namespace {
@@ -60,131 +87,157 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                     pack_bf16x2(x[6], x[7]));
 }
-
-// x over the root of its mean square over the head, times w.
-__device__ __forceinline__ void norm8(float (&x)[8], const float* w, float eps, int t,
-                                      unsigned lanes) {
-  float s[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    s[i] = __fadd_rn(__fmul_rn(x[2 * i], x[2 * i]), __fmul_rn(x[2 * i + 1], x[2 * i + 1]));
-  float sum = __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
-#pragma unroll
-  for (int d = 1; d < 16; d *= 2) sum = __fadd_rn(sum, __shfl_xor_sync(lanes, sum, d));
-  const float inv =
-      __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.f / kHeadDim), eps)));
-  const float4* wp = reinterpret_cast<const float4*>(w + t * 8);
-  const float4 w0 = __ldg(wp), w1 = __ldg(wp + 1);
-  const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], inv), wv[i]);
+__device__ __forceinline__ void load8f(const float* a, float (&x)[8]) {
+  const float4 u = __ldg(reinterpret_cast<const float4*>(a));
+  const float4 v = __ldg(reinterpret_cast<const float4*>(a) + 1);
+  x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+  x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
 }
 
-// The first rot_dim dims of a head rotated by table row `rpos`.  All 16 lanes
-// take part in the exchange.
-__device__ __forceinline__ void rotate8(float (&x)[8], const QkvParams& p, int rpos, int t,
-                                        unsigned lanes) {
+// A lane's eight dims as pairs of floats, dims i and i + 4 in one: sums over
+// neighbours then take both halves of the eight at once.
+struct Dims {
+  f2 v[4];
+};
+__device__ __forceinline__ Dims unpack(const uint4& w) {
+  auto lo = [](uint32_t a) { return __uint_as_float(a << 16); };
+  auto hi = [](uint32_t a) { return __uint_as_float(a & 0xFFFF0000u); };
+  Dims d;
+  d.v[0] = f2{lo(w.x), lo(w.z)};
+  d.v[1] = f2{hi(w.x), hi(w.z)};
+  d.v[2] = f2{lo(w.y), lo(w.w)};
+  d.v[3] = f2{hi(w.y), hi(w.w)};
+  return d;
+}
+__device__ __forceinline__ Dims dims_of(const float (&x)[8]) {
+  Dims d;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d.v[i] = f2{x[i], x[i + 4]};
+  return d;
+}
+__device__ __forceinline__ void floats_of(const Dims& d, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = d.v[i].x;
+    x[i + 4] = d.v[i].y;
+  }
+}
+
+// (A packed sum of packed products would become a packed multiply-add, rounded
+// once: sums of products are scalar.)
+__device__ __forceinline__ f2 add_each(f2 a, f2 b) {
+  return f2{__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)};
+}
+
+// The lane's share of the sum of squares: neighbours first.
+__device__ __forceinline__ float squares(const Dims& d) {
+  const f2 a = add_each(fmul2(d.v[0], d.v[0]), fmul2(d.v[1], d.v[1]));
+  const f2 b = add_each(fmul2(d.v[2], d.v[2]), fmul2(d.v[3], d.v[3]));
+  const f2 c = add_each(a, b);
+  return __fadd_rn(c.x, c.y);
+}
+
+// 1 / sqrt(mean square + eps) of H heads from the lanes' shares.  Four heads:
+// the lanes 1 and 2 apart split the heads among them while they add, so that
+// each lane sums, and takes the root of, one head, and the roots are handed
+// round.  Every sum is the same pair of numbers as one head alone would add.
+template <int H>
+__device__ __forceinline__ void roots(float (&s)[H], float eps, int t, unsigned lanes) {
+  auto root = [&](float sum) {
+    return __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.f / kHeadDim), eps)));
+  };
+  if (H == 4) {
+    const bool b0 = t & 1, b1 = t & 2;
+    float k0 = b0 ? s[2 % H] : s[0], k1 = b0 ? s[3 % H] : s[1 % H];
+    k0 = __fadd_rn(k0, __shfl_xor_sync(lanes, b0 ? s[0] : s[2 % H], 1));
+    k1 = __fadd_rn(k1, __shfl_xor_sync(lanes, b0 ? s[1 % H] : s[3 % H], 1));
+    float k = __fadd_rn(b1 ? k1 : k0, __shfl_xor_sync(lanes, b1 ? k0 : k1, 2));
+    k = __fadd_rn(k, __shfl_xor_sync(lanes, k, 4));
+    k = __fadd_rn(k, __shfl_xor_sync(lanes, k, 8));
+    const float inv = root(k);
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      s[h] = __shfl_sync(lanes, inv, (threadIdx.x & 16) + (h >> 1) + 2 * (h & 1));
+  } else {
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+#pragma unroll
+      for (int d = 1; d < 16; d *= 2) s[h] = __fadd_rn(s[h], __shfl_xor_sync(lanes, s[h], d));
+      s[h] = root(s[h]);
+    }
+  }
+}
+
+// How a lane's eight dims turn: cos and sin of its pairs, and where the other
+// halves of the pairs are.  (Interleaved: pairs of neighbours, four of each.)
+struct Turn {
+  Dims c, s;               // s negated where a lane holds the pairs' first dims
+  int from;                // the lane (of the warp) that holds the partners
+  bool on;                 // this lane's dims turn
+};
+
+__device__ __forceinline__ Turn make_turn(const QkvParams& p, int rpos, int t) {
+  Turn u;
   const int half = p.rot_dim / 2;
-  const float* cp = p.rope_cos + (size_t)rpos * half;
-  const float* sp = p.rope_sin + (size_t)rpos * half;
-  if (p.interleaved) {                       // dims 2i and 2i + 1: a thread's own
-    if (t * 8 >= p.rot_dim) return;
-    const float4 c4 = __ldg(reinterpret_cast<const float4*>(cp + t * 4));
-    const float4 s4 = __ldg(reinterpret_cast<const float4*>(sp + t * 4));
-    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+  const size_t row = (size_t)rpos * half;
+  u.from = 0;
+  u.on = t * 8 < p.rot_dim;
+  if (p.interleaved) {                       // dims 2i and 2i + 1: a lane's own
+    if (!u.on) return u;
+    const float4 c4 = __ldg(reinterpret_cast<const float4*>(p.rope_cos + row + t * 4));
+    const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.rope_sin + row + t * 4));
+    const float c[8] = {c4.x, c4.x, c4.y, c4.y, c4.z, c4.z, c4.w, c4.w};
+    const float s[8] = {-s4.x, s4.x, -s4.y, s4.y, -s4.z, s4.z, -s4.w, s4.w};
+    u.c = dims_of(c);
+    u.s = dims_of(s);
+    return u;
+  }
+  const int hl = half / 8;                   // dims i and i + half: half / 8 lanes apart
+  const bool second = t >= hl;
+  u.from = (threadIdx.x & 16) + (!u.on ? t : second ? t - hl : t + hl);
+  if (!u.on) return u;
+  const int i0 = (second ? t - hl : t) * 8;
+  float c[8], s[8];
+  load8f(p.rope_cos + row + i0, c);
+  load8f(p.rope_sin + row + i0, s);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = second ? s[i] : -s[i];
+  u.c = dims_of(c);
+  u.s = dims_of(s);
+  return u;
+}
+
+// Eight dims of a head rotated: a c - b s and b c + a s are both the dim's own
+// product and, rounded on its own, its partner's under sin's sign.  All 16 lanes
+// take part in the exchange.
+__device__ __forceinline__ void rotate(Dims& x, const Turn& u, bool interleaved, unsigned lanes) {
+  Dims o;
+  if (interleaved) {                         // dims 0, 1 and 2, 3 of each four
+    o.v[0] = x.v[1];
+    o.v[1] = x.v[0];
+    o.v[2] = x.v[3];
+    o.v[3] = x.v[2];
+  } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-      x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+      o.v[i].x = __shfl_sync(lanes, x.v[i].x, u.from);
+      o.v[i].y = __shfl_sync(lanes, x.v[i].y, u.from);
     }
-    return;
   }
-  // dims i and i + half: the thread half / 8 lanes away holds the partners
-  const int hl = half / 8;
-  const bool second = t >= hl;
-  const int from = (threadIdx.x & 16) + (t >= 2 * hl ? t : second ? t - hl : t + hl);
-  float other[8];
+  if (!u.on) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) other[i] = __shfl_sync(lanes, x[i], from);
-  if (t >= 2 * hl) return;
-  const int i0 = (second ? t - hl : t) * 8;
-  const float4 c0 = __ldg(reinterpret_cast<const float4*>(cp + i0));
-  const float4 c1 = __ldg(reinterpret_cast<const float4*>(cp + i0 + 4));
-  const float4 s0 = __ldg(reinterpret_cast<const float4*>(sp + i0));
-  const float4 s1 = __ldg(reinterpret_cast<const float4*>(sp + i0 + 4));
-  const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-  const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float a = second ? other[e] : x[e];   // dim i
-    const float b = second ? x[e] : other[e];   // dim i + half
-    x[e] = second ? __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]))
-                  : __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
-  }
+  for (int i = 0; i < 4; ++i)
+    x.v[i] = add_each(fmul2(x.v[i], u.c.v[i]), fmul2(o.v[i], u.s.v[i]));
 }
 
-}  // namespace
-
-__global__ void __launch_bounds__(256) write_qkv_kernel(const __grid_constant__ QkvParams p) {
-  allow_next_grid();
-  wait_prior_grid();
-  const int slots = p.q_heads + p.hkv;                     // heads of a row: q, then kv
-  const int gid = blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int t = threadIdx.x & 15;                          // 8-element slice
-  if (gid >= p.rows * slots) return;
-  const unsigned lanes = 0xFFFFu << (threadIdx.x & 16);    // the head's 16 threads
-  const int row = gid / slots;
-  const int slot = gid - row * slots;
-  int ri = 0;
-  while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
-  const WriteRun& run = p.runs[ri];
-  const int pos = run.pos0 + (row - run.row0);
-  int rpos = pos;
-  if (p.rope_cos && p.rope_pos) rpos = __ldg(p.rope_pos + row);
-  const bool off_table = p.rope_cos && (unsigned)rpos >= (unsigned)p.rope_n;
-  float x[8];
-  if (slot < p.q_heads) {
-    const uint4 in = *reinterpret_cast<const uint4*>(p.q + (size_t)row * p.q_stride +
-                                                     slot * kHeadDim + t * 8);
-    if (off_table) {                                       // all 16 lanes alike
-      if (t == 0) flag_error(p.err_flag, kErrRopeRange);
-      return;
-    }
-    unpack8(in, x);
-    if (p.q_weight) norm8(x, p.q_weight, p.eps, t, lanes);
-    if (p.rope_cos) rotate8(x, p, rpos, t, lanes);
-    *reinterpret_cast<uint4*>(p.q_out + ((size_t)row * p.q_heads + slot) * kHeadDim + t * 8) =
-        p.q_weight || p.rope_cos ? pack8(x) : in;
-    return;
-  }
-  const int g = slot - p.q_heads;
-  const int pid = run.page_table ? __ldg(run.page_table + (pos >> 8)) : 0;
-  const uint4 kv = *reinterpret_cast<const uint4*>(p.k + (size_t)row * p.k_stride +
-                                                   g * kHeadDim + t * 8);
-  const uint4 vv = *reinterpret_cast<const uint4*>(p.v + (size_t)row * p.v_stride +
-                                                   g * kHeadDim + t * 8);
-  if (off_table) {
-    if (t == 0) flag_error(p.err_flag, kErrRopeRange);
-    return;
-  }
-  size_t dst_row;
-  if (run.page_table) {
-    if ((unsigned)pid >= (unsigned)p.num_pages) {
-      if (t == 0) flag_error(p.err_flag, kErrBadPage);
-      return;
-    }
-    dst_row = ((size_t)pid * p.hkv + g) * kPage + (pos & (kPage - 1));
-  } else {
-    dst_row = (size_t)g * run.slab_cap + pos;
-  }
-  unpack8(kv, x);
-  if (p.k_weight) norm8(x, p.k_weight, p.eps, t, lanes);
-  if (p.rope_cos) rotate8(x, p, rpos, t, lanes);
+// A row's K (x, and kx as bf16) and V of one kv head into the cache.
+__device__ __forceinline__ void store_kv(const QkvParams& p, const WriteRun& run, size_t dst_row,
+                                         int g, int t, unsigned lanes, float (&x)[8],
+                                         const uint4& kx, const uint4& vv) {
   if (p.kv == kKvBf16) {
     __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(run.k_dst) + dst_row * kHeadDim + t * 8;
     __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(run.v_dst) + dst_row * kHeadDim + t * 8;
-    *reinterpret_cast<uint4*>(kd) = p.k_weight || p.rope_cos ? pack8(x) : kv;
+    *reinterpret_cast<uint4*>(kd) = kx;
     *reinterpret_cast<uint4*>(vd) = vv;
     return;
   }
@@ -192,30 +245,132 @@ __global__ void __launch_bounds__(256) write_qkv_kernel(const __grid_constant__ 
   unpack8(vv, vf);
   uint8_t* kb = static_cast<uint8_t*>(run.k_dst);
   uint8_t* vb = static_cast<uint8_t*>(run.v_dst);
+  const float gk = __ldg(p.k_scale + g), gv = __ldg(p.v_scale + g);
   if (p.kv == kKvFp4) {
     const size_t codes = fp4_codes(dst_row) + t * 4, scales = fp4_scales(dst_row) + (t >> 1);
     uint32_t ks, vs;
-    *reinterpret_cast<uint32_t*>(kb + codes) = quant8_fp4(x, __ldg(p.k_scale + g), lanes, ks);
-    *reinterpret_cast<uint32_t*>(vb + codes) = quant8_fp4(vf, __ldg(p.v_scale + g), lanes, vs);
+    *reinterpret_cast<uint32_t*>(kb + codes) = quant8_fp4(x, gk, lanes, ks);
+    *reinterpret_cast<uint32_t*>(vb + codes) = quant8_fp4(vf, gv, lanes, vs);
     if (!(t & 1)) {
       kb[scales] = (uint8_t)ks;
       vb[scales] = (uint8_t)vs;
     }
     return;
   }
-  *reinterpret_cast<uint2*>(kb + dst_row * kHeadDim + t * 8) = quant8(x, __ldg(p.k_scale + g));
-  *reinterpret_cast<uint2*>(vb + dst_row * kHeadDim + t * 8) = quant8(vf, __ldg(p.v_scale + g));
+  *reinterpret_cast<uint2*>(kb + dst_row * kHeadDim + t * 8) = quant8(x, gk);
+  *reinterpret_cast<uint2*>(vb + dst_row * kHeadDim + t * 8) = quant8(vf, gv);
+}
+
+}  // namespace
+
+// H: query heads of a 16-lane group at most; a group of kv heads has half as
+// many (but one), each with its K and V.
+template <int H>
+__global__ void __launch_bounds__(256, H > 1 ? 3 : 4)
+    write_qkv_kernel(const __grid_constant__ QkvParams p) {
+  constexpr int HK = H > 1 ? H / 2 : 1;
+  allow_next_grid();
+  wait_prior_grid();
+  const int q_units = (p.q_heads + H - 1) / H, units = q_units + (p.hkv + HK - 1) / HK;
+  const int gid = blockIdx.x * (blockDim.x / 16) + (threadIdx.x >> 4);
+  const int t = threadIdx.x & 15;                          // 8-element slice
+  if (gid >= p.rows * units) return;
+  const unsigned lanes = 0xFFFFu << (threadIdx.x & 16);    // the group's 16 threads
+  const int row = gid / units;
+  const int unit = gid - row * units;
+  int ri = 0;
+  while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
+  const WriteRun& run = p.runs[ri];
+  const int pos = run.pos0 + (row - run.row0);
+  int rpos = pos;
+  if (p.rope_pos) rpos = __ldg(p.rope_pos + row);
+  const bool is_q = unit < q_units;
+  // ---- the heads' dims are on their way before anything else is looked at
+  uint4 in[H], vin[HK];
+  const int h0 = is_q ? unit * H : (unit - q_units) * HK;
+  const int nh = min(is_q ? H : HK, (is_q ? p.q_heads : p.hkv) - h0);
+  const __nv_bfloat16* src =
+      (is_q ? p.q + (size_t)row * p.q_stride : p.k + (size_t)row * p.k_stride) + h0 * kHeadDim +
+      t * 8;
+  const int pid = !is_q && run.page_table ? __ldg(run.page_table + (pos >> 8)) : 0;
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    if (h < nh) in[h] = *reinterpret_cast<const uint4*>(src + h * kHeadDim);
+  if (!is_q) {
+    const __nv_bfloat16* vs = p.v + (size_t)row * p.v_stride + h0 * kHeadDim + t * 8;
+#pragma unroll
+    for (int h = 0; h < HK; ++h)
+      if (h < nh) vin[h] = *reinterpret_cast<const uint4*>(vs + h * kHeadDim);
+  }
+  const float* weight = is_q ? p.q_weight : p.k_weight;
+  Dims w;
+  if (weight) {
+    float f[8];
+    load8f(weight + t * 8, f);
+    w = dims_of(f);
+  }
+  Turn turn;
+  if (p.rope_cos) {
+    if ((unsigned)rpos >= (unsigned)p.rope_n) {            // all 16 lanes alike
+      if (t == 0) flag_error(p.err_flag, kErrRopeRange);
+      return;
+    }
+    turn = make_turn(p, rpos, t);
+  }
+  if (!is_q && run.page_table && (unsigned)pid >= (unsigned)p.num_pages) {
+    if (t == 0) flag_error(p.err_flag, kErrBadPage);
+    return;
+  }
+  // ---- the heads' roots together, then head by head
+  const bool turns = weight || p.rope_cos;
+  float inv[H];
+  if (weight) {
+#pragma unroll
+    for (int h = 0; h < H; ++h) inv[h] = h < nh ? squares(unpack(in[h])) : 0.f;
+    roots<H>(inv, p.eps, t, lanes);
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    if (h >= nh) break;
+    Dims x = unpack(in[h]);
+    if (weight) {
+      const f2 r = f2{inv[h], inv[h]};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x.v[i] = fmul2(fmul2(x.v[i], r), w.v[i]);
+    }
+    if (p.rope_cos) rotate(x, turn, p.interleaved, lanes);
+    float f[8];
+    floats_of(x, f);
+    if (is_q) {
+      *reinterpret_cast<uint4*>(p.q_out + ((size_t)row * p.q_heads + h0 + h) * kHeadDim + t * 8) =
+          turns ? pack8(f) : in[h];
+    } else if (h < HK) {
+      const int g = h0 + h;
+      const size_t dst_row = run.page_table
+                                 ? ((size_t)pid * p.hkv + g) * kPage + (pos & (kPage - 1))
+                                 : (size_t)g * run.slab_cap + pos;
+      store_kv(p, run, dst_row, g, t, lanes, f, turns ? pack8(f) : in[h], vin[h < HK ? h : 0]);
+    }
+  }
 }
 
 cudaError_t launch_rope_table(const TableParams& p, cudaStream_t s) {
-  const int64_t threads = (int64_t)p.n * (p.half / 4);
-  const int grid = (int)((threads + kTableThreads - 1) / kTableThreads);
-  return launch_pdl(rope_table_kernel, dim3(grid), dim3(kTableThreads), 0, s, p);
+  const int64_t rows = (int64_t)(kTableThreads / (p.half / 4)) * p.steps;
+  return launch_pdl(rope_table_kernel, dim3((unsigned)((p.n + rows - 1) / rows)),
+                    dim3(kTableThreads), 0, s, p);
 }
 
+namespace {
+template <int H>
+cudaError_t launch_rows(const QkvParams& p, cudaStream_t s) {
+  constexpr int HK = H > 1 ? H / 2 : 1;
+  const int groups = p.rows * ((p.q_heads + H - 1) / H + (p.hkv + HK - 1) / HK);
+  return launch_pdl(write_qkv_kernel<H>, dim3((groups + 15) / 16), dim3(256), 0, s, p);
+}
+}  // namespace
+
 cudaError_t launch_write_qkv(const QkvParams& p, cudaStream_t s) {
-  const int heads = p.rows * (p.q_heads + p.hkv);
-  return launch_pdl(write_qkv_kernel, dim3((heads + 15) / 16), dim3(256), 0, s, p);
+  return p.wide ? launch_rows<4>(p, s) : launch_rows<1>(p, s);
 }
 
 }  // namespace tfpa

@@ -20,8 +20,8 @@ class Rows(Plane):
         super().__init__(rows, heads, 128, ptr=ptr)
         self._s, self._dense = (stride or heads * 128, head, last), dense
 
-    def stride(self, i):
-        return self._s[i]
+    def stride(self, i=None):
+        return self._s if i is None else self._s[i]
 
     def is_contiguous(self):
         return self._dense
