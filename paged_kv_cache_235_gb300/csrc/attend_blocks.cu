@@ -31,6 +31,7 @@ namespace {
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
+constexpr int kRow = kHeadDim + 4;          // a state's row: the four columns' in banks of their own
 
 template <int KV>
 struct Cfg {
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(kThreads)
   // ---- the warps' states, folded: [warp][vector][dim] in the ring, which every
   // load has left, then [vector][dim] behind them
   float* fold = reinterpret_cast<float*>(ring);
-  float* mine = fold + kConsumers * kVecs * kHeadDim;
+  float* mine = fold + kConsumers * kVecs * kRow;
   if (warp < kConsumers) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(kThreads)
       for (int t = 0; t < 8; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          fold[(warp * kVecs + 8 * n + 2 * c + (j & 1)) * kHeadDim +
+          fold[(warp * kVecs + 8 * n + 2 * c + (j & 1)) * kRow +
                dim_of<KV>(t, gq + 8 * (j >> 1))] = o[n][t][j];
   }
   __syncthreads();
@@ -493,14 +494,14 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int w = 0; w < kConsumers; ++w) {
       const float a = sh.m[w][v] == -INFINITY ? 0.f : fast_exp2(sh.m[w][v] - M);
-      const float4 x = *reinterpret_cast<const float4*>(fold + (w * kVecs + v) * kHeadDim + d);
+      const float4 x = *reinterpret_cast<const float4*>(fold + (w * kVecs + v) * kRow + d);
       L = fmaf(a, sh.l[w][v], L);
       acc.x = fmaf(a, x.x, acc.x);
       acc.y = fmaf(a, x.y, acc.y);
       acc.z = fmaf(a, x.z, acc.z);
       acc.w = fmaf(a, x.w, acc.w);
     }
-    *reinterpret_cast<float4*>(mine + v * kHeadDim + d) = acc;
+    *reinterpret_cast<float4*>(mine + v * kRow + d) = acc;
     if (d == 0) {
       sh.part_m[v] = M;
       sh.part_l[v] = L;
@@ -514,27 +515,42 @@ __global__ void __launch_bounds__(kThreads)
     cluster_sync();
   else
     __syncthreads();
-  for (int i = part * kThreads + tid; i < vecs * (kHeadDim / 4); i += p.parts * kThreads) {
-    const int v = i / (kHeadDim / 4), d = i % (kHeadDim / 4) * 4;
-    float M = -INFINITY, L = 0.f;
-    const uint32_t pm = smem_u32(&sh.part_m[v]), pl = smem_u32(&sh.part_l[v]);
-    for (int r = 0; r < p.parts; ++r)
-      M = fmaxf(M, __uint_as_float(ld_cluster_u32(mapa_shared(pm, r))));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int r = 0; r < p.parts; ++r) {
-      const float mr = __uint_as_float(ld_cluster_u32(mapa_shared(pm, r)));
-      const float a = mr == -INFINITY ? 0.f : fast_exp2(mr - M);
-      L = fmaf(a, __uint_as_float(ld_cluster_u32(mapa_shared(pl, r))), L);
-      const float4 x = ld_cluster_f4(mapa_shared(smem_u32(mine + v * kHeadDim + d), r));
-      acc.x = fmaf(a, x.x, acc.x);
-      acc.y = fmaf(a, x.y, acc.y);
-      acc.z = fmaf(a, x.z, acc.z);
-      acc.w = fmaf(a, x.w, acc.w);
+  // eight lanes an element of four dims, a part each: one trip to the other CTAs
+  const int j = lane & 7;
+  const int per_cta = (vecs * (kHeadDim / 4) + p.parts - 1) / p.parts;
+  const int e1 = min(vecs * (kHeadDim / 4), (part + 1) * per_cta);
+  for (int e0 = part * per_cta + (warp * 32 + lane) / 8; e0 - (lane >> 3) < e1;
+       e0 += kThreads / 8) {
+    const int e = min(e0, e1 - 1), v = e / (kHeadDim / 4), d = e % (kHeadDim / 4) * 4;
+    float mj = -INFINITY, lj = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j < p.parts) {
+      mj = __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.part_m[v]), j)));
+      lj = __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.part_l[v]), j)));
+      x = ld_cluster_f4(mapa_shared(smem_u32(mine + v * kRow + d), j));
     }
+    float M = mj;
+#pragma unroll
+    for (int k = 1; k < 8; k *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+    const float a = mj == -INFINITY ? 0.f : fast_exp2(mj - M);
+    float L = a * lj;
+    x.x *= a;
+    x.y *= a;
+    x.z *= a;
+    x.w *= a;
+#pragma unroll
+    for (int k = 1; k < 8; k *= 2) {
+      L += __shfl_xor_sync(0xffffffffu, L, k);
+      x.x += __shfl_xor_sync(0xffffffffu, x.x, k);
+      x.y += __shfl_xor_sync(0xffffffffu, x.y, k);
+      x.z += __shfl_xor_sync(0xffffffffu, x.z, k);
+      x.w += __shfl_xor_sync(0xffffffffu, x.w, k);
+    }
+    if (j != 0 || e0 >= e1) continue;
     const float f = L == 0.f ? 0.f : vs / L;         // no key: zeros
     uint2 w;
-    w.x = pack_bf16x2(acc.x * f, acc.y * f);
-    w.y = pack_bf16x2(acc.z * f, acc.w * f);
+    w.x = pack_bf16x2(x.x * f, x.y * f);
+    w.y = pack_bf16x2(x.z * f, x.w * f);
     *reinterpret_cast<uint2*>(p.out + (head0 + v) * kHeadDim + d) = w;
     if (d == 0 && p.lse)
       p.lse[head0 + v] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
@@ -546,7 +562,7 @@ __global__ void __launch_bounds__(kThreads)
 template <int KV, int NT>
 cudaError_t launch(const BlocksParams& p, cudaStream_t s) {
   constexpr int kSmem = Cfg<KV>::kRing + 1024;
-  static_assert((kConsumers + 1) * 8 * NT * kHeadDim * 4 <= Cfg<KV>::kRing, "fold buffers");
+  static_assert((kConsumers + 1) * 8 * NT * kRow * 4 <= Cfg<KV>::kRing, "fold buffers");
   static PerDeviceOnce configured;
   const cudaError_t e = configured.run([] {
     return cudaFuncSetAttribute(decode_blocks_kernel<KV, NT>,

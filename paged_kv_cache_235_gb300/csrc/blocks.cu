@@ -145,7 +145,9 @@ struct SelShared {
   union {
     uint32_t hist[kBins];
     double q64[256];         // sum_h min(q, 0) (0..127), sum_h max(q, 0) (128..255), for exact
-  };                         // scores, between two uses of the histogram
+                             // scores, between two uses of the histogram
+    float q32[4][256];       // and before its first use, of each row
+  };
   uint32_t most[kMaxCluster * kSelWarps];   // largest |bound| (bf16 bits; ~0: a score was no
                                             // number), of every warp of the cluster
   uint32_t warp_s[kSelWarps];
@@ -224,23 +226,46 @@ __device__ __forceinline__ float reduce8(const float (&v)[8], int lane) {
 }
 
 // The rows' blocks from the keys in this CTA's shared memory: the want-th
-// largest, what is near it, and the list.
+// largest, what is near it, and the list.  A thread takes eight consecutive keys
+// of a round of 2,048, and keeps them in registers where one round is all.
 __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bfloat16* q, int g,
                        int n, int ranks, float q1, uint32_t* key32, uint64_t* key64,
                        SelShared& sh, int32_t* out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kRound = 8 * kSelThreads;
+  const bool one = n <= kRound;
+  bool loaded = false;
+  uint32_t k[8];
+  // fn(first block, its eight keys), round by round
+  auto rounds = [&](auto&& fn) {
+    for (int base = 0; base < n; base += kRound) {
+      const int b = base + 8 * tid;
+      if (!one || !loaded) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k[i] = kAbsent;
+        if (b < n) {                     // (the keys' memory is whole eights)
+          const uint4 u = *reinterpret_cast<const uint4*>(key32 + b);
+          const uint4 v = *reinterpret_cast<const uint4*>(key32 + b + 4);
+          const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (b + i < n) k[i] = w[i];
+        }
+      }
+      fn(b);
+    }
+    loaded = true;
+  };
   // ---- how many are free to choose from, and their range
   uint32_t counts = 0, kmin = 0xFFFFFFFFu, kmax = 0;     // counts: taken << 16 | free (18,432 at most)
-  for (int b = tid; b < n; b += kSelThreads) {
-    const uint32_t k = key32[b];
-    if (k == kTaken) {
-      counts += 0x10000u;
-    } else if (k != kAbsent) {
-      ++counts;
-      kmin = min(kmin, k);
-      kmax = max(kmax, k);
+  rounds([&](int) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      counts += k[i] == kTaken ? 0x10000u : k[i] != kAbsent ? 1u : 0u;
+      kmin = min(kmin, k[i] - 1u);       // (kAbsent wraps to the largest)
+      kmax = max(kmax, k[i] == kTaken ? 0u : k[i]);
     }
-  }
+  });
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   counts = __reduce_add_sync(0xffffffffu, counts);
@@ -250,9 +275,14 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
     sh.warp_s[warp] = counts;
   }
   if (tid == 0) sh.count = 0;
-  for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+  auto clear = [&] {
+    reinterpret_cast<uint4*>(sh.hist)[tid] = make_uint4(0, 0, 0, 0);
+    reinterpret_cast<uint4*>(sh.hist)[tid + kSelThreads] = make_uint4(0, 0, 0, 0);
+  };
+  static_assert(kBins == 8 * kSelThreads, "histogram");
+  clear();
   __syncthreads();
-  uint32_t ntaken = 0, nfree = 0, most = 0;
+  uint32_t ntaken = 0, nfree = 0;
 #pragma unroll
   for (int w = 0; w < kSelWarps; ++w) {
     kmin = min(kmin, sh.warp_lo[w]);
@@ -260,6 +290,7 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
     ntaken += sh.warp_s[w] >> 16;
     nfree += sh.warp_s[w] & 0xFFFFu;
   }
+  kmin += 1u;
   const uint32_t want = min(nfree, p.nsel > (int)ntaken ? p.nsel - ntaken : 0u);
   uint32_t in_from = 0;                  // keys from here on are in, but for near ones
   float low = 0.f, top = 0.f;
@@ -267,7 +298,9 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
   if (want == 0) {
     in_from = kTaken;
   } else if (want < nfree) {
-    for (int i = 0; i < ranks * kSelWarps; ++i) most = max(most, sh.most[i]);
+    uint32_t most = lane < ranks * kSelWarps ? sh.most[lane] : 0u;
+    if (lane + 32 < ranks * kSelWarps) most = max(most, sh.most[lane + 32]);
+    most = __reduce_max_sync(0xffffffffu, most);
     // ---- the want-th largest key
     const uint32_t differ = kmin ^ kmax;
     int shift = differ ? 32 - __clz(differ) : 0;         // bits that are not the same in all
@@ -277,16 +310,20 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
       const int bits = min(shift, 11);
       const uint32_t high = shift == 32 ? 0u : ~0u << shift;
       shift -= bits;
-      for (int b = tid; b < n; b += kSelThreads) {
-        const uint32_t k = key32[b];
-        if (is_score(k) && (k & high) == prefix)
-          atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1)], 1u);
-      }
+      rounds([&](int) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (is_score(k[i]) && (k[i] & high) == prefix)
+            atomicAdd(&sh.hist[(k[i] >> shift) & ((1u << bits) - 1)], 1u);
+      });
       __syncthreads();
       // thread t: the eight bins from 2047 - 8 t down
-      uint32_t c[8], sum = 0;
+      const uint4 u = reinterpret_cast<const uint4*>(sh.hist)[kBins / 4 - 1 - 2 * tid];
+      const uint4 v = reinterpret_cast<const uint4*>(sh.hist)[kBins / 4 - 2 - 2 * tid];
+      const uint32_t c[8] = {u.w, u.z, u.y, u.x, v.w, v.z, v.y, v.x};
+      uint32_t sum = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += c[i] = sh.hist[kBins - 1 - 8 * tid - i];
+      for (int i = 0; i < 8; ++i) sum += c[i];
       uint32_t total, above = sel_prefix(sum, sh.warp_s, total);
       if (above < rest && rest <= above + sum) {
 #pragma unroll
@@ -306,26 +343,30 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
       if (shift > 0 && same <= kNear) {
         // few share the leading bits: the rest-th largest of them directly
         const uint32_t lead = ~0u << shift;
-        for (int b = tid; b < n; b += kSelThreads) {
-          const uint32_t k = key32[b];
-          if (is_score(k) && (k & lead) == prefix) sh.near_k[atomicAdd(&sh.count, 1u)] = k;
-        }
+        rounds([&](int) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (is_score(k[i]) && (k[i] & lead) == prefix)
+              sh.near_k[atomicAdd(&sh.count, 1u)] = k[i];
+        });
         __syncthreads();
         if (tid < (int)same) {
-          const uint32_t k = (uint32_t)sh.near_k[tid];
+          const uint32_t mine = (uint32_t)sh.near_k[tid];
           uint32_t more = 0, equal = 0;
+#pragma unroll 4
           for (uint32_t i = 0; i < same; ++i) {
-            more += (uint32_t)sh.near_k[i] > k;
-            equal += (uint32_t)sh.near_k[i] == k;
+            const uint32_t other = (uint32_t)sh.near_k[i];
+            more += other > mine;
+            equal += other == mine;
           }
-          if (more < rest && rest <= more + equal) sh.border = k;
+          if (more < rest && rest <= more + equal) sh.border = mine;
         }
         __syncthreads();
         prefix = sh.border;
         break;
       }
       if (shift > 0) {
-        for (int i = tid; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+        clear();
         __syncthreads();
       }
     }
@@ -339,26 +380,24 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
     all = most >= 0x7F80u || !(e < INFINITY);
     top = at + 2.125f * e;
     low = at - 2.125f * e;
+    auto is_near = [&](uint32_t x) {
+      if (!is_score(x)) return false;
+      const float s = value32(x);
+      return all || (s >= low && s <= top);
+    };
     uint32_t both = 0;                   // in << 16 | near
-    for (int b = tid; b < n; b += kSelThreads) {
-      const uint32_t k = key32[b];
-      if (!is_score(k)) continue;
-      const float s = value32(k);
-      both += all || (s >= low && s <= top) ? 1u : s > top ? 0x10000u : 0u;
-    }
+    rounds([&](int) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        both += is_near(k[i]) ? 1u : is_score(k[i]) && value32(k[i]) > top ? 0x10000u : 0u;
+    });
     uint32_t total;
     sel_prefix(both, sh.warp_s, total);
     const uint32_t near = total & 0xFFFFu, need = want - (total >> 16);
     if (near == need) {
-      in_from = all ? 1u : order32(low);
-      all = false;
+      in_from = order32(low);
     } else {
       // ---- the near ones' exact scores
-      auto is_near = [&](uint32_t k) {
-        if (!is_score(k)) return false;
-        const float s = value32(k);
-        return all || (s >= low && s <= top);
-      };
       if (tid < 128) {
         double down = 0.0, up = 0.0;
         for (int h = 0; h < p.group; ++h) {
@@ -372,15 +411,17 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
       if (tid == 0) sh.count = 0;
       __syncthreads();
       if (near <= kNear) {
-        for (int b = tid; b < n; b += kSelThreads) {
-          const uint32_t k = key32[b];
-          if (is_near(k)) {
-            sh.near_i[atomicAdd(&sh.count, 1u)] = b;
-            key32[b] = kAbsent;
-          } else if (is_score(k)) {
-            key32[b] = value32(k) > top ? kTaken : kAbsent;
+        rounds([&](int b) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (is_near(k[i])) {
+              sh.near_i[atomicAdd(&sh.count, 1u)] = b + i;
+              key32[b + i] = kAbsent;
+            } else if (is_score(k[i])) {
+              key32[b + i] = value32(k[i]) > top ? kTaken : kAbsent;
+            }
           }
-        }
+        });
         __syncthreads();
         for (uint32_t i = warp; i < near; i += kSelWarps) {
           const uint4 w = bound_load(run, bound_at(p, run, g, sh.near_i[i]), lane);
@@ -389,28 +430,28 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
         }
         __syncthreads();
         if (tid < (int)near) {
-          const uint64_t k = sh.near_k[tid];
+          const uint64_t mine = sh.near_k[tid];
           const int b = sh.near_i[tid];
           uint32_t before = 0;
           for (uint32_t i = 0; i < near; ++i)
-            before += sh.near_k[i] > k || (sh.near_k[i] == k && sh.near_i[i] < b);
+            before += sh.near_k[i] > mine || (sh.near_k[i] == mine && sh.near_i[i] < b);
           if (before < need) key32[b] = kTaken;
         }
       } else {
         // many (equal blocks, scores that are no numbers): the need-th largest of
         // their exact keys, 8 bits at a time
         for (int b = warp; b < n; b += kSelWarps) {
-          const uint32_t k = key32[b];
-          const bool mine = is_near(k);
-          uint64_t x = 0;                // 0 marks a block that is not near
+          const uint32_t x = key32[b];
+          const bool mine = is_near(x);
+          uint64_t exact = 0;            // 0 marks a block that is not near
           if (mine) {
             const uint4 w = bound_load(run, bound_at(p, run, g, b), lane);
-            x = max(order64(score64(sh, w, lane)), (uint64_t)1);
+            exact = max(order64(score64(sh, w, lane)), (uint64_t)1);
           }
           __syncwarp();
           if (lane == 0) {
-            key64[b] = x;
-            if (!mine && is_score(k)) key32[b] = value32(k) > top ? kTaken : kAbsent;
+            key64[b] = exact;
+            if (!mine && is_score(x)) key32[b] = value32(x) > top ? kTaken : kAbsent;
           }
         }
         uint64_t prefix64 = 0;
@@ -420,9 +461,9 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
           sh.hist[tid] = 0;
           __syncthreads();
           for (int b = tid; b < n; b += kSelThreads) {
-            const uint64_t k = key64[b];
-            if (k && (shift64 == 56 || (k >> (shift64 + 8)) == (prefix64 >> (shift64 + 8))))
-              atomicAdd(&sh.hist[(k >> shift64) & 255], 1u);
+            const uint64_t x = key64[b];
+            if (x && (shift64 == 56 || (x >> (shift64 + 8)) == (prefix64 >> (shift64 + 8))))
+              atomicAdd(&sh.hist[(x >> shift64) & 255], 1u);
           }
           __syncthreads();
           const uint32_t c = sh.hist[255 - tid];
@@ -440,28 +481,32 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
         uint32_t seen = 0;
         for (int b0 = 0; b0 < n; b0 += kSelThreads) {
           const int b = b0 + tid;
-          const uint64_t k = b < n ? key64[b] : 0;
+          const uint64_t x = b < n ? key64[b] : 0;
           uint32_t sum;
-          const uint32_t before = seen + sel_prefix(k == prefix64, sh.warp_s, sum);
-          if (k) key32[b] = k > prefix64 || (k == prefix64 && before < left) ? kTaken : kAbsent;
+          const uint32_t before = seen + sel_prefix(x == prefix64, sh.warp_s, sum);
+          if (x) key32[b] = x > prefix64 || (x == prefix64 && before < left) ? kTaken : kAbsent;
           seen += sum;
         }
       }
-      in_from = kTaken;                  // the keys say it all now
+      __syncthreads();
+      loaded = false;                    // the keys say it all now
+      in_from = kTaken;
     }
   }
-  // ---- the chosen blocks, ascending: a thread takes consecutive ones.  (Every key
-  // but kAbsent is at least 1.)
+  // ---- the chosen blocks, ascending.  (Every key but kAbsent is at least 1.)
   in_from = max(in_from, 1u);
-  __syncthreads();
-  const int per = (n + kSelThreads - 1) / kSelThreads;
-  const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
-  uint32_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += key32[b] >= in_from;
-  uint32_t total, at = sel_prefix(mine, sh.warp_s, total);
-  for (int b = b0; b < b1; ++b)
-    if (key32[b] >= in_from) out[at++] = b;
-  for (uint32_t i = total + tid; i < (uint32_t)p.nsel; i += kSelThreads) out[i] = -1;
+  uint32_t filled = 0;
+  rounds([&](int b) {
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mine += k[i] >= in_from;
+    uint32_t total, at = filled + sel_prefix(mine, sh.warp_s, total);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k[i] >= in_from) out[at++] = b + i;
+    filled += total;
+  });
+  for (uint32_t i = filled + tid; i < (uint32_t)p.nsel; i += kSelThreads) out[i] = -1;
 }
 
 // R: rows of a cluster at most.  The grid: clusters of p.cluster CTAs, one for
@@ -500,22 +545,29 @@ __global__ void __launch_bounds__(kSelThreads, R == 1 ? 4 : 2)
       }
     }
   } else {
-    // ---- the query heads' negative (lanes 0-15) and positive parts, summed
+    // ---- the query heads' negative parts (threads 0-127) and positive ones,
+    // summed a head dim a thread
+    static_assert(kSelThreads == 256, "a thread a sum");
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) qf[r][i] = 0.f;
-      if (r >= rows) continue;
-      const uint4* qp = reinterpret_cast<const uint4*>(
-          p.q + ((size_t)(row0 + r) * p.hq + (size_t)g * p.group) * kHeadDim) + (lane & 15);
-#pragma unroll 4
+      if (r >= rows) break;
+      const __nv_bfloat16* qp =
+          p.q + ((size_t)(row0 + r) * p.hq + (size_t)g * p.group) * kHeadDim + (tid & 127);
+      float s = 0.f;
+#pragma unroll 8
       for (int h = 0; h < p.group; ++h) {
-        float x[8];
-        unpack8(__ldg(qp + h * 16), x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          qf[r][i] += lane < 16 ? (x[i] > 0.f ? 0.f : x[i]) : (x[i] < 0.f ? 0.f : x[i]);
+        const float x = __bfloat162float(qp[(size_t)h * kHeadDim]);
+        s += tid < 128 ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x);
       }
+      sh.q32[r][tid] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float4 u = *reinterpret_cast<const float4*>(&sh.q32[r < rows ? r : 0][lane * 8]);
+      const float4 v = *reinterpret_cast<const float4*>(&sh.q32[r < rows ? r : 0][lane * 8 + 4]);
+      qf[r][0] = u.x; qf[r][1] = u.y; qf[r][2] = u.z; qf[r][3] = u.w;
+      qf[r][4] = v.x; qf[r][5] = v.y; qf[r][6] = v.z; qf[r][7] = v.w;
     }
     // ---- this CTA's blocks, eight a warp and step
     const int chunk = ((n + nc - 1) / nc + 7) & ~7;

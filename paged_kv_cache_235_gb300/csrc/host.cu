@@ -1901,6 +1901,7 @@ int select_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const t
       p.runs[i].group0 = p.groups;
       p.groups += (p.runs[i].nrows + p.rows_per - 1) / p.rows_per;
     }
+    p.cap = (p.cap + 7) & ~7;           // whole eights of keys
     p.cluster = p.rows_per;
     while (p.cluster < 8 && (int64_t)p.groups * c->hkv * p.cluster * 2 <= 4 * nsm &&
            p.cap / (p.cluster * 2) >= 64)
