@@ -1,11 +1,14 @@
 // Attention of each row over its own blocks of keys (tfpa_decode_blocks).
 //
 // A work item is a row, a kv head and up to 8 or 16 of its query heads; its
-// list of blocks is cut into equal parts, one CTA each, and the item's CTAs are
-// a cluster: their parts' states (running maximum, sum, unnormalised output)
+// list of blocks is cut into up to eight equal parts.  The item's CTAs are a
+// cluster, and their parts' states (running maximum, sum, unnormalised output)
 // meet in distributed shared memory, so there is one launch, no scratch and no
-// merge kernel.  The parts follow from the list's length alone, so a row's bytes
-// do not depend on its batch.
+// merge kernel.  The parts follow from the list's length alone and each has a
+// state of its own, so a row's bytes do not depend on its batch; how many of them
+// a CTA takes, one after the other, does (a CTA of few keys is mostly start and
+// end: 32 rows' lists of 2,048 keys over 4 bits 41 us with a part each, 25 us
+// with four).
 // Per CTA:
 //   warp 4      producer: a lane a list entry looks the entry and its page up
 //               (the chain of two loads runs once a 32 entries), then blocks
@@ -31,7 +34,7 @@ namespace {
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
-constexpr int kRow = kHeadDim + 4;          // a state's row: the four columns' in banks of their own
+constexpr int kRow = kHeadDim + 4;   // floats of a state's row: columns in banks of their own
 
 template <int KV>
 struct Cfg {
@@ -49,10 +52,10 @@ struct Cfg {
 
 struct Shared {
   uint64_t full[8], empty[8];
-  int key0[8];                 // first key of a stage; -1: the list's end
+  int key0[8];                 // first key of a stage; -1: a part's end
   int lost;                    // a wait gave up
   float m[kConsumers][16], l[kConsumers][16];
-  float part_m[16], part_l[16];   // the CTA's part, read by the cluster
+  float part_m[8][16], part_l[8][16];   // the CTA's parts, read by the cluster
 };
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
@@ -85,7 +88,8 @@ __device__ __forceinline__ void load_k(uint32_t sb, int row, int c, uint32_t (&k
   if (KV == kKvBf16) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 w = lds128(swz128(sb + (i >> 1) * (Cfg<KV>::kHalfStage / 2), row, 2 * c + (i & 1)));
+      const uint32_t at = sb + (i >> 1) * (Cfg<KV>::kHalfStage / 2);
+      const uint4 w = lds128(swz128(at, row, 2 * c + (i & 1)));
       k[4 * i] = w.x;
       k[4 * i + 1] = w.y;
       k[4 * i + 2] = w.z;
@@ -194,7 +198,8 @@ __device__ __forceinline__ void add_pv(uint32_t sb, int r0, int lane, const uint
       ldmatrix_x4_trans(w, swz128(sb, row, t + (lane >> 4)));
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t x = prmt(w[2 * u] & keep0, 0, 0x3120), y = prmt(w[2 * u + 1] & keep1, 0, 0x3120);
+        const uint32_t x = prmt(w[2 * u] & keep0, 0, 0x3120);
+        const uint32_t y = prmt(w[2 * u + 1] & keep1, 0, 0x3120);
         const uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)(x & 0xFFFF)),
                                e4m3x2_to_f16x2((uint16_t)(x >> 16)),
                                e4m3x2_to_f16x2((uint16_t)(y & 0xFFFF)),
@@ -234,15 +239,15 @@ __device__ __forceinline__ void add_pv(uint32_t sb, int r0, int lane, const uint
   }
 }
 
-// The producer warp: units [u0, u1) of the list, 64 keys each (a block of `per`
-// units an entry).  False if a wait gave up.
+// The producer warp: a part, units [u0, u1) of the list, 64 keys each (a block of
+// `per` units an entry), and its end.  False if a wait gave up.
 template <int KV>
 __device__ bool produce(const BlocksParams& p, const BlocksRun& run, const int32_t* list, int u0,
-                        int u1, int per, int pos, int g, uint8_t* ring, Shared& sh) {
+                        int u1, int per, int pos, int g, uint8_t* ring, Shared& sh,
+                        uint32_t& stage) {
   using C = Cfg<KV>;
   const int lane = threadIdx.x & 31;
   const int i1 = (u1 + per - 1) / per;
-  uint32_t stage = 0;
   for (int base = u0 / per; base < i1; base += 32) {
     // a lane an entry: the block, and the storage row of its first key
     int b = -1, row0 = 0;
@@ -307,6 +312,7 @@ __device__ bool produce(const BlocksParams& p, const BlocksRun& run, const int32
     sh.key0[buf] = -1;
     mbar_arrive(&sh.full[buf]);
   }
+  ++stage;
   return true;
 }
 
@@ -331,9 +337,9 @@ __global__ void __launch_bounds__(kThreads)
   allow_next_grid();
   __syncthreads();
   wait_prior_grid();
-  // ---- the item, and this CTA's part of its list
-  const int part = blockIdx.x % p.parts;
-  int item = blockIdx.x / p.parts;
+  // ---- the item, and this CTA's parts of its list
+  const int cta = blockIdx.x % p.ctas;
+  int item = blockIdx.x / p.ctas;
   const int qtiles = (p.group + kVecs - 1) / kVecs;
   const int qt = item % qtiles;
   item /= qtiles;
@@ -342,17 +348,26 @@ __global__ void __launch_bounds__(kThreads)
   while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
   const BlocksRun& run = p.runs[ri];
   const int pos = run.pos0 + (row - run.row0);
-  const int32_t* list = p.blocks + ((size_t)row * p.hkv + g) * p.nsel;
-  const int per = p.block / 64;
-  const int u0 = (int)((int64_t)p.nsel * per * part / p.parts);
-  const int u1 = (int)((int64_t)p.nsel * per * (part + 1) / p.parts);
+  const int part0 = cta * p.cta_parts, nparts = min(p.cta_parts, p.parts - part0);
+  // the warps' states, [warp][vector][dim], then the parts': in the ring where its
+  // last load has left before the first of them is written, else behind it
+  float* fold = reinterpret_cast<float*>(ring + (p.cta_parts > 1 ? C::kRing : 0));
+  float* mine = fold + kConsumers * kVecs * kRow;
   const int vecs = min(kVecs, p.group - qt * kVecs);     // query vectors of this item
   const size_t head0 = (size_t)row * p.hq + (size_t)g * p.group + qt * kVecs;
 
   const int gq = lane >> 2, c = lane & 3;
   float o[NT][8][4], m[NT][2], l[NT][2];
   if (warp == kConsumers) {
-    if (!produce<KV>(p, run, list, u0, u1, per, pos, g, ring, sh)) sh.lost = 1;
+    const int32_t* list = p.blocks + ((size_t)row * p.hkv + g) * p.nsel;
+    const int per = p.block / 64;
+    const int64_t units = (int64_t)p.nsel * per;
+    uint32_t stage = 0;
+    bool ok = true;
+    for (int i = part0; ok && i < part0 + nparts; ++i)
+      ok = produce<KV>(p, run, list, (int)(units * i / p.parts), (int)(units * (i + 1) / p.parts),
+                       per, pos, g, ring, sh, stage);
+    if (!ok) sh.lost = 1;
   } else {
     uint32_t q[NT][16];
     float sc[NT][2];
@@ -365,169 +380,177 @@ __global__ void __launch_bounds__(kThreads)
       // the factors of the vectors in this lane's columns, 2c and 2c + 1
       sc[n][0] = __shfl_sync(0xffffffffu, f, 8 * c);
       sc[n][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
-      m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-      for (int t = 0; t < 8; ++t) o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.f;
     }
     const int r0 = 16 * (warp % C::kStageWarps);
     // Every warp passes every stage, also those that are the other group's: the
     // parity of a phase tells it from the next one only, so a warp must not be
     // two loads of a stage ahead of what it has seen.
-    for (uint32_t stage = 0;; ++stage) {
-      const int buf = stage % C::kStages;
-      if (!warp_wait(&sh.full[buf], (stage / C::kStages) & 1, p.err_flag)) {
-        sh.lost = 1;
-        break;
+    uint32_t stage = 0;
+    bool live = true;                      // no wait of this warp has given up
+    for (int slot = 0; slot < nparts; ++slot) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.f;
       }
-      const int first = sh.key0[buf];
-      if (first < 0) break;
-      const int key0 = first + r0;
-      if (stage % C::kGroups == (uint32_t)(warp / C::kStageWarps) && key0 <= pos) {
-        const uint32_t sk = smem_u32(ring + (size_t)buf * C::kStageBytes);
-        // ---- S^T = K Q^T: keys key_of(gq), key_of(gq + 8); vectors 2c, 2c + 1
-        float s[NT][4];
-        {
-          uint32_t ka[16], kb[16];
-          load_k<KV>(sk, r0 + key_of<KV>(gq), c, ka);
-          load_k<KV>(sk, r0 + key_of<KV>(gq + 8), c, kb);
+      // (counted from the part's own first stage, so that a warp's keys are the
+      // same in whatever CTA the part runs)
+      for (uint32_t turn = 0; live; ++stage, ++turn) {
+        const int buf = stage % C::kStages;
+        live = warp_wait(&sh.full[buf], (stage / C::kStages) & 1, p.err_flag);
+        if (!live) break;
+        const int first = sh.key0[buf];
+        if (first < 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.empty[buf]);
+          ++stage;
+          break;
+        }
+        const int key0 = first + r0;
+        if (turn % C::kGroups == (uint32_t)(warp / C::kStageWarps) && key0 <= pos) {
+          const uint32_t sk = smem_u32(ring + (size_t)buf * C::kStageBytes);
+          // ---- S^T = K Q^T: keys key_of(gq), key_of(gq + 8); vectors 2c, 2c + 1
+          float s[NT][4];
+          {
+            uint32_t ka[16], kb[16];
+            load_k<KV>(sk, r0 + key_of<KV>(gq), c, ka);
+            load_k<KV>(sk, r0 + key_of<KV>(gq + 8), c, kb);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t a[4] = {ka[2 * ks], kb[2 * ks], ka[2 * ks + 1], kb[2 * ks + 1]};
+            for (int ks = 0; ks < 8; ++ks) {
+              const uint32_t a[4] = {ka[2 * ks], kb[2 * ks], ka[2 * ks + 1], kb[2 * ks + 1]};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if (C::kF16)
-                mma_f16_free(s[n], a, q[n][2 * ks], q[n][2 * ks + 1]);
-              else
-                mma_bf16(s[n], a, q[n][2 * ks], q[n][2 * ks + 1]);
+              for (int n = 0; n < NT; ++n) {
+                if (C::kF16)
+                  mma_f16_free(s[n], a, q[n][2 * ks], q[n][2 * ks + 1]);
+                else
+                  mma_bf16(s[n], a, q[n][2 * ks], q[n][2 * ks + 1]);
+              }
             }
           }
-        }
-        const bool see0 = key0 + key_of<KV>(gq) <= pos, see1 = key0 + key_of<KV>(gq + 8) <= pos;
-        // ---- online softmax over the tile's keys, a column a vector
-        uint32_t pb[NT][2];
-        bool resc = false;
-        float al[NT][2];
+          const bool see0 = key0 + key_of<KV>(gq) <= pos, see1 = key0 + key_of<KV>(gq + 8) <= pos;
+          // ---- online softmax over the tile's keys, a column a vector
+          uint32_t pb[NT][2];
+          bool resc = false;
+          float al[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+          for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            s[n][e] = see0 ? s[n][e] * sc[n][e] : -INFINITY;
-            s[n][2 + e] = see1 ? s[n][2 + e] * sc[n][e] : -INFINITY;
-            float mx = fmaxf(s[n][e], s[n][2 + e]);
+            for (int e = 0; e < 2; ++e) {
+              s[n][e] = see0 ? s[n][e] * sc[n][e] : -INFINITY;
+              s[n][2 + e] = see1 ? s[n][2 + e] * sc[n][e] : -INFINITY;
+              float mx = fmaxf(s[n][e], s[n][2 + e]);
 #pragma unroll
-            for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            al[n][e] = 1.f;
-            if (mx > m[n][e] + kRescaleThreshold) {      // the maximum moves by 2^8 at least
-              al[n][e] = fast_exp2(m[n][e] - mx);
-              l[n][e] *= al[n][e];
-              m[n][e] = mx;
-              resc = true;
+              for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+              al[n][e] = 1.f;
+              if (mx > m[n][e] + kRescaleThreshold) {      // the maximum moves by 2^8 at least
+                al[n][e] = fast_exp2(m[n][e] - mx);
+                l[n][e] *= al[n][e];
+                m[n][e] = mx;
+                resc = true;
+              }
+              const float base = m[n][e] == -INFINITY ? 0.f : m[n][e];
+              s[n][e] = fast_exp2(s[n][e] - base);
+              s[n][2 + e] = fast_exp2(s[n][2 + e] - base);
+              l[n][e] += s[n][e] + s[n][2 + e];
             }
-            const float base = m[n][e] == -INFINITY ? 0.f : m[n][e];
-            s[n][e] = fast_exp2(s[n][e] - base);
-            s[n][2 + e] = fast_exp2(s[n][2 + e] - base);
-            l[n][e] += s[n][e] + s[n][2 + e];
+            // weights rounded to the operands' 16 bits; the sums are not
+            pb[n][0] = transpose8x8(C::kF16 ? pack_f16x2(s[n][0], s[n][1])
+                                            : pack_bf16x2(s[n][0], s[n][1]));
+            pb[n][1] = transpose8x8(C::kF16 ? pack_f16x2(s[n][2], s[n][3])
+                                            : pack_bf16x2(s[n][2], s[n][3]));
           }
-          // weights rounded to the operands' 16 bits; the sums are not
-          const uint32_t w0 = C::kF16 ? pack_f16x2(s[n][0], s[n][1]) : pack_bf16x2(s[n][0], s[n][1]);
-          const uint32_t w1 = C::kF16 ? pack_f16x2(s[n][2], s[n][3]) : pack_bf16x2(s[n][2], s[n][3]);
-          pb[n][0] = transpose8x8(w0);
-          pb[n][1] = transpose8x8(w1);
+          if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[n][t][j] *= al[n][j & 1];
+          }
+          // ---- O^T += V^T P^T
+          auto mask = [&](int i) {
+            return (key0 + key_of<KV>(2 * c + i) <= pos ? 0xFFFFu : 0u) |
+                   (key0 + key_of<KV>(2 * c + 1 + i) <= pos ? 0xFFFF0000u : 0u);
+          };
+          add_pv<KV, NT>(sk + C::kHalfStage, r0, lane, pb, mask(0), mask(8), o);
         }
-        if (__any_sync(0xffffffffu, resc)) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) o[n][t][j] *= al[n][j & 1];
-        }
-        // ---- O^T += V^T P^T
-        auto mask = [&](int i) {
-          return (key0 + key_of<KV>(2 * c + i) <= pos ? 0xFFFFu : 0u) |
-                 (key0 + key_of<KV>(2 * c + 1 + i) <= pos ? 0xFFFF0000u : 0u);
-        };
-        add_pv<KV, NT>(sk + C::kHalfStage, r0, lane, pb, mask(0), mask(8), o);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[buf]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.empty[buf]);
+      // ---- the part's state: the warps', folded.  (A warp that gave up comes here
+      // too: the barriers count on all four.)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+      named_bar_sync(1, 32 * kConsumers);    // the last part's fold, or the ring, is read
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (gq == 0) {
+            sh.m[warp][8 * n + 2 * c + e] = m[n][e];
+            sh.l[warp][8 * n + 2 * c + e] = l[n][e];
+          }
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            fold[(warp * kVecs + 8 * n + 2 * c + (j & 1)) * kRow +
+                 dim_of<KV>(t, gq + 8 * (j >> 1))] = o[n][t][j];
+      }
+      named_bar_sync(1, 32 * kConsumers);
+      for (int i = tid; i < vecs * (kHeadDim / 4); i += 32 * kConsumers) {
+        const int v = i / (kHeadDim / 4), d = i % (kHeadDim / 4) * 4;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, sh.m[w][v]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) {
+          const float a = sh.m[w][v] == -INFINITY ? 0.f : fast_exp2(sh.m[w][v] - M);
+          const float4 x = *reinterpret_cast<const float4*>(fold + (w * kVecs + v) * kRow + d);
+          L = fmaf(a, sh.l[w][v], L);
+          acc.x = fmaf(a, x.x, acc.x);
+          acc.y = fmaf(a, x.y, acc.y);
+          acc.z = fmaf(a, x.z, acc.z);
+          acc.w = fmaf(a, x.w, acc.w);
+        }
+        *reinterpret_cast<float4*>(mine + (slot * kVecs + v) * kRow + d) = acc;
+        if (d == 0) {
+          sh.part_m[slot][v] = M;
+          sh.part_l[slot][v] = L;
+        }
+      }
     }
-    // ---- this warp's state
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int d = 4; d < 32; d *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
-        if (gq == 0) {
-          sh.m[warp][8 * n + 2 * c + e] = m[n][e];
-          sh.l[warp][8 * n + 2 * c + e] = l[n][e];
-        }
-      }
+    if (!live) sh.lost = 1;
   }
   __syncthreads();
   if (sh.lost) let_copies_land();
-  // ---- the warps' states, folded: [warp][vector][dim] in the ring, which every
-  // load has left, then [vector][dim] behind them
-  float* fold = reinterpret_cast<float*>(ring);
-  float* mine = fold + kConsumers * kVecs * kRow;
-  if (warp < kConsumers) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          fold[(warp * kVecs + 8 * n + 2 * c + (j & 1)) * kRow +
-               dim_of<KV>(t, gq + 8 * (j >> 1))] = o[n][t][j];
-  }
-  __syncthreads();
-  for (int i = tid; i < vecs * (kHeadDim / 4); i += kThreads) {
-    const int v = i / (kHeadDim / 4), d = i % (kHeadDim / 4) * 4;
-    float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, sh.m[w][v]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kConsumers; ++w) {
-      const float a = sh.m[w][v] == -INFINITY ? 0.f : fast_exp2(sh.m[w][v] - M);
-      const float4 x = *reinterpret_cast<const float4*>(fold + (w * kVecs + v) * kRow + d);
-      L = fmaf(a, sh.l[w][v], L);
-      acc.x = fmaf(a, x.x, acc.x);
-      acc.y = fmaf(a, x.y, acc.y);
-      acc.z = fmaf(a, x.z, acc.z);
-      acc.w = fmaf(a, x.w, acc.w);
-    }
-    *reinterpret_cast<float4*>(mine + v * kRow + d) = acc;
-    if (d == 0) {
-      sh.part_m[v] = M;
-      sh.part_l[v] = L;
-    }
-  }
   // ---- the parts, in the cluster's shared memory: each CTA finishes its share
   // of the item's elements
   const float vs = C::kF16 ? __ldg(p.v_scale + g) : 1.f;
   __syncwarp();
-  if (p.parts > 1)
-    cluster_sync();
-  else
-    __syncthreads();
+  if (p.ctas > 1) cluster_sync();
   // eight lanes an element of four dims, a part each: one trip to the other CTAs
-  const int j = lane & 7;
-  const int per_cta = (vecs * (kHeadDim / 4) + p.parts - 1) / p.parts;
-  const int e1 = min(vecs * (kHeadDim / 4), (part + 1) * per_cta);
-  for (int e0 = part * per_cta + (warp * 32 + lane) / 8; e0 - (lane >> 3) < e1;
+  const int j = lane & 7, jc = j / p.cta_parts, js = j - jc * p.cta_parts;
+  const int share = (vecs * (kHeadDim / 4) + p.ctas - 1) / p.ctas;
+  const int e1 = min(vecs * (kHeadDim / 4), (cta + 1) * share);
+  for (int e0 = cta * share + (warp * 32 + lane) / 8; e0 - (lane >> 3) < e1;
        e0 += kThreads / 8) {
     const int e = min(e0, e1 - 1), v = e / (kHeadDim / 4), d = e % (kHeadDim / 4) * 4;
     float mj = -INFINITY, lj = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (j < p.parts) {
-      mj = __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.part_m[v]), j)));
-      lj = __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.part_l[v]), j)));
-      x = ld_cluster_f4(mapa_shared(smem_u32(mine + v * kRow + d), j));
+      mj = __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.part_m[js][v]), jc)));
+      lj = __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.part_l[js][v]), jc)));
+      x = ld_cluster_f4(mapa_shared(smem_u32(mine + (js * kVecs + v) * kRow + d), jc));
     }
     float M = mj;
 #pragma unroll
@@ -556,23 +579,31 @@ __global__ void __launch_bounds__(kThreads)
       p.lse[head0 + v] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
   }
   __syncwarp();
-  if (p.parts > 1) cluster_sync();                   // read, before a CTA's memory goes
+  if (p.ctas > 1) cluster_sync();                    // read, before a CTA's memory goes
+}
+
+// Shared memory of a CTA that takes `parts` parts.
+template <int KV, int NT>
+constexpr int smem_of(int parts) {
+  constexpr int kState = 8 * NT * kRow * 4;
+  return Cfg<KV>::kRing + 1024 + (parts > 1 ? (kConsumers + parts) * kState : 0);
 }
 
 template <int KV, int NT>
 cudaError_t launch(const BlocksParams& p, cudaStream_t s) {
-  constexpr int kSmem = Cfg<KV>::kRing + 1024;
   static_assert((kConsumers + 1) * 8 * NT * kRow * 4 <= Cfg<KV>::kRing, "fold buffers");
+  static_assert(smem_of<KV, NT>(8) + sizeof(Shared) <= 232448, "shared memory");
   static PerDeviceOnce configured;
   const cudaError_t e = configured.run([] {
     return cudaFuncSetAttribute(decode_blocks_kernel<KV, NT>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                smem_of<KV, NT>(8));
   });
   if (e != cudaSuccess) return e;
   const int qtiles = (p.group + 8 * NT - 1) / (8 * NT);
-  const dim3 grid(p.rows * p.hkv * qtiles * p.parts);
-  return launch_pdl_cluster(decode_blocks_kernel<KV, NT>, grid, dim3(kThreads), kSmem, s, p,
-                            p.parts);
+  const dim3 grid(p.rows * p.hkv * qtiles * p.ctas);
+  return launch_pdl_cluster(decode_blocks_kernel<KV, NT>, grid, dim3(kThreads),
+                            smem_of<KV, NT>(p.cta_parts), s, p, p.ctas);
 }
 
 template <int KV>

@@ -257,7 +257,8 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
     loaded = true;
   };
   // ---- how many are free to choose from, and their range
-  uint32_t counts = 0, kmin = 0xFFFFFFFFu, kmax = 0;     // counts: taken << 16 | free (18,432 at most)
+  uint32_t counts = 0;                   // taken << 16 | free (18,432 at most)
+  uint32_t kmin = 0xFFFFFFFFu, kmax = 0;
   rounds([&](int) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -546,21 +547,30 @@ __global__ void __launch_bounds__(kSelThreads, R == 1 ? 4 : 2)
     }
   } else {
     // ---- the query heads' negative parts (threads 0-127) and positive ones,
-    // summed a head dim a thread
+    // summed: a head dim a thread, four heads of all rows on their way at once
     static_assert(kSelThreads == 256, "a thread a sum");
+    float sum[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (r >= rows) break;
-      const __nv_bfloat16* qp =
-          p.q + ((size_t)(row0 + r) * p.hq + (size_t)g * p.group) * kHeadDim + (tid & 127);
-      float s = 0.f;
-#pragma unroll 8
-      for (int h = 0; h < p.group; ++h) {
-        const float x = __bfloat162float(qp[(size_t)h * kHeadDim]);
-        s += tid < 128 ? (x > 0.f ? 0.f : x) : (x < 0.f ? 0.f : x);
-      }
-      sh.q32[r][tid] = s;
+    for (int r = 0; r < R; ++r) sum[r] = 0.f;
+    const __nv_bfloat16* qp =
+        p.q + ((size_t)row0 * p.hq + (size_t)g * p.group) * kHeadDim + (tid & 127);
+    for (int h0 = 0; h0 < p.group; h0 += 4) {
+      float x[R][4];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          x[r][h] = r < rows && h0 + h < p.group
+                        ? __bfloat162float(qp[((size_t)r * p.hq + h0 + h) * kHeadDim])
+                        : 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          sum[r] += tid < 128 ? (x[r][h] > 0.f ? 0.f : x[r][h]) : (x[r][h] < 0.f ? 0.f : x[r][h]);
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r) sh.q32[r][tid] = sum[r];
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < R; ++r) {

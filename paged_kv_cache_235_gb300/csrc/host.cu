@@ -1895,7 +1895,8 @@ int select_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const t
     p.recent = recent;
     // Up to four rows of a run share the reads of the bounds; a cluster has a CTA
     // for each of them to choose in.  More CTAs while the GPU holds them (four a
-    // SM) and each has 64 blocks, eight a warp.
+    // SM, two with four rows, by their registers) and each has 64 blocks, eight a
+    // warp.
     p.rows_per = longest >= 3 ? 4 : longest;
     for (int i = 0; i < nr; ++i) {
       p.runs[i].group0 = p.groups;
@@ -1903,7 +1904,8 @@ int select_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const t
     }
     p.cap = (p.cap + 7) & ~7;           // whole eights of keys
     p.cluster = p.rows_per;
-    while (p.cluster < 8 && (int64_t)p.groups * c->hkv * p.cluster * 2 <= 4 * nsm &&
+    const int64_t at_once = (p.rows_per == 1 ? 4 : 2) * nsm;
+    while (p.cluster < 8 && (int64_t)p.groups * c->hkv * p.cluster * 2 <= at_once &&
            p.cap / (p.cluster * 2) >= 64)
       p.cluster *= 2;
     record(16, base, nrows, nr, p.groups * c->hkv, p.groups * c->hkv * p.cluster,
@@ -1914,11 +1916,23 @@ int select_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const t
   return TFPA_OK;
 }
 
-// CTAs that share a row's list: one for every 128 keys, up to a cluster of
-// eight.  A function of the list's length only, so a row's bytes do not depend on
-// its batch.
+// Parts of a row's list: one for every 128 keys, up to eight.  A function of the
+// list's length only, so a row's bytes do not depend on its batch.
 int32_t block_parts(int32_t block, int32_t nsel) {
   return (int32_t)std::min<int64_t>(8, ((int64_t)nsel * (block / 64) + 1) / 2);
+}
+
+// Parts that a CTA takes one after the other: as few as let all of the launch's
+// CTAs run at once (four a SM with one part, three with two, two with more, whose
+// states take shared memory).
+int32_t cta_parts(int64_t items, int32_t parts, bool wide, int nsm) {
+  int32_t k = 1;
+  for (; k < parts; k *= 2) {
+    const int64_t ctas = items * ((parts + k - 1) / k);
+    const int at_once = wide ? 2 : k == 1 ? 4 : k == 2 ? 3 : 2;
+    if (ctas <= (int64_t)nsm * at_once) break;
+  }
+  return std::min(k, parts);
 }
 
 constexpr int32_t kMaxListed = 1 << 24;   // entries of a list, at most
@@ -1943,6 +1957,8 @@ int blocks_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
   if ((int64_t)rows * c->hkv * qtiles * parts > INT32_MAX) return TFPA_EINVAL;
   if (rows == 0) return TFPA_OK;
   if ((e = check_device())) return e;
+  const int nsm = sm_count();
+  if (nsm < 1) return TFPA_ECUDA;
   thread_local BlocksParams p;
   size_t ri = 0;
   while (ri < runs.size()) {
@@ -1991,7 +2007,9 @@ int blocks_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
       if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, fp8 ? 64 : 32, p.maps, nsrc))) return e;
     }
     const int32_t items = (int32_t)(nrows * c->hkv * qtiles);
-    record(17, base, nrows, nr, items, items * parts, base * hd, base * hd);
+    p.cta_parts = cta_parts(items, parts, G > 8, nsm);
+    p.ctas = (parts + p.cta_parts - 1) / p.cta_parts;
+    record(17, base, nrows, nr, items, items * p.ctas, base * hd, base * hd);
     if (!dry_run())
       if ((e = to_err(launch_decode_blocks(p, c->dtype, stream)))) return e;
   }

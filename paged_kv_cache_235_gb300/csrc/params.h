@@ -433,7 +433,9 @@ struct BlocksParams {
   int32_t num_pages;
   int32_t block;
   int32_t nsel;
-  int32_t parts;              // CTAs (a cluster) of a row, kv head and query tile
+  int32_t parts;              // of a list, each with a state of its own
+  int32_t cta_parts;          // that a CTA takes
+  int32_t ctas;               // (a cluster) of a row, kv head and query tile
   float scale_log2;
 };
 
