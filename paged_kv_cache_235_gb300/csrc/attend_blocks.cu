@@ -54,8 +54,7 @@ struct Shared {
   uint64_t full[8], empty[8];
   int key0[8];                 // first key of a stage; -1: a part's end
   int lost;                    // a wait gave up
-  float m[kConsumers][16], l[kConsumers][16];
-  float part_m[8][16], part_l[8][16];   // the CTA's parts, read by the cluster
+  float m[16], l[16];          // the CTA's state, read by the cluster (with the ring's start)
 };
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
@@ -239,6 +238,58 @@ __device__ __forceinline__ void add_pv(uint32_t sb, int r0, int lane, const uint
   }
 }
 
+// Two states' common maximum goes into m; the factor that this one's sums take.
+__device__ __forceinline__ float toward(float& m, float other) {
+  const float M = fmaxf(m, other);
+  const float a = m == -INFINITY ? 0.f : fast_exp2(m - M);
+  m = M;
+  return a;
+}
+
+// A warp's state in shared memory, [float4 of its fragments][lane], its maxima and
+// sums behind them.
+template <int NT>
+constexpr int kStateBytes = (8 * NT + NT) * 32 * 16;
+template <int NT>
+__device__ __forceinline__ void put_state(float4* to, int lane, const float (&o)[NT][8][4],
+                                          const float (&m)[NT][2], const float (&l)[NT][2]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      to[(8 * n + t) * 32 + lane] = make_float4(o[n][t][0], o[n][t][1], o[n][t][2], o[n][t][3]);
+    to[(8 * NT + n) * 32 + lane] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
+  }
+}
+// The state there and this one, in this one.  (Products and sums rounded on their
+// own: the result is the same whichever of the two is there.)
+template <int NT>
+__device__ __forceinline__ void take_state(const float4* from, int lane, float (&o)[NT][8][4],
+                                           float (&m)[NT][2], float (&l)[NT][2]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const float4 ml = from[(8 * NT + n) * 32 + lane];
+    float om[2] = {ml.x, ml.y};
+    const float ol[2] = {ml.z, ml.w};
+    float a[2], b[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float was = m[n][e];
+      a[e] = toward(m[n][e], om[e]);
+      b[e] = toward(om[e], was);
+      l[n][e] = __fadd_rn(__fmul_rn(l[n][e], a[e]), __fmul_rn(ol[e], b[e]));
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const float4 x = from[(8 * n + t) * 32 + lane];
+      const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[n][t][j] = __fadd_rn(__fmul_rn(o[n][t][j], a[j & 1]), __fmul_rn(y[j], b[j & 1]));
+    }
+  }
+}
+
 // The producer warp: a part, units [u0, u1) of the list, 64 keys each (a block of
 // `per` units an entry), and its end.  False if a wait gave up.
 template <int KV>
@@ -316,8 +367,9 @@ __device__ bool produce(const BlocksParams& p, const BlocksRun& run, const int32
   return true;
 }
 
-template <int KV, int NT>
-__global__ void __launch_bounds__(kThreads)
+// ONE: a CTA has one part (its code apart from the other keeps its registers).
+template <int KV, int NT, bool ONE>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
     decode_blocks_kernel(const __grid_constant__ BlocksParams p) {
   using C = Cfg<KV>;
   constexpr int kVecs = 8 * NT;
@@ -348,11 +400,11 @@ __global__ void __launch_bounds__(kThreads)
   while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
   const BlocksRun& run = p.runs[ri];
   const int pos = run.pos0 + (row - run.row0);
-  const int part0 = cta * p.cta_parts, nparts = min(p.cta_parts, p.parts - part0);
-  // the warps' states, [warp][vector][dim], then the parts': in the ring where its
-  // last load has left before the first of them is written, else behind it
-  float* fold = reinterpret_cast<float*>(ring + (p.cta_parts > 1 ? C::kRing : 0));
-  float* mine = fold + kConsumers * kVecs * kRow;
+  const int part0 = ONE ? cta : cta * p.cta_parts;
+  const int nparts = ONE ? 1 : min(p.cta_parts, p.parts - part0);
+  float4* pending = reinterpret_cast<float4*>(ring + C::kRing);   // [level][NT * 8 + NT][lane]
+  // the CTA's state, once the ring is done
+  float* mine = reinterpret_cast<float*>(ring + (ONE ? 4 * kStateBytes<NT> : 0));
   const int vecs = min(kVecs, p.group - qt * kVecs);     // query vectors of this item
   const size_t head0 = (size_t)row * p.hq + (size_t)g * p.group + qt * kVecs;
 
@@ -402,12 +454,7 @@ __global__ void __launch_bounds__(kThreads)
         live = warp_wait(&sh.full[buf], (stage / C::kStages) & 1, p.err_flag);
         if (!live) break;
         const int first = sh.key0[buf];
-        if (first < 0) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.empty[buf]);
-          ++stage;
-          break;
-        }
+        if (first < 0) break;              // (the marker's stage is the fold's until released)
         const int key0 = first + r0;
         if (turn % C::kGroups == (uint32_t)(warp / C::kStageWarps) && key0 <= pos) {
           const uint32_t sk = smem_u32(ring + (size_t)buf * C::kStageBytes);
@@ -481,93 +528,165 @@ __global__ void __launch_bounds__(kThreads)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[buf]);
       }
-      // ---- the part's state: the warps', folded.  (A warp that gave up comes here
-      // too: the barriers count on all four.)
+      // ---- the part's state: the warps' in pairs, (0, 2) and (1, 3), then the two.
+      // (A warp that gave up comes here too: the barriers count on all four.)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
-      named_bar_sync(1, 32 * kConsumers);    // the last part's fold, or the ring, is read
+      constexpr int kState = kStateBytes<NT> / 16;
+      if (ONE) {
+        // the only part: the whole ring is free, and all four warps fold
+        float4* all = reinterpret_cast<float4*>(ring);
+        named_bar_sync(1, 32 * kConsumers);
+        put_state<NT>(all + warp * kState, lane, o, m, l);
+        named_bar_sync(1, 32 * kConsumers);
+        break;
+      }
+      constexpr bool kInStage = C::kStageBytes >= 2 * kStateBytes<NT>;
+      float4* fold = reinterpret_cast<float4*>(
+          kInStage ? ring + (stage % C::kStages) * C::kStageBytes
+                   : ring + C::kRing + 3 * kStateBytes<NT>);
+      if (!kInStage) named_bar_sync(1, 32 * kConsumers);   // the last part's fold is read
+      if (warp >= 2) put_state<NT>(fold + (warp - 2) * (kStateBytes<NT> / 16), lane, o, m, l);
+      named_bar_sync(1, 32 * kConsumers);
+      if (warp < 2) {
+        take_state<NT>(fold + warp * (kStateBytes<NT> / 16), lane, o, m, l);
+        if (warp == 1) put_state<NT>(fold + kStateBytes<NT> / 16, lane, o, m, l);
+        named_bar_sync(2, 64);
+        if (warp == 0) {
+          take_state<NT>(fold + kStateBytes<NT> / 16, lane, o, m, l);
+          // and the parts' in pairs, pairs of pairs and so on, as the cluster goes on
+          // to do: the states of the levels that lack their second half wait
+          int level = 0;
+          for (; slot >> level & 1; ++level)
+            take_state<NT>(pending + level * (kStateBytes<NT> / 16), lane, o, m, l);
+          if (slot + 1 < nparts)
+            put_state<NT>(pending + level * (kStateBytes<NT> / 16), lane, o, m, l);
+          else
+            for (; slot >> level; ++level)
+              if (slot >> level & 1)
+                take_state<NT>(pending + level * (kStateBytes<NT> / 16), lane, o, m, l);
+        }
+      }
+      __syncwarp();
+      if (live && lane == 0) mbar_arrive(&sh.empty[stage % C::kStages]);
+      ++stage;
+    }
+    // ---- the CTA's state, [vector][dim], for the cluster
+    if (ONE) {
+      float4* all = reinterpret_cast<float4*>(ring);
+      constexpr int kState = kStateBytes<NT> / 16;
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) {
+        const int t = (i * kConsumers + warp) % 8, n = (i * kConsumers + warp) / 8;
+        // the pairs (0, 2) and (1, 3), then the two, as take_state adds them
+        float4 ml[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) ml[w] = all[w * kState + (8 * NT + n) * 32 + lane];
+        float f[4][2], h[2][2], mm[2], ll[2];   // factors of the pairs, and of the two
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float m4[4], l4[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            m4[w] = e ? ml[w].y : ml[w].x;
+            l4[w] = e ? ml[w].w : ml[w].z;
+          }
+          float ma = m4[0], mb = m4[1], m2 = m4[2], m3 = m4[3];
+          const float a0 = toward(ma, m4[2]), a2 = toward(m2, m4[0]);
+          const float b1 = toward(mb, m4[3]), b3 = toward(m3, m4[1]);
+          const float la = __fadd_rn(__fmul_rn(l4[0], a0), __fmul_rn(l4[2], a2));
+          const float lb = __fadd_rn(__fmul_rn(l4[1], b1), __fmul_rn(l4[3], b3));
+          float mt = ma, mu = mb;
+          h[0][e] = toward(mt, mb);
+          h[1][e] = toward(mu, ma);
+          mm[e] = mt;
+          ll[e] = __fadd_rn(__fmul_rn(la, h[0][e]), __fmul_rn(lb, h[1][e]));
+          f[0][e] = a0;
+          f[1][e] = b1;
+          f[2][e] = a2;
+          f[3][e] = b3;
+        }
+        float x[4][4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float4 y = all[w * kState + (8 * n + t) * 32 + lane];
+          x[w][0] = y.x;
+          x[w][1] = y.y;
+          x[w][2] = y.z;
+          x[w][3] = y.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int e = j & 1;
+          const float xa = __fadd_rn(__fmul_rn(x[0][j], f[0][e]), __fmul_rn(x[2][j], f[2][e]));
+          const float xb = __fadd_rn(__fmul_rn(x[1][j], f[1][e]), __fmul_rn(x[3][j], f[3][e]));
+          mine[(8 * n + 2 * c + e) * kRow + dim_of<KV>(t, gq + 8 * (j >> 1))] =
+              __fadd_rn(__fmul_rn(xa, h[0][e]), __fmul_rn(xb, h[1][e]));
+        }
+        if (t == 0 && gq == 0) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            sh.m[8 * n + 2 * c + e] = mm[e];
+            sh.l[8 * n + 2 * c + e] = ll[e];
+          }
+        }
+      }
+    } else if (warp == 0) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (gq == 0) {
-            sh.m[warp][8 * n + 2 * c + e] = m[n][e];
-            sh.l[warp][8 * n + 2 * c + e] = l[n][e];
-          }
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            fold[(warp * kVecs + 8 * n + 2 * c + (j & 1)) * kRow +
-                 dim_of<KV>(t, gq + 8 * (j >> 1))] = o[n][t][j];
-      }
-      named_bar_sync(1, 32 * kConsumers);
-      for (int i = tid; i < vecs * (kHeadDim / 4); i += 32 * kConsumers) {
-        const int v = i / (kHeadDim / 4), d = i % (kHeadDim / 4) * 4;
-        float M = -INFINITY, L = 0.f;
+            mine[(8 * n + 2 * c + (j & 1)) * kRow + dim_of<KV>(t, gq + 8 * (j >> 1))] = o[n][t][j];
 #pragma unroll
-        for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, sh.m[w][v]);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kConsumers; ++w) {
-          const float a = sh.m[w][v] == -INFINITY ? 0.f : fast_exp2(sh.m[w][v] - M);
-          const float4 x = *reinterpret_cast<const float4*>(fold + (w * kVecs + v) * kRow + d);
-          L = fmaf(a, sh.l[w][v], L);
-          acc.x = fmaf(a, x.x, acc.x);
-          acc.y = fmaf(a, x.y, acc.y);
-          acc.z = fmaf(a, x.z, acc.z);
-          acc.w = fmaf(a, x.w, acc.w);
-        }
-        *reinterpret_cast<float4*>(mine + (slot * kVecs + v) * kRow + d) = acc;
-        if (d == 0) {
-          sh.part_m[slot][v] = M;
-          sh.part_l[slot][v] = L;
-        }
+        for (int e = 0; e < 2; ++e)
+          if (gq == 0) {
+            sh.m[8 * n + 2 * c + e] = m[n][e];
+            sh.l[8 * n + 2 * c + e] = l[n][e];
+          }
       }
     }
     if (!live) sh.lost = 1;
   }
   __syncthreads();
   if (sh.lost) let_copies_land();
-  // ---- the parts, in the cluster's shared memory: each CTA finishes its share
-  // of the item's elements
+  // ---- the CTAs' states, in the cluster's shared memory: each CTA finishes its
+  // share of the item's elements, eight lanes one of four dims, a CTA each, so that
+  // there is one trip to the other CTAs; pairs first, like the parts
   const float vs = C::kF16 ? __ldg(p.v_scale + g) : 1.f;
   __syncwarp();
   if (p.ctas > 1) cluster_sync();
-  // eight lanes an element of four dims, a part each: one trip to the other CTAs
-  const int j = lane & 7, jc = j / p.cta_parts, js = j - jc * p.cta_parts;
+  const int j = lane & 7;
   const int share = (vecs * (kHeadDim / 4) + p.ctas - 1) / p.ctas;
   const int e1 = min(vecs * (kHeadDim / 4), (cta + 1) * share);
-  for (int e0 = cta * share + (warp * 32 + lane) / 8; e0 - (lane >> 3) < e1;
-       e0 += kThreads / 8) {
+  for (int e0 = cta * share + (warp * 32 + lane) / 8; e0 - (lane >> 3) < e1; e0 += kThreads / 8) {
     const int e = min(e0, e1 - 1), v = e / (kHeadDim / 4), d = e % (kHeadDim / 4) * 4;
-    float mj = -INFINITY, lj = 0.f;
+    float M = -INFINITY, L = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (j < p.parts) {
-      mj = __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.part_m[js][v]), jc)));
-      lj = __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.part_l[js][v]), jc)));
-      x = ld_cluster_f4(mapa_shared(smem_u32(mine + (js * kVecs + v) * kRow + d), jc));
+    if (j < p.ctas) {
+      M = __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.m[v]), j)));
+      L = __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.l[v]), j)));
+      x = ld_cluster_f4(mapa_shared(smem_u32(mine + v * kRow + d), j));
     }
-    float M = mj;
-#pragma unroll
-    for (int k = 1; k < 8; k *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
-    const float a = mj == -INFINITY ? 0.f : fast_exp2(mj - M);
-    float L = a * lj;
-    x.x *= a;
-    x.y *= a;
-    x.z *= a;
-    x.w *= a;
 #pragma unroll
     for (int k = 1; k < 8; k *= 2) {
-      L += __shfl_xor_sync(0xffffffffu, L, k);
-      x.x += __shfl_xor_sync(0xffffffffu, x.x, k);
-      x.y += __shfl_xor_sync(0xffffffffu, x.y, k);
-      x.z += __shfl_xor_sync(0xffffffffu, x.z, k);
-      x.w += __shfl_xor_sync(0xffffffffu, x.w, k);
+      const float a = toward(M, __shfl_xor_sync(0xffffffffu, M, k));
+      const bool there = ((j ^ k) & ~(k - 1)) < p.ctas;    // the other half has a CTA
+      auto both = [&](float y) {
+        y = __fmul_rn(y, a);
+        const float z = __shfl_xor_sync(0xffffffffu, y, k);
+        return there ? __fadd_rn(y, z) : y;
+      };
+      L = both(L);
+      x.x = both(x.x);
+      x.y = both(x.y);
+      x.z = both(x.z);
+      x.w = both(x.w);
     }
     if (j != 0 || e0 >= e1) continue;
     const float f = L == 0.f ? 0.f : vs / L;         // no key: zeros
@@ -582,33 +701,37 @@ __global__ void __launch_bounds__(kThreads)
   if (p.ctas > 1) cluster_sync();                    // read, before a CTA's memory goes
 }
 
-// Shared memory of a CTA that takes `parts` parts.
+// Shared memory of a CTA that takes `parts` parts: the ring, the states that wait
+// for their second half, and the fold's where a stage does not hold it.
 template <int KV, int NT>
 constexpr int smem_of(int parts) {
-  constexpr int kState = 8 * NT * kRow * 4;
-  return Cfg<KV>::kRing + 1024 + (parts > 1 ? (kConsumers + parts) * kState : 0);
+  const bool in_stage = Cfg<KV>::kStageBytes >= 2 * kStateBytes<NT>;
+  const int levels = parts > 4 ? 3 : parts > 2 ? 2 : parts > 1 ? 1 : 0;
+  return Cfg<KV>::kRing + 1024 + (parts == 1 ? 0 : in_stage ? levels : 5) * kStateBytes<NT>;
 }
 
-template <int KV, int NT>
+template <int KV, int NT, bool ONE>
 cudaError_t launch(const BlocksParams& p, cudaStream_t s) {
-  static_assert((kConsumers + 1) * 8 * NT * kRow * 4 <= Cfg<KV>::kRing, "fold buffers");
+  static_assert(4 * kStateBytes<NT> + 8 * NT * kRow * 4 <= Cfg<KV>::kRing, "the states' memory");
   static_assert(smem_of<KV, NT>(8) + sizeof(Shared) <= 232448, "shared memory");
   static PerDeviceOnce configured;
   const cudaError_t e = configured.run([] {
-    return cudaFuncSetAttribute(decode_blocks_kernel<KV, NT>,
+    return cudaFuncSetAttribute(decode_blocks_kernel<KV, NT, ONE>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem_of<KV, NT>(8));
+                                smem_of<KV, NT>(ONE ? 1 : 8));
   });
   if (e != cudaSuccess) return e;
   const int qtiles = (p.group + 8 * NT - 1) / (8 * NT);
   const dim3 grid(p.rows * p.hkv * qtiles * p.ctas);
-  return launch_pdl_cluster(decode_blocks_kernel<KV, NT>, grid, dim3(kThreads),
+  return launch_pdl_cluster(decode_blocks_kernel<KV, NT, ONE>, grid, dim3(kThreads),
                             smem_of<KV, NT>(p.cta_parts), s, p, p.ctas);
 }
 
 template <int KV>
 cudaError_t launch_of(const BlocksParams& p, cudaStream_t s) {
-  return p.group <= 8 ? launch<KV, 1>(p, s) : launch<KV, 2>(p, s);
+  if (p.group <= 8)
+    return p.cta_parts == 1 ? launch<KV, 1, true>(p, s) : launch<KV, 1, false>(p, s);
+  return p.cta_parts == 1 ? launch<KV, 2, true>(p, s) : launch<KV, 2, false>(p, s);
 }
 
 }  // namespace

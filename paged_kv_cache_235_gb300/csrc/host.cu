@@ -1922,16 +1922,12 @@ int32_t block_parts(int32_t block, int32_t nsel) {
   return (int32_t)std::min<int64_t>(8, ((int64_t)nsel * (block / 64) + 1) / 2);
 }
 
-// Parts that a CTA takes one after the other: as few as let all of the launch's
-// CTAs run at once (four a SM with one part, three with two, two with more, whose
-// states take shared memory).
-int32_t cta_parts(int64_t items, int32_t parts, bool wide, int nsm) {
+// Parts that a CTA takes one after the other: as few as let the launch have four
+// CTAs a SM at most (32 rows' lists of 2,048 keys over 4 bits, 256 items of eight
+// parts: a part each 34 us, two 27, four 24, eight 39).
+int32_t cta_parts(int64_t items, int32_t parts, int nsm) {
   int32_t k = 1;
-  for (; k < parts; k *= 2) {
-    const int64_t ctas = items * ((parts + k - 1) / k);
-    const int at_once = wide ? 2 : k == 1 ? 4 : k == 2 ? 3 : 2;
-    if (ctas <= (int64_t)nsm * at_once) break;
-  }
+  while (k < parts && items * ((parts + k - 1) / k) > 4 * (int64_t)nsm) k *= 2;
   return std::min(k, parts);
 }
 
@@ -2007,7 +2003,7 @@ int blocks_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
       if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, fp8 ? 64 : 32, p.maps, nsrc))) return e;
     }
     const int32_t items = (int32_t)(nrows * c->hkv * qtiles);
-    p.cta_parts = cta_parts(items, parts, G > 8, nsm);
+    p.cta_parts = cta_parts(items, parts, nsm);
     p.ctas = (parts + p.cta_parts - 1) / p.cta_parts;
     record(17, base, nrows, nr, items, items * p.ctas, base * hd, base * hd);
     if (!dry_run())
