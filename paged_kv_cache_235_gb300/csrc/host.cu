@@ -1661,6 +1661,8 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 // From this many heads on a thread group takes several: one a group then no
 // longer has all of them on the GPU at once.
 constexpr int32_t kWideHeads = 8192;
+// Warps of a call, about: 24 a SM at once.
+constexpr int32_t kRowWarps = 3648;
 
 int qkv_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const tfpa_qkv* in,
              const int32_t* row_seg, const int32_t* row_pos, int32_t rows, void* q_out,
@@ -1756,8 +1758,12 @@ int qkv_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const tfpa
     p.kv = c->dtype;
     const int32_t heads = nrows * (q_heads + c->hkv);
     p.wide = heads >= kWideHeads;
-    record(14, base, nrows, nr, heads, (heads + 15) / 16, in->q ? base * in->q_stride : 0,
-           in->q ? (int64_t)base * c->hq * hd : 0);
+    const int32_t step = p.wide ? 4 : 1, kv_step = p.wide ? 2 : 1;   // heads of a unit
+    const int32_t pairs =
+        (q_heads + 2 * step - 1) / (2 * step) + (c->hkv + 2 * kv_step - 1) / (2 * kv_step);
+    p.slices = p.wide ? (int32_t)std::min<int64_t>(pairs, (kRowWarps + nrows - 1) / nrows) : pairs;
+    record(14, base, nrows, nr, heads, (int32_t)(((int64_t)nrows * p.slices + 7) / 8),
+           in->q ? base * in->q_stride : 0, in->q ? (int64_t)base * c->hq * hd : 0);
     if (!dry_run())
       if ((e = to_err(launch_write_qkv(p, stream)))) return e;
   }

@@ -358,7 +358,8 @@ struct QkvParams {
   int32_t hkv;
   int32_t num_pages;
   int32_t kv;                 // KvType
-  int32_t wide;               // four heads a thread group instead of one
+  int32_t wide;               // four heads a step of a half-warp instead of one
+  int32_t slices;             // warps of a row
 };
 
 // Bounds of the blocks of a launch: each run is consecutive blocks of a stream.

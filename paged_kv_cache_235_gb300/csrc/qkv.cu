@@ -9,10 +9,10 @@
 // taken to within an eighth of a turn of a quarter turn (its top bits) and
 // only then rounded to float32.  Bound by the stores, 8 bytes an entry.
 //
-// Rows.  A 16-thread group takes a q head, or a kv head's K and V, of a row,
-// and where there are rows enough four q heads or two kv heads: their loads are
-// then in flight together and share the row's angles and the weights.  A thread
-// holds 8 head dims.  The mean
+// Rows.  A half-warp takes a q head, or a kv head's K and V, of a row, and where
+// there are rows enough several times four q heads or two kv heads: their
+// loads are then in flight together, they share the row's angles and the
+// weights, and their roots are taken at once.  A thread holds 8 head dims.  The mean
 // square is added up pair by pair (a thread's 8, then lanes 1, 2, 4, 8
 // apart), and every product, sum, quotient and root is rounded to float32 on
 // its own, so that the stored codes are a function of the inputs alone.
@@ -94,6 +94,11 @@ __device__ __forceinline__ void load8f(const float* a, float (&x)[8]) {
   x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
 }
 
+// Every exchange is the whole warp's, whose halves go through their heads in step:
+// one under a mask of 16 lanes costs several instructions more (4,096 rows of 40
+// heads 30 us).
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
 // A lane's eight dims as pairs of floats, dims i and i + 4 in one: sums over
 // neighbours then take both halves of the eight at once.
 struct Dims {
@@ -142,27 +147,27 @@ __device__ __forceinline__ float squares(const Dims& d) {
 // each lane sums, and takes the root of, one head, and the roots are handed
 // round.  Every sum is the same pair of numbers as one head alone would add.
 template <int H>
-__device__ __forceinline__ void roots(float (&s)[H], float eps, int t, unsigned lanes) {
+__device__ __forceinline__ void roots(float (&s)[H], float eps, int t) {
   auto root = [&](float sum) {
     return __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.f / kHeadDim), eps)));
   };
   if (H == 4) {
     const bool b0 = t & 1, b1 = t & 2;
     float k0 = b0 ? s[2 % H] : s[0], k1 = b0 ? s[3 % H] : s[1 % H];
-    k0 = __fadd_rn(k0, __shfl_xor_sync(lanes, b0 ? s[0] : s[2 % H], 1));
-    k1 = __fadd_rn(k1, __shfl_xor_sync(lanes, b0 ? s[1 % H] : s[3 % H], 1));
-    float k = __fadd_rn(b1 ? k1 : k0, __shfl_xor_sync(lanes, b1 ? k0 : k1, 2));
-    k = __fadd_rn(k, __shfl_xor_sync(lanes, k, 4));
-    k = __fadd_rn(k, __shfl_xor_sync(lanes, k, 8));
+    k0 = __fadd_rn(k0, __shfl_xor_sync(kAll, b0 ? s[0] : s[2 % H], 1));
+    k1 = __fadd_rn(k1, __shfl_xor_sync(kAll, b0 ? s[1 % H] : s[3 % H], 1));
+    float k = __fadd_rn(b1 ? k1 : k0, __shfl_xor_sync(kAll, b1 ? k0 : k1, 2));
+    k = __fadd_rn(k, __shfl_xor_sync(kAll, k, 4));
+    k = __fadd_rn(k, __shfl_xor_sync(kAll, k, 8));
     const float inv = root(k);
 #pragma unroll
     for (int h = 0; h < H; ++h)
-      s[h] = __shfl_sync(lanes, inv, (threadIdx.x & 16) + (h >> 1) + 2 * (h & 1));
+      s[h] = __shfl_sync(kAll, inv, (threadIdx.x & 16) + (h >> 1) + 2 * (h & 1));
   } else {
 #pragma unroll
     for (int h = 0; h < H; ++h) {
 #pragma unroll
-      for (int d = 1; d < 16; d *= 2) s[h] = __fadd_rn(s[h], __shfl_xor_sync(lanes, s[h], d));
+      for (int d = 1; d < 16; d *= 2) s[h] = __fadd_rn(s[h], __shfl_xor_sync(kAll, s[h], d));
       s[h] = root(s[h]);
     }
   }
@@ -208,9 +213,9 @@ __device__ __forceinline__ Turn make_turn(const QkvParams& p, int rpos, int t) {
 }
 
 // Eight dims of a head rotated: a c - b s and b c + a s are both the dim's own
-// product and, rounded on its own, its partner's under sin's sign.  All 16 lanes
-// take part in the exchange.
-__device__ __forceinline__ void rotate(Dims& x, const Turn& u, bool interleaved, unsigned lanes) {
+// product and, rounded on its own, its partner's under sin's sign.  The whole warp
+// takes part in the exchange.
+__device__ __forceinline__ void rotate(Dims& x, const Turn& u, bool interleaved) {
   Dims o;
   if (interleaved) {                         // dims 0, 1 and 2, 3 of each four
     o.v[0] = x.v[1];
@@ -220,8 +225,8 @@ __device__ __forceinline__ void rotate(Dims& x, const Turn& u, bool interleaved,
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      o.v[i].x = __shfl_sync(lanes, x.v[i].x, u.from);
-      o.v[i].y = __shfl_sync(lanes, x.v[i].y, u.from);
+      o.v[i].x = __shfl_sync(kAll, x.v[i].x, u.from);
+      o.v[i].y = __shfl_sync(kAll, x.v[i].y, u.from);
     }
   }
   if (!u.on) return;
@@ -230,11 +235,13 @@ __device__ __forceinline__ void rotate(Dims& x, const Turn& u, bool interleaved,
     x.v[i] = add_each(fmul2(x.v[i], u.c.v[i]), fmul2(o.v[i], u.s.v[i]));
 }
 
-// A row's K (x, and kx as bf16) and V of one kv head into the cache.
+// A row's K (x, and kx as bf16) and V of one kv head into the cache, if it is
+// there; the whole warp comes here.
 __device__ __forceinline__ void store_kv(const QkvParams& p, const WriteRun& run, size_t dst_row,
-                                         int g, int t, unsigned lanes, float (&x)[8],
+                                         int g, int t, bool live, float (&x)[8],
                                          const uint4& kx, const uint4& vv) {
   if (p.kv == kKvBf16) {
+    if (!live) return;
     __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(run.k_dst) + dst_row * kHeadDim + t * 8;
     __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(run.v_dst) + dst_row * kHeadDim + t * 8;
     *reinterpret_cast<uint4*>(kd) = kx;
@@ -249,107 +256,141 @@ __device__ __forceinline__ void store_kv(const QkvParams& p, const WriteRun& run
   if (p.kv == kKvFp4) {
     const size_t codes = fp4_codes(dst_row) + t * 4, scales = fp4_scales(dst_row) + (t >> 1);
     uint32_t ks, vs;
-    *reinterpret_cast<uint32_t*>(kb + codes) = quant8_fp4(x, gk, lanes, ks);
-    *reinterpret_cast<uint32_t*>(vb + codes) = quant8_fp4(vf, gv, lanes, vs);
+    const uint32_t kc = quant8_fp4(x, gk, kAll, ks), vc = quant8_fp4(vf, gv, kAll, vs);
+    if (!live) return;
+    *reinterpret_cast<uint32_t*>(kb + codes) = kc;
+    *reinterpret_cast<uint32_t*>(vb + codes) = vc;
     if (!(t & 1)) {
       kb[scales] = (uint8_t)ks;
       vb[scales] = (uint8_t)vs;
     }
     return;
   }
+  if (!live) return;
   *reinterpret_cast<uint2*>(kb + dst_row * kHeadDim + t * 8) = quant8(x, gk);
   *reinterpret_cast<uint2*>(vb + dst_row * kHeadDim + t * 8) = quant8(vf, gv);
 }
 
 }  // namespace
 
-// H: query heads of a 16-lane group at most; a group of kv heads has half as
-// many (but one), each with its K and V.
+// A warp walks over every p.slices-th pair of a row's units, a unit a half-warp:
+// H query heads, or half as many kv heads (but one) with their K and V.  The row's
+// angles stay in registers.
 template <int H>
 __global__ void __launch_bounds__(256, H > 1 ? 3 : 4)
     write_qkv_kernel(const __grid_constant__ QkvParams p) {
   constexpr int HK = H > 1 ? H / 2 : 1;
   allow_next_grid();
   wait_prior_grid();
-  const int q_units = (p.q_heads + H - 1) / H, units = q_units + (p.hkv + HK - 1) / HK;
-  const int gid = blockIdx.x * (blockDim.x / 16) + (threadIdx.x >> 4);
+  const int wid = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
   const int t = threadIdx.x & 15;                          // 8-element slice
-  if (gid >= p.rows * units) return;
-  const unsigned lanes = 0xFFFFu << (threadIdx.x & 16);    // the group's 16 threads
-  const int row = gid / units;
-  const int unit = gid - row * units;
+  const int side = (threadIdx.x >> 4) & 1;                 // half-warp: its unit of a pair
+  const int row = wid / p.slices;
+  if (row >= p.rows) return;
+  int pair = wid - row * p.slices;
   int ri = 0;
   while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
   const WriteRun& run = p.runs[ri];
   const int pos = run.pos0 + (row - run.row0);
+  const int q_pairs = (p.q_heads + 2 * H - 1) / (2 * H);
+  const int kv_pairs = (p.hkv + 2 * HK - 1) / (2 * HK);
   int rpos = pos;
   if (p.rope_pos) rpos = __ldg(p.rope_pos + row);
-  const bool is_q = unit < q_units;
-  // ---- the heads' dims are on their way before anything else is looked at
-  uint4 in[H], vin[HK];
-  const int h0 = is_q ? unit * H : (unit - q_units) * HK;
-  const int nh = min(is_q ? H : HK, (is_q ? p.q_heads : p.hkv) - h0);
-  const __nv_bfloat16* src =
-      (is_q ? p.q + (size_t)row * p.q_stride : p.k + (size_t)row * p.k_stride) + h0 * kHeadDim +
-      t * 8;
-  const int pid = !is_q && run.page_table ? __ldg(run.page_table + (pos >> 8)) : 0;
+  const int pid = run.page_table ? __ldg(run.page_table + (pos >> 8)) : 0;
+  uint4 in[H];
+  // n: heads that are there (none: a half-warp that only keeps in step)
+  auto load = [&](const __nv_bfloat16* from, int n) {
 #pragma unroll
-  for (int h = 0; h < H; ++h)
-    if (h < nh) in[h] = *reinterpret_cast<const uint4*>(src + h * kHeadDim);
-  if (!is_q) {
-    const __nv_bfloat16* vs = p.v + (size_t)row * p.v_stride + h0 * kHeadDim + t * 8;
-#pragma unroll
-    for (int h = 0; h < HK; ++h)
-      if (h < nh) vin[h] = *reinterpret_cast<const uint4*>(vs + h * kHeadDim);
-  }
-  const float* weight = is_q ? p.q_weight : p.k_weight;
-  Dims w;
-  if (weight) {
-    float f[8];
-    load8f(weight + t * 8, f);
-    w = dims_of(f);
-  }
+    for (int h = 0; h < H; ++h)
+      in[h] = h < n ? __ldg(reinterpret_cast<const uint4*>(from + h * kHeadDim))
+                    : make_uint4(0, 0, 0, 0);
+  };
+  const __nv_bfloat16* qp = p.q + (size_t)row * p.q_stride + t * 8;
+  // the first unit's dims are on their way before anything else is looked at
+  int h0 = (2 * pair + side) * H;
+  if (pair < q_pairs) load(qp + h0 * kHeadDim, p.q_heads - h0);
   Turn turn;
   if (p.rope_cos) {
-    if ((unsigned)rpos >= (unsigned)p.rope_n) {            // all 16 lanes alike
-      if (t == 0) flag_error(p.err_flag, kErrRopeRange);
+    if ((unsigned)rpos >= (unsigned)p.rope_n) {            // the whole warp's row
+      if ((threadIdx.x & 31) == 0) flag_error(p.err_flag, kErrRopeRange);
       return;
     }
     turn = make_turn(p, rpos, t);
   }
-  if (!is_q && run.page_table && (unsigned)pid >= (unsigned)p.num_pages) {
-    if (t == 0) flag_error(p.err_flag, kErrBadPage);
-    return;
-  }
-  // ---- the heads' roots together, then head by head
-  const bool turns = weight || p.rope_cos;
+  Dims w;
+  auto load_weight = [&](const float* a) {
+    if (!a) return;
+    float f[8];
+    load8f(a + t * 8, f);
+    w = dims_of(f);
+  };
+  // The heads' roots together; then a head's dims, normed and turned.
   float inv[H];
-  if (weight) {
+  auto find_roots = [&](const float* weight) {
+    if (!weight) return;
 #pragma unroll
-    for (int h = 0; h < H; ++h) inv[h] = h < nh ? squares(unpack(in[h])) : 0.f;
-    roots<H>(inv, p.eps, t, lanes);
-  }
-#pragma unroll
-  for (int h = 0; h < H; ++h) {
-    if (h >= nh) break;
+    for (int h = 0; h < H; ++h) inv[h] = squares(unpack(in[h]));
+    roots<H>(inv, p.eps, t);
+  };
+  auto finish = [&](int h, const float* weight, float (&f)[8]) {
     Dims x = unpack(in[h]);
     if (weight) {
       const f2 r = f2{inv[h], inv[h]};
 #pragma unroll
       for (int i = 0; i < 4; ++i) x.v[i] = fmul2(fmul2(x.v[i], r), w.v[i]);
     }
-    if (p.rope_cos) rotate(x, turn, p.interleaved, lanes);
-    float f[8];
+    if (p.rope_cos) rotate(x, turn, p.interleaved);
     floats_of(x, f);
-    if (is_q) {
-      *reinterpret_cast<uint4*>(p.q_out + ((size_t)row * p.q_heads + h0 + h) * kHeadDim + t * 8) =
-          turns ? pack8(f) : in[h];
-    } else if (h < HK) {
-      const int g = h0 + h;
+  };
+  if (pair < q_pairs) {
+    load_weight(p.q_weight);
+    const bool turns = p.q_weight || p.rope_cos;
+    __nv_bfloat16* to = p.q_out + (size_t)row * p.q_heads * kHeadDim + t * 8;
+    while (true) {
+      const int n = p.q_heads - h0;
+      find_roots(p.q_weight);
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        float f[8];
+        finish(h, p.q_weight, f);
+        if (h < n)
+          *reinterpret_cast<uint4*>(to + (h0 + h) * kHeadDim) = turns ? pack8(f) : in[h];
+      }
+      pair += p.slices;
+      if (pair >= q_pairs) break;
+      h0 = (2 * pair + side) * H;
+      load(qp + h0 * kHeadDim, p.q_heads - h0);
+    }
+  }
+  pair -= q_pairs;
+  if (pair >= kv_pairs) return;
+  if (run.page_table && (unsigned)pid >= (unsigned)p.num_pages) {
+    if ((threadIdx.x & 31) == 0) flag_error(p.err_flag, kErrBadPage);
+    return;
+  }
+  load_weight(p.k_weight);
+  const bool turns = p.k_weight || p.rope_cos;
+  const __nv_bfloat16* kp = p.k + (size_t)row * p.k_stride + t * 8;
+  const __nv_bfloat16* vp = p.v + (size_t)row * p.v_stride + t * 8;
+  for (; pair < kv_pairs; pair += p.slices) {
+    const int g0 = (2 * pair + side) * HK, n = min(HK, p.hkv - g0);
+    load(kp + g0 * kHeadDim, n);
+    uint4 vin[HK];
+#pragma unroll
+    for (int h = 0; h < HK; ++h)
+      vin[h] = h < n ? __ldg(reinterpret_cast<const uint4*>(vp + (g0 + h) * kHeadDim))
+                     : make_uint4(0, 0, 0, 0);
+    find_roots(p.k_weight);
+#pragma unroll
+    for (int h = 0; h < HK; ++h) {
+      const bool live = h < n;
+      const int g = live ? g0 + h : 0;
       const size_t dst_row = run.page_table
                                  ? ((size_t)pid * p.hkv + g) * kPage + (pos & (kPage - 1))
                                  : (size_t)g * run.slab_cap + pos;
-      store_kv(p, run, dst_row, g, t, lanes, f, turns ? pack8(f) : in[h], vin[h < HK ? h : 0]);
+      float f[8];
+      finish(h, p.k_weight, f);
+      store_kv(p, run, dst_row, g, t, live, f, turns ? pack8(f) : in[h], vin[h]);
     }
   }
 }
@@ -360,17 +401,10 @@ cudaError_t launch_rope_table(const TableParams& p, cudaStream_t s) {
                     dim3(kTableThreads), 0, s, p);
 }
 
-namespace {
-template <int H>
-cudaError_t launch_rows(const QkvParams& p, cudaStream_t s) {
-  constexpr int HK = H > 1 ? H / 2 : 1;
-  const int groups = p.rows * ((p.q_heads + H - 1) / H + (p.hkv + HK - 1) / HK);
-  return launch_pdl(write_qkv_kernel<H>, dim3((groups + 15) / 16), dim3(256), 0, s, p);
-}
-}  // namespace
-
 cudaError_t launch_write_qkv(const QkvParams& p, cudaStream_t s) {
-  return p.wide ? launch_rows<4>(p, s) : launch_rows<1>(p, s);
+  const dim3 grid((unsigned)(((int64_t)p.rows * p.slices + 7) / 8));
+  return p.wide ? launch_pdl(write_qkv_kernel<4>, grid, dim3(256), 0, s, p)
+                : launch_pdl(write_qkv_kernel<1>, grid, dim3(256), 0, s, p);
 }
 
 }  // namespace tfpa
