@@ -1661,8 +1661,6 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 // From this many heads on a thread group takes several: one a group then no
 // longer has all of them on the GPU at once.
 constexpr int32_t kWideHeads = 8192;
-// Warps of a call, about: 24 a SM at once.
-constexpr int32_t kRowWarps = 3648;
 
 int qkv_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const tfpa_qkv* in,
              const int32_t* row_seg, const int32_t* row_pos, int32_t rows, void* q_out,
@@ -1708,6 +1706,8 @@ int qkv_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const tfpa
       if (r.pos0 + r.nrows > in->rope_n) return TFPA_ERANGE;
   if (rows == 0) return TFPA_OK;
   if ((e = check_device())) return e;
+  const int nsm = sm_count();
+  if (nsm < 1) return TFPA_ECUDA;
   thread_local QkvParams p;
   size_t ri = 0;
   while (ri < runs.size()) {
@@ -1755,17 +1755,17 @@ int qkv_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const tfpa
     p.q_heads = q_heads;
     p.hkv = c->hkv;
     p.num_pages = c->num_pages;
-    p.kv = c->dtype;
     const int32_t heads = nrows * (q_heads + c->hkv);
     p.wide = heads >= kWideHeads;
-    const int32_t step = p.wide ? 4 : 1, kv_step = p.wide ? 2 : 1;   // heads of a unit
-    const int32_t pairs =
-        (q_heads + 2 * step - 1) / (2 * step) + (c->hkv + 2 * kv_step - 1) / (2 * kv_step);
-    p.slices = p.wide ? (int32_t)std::min<int64_t>(pairs, (kRowWarps + nrows - 1) / nrows) : pairs;
-    record(14, base, nrows, nr, heads, (int32_t)(((int64_t)nrows * p.slices + 7) / 8),
-           in->q ? base * in->q_stride : 0, in->q ? (int64_t)base * c->hq * hd : 0);
+    const int32_t step = p.wide ? 4 : 1, kv_step = p.wide ? 2 : 1;   // heads of half a unit
+    const int64_t units = (int64_t)nrows * ((q_heads + 2 * step - 1) / (2 * step) +
+                                            (c->hkv + 2 * kv_step - 1) / (2 * kv_step));
+    // one unit a warp, or what the GPU holds at once: two blocks of eight a SM
+    p.warps = p.wide ? (int32_t)std::min<int64_t>(units, 16 * (int64_t)nsm) : (int32_t)units;
+    record(14, base, nrows, nr, heads, p.warps, in->q ? base * in->q_stride : 0,
+           in->q ? (int64_t)base * c->hq * hd : 0);
     if (!dry_run())
-      if ((e = to_err(launch_write_qkv(p, stream)))) return e;
+      if ((e = to_err(launch_write_qkv(p, c->dtype, stream)))) return e;
   }
   return TFPA_OK;
 }

@@ -357,9 +357,8 @@ struct QkvParams {
   int32_t q_heads;            // 0: no q
   int32_t hkv;
   int32_t num_pages;
-  int32_t kv;                 // KvType
   int32_t wide;               // four heads a step of a half-warp instead of one
-  int32_t slices;             // warps of a row
+  int32_t warps;              // of the launch
 };
 
 // Bounds of the blocks of a launch: each run is consecutive blocks of a stream.
@@ -442,7 +441,7 @@ struct BlocksParams {
 
 // Launchers (defined next to their kernels).
 cudaError_t launch_rope_table(const TableParams& p, cudaStream_t s);
-cudaError_t launch_write_qkv(const QkvParams& p, cudaStream_t s);
+cudaError_t launch_write_qkv(const QkvParams& p, int kv, cudaStream_t s);
 cudaError_t launch_key_bounds(const BoundsParams& p, int kv, cudaStream_t s);
 cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t s);
 cudaError_t launch_decode_blocks(const BlocksParams& p, int kv, cudaStream_t s);

@@ -237,10 +237,11 @@ __device__ __forceinline__ void rotate(Dims& x, const Turn& u, bool interleaved)
 
 // A row's K (x, and kx as bf16) and V of one kv head into the cache, if it is
 // there; the whole warp comes here.
+template <int KV>
 __device__ __forceinline__ void store_kv(const QkvParams& p, const WriteRun& run, size_t dst_row,
                                          int g, int t, bool live, float (&x)[8],
                                          const uint4& kx, const uint4& vv) {
-  if (p.kv == kKvBf16) {
+  if (KV == kKvBf16) {
     if (!live) return;
     __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(run.k_dst) + dst_row * kHeadDim + t * 8;
     __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(run.v_dst) + dst_row * kHeadDim + t * 8;
@@ -253,7 +254,7 @@ __device__ __forceinline__ void store_kv(const QkvParams& p, const WriteRun& run
   uint8_t* kb = static_cast<uint8_t*>(run.k_dst);
   uint8_t* vb = static_cast<uint8_t*>(run.v_dst);
   const float gk = __ldg(p.k_scale + g), gv = __ldg(p.v_scale + g);
-  if (p.kv == kKvFp4) {
+  if (KV == kKvFp4) {
     const size_t codes = fp4_codes(dst_row) + t * 4, scales = fp4_scales(dst_row) + (t >> 1);
     uint32_t ks, vs;
     const uint32_t kc = quant8_fp4(x, gk, kAll, ks), vc = quant8_fp4(vf, gv, kAll, vs);
@@ -273,124 +274,121 @@ __device__ __forceinline__ void store_kv(const QkvParams& p, const WriteRun& run
 
 }  // namespace
 
-// A warp walks over every p.slices-th pair of a row's units, a unit a half-warp:
-// H query heads, or half as many kv heads (but one) with their K and V.  The row's
-// angles stay in registers.
-template <int H>
-__global__ void __launch_bounds__(256, H > 1 ? 3 : 4)
+// A warp takes an equal run of the call's units in row order; a unit is a pair of
+// steps, one a half-warp: H query heads, or half as many kv heads (but one) with
+// their K and V.  A row's angles, and the weights, stay in registers.
+template <int KV, int H>
+__global__ void __launch_bounds__(H > 1 ? 256 : 64, H > 1 ? 2 : 8)
     write_qkv_kernel(const __grid_constant__ QkvParams p) {
   constexpr int HK = H > 1 ? H / 2 : 1;
   allow_next_grid();
   wait_prior_grid();
   const int wid = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+  if (wid >= p.warps) return;
   const int t = threadIdx.x & 15;                          // 8-element slice
-  const int side = (threadIdx.x >> 4) & 1;                 // half-warp: its unit of a pair
-  const int row = wid / p.slices;
-  if (row >= p.rows) return;
-  int pair = wid - row * p.slices;
+  const int side = (threadIdx.x >> 4) & 1;                 // half-warp: its step of a unit
+  const int q_units = (p.q_heads + 2 * H - 1) / (2 * H);
+  const int units = q_units + (p.hkv + 2 * HK - 1) / (2 * HK);
+  const int64_t all = (int64_t)p.rows * units;
+  int left = (int)(all * (wid + 1) / p.warps);
+  int unit = (int)(all * wid / p.warps);
+  left -= unit;
+  int row = unit / units;
+  unit -= row * units;
   int ri = 0;
   while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
-  const WriteRun& run = p.runs[ri];
-  const int pos = run.pos0 + (row - run.row0);
-  const int q_pairs = (p.q_heads + 2 * H - 1) / (2 * H);
-  const int kv_pairs = (p.hkv + 2 * HK - 1) / (2 * HK);
-  int rpos = pos;
-  if (p.rope_pos) rpos = __ldg(p.rope_pos + row);
-  const int pid = run.page_table ? __ldg(run.page_table + (pos >> 8)) : 0;
-  uint4 in[H];
-  // n: heads that are there (none: a half-warp that only keeps in step)
-  auto load = [&](const __nv_bfloat16* from, int n) {
+
+  uint4 in[H], vin[HK];
+  Turn turn;
+  Dims w;
+  float inv[H];
+  int pos = 0, pid = 0;
+  const float* weight = nullptr;           // whose values w holds
+  bool fresh = true, on_table = true;      // a row's first unit of this warp; its angles are there
+  for (; left > 0; --left) {
+    const bool is_q = unit < q_units;
+    // ---- the unit's dims are on their way before anything else is looked at.  n:
+    // heads that are there (none: a half-warp that only keeps in step)
+    const int h0 = is_q ? (2 * unit + side) * H : (2 * (unit - q_units) + side) * HK;
+    const int n = is_q ? p.q_heads - h0 : min(HK, p.hkv - h0);
+    const __nv_bfloat16* from =
+        (is_q ? p.q + (size_t)row * p.q_stride : p.k + (size_t)row * p.k_stride) +
+        h0 * kHeadDim + t * 8;
 #pragma unroll
     for (int h = 0; h < H; ++h)
       in[h] = h < n ? __ldg(reinterpret_cast<const uint4*>(from + h * kHeadDim))
                     : make_uint4(0, 0, 0, 0);
-  };
-  const __nv_bfloat16* qp = p.q + (size_t)row * p.q_stride + t * 8;
-  // the first unit's dims are on their way before anything else is looked at
-  int h0 = (2 * pair + side) * H;
-  if (pair < q_pairs) load(qp + h0 * kHeadDim, p.q_heads - h0);
-  Turn turn;
-  if (p.rope_cos) {
-    if ((unsigned)rpos >= (unsigned)p.rope_n) {            // the whole warp's row
-      if ((threadIdx.x & 31) == 0) flag_error(p.err_flag, kErrRopeRange);
-      return;
-    }
-    turn = make_turn(p, rpos, t);
-  }
-  Dims w;
-  auto load_weight = [&](const float* a) {
-    if (!a) return;
-    float f[8];
-    load8f(a + t * 8, f);
-    w = dims_of(f);
-  };
-  // The heads' roots together; then a head's dims, normed and turned.
-  float inv[H];
-  auto find_roots = [&](const float* weight) {
-    if (!weight) return;
+    if (!is_q) {
+      const __nv_bfloat16* vp = p.v + (size_t)row * p.v_stride + h0 * kHeadDim + t * 8;
 #pragma unroll
-    for (int h = 0; h < H; ++h) inv[h] = squares(unpack(in[h]));
-    roots<H>(inv, p.eps, t);
-  };
-  auto finish = [&](int h, const float* weight, float (&f)[8]) {
-    Dims x = unpack(in[h]);
-    if (weight) {
-      const f2 r = f2{inv[h], inv[h]};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x.v[i] = fmul2(fmul2(x.v[i], r), w.v[i]);
+      for (int h = 0; h < HK; ++h)
+        vin[h] = h < n ? __ldg(reinterpret_cast<const uint4*>(vp + h * kHeadDim))
+                       : make_uint4(0, 0, 0, 0);
     }
-    if (p.rope_cos) rotate(x, turn, p.interleaved);
-    floats_of(x, f);
-  };
-  if (pair < q_pairs) {
-    load_weight(p.q_weight);
-    const bool turns = p.q_weight || p.rope_cos;
-    __nv_bfloat16* to = p.q_out + (size_t)row * p.q_heads * kHeadDim + t * 8;
-    while (true) {
-      const int n = p.q_heads - h0;
-      find_roots(p.q_weight);
+    if (fresh) {
+      while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
+      const WriteRun& run = p.runs[ri];
+      pos = run.pos0 + (row - run.row0);
+      pid = run.page_table ? __ldg(run.page_table + (pos >> 8)) : 0;
+      if (p.rope_cos) {
+        const int rpos = p.rope_pos ? __ldg(p.rope_pos + row) : pos;
+        on_table = (unsigned)rpos < (unsigned)p.rope_n;    // the whole warp's row
+        if (on_table)
+          turn = make_turn(p, rpos, t);
+        else if ((threadIdx.x & 31) == 0)
+          flag_error(p.err_flag, kErrRopeRange);
+      }
+      fresh = false;
+    }
+    const float* need = is_q ? p.q_weight : p.k_weight;
+    if (need && need != weight) {
+      float f[8];
+      load8f(need + t * 8, f);
+      w = dims_of(f);
+      weight = need;
+    }
+    const WriteRun& run = p.runs[ri];
+    const bool on_page = is_q || !run.page_table || (unsigned)pid < (unsigned)p.num_pages;
+    if (!on_page && (threadIdx.x & 31) == 0) flag_error(p.err_flag, kErrBadPage);
+    if (on_table && on_page) {
+      // ---- the heads' roots together; then head by head
+      const bool turns = need || p.rope_cos;
+      if (need) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) inv[h] = squares(unpack(in[h]));
+        roots<H>(inv, p.eps, t);
+      }
 #pragma unroll
       for (int h = 0; h < H; ++h) {
+        if (!is_q && h >= HK) break;
+        Dims x = unpack(in[h]);
+        if (need) {
+          const f2 r = f2{inv[h], inv[h]};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x.v[i] = fmul2(fmul2(x.v[i], r), w.v[i]);
+        }
+        if (p.rope_cos) rotate(x, turn, p.interleaved);
         float f[8];
-        finish(h, p.q_weight, f);
-        if (h < n)
-          *reinterpret_cast<uint4*>(to + (h0 + h) * kHeadDim) = turns ? pack8(f) : in[h];
+        floats_of(x, f);
+        const uint4 y = turns ? pack8(f) : in[h];
+        const bool live = h < n;
+        if (is_q) {
+          if (live)
+            *reinterpret_cast<uint4*>(
+                p.q_out + ((size_t)row * p.q_heads + h0 + h) * kHeadDim + t * 8) = y;
+        } else if (h < HK) {
+          const int g = live ? h0 + h : 0;
+          const size_t dst_row = run.page_table
+                                     ? ((size_t)pid * p.hkv + g) * kPage + (pos & (kPage - 1))
+                                     : (size_t)g * run.slab_cap + pos;
+          store_kv<KV>(p, run, dst_row, g, t, live, f, y, vin[h < HK ? h : 0]);
+        }
       }
-      pair += p.slices;
-      if (pair >= q_pairs) break;
-      h0 = (2 * pair + side) * H;
-      load(qp + h0 * kHeadDim, p.q_heads - h0);
     }
-  }
-  pair -= q_pairs;
-  if (pair >= kv_pairs) return;
-  if (run.page_table && (unsigned)pid >= (unsigned)p.num_pages) {
-    if ((threadIdx.x & 31) == 0) flag_error(p.err_flag, kErrBadPage);
-    return;
-  }
-  load_weight(p.k_weight);
-  const bool turns = p.k_weight || p.rope_cos;
-  const __nv_bfloat16* kp = p.k + (size_t)row * p.k_stride + t * 8;
-  const __nv_bfloat16* vp = p.v + (size_t)row * p.v_stride + t * 8;
-  for (; pair < kv_pairs; pair += p.slices) {
-    const int g0 = (2 * pair + side) * HK, n = min(HK, p.hkv - g0);
-    load(kp + g0 * kHeadDim, n);
-    uint4 vin[HK];
-#pragma unroll
-    for (int h = 0; h < HK; ++h)
-      vin[h] = h < n ? __ldg(reinterpret_cast<const uint4*>(vp + (g0 + h) * kHeadDim))
-                     : make_uint4(0, 0, 0, 0);
-    find_roots(p.k_weight);
-#pragma unroll
-    for (int h = 0; h < HK; ++h) {
-      const bool live = h < n;
-      const int g = live ? g0 + h : 0;
-      const size_t dst_row = run.page_table
-                                 ? ((size_t)pid * p.hkv + g) * kPage + (pos & (kPage - 1))
-                                 : (size_t)g * run.slab_cap + pos;
-      float f[8];
-      finish(h, p.k_weight, f);
-      store_kv(p, run, dst_row, g, t, live, f, turns ? pack8(f) : in[h], vin[h]);
+    if (++unit == units) {
+      unit = 0;
+      ++row;
+      fresh = true;
     }
   }
 }
@@ -401,10 +399,19 @@ cudaError_t launch_rope_table(const TableParams& p, cudaStream_t s) {
                     dim3(kTableThreads), 0, s, p);
 }
 
-cudaError_t launch_write_qkv(const QkvParams& p, cudaStream_t s) {
-  const dim3 grid((unsigned)(((int64_t)p.rows * p.slices + 7) / 8));
-  return p.wide ? launch_pdl(write_qkv_kernel<4>, grid, dim3(256), 0, s, p)
-                : launch_pdl(write_qkv_kernel<1>, grid, dim3(256), 0, s, p);
+namespace {
+template <int KV>
+cudaError_t launch_rows(const QkvParams& p, cudaStream_t s) {
+  return p.wide
+             ? launch_pdl(write_qkv_kernel<KV, 4>, dim3((p.warps + 7) / 8), dim3(256), 0, s, p)
+             : launch_pdl(write_qkv_kernel<KV, 1>, dim3((p.warps + 1) / 2), dim3(64), 0, s, p);
+}
+}  // namespace
+
+cudaError_t launch_write_qkv(const QkvParams& p, int kv, cudaStream_t s) {
+  return kv == kKvBf16  ? launch_rows<kKvBf16>(p, s)
+         : kv == kKvFp8 ? launch_rows<kKvFp8>(p, s)
+                        : launch_rows<kKvFp4>(p, s);
 }
 
 }  // namespace tfpa
