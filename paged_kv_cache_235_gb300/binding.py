@@ -692,23 +692,26 @@ def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, r
     e.g. of one fused projection's output; q and q_out may both be None."""
     cs, n = _segs(segs)
     rs, rp = _i32(row_seg), _i32(row_pos)
-    rows = len(rs)
-    table = half = 0
+    rows, hq, hkv = len(rs), cache.hq, cache.hkv
+    table = half = cos = sin = 0
     if rope_cos is not None:
-        table, half = rope_cos.shape
-        if rope_sin.shape != (table, half) or not (rope_cos.is_contiguous()
-                                                   and rope_sin.is_contiguous()):
+        table, half = shape = rope_cos.shape
+        if rope_sin.shape != shape or not (rope_cos.is_contiguous()
+                                           and rope_sin.is_contiguous()):
             raise ValueError("rope_cos and rope_sin must be contiguous tables of one shape")
-    hq, hkv = cache.hq, cache.hkv
-    if q_out is not None and (q_out.shape != (rows, hq, HEAD_DIM) or not q_out.is_contiguous()):
-        raise ValueError("q_out must be contiguous [rows][hq][128]")
-    a = _pack_qkv(_ptr(q) or 0, _ptr(k) or 0, _ptr(v) or 0,
-                  0 if q is None else _heads(q, rows, hq, "q"), _heads(k, rows, hkv, "k"),
-                  _heads(v, rows, hkv, "v"), _ptr(q_weight) or 0, _ptr(k_weight) or 0,
-                  _ptr(rope_cos) or 0, _ptr(rope_sin) or 0, _ptr(rope_pos) or 0, table, 2 * half,
-                  1 if interleaved else 0, eps)
-    _check(lib().tfpa_write_qkv(ctypes.byref(cache.c()), cs, n, a, _ptr(rs), _ptr(rp), rows,
-                                _ptr(q_out), _stream(stream)), "tfpa_write_qkv")
+        cos, sin = rope_cos.data_ptr() or 0, rope_sin.data_ptr() or 0
+    qp = qs = op = 0
+    if q is not None:
+        qp, qs = q.data_ptr() or 0, _heads(q, rows, hq, "q")
+    if q_out is not None:
+        if q_out.shape != (rows, hq, HEAD_DIM) or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous [rows][hq][128]")
+        op = q_out.data_ptr() or 0
+    a = _pack_qkv(qp, k.data_ptr() or 0, v.data_ptr() or 0, qs, _heads(k, rows, hkv, "k"),
+                  _heads(v, rows, hkv, "v"), _ptr(q_weight) or 0, _ptr(k_weight) or 0, cos, sin,
+                  _ptr(rope_pos) or 0, table, 2 * half, 1 if interleaved else 0, eps)
+    _check(lib().tfpa_write_qkv(ctypes.byref(cache.c()), cs, n, a, _np_ptr(rs), _np_ptr(rp), rows,
+                                op, _stream(stream)), "tfpa_write_qkv")
 
 
 @dataclass(eq=False)

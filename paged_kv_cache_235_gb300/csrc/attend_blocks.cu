@@ -131,7 +131,7 @@ __device__ __forceinline__ void load_q(const __nv_bfloat16* h, int c, float scal
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int at = KV == kKvBf16 ? (i >> 1) * 8 + 2 * c + (i & 1) : 4 * c + i;
-    const uint4 w = h ? __ldg(qp + at) : make_uint4(0, 0, 0, 0);
+    const uint4 w = h ? *(qp + at) : make_uint4(0, 0, 0, 0);
     q[4 * i] = w.x;
     q[4 * i + 1] = w.y;
     q[4 * i + 2] = w.z;
@@ -302,12 +302,12 @@ __device__ bool produce(const BlocksParams& p, const BlocksRun& run, const int32
   for (int base = u0 / per; base < i1; base += 32) {
     // a lane an entry: the block, and the storage row of its first key
     int b = -1, row0 = 0;
-    if (base + lane < i1) b = __ldg(list + base + lane);
+    if (base + lane < i1) b = *(list + base + lane);
     if (b >= 0 && (int64_t)b * p.block > pos) b = -1;
     if (b >= 0) {
       const int key0 = b * p.block;
       if (run.page_table) {
-        const int pid = __ldg(run.page_table + (key0 >> 8));
+        const int pid = *(run.page_table + (key0 >> 8));
         if ((unsigned)pid < (unsigned)p.num_pages) {
           row0 = (pid * p.hkv + g) * kPage + (key0 & (kPage - 1));
         } else {
@@ -396,9 +396,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
   const int qt = item % qtiles;
   item /= qtiles;
   const int row = item / p.hkv, g = item % p.hkv;
-  int ri = 0;
-  while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
-  const BlocksRun& run = p.runs[ri];
+  const BlocksRun& run = p.runs[run_holding(p.runs, p.nruns, &BlocksRun::row0, row)];
   const int pos = run.pos0 + (row - run.row0);
   const int part0 = ONE ? cta : cta * p.cta_parts;
   const int nparts = ONE ? 1 : min(p.cta_parts, p.parts - part0);
@@ -423,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
   } else {
     uint32_t q[NT][16];
     float sc[NT][2];
-    const float scale = C::kF16 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
+    const float scale = C::kF16 ? p.scale_log2 * *(p.k_scale + g) : p.scale_log2;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int v = 8 * n + gq;
@@ -658,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
   // ---- the CTAs' states, in the cluster's shared memory: each CTA finishes its
   // share of the item's elements, eight lanes one of four dims, a CTA each, so that
   // there is one trip to the other CTAs; pairs first, like the parts
-  const float vs = C::kF16 ? __ldg(p.v_scale + g) : 1.f;
+  const float vs = C::kF16 ? *(p.v_scale + g) : 1.f;
   __syncwarp();
   if (p.ctas > 1) cluster_sync();
   const int j = lane & 7;

@@ -33,9 +33,7 @@ __global__ void __launch_bounds__(kBoundThreads)
   wait_prior_grid();
   const int g = blockIdx.x % p.hkv;
   const int item = blockIdx.x / p.hkv;
-  int ri = 0;
-  while (ri + 1 < p.nruns && p.runs[ri + 1].item0 <= item) ++ri;
-  const BoundsRun& run = p.runs[ri];
+  const BoundsRun& run = p.runs[run_holding(p.runs, p.nruns, &BoundsRun::item0, item)];
   const int block = run.block0 + (item - run.item0);
   const int64_t key0 = (int64_t)block * p.block;
   const int n = (int)min((int64_t)p.block, run.seq_len - key0);
@@ -43,7 +41,7 @@ __global__ void __launch_bounds__(kBoundThreads)
   const int per_page = kPage / p.block, in_page = block % per_page;
   size_t row0, at;
   if (run.page_table) {
-    const int pid = __ldg(run.page_table + page);
+    const int pid = *(run.page_table + page);
     if ((unsigned)pid >= (unsigned)p.num_pages) {
       if (threadIdx.x == 0) flag_error(p.err_flag, kErrBadPage);
       return;
@@ -188,13 +186,13 @@ __device__ __forceinline__ uint32_t sel_prefix(uint32_t x, uint32_t* warp_s, uin
 __device__ __forceinline__ int bound_at(const SelectParams& p, const SelRun& run, int g, int b) {
   const int per_page = kPage / p.block;
   if (!run.page_table) return g * (run.slab_cap / p.block) + b;
-  const int pid = __ldg(run.page_table + b / per_page);
+  const int pid = *(run.page_table + b / per_page);
   if ((unsigned)pid >= (unsigned)p.num_pages) return -1;
   return (pid * p.hkv + g) * per_page + b % per_page;
 }
 // This lane's 16 bytes of it: lanes 0-15 the smallest, 16-31 the largest.
 __device__ __forceinline__ uint4 bound_load(const SelRun& run, int at, int lane) {
-  return __ldg(static_cast<const uint4*>(run.bounds) + (size_t)at * 32 + lane);
+  return *(static_cast<const uint4*>(run.bounds) + (size_t)at * 32 + lane);
 }
 
 // The score of a block from the whole warp's bounds, in 64 bits.  Every block's
@@ -526,9 +524,7 @@ __global__ void __launch_bounds__(kSelThreads, R == 1 ? 4 : 2)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = nc > 1 ? (int)cluster_ctarank() : 0;
   const int item = blockIdx.x / nc, g = item % p.hkv, group = item / p.hkv;
-  int ri = 0;
-  while (ri + 1 < p.nruns && p.runs[ri + 1].group0 <= group) ++ri;
-  const SelRun& run = p.runs[ri];
+  const SelRun& run = p.runs[run_holding(p.runs, p.nruns, &SelRun::group0, group)];
   const int in_run = (group - run.group0) * R;           // first row of the group, in its run
   const int rows = min(R, run.nrows - in_run);
   const int row0 = run.row0 + in_run, pos0 = run.pos0 + in_run;
@@ -546,6 +542,23 @@ __global__ void __launch_bounds__(kSelThreads, R == 1 ? 4 : 2)
       }
     }
   } else {
+    // ---- this CTA's blocks, eight a warp and step
+    const int chunk = ((n + nc - 1) / nc + 7) & ~7;
+    const int lo = min(n, rank * chunk), hi = min(n, lo + chunk);
+    uint32_t most = 0;
+    bool nonfinite = false, may_write = !waits;
+    auto find = [&](int b) { return b < hi ? bound_at(p, run, g, b) : -1; };
+    int b0 = lo + warp * 8;
+    int at = find(b0 + (lane & 7));
+    uint4 w[8];
+    auto load = [&] {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int a = __shfl_sync(0xffffffffu, at, j);
+        w[j] = a >= 0 ? bound_load(run, a, lane) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    load();                                  // under way while the queries are summed
     // ---- the query heads' negative parts (threads 0-127) and positive ones,
     // summed: a head dim a thread, four heads of all rows on their way at once
     static_assert(kSelThreads == 256, "a thread a sum");
@@ -579,21 +592,7 @@ __global__ void __launch_bounds__(kSelThreads, R == 1 ? 4 : 2)
       qf[r][0] = u.x; qf[r][1] = u.y; qf[r][2] = u.z; qf[r][3] = u.w;
       qf[r][4] = v.x; qf[r][5] = v.y; qf[r][6] = v.z; qf[r][7] = v.w;
     }
-    // ---- this CTA's blocks, eight a warp and step
-    const int chunk = ((n + nc - 1) / nc + 7) & ~7;
-    const int lo = min(n, rank * chunk), hi = min(n, lo + chunk);
-    uint32_t most = 0;
-    bool nonfinite = false, may_write = !waits;
-    auto find = [&](int b) { return b < hi ? bound_at(p, run, g, b) : -1; };
-    int b0 = lo + warp * 8;
-    int at = find(b0 + (lane & 7));
     for (; b0 < hi; b0 += kSelWarps * 8) {
-      uint4 w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int a = __shfl_sync(0xffffffffu, at, j);
-        w[j] = a >= 0 ? bound_load(run, a, lane) : make_uint4(0, 0, 0, 0);
-      }
       const int here = __shfl_sync(0xffffffffu, at, lane >> 2);   // the block this lane answers for
       at = find(b0 + kSelWarps * 8 + (lane & 7));
       float s[R][8];
@@ -619,6 +618,7 @@ __global__ void __launch_bounds__(kSelThreads, R == 1 ? 4 : 2)
         const float v = reduce8(s[r], lane);
         if ((lane & 3) == r) mine = v;
       }
+      load();
       const int r = lane & 3;                            // and the row
       if (!may_write) {
         __syncwarp();

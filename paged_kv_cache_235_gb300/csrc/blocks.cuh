@@ -15,14 +15,14 @@ struct Raw8 {
   __device__ __forceinline__ void load(const void* base, size_t row, int t) {
     const uint8_t* b = static_cast<const uint8_t*>(base);
     if (KV == kKvBf16) {
-      w = __ldg(reinterpret_cast<const uint4*>(b + (row * kHeadDim + t * 8) * 2));
+      w = *(reinterpret_cast<const uint4*>(b + (row * kHeadDim + t * 8) * 2));
     } else if (KV == kKvFp8) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(b + row * kHeadDim + t * 8));
+      const uint2 v = *(reinterpret_cast<const uint2*>(b + row * kHeadDim + t * 8));
       w.x = v.x;
       w.y = v.y;
     } else {
-      w.x = __ldg(reinterpret_cast<const uint32_t*>(b + fp4_codes(row) + t * 4));
-      w.y = __ldg(b + fp4_scales(row) + (t >> 1));
+      w.x = *(reinterpret_cast<const uint32_t*>(b + fp4_codes(row) + t * 4));
+      w.y = *(b + fp4_scales(row) + (t >> 1));
     }
   }
   __device__ __forceinline__ void words(uint32_t (&h)[4]) const {

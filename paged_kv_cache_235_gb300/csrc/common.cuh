@@ -45,6 +45,18 @@ __device__ __forceinline__ void allow_next_grid() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// The run, of runs in ascending order of `first`, that holds item `at`: the last
+// whose first item is at or before it.
+template <typename R>
+__device__ __forceinline__ int run_holding(const R* runs, int nruns, int R::*first, int at) {
+  int lo = 0, hi = nruns - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (runs[mid].*first <= at) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
 // Launches `kernel` with programmatic stream serialization (see above).
 template <typename P>
 cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t s,

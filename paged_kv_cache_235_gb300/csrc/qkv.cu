@@ -16,6 +16,8 @@
 // square is added up pair by pair (a thread's 8, then lanes 1, 2, 4, 8
 // apart), and every product, sum, quotient and root is rounded to float32 on
 // its own, so that the stored codes are a function of the inputs alone.
+// (No read-only loads in these kernels and the block kernels: they may start
+// while the kernel before them still writes what they will read.)
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -88,8 +90,8 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 __device__ __forceinline__ void load8f(const float* a, float (&x)[8]) {
-  const float4 u = __ldg(reinterpret_cast<const float4*>(a));
-  const float4 v = __ldg(reinterpret_cast<const float4*>(a) + 1);
+  const float4 u = *(reinterpret_cast<const float4*>(a));
+  const float4 v = *(reinterpret_cast<const float4*>(a) + 1);
   x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
   x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
 }
@@ -189,8 +191,8 @@ __device__ __forceinline__ Turn make_turn(const QkvParams& p, int rpos, int t) {
   u.on = t * 8 < p.rot_dim;
   if (p.interleaved) {                       // dims 2i and 2i + 1: a lane's own
     if (!u.on) return u;
-    const float4 c4 = __ldg(reinterpret_cast<const float4*>(p.rope_cos + row + t * 4));
-    const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.rope_sin + row + t * 4));
+    const float4 c4 = *(reinterpret_cast<const float4*>(p.rope_cos + row + t * 4));
+    const float4 s4 = *(reinterpret_cast<const float4*>(p.rope_sin + row + t * 4));
     const float c[8] = {c4.x, c4.x, c4.y, c4.y, c4.z, c4.z, c4.w, c4.w};
     const float s[8] = {-s4.x, s4.x, -s4.y, s4.y, -s4.z, s4.z, -s4.w, s4.w};
     u.c = dims_of(c);
@@ -253,7 +255,7 @@ __device__ __forceinline__ void store_kv(const QkvParams& p, const WriteRun& run
   unpack8(vv, vf);
   uint8_t* kb = static_cast<uint8_t*>(run.k_dst);
   uint8_t* vb = static_cast<uint8_t*>(run.v_dst);
-  const float gk = __ldg(p.k_scale + g), gv = __ldg(p.v_scale + g);
+  const float gk = *(p.k_scale + g), gv = *(p.v_scale + g);
   if (KV == kKvFp4) {
     const size_t codes = fp4_codes(dst_row) + t * 4, scales = fp4_scales(dst_row) + (t >> 1);
     uint32_t ks, vs;
@@ -295,8 +297,7 @@ __global__ void __launch_bounds__(H > 1 ? 256 : 64, H > 1 ? 2 : 8)
   left -= unit;
   int row = unit / units;
   unit -= row * units;
-  int ri = 0;
-  while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
+  int ri = run_holding(p.runs, p.nruns, &WriteRun::row0, row);
 
   uint4 in[H], vin[HK];
   Turn turn;
@@ -316,22 +317,22 @@ __global__ void __launch_bounds__(H > 1 ? 256 : 64, H > 1 ? 2 : 8)
         h0 * kHeadDim + t * 8;
 #pragma unroll
     for (int h = 0; h < H; ++h)
-      in[h] = h < n ? __ldg(reinterpret_cast<const uint4*>(from + h * kHeadDim))
+      in[h] = h < n ? *(reinterpret_cast<const uint4*>(from + h * kHeadDim))
                     : make_uint4(0, 0, 0, 0);
     if (!is_q) {
       const __nv_bfloat16* vp = p.v + (size_t)row * p.v_stride + h0 * kHeadDim + t * 8;
 #pragma unroll
       for (int h = 0; h < HK; ++h)
-        vin[h] = h < n ? __ldg(reinterpret_cast<const uint4*>(vp + h * kHeadDim))
+        vin[h] = h < n ? *(reinterpret_cast<const uint4*>(vp + h * kHeadDim))
                        : make_uint4(0, 0, 0, 0);
     }
     if (fresh) {
       while (ri + 1 < p.nruns && p.runs[ri + 1].row0 <= row) ++ri;
       const WriteRun& run = p.runs[ri];
       pos = run.pos0 + (row - run.row0);
-      pid = run.page_table ? __ldg(run.page_table + (pos >> 8)) : 0;
+      pid = run.page_table ? *(run.page_table + (pos >> 8)) : 0;
       if (p.rope_cos) {
-        const int rpos = p.rope_pos ? __ldg(p.rope_pos + row) : pos;
+        const int rpos = p.rope_pos ? *(p.rope_pos + row) : pos;
         on_table = (unsigned)rpos < (unsigned)p.rope_n;    // the whole warp's row
         if (on_table)
           turn = make_turn(p, rpos, t);
