@@ -146,10 +146,10 @@ struct SelShared {
                              // scores, between two uses of the histogram
     float q32[4][256];       // and before its first use, of each row
   };
-  uint32_t most[kMaxCluster * kSelWarps];   // largest |bound| (bf16 bits; ~0: a score was no
-                                            // number), of every warp of the cluster
+  uint4 seen[kMaxCluster * kSelWarps];      // what every warp of the cluster has seen: the largest
+                                            // |bound| (bf16 bits; ~0: a score was no number), the
+                                            // smallest and largest key, taken << 16 | free blocks
   uint32_t warp_s[kSelWarps];
-  uint32_t warp_lo[kSelWarps], warp_hi[kSelWarps];
   uint32_t pick[3];
   uint32_t count;
   uint32_t border;
@@ -227,8 +227,8 @@ __device__ __forceinline__ float reduce8(const float (&v)[8], int lane) {
 // largest, what is near it, and the list.  A thread takes eight consecutive keys
 // of a round of 2,048, and keeps them in registers where one round is all.
 __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bfloat16* q, int g,
-                       int n, int ranks, float q1, uint32_t* key32, uint64_t* key64,
-                       SelShared& sh, int32_t* out) {
+                       int n, bool every, int ranks, float q1, uint32_t* key32,
+                       uint64_t* key64, SelShared& sh, int32_t* out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kRound = 8 * kSelThreads;
   const bool one = n <= kRound;
@@ -254,42 +254,32 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
     }
     loaded = true;
   };
-  // ---- how many are free to choose from, and their range
-  uint32_t counts = 0;                   // taken << 16 | free (18,432 at most)
-  uint32_t kmin = 0xFFFFFFFFu, kmax = 0;
-  rounds([&](int) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      counts += k[i] == kTaken ? 0x10000u : k[i] != kAbsent ? 1u : 0u;
-      kmin = min(kmin, k[i] - 1u);       // (kAbsent wraps to the largest)
-      kmax = max(kmax, k[i] == kTaken ? 0u : k[i]);
-    }
-  });
-  kmin = __reduce_min_sync(0xffffffffu, kmin);
-  kmax = __reduce_max_sync(0xffffffffu, kmax);
-  counts = __reduce_add_sync(0xffffffffu, counts);
-  if (lane == 0) {
-    sh.warp_lo[warp] = kmin;
-    sh.warp_hi[warp] = kmax;
-    sh.warp_s[warp] = counts;
-  }
-  if (tid == 0) sh.count = 0;
   auto clear = [&] {
     reinterpret_cast<uint4*>(sh.hist)[tid] = make_uint4(0, 0, 0, 0);
     reinterpret_cast<uint4*>(sh.hist)[tid + kSelThreads] = make_uint4(0, 0, 0, 0);
   };
   static_assert(kBins == 8 * kSelThreads, "histogram");
-  clear();
-  __syncthreads();
-  uint32_t ntaken = 0, nfree = 0;
-#pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    kmin = min(kmin, sh.warp_lo[w]);
-    kmax = max(kmax, sh.warp_hi[w]);
-    ntaken += sh.warp_s[w] >> 16;
-    nfree += sh.warp_s[w] & 0xFFFFu;
+  // ---- how many are free to choose from, and their range
+  uint32_t ntaken = 0, nfree = 0, kmin = 0xFFFFFFFFu, kmax = 0, most = 0;
+  if (!every) {
+    clear();
+    if (tid == 0) sh.count = 0;
+    uint32_t counts = 0;                 // taken << 16 | free (18,432 at most)
+    for (int i = lane; i < ranks * kSelWarps; i += 32) {
+      const uint4 v = sh.seen[i];
+      most = max(most, v.x);
+      kmin = min(kmin, v.y);
+      kmax = max(kmax, v.z);
+      counts += v.w;
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    kmin = __reduce_min_sync(0xffffffffu, kmin);
+    kmax = __reduce_max_sync(0xffffffffu, kmax);
+    counts = __reduce_add_sync(0xffffffffu, counts);
+    ntaken = counts >> 16;
+    nfree = counts & 0xFFFFu;
+    __syncthreads();
   }
-  kmin += 1u;
   const uint32_t want = min(nfree, p.nsel > (int)ntaken ? p.nsel - ntaken : 0u);
   uint32_t in_from = 0;                  // keys from here on are in, but for near ones
   float low = 0.f, top = 0.f;
@@ -297,13 +287,19 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
   if (want == 0) {
     in_from = kTaken;
   } else if (want < nfree) {
-    uint32_t most = lane < ranks * kSelWarps ? sh.most[lane] : 0u;
-    if (lane + 32 < ranks * kSelWarps) most = max(most, sh.most[lane + 32]);
-    most = __reduce_max_sync(0xffffffffu, most);
+    // ---- how far a float32 score may be off: its roundings' sum |q| |bound|, the
+    // sums over G heads (all of one sign), 8 products and sums of a lane, 5 of the
+    // reduction, 2^-24 each; e is twice that.  The exact want-th largest score is
+    // within e of the one found in float32, so a score beyond that by more than 2 e
+    // is decided; the others are near.
+    const float e = (float)(16 + p.group) * 0x1p-23f * q1 * __uint_as_float(most << 16) + 1e-40f;
+    all = most >= 0x7F80u || !(e < INFINITY);
+    bool decided = false;
     // ---- the want-th largest key
     const uint32_t differ = kmin ^ kmax;
     int shift = differ ? 32 - __clz(differ) : 0;         // bits that are not the same in all
     uint32_t prefix = shift == 32 ? 0u : kmin >> shift << shift;
+    const uint32_t first_high = shift == 32 ? 0u : ~0u << shift;
     uint32_t rest = want;
     while (shift > 0) {
       const int bits = min(shift, 11);
@@ -339,6 +335,55 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
       prefix |= sh.pick[0] << shift;
       rest = sh.pick[1];
       const uint32_t same = sh.pick[2];
+      // Few keys in the border's bin and the two beside it, and the near ones among
+      // them: one warp settles it.
+      const int bin = (int)sh.pick[0];
+      const uint32_t up = bin + 1 < kBins ? sh.hist[bin + 1] : 0u;
+      const uint32_t down = bin > 0 ? sh.hist[bin - 1] : 0u;
+      if (high == first_high && shift > 0 && !all && same + up + down <= 32) {
+        rounds([&](int b) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int at = (int)((k[i] >> shift) & (kBins - 1)) - bin;
+            if (is_score(k[i]) && at >= -1 && at <= 1)
+              sh.near_k[atomicAdd(&sh.count, 1u)] = k[i];
+          }
+        });
+        __syncthreads();
+        if (warp == 0) {
+          const uint32_t cnt = same + up + down, nth = rest + up;
+          const bool there = (uint32_t)lane < cnt;
+          const uint32_t mine = there ? (uint32_t)sh.near_k[lane] : 0u;
+          uint32_t more = 0, equal = 0;
+          for (uint32_t i = 0; i < cnt; ++i) {
+            const uint32_t other = __shfl_sync(0xffffffffu, mine, i);
+            more += other > mine;
+            equal += other == mine;
+          }
+          const unsigned who =
+              __ballot_sync(0xffffffffu, there && more < nth && nth <= more + equal);
+          const uint32_t border = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
+          const float at = value32(border), s = value32(mine);
+          const float t = at + 2.125f * e, l = at - 2.125f * e;
+          const uint32_t in = __popc(__ballot_sync(0xffffffffu, there && s > t));
+          const uint32_t near = __popc(__ballot_sync(0xffffffffu, there && s <= t && s >= l));
+          // (bins beyond the first and the last of the range are empty)
+          const uint32_t edge = prefix;
+          const bool inside = (bin == 0 || order32(l) >= edge - (1u << shift)) &&
+                              (bin == kBins - 1 || order32(t) - edge < (2u << shift));
+          if (lane == 0) {
+            sh.border = border;
+            sh.pick[0] = inside && near == nth - in;
+            sh.pick[1] = order32(l);
+            sh.count = 0;
+          }
+        }
+        __syncthreads();
+        prefix = sh.border;
+        decided = sh.pick[0];
+        in_from = sh.pick[1];
+        break;
+      }
       if (shift > 0 && same <= kNear) {
         // few share the leading bits: the rest-th largest of them directly
         const uint32_t lead = ~0u << shift;
@@ -369,14 +414,8 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
         __syncthreads();
       }
     }
-    // ---- who is in, who is out, and who is too near to tell.  A float32 score is
-    // off by its roundings' sum |q| |bound|: the sums over G heads (all of one
-    // sign), 8 products and sums of a lane, 5 of the reduction, 2^-24 each; e is
-    // twice that.  The exact want-th largest is within e of the one found, so a
-    // score beyond it by more than 2 e is decided.
-    const float e = (float)(16 + p.group) * 0x1p-23f * q1 * __uint_as_float(most << 16) + 1e-40f;
+    // ---- else who is in, who is out, and who is too near to tell
     const float at = value32(prefix);
-    all = most >= 0x7F80u || !(e < INFINITY);
     top = at + 2.125f * e;
     low = at - 2.125f * e;
     auto is_near = [&](uint32_t x) {
@@ -385,15 +424,17 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
       return all || (s >= low && s <= top);
     };
     uint32_t both = 0;                   // in << 16 | near
-    rounds([&](int) {
+    if (!decided) rounds([&](int) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         both += is_near(k[i]) ? 1u : is_score(k[i]) && value32(k[i]) > top ? 0x10000u : 0u;
     });
-    uint32_t total;
-    sel_prefix(both, sh.warp_s, total);
+    uint32_t total = want << 16;
+    if (!decided) sel_prefix(both, sh.warp_s, total);
     const uint32_t near = total & 0xFFFFu, need = want - (total >> 16);
-    if (near == need) {
+    if (decided) {
+      // in_from says it
+    } else if (near == need) {
       in_from = order32(low);
     } else {
       // ---- the near ones' exact scores
@@ -546,6 +587,7 @@ __global__ void __launch_bounds__(kSelThreads, R == 1 ? 4 : 2)
     const int chunk = ((n + nc - 1) / nc + 7) & ~7;
     const int lo = min(n, rank * chunk), hi = min(n, lo + chunk);
     uint32_t most = 0;
+    uint32_t kmin = 0xFFFFFFFFu, kmax = 0, counts = 0;     // of this lane's row
     bool nonfinite = false, may_write = !waits;
     auto find = [&](int b) { return b < hi ? bound_at(p, run, g, b) : -1; };
     int b0 = lo + warp * 8;
@@ -634,10 +676,14 @@ __global__ void __launch_bounds__(kSelThreads, R == 1 ? 4 : 2)
             flag_error(p.err_flag, kErrBadPage);
           } else if (b < p.sink || b > last - p.recent) {
             key = kTaken;
+            counts += 0x10000u;
           } else {
             const bool number = fabsf(mine) < INFINITY;
             nonfinite |= !number;
             key = order32(number ? mine : 0.f);
+            kmin = min(kmin, key);
+            kmax = max(kmax, key);
+            ++counts;
           }
           if (waits)
             st_cluster_u32(mapa_shared(smem_u32(key32 + b), r), key);
@@ -650,12 +696,18 @@ __global__ void __launch_bounds__(kSelThreads, R == 1 ? 4 : 2)
     if (!may_write) cluster_wait();
     most = max(most & 0xFFFFu, most >> 16);
     most = __reduce_max_sync(0xffffffffu, nonfinite ? 0xFFFFu : most);
+#pragma unroll
+    for (int d = 4; d < 32; d *= 2) {        // the lanes of one row
+      kmin = min(kmin, __shfl_xor_sync(0xffffffffu, kmin, d));
+      kmax = max(kmax, __shfl_xor_sync(0xffffffffu, kmax, d));
+      counts += __shfl_xor_sync(0xffffffffu, counts, d);
+    }
     if (lane < rows) {
-      uint32_t* slot = &sh.most[rank * kSelWarps + warp];
+      uint4* slot = &sh.seen[rank * kSelWarps + warp];
       if (waits)
-        st_cluster_u32(mapa_shared(smem_u32(slot), lane), most);
+        st_cluster128(mapa_shared(smem_u32(slot), lane), most, kmin, kmax, counts);
       else
-        *slot = most;
+        *slot = make_uint4(most, kmin, kmax, counts);
     }
   }
   __syncwarp();
@@ -680,7 +732,7 @@ __global__ void __launch_bounds__(kSelThreads, R == 1 ? 4 : 2)
   }
   const int row = row0 + rank;
   choose(p, run, p.q + ((size_t)row * p.hq + (size_t)g * p.group) * kHeadDim, g,
-         (pos0 + rank) / p.block + 1, nc, q1, key32, key64, sh,
+         (pos0 + rank) / p.block + 1, every, nc, q1, key32, key64, sh,
          p.blocks + ((size_t)row * p.hkv + g) * p.nsel);
 }
 

@@ -1642,6 +1642,8 @@ extern "C" int tfpa_rope_table(const tfpa_rope_spec* spec, int64_t first, int32_
   if (first < 0 || first + (int64_t)n > kMaxRopePos || first > kMaxRopePos) return TFPA_ERANGE;
   if (n == 0) return TFPA_OK;
   if ((e = check_device())) return e;
+  const int nsm = sm_count();
+  if (nsm < 1) return TFPA_ECUDA;
   TableParams p{};
   p.cos = cos;
   p.sin = sin;
@@ -1650,9 +1652,8 @@ extern "C" int tfpa_rope_table(const tfpa_rope_spec* spec, int64_t first, int32_
   p.first = first;
   p.n = n;
   p.attn_scale = (float)spec->attn_scale;
-  p.steps = n >= 32768 ? 8 : 1;     // the threads of 8 a row still cover the GPU twice
   record(13, 0, n, 0, n, 0, 0, 0);
-  return dry_run() ? TFPA_OK : to_err(launch_rope_table(p, stream));
+  return dry_run() ? TFPA_OK : to_err(launch_rope_table(p, nsm, stream));
 }
 
 // ------------------------------------------------------------ a projection's rows
@@ -1907,8 +1908,8 @@ int select_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const t
     p.recent = recent;
     // Up to four rows of a run share the reads of the bounds; a cluster has a CTA
     // for each of them to choose in.  More CTAs while the GPU holds them (four a
-    // SM, two with four rows, by their registers) and each has 64 blocks, eight a
-    // warp.
+    // SM, two with four rows, by their registers) and each has 32 blocks, eight a
+    // warp of four (313 blocks: eight CTAs 7.6 us, four 8.8).
     p.rows_per = longest >= 3 ? 4 : longest;
     for (int i = 0; i < nr; ++i) {
       p.runs[i].group0 = p.groups;
@@ -1918,7 +1919,7 @@ int select_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const t
     p.cluster = p.rows_per;
     const int64_t at_once = (p.rows_per == 1 ? 4 : 2) * nsm;
     while (p.cluster < 8 && (int64_t)p.groups * c->hkv * p.cluster * 2 <= at_once &&
-           p.cap / (p.cluster * 2) >= 64)
+           p.cap / (p.cluster * 2) >= 32)
       p.cluster *= 2;
     record(16, base, nrows, nr, p.groups * c->hkv, p.groups * c->hkv * p.cluster,
            (int64_t)base * c->hq * kHeadDim, (int64_t)base * c->hkv * nsel);

@@ -330,7 +330,6 @@ struct TableParams {
   int64_t first;              // position of the first row
   int32_t n;
   int32_t half;               // frequencies: rot_dim / 2
-  int32_t steps;              // rows a thread takes
   float attn_scale;
 };
 
@@ -440,7 +439,7 @@ struct BlocksParams {
 };
 
 // Launchers (defined next to their kernels).
-cudaError_t launch_rope_table(const TableParams& p, cudaStream_t s);
+cudaError_t launch_rope_table(const TableParams& p, int sms, cudaStream_t s);
 cudaError_t launch_write_qkv(const QkvParams& p, int kv, cudaStream_t s);
 cudaError_t launch_key_bounds(const BoundsParams& p, int kv, cudaStream_t s);
 cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t s);

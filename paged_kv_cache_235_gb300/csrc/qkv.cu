@@ -28,6 +28,7 @@ namespace tfpa {
 
 namespace {
 constexpr int kTableThreads = 256;
+constexpr int kTableBlocks = 5;             // of a SM
 
 // sin and cos of |x| <= pi / 4 by their Taylor polynomials, cut where the next
 // term is below 2^-29 (x^11 / 11! and x^12 / 12!); with the few roundings of the
@@ -46,25 +47,31 @@ __device__ __forceinline__ void sin_cos(float x, float& sn, float& cs) {
 }
 }  // namespace
 
-// A thread keeps four frequencies and takes p.steps rows of them (indexing the
-// launch parameters by lane costs a pass through the constant cache each).
-__global__ void __launch_bounds__(kTableThreads)
+// A thread keeps four frequencies and walks over rows, the whole grid at a time:
+// a position's fractions are the last one's and a step's (indexing the launch
+// parameters by lane costs a pass through the constant cache each).
+__global__ void __launch_bounds__(kTableThreads, kTableBlocks)
     rope_table_kernel(const __grid_constant__ TableParams p) {
   allow_next_grid();
   wait_prior_grid();
   const int quads = p.half / 4, rows = kTableThreads / quads;
   const int r = threadIdx.x / quads, f0 = (threadIdx.x - r * quads) * 4;
   if (r >= rows) return;
-  uint64_t f[4];
+  int64_t row = (int64_t)blockIdx.x * rows + r;
+  const int64_t step = (int64_t)gridDim.x * rows;
+  uint64_t at[4], more[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) f[j] = p.turns[f0 + j];
-  int64_t row = (int64_t)blockIdx.x * rows * p.steps + r;
-  for (int i = 0; i < p.steps && row < p.n; ++i, row += rows) {
-    const uint64_t t = (uint64_t)(p.first + row);
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t f = p.turns[f0 + j];
+    at[j] = f * (uint64_t)(p.first + row);
+    more[j] = f * (uint64_t)step;
+  }
+  for (; row < p.n; row += step) {
     float c[4], s[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint64_t turn = t * f[j];
+      const uint64_t turn = at[j];
+      at[j] += more[j];
       // the nearest quarter turn, and what is left of it (at most an eighth) in
       // radians; the low word counts where the angle itself is small
       const uint32_t quarter = ((uint32_t)(turn >> 32) + (1u << 29)) >> 30;
@@ -77,9 +84,9 @@ __global__ void __launch_bounds__(kTableThreads)
       c[j] = p.attn_scale * (quarter == 1 || quarter == 2 ? -u : u);
       s[j] = p.attn_scale * (quarter & 2 ? -v : v);
     }
-    const size_t at = (size_t)row * p.half + f0;
-    *reinterpret_cast<float4*>(p.cos + at) = make_float4(c[0], c[1], c[2], c[3]);
-    *reinterpret_cast<float4*>(p.sin + at) = make_float4(s[0], s[1], s[2], s[3]);
+    const size_t to = (size_t)row * p.half + f0;
+    *reinterpret_cast<float4*>(p.cos + to) = make_float4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<float4*>(p.sin + to) = make_float4(s[0], s[1], s[2], s[3]);
   }
 }
 
@@ -394,10 +401,10 @@ __global__ void __launch_bounds__(H > 1 ? 256 : 64, H > 1 ? 2 : 8)
   }
 }
 
-cudaError_t launch_rope_table(const TableParams& p, cudaStream_t s) {
-  const int64_t rows = (int64_t)(kTableThreads / (p.half / 4)) * p.steps;
-  return launch_pdl(rope_table_kernel, dim3((unsigned)((p.n + rows - 1) / rows)),
-                    dim3(kTableThreads), 0, s, p);
+cudaError_t launch_rope_table(const TableParams& p, int sms, cudaStream_t s) {
+  const int rows = kTableThreads / (p.half / 4);
+  const int grid = (int)min((int64_t)kTableBlocks * sms, ((int64_t)p.n + rows - 1) / rows);
+  return launch_pdl(rope_table_kernel, dim3(grid), dim3(kTableThreads), 0, s, p);
 }
 
 namespace {

@@ -221,3 +221,82 @@ def test_no_thread_leaves_its_role_alone(name):
         src = strip(f.read())
     bad = [(line, s) for line, s, h in statements(src) if re.search(r"\bgoto\b", s) and alone(s, h)]
     assert not bad, bad
+
+
+WAITS = ["attend_blocks.cu", "blocks.cu"]
+
+
+@pytest.mark.parametrize("name", WAITS)
+def test_a_warp_waits_as_one(name):
+    """No lane waits, or leaves a loop, on an answer of its own: every wait is a whole warp's."""
+    from tests.test_wait_forms import CSRC, WAIT, statements, strip
+    with open(os.path.join(CSRC, name)) as f:
+        src = strip(f.read())
+    assert not [(line, s) for line, s, _ in statements(src) if WAIT.search(s)]
+    waits = [s for _, s, _ in statements(src) if "warp_wait" in s]
+    assert len(waits) == (3 if name == "attend_blocks.cu" else 0), waits
+
+
+def test_loads_in_flight_land_before_a_block_ends():
+    from tests.test_wait_forms import CSRC, strip
+    with open(os.path.join(CSRC, "attend_blocks.cu")) as f:
+        src = " ".join(strip(f.read()).split())
+    assert src.count("if (sh.lost) let_copies_land();") == 1
+
+
+# ---------------------------------------------------------------- host memory
+def child(name):
+    """As in tests/test_host_memory.py: a process whose address space leaves no room for a call's row groups."""
+    import resource
+    import numpy as np
+    n = 8_000_000
+    rs, rp = np.zeros(n, np.int32), np.zeros(n, np.int32)
+    rp[1::2] = 5                                                 # no two rows in one group
+    c = B.Cache("bf16", 8, 2, FAKE, FAKE, num_pages=64)
+    segs = [B.Seg(1000, page_table=FAKE)]
+    rows = lambda h, p: Rows(n, h, p)  # noqa: E731
+    q, k, v, out = rows(8, FAKE), rows(2, FAKE), rows(2, FAKE), rows(8, 1 << 50)
+    blocks, bnd = Plane(n, 2, 4, ptr=FAKE), B.Bounds(64, FAKE)
+    calls = {
+        "qkv": lambda: B.tfpa_write_qkv(c, segs, q, k, v, out, rs, rp, stream=0),
+        "bounds": lambda: B.tfpa_key_bounds(c, segs, bnd, rs, rp, stream=0),
+        "select": lambda: B.tfpa_select_blocks(c, segs, bnd, FAKE, rs, rp, blocks, stream=0),
+        "attend": lambda: B.tfpa_decode_blocks(c, segs, FAKE, rs, rp, blocks, 64, 0.1, FAKE, stream=0),
+    }
+    with open("/proc/self/status") as f:
+        size = next(int(x.split()[1]) for x in f if x.startswith("VmSize")) * 1024
+    with B.record_launches() as rec:
+        resource.setrlimit(resource.RLIMIT_AS, (size + (16 << 20), resource.RLIM_INFINITY))
+        try:
+            calls[name]()
+            print("done")
+        except B.TfpaError as e:
+            print("code", e.code, len(rec), B.strerror(e.code))
+        resource.setrlimit(resource.RLIMIT_AS, (resource.RLIM_INFINITY, resource.RLIM_INFINITY))
+
+
+@pytest.mark.parametrize("name", ["qkv", "bounds", "select", "attend"])
+def test_host_memory_that_runs_out_is_an_error_code(name):
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", f"from tests.test_blocks_host import child; child({name!r})"], cwd=root, capture_output=True,
+                       text=True, timeout=120, env=dict(os.environ, OPENBLAS_NUM_THREADS="1", OMP_NUM_THREADS="1"))
+    assert r.returncode == 0, (r.returncode, r.stderr[-600:])
+    assert r.stdout.split()[:3] == ["code", str(B.TFPA_ENOMEM), "0"], r.stdout
+
+
+def test_parts_of_a_list_follow_from_its_length_and_ctas_from_the_batch():
+    """A part for every 128 keys, up to eight; a CTA takes as few as let the launch have four CTAs a SM (152 SMs here)."""
+    segs = [B.Seg(60000, page_table=3 * FAKE)]
+    c = _cache(num_pages=4096)
+
+    def grids(rows, nsel, block=64):
+        with B.record_launches() as rec:
+            B.tfpa_decode_blocks(c, segs, FAKE, [0] * rows, list(range(50000, 50000 + rows)), Plane(rows, 8, nsel, ptr=FAKE), block, 0.1, FAKE,
+                                 stream=0)
+        return [(r["items"], r["grid"]) for r in rec]
+    assert grids(1, 1) == [(8, 8)] and grids(1, 2) == [(8, 8)] and grids(1, 3) == [(8, 16)] and grids(1, 1, 256) == [(8, 16)]
+    assert grids(1, 64) == [(8, 64)] and grids(8, 64) == [(64, 512)]
+    assert grids(16, 64) == [(128, 512)] and grids(32, 64) == [(256, 512)] and grids(100, 64) == [(800, 800)]
+    assert grids(32, 9) == [(256, 512)]                          # five parts: four in one CTA, one in the other

@@ -559,3 +559,81 @@ def test_calls_of_several_threads_at_once():
         check_choice(c, b, q, rs, rp, 8, 0, 1, got=lists)
         o, l = check_attend(c, q, rs, rp, lists, 64)
         assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("kv", KVS)
+@pytest.mark.parametrize("hq,hkv,rows", [(8, 2, 1), (32, 2, 2), (8, 2, 90)])
+def test_long_lists(kv, hq, hkv, rows):
+    """Dozens of key stages a part, so that every buffer is filled again and again; rows enough that a CTA takes several
+    parts of a list."""
+    c = LongCase(kv, [30000, 9000], [True, False], hq, hkv, 72)
+    rs, rp = last_rows(c.lengths, [rows, rows])
+    nsel = 300 if rows < 10 else 60
+    check_attend(c, c.q(len(rs)), rs, rp, random_lists(c, rs, rp, nsel, 64, 73), 64)
+    assert int(c.err.item()) == 0
+
+
+@pytest.mark.parametrize("kv", KVS)
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (32, 2), (6, 1)])
+def test_a_row_is_the_same_bytes_whatever_parts_a_cta_takes(kv, hq, hkv):
+    """Batches of 1 to 600 rows: one, two, four or eight parts of a list in a CTA, for lists of two to eight parts."""
+    c = LongCase(kv, [4000, 2000], [True, False], hq, hkv, 74)
+    rs, rp = last_rows(c.lengths, [300, 300])
+    q = c.q(600)
+    for nsel in (3, 11, 40):
+        lists = random_lists(c, rs, rp, nsel, 64, 75)
+        out, lse = run_attend(c, q, rs, rp, lists, 64)
+        for n in (1, 25, 50, 120, 250):
+            o, l = run_attend(c, q[:n].contiguous(), rs[:n], rp[:n], lists[:n].contiguous(), 64)
+            assert torch.equal(o.view(torch.int16), out[:n].view(torch.int16)) and torch.equal(l, lse[:n]), (nsel, n)
+
+
+@pytest.mark.parametrize("block", [64, 256])
+def test_rows_of_a_run_share_their_reads(block):
+    """Runs of 2, 3, 4, 5 and 9 rows that cross a block's border, in one call and row by row: the same blocks."""
+    lengths = [4099, 4098, 4100, 8193, 4104]
+    c = LongCase("bf16", lengths, [True, False, True, True, True], 8, 2, 76)
+    b = random_bounds(c, block, 77)
+    rs, rp = last_rows(lengths, [2, 3, 4, 5, 9])
+    q = c.q(len(rs))
+    got = torch.empty(len(rs), 2, 12, dtype=torch.int32, device="cuda")
+    B.tfpa_select_blocks(c.cache, c.segs, b, q, rs, rp, got, sink=1, recent=2)
+    check_choice(c, b, q, rs, rp, 12, 1, 2, got=got)
+    for r in range(len(rs)):
+        one_row = torch.empty(1, 2, 12, dtype=torch.int32, device="cuda")
+        B.tfpa_select_blocks(c.cache, c.segs, b, q[r:r + 1].contiguous(), rs[r:r + 1], rp[r:r + 1], one_row, sink=1, recent=2)
+        assert torch.equal(one_row[0], got[r])
+
+
+def test_a_prompt_chunk_over_its_own_blocks():
+    """Hundreds of rows of one run, each with blocks of its own: bounds, choice and attention."""
+    c = LongCase("fp8", [2500], [True], 8, 2, 78)
+    b = bound_store(c, 64)
+    B.tfpa_key_bounds(c.cache, c.segs, b, np.zeros(2500), np.arange(2500))
+    rs, rp = np.zeros(700, np.int32), np.arange(1800, 2500, dtype=np.int32)
+    q = c.q(700)
+    lists = torch.empty(700, 2, 9, dtype=torch.int32, device="cuda")
+    B.tfpa_select_blocks(c.cache, c.segs, b, q, rs, rp, lists, sink=1, recent=2)
+    pick = np.arange(0, 700, 29)
+    check_choice(c, b, q[torch.from_numpy(pick).cuda()].contiguous(), rs[pick], rp[pick], 9, 1, 2,
+                 got=lists[torch.from_numpy(pick).cuda()])
+    check_attend(c, q, rs, rp, lists, 64)
+
+
+def test_after_an_eviction_the_bounds_are_taken_anew():
+    """tfpa_evict_kv moves keys: with the bounds of all rows taken again, blocks and attention are those of the cut stream."""
+    c = LongCase("bf16", [2000], [True], 8, 2, 79)
+    b = bound_store(c, 64)
+    cap = 2048
+    mass = torch.rand(1, 2, cap, generator=c.g, device="cuda")
+    moves = B.make_moves(1, 2, cap)
+    B.tfpa_evict_kv(c.cache, c.segs, [900], mass, moves, sink=4, recent=64)
+    c.lengths, c.segs = [900], [B.Seg(900, page_table=c.segs[0].page_table)]
+    B.tfpa_key_bounds(c.cache, c.segs, b, np.zeros(900), np.arange(900))
+    for blk in range(15):
+        assert torch.equal(bound_view(c, b, 0, blk).double(), exact_bounds(c, 0, blk, 64))
+    q, rs, rp = c.q(1), [0], [899]
+    lists = torch.empty(1, 2, 5, dtype=torch.int32, device="cuda")
+    B.tfpa_select_blocks(c.cache, c.segs, b, q, rs, rp, lists, sink=1, recent=1)
+    check_choice(c, b, q, rs, rp, 5, 1, 1, got=lists)
+    check_attend(c, q, rs, rp, lists, 64)
