@@ -238,6 +238,12 @@ __device__ __forceinline__ void add_pv(uint32_t sb, int r0, int lane, const uint
   }
 }
 
+// Lanes of a waiting state.
+template <int NT>
+__host__ __device__ constexpr int waiting_lanes(int group) {
+  return NT == 1 && group <= 4 ? 16 : 32;
+}
+
 // Two states' common maximum goes into m; the factor that this one's sums take.
 __device__ __forceinline__ float toward(float& m, float other) {
   const float M = fmaxf(m, other);
@@ -247,28 +253,33 @@ __device__ __forceinline__ float toward(float& m, float other) {
 }
 
 // A warp's state in shared memory, [float4 of its fragments][lane], its maxima and
-// sums behind them.
+// sums behind them.  `lanes`: 32, or 16 where the vectors are four at most (a
+// lane's columns are vectors 2c and 2c + 1): `at` is then -1 in the others.
 template <int NT>
 constexpr int kStateBytes = (8 * NT + NT) * 32 * 16;
 template <int NT>
-__device__ __forceinline__ void put_state(float4* to, int lane, const float (&o)[NT][8][4],
-                                          const float (&m)[NT][2], const float (&l)[NT][2]) {
+__device__ __forceinline__ void put_state(float4* to, int lanes, int at,
+                                          const float (&o)[NT][8][4], const float (&m)[NT][2],
+                                          const float (&l)[NT][2]) {
+  if (at < 0) return;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int t = 0; t < 8; ++t)
-      to[(8 * n + t) * 32 + lane] = make_float4(o[n][t][0], o[n][t][1], o[n][t][2], o[n][t][3]);
-    to[(8 * NT + n) * 32 + lane] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
+      to[(8 * n + t) * lanes + at] = make_float4(o[n][t][0], o[n][t][1], o[n][t][2], o[n][t][3]);
+    to[(8 * NT + n) * lanes + at] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
   }
 }
 // The state there and this one, in this one.  (Products and sums rounded on their
 // own: the result is the same whichever of the two is there.)
 template <int NT>
-__device__ __forceinline__ void take_state(const float4* from, int lane, float (&o)[NT][8][4],
-                                           float (&m)[NT][2], float (&l)[NT][2]) {
+__device__ __forceinline__ void take_state(const float4* from, int lanes, int at,
+                                           float (&o)[NT][8][4], float (&m)[NT][2],
+                                           float (&l)[NT][2]) {
+  if (at < 0) return;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const float4 ml = from[(8 * NT + n) * 32 + lane];
+    const float4 ml = from[(8 * NT + n) * lanes + at];
     float om[2] = {ml.x, ml.y};
     const float ol[2] = {ml.z, ml.w};
     float a[2], b[2];
@@ -281,7 +292,7 @@ __device__ __forceinline__ void take_state(const float4* from, int lane, float (
     }
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-      const float4 x = from[(8 * n + t) * 32 + lane];
+      const float4 x = from[(8 * n + t) * lanes + at];
       const float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -400,7 +411,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
   const int pos = run.pos0 + (row - run.row0);
   const int part0 = ONE ? cta : cta * p.cta_parts;
   const int nparts = ONE ? 1 : min(p.cta_parts, p.parts - part0);
-  float4* pending = reinterpret_cast<float4*>(ring + C::kRing);   // [level][NT * 8 + NT][lane]
+  // the states that wait, [level], behind the ring and the fold where that is there too
+  constexpr bool kInStage = C::kStageBytes >= 2 * kStateBytes<NT>;
+  float4* pending =
+      reinterpret_cast<float4*>(ring + C::kRing + (kInStage ? 0 : 2 * kStateBytes<NT>));
   // the CTA's state, once the ring is done
   float* mine = reinterpret_cast<float*>(ring + (ONE ? 4 * kStateBytes<NT> : 0));
   const int vecs = min(kVecs, p.group - qt * kVecs);     // query vectors of this item
@@ -477,26 +491,46 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
             }
           }
           const bool see0 = key0 + key_of<KV>(gq) <= pos, see1 = key0 + key_of<KV>(gq + 8) <= pos;
-          // ---- online softmax over the tile's keys, a column a vector
-          uint32_t pb[NT][2];
-          bool resc = false;
-          float al[NT][2];
+          // ---- online softmax over the tile's keys, a column a vector.  The running
+          // maximum moves by 2^8 at least, which after a part's first keys is rare:
+          // one vote asks whether some score passes it by that.
+          bool passes = false;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               s[n][e] = see0 ? s[n][e] * sc[n][e] : -INFINITY;
               s[n][2 + e] = see1 ? s[n][2 + e] * sc[n][e] : -INFINITY;
-              float mx = fmaxf(s[n][e], s[n][2 + e]);
+              passes |= fmaxf(s[n][e], s[n][2 + e]) > m[n][e] + kRescaleThreshold;
+            }
+          if (__any_sync(0xffffffffu, passes)) {
 #pragma unroll
-              for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-              al[n][e] = 1.f;
-              if (mx > m[n][e] + kRescaleThreshold) {      // the maximum moves by 2^8 at least
-                al[n][e] = fast_exp2(m[n][e] - mx);
-                l[n][e] *= al[n][e];
-                m[n][e] = mx;
-                resc = true;
+            for (int n = 0; n < NT; ++n) {
+              float al[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(s[n][e], s[n][2 + e]);
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2)
+                  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                al[e] = 1.f;
+                if (mx > m[n][e] + kRescaleThreshold) {
+                  al[e] = fast_exp2(m[n][e] - mx);
+                  l[n][e] *= al[e];
+                  m[n][e] = mx;
+                }
               }
+#pragma unroll
+              for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[n][t][j] *= al[j & 1];
+            }
+          }
+          uint32_t pb[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
               const float base = m[n][e] == -INFINITY ? 0.f : m[n][e];
               s[n][e] = fast_exp2(s[n][e] - base);
               s[n][2 + e] = fast_exp2(s[n][2 + e] - base);
@@ -507,14 +541,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
                                             : pack_bf16x2(s[n][0], s[n][1]));
             pb[n][1] = transpose8x8(C::kF16 ? pack_f16x2(s[n][2], s[n][3])
                                             : pack_bf16x2(s[n][2], s[n][3]));
-          }
-          if (__any_sync(0xffffffffu, resc)) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int t = 0; t < 8; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[n][t][j] *= al[n][j & 1];
           }
           // ---- O^T += V^T P^T
           auto mask = [&](int i) {
@@ -539,34 +565,36 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
         // the only part: the whole ring is free, and all four warps fold
         float4* all = reinterpret_cast<float4*>(ring);
         named_bar_sync(1, 32 * kConsumers);
-        put_state<NT>(all + warp * kState, lane, o, m, l);
+        put_state<NT>(all + warp * kState, 32, lane, o, m, l);
         named_bar_sync(1, 32 * kConsumers);
         break;
       }
-      constexpr bool kInStage = C::kStageBytes >= 2 * kStateBytes<NT>;
       float4* fold = reinterpret_cast<float4*>(
           kInStage ? ring + (stage % C::kStages) * C::kStageBytes
-                   : ring + C::kRing + 3 * kStateBytes<NT>);
+                   : ring + C::kRing);
       if (!kInStage) named_bar_sync(1, 32 * kConsumers);   // the last part's fold is read
-      if (warp >= 2) put_state<NT>(fold + (warp - 2) * (kStateBytes<NT> / 16), lane, o, m, l);
+      if (warp >= 2) put_state<NT>(fold + (warp - 2) * (kStateBytes<NT> / 16), 32, lane, o, m, l);
       named_bar_sync(1, 32 * kConsumers);
       if (warp < 2) {
-        take_state<NT>(fold + warp * (kStateBytes<NT> / 16), lane, o, m, l);
-        if (warp == 1) put_state<NT>(fold + kStateBytes<NT> / 16, lane, o, m, l);
+        take_state<NT>(fold + warp * (kStateBytes<NT> / 16), 32, lane, o, m, l);
+        if (warp == 1) put_state<NT>(fold + kStateBytes<NT> / 16, 32, lane, o, m, l);
         named_bar_sync(2, 64);
         if (warp == 0) {
-          take_state<NT>(fold + kStateBytes<NT> / 16, lane, o, m, l);
+          take_state<NT>(fold + kStateBytes<NT> / 16, 32, lane, o, m, l);
           // and the parts' in pairs, pairs of pairs and so on, as the cluster goes on
           // to do: the states of the levels that lack their second half wait
+          const int lanes = waiting_lanes<NT>(p.group);
+          const int at = lanes == 32 ? lane : c < 2 ? 2 * gq + c : -1;
+          const int wait = kStateBytes<NT> / 16 / 32 * lanes;
           int level = 0;
           for (; slot >> level & 1; ++level)
-            take_state<NT>(pending + level * (kStateBytes<NT> / 16), lane, o, m, l);
+            take_state<NT>(pending + level * wait, lanes, at, o, m, l);
           if (slot + 1 < nparts)
-            put_state<NT>(pending + level * (kStateBytes<NT> / 16), lane, o, m, l);
+            put_state<NT>(pending + level * wait, lanes, at, o, m, l);
           else
             for (; slot >> level; ++level)
               if (slot >> level & 1)
-                take_state<NT>(pending + level * (kStateBytes<NT> / 16), lane, o, m, l);
+                take_state<NT>(pending + level * wait, lanes, at, o, m, l);
         }
       }
       __syncwarp();
@@ -699,30 +727,32 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
   if (p.ctas > 1) cluster_sync();                    // read, before a CTA's memory goes
 }
 
-// Shared memory of a CTA that takes `parts` parts: the ring, the states that wait
-// for their second half, and the fold's where a stage does not hold it.
+// Shared memory of a CTA that takes `parts` parts of `group` vectors: the ring, and
+// the fold's two states where a stage does not hold them, and those that wait for
+// their second half.
 template <int KV, int NT>
-constexpr int smem_of(int parts) {
-  const bool in_stage = Cfg<KV>::kStageBytes >= 2 * kStateBytes<NT>;
+constexpr int smem_of(int parts, int group) {
+  const int fold = Cfg<KV>::kStageBytes >= 2 * kStateBytes<NT> ? 0 : 2 * kStateBytes<NT>;
   const int levels = parts > 4 ? 3 : parts > 2 ? 2 : parts > 1 ? 1 : 0;
-  return Cfg<KV>::kRing + 1024 + (parts == 1 ? 0 : in_stage ? levels : 5) * kStateBytes<NT>;
+  const int waits = levels * (kStateBytes<NT> / 32 * waiting_lanes<NT>(group));
+  return Cfg<KV>::kRing + 1024 + (parts == 1 ? 0 : fold + waits);
 }
 
 template <int KV, int NT, bool ONE>
 cudaError_t launch(const BlocksParams& p, cudaStream_t s) {
   static_assert(4 * kStateBytes<NT> + 8 * NT * kRow * 4 <= Cfg<KV>::kRing, "the states' memory");
-  static_assert(smem_of<KV, NT>(8) + sizeof(Shared) <= 232448, "shared memory");
+  static_assert(smem_of<KV, NT>(8, 16) + sizeof(Shared) <= 232448, "shared memory");
   static PerDeviceOnce configured;
   const cudaError_t e = configured.run([] {
     return cudaFuncSetAttribute(decode_blocks_kernel<KV, NT, ONE>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem_of<KV, NT>(ONE ? 1 : 8));
+                                smem_of<KV, NT>(ONE ? 1 : 8, 16));
   });
   if (e != cudaSuccess) return e;
   const int qtiles = (p.group + 8 * NT - 1) / (8 * NT);
   const dim3 grid(p.rows * p.hkv * qtiles * p.ctas);
   return launch_pdl_cluster(decode_blocks_kernel<KV, NT, ONE>, grid, dim3(kThreads),
-                            smem_of<KV, NT>(p.cta_parts), s, p, p.ctas);
+                            smem_of<KV, NT>(p.cta_parts, p.group), s, p, p.ctas);
 }
 
 template <int KV>
