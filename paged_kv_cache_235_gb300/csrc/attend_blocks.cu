@@ -597,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
                 take_state<NT>(pending + level * wait, lanes, at, o, m, l);
         }
       }
+      if (kInStage && warp > 0) fence_proxy_async_smem();  // copies overwrite the fold next
       __syncwarp();
       if (live && lane == 0) mbar_arrive(&sh.empty[stage % C::kStages]);
       ++stage;
