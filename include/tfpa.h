@@ -635,7 +635,8 @@ int tfpa_rope_table(const tfpa_rope_spec* spec, int64_t first, int32_t n, float*
  * are stored as tfpa_write_kv stores them (K unrounded before a quantised
  * store).  q and q_out may both be NULL (K and V only), and q_out may be q
  * itself when q_stride is hq * 128; else q_out shares no memory with an input
- * (TFPA_EINVAL).
+ * (TFPA_EINVAL).  A position that two rows of one call name holds either's K and
+ * V afterwards, or some of both.
  * A rotary position outside the table leaves the row's q_out, K and V unwritten
  * and ORs 4 into cache->err_flag (without rope_pos it is TFPA_ERANGE); a page
  * id out of range leaves its K and V unwritten and ORs 1. */
@@ -665,7 +666,8 @@ int tfpa_write_qkv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
  * head the smallest and then the largest stored K of every head dim is kept,
  * as the stored value without k_scale (exact in bf16 for every cache type; a
  * NaN counts as 0).  Bounds go with the pages: streams that share a page share
- * its bounds. */
+ * its bounds.  A call that stores, moves or restores keys leaves them as they
+ * are: tfpa_key_bounds brings them up to date. */
 typedef struct {
   int32_t block;
   void* pool;                     /* DEVICE bf16 [num_pages][hkv][256 / block][2][128],    */
@@ -689,7 +691,8 @@ int tfpa_key_bounds(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
  * them), then those of largest
  *   score = sum over the kv head's query heads h and dims d of
  *           max(q_hd, 0) largest_d + min(q_hd, 0) smallest_d,
- * which no sum of the heads' scores with a key of the block exceeds; ties go to
+ * which (k_scale above 0) no sum of the heads' scores with a key of the block
+ * exceeds, k_scale and softmax_scale left out; ties go to
  * the lower block, and a score that is not a number (an infinite bound under a
  * zero of q) counts as largest.  The choice is that of exact arithmetic: scores
  * too near the border for float32 are taken in 64 bits.

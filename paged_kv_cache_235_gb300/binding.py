@@ -664,10 +664,18 @@ def tfpa_rope_table(spec: RopeSpec, first: int, cos, sin, stream=None) -> None:
     ``[n][rot_dim / 2]``), as many as they have."""
     want = (cos.shape[0], spec.rot_dim // 2)
     for t in (cos, sin):
+        _width(t, 4, "a table")
         if tuple(t.shape) != want or not t.is_contiguous():
             raise ValueError(f"expected contiguous {list(want)} tables")
     _check(lib().tfpa_rope_table(ctypes.byref(spec.c()), int(first), int(want[0]), _ptr(cos),
                                  _ptr(sin), _stream(stream)), "tfpa_rope_table")
+
+
+def _width(t, size: int, what: str) -> None:
+    """Refuses a tensor whose elements are not of the size that the call reads or writes."""
+    d = getattr(t, "dtype", None)
+    if d is not None and d.itemsize != size:
+        raise ValueError(f"{what} must have elements of {size} bytes")
 
 
 def _heads(t, rows: int, heads: int, what: str) -> int:
@@ -699,6 +707,12 @@ def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, r
         if rope_sin.shape != shape or not (rope_cos.is_contiguous()
                                            and rope_sin.is_contiguous()):
             raise ValueError("rope_cos and rope_sin must be contiguous tables of one shape")
+        _width(rope_cos, 4, "rope_cos")
+        _width(rope_sin, 4, "rope_sin")
+        if rope_pos is not None:
+            _width(rope_pos, 4, "rope_pos")
+            if getattr(rope_pos, "shape", (rows,)) != (rows,):
+                raise ValueError("rope_pos holds one position per row")
         cos, sin = rope_cos.data_ptr() or 0, rope_sin.data_ptr() or 0
     qp = qs = op = 0
     if q is not None:
@@ -756,6 +770,7 @@ def _list_shape(blocks, rows: int, hkv: int) -> int:
     shape = blocks.shape
     if len(shape) != 3 or shape[0] != rows or shape[1] != hkv or not blocks.is_contiguous():
         raise ValueError("blocks must be contiguous [rows][hkv][nsel]")
+    _width(blocks, 4, "blocks")
     return shape[2]
 
 

@@ -1639,7 +1639,7 @@ extern "C" int tfpa_rope_table(const tfpa_rope_spec* spec, int64_t first, int32_
   if ((e = rope_freqs(spec, freq))) return e;
   if (n < 0 || (n > 0 && (!cos || !sin || !aligned(cos, 16) || !aligned(sin, 16))))
     return TFPA_EINVAL;
-  if (first < 0 || first + (int64_t)n > kMaxRopePos || first > kMaxRopePos) return TFPA_ERANGE;
+  if (first < 0 || first > kMaxRopePos - n) return TFPA_ERANGE;
   if (n == 0) return TFPA_OK;
   if ((e = check_device())) return e;
   const int nsm = sm_count();
@@ -1936,8 +1936,8 @@ int32_t block_parts(int32_t block, int32_t nsel) {
 }
 
 // Parts that a CTA takes one after the other: as few as let the launch have four
-// CTAs a SM at most (32 rows' lists of 2,048 keys over 4 bits, 256 items of eight
-// parts: a part each 34 us, two 27, four 24, eight 39).
+// CTAs a SM at most (a step with 32 rows' lists of 2,048 keys over 4 bits, 256 items
+// of eight parts: a part each 68.9 us, two 61.6, four 58.8, eight 73.8).
 int32_t cta_parts(int64_t items, int32_t parts, int nsm) {
   int32_t k = 1;
   while (k < parts && items * ((parts + k - 1) / k) > 4 * (int64_t)nsm) k *= 2;

@@ -49,7 +49,7 @@ def table(first=0, n=16, cos=FAKE, sin=2 * FAKE, **kw):
     (dict(scaling="bands", factor=2.0, low=1.0, high=4.0), B.TFPA_EINVAL), (dict(scaling="ramp", factor=2.0, orig_len=100, low=4.0, high=4.0), B.TFPA_EINVAL),
     (dict(scaling="ramp", factor=2.0, orig_len=100, low=0.0, high=4.0), B.TFPA_EINVAL),
     (dict(cos=None), B.TFPA_EINVAL), (dict(sin=FAKE + 4), B.TFPA_EINVAL), (dict(first=-1), B.TFPA_ERANGE), (dict(first=2**31 - 15), B.TFPA_ERANGE),
-    (dict(first=2**62), B.TFPA_ERANGE)])
+    (dict(first=2**62), B.TFPA_ERANGE), (dict(first=2**63 - 1), B.TFPA_ERANGE)])
 def test_table_refusals(kw, code):
     refused(code, lambda: table(**kw))
 
@@ -195,6 +195,23 @@ def test_block_lists_shapes_are_checked():
     for shape in ((1, 7, 4), (2, 8, 4), (1, 8)):
         with pytest.raises(ValueError):
             B.tfpa_decode_blocks(_cache(), [LONG], FAKE, [0], [5], Plane(*shape), 64, 0.1, FAKE, stream=0)
+
+
+def test_elements_of_another_size_are_refused():
+    """A tensor of narrower elements would be read or written past its end."""
+    torch = pytest.importorskip("torch")
+    half = torch.zeros(4, 64, dtype=torch.float16)
+    full = torch.zeros(4, 64)
+    for f in (lambda: B.tfpa_rope_table(B.RopeSpec(1e4), 0, half, half, stream=0),
+              lambda: B.tfpa_rope_table(B.RopeSpec(1e4), 0, full, half, stream=0),
+              lambda: qkv(rope_cos=full, rope_sin=half),
+              lambda: qkv(rope_cos=full, rope_sin=full, rope_pos=torch.zeros(1, dtype=torch.int16)),
+              lambda: qkv(rope_cos=full, rope_sin=full, rope_pos=torch.zeros(2, dtype=torch.int32)),
+              lambda: B.tfpa_select_blocks(_cache(), [LONG], B.Bounds(64, FAKE), FAKE, [0], [5], torch.zeros(1, 8, 16, dtype=torch.int16)),
+              lambda: B.tfpa_decode_blocks(_cache(), [LONG], FAKE, [0], [5], torch.zeros(1, 8, 16, dtype=torch.int16), 64, 0.1, FAKE)):
+        with B.record_launches() as rec, pytest.raises(ValueError):
+            f()
+        assert rec == []
 
 
 def test_bounds_of_the_blocks_that_rows_fall_into():

@@ -637,3 +637,90 @@ def test_after_an_eviction_the_bounds_are_taken_anew():
     B.tfpa_select_blocks(c.cache, c.segs, b, q, rs, rp, lists, sink=1, recent=1)
     check_choice(c, b, q, rs, rp, 5, 1, 1, got=lists)
     check_attend(c, q, rs, rp, lists, 64)
+
+
+# ---------------------------------------------------------------- ends of what the calls allow
+@pytest.mark.parametrize("kv", KVS)
+def test_pages_far_into_a_pool(kv):
+    """The same rows on a pool's first pages and on its last, whose elements lie past 2^32 bytes: the same bytes."""
+    row = {"bf16": 256, "fp8": 128, "fp4": 72}[kv]
+    hkv, hq, L = 2, 8, 1500
+    n = 2**32 // (row * 256 * hkv) + 40
+    pool = [torch.empty(n * hkv * 256 * row, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    one = torch.full((hkv,), 0.01, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache = B.Cache(kv, hq, hkv, *pool, *((None, None) if kv == "bf16" else (one, one)), err, n)
+    b = B.make_bounds(n, hkv, 64)
+    gen = torch.Generator(device="cuda").manual_seed(91)
+    x = torch.randn(L, hq + 2 * hkv, 128, generator=gen, device="cuda").to(torch.bfloat16)
+    got = []
+    for first in (3, n - 6):
+        seg = B.Seg(L, page_table=torch.arange(first, first + 6, dtype=torch.int32, device="cuda"))
+        rs, rp = np.zeros(L, np.int32), np.arange(L, dtype=np.int32)
+        q, out = (torch.empty(L, hq, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        lists = torch.empty(L, hkv, 5, dtype=torch.int32, device="cuda")
+        B.tfpa_write_qkv(cache, [seg], x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], q, rs, rp)
+        B.tfpa_key_bounds(cache, [seg], b, rs, rp)
+        B.tfpa_select_blocks(cache, [seg], b, q, rs, rp, lists, sink=1, recent=1)
+        B.tfpa_decode_blocks(cache, [seg], q, rs, rp, lists, 64, SCALE, out)
+        lo, hi = b.pool[first:first + 6].float().unbind(3)
+        got.append([q, lists, out, b.pool[first:first + 6].clone()])
+        assert (lo[:5] < 0).all() and (hi[:5] > 0).all() and torch.isfinite(out.float()).all()
+    assert int(err.item()) == 0
+    assert all(torch.equal(u, v) for u, v in zip(*got))
+    k = x[L - 1, hq:hq + hkv].float()
+    w = x[L - 1, hq + hkv:].float()
+    kk, vv = (torch.empty(1, hkv, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    B.tfpa_read_kv(cache, [seg], kk, vv, [0], [L - 1])
+    # a value is off by half a step of its type at most; bf16 stores it as it is, e2m1's largest step is 2 of 6
+    off = {"bf16": 0.0, "fp8": 2.0 ** -4, "fp4": 0.0}[kv]
+    for have, want in ((kk, k), (vv, w)):
+        d = (have[0].float() - want).abs()
+        if kv == "fp4":
+            assert (d <= want.abs().view(hkv, 8, 16).amax(-1).repeat_interleave(16, -1) * (1 / 6 + 2.0 ** -4 + 2.0 ** -8)).all()
+        else:
+            assert (d <= off * want.abs() + 2.0 ** -10 * 0.01 * (off > 0) + 2.0 ** -8 * want.abs() * (off > 0)).all()
+
+
+@pytest.mark.parametrize("kv", KVS)
+def test_the_same_position_twice(kv):
+    """Two rows of one call at one position: both have their q and attention, the position holds a K and V of theirs."""
+    c = LongCase(kv, [700], [True], 8, 2, 92)
+    x = torch.randn(2, 12, 128, generator=c.g, device="cuda").to(torch.bfloat16)
+    x[1] = x[0]
+    x[1, :8] = -x[0, :8]
+    q = torch.empty(2, 8, 128, dtype=torch.bfloat16, device="cuda")
+    rs, rp = [0, 0], [699, 699]
+    B.tfpa_write_qkv(c.cache, c.segs, x[:, :8], x[:, 8:10], x[:, 10:], q, rs, rp)
+    assert torch.equal(q, x[:, :8])
+    b = bound_store(c, 64)
+    every = np.zeros(700, np.int32), np.arange(700, dtype=np.int32)
+    B.tfpa_key_bounds(c.cache, c.segs, b, np.concatenate([every[0]] * 2), np.concatenate([every[1]] * 2))
+    for blk in range(11):
+        assert torch.equal(bound_view(c, b, 0, blk).double(), exact_bounds(c, 0, blk, 64))
+    lists = torch.empty(2, 2, 4, dtype=torch.int32, device="cuda")
+    B.tfpa_select_blocks(c.cache, c.segs, b, q, rs, rp, lists, sink=0, recent=1)
+    check_choice(c, b, q, rs, rp, 4, 0, 1, got=lists)
+    check_attend(c, q, rs, rp, lists, 64)
+
+
+@pytest.mark.parametrize("kv", KVS)
+def test_a_very_long_list_of_few_blocks(kv):
+    """A list of 2^20 entries, all but the first, a middle one and the last of them empty."""
+    c = LongCase(kv, [5000], [True], 4, 1, 93)
+    lists = torch.full((1, 1, 2**20), -1, dtype=torch.int32, device="cuda")
+    lists[0, 0, 0], lists[0, 0, 2**19 + 77], lists[0, 0, -1] = 5, 78, 0
+    check_attend(c, c.q(1), [0], [4999], lists, 64)
+    assert int(c.err.item()) == 0
+
+
+def test_many_query_heads_of_one_kv_head():
+    """128 query heads of one kv head, in the selection and in the attention."""
+    c = LongCase("bf16", [3000, 200], [True, False], 128, 1, 94)
+    b = random_bounds(c, 64, 95)
+    rs, rp = last_rows(c.lengths, [3, 1])
+    q = c.q(len(rs))
+    lists = torch.empty(len(rs), 1, 9, dtype=torch.int32, device="cuda")
+    B.tfpa_select_blocks(c.cache, c.segs, b, q, rs, rp, lists, sink=1, recent=2)
+    check_choice(c, b, q, rs, rp, 9, 1, 2, got=lists)
+    check_attend(c, q, rs, rp, lists, 64)
