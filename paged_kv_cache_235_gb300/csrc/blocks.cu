@@ -195,6 +195,43 @@ __device__ __forceinline__ uint4 bound_load(const SelRun& run, int at, int lane)
   return *(static_cast<const uint4*>(run.bounds) + (size_t)at * 32 + lane);
 }
 
+// The query heads' negative parts of head dim d, and the positive ones, summed as
+// float64 would: in float32 where no sum rounds, which heads of like size see to
+// (64-bit adds are a sixty-fourth of the rate).
+__device__ __forceinline__ void sum_heads64(const __nv_bfloat16* q, int group, int d,
+                                            SelShared& sh) {
+  float down = 0.f, up = 0.f;
+  bool exact = true;
+  // of one sign, so a sum that does not round gives both back
+  auto add = [&](float& a, float x) {
+    const float t = a + x;
+    exact = exact && t - a == x && t - x == a;
+    a = t;
+  };
+  for (int h0 = 0; h0 < group; h0 += 4) {
+    float x[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      x[h] = h0 + h < group ? __bfloat162float(q[(size_t)(h0 + h) * kHeadDim + d]) : 0.f;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      add(down, x[h] > 0.f ? 0.f : x[h]);
+      add(up, x[h] < 0.f ? 0.f : x[h]);
+    }
+  }
+  double a = down, b = up;
+  if (!exact) {
+    a = b = 0.0;
+    for (int h = 0; h < group; ++h) {
+      const float x = __bfloat162float(q[(size_t)h * kHeadDim + d]);
+      a += x > 0.f ? 0.f : x;
+      b += x < 0.f ? 0.f : x;
+    }
+  }
+  sh.q64[d] = a;
+  sh.q64[128 + d] = b;
+}
+
 // The score of a block from the whole warp's bounds, in 64 bits.  Every block's
 // sum runs in the same order, so equal bounds give equal scores.
 __device__ __forceinline__ double score64(const SelShared& sh, const uint4& w, int lane) {
@@ -289,12 +326,13 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
   } else if (want < nfree) {
     // ---- how far a float32 score may be off: its roundings' sum |q| |bound|, the
     // sums over G heads (all of one sign), 8 products and sums of a lane, 5 of the
-    // reduction, 2^-24 each; e is twice that.  The exact want-th largest score is
-    // within e of the one found in float32, so a score beyond that by more than 2 e
-    // is decided; the others are near.
+    // reduction, 2^-24 each; e is twice that and more.  The exact want-th largest
+    // score is within half of e of the one found in float32, so a score beyond that
+    // by more than e (and a sixteenth, for the roundings here) is decided; the others
+    // are near.
     const float e = (float)(16 + p.group) * 0x1p-23f * q1 * __uint_as_float(most << 16) + 1e-40f;
     all = most >= 0x7F80u || !(e < INFINITY);
-    bool decided = false;
+    bool decided = false, listed = false;  // no near one to tell; the near ones are in near_i
     // ---- the want-th largest key
     const uint32_t differ = kmin ^ kmax;
     int shift = differ ? 32 - __clz(differ) : 0;         // bits that are not the same in all
@@ -345,8 +383,11 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int at = (int)((k[i] >> shift) & (kBins - 1)) - bin;
-            if (is_score(k[i]) && at >= -1 && at <= 1)
-              sh.near_k[atomicAdd(&sh.count, 1u)] = k[i];
+            if (is_score(k[i]) && at >= -1 && at <= 1) {
+              const uint32_t to = atomicAdd(&sh.count, 1u);
+              sh.near_k[to] = k[i];
+              sh.near_i[to] = b + i;
+            }
           }
         });
         __syncthreads();
@@ -354,8 +395,10 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
           const uint32_t cnt = same + up + down, nth = rest + up;
           const bool there = (uint32_t)lane < cnt;
           const uint32_t mine = there ? (uint32_t)sh.near_k[lane] : 0u;
+          const int block = there ? sh.near_i[lane] : 0;
           uint32_t more = 0, equal = 0;
-          for (uint32_t i = 0; i < cnt; ++i) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {       // (0 behind the last: below every key)
             const uint32_t other = __shfl_sync(0xffffffffu, mine, i);
             more += other > mine;
             equal += other == mine;
@@ -364,23 +407,30 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
               __ballot_sync(0xffffffffu, there && more < nth && nth <= more + equal);
           const uint32_t border = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
           const float at = value32(border), s = value32(mine);
-          const float t = at + 2.125f * e, l = at - 2.125f * e;
+          const float t = at + 1.0625f * e, l = at - 1.0625f * e;
           const uint32_t in = __popc(__ballot_sync(0xffffffffu, there && s > t));
-          const uint32_t near = __popc(__ballot_sync(0xffffffffu, there && s <= t && s >= l));
+          const bool is_near = there && s <= t && s >= l;
+          const unsigned nears = __ballot_sync(0xffffffffu, is_near);
           // (bins beyond the first and the last of the range are empty)
           const uint32_t edge = prefix;
           const bool inside = (bin == 0 || order32(l) >= edge - (1u << shift)) &&
                               (bin == kBins - 1 || order32(t) - edge < (2u << shift));
+          if (is_near) sh.near_i[__popc(nears & ((1u << lane) - 1))] = block;
           if (lane == 0) {
+            const bool plain = (uint32_t)__popc(nears) == nth - in;
             sh.border = border;
-            sh.pick[0] = inside && near == nth - in;
-            sh.pick[1] = order32(l);
-            sh.count = 0;
+            sh.pick[0] = !inside ? 0u : plain ? 1u : 2u;
+            sh.pick[1] = plain ? order32(l) : order32(t) + 1;
+            sh.pick[2] = nth - in;
+            sh.count = inside ? __popc(nears) : 0;
           }
+        } else if (warp >= kSelWarps / 2) {
+          sum_heads64(q, p.group, tid - kSelThreads / 2, sh);   // in case; the histogram is read
         }
         __syncthreads();
         prefix = sh.border;
-        decided = sh.pick[0];
+        decided = sh.pick[0] == 1;
+        listed = sh.pick[0] == 2;
         in_from = sh.pick[1];
         break;
       }
@@ -416,38 +466,50 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
     }
     // ---- else who is in, who is out, and who is too near to tell
     const float at = value32(prefix);
-    top = at + 2.125f * e;
-    low = at - 2.125f * e;
+    top = at + 1.0625f * e;
+    low = at - 1.0625f * e;
     auto is_near = [&](uint32_t x) {
       if (!is_score(x)) return false;
       const float s = value32(x);
       return all || (s >= low && s <= top);
     };
+    // the first `need` of the near ones in near_i, by their exact scores
+    auto settle = [&](uint32_t near, uint32_t need) {
+      for (uint32_t i = warp; i < near; i += kSelWarps) {
+        const uint4 w = bound_load(run, bound_at(p, run, g, sh.near_i[i]), lane);
+        const double s = score64(sh, w, lane);
+        if (lane == 0) sh.near_k[i] = order64(s);
+      }
+      __syncthreads();
+      if (tid < (int)near) {
+        const uint64_t mine = sh.near_k[tid];
+        const int b = sh.near_i[tid];
+        uint32_t before = 0;
+        for (uint32_t i = 0; i < near; ++i)
+          before += sh.near_k[i] > mine || (sh.near_k[i] == mine && sh.near_i[i] < b);
+        if (before < need) key32[b] = kTaken;
+      }
+    };
     uint32_t both = 0;                   // in << 16 | near
-    if (!decided) rounds([&](int) {
+    if (!decided && !listed) rounds([&](int) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         both += is_near(k[i]) ? 1u : is_score(k[i]) && value32(k[i]) > top ? 0x10000u : 0u;
     });
     uint32_t total = want << 16;
-    if (!decided) sel_prefix(both, sh.warp_s, total);
+    if (!decided && !listed) sel_prefix(both, sh.warp_s, total);
     const uint32_t near = total & 0xFFFFu, need = want - (total >> 16);
     if (decided) {
       // in_from says it
+    } else if (listed) {
+      settle(sh.count, sh.pick[2]);
+      __syncthreads();
+      loaded = false;                    // the near ones that are in say so now
     } else if (near == need) {
       in_from = order32(low);
     } else {
       // ---- the near ones' exact scores
-      if (tid < 128) {
-        double down = 0.0, up = 0.0;
-        for (int h = 0; h < p.group; ++h) {
-          const float x = __bfloat162float(q[(size_t)h * kHeadDim + tid]);
-          down += x > 0.f ? 0.f : x;
-          up += x < 0.f ? 0.f : x;
-        }
-        sh.q64[tid] = down;
-        sh.q64[128 + tid] = up;
-      }
+      if (tid < 128) sum_heads64(q, p.group, tid, sh);
       if (tid == 0) sh.count = 0;
       __syncthreads();
       if (near <= kNear) {
@@ -463,20 +525,7 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
           }
         });
         __syncthreads();
-        for (uint32_t i = warp; i < near; i += kSelWarps) {
-          const uint4 w = bound_load(run, bound_at(p, run, g, sh.near_i[i]), lane);
-          const double s = score64(sh, w, lane);
-          if (lane == 0) sh.near_k[i] = order64(s);
-        }
-        __syncthreads();
-        if (tid < (int)near) {
-          const uint64_t mine = sh.near_k[tid];
-          const int b = sh.near_i[tid];
-          uint32_t before = 0;
-          for (uint32_t i = 0; i < near; ++i)
-            before += sh.near_k[i] > mine || (sh.near_k[i] == mine && sh.near_i[i] < b);
-          if (before < need) key32[b] = kTaken;
-        }
+        settle(near, need);
       } else {
         // many (equal blocks, scores that are no numbers): the need-th largest of
         // their exact keys, 8 bits at a time
