@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
   extern __shared__ uint8_t ring_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(ring_raw) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = (int)same_in_warp((uint32_t)tid >> 5);
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sh.full[i], 1);

@@ -266,7 +266,7 @@ __device__ __forceinline__ float reduce8(const float (&v)[8], int lane) {
 __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bfloat16* q, int g,
                        int n, bool every, int ranks, float q1, uint32_t* key32,
                        uint64_t* key64, SelShared& sh, int32_t* out) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = (int)same_in_warp((uint32_t)tid >> 5);
   constexpr int kRound = 8 * kSelThreads;
   const bool one = n <= kRound;
   bool loaded = false;
@@ -370,14 +370,14 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
         }
       }
       __syncthreads();
-      prefix |= sh.pick[0] << shift;
-      rest = sh.pick[1];
-      const uint32_t same = sh.pick[2];
+      const int bin = (int)same_in_warp(sh.pick[0]);
+      prefix |= (uint32_t)bin << shift;
+      rest = same_in_warp(sh.pick[1]);
+      const uint32_t same = same_in_warp(sh.pick[2]);
       // Few keys in the border's bin and the two beside it, and the near ones among
       // them: one warp settles it.
-      const int bin = (int)sh.pick[0];
-      const uint32_t up = bin + 1 < kBins ? sh.hist[bin + 1] : 0u;
-      const uint32_t down = bin > 0 ? sh.hist[bin - 1] : 0u;
+      const uint32_t up = bin + 1 < kBins ? same_in_warp(sh.hist[bin + 1]) : 0u;
+      const uint32_t down = bin > 0 ? same_in_warp(sh.hist[bin - 1]) : 0u;
       if (high == first_high && shift > 0 && !all && same + up + down <= 32) {
         rounds([&](int b) {
 #pragma unroll
@@ -428,9 +428,10 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
           sum_heads64(q, p.group, tid - kSelThreads / 2, sh);   // in case; the histogram is read
         }
         __syncthreads();
+        const uint32_t how = same_in_warp(sh.pick[0]);
         prefix = sh.border;
-        decided = sh.pick[0] == 1;
-        listed = sh.pick[0] == 2;
+        decided = how == 1;
+        listed = how == 2;
         in_from = sh.pick[1];
         break;
       }
@@ -498,11 +499,12 @@ __device__ void choose(const SelectParams& p, const SelRun& run, const __nv_bflo
     });
     uint32_t total = want << 16;
     if (!decided && !listed) sel_prefix(both, sh.warp_s, total);
+    total = same_in_warp(total);
     const uint32_t near = total & 0xFFFFu, need = want - (total >> 16);
     if (decided) {
       // in_from says it
     } else if (listed) {
-      settle(sh.count, sh.pick[2]);
+      settle(same_in_warp(sh.count), sh.pick[2]);
       __syncthreads();
       loaded = false;                    // the near ones that are in say so now
     } else if (near == need) {
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(kSelThreads, R == 1 ? 4 : 2)
   if (nc > 1) cluster_arrive();              // every CTA has to run before its memory is written
   allow_next_grid();
   wait_prior_grid();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = (int)same_in_warp((uint32_t)tid >> 5);
   const int rank = nc > 1 ? (int)cluster_ctarank() : 0;
   const int item = blockIdx.x / nc, g = item % p.hkv, group = item / p.hkv;
   const SelRun& run = p.runs[run_holding(p.runs, p.nruns, &SelRun::group0, group)];

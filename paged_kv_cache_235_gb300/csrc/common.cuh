@@ -242,6 +242,13 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// A value that all lanes of the warp hold alike, in a form that the compiler knows
+// to be: where it cannot tell that a branch or a loop goes one way for the whole
+// warp, each exchange between lanes behind it costs some 300 cycles.
+__device__ __forceinline__ uint32_t same_in_warp(uint32_t x) {
+  return __reduce_max_sync(0xffffffffu, x);
+}
+
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }

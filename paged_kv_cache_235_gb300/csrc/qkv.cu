@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(H > 1 ? 256 : 64, H > 1 ? 2 : 8)
   constexpr int HK = H > 1 ? H / 2 : 1;
   allow_next_grid();
   wait_prior_grid();
-  const int wid = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+  const int wid = blockIdx.x * (blockDim.x / 32) + (int)same_in_warp(threadIdx.x >> 5);
   if (wid >= p.warps) return;
   const int t = threadIdx.x & 15;                          // 8-element slice
   const int side = (threadIdx.x >> 4) & 1;                 // half-warp: its step of a unit
