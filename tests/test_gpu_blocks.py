@@ -318,8 +318,9 @@ def attend64(c, q, rs, rp, lists, block):
                 z = e.sum(-1, keepdim=True)
                 es = 2 * 128 * U * xa + 2.0 ** -20
                 out[r, h], lse[r, h] = e @ v / z, (m + z.log())[:, 0]
-                # a weight rounds to bf16 (2^-9 of it) or f16 (2^-11); below 2^-14 an f16 one to a multiple of 2^-24
-                wr = 2.0 ** -9 if c.kv == "bf16" else 2.0 ** -11
+                # a weight rounds to bf16 (8 significant bits: 2^-8 of it at most) or f16 (11: 2^-11); below 2^-14 an f16
+                # one to a multiple of 2^-24
+                wr = 2.0 ** -8 if c.kv == "bf16" else 2.0 ** -11
                 tol[r, h] = (2.0 ** -8 * out[r, h].abs() + (e @ v.abs() / z) * (wr + 2 * es)
                              + len(key) * 2.0 ** -25 / z * v.abs().max() + 1e-30)
                 ltol[r, h] = es[:, 0] + 4 * U * (lse[r, h].abs() + m[:, 0].abs() + 20)
