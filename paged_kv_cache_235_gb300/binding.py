@@ -39,7 +39,7 @@ EXPORTS = ("tfpa_pages_per_split", "tfpa_num_splits", "tfpa_write_kv", "tfpa_dec
            "tfpa_plan_dyn_pack", "tfpa_plan_shape", "tfpa_plan_capture", "tfpa_plan_replay",
            "tfpa_decode_append", "tfpa_plan_decode_append", "tfpa_row_splits", "tfpa_read_kv",
            "tfpa_key_mass", "tfpa_evict_kv", "tfpa_rope_table", "tfpa_write_qkv",
-           "tfpa_key_bounds", "tfpa_select_blocks", "tfpa_decode_blocks")
+           "tfpa_key_bounds", "tfpa_select_blocks", "tfpa_decode_blocks", "tfpa_call")
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 
 
@@ -92,6 +92,26 @@ class tfpa_qkv(ctypes.Structure):
 
 class tfpa_bounds(ctypes.Structure):
     _fields_ = [("block", ctypes.c_int32), ("pool", ctypes.c_void_p), ("slabs", ctypes.c_void_p)]
+
+
+class _tfpa_call_rope(ctypes.Structure):
+    _fields_ = [("spec", ctypes.c_void_p), ("first", ctypes.c_int64), ("cos", ctypes.c_void_p),
+                ("sin", ctypes.c_void_p)]
+
+
+class _tfpa_call_union(ctypes.Union):
+    _fields_ = [("qkv", tfpa_qkv), ("rope", _tfpa_call_rope)]
+
+
+class tfpa_call_args(ctypes.Structure):
+    _fields_ = [("op", ctypes.c_int32), ("nseg", ctypes.c_int32), ("cache", ctypes.c_void_p),
+                ("segs", ctypes.c_void_p), ("row_seg", ctypes.c_void_p),
+                ("row_pos", ctypes.c_void_p), ("stream", ctypes.c_void_p),
+                ("bounds", ctypes.c_void_p), ("q", ctypes.c_void_p), ("blocks", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("nsel", ctypes.c_int32), ("sink", ctypes.c_int32),
+                ("recent", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_double), ("u", _tfpa_call_union)]
 
 
 class tfpa_launch_record(ctypes.Structure):
@@ -222,6 +242,8 @@ def lib():
         L.tfpa_decode_blocks.argtypes = [P(tfpa_cache), P(tfpa_seg), i32, vp, vp, vp, i32, i32,
                                          i32, vp, ctypes.c_float, vp, vp, vp]
         L.tfpa_decode_blocks.restype = ctypes.c_int
+        L.tfpa_call.argtypes = [vp]
+        L.tfpa_call.restype = ctypes.c_int
         L.tfpa_set_launch_hook.argtypes = [HOOK, vp, ctypes.c_int]
         L.tfpa_set_launch_hook.restype = None
         L.tfpa_strerror.argtypes = [ctypes.c_int]
@@ -667,8 +689,41 @@ def tfpa_rope_table(spec: RopeSpec, first: int, cos, sin, stream=None) -> None:
         _width(t, 4, "a table")
         if tuple(t.shape) != want or not t.is_contiguous():
             raise ValueError(f"expected contiguous {list(want)} tables")
-    _check(lib().tfpa_rope_table(ctypes.byref(spec.c()), int(first), int(want[0]), _ptr(cos),
-                                 _ptr(sin), _stream(stream)), "tfpa_rope_table")
+    _check(lib().tfpa_call(_pack_call_rope(
+        _OP_ROPE_TABLE, 0, 0, 0, 0, 0, _stream(stream) or 0, 0, 0, 0, 0, 0, want[0], 0, 0, 0, 0, 0,
+        0.0, _addressof(spec.c()), first, _ptr(cos) or 0, _ptr(sin) or 0)), "tfpa_rope_table")
+
+
+# tfpa_call_args packed: ctypes takes 0.1 us or more for each argument of a call, and five times
+# as long to fill the structure
+_CALL = "@2i10P6id"
+_pack_call = struct.Struct(_CALL).pack
+_pack_call_rope = struct.Struct(_CALL + "Pq2P").pack
+_pack_call_qkv = struct.Struct(_CALL + "3P3q5P3if").pack
+assert struct.calcsize(_CALL + "3P3q5P3if") == ctypes.sizeof(tfpa_call_args)
+assert struct.calcsize(_CALL) == tfpa_call_args.u.offset
+_OP_ROPE_TABLE, _OP_WRITE_QKV, _OP_KEY_BOUNDS, _OP_SELECT_BLOCKS, _OP_DECODE_BLOCKS = range(5)
+_INT32 = np.dtype(np.int32)
+
+
+def _row_ptr(a):
+    """A row table as int32 (kept until the call is over) and its address."""
+    if type(a) is np.ndarray and a.dtype is _INT32:
+        try:
+            return a, _addressof(_c_char.from_buffer(a))     # (refuses what is not contiguous)
+        except (TypeError, ValueError, BufferError):
+            pass
+    a = _i32(a)
+    return a, _np_ptr(a)
+
+
+def _rows(row_seg, row_pos):
+    rs, sp = _row_ptr(row_seg)
+    rp, pp = _row_ptr(row_pos)
+    rows = len(rs)
+    if len(rp) != rows:
+        raise ValueError("row_seg and row_pos must be of one length")
+    return rows, sp, pp, (rs, rp)
 
 
 def _width(t, size: int, what: str) -> None:
@@ -686,11 +741,6 @@ def _heads(t, rows: int, heads: int, what: str) -> int:
     return s[0] if rows > 1 else heads * HEAD_DIM
 
 
-# tfpa_qkv, packed in a fifth of the time that its ctypes structure takes to fill
-_pack_qkv = struct.Struct("@3P3q5P3if").pack
-assert struct.calcsize("@3P3q5P3if") == ctypes.sizeof(tfpa_qkv)
-
-
 def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, row_pos,
                    q_weight=None, k_weight=None, eps: float = 1e-6, rope_cos=None, rope_sin=None,
                    rope_pos=None, interleaved: bool = False, stream=None) -> None:
@@ -699,8 +749,8 @@ def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, r
     ``q_out``, K and V into the cache.  ``q``, ``k`` and ``v`` are ``[rows][heads][128]`` views,
     e.g. of one fused projection's output; q and q_out may both be None."""
     cs, n = _segs(segs)
-    rs, rp = _i32(row_seg), _i32(row_pos)
-    rows, hq, hkv = len(rs), cache.hq, cache.hkv
+    rows, sp, pp, keep = _rows(row_seg, row_pos)
+    hq, hkv = cache.hq, cache.hkv
     table = half = cos = sin = 0
     if rope_cos is not None:
         table, half = shape = rope_cos.shape
@@ -721,11 +771,12 @@ def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, r
         if q_out.shape != (rows, hq, HEAD_DIM) or not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous [rows][hq][128]")
         op = q_out.data_ptr() or 0
-    a = _pack_qkv(qp, k.data_ptr() or 0, v.data_ptr() or 0, qs, _heads(k, rows, hkv, "k"),
-                  _heads(v, rows, hkv, "v"), _ptr(q_weight) or 0, _ptr(k_weight) or 0, cos, sin,
-                  _ptr(rope_pos) or 0, table, 2 * half, 1 if interleaved else 0, eps)
-    _check(lib().tfpa_write_qkv(ctypes.byref(cache.c()), cs, n, a, _np_ptr(rs), _np_ptr(rp), rows,
-                                op, _stream(stream)), "tfpa_write_qkv")
+    _check(lib().tfpa_call(_pack_call_qkv(
+        _OP_WRITE_QKV, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0, 0, 0,
+        0, op, 0, rows, 0, 0, 0, 0, 0, 0.0, qp, k.data_ptr() or 0, v.data_ptr() or 0, qs,
+        _heads(k, rows, hkv, "k"), _heads(v, rows, hkv, "v"), _ptr(q_weight) or 0,
+        _ptr(k_weight) or 0, cos, sin, _ptr(rope_pos) or 0, table, 2 * half,
+        1 if interleaved else 0, eps)), "tfpa_write_qkv")
 
 
 @dataclass(eq=False)
@@ -761,9 +812,10 @@ def tfpa_key_bounds(cache: Cache, segs: Sequence[Seg], bounds: Bounds, row_seg, 
                     stream=None) -> None:
     """The bounds of every block that holds one of the rows, taken anew from the stored keys."""
     cs, n = _segs(segs)
-    rs, rp = _i32(row_seg), _i32(row_pos)
-    _check(lib().tfpa_key_bounds(ctypes.byref(cache.c()), cs, n, ctypes.byref(bounds.of(n)),
-                                 _ptr(rs), _ptr(rp), len(rs), _stream(stream)), "tfpa_key_bounds")
+    rows, sp, pp, keep = _rows(row_seg, row_pos)
+    _check(lib().tfpa_call(_pack_call(
+        _OP_KEY_BOUNDS, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0,
+        _addressof(bounds.of(n)), 0, 0, 0, 0, rows, 0, 0, 0, 0, 0, 0.0)), "tfpa_key_bounds")
 
 
 def _list_shape(blocks, rows: int, hkv: int) -> int:
@@ -779,24 +831,24 @@ def tfpa_select_blocks(cache: Cache, segs: Sequence[Seg], bounds: Bounds, q, row
     """Each row's and kv head's blocks of largest bound into ``blocks`` (device int32
     ``[rows][hkv][nsel]``), the first ``sink`` and the last ``recent`` among them."""
     cs, n = _segs(segs)
-    rs, rp = _i32(row_seg), _i32(row_pos)
-    nsel = _list_shape(blocks, len(rs), cache.hkv)
-    _check(lib().tfpa_select_blocks(ctypes.byref(cache.c()), cs, n, ctypes.byref(bounds.of(n)),
-                                    _ptr(q), _ptr(rs), _ptr(rp), len(rs), nsel, int(sink),
-                                    int(recent), _ptr(blocks), _stream(stream)),
-           "tfpa_select_blocks")
+    rows, sp, pp, keep = _rows(row_seg, row_pos)
+    nsel = _list_shape(blocks, rows, cache.hkv)
+    _check(lib().tfpa_call(_pack_call(
+        _OP_SELECT_BLOCKS, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0,
+        _addressof(bounds.of(n)), _ptr(q) or 0, _ptr(blocks) or 0, 0, 0, rows, 0, nsel, sink, recent,
+        0, 0.0)), "tfpa_select_blocks")
 
 
 def tfpa_decode_blocks(cache: Cache, segs: Sequence[Seg], q, row_seg, row_pos, blocks, block: int,
                        softmax_scale, out, lse=None, stream=None) -> None:
     """Attention of each row over its own blocks (``blocks`` as tfpa_select_blocks leaves it)."""
     cs, n = _segs(segs)
-    rs, rp = _i32(row_seg), _i32(row_pos)
-    nsel = _list_shape(blocks, len(rs), cache.hkv)
-    _check(lib().tfpa_decode_blocks(ctypes.byref(cache.c()), cs, n, _ptr(q), _ptr(rs), _ptr(rp),
-                                    len(rs), int(block), nsel, _ptr(blocks),
-                                    float(softmax_scale), _ptr(out), _ptr(lse),
-                                    _stream(stream)), "tfpa_decode_blocks")
+    rows, sp, pp, keep = _rows(row_seg, row_pos)
+    nsel = _list_shape(blocks, rows, cache.hkv)
+    _check(lib().tfpa_call(_pack_call(
+        _OP_DECODE_BLOCKS, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0, 0,
+        _ptr(q) or 0, _ptr(blocks) or 0, _ptr(out) or 0, _ptr(lse) or 0, rows, block, nsel, 0, 0, 0,
+        softmax_scale)), "tfpa_decode_blocks")
 
 
 class Plan:

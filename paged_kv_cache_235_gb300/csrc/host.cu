@@ -2056,6 +2056,31 @@ extern "C" int tfpa_decode_blocks(const tfpa_cache* cache, const tfpa_seg* segs,
   });
 }
 
+extern "C" int tfpa_call(const tfpa_call_args* c) {
+  if (!c) return TFPA_EINVAL;
+  switch (c->op) {
+    case TFPA_OP_ROPE_TABLE:
+      return tfpa_rope_table(c->u.rope.spec, c->u.rope.first, c->rows, c->u.rope.cos,
+                             c->u.rope.sin, c->stream);
+    case TFPA_OP_WRITE_QKV:
+      return tfpa_write_qkv(c->cache, c->segs, c->nseg, &c->u.qkv, c->row_seg, c->row_pos,
+                            c->rows, c->out, c->stream);
+    case TFPA_OP_KEY_BOUNDS:
+      return tfpa_key_bounds(c->cache, c->segs, c->nseg, c->bounds, c->row_seg, c->row_pos,
+                             c->rows, c->stream);
+    case TFPA_OP_SELECT_BLOCKS:
+      return tfpa_select_blocks(c->cache, c->segs, c->nseg, c->bounds, c->q, c->row_seg,
+                                c->row_pos, c->rows, c->nsel, c->sink, c->recent, c->blocks,
+                                c->stream);
+    case TFPA_OP_DECODE_BLOCKS:
+      return tfpa_decode_blocks(c->cache, c->segs, c->nseg, c->q, c->row_seg, c->row_pos,
+                                c->rows, c->block, c->nsel, c->blocks, (float)c->softmax_scale,
+                                c->out, c->lse, c->stream);
+    default:
+      return TFPA_EINVAL;
+  }
+}
+
 extern "C" void tfpa_set_launch_hook(tfpa_launch_hook hook, void* user, int dry_run_flag) {
   g_hook_user.store(user, std::memory_order_relaxed);
   g_hook_dry.store(hook ? dry_run_flag : 0, std::memory_order_relaxed);

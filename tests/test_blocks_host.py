@@ -197,6 +197,62 @@ def test_block_lists_shapes_are_checked():
             B.tfpa_decode_blocks(_cache(), [LONG], FAKE, [0], [5], Plane(*shape), 64, 0.1, FAKE, stream=0)
 
 
+def test_calls_with_their_arguments_in_memory():
+    """tfpa_call does what the call that it names does, and refuses names that there are not."""
+    import ctypes
+    import numpy as np
+    L = B.lib()
+    c, n = _cache(), 2
+    segs = B.SegTable([LONG])
+    rs, rp = np.zeros(n, np.int32), np.array([999, 1000], np.int32)
+    b = B.Bounds(64, FAKE).c()
+    spec = B.RopeSpec(1e4).c()
+    q = B.tfpa_qkv(8 * FAKE, 9 * FAKE, 10 * FAKE, 32 * 128, 8 * 128, 8 * 128, eps=1e-6)
+    at = (ctypes.byref(c.c()), segs.arr, 1)
+    rows = (rs.ctypes.data, rp.ctypes.data, n)
+    with B.record_launches() as direct:
+        assert L.tfpa_rope_table(ctypes.byref(spec), 7, n, FAKE, 2 * FAKE, 0) == 0
+        assert L.tfpa_write_qkv(*at, ctypes.string_at(ctypes.byref(q), ctypes.sizeof(q)), *rows, 11 * FAKE, 0) == 0
+        assert L.tfpa_key_bounds(*at, ctypes.byref(b), *rows, 0) == 0
+        assert L.tfpa_select_blocks(*at, ctypes.byref(b), FAKE, *rows, 4, 1, 2, 2 * FAKE, 0) == 0
+        assert L.tfpa_decode_blocks(*at, FAKE, *rows, 64, 4, 2 * FAKE, 0.1, 3 * FAKE, None, 0) == 0
+    with B.record_launches() as rec:
+        for op in range(5):
+            a = B.tfpa_call_args(op=op, nseg=1, cache=ctypes.addressof(c.c()), segs=ctypes.addressof(segs.arr), row_seg=rows[0], row_pos=rows[1],
+                                 bounds=ctypes.addressof(b), q=FAKE, blocks=2 * FAKE, out=11 * FAKE if op == 1 else 3 * FAKE, rows=n, block=64, nsel=4,
+                                 sink=1, recent=2, softmax_scale=0.1)
+            if op == 0:
+                a.u.rope.spec, a.u.rope.first, a.u.rope.cos, a.u.rope.sin = ctypes.addressof(spec), 7, FAKE, 2 * FAKE
+            else:
+                a.u.qkv = q
+            assert L.tfpa_call(ctypes.string_at(ctypes.byref(a), ctypes.sizeof(a))) == 0
+    assert rec == direct and [r["kind"] for r in rec] == ["rope_table", "write_qkv", "key_bounds", "select_blocks", "decode_blocks"]
+    with B.record_launches() as rec:
+        for op in (-1, 5, 2**31 - 1):
+            a.op = op
+            assert L.tfpa_call(ctypes.string_at(ctypes.byref(a), ctypes.sizeof(a))) == B.TFPA_EINVAL
+        assert L.tfpa_call(None) == B.TFPA_EINVAL
+        a.op, a.softmax_scale = 4, 1e300                     # infinite as a float
+        assert L.tfpa_call(ctypes.string_at(ctypes.byref(a), ctypes.sizeof(a))) == B.TFPA_EINVAL
+    assert rec == []
+
+
+def test_row_tables_of_other_kinds():
+    """Lists, other integers, read-only and strided tables, and tables of two lengths."""
+    import numpy as np
+    frozen = np.array([998, 999], np.int32)
+    frozen.flags.writeable = False
+    for rs, rp in (([0, 0], [998, 999]), (np.zeros(2, np.int64), np.array([998, 999])), (np.zeros(2, np.int32), frozen),
+                   (np.zeros(4, np.int32)[::2], np.array([998, 5, 999, 5], np.int32)[::2])):
+        with B.record_launches() as rec:
+            B.tfpa_key_bounds(_cache(), [LONG], B.Bounds(64, FAKE), rs, rp, stream=0)
+        assert [(r["kind"], r["rows"], r["runs"]) for r in rec] == [("key_bounds", 2, 1)]
+    for f in (lambda: B.tfpa_key_bounds(_cache(), [LONG], B.Bounds(64, FAKE), [0, 0], [5], stream=0),
+              lambda: attend(rows=((0, 5),)) or B.tfpa_decode_blocks(_cache(), [LONG], FAKE, [0], [5, 6], Plane(1, 8, 4), 64, 0.1, FAKE, stream=0)):
+        with B.record_launches(), pytest.raises(ValueError):
+            f()
+
+
 def test_elements_of_another_size_are_refused():
     """A tensor of narrower elements would be read or written past its end."""
     torch = pytest.importorskip("torch")
