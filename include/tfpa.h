@@ -666,7 +666,8 @@ int tfpa_write_qkv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
  * head the smallest and then the largest stored K of every head dim is kept,
  * as the stored value without k_scale (exact in bf16 for every cache type; a
  * NaN counts as 0).  Bounds go with the pages: streams that share a page share
- * its bounds.  A call that stores, moves or restores keys leaves them as they
+ * its bounds (a block that one of them ends in is then taken up to the end of the
+ * one whose rows were called last: of two in one call, either).  A call that stores, moves or restores keys leaves them as they
  * are: tfpa_key_bounds brings them up to date. */
 typedef struct {
   int32_t block;
