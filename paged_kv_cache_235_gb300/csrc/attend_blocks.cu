@@ -23,9 +23,9 @@
 //               O^T = V^T P^T.  Each warp keeps its own softmax state.
 // What bounds it is the stream of K and V out of memory, with the start and the
 // cluster's end around it: 8 streams' lists of 4,096 bf16 keys (134 MB, a part a
-// CTA) take 26.5 us, 5.1 TB/s, one stream's 5.5 us.  With four draft rows a stream,
+// CTA) take 26.4 us, 5.1 TB/s, one stream's 5.5 us.  With four draft rows a stream,
 // whose lists mostly name the same blocks, it is the second-level cache's reads
-// over bf16 (32 lists of 2,048 keys: 36.5 us, 7.4 TB/s) and over the narrower types
+// over bf16 (32 lists of 2,048 keys: 37.1 us, 7.2 TB/s) and over the narrower types
 // the consumers' instructions, most of them conversions (e4m3 29.9 us, 4 bits 30.0,
 // an instruction in 55 % of the cycles; folding the parts' states is 1.5 us of it).
 #include "cluster.cuh"
@@ -166,17 +166,21 @@ __device__ __forceinline__ void load_q(const __nv_bfloat16* h, int c, float scal
 // O^T += V^T P^T over 16 keys at rows r0.. of the stage (V at sb).  keep:
 // masks of a lane's keys (columns 2c, 2c + 1 and 2c + 8, 2c + 9), which zero
 // what lies behind the row's position (a weight of 0 would not: 0 NaN = NaN).
+// pl: what bf16 leaves of the weights (over bf16 caches).
 template <int KV, int NT>
 __device__ __forceinline__ void add_pv(uint32_t sb, int r0, int lane, const uint32_t (&pb)[NT][2],
-                                       uint32_t keep0, uint32_t keep1, float (&o)[NT][8][4]) {
+                                       const uint32_t (&pl)[NT][2], uint32_t keep0, uint32_t keep1,
+                                       float (&o)[NT][8][4]) {
   const int gq = lane >> 2, c = lane & 3;
   auto mma = [&](int t, const uint32_t (&a)[4]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (Cfg<KV>::kF16)
+      if (Cfg<KV>::kF16) {
         mma_f16_free(o[n][t], a, pb[n][0], pb[n][1]);
-      else
+      } else {
         mma_bf16(o[n][t], a, pb[n][0], pb[n][1]);
+        mma_bf16(o[n][t], a, pl[n][0], pl[n][1]);
+      }
     }
   };
   if (KV == kKvBf16) {
@@ -531,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
                 for (int j = 0; j < 4; ++j) o[n][t][j] *= al[j & 1];
             }
           }
-          uint32_t pb[NT][2];
+          uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -541,18 +545,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
               s[n][2 + e] = fast_exp2(s[n][2 + e] - base);
               l[n][e] += s[n][e] + s[n][2 + e];
             }
-            // weights rounded to the operands' 16 bits; the sums are not
-            pb[n][0] = transpose8x8(C::kF16 ? pack_f16x2(s[n][0], s[n][1])
-                                            : pack_bf16x2(s[n][0], s[n][1]));
-            pb[n][1] = transpose8x8(C::kF16 ? pack_f16x2(s[n][2], s[n][3])
-                                            : pack_bf16x2(s[n][2], s[n][3]));
+            // Weights rounded to f16's 11 bits; bf16's 8 would show in out, which is
+            // rounded to them too: a weight's first 8 bits, and the rest rounded to 8
+            // more, which costs 0.2 us of a batch's 26.2.  (The rest is never 0 or negative beside a weight above 2^-102: an
+            // infinite V keeps its sign.)  The sums are not rounded.
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float x = s[n][2 * i], y = s[n][2 * i + 1];
+              if (C::kF16) {
+                pb[n][i] = transpose8x8(pack_f16x2(x, y));
+              } else {
+                auto rest = [](float v) {
+                  return fmaxf(v - __uint_as_float(__float_as_uint(v) & 0xFFFF0000u), v * 0x1p-24f);
+                };
+                pb[n][i] = transpose8x8(prmt(__float_as_uint(x), __float_as_uint(y), 0x7632));
+                pl[n][i] = transpose8x8(pack_bf16x2(rest(x), rest(y)));
+              }
+            }
           }
           // ---- O^T += V^T P^T
           auto mask = [&](int i) {
             return (key0 + key_of<KV>(2 * c + i) <= pos ? 0xFFFFu : 0u) |
                    (key0 + key_of<KV>(2 * c + 1 + i) <= pos ? 0xFFFF0000u : 0u);
           };
-          add_pv<KV, NT>(sk + C::kHalfStage, r0, lane, pb, mask(0), mask(8), o);
+          add_pv<KV, NT>(sk + C::kHalfStage, r0, lane, pb, pl, mask(0), mask(8), o);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[buf]);
