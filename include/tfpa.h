@@ -609,7 +609,7 @@ typedef struct {
   double base;                    /* > 1                                                   */
   double factor;                  /* >= 1 (not read for TFPA_ROPE_NONE)                    */
   double low, high;               /* TFPA_ROPE_BANDS, _RAMP: 0 < low < high                */
-  double attn_scale;              /* > 0; 1: none                                          */
+  double attn_scale;              /* > 0, also as a float; 1: none                         */
   int32_t rot_dim;                /* a multiple of 16, at most 128                         */
   int32_t scaling;
   int32_t orig_len;               /* TFPA_ROPE_BANDS, _RAMP: >= 1                          */
@@ -666,9 +666,10 @@ int tfpa_write_qkv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
  * head the smallest and then the largest stored K of every head dim is kept,
  * as the stored value without k_scale (exact in bf16 for every cache type; a
  * NaN counts as 0).  Bounds go with the pages: streams that share a page share
- * its bounds (a block that one of them ends in is then taken up to the end of the
- * one whose rows were called last: of two in one call, either).  A call that stores, moves or restores keys leaves them as they
- * are: tfpa_key_bounds brings them up to date. */
+ * its bounds (a block that one of them ends in is then taken up to the end of
+ * the one whose rows were called last: of two in one call, either).  A call that
+ * stores, moves or restores keys leaves them as they are: tfpa_key_bounds brings
+ * them up to date. */
 typedef struct {
   int32_t block;
   void* pool;                     /* DEVICE bf16 [num_pages][hkv][256 / block][2][128],    */

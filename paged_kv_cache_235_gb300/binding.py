@@ -835,8 +835,8 @@ def tfpa_select_blocks(cache: Cache, segs: Sequence[Seg], bounds: Bounds, q, row
     nsel = _list_shape(blocks, rows, cache.hkv)
     _check(lib().tfpa_call(_pack_call(
         _OP_SELECT_BLOCKS, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0,
-        _addressof(bounds.of(n)), _ptr(q) or 0, _ptr(blocks) or 0, 0, 0, rows, 0, nsel, sink, recent,
-        0, 0.0)), "tfpa_select_blocks")
+        _addressof(bounds.of(n)), _ptr(q) or 0, _ptr(blocks) or 0, 0, 0, rows, 0, nsel, sink,
+        recent, 0, 0.0)), "tfpa_select_blocks")
 
 
 def tfpa_decode_blocks(cache: Cache, segs: Sequence[Seg], q, row_seg, row_pos, blocks, block: int,
@@ -846,9 +846,9 @@ def tfpa_decode_blocks(cache: Cache, segs: Sequence[Seg], q, row_seg, row_pos, b
     rows, sp, pp, keep = _rows(row_seg, row_pos)
     nsel = _list_shape(blocks, rows, cache.hkv)
     _check(lib().tfpa_call(_pack_call(
-        _OP_DECODE_BLOCKS, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0, 0,
-        _ptr(q) or 0, _ptr(blocks) or 0, _ptr(out) or 0, _ptr(lse) or 0, rows, block, nsel, 0, 0, 0,
-        softmax_scale)), "tfpa_decode_blocks")
+        _OP_DECODE_BLOCKS, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0,
+        0, _ptr(q) or 0, _ptr(blocks) or 0, _ptr(out) or 0, _ptr(lse) or 0, rows, block, nsel, 0,
+        0, 0, softmax_scale)), "tfpa_decode_blocks")
 
 
 class Plan:

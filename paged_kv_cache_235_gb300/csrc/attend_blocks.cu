@@ -547,8 +547,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
             }
             // Weights rounded to f16's 11 bits; bf16's 8 would show in out, which is
             // rounded to them too: a weight's first 8 bits, and the rest rounded to 8
-            // more, which costs 0.2 us of a batch's 26.2.  (The rest is never 0 or negative beside a weight above 2^-102: an
-            // infinite V keeps its sign.)  The sums are not rounded.
+            // more, which costs 0.2 us of a batch's 26.2.  (The rest is never 0 or
+            // negative beside a weight above 2^-102: an infinite V keeps its sign.)
+            // The sums are not rounded.
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float x = s[n][2 * i], y = s[n][2 * i + 1];

@@ -1591,7 +1591,7 @@ uint64_t turns_of(double f) {
 int rope_freqs(const tfpa_rope_spec* r, double* freq) {
   if (!r || r->rot_dim < 16 || r->rot_dim > kHeadDim || r->rot_dim % 16) return TFPA_EINVAL;
   if (!std::isfinite(r->base) || !(r->base > 1.0) || !std::isfinite(r->attn_scale) ||
-      !(r->attn_scale > 0.0))
+      !((float)r->attn_scale > 0.f) || !std::isfinite((float)r->attn_scale))
     return TFPA_EINVAL;
   const int n = r->rot_dim / 2;
   const double d = r->rot_dim, f = r->factor;
@@ -1652,6 +1652,7 @@ extern "C" int tfpa_rope_table(const tfpa_rope_spec* spec, int64_t first, int32_
   p.first = first;
   p.n = n;
   p.attn_scale = (float)spec->attn_scale;
+  p.attn_rest = (float)(spec->attn_scale - (double)p.attn_scale);
   record(13, 0, n, 0, n, 0, 0, 0);
   return dry_run() ? TFPA_OK : to_err(launch_rope_table(p, nsm, stream));
 }

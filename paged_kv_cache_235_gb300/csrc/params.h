@@ -330,7 +330,7 @@ struct TableParams {
   int64_t first;              // position of the first row
   int32_t n;
   int32_t half;               // frequencies: rot_dim / 2
-  float attn_scale;
+  float attn_scale, attn_rest;   // the tables' factor, and what float32 leaves of it
 };
 
 // A projection's rows: norm, rotation, q out, K and V stored.

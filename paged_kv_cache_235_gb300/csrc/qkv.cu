@@ -8,7 +8,7 @@
 // its low bits and one in float64 costs its slow sine.  The fraction is
 // taken to within an eighth of a turn of a quarter turn (its top bits) and
 // only then rounded to float32.  Bound by the stores, 8 bytes an entry: 131,072
-// positions of 64 frequencies (67 MB) in 11.2 us, 6.0 TB/s, the integer pipe close
+// positions of 64 frequencies (67 MB) in 11.5 us, 5.8 TB/s, the integer pipe close
 // behind (five instructions an entry more, for the signs, cost 0.7 us).
 //
 // Rows.  A half-warp takes a q head, or a kv head's K and V, of a row, and where
@@ -35,21 +35,22 @@ namespace {
 constexpr int kTableThreads = 256;
 constexpr int kTableBlocks = 5;             // of a SM
 
-// sin and cos of |x| <= pi / 4 by their Taylor polynomials, cut where the next
-// term is below 2^-29 (x^11 / 11! and x^12 / 12!); with the few roundings of the
-// last steps both are within 1.5 2^-24 of the value at 1.
-__device__ __forceinline__ void sin_cos(float x, float& sn, float& cs) {
-  const float y = x * x;
+// sin and cos of |x| <= pi / 4, times scale + rest, by their Taylor polynomials, cut
+// where the next term is below 2^-29 (x^11 / 11! and x^12 / 12!).  The factor goes in
+// before the last step, whose rounding is then most of a value's error.
+__device__ __forceinline__ void sin_cos(float x, float scale, float rest, float& sn, float& cs) {
+  const float y = x * x, z = x * scale;
   float a = fmaf(y, 1.f / 362880.f, -1.f / 5040.f);
   a = fmaf(y, a, 1.f / 120.f);
   a = fmaf(y, a, -1.f / 6.f);
-  sn = fmaf(x * y, a, x);
+  sn = fmaf(z * y, a, z);
   float b = fmaf(y, -1.f / 3628800.f, 1.f / 40320.f);
   b = fmaf(y, b, -1.f / 720.f);
   b = fmaf(y, b, 1.f / 24.f);
   b = fmaf(y, b, -0.5f);
-  cs = fmaf(y, b, 1.f);
+  cs = fmaf(y * scale, b, rest) + scale;
 }
+
 // x, its sign flipped where the top bit of w is set.
 __device__ __forceinline__ float signed_as(float x, uint32_t w) {
   return __uint_as_float(__float_as_uint(x) ^ (w & 0x80000000u));
@@ -88,10 +89,10 @@ __global__ void __launch_bounds__(kTableThreads, kTableBlocks)
                            (float)(uint32_t)turn) *
                       (float)(6.283185307179586 * 0x1p-64);
       float sn, cs;
-      sin_cos(x, sn, cs);
+      sin_cos(x, p.attn_scale, p.attn_rest, sn, cs);
       const bool odd = hi & 0x40000000u;
-      c[j] = p.attn_scale * signed_as(odd ? sn : cs, hi + 0x40000000u);
-      s[j] = p.attn_scale * signed_as(odd ? cs : sn, hi);
+      c[j] = signed_as(odd ? sn : cs, hi + 0x40000000u);
+      s[j] = signed_as(odd ? cs : sn, hi);
     }
     const size_t to = (size_t)row * p.half + f0;
     *reinterpret_cast<float4*>(p.cos + to) = make_float4(c[0], c[1], c[2], c[3]);

@@ -44,6 +44,7 @@ def table(first=0, n=16, cos=FAKE, sin=2 * FAKE, **kw):
     (dict(base=1.0), B.TFPA_EINVAL), (dict(base=float("nan")), B.TFPA_EINVAL), (dict(base=float("inf")), B.TFPA_EINVAL),
     (dict(rot_dim=0), B.TFPA_EINVAL), (dict(rot_dim=8), B.TFPA_EINVAL), (dict(rot_dim=144), B.TFPA_EINVAL), (dict(rot_dim=40), B.TFPA_EINVAL),
     (dict(scaling="other"), B.TFPA_EINVAL), (dict(attn_scale=0.0), B.TFPA_EINVAL), (dict(attn_scale=float("inf")), B.TFPA_EINVAL),
+    (dict(attn_scale=1e39), B.TFPA_EINVAL), (dict(attn_scale=1e-60), B.TFPA_EINVAL),
     (dict(scaling="linear", factor=0.5), B.TFPA_EINVAL), (dict(scaling="base", factor=float("nan")), B.TFPA_EINVAL),
     (dict(scaling="base", factor=1e300, base=1e300), B.TFPA_EINVAL),
     (dict(scaling="bands", factor=2.0, low=1.0, high=4.0), B.TFPA_EINVAL), (dict(scaling="ramp", factor=2.0, orig_len=100, low=4.0, high=4.0), B.TFPA_EINVAL),
