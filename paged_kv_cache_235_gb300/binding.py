@@ -787,15 +787,21 @@ class Bounds(_Cached):
     pool: object = None               # bf16 [num_pages][hkv][256 / block][2][128]
     slabs: Optional[Sequence] = None  # bf16 [hkv][slab_cap / block][2][128] each
 
-    def _make_c(self) -> tfpa_bounds:
-        arr = None
-        if self.slabs is not None:
-            arr = (ctypes.c_void_p * max(1, len(self.slabs)))(*[_ptr(s) for s in self.slabs])
-            object.__setattr__(self, "_arr", arr)
-        return tfpa_bounds(self.block, _ptr(self.pool),
-                           None if arr is None else ctypes.addressof(arr))
+    def c(self) -> tfpa_bounds:
+        # the list may change in place: the pointers are those of its present entries
+        at = None if self.slabs is None else [_ptr(s) for s in self.slabs]
+        cs = self.__dict__.get("_cs")
+        if cs is None or cs.at != at:
+            arr = None if at is None else (ctypes.c_void_p * max(1, len(at)))(*at)
+            cs = tfpa_bounds(self.block, _ptr(self.pool),
+                             None if arr is None else ctypes.addressof(arr))
+            cs.at, cs.arr = at, arr
+            object.__setattr__(self, "_cs", cs)
+        return cs
 
     def of(self, nseg: int) -> tfpa_bounds:
+        """The struct for a call of nseg segments, which keeps it until the call is over (another
+        thread's call may put one of other entries in its place)."""
         if self.slabs is not None and len(self.slabs) != nseg:
             raise ValueError("slabs holds one entry per segment")
         return self.c()
@@ -813,9 +819,10 @@ def tfpa_key_bounds(cache: Cache, segs: Sequence[Seg], bounds: Bounds, row_seg, 
     """The bounds of every block that holds one of the rows, taken anew from the stored keys."""
     cs, n = _segs(segs)
     rows, sp, pp, keep = _rows(row_seg, row_pos)
+    bc = bounds.of(n)
     _check(lib().tfpa_call(_pack_call(
         _OP_KEY_BOUNDS, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0,
-        _addressof(bounds.of(n)), 0, 0, 0, 0, rows, 0, 0, 0, 0, 0, 0.0)), "tfpa_key_bounds")
+        _addressof(bc), 0, 0, 0, 0, rows, 0, 0, 0, 0, 0, 0.0)), "tfpa_key_bounds")
 
 
 def _list_shape(blocks, rows: int, hkv: int) -> int:
@@ -833,9 +840,10 @@ def tfpa_select_blocks(cache: Cache, segs: Sequence[Seg], bounds: Bounds, q, row
     cs, n = _segs(segs)
     rows, sp, pp, keep = _rows(row_seg, row_pos)
     nsel = _list_shape(blocks, rows, cache.hkv)
+    bc = bounds.of(n)
     _check(lib().tfpa_call(_pack_call(
         _OP_SELECT_BLOCKS, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0,
-        _addressof(bounds.of(n)), _ptr(q) or 0, _ptr(blocks) or 0, 0, 0, rows, 0, nsel, sink,
+        _addressof(bc), _ptr(q) or 0, _ptr(blocks) or 0, 0, 0, rows, 0, nsel, sink,
         recent, 0, 0.0)), "tfpa_select_blocks")
 
 
