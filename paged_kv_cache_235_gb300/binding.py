@@ -686,7 +686,7 @@ def tfpa_rope_table(spec: RopeSpec, first: int, cos, sin, stream=None) -> None:
     ``[n][rot_dim / 2]``), as many as they have."""
     want = (cos.shape[0], spec.rot_dim // 2)
     for t in (cos, sin):
-        _width(t, 4, "a table")
+        _typed(t, _FLOAT32, "a table")
         if tuple(t.shape) != want or not t.is_contiguous():
             raise ValueError(f"expected contiguous {list(want)} tables")
     _check(lib().tfpa_call(_pack_call_rope(
@@ -726,11 +726,38 @@ def _rows(row_seg, row_pos):
     return rows, sp, pp, (rs, rp)
 
 
-def _width(t, size: int, what: str) -> None:
-    """Refuses a tensor whose elements are not of the size that the call reads or writes."""
+class _Elements(dict):
+    """Whether a dtype is one of those that a call's operand may have, found out once a dtype."""
+
+    def __init__(self, *names: str):
+        super().__init__()
+        self.names = names
+
+    def __missing__(self, d) -> bool:
+        self[d] = ok = str(d).rpartition(".")[2] in self.names
+        return ok
+
+
+_BF16 = _Elements("bfloat16", "int16", "uint16")     # or its bits
+_FLOAT32 = _Elements("float32")
+_INTS = _Elements("int32", "uint32")
+
+
+def _typed(t, kind: _Elements, what: str) -> None:
+    """Refuses a tensor whose elements are not what the call reads or writes (an address, or what
+    else has no dtype, is taken as it is)."""
     d = getattr(t, "dtype", None)
-    if d is not None and d.itemsize != size:
-        raise ValueError(f"{what} must have elements of {size} bytes")
+    if d is not None and not kind[d]:
+        raise ValueError(f"{what} must be {kind.names[0]}, not {d}")
+
+
+def _weight(t, what: str) -> int:
+    """A norm weight's address."""
+    if hasattr(t, "data_ptr"):
+        _typed(t, _FLOAT32, what)
+        if t.numel() != HEAD_DIM or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous [{HEAD_DIM}]")
+    return _ptr(t) or 0
 
 
 def _heads(t, rows: int, heads: int, what: str) -> int:
@@ -738,6 +765,7 @@ def _heads(t, rows: int, heads: int, what: str) -> int:
     s = t.stride()
     if t.shape != (rows, heads, HEAD_DIM) or s[2] != 1 or (heads > 1 and s[1] != HEAD_DIM):
         raise ValueError(f"{what} must be [rows][heads][{HEAD_DIM}] with heads one after the other")
+    _typed(t, _BF16, what)
     return s[0] if rows > 1 else heads * HEAD_DIM
 
 
@@ -757,12 +785,12 @@ def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, r
         if rope_sin.shape != shape or not (rope_cos.is_contiguous()
                                            and rope_sin.is_contiguous()):
             raise ValueError("rope_cos and rope_sin must be contiguous tables of one shape")
-        _width(rope_cos, 4, "rope_cos")
-        _width(rope_sin, 4, "rope_sin")
-        if rope_pos is not None:
-            _width(rope_pos, 4, "rope_pos")
-            if getattr(rope_pos, "shape", (rows,)) != (rows,):
-                raise ValueError("rope_pos holds one position per row")
+        _typed(rope_cos, _FLOAT32, "rope_cos")
+        _typed(rope_sin, _FLOAT32, "rope_sin")
+        if hasattr(rope_pos, "data_ptr"):
+            _typed(rope_pos, _INTS, "rope_pos")
+            if rope_pos.shape != (rows,) or not rope_pos.is_contiguous():
+                raise ValueError("rope_pos must be contiguous, one position per row")
         cos, sin = rope_cos.data_ptr() or 0, rope_sin.data_ptr() or 0
     qp = qs = op = 0
     if q is not None:
@@ -770,12 +798,13 @@ def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, r
     if q_out is not None:
         if q_out.shape != (rows, hq, HEAD_DIM) or not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous [rows][hq][128]")
+        _typed(q_out, _BF16, "q_out")
         op = q_out.data_ptr() or 0
     _check(lib().tfpa_call(_pack_call_qkv(
         _OP_WRITE_QKV, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0, 0, 0,
         0, op, 0, rows, 0, 0, 0, 0, 0, 0.0, qp, k.data_ptr() or 0, v.data_ptr() or 0, qs,
-        _heads(k, rows, hkv, "k"), _heads(v, rows, hkv, "v"), _ptr(q_weight) or 0,
-        _ptr(k_weight) or 0, cos, sin, _ptr(rope_pos) or 0, table, 2 * half,
+        _heads(k, rows, hkv, "k"), _heads(v, rows, hkv, "v"), _weight(q_weight, "q_weight"),
+        _weight(k_weight, "k_weight"), cos, sin, _ptr(rope_pos) or 0, table, 2 * half,
         1 if interleaved else 0, eps)), "tfpa_write_qkv")
 
 
@@ -829,7 +858,7 @@ def _list_shape(blocks, rows: int, hkv: int) -> int:
     shape = blocks.shape
     if len(shape) != 3 or shape[0] != rows or shape[1] != hkv or not blocks.is_contiguous():
         raise ValueError("blocks must be contiguous [rows][hkv][nsel]")
-    _width(blocks, 4, "blocks")
+    _typed(blocks, _INTS, "blocks")
     return shape[2]
 
 

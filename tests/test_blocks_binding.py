@@ -3,8 +3,12 @@ library, and of what they refuse before they call it (no GPU)."""
 
 import ctypes
 
+import pytest
+import torch
+
 from paged_kv_cache_235_gb300 import binding as B
 from tests.test_blocks_host import FAKE, LONG, SLAB, bounds, select
+from tests.test_evict_host import _cache
 
 
 # ---------------------------------------------------------------- bounds of slabs
@@ -63,3 +67,71 @@ def test_what_a_call_was_handed_lives_until_it_is_over(monkeypatch):
         b.slabs[1] = FAKE
         f(rows=((1, 5),), b=b, segs=[LONG, SLAB])
     assert seen == [[64, FAKE, 0, FAKE]] * 2
+
+
+# ---------------------------------------------------------------- element types and sizes
+def refuses(what, f):
+    """A ValueError that names what is wrong, and no launch."""
+    with B.record_launches() as rec, pytest.raises(ValueError) as e:
+        f()
+    assert what in str(e.value) and not isinstance(e.value, B.TfpaError) and rec == []
+
+
+def rows_of(n=2, heads=8, dtype=torch.bfloat16):
+    return torch.zeros(n, heads, 128, dtype=dtype)
+
+
+def write(q=None, k=None, v=None, q_out=None, n=2, **kw):
+    k = rows_of(n) if k is None else k
+    v = rows_of(n) if v is None else v
+    B.tfpa_write_qkv(_cache(), [LONG], q, k, v, q_out, [0] * n, list(range(n)), stream=0, **kw)
+
+
+WRONG_ROWS = [torch.float32, torch.float16, torch.int8, torch.uint8, torch.float64, torch.int32]
+
+
+@pytest.mark.parametrize("dtype", WRONG_ROWS)
+def test_a_projections_rows_are_bf16(dtype):
+    """One-byte rows would be read (q_out written) past their end, others are other numbers."""
+    bad, q, out = rows_of(dtype=dtype), rows_of(heads=32), rows_of(heads=32)
+    refuses("k must", lambda: write(k=bad))
+    refuses("v must", lambda: write(v=bad))
+    refuses("q must", lambda: write(q=rows_of(heads=32, dtype=dtype), q_out=out))
+    refuses("q_out must", lambda: write(q=q, q_out=rows_of(heads=32, dtype=dtype)))
+
+
+@pytest.mark.parametrize("name", ["q_weight", "k_weight"])
+@pytest.mark.parametrize("w", [torch.ones(128, dtype=torch.bfloat16), torch.ones(128, dtype=torch.float16), torch.ones(128, dtype=torch.float64),
+                               torch.ones(64), torch.ones(127), torch.ones(8, 128), torch.ones(256)[::2], torch.ones(0)],
+                         ids=["bf16", "f16", "f64", "64", "127", "a head each", "strided", "none"])
+def test_weights_are_128_float32(name, w):
+    """Models hold them as bf16: 256 bytes, where 512 are read."""
+    refuses(name, lambda: write(q=rows_of(heads=32), q_out=rows_of(heads=32), **{name: w}))
+
+
+@pytest.mark.parametrize("pos", [torch.zeros(2), torch.zeros(2, dtype=torch.int64), torch.zeros(2, 2, dtype=torch.int32)[:, 0],
+                                 torch.zeros(4, dtype=torch.int32)[::2]], ids=["f32", "i64", "column", "strided"])
+def test_rotary_positions_are_int32_one_after_the_other(pos):
+    t = torch.zeros(8, 64)
+    refuses("rope_pos", lambda: write(rope_cos=t, rope_sin=t, rope_pos=pos))
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.float16, torch.float64])
+def test_tables_are_float32(dtype):
+    bad, good = torch.zeros(8, 64, dtype=dtype), torch.zeros(8, 64)
+    refuses("rope_cos", lambda: write(rope_cos=bad, rope_sin=good))
+    refuses("rope_sin", lambda: write(rope_cos=good, rope_sin=bad))
+    refuses("table", lambda: B.tfpa_rope_table(B.RopeSpec(1e4), 0, bad, good, stream=0))
+    refuses("table", lambda: B.tfpa_rope_table(B.RopeSpec(1e4), 0, good, bad, stream=0))
+
+
+def test_rows_weights_and_tables_that_are_right_are_taken():
+    """bf16, or its bits; weights of any shape of 128; addresses."""
+    t, w = torch.zeros(8, 64), torch.ones(1, 128)
+    with B.record_launches() as rec:
+        write(q=rows_of(heads=32), q_out=rows_of(heads=32), q_weight=w, k_weight=w[0], rope_cos=t, rope_sin=t,
+              rope_pos=torch.zeros(2, dtype=torch.int32))
+        write(k=rows_of(dtype=torch.int16), v=rows_of(dtype=torch.int16))
+        write(k_weight=FAKE, rope_cos=t, rope_sin=t, rope_pos=FAKE)
+        write(n=0)
+    assert [(r["kind"], r["rows"]) for r in rec] == [("write_qkv", 2)] * 3
