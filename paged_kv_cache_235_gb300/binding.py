@@ -751,6 +751,19 @@ def _typed(t, kind: _Elements, what: str) -> None:
         raise ValueError(f"{what} must be {kind.names[0]}, not {d}")
 
 
+def _rows_ptr(t, kind: _Elements, count: int, what: str) -> int:
+    """The address of an operand of ``count`` elements one after the other (or more: a buffer for
+    more rows than the call has)."""
+    try:
+        short = t.numel() < count or not t.is_contiguous() or not kind[t.dtype]
+    except AttributeError:                    # an address, or none
+        return _ptr(t) or 0
+    if short:
+        raise ValueError(f"{what} must be contiguous {kind.names[0]} of {count} elements, not "
+                         f"{t.dtype} {list(t.shape)} of strides {list(t.stride())}")
+    return t.data_ptr()
+
+
 def _weight(t, what: str) -> int:
     """A norm weight's address."""
     if hasattr(t, "data_ptr"):
@@ -865,27 +878,34 @@ def _list_shape(blocks, rows: int, hkv: int) -> int:
 def tfpa_select_blocks(cache: Cache, segs: Sequence[Seg], bounds: Bounds, q, row_seg, row_pos,
                        blocks, sink: int = 0, recent: int = 1, stream=None) -> None:
     """Each row's and kv head's blocks of largest bound into ``blocks`` (device int32
-    ``[rows][hkv][nsel]``), the first ``sink`` and the last ``recent`` among them."""
+    ``[rows][hkv][nsel]``), the first ``sink`` and the last ``recent`` among them.  ``q``: device
+    bf16 ``[rows][hq][128]``."""
     cs, n = _segs(segs)
     rows, sp, pp, keep = _rows(row_seg, row_pos)
     nsel = _list_shape(blocks, rows, cache.hkv)
     bc = bounds.of(n)
+    qp = _rows_ptr(q, _BF16, rows * cache.hq * HEAD_DIM, "q")
     _check(lib().tfpa_call(_pack_call(
         _OP_SELECT_BLOCKS, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0,
-        _addressof(bc), _ptr(q) or 0, _ptr(blocks) or 0, 0, 0, rows, 0, nsel, sink,
+        _addressof(bc), qp, _ptr(blocks) or 0, 0, 0, rows, 0, nsel, sink,
         recent, 0, 0.0)), "tfpa_select_blocks")
 
 
 def tfpa_decode_blocks(cache: Cache, segs: Sequence[Seg], q, row_seg, row_pos, blocks, block: int,
                        softmax_scale, out, lse=None, stream=None) -> None:
-    """Attention of each row over its own blocks (``blocks`` as tfpa_select_blocks leaves it)."""
+    """Attention of each row over its own blocks (``blocks`` as tfpa_select_blocks leaves it).
+    ``q`` and ``out``: device bf16 ``[rows][hq][128]``; ``lse``: device float32 ``[rows][hq]``."""
     cs, n = _segs(segs)
     rows, sp, pp, keep = _rows(row_seg, row_pos)
     nsel = _list_shape(blocks, rows, cache.hkv)
+    heads = rows * cache.hq
+    qp = _rows_ptr(q, _BF16, heads * HEAD_DIM, "q")
+    op = _rows_ptr(out, _BF16, heads * HEAD_DIM, "out")
+    lp = 0 if lse is None else _rows_ptr(lse, _FLOAT32, heads, "lse")
     _check(lib().tfpa_call(_pack_call(
         _OP_DECODE_BLOCKS, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0,
-        0, _ptr(q) or 0, _ptr(blocks) or 0, _ptr(out) or 0, _ptr(lse) or 0, rows, block, nsel, 0,
-        0, 0, softmax_scale)), "tfpa_decode_blocks")
+        0, qp, _ptr(blocks) or 0, op, lp, rows, block, nsel, 0, 0, 0, softmax_scale)),
+        "tfpa_decode_blocks")
 
 
 class Plan:

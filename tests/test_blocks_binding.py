@@ -135,3 +135,49 @@ def test_rows_weights_and_tables_that_are_right_are_taken():
         write(k_weight=FAKE, rope_cos=t, rope_sin=t, rope_pos=FAKE)
         write(n=0)
     assert [(r["kind"], r["rows"]) for r in rec] == [("write_qkv", 2)] * 3
+
+
+def lists(n=2, nsel=4):
+    return torch.zeros(n, 8, nsel, dtype=torch.int32)
+
+
+def choose(q, n=2):
+    B.tfpa_select_blocks(_cache(), [LONG], B.Bounds(64, FAKE), q, [0] * n, list(range(n)), lists(n), stream=0)
+
+
+def attend(q, out=FAKE, lse=None, n=2):
+    B.tfpa_decode_blocks(_cache(), [LONG], q, [0] * n, list(range(n)), lists(n), 64, 0.1, out, lse, stream=0)
+
+
+HEADS = rows_of(heads=32)
+WRONG_HEADS = {"f32": HEADS.float(), "f16": HEADS.half(), "i8": HEADS.to(torch.int8), "one row": HEADS[:1], "a head less": HEADS[:, :31].contiguous(),
+               "strided": rows_of(heads=64)[:, ::2], "rows apart": rows_of(heads=48)[:, :32], "transposed": rows_of(32, 2).transpose(0, 1),
+               "none": HEADS[:0]}
+
+
+@pytest.mark.parametrize("name", WRONG_HEADS)
+def test_q_and_out_are_bf16_of_every_row(name):
+    """What is smaller than the rows' heads would be read, or written, past its end."""
+    bad = WRONG_HEADS[name]
+    refuses("q must", lambda: choose(bad))
+    refuses("q must", lambda: attend(bad))
+    refuses("out must", lambda: attend(HEADS, bad))
+
+
+@pytest.mark.parametrize("lse", [torch.zeros(2, 32, dtype=torch.bfloat16), torch.zeros(2, 32, dtype=torch.float64), torch.zeros(1, 32),
+                                 torch.zeros(2, 31), torch.zeros(2, 64)[:, ::2], torch.zeros(32, 2).t()],
+                         ids=["bf16", "f64", "one row", "a head less", "strided", "transposed"])
+def test_lse_is_float32_of_every_row(lse):
+    refuses("lse must", lambda: attend(HEADS, HEADS, lse))
+
+
+def test_q_out_and_lse_that_are_right_are_taken():
+    """Any shape that holds the rows, buffers for more rows among them; bf16's bits; addresses."""
+    with B.record_launches() as rec:
+        choose(HEADS)
+        choose(HEADS.view(2, -1).view(torch.int16))
+        attend(HEADS, HEADS.clone(), torch.zeros(2, 32))
+        attend(rows_of(9, 32), rows_of(9, 32).view(-1), torch.zeros(9 * 32))
+        attend(FAKE, FAKE, FAKE)
+        attend(HEADS[:0], HEADS[:0], torch.zeros(0, 32), n=0)
+    assert [r["kind"] for r in rec] == ["select_blocks"] * 2 + ["decode_blocks"] * 3
