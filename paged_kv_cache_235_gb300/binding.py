@@ -837,16 +837,36 @@ class Bounds(_Cached):
             arr = None if at is None else (ctypes.c_void_p * max(1, len(at)))(*at)
             cs = tfpa_bounds(self.block, _ptr(self.pool),
                              None if arr is None else ctypes.addressof(arr))
-            cs.at, cs.arr = at, arr
+            cs.at, cs.arr, cs.fits = at, arr, None
             object.__setattr__(self, "_cs", cs)
         return cs
 
-    def of(self, nseg: int) -> tfpa_bounds:
-        """The struct for a call of nseg segments, which keeps it until the call is over (another
-        thread's call may put one of other entries in its place)."""
-        if self.slabs is not None and len(self.slabs) != nseg:
-            raise ValueError("slabs holds one entry per segment")
-        return self.c()
+    def of(self, cache: Cache, segs) -> tfpa_bounds:
+        """The struct for a call, which keeps it until the call is over (another thread's call may
+        put one of other entries in its place).  Tensors have to be of the shapes above."""
+        cs, per = self.c(), PAGE // max(1, self.block)
+        if cs.fits != (cache.hkv, cache.num_pages):
+            _bounds_shape(self.pool, cache.num_pages, cache.hkv, per)
+            cs.fits = cache.hkv, cache.num_pages
+        if self.slabs is not None:
+            if len(self.slabs) != len(segs):
+                raise ValueError("slabs holds one entry per segment")
+            for t, s in zip(self.slabs, segs):
+                if s.page_table is None:
+                    _bounds_shape(t, cache.hkv, s.slab_cap // PAGE * per)
+        return cs
+
+
+def _bounds_shape(t, *want: int) -> None:
+    """Refuses bounds of other shapes than ``[want..][2][128]``, but for a pool (three numbers) of
+    more pages.  (An address has no shape.)"""
+    if not hasattr(t, "data_ptr"):
+        return
+    shape, full = tuple(t.shape), (*want, 2, HEAD_DIM)
+    if (shape[1:] != full[1:] or shape[0] < want[0] or (len(want) < 3 and shape[0] != want[0])
+            or not t.is_contiguous()):
+        raise ValueError(f"bounds of shape {list(shape)} where contiguous {list(full)} is needed")
+    _typed(t, _BF16, "bounds of a pool or slab")
 
 
 def make_bounds(num_pages: int, hkv: int, block: int, device="cuda") -> Bounds:
@@ -861,7 +881,7 @@ def tfpa_key_bounds(cache: Cache, segs: Sequence[Seg], bounds: Bounds, row_seg, 
     """The bounds of every block that holds one of the rows, taken anew from the stored keys."""
     cs, n = _segs(segs)
     rows, sp, pp, keep = _rows(row_seg, row_pos)
-    bc = bounds.of(n)
+    bc = bounds.of(cache, segs)
     _check(lib().tfpa_call(_pack_call(
         _OP_KEY_BOUNDS, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0,
         _addressof(bc), 0, 0, 0, 0, rows, 0, 0, 0, 0, 0, 0.0)), "tfpa_key_bounds")
@@ -883,7 +903,7 @@ def tfpa_select_blocks(cache: Cache, segs: Sequence[Seg], bounds: Bounds, q, row
     cs, n = _segs(segs)
     rows, sp, pp, keep = _rows(row_seg, row_pos)
     nsel = _list_shape(blocks, rows, cache.hkv)
-    bc = bounds.of(n)
+    bc = bounds.of(cache, segs)
     qp = _rows_ptr(q, _BF16, rows * cache.hq * HEAD_DIM, "q")
     _check(lib().tfpa_call(_pack_call(
         _OP_SELECT_BLOCKS, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0,

@@ -181,3 +181,70 @@ def test_q_out_and_lse_that_are_right_are_taken():
         attend(FAKE, FAKE, FAKE)
         attend(HEADS[:0], HEADS[:0], torch.zeros(0, 32), n=0)
     assert [r["kind"] for r in rec] == ["select_blocks"] * 2 + ["decode_blocks"] * 3
+
+
+# ---------------------------------------------------------------- the size of bounds
+class Pool:
+    """A pool's shape and type without its memory."""
+
+    def __init__(self, *shape, dtype=torch.bfloat16, dense=True, ptr=FAKE):
+        self.shape, self.dtype, self._dense, self._p = torch.Size(shape), dtype, dense, ptr
+
+    def is_contiguous(self):
+        return self._dense
+
+    def data_ptr(self):
+        return self._p
+
+
+WRONG_POOLS = {"blocks of 128": Pool(4096, 8, 2, 2, 128), "blocks of 256": Pool(4096, 8, 1, 2, 128), "fewer pages": Pool(4095, 8, 4, 2, 128),
+               "a head less": Pool(4096, 7, 4, 2, 128), "a head more": Pool(4096, 9, 4, 2, 128), "one bound": Pool(4096, 8, 4, 1, 128),
+               "narrow": Pool(4096, 8, 4, 2, 64), "f32": Pool(4096, 8, 4, 2, 128, dtype=torch.float32),
+               "i8": Pool(4096, 8, 4, 2, 128, dtype=torch.int8), "strided": Pool(4096, 8, 4, 2, 128, dense=False),
+               "flat": Pool(4096 * 8 * 4 * 256)}
+
+
+@pytest.mark.parametrize("name", WRONG_POOLS)
+def test_a_pool_of_bounds_has_the_caches_shape(name):
+    """Bounds of 128 positions under blocks of 64 were written past the pool's end."""
+    for f in (bounds, select):
+        refuses("bounds of", lambda: f(b=B.Bounds(64, WRONG_POOLS[name])))
+        refuses("bounds of", lambda: f(b=B.Bounds(64, WRONG_POOLS[name], [None])))
+
+
+def test_a_pool_is_looked_at_again_for_another_cache_and_another_block():
+    b = B.Bounds(64, Pool(4096, 8, 4, 2, 128))
+    with B.record_launches() as rec:
+        bounds(b=b)
+        bounds(b=b)
+        bounds(b=B.Bounds(128, Pool(5000, 8, 2, 2, 128, dtype=torch.int16)))
+        bounds(b=B.Bounds(64, Pool(4096, 8, 4, 2, 128)), cache=_cache(num_pages=4000))
+    assert len(rec) == 4
+    refuses("bounds of", lambda: bounds(b=b, cache=_cache(num_pages=4097)))
+    refuses("bounds of", lambda: bounds(b=b, cache=_cache(hq=8, hkv=4)))
+    b.block = 128
+    refuses("bounds of", lambda: bounds(b=b))
+    b.block, b.pool = 64, Pool(4096, 8, 2, 2, 128)
+    refuses("bounds of", lambda: bounds(b=b))
+
+
+WRONG_SLABS = {"blocks of 128": Pool(8, 6, 2, 128), "a block less": Pool(8, 11, 2, 128), "a head less": Pool(7, 12, 2, 128),
+               "f32": Pool(8, 12, 2, 128, dtype=torch.float32), "strided": Pool(8, 12, 2, 128, dense=False)}
+
+
+@pytest.mark.parametrize("name", WRONG_SLABS)
+@pytest.mark.parametrize("table", [False, True])
+def test_bounds_of_a_slab_have_its_shape(name, table):
+    """A slab of 768 positions has twelve blocks of 64; heads lie slab_cap / block blocks apart."""
+    segs = [LONG, SLAB]
+    segs = B.SegTable(segs) if table else segs
+    b = B.Bounds(64, FAKE, [None, Pool(8, 12, 2, 128)])
+    for f in (bounds, select):
+        with B.record_launches() as rec:
+            f(rows=((1, 5),), b=b, segs=segs)
+        assert len(rec) == 1
+        refuses("bounds of", lambda: f(rows=((1, 5),), b=B.Bounds(64, FAKE, [None, WRONG_SLABS[name]]), segs=segs))
+    b.slabs[1] = WRONG_SLABS[name]
+    refuses("bounds of", lambda: bounds(rows=((1, 5),), b=b, segs=segs))
+    longer = B.Seg(700, k_slab=FAKE, v_slab=FAKE, slab_cap=1024)
+    refuses("bounds of", lambda: bounds(rows=((1, 5),), b=B.Bounds(64, FAKE, [None, Pool(8, 12, 2, 128)]), segs=[LONG, longer]))
