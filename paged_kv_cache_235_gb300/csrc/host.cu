@@ -1699,12 +1699,20 @@ int qkv_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const tfpa
   if (in->q && rows > 0) {
     // q_out may be q itself, row for row; else it shares no memory with an input
     const int64_t out_bytes = (int64_t)rows * c->hq * hd * 2;
-    const auto shares = [&](const void* p, int64_t stride, int64_t heads) {
-      return overlap(q_out, out_bytes, p, ((rows - 1) * stride + heads * hd) * 2);
+    const auto shares = [&](const void* p, int64_t bytes) {
+      return p && overlap(q_out, out_bytes, p, bytes);
+    };
+    const auto shares_rows = [&](const void* p, int64_t stride, int64_t heads) {
+      return shares(p, ((rows - 1) * stride + heads * hd) * 2);
     };
     const bool in_place = q_out == in->q && in->q_stride == c->hq * hd;
-    if ((!in_place && shares(in->q, in->q_stride, c->hq)) ||
-        shares(in->k, in->k_stride, c->hkv) || shares(in->v, in->v_stride, c->hkv))
+    if ((!in_place && shares_rows(in->q, in->q_stride, c->hq)) ||
+        shares_rows(in->k, in->k_stride, c->hkv) || shares_rows(in->v, in->v_stride, c->hkv) ||
+        shares(in->q_weight, hd * 4) || shares(in->k_weight, hd * 4))
+      return TFPA_EINVAL;
+    const int64_t table = in->rope_cos ? (int64_t)in->rope_n * (in->rot_dim / 2) * 4 : 0;
+    if (in->rope_cos && (shares(in->rope_cos, table) || shares(in->rope_sin, table) ||
+                         shares(in->rope_pos, (int64_t)rows * 4)))
       return TFPA_EINVAL;
   }
   thread_local std::vector<Run> runs;   // reused by every call of this thread
