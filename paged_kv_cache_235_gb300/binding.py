@@ -793,6 +793,8 @@ def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, r
     rows, sp, pp, keep = _rows(row_seg, row_pos)
     hq, hkv = cache.hq, cache.hkv
     table = half = cos = sin = 0
+    if (rope_cos is None) != (rope_sin is None):
+        raise ValueError("rope_cos and rope_sin come together")
     if rope_cos is not None:
         table, half = shape = rope_cos.shape
         if rope_sin.shape != shape or not (rope_cos.is_contiguous()

@@ -125,6 +125,13 @@ def test_tables_are_float32(dtype):
     refuses("table", lambda: B.tfpa_rope_table(B.RopeSpec(1e4), 0, good, bad, stream=0))
 
 
+def test_tables_come_together():
+    """One of the two alone was an AttributeError, or K and q unrotated without a word."""
+    t = torch.zeros(8, 64)
+    refuses("rope_cos and rope_sin", lambda: write(rope_sin=t))
+    refuses("rope_cos and rope_sin", lambda: write(rope_cos=t))
+
+
 def test_rows_weights_and_tables_that_are_right_are_taken():
     """bf16, or its bits; weights of any shape of 128; addresses."""
     t, w = torch.zeros(8, 64), torch.ones(1, 128)
