@@ -686,7 +686,8 @@ def tfpa_rope_table(spec: RopeSpec, first: int, cos, sin, stream=None) -> None:
     ``[n][rot_dim / 2]``), as many as they have."""
     want = (cos.shape[0], spec.rot_dim // 2)
     for t in (cos, sin):
-        _typed(t, _FLOAT32, "a table")
+        if not _FLOAT32[getattr(t, "dtype", None)]:
+            raise _other_type(t, _FLOAT32, "a table")
         if tuple(t.shape) != want or not t.is_contiguous():
             raise ValueError(f"expected contiguous {list(want)} tables")
     _check(lib().tfpa_call(_pack_call_rope(
@@ -727,10 +728,11 @@ def _rows(row_seg, row_pos):
 
 
 class _Elements(dict):
-    """Whether a dtype is one of those that a call's operand may have, found out once a dtype."""
+    """Whether a dtype is one of those that a call's operand may have, found out once a dtype (what
+    has no dtype, as an address, is taken as it is)."""
 
     def __init__(self, *names: str):
-        super().__init__()
+        super().__init__({None: True})
         self.names = names
 
     def __missing__(self, d) -> bool:
@@ -743,34 +745,32 @@ _FLOAT32 = _Elements("float32")
 _INTS = _Elements("int32", "uint32")
 
 
-def _typed(t, kind: _Elements, what: str) -> None:
-    """Refuses a tensor whose elements are not what the call reads or writes (an address, or what
-    else has no dtype, is taken as it is)."""
-    d = getattr(t, "dtype", None)
-    if d is not None and not kind[d]:
-        raise ValueError(f"{what} must be {kind.names[0]}, not {d}")
+def _other_type(t, kind: _Elements, what: str) -> ValueError:
+    return ValueError(f"{what} must be {kind.names[0]}, not {t.dtype}")
 
 
 def _rows_ptr(t, kind: _Elements, count: int, what: str) -> int:
     """The address of an operand of ``count`` elements one after the other (or more: a buffer for
     more rows than the call has)."""
     try:
-        short = t.numel() < count or not t.is_contiguous() or not kind[t.dtype]
-    except AttributeError:                    # an address, or none
+        if kind[t.dtype] and t.numel() >= count and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not hasattr(t, "data_ptr") or not hasattr(t, "dtype"):     # an address, or none
         return _ptr(t) or 0
-    if short:
-        raise ValueError(f"{what} must be contiguous {kind.names[0]} of {count} elements, not "
-                         f"{t.dtype} {list(t.shape)} of strides {list(t.stride())}")
-    return t.data_ptr()
+    raise ValueError(f"{what} must be contiguous {kind.names[0]} of {count} elements, not "
+                     f"{t.dtype} {list(t.shape)} of strides {list(t.stride())}")
 
 
 def _weight(t, what: str) -> int:
     """A norm weight's address."""
-    if hasattr(t, "data_ptr"):
-        _typed(t, _FLOAT32, what)
-        if t.numel() != HEAD_DIM or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous [{HEAD_DIM}]")
-    return _ptr(t) or 0
+    if t is None:
+        return 0
+    p = _rows_ptr(t, _FLOAT32, HEAD_DIM, what)
+    if type(t) is not int and hasattr(t, "numel") and t.numel() != HEAD_DIM:
+        raise ValueError(f"{what} holds {HEAD_DIM} values")
+    return p
 
 
 def _heads(t, rows: int, heads: int, what: str) -> int:
@@ -778,7 +778,8 @@ def _heads(t, rows: int, heads: int, what: str) -> int:
     s = t.stride()
     if t.shape != (rows, heads, HEAD_DIM) or s[2] != 1 or (heads > 1 and s[1] != HEAD_DIM):
         raise ValueError(f"{what} must be [rows][heads][{HEAD_DIM}] with heads one after the other")
-    _typed(t, _BF16, what)
+    if not _BF16[getattr(t, "dtype", None)]:
+        raise _other_type(t, _BF16, what)
     return s[0] if rows > 1 else heads * HEAD_DIM
 
 
@@ -800,10 +801,13 @@ def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, r
         if rope_sin.shape != shape or not (rope_cos.is_contiguous()
                                            and rope_sin.is_contiguous()):
             raise ValueError("rope_cos and rope_sin must be contiguous tables of one shape")
-        _typed(rope_cos, _FLOAT32, "rope_cos")
-        _typed(rope_sin, _FLOAT32, "rope_sin")
+        if not _FLOAT32[getattr(rope_cos, "dtype", None)]:
+            raise _other_type(rope_cos, _FLOAT32, "rope_cos")
+        if not _FLOAT32[getattr(rope_sin, "dtype", None)]:
+            raise _other_type(rope_sin, _FLOAT32, "rope_sin")
         if hasattr(rope_pos, "data_ptr"):
-            _typed(rope_pos, _INTS, "rope_pos")
+            if not _INTS[getattr(rope_pos, "dtype", None)]:
+                raise _other_type(rope_pos, _INTS, "rope_pos")
             if rope_pos.shape != (rows,) or not rope_pos.is_contiguous():
                 raise ValueError("rope_pos must be contiguous, one position per row")
         cos, sin = rope_cos.data_ptr() or 0, rope_sin.data_ptr() or 0
@@ -813,7 +817,8 @@ def tfpa_write_qkv(cache: Cache, segs: Sequence[Seg], q, k, v, q_out, row_seg, r
     if q_out is not None:
         if q_out.shape != (rows, hq, HEAD_DIM) or not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous [rows][hq][128]")
-        _typed(q_out, _BF16, "q_out")
+        if not _BF16[getattr(q_out, "dtype", None)]:
+            raise _other_type(q_out, _BF16, "q_out")
         op = q_out.data_ptr() or 0
     _check(lib().tfpa_call(_pack_call_qkv(
         _OP_WRITE_QKV, n, _addressof(cache.c()), _addressof(cs), sp, pp, _stream(stream) or 0, 0, 0,
@@ -846,11 +851,12 @@ class Bounds(_Cached):
     def of(self, cache: Cache, segs) -> tfpa_bounds:
         """The struct for a call, which keeps it until the call is over (another thread's call may
         put one of other entries in its place).  Tensors have to be of the shapes above."""
-        cs, per = self.c(), PAGE // max(1, self.block)
+        cs = self.c()
         if cs.fits != (cache.hkv, cache.num_pages):
-            _bounds_shape(self.pool, cache.num_pages, cache.hkv, per)
+            _bounds_shape(self.pool, cache.num_pages, cache.hkv, PAGE // max(1, self.block))
             cs.fits = cache.hkv, cache.num_pages
         if self.slabs is not None:
+            per = PAGE // max(1, self.block)
             if len(self.slabs) != len(segs):
                 raise ValueError("slabs holds one entry per segment")
             for t, s in zip(self.slabs, segs):
@@ -868,7 +874,8 @@ def _bounds_shape(t, *want: int) -> None:
     if (shape[1:] != full[1:] or shape[0] < want[0] or (len(want) < 3 and shape[0] != want[0])
             or not t.is_contiguous()):
         raise ValueError(f"bounds of shape {list(shape)} where contiguous {list(full)} is needed")
-    _typed(t, _BF16, "bounds of a pool or slab")
+    if not _BF16[getattr(t, "dtype", None)]:
+        raise _other_type(t, _BF16, "bounds of a pool or slab")
 
 
 def make_bounds(num_pages: int, hkv: int, block: int, device="cuda") -> Bounds:
@@ -893,7 +900,8 @@ def _list_shape(blocks, rows: int, hkv: int) -> int:
     shape = blocks.shape
     if len(shape) != 3 or shape[0] != rows or shape[1] != hkv or not blocks.is_contiguous():
         raise ValueError("blocks must be contiguous [rows][hkv][nsel]")
-    _typed(blocks, _INTS, "blocks")
+    if not _INTS[getattr(blocks, "dtype", None)]:
+        raise _other_type(blocks, _INTS, "blocks")
     return shape[2]
 
 
