@@ -696,7 +696,7 @@ int tfpa_key_bounds(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
  * which (k_scale above 0) no sum of the heads' scores with a key of the block
  * exceeds, k_scale and softmax_scale left out; ties go to
  * the lower block, and a score that is not a number (an infinite bound under a
- * zero of q) counts as largest.  The choice is that of exact arithmetic: scores
+ * zero of q) counts as larger than an infinite one.  The choice is that of exact arithmetic: scores
  * too near the border for float32 are taken in 64 bits.
  *   q      : DEVICE bf16 [rows][hq][128], 16-byte aligned (as tfpa_decode's)
  *   blocks : DEVICE int32 [rows][hkv][nsel], written: block numbers ascending,

@@ -1,5 +1,5 @@
-"""Blocks and attention over them on the GPU, at the ends of their definitions: scores that 64 bits cannot tell, batches
-of more streams than a launch takes."""
+"""Blocks and attention over them on the GPU, at the ends of their definitions: scores that are no numbers, scores that
+64 bits cannot tell, batches of more streams than a launch takes."""
 
 from fractions import Fraction
 
@@ -22,6 +22,19 @@ def selected(c, b, q, rs, rp, nsel, sink=0, recent=0):
 
 
 # ---------------------------------------------------------------- selection
+@pytest.mark.parametrize("L", [3000, 20000])               # few blocks too near to tell, and many
+def test_a_score_that_is_no_number_counts_as_largest(L):
+    """NaN (0 times an infinite bound) before +inf, and of each the lower block first."""
+    c, b, rs, rp = one(L)
+    q = c.q(1).abs()
+    q[..., 4] = 0.0
+    at = blocks_of(c, b)
+    for blk, dim in ((5, 9), (11, 4), (17, 9), (20, 4), (31, 9)):      # dim 9: +inf; dim 4, under zeros of q: NaN
+        b.pool[at[blk][0], :, at[blk][1], 1, dim] = float("inf")
+    for nsel, want in ((1, [11]), (2, [11, 20]), (3, [5, 11, 20]), (4, [5, 11, 17, 20]), (5, [5, 11, 17, 20, 31])):
+        assert selected(c, b, q, rs, rp, nsel)[0, 0].tolist() == want
+
+
 @pytest.mark.parametrize("n", [47, 200])
 def test_scores_that_64_bits_cannot_tell(n):
     """Large bounds that cancel: a chosen block's exact score is below another's by no more than the two sums' roundings."""
