@@ -1,5 +1,5 @@
 """Blocks and attention over them on the GPU, at the ends of their definitions: scores that are no numbers, scores that
-64 bits cannot tell, batches of more streams than a launch takes."""
+64 bits cannot tell, weights far below a row's largest, batches of more streams than a launch takes."""
 
 from fractions import Fraction
 
@@ -8,8 +8,8 @@ import pytest
 import torch
 
 from paged_kv_cache_235_gb300 import binding as B
-from tests.gpu64 import LongCase, last_rows
-from tests.test_gpu_blocks import (attend64, blocks_of, bound_store, bound_view, check_choice, exact_bounds, one,
+from tests.gpu64 import SCALE, LongCase, last_rows
+from tests.test_gpu_blocks import (KVS, attend64, blocks_of, bound_store, bound_view, check_choice, exact_bounds, one,
                                    random_bounds, random_lists, run_attend)
 
 pytestmark = pytest.mark.gpu
@@ -113,3 +113,35 @@ def test_a_batch_in_which_one_cta_chooses_for_a_row(streams, L):
     pick = np.array([0, 1, 33, 62, 63, 64, 65, streams - 1])
     at = torch.from_numpy(pick).cuda()
     check_choice(c, b, q[at].contiguous(), rs[pick], rp[pick], 20, 1, 2, got=got[at])
+
+
+# ---------------------------------------------------------------- attention
+@pytest.mark.parametrize("kv", KVS)
+@pytest.mark.parametrize("nsel", [2, 16, 64])
+def test_weights_far_below_a_rows_largest(kv, nsel):
+    """A sixteenth of the keys takes nearly all the weight and has no value: what comes out is the sum of weights of
+    2^-20 to 2^-28 of the largest."""
+    c = LongCase(kv, [4096], [True], 4, 1, 208)
+    k, v = torch.zeros(4096, 1, 128, dtype=torch.bfloat16, device="cuda"), torch.ones(4096, 1, 128, dtype=torch.bfloat16, device="cuda")
+    k[::16, :, 0], v[::16] = 4.0, 0.0
+    v[:, :, 64:] *= -0.5
+    B.tfpa_write_kv(c.cache, c.segs, k, v, np.zeros(4096), np.arange(4096))
+    k0 = float(c.values(0, 0, 0)[0, 0])                # 4 as it is stored
+    q = torch.zeros(1, 4, 128, dtype=torch.bfloat16, device="cuda")
+    q[0, :, 0] = torch.tensor([20.0, 24.0, 26.0, 28.0], device="cuda") * float(np.log(2)) / (SCALE * k0)
+    lists = random_lists(c, [0], [4095], nsel, 64, 209)
+    out, lse = run_attend(c, q, [0], [4095], lists, 64)
+    ref, rl, tol, ltol = attend64(c, q, [0], [4095], lists, 64)
+    # tol has an absolute part of 2^-25 of the largest weight a key, which would let all of these go; here a key's
+    # weight may be off by 2^-32 of the largest (f16's last bit, 2^-24, halved, of weights up to 2^7)
+    K, V = c.values(0, 0, 0), c.values(0, 1, 0)
+    key = (lists[0, 0].long()[:, None] * 64 + torch.arange(64, device="cuda")).flatten()
+    e = (SCALE * q[0].double() @ K[key].T)
+    e = (e - e.amax(-1, keepdim=True)).exp()
+    z = e.sum(-1, keepdim=True)
+    es = 2 * 128 * 2.0 ** -24 * 28 * float(np.log(2)) + 2.0 ** -20           # of a score, as attend64 has it
+    small = 2.0 ** -8 * ref[0].abs() + (e @ V[key].abs() / z) * (2.0 ** -11 + 2 * es) + len(key) * 2.0 ** -32 / z * V.abs().max()
+    err = (out[0].double() - ref[0]).abs()
+    assert (ref[0].abs() > 4 * small).all()            # the test tells them from nothing
+    assert (err <= small).all(), (err / small).max()
+    assert ((lse.double() - rl).abs() <= ltol).all()
