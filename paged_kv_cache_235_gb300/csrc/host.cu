@@ -1944,12 +1944,21 @@ int32_t block_parts(int32_t block, int32_t nsel) {
   return (int32_t)std::min<int64_t>(8, ((int64_t)nsel * (block / 64) + 1) / 2);
 }
 
-// Parts that a CTA takes one after the other: as few as let the launch have four
-// CTAs a SM at most (a step with 32 rows' lists of 2,048 keys over 4 bits, 256 items
-// of eight parts: a part each 68.9 us, two 61.6, four 58.8, eight 73.8).
-int32_t cta_parts(int64_t items, int32_t parts, int nsm) {
+// Parts that a CTA takes one after the other: as few as let the launch have as many
+// CTAs a SM as the kernel is built for, four with up to eight query vectors and two
+// with more (by their registers).  A part each, two, four and eight, in us, the
+// rule's choice starred:
+//   32 lists of 2,048 keys of 8 kv heads, 4 heads each (256 items):
+//     bf16 48.6  42.8  37.2*  52.4;  e4m3 40.0  33.3  30.0*  42.3;  4 bits 40.3  33.1  30.1*  47.0
+//   8 lists of 4,096 keys of 8 kv heads (64 items), 4 heads each:
+//     bf16 26.6*  32.2  42.8  69.1;  e4m3 18.5*  23.8  30.6  46.0;  4 bits 16.4*  23.8  30.6  46.2
+//   8 heads each (three CTAs a SM fit over bf16 and e4m3): bf16 27.6*  33.3  45.7;  e4m3 19.3*  25.1  34.4
+//   16 heads each: bf16 38.0  33.0*  51.3;  e4m3 28.6  23.5*  38.2;  4 bits 28.4  23.2*  39.2
+//   32 heads each (128 items): bf16 65.1  56.4  51.9*;  e4m3 52.2  43.7  39.3*;  4 bits 54.8  45.0  40.7*
+int32_t cta_parts(int64_t items, int32_t parts, int32_t group, int nsm) {
+  const int64_t at_once = (group <= 8 ? 4 : 2) * (int64_t)nsm;
   int32_t k = 1;
-  while (k < parts && items * ((parts + k - 1) / k) > 4 * (int64_t)nsm) k *= 2;
+  while (k < parts && items * ((parts + k - 1) / k) > at_once) k *= 2;
   return std::min(k, parts);
 }
 
@@ -2025,7 +2034,7 @@ int blocks_impl(const tfpa_cache* c, const tfpa_seg* segs, int32_t nseg, const v
       if ((e = fill_maps(c, segs, ss, fp8, fp8 ? 128 : 64, fp8 ? 64 : 32, p.maps, nsrc))) return e;
     }
     const int32_t items = (int32_t)(nrows * c->hkv * qtiles);
-    p.cta_parts = cta_parts(items, parts, nsm);
+    p.cta_parts = cta_parts(items, parts, G, nsm);
     p.ctas = (parts + p.cta_parts - 1) / p.cta_parts;
     record(17, base, nrows, nr, items, items * p.ctas, base * hd, base * hd);
     if (!dry_run())

@@ -255,3 +255,15 @@ def test_bounds_of_a_slab_have_its_shape(name, table):
     refuses("bounds of", lambda: bounds(rows=((1, 5),), b=b, segs=segs))
     longer = B.Seg(700, k_slab=FAKE, v_slab=FAKE, slab_cap=1024)
     refuses("bounds of", lambda: bounds(rows=((1, 5),), b=B.Bounds(64, FAKE, [None, Pool(8, 12, 2, 128)]), segs=[LONG, longer]))
+
+
+# ---------------------------------------------------------------- launches
+@pytest.mark.parametrize("hq,hkv,items", [(32, 8, 64), (64, 8, 64), (72, 8, 64), (128, 8, 64), (256, 8, 128), (16, 1, 8), (128, 1, 64)])
+def test_ctas_of_a_batch_are_no_more_than_the_kernel_has_on_the_gpu(hq, hkv, items):
+    """Four CTAs a SM with up to eight query heads a kv head, two with more (152 SMs here): eight lists of eight parts."""
+    with B.record_launches() as rec:
+        B.tfpa_decode_blocks(_cache(hq=hq, hkv=hkv), [LONG], FAKE, [0] * 8, list(range(4000, 4008)), Pool(8, hkv, 64, dtype=torch.int32), 64, 0.1,
+                             FAKE, stream=0)
+    most = 152 * (4 if hq // hkv <= 8 else 2)
+    ctas = max(n for n in (8, 4, 2, 1) if items * n <= most)
+    assert [(r["items"], r["grid"]) for r in rec] == [(items, items * ctas)]
