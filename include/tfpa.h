@@ -596,8 +596,11 @@ int tfpa_evict_kv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
  *                     [0, 1]; dim(n) = rot_dim ln(orig_len / (2 pi n)) /
  *                     (2 ln base), a = max(floor(dim(high)), 0),
  *                     b = min(ceil(dim(low)), rot_dim - 1)
- * The frequencies are formed in 64 bits and the angle modulo one turn to 2^-64
- * of a turn, so far positions lose nothing. */
+ * The frequencies are formed in 64 bits, and position times frequency modulo one
+ * turn is exact for the frequency as it is held.  So an angle is off by the
+ * position times the frequency's own error, which is 2^-65 of a turn and (but
+ * for a frequency of 1) a few 2^-53 of the frequency: below 10^-10 radians at
+ * position 131,072 and 10^-6 at 2^31, beside the tables' own rounding to float32. */
 enum {
   TFPA_ROPE_NONE = 0,
   TFPA_ROPE_LINEAR = 1,
@@ -696,8 +699,11 @@ int tfpa_key_bounds(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
  * which (k_scale above 0) no sum of the heads' scores with a key of the block
  * exceeds, k_scale and softmax_scale left out; ties go to
  * the lower block, and a score that is not a number (an infinite bound under a
- * zero of q) counts as larger than an infinite one.  The choice is that of exact arithmetic: scores
- * too near the border for float32 are taken in 64 bits.
+ * zero of q) counts as larger than an infinite one.  Scores too near the border
+ * for float32 are taken in float64, every block's sum in the same order: off by
+ * (14 + query heads a kv head) * 2^-53 of the sum of its terms' magnitudes at
+ * most, so the choice is that of exact arithmetic but between blocks whose scores
+ * are nearer than that (equal bounds give equal scores).
  *   q      : DEVICE bf16 [rows][hq][128], 16-byte aligned (as tfpa_decode's)
  *   blocks : DEVICE int32 [rows][hkv][nsel], written: block numbers ascending,
  *            -1 behind the last where there are fewer than nsel.

@@ -4,8 +4,8 @@
 // Tables.  cos and sin of position t and frequency f are those of the
 // fraction of a turn t f / 2 pi mod 1.  f / 2 pi is kept as a fraction of
 // 2^64, so the product modulo one turn is a 64-bit integer product that
-// wraps: exact for any position, where an angle in float32 would have lost
-// its low bits and one in float64 costs its slow sine.  The fraction is
+// wraps: exact for the fraction as it is kept, at any position, where an angle in
+// float32 would have lost its low bits and one in float64 costs its slow sine.  The fraction is
 // taken to within an eighth of a turn of a quarter turn (its top bits) and
 // only then rounded to float32.  Bound by the stores, 8 bytes an entry: 131,072
 // positions of 64 frequencies (67 MB) in 11.5 us, 5.8 TB/s, the integer pipe close

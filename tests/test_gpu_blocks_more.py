@@ -51,7 +51,7 @@ def test_scores_that_64_bits_cannot_tell(n):
         e[i] = rng.permutation([big, -big, 2 * big, -2 * big, *(rng.integers(1, 9, 4) / 8.0)])
         b.pool[at[i][0], 0, at[i][1], 1, :8] = torch.from_numpy(e[i]).to(torch.bfloat16)
     exact = [sum(Fraction(float(x)) for x in row) for row in e]
-    off = [270 * Fraction(1, 2 ** 53) * sum(abs(Fraction(float(x))) for x in row) for row in e]
+    off = [(14 + 1) * Fraction(1, 2 ** 53) * sum(abs(Fraction(float(x))) for x in row) for row in e]
     for nsel in (1, 10, 40):
         got = selected(c, b, q, [0], [64 * n - 1], nsel)[0, 0]
         assert (got >= 0).all() and (np.diff(got) > 0).all()
