@@ -670,7 +670,8 @@ int tfpa_write_qkv(const tfpa_cache* cache, const tfpa_seg* segs, int32_t nseg,
  * as the stored value without k_scale (exact in bf16 for every cache type; a
  * NaN counts as 0).  Bounds go with the pages: streams that share a page share
  * its bounds (a block that one of them ends in is then taken up to the end of
- * the one whose rows were called last: of two in one call, either).  A call that
+ * the one whose rows were called last: of two in one call either, or some of
+ * both).  A call that
  * stores, moves or restores keys leaves them as they are: tfpa_key_bounds brings
  * them up to date. */
 typedef struct {

@@ -319,6 +319,7 @@ def _i32(a) -> np.ndarray:
 
 class _Cached:
     """Keeps the C struct of a dataclass until one of its fields is assigned."""
+    _cs = None
 
     def __setattr__(self, k, v):
         object.__setattr__(self, k, v)
@@ -326,7 +327,7 @@ class _Cached:
             object.__setattr__(self, "_cs", None)
 
     def c(self):
-        cs = self.__dict__.get("_cs")
+        cs = self._cs
         if cs is None:
             cs = self._make_c()
             object.__setattr__(self, "_cs", cs)
@@ -707,42 +708,42 @@ _OP_ROPE_TABLE, _OP_WRITE_QKV, _OP_KEY_BOUNDS, _OP_SELECT_BLOCKS, _OP_DECODE_BLO
 _INT32 = np.dtype(np.int32)
 
 
-def _row_ptr(a):
-    """A row table as int32 (kept until the call is over) and its address."""
-    if type(a) is np.ndarray and a.dtype is _INT32:
-        try:
-            return a, _addressof(_c_char.from_buffer(a))     # (refuses what is not contiguous)
-        except (TypeError, ValueError, BufferError):
-            pass
-    a = _i32(a)
-    return a, _np_ptr(a)
-
-
 def _rows(row_seg, row_pos):
-    rs, sp = _row_ptr(row_seg)
-    rp, pp = _row_ptr(row_pos)
-    rows = len(rs)
-    if len(rp) != rows:
+    """Rows, the row tables' addresses, and what has to live until the call is over."""
+    try:
+        if row_seg.dtype is _INT32 and row_pos.dtype is _INT32:
+            # (refuses what is not contiguous)
+            sp = _addressof(_c_char.from_buffer(row_seg))
+            pp = _addressof(_c_char.from_buffer(row_pos))
+        else:
+            sp = None
+    except (AttributeError, TypeError, ValueError, BufferError):
+        sp = None
+    if sp is None:
+        row_seg, row_pos = _i32(row_seg), _i32(row_pos)
+        sp, pp = _np_ptr(row_seg), _np_ptr(row_pos)
+    rows = len(row_seg)
+    if len(row_pos) != rows:
         raise ValueError("row_seg and row_pos must be of one length")
-    return rows, sp, pp, (rs, rp)
+    return rows, sp, pp, (row_seg, row_pos)
 
 
 class _Elements(dict):
     """Whether a dtype is one of those that a call's operand may have, found out once a dtype (what
     has no dtype, as an address, is taken as it is)."""
 
-    def __init__(self, *names: str):
+    def __init__(self, size: int, *names: str):
         super().__init__({None: True})
-        self.names = names
+        self.size, self.names = size, names
 
     def __missing__(self, d) -> bool:
         self[d] = ok = str(d).rpartition(".")[2] in self.names
         return ok
 
 
-_BF16 = _Elements("bfloat16", "int16", "uint16")     # or its bits
-_FLOAT32 = _Elements("float32")
-_INTS = _Elements("int32", "uint32")
+_BF16 = _Elements(2, "bfloat16", "int16", "uint16")  # or its bits
+_FLOAT32 = _Elements(4, "float32")
+_INTS = _Elements(4, "int32", "uint32")
 
 
 def _other_type(t, kind: _Elements, what: str) -> ValueError:
@@ -753,7 +754,7 @@ def _rows_ptr(t, kind: _Elements, count: int, what: str) -> int:
     """The address of an operand of ``count`` elements one after the other (or more: a buffer for
     more rows than the call has)."""
     try:
-        if kind[t.dtype] and t.numel() >= count and t.is_contiguous():
+        if kind[t.dtype] and t.nbytes >= count * kind.size and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
@@ -767,10 +768,15 @@ def _weight(t, what: str) -> int:
     """A norm weight's address."""
     if t is None:
         return 0
-    p = _rows_ptr(t, _FLOAT32, HEAD_DIM, what)
-    if type(t) is not int and hasattr(t, "numel") and t.numel() != HEAD_DIM:
-        raise ValueError(f"{what} holds {HEAD_DIM} values")
-    return p
+    try:
+        if t.nbytes == 4 * HEAD_DIM and _FLOAT32[t.dtype] and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if hasattr(t, "data_ptr"):
+        raise ValueError(f"{what} must be contiguous float32 [{HEAD_DIM}], not {t.dtype} "
+                         f"{list(t.shape)} of strides {list(t.stride())}")
+    return _ptr(t) or 0                       # an address
 
 
 def _heads(t, rows: int, heads: int, what: str) -> int:
@@ -839,7 +845,7 @@ class Bounds(_Cached):
     def c(self) -> tfpa_bounds:
         # the list may change in place: the pointers are those of its present entries
         at = None if self.slabs is None else [_ptr(s) for s in self.slabs]
-        cs = self.__dict__.get("_cs")
+        cs = self._cs
         if cs is None or cs.at != at:
             arr = None if at is None else (ctypes.c_void_p * max(1, len(at)))(*at)
             cs = tfpa_bounds(self.block, _ptr(self.pool),
@@ -851,7 +857,9 @@ class Bounds(_Cached):
     def of(self, cache: Cache, segs) -> tfpa_bounds:
         """The struct for a call, which keeps it until the call is over (another thread's call may
         put one of other entries in its place).  Tensors have to be of the shapes above."""
-        cs = self.c()
+        cs = self._cs
+        if cs is None or self.slabs is not None:
+            cs = self.c()
         if cs.fits != (cache.hkv, cache.num_pages):
             _bounds_shape(self.pool, cache.num_pages, cache.hkv, PAGE // max(1, self.block))
             cs.fits = cache.hkv, cache.num_pages

@@ -1946,13 +1946,14 @@ int32_t block_parts(int32_t block, int32_t nsel) {
 
 // Parts that a CTA takes one after the other: as few as let the launch have as many
 // CTAs a SM as the kernel is built for, four with up to eight query vectors and two
-// with more (by their registers).  A part each, two, four and eight, in us, the
-// rule's choice starred:
+// with more (by their registers; the states that wait take the fourth's shared memory
+// over bf16 and e4m3 from four parts of five to eight vectors on, and at eight parts of
+// fewer).  A part each, two, four and eight, in us, the rule's choice starred:
 //   32 lists of 2,048 keys of 8 kv heads, 4 heads each (256 items):
 //     bf16 48.6  42.8  37.2*  52.4;  e4m3 40.0  33.3  30.0*  42.3;  4 bits 40.3  33.1  30.1*  47.0
 //   8 lists of 4,096 keys of 8 kv heads (64 items), 4 heads each:
 //     bf16 26.6*  32.2  42.8  69.1;  e4m3 18.5*  23.8  30.6  46.0;  4 bits 16.4*  23.8  30.6  46.2
-//   8 heads each (three CTAs a SM fit over bf16 and e4m3): bf16 27.6*  33.3  45.7;  e4m3 19.3*  25.1  34.4
+//   8 heads each: bf16 27.6*  33.3  45.7;  e4m3 19.3*  25.1  34.4;  4 bits 17.6*  24.7  32.0
 //   16 heads each: bf16 38.0  33.0*  51.3;  e4m3 28.6  23.5*  38.2;  4 bits 28.4  23.2*  39.2
 //   32 heads each (128 items): bf16 65.1  56.4  51.9*;  e4m3 52.2  43.7  39.3*;  4 bits 54.8  45.0  40.7*
 int32_t cta_parts(int64_t items, int32_t parts, int32_t group, int nsm) {
