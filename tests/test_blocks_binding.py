@@ -267,3 +267,21 @@ def test_ctas_of_a_batch_are_no_more_than_the_kernel_has_on_the_gpu(hq, hkv, ite
     most = 152 * (4 if hq // hkv <= 8 else 2)
     ctas = max(n for n in (8, 4, 2, 1) if items * n <= most)
     assert [(r["items"], r["grid"]) for r in rec] == [(items, items * ctas)]
+
+
+def test_launches_of_more_than_64_runs_are_cut():
+    """Each launch takes 64 runs; its q, lists and output start at its first row."""
+    n, nsel = 150, 5
+    rows = [(i % 2, 3 * i) for i in range(n)]
+    rs, rp = [r[0] for r in rows], [r[1] for r in rows]
+    segs = [LONG, SLAB]
+    b = B.Bounds(64, FAKE, [None, 3 * FAKE])
+    with B.record_launches() as rec:
+        B.tfpa_key_bounds(_cache(), segs, b, rs, rp, stream=0)
+        B.tfpa_select_blocks(_cache(), segs, b, FAKE, rs, rp, Pool(n, 8, nsel, dtype=torch.int32), stream=0)
+        B.tfpa_decode_blocks(_cache(), segs, FAKE, rs, rp, Pool(n, 8, nsel, dtype=torch.int32), 64, 0.1, FAKE, stream=0)
+    cuts = ((0, 64), (64, 64), (128, 22))
+    at = [(r["kind"], r["row0"], r["rows"], r["runs"], r["items"], r["q_offset"], r["out_offset"]) for r in rec]
+    assert at == ([("key_bounds", a, k, k, 8 * k, 0, 0) for a, k in cuts]
+                  + [("select_blocks", a, k, k, 8 * k, a * 32 * 128, a * 8 * nsel) for a, k in cuts]
+                  + [("decode_blocks", a, k, k, 8 * k, a * 32 * 128, a * 32 * 128) for a, k in cuts])
