@@ -7,8 +7,8 @@
 // merge kernel.  The parts follow from the list's length alone and each has a
 // state of its own, so a row's bytes do not depend on its batch; how many of them
 // a CTA takes, one after the other, does (a CTA of few keys is mostly start and
-// end: a step with 32 rows' lists of 2,048 keys over 4 bits 68.9 us with a part
-// each, 58.8 us with four).
+// end: 32 rows' lists of 2,048 keys over 4 bits 40.3 us with a part each, 30.3 us
+// with four).
 // Per CTA:
 //   warp 4      producer: a lane a list entry looks the entry and its page up
 //               (the chain of two loads runs once a 32 entries), then blocks
@@ -23,11 +23,17 @@
 //               O^T = V^T P^T.  Each warp keeps its own softmax state.
 // What bounds it is the stream of K and V out of memory, with the start and the
 // cluster's end around it: 8 streams' lists of 4,096 bf16 keys (134 MB, a part a
-// CTA) take 26.4 us, 5.1 TB/s, one stream's 5.5 us.  With four draft rows a stream,
+// CTA) take 26.5 us, 5.1 TB/s, one stream's 5.5 us.  Over e4m3 (67 MB) they take 18.4
+// us, 3.6 TB/s, over 4 bits (38 MB) 16.5 us, 2.3 TB/s: the start and the end stay, and
+// the consumers issue in 37 and 46 % of the cycles.  With four draft rows a stream,
 // whose lists mostly name the same blocks, it is the second-level cache's reads
 // over bf16 (32 lists of 2,048 keys: 37.1 us, 7.2 TB/s) and over the narrower types
-// the consumers' instructions, most of them conversions (e4m3 29.9 us, 4 bits 30.0,
+// the consumers' instructions, most of them conversions (e4m3 30.2 us, 4 bits 30.3,
 // an instruction in 55 % of the cycles; folding the parts' states is 1.5 us of it).
+// One stream's long list is bound by its eight parts a kv head: 65,536 bf16 keys of 2
+// kv heads 109 us (16 CTAs, 0.6 TB/s), of 8 kv heads 111 us (64 CTAs, 2.4 TB/s).  The
+// kernels of several parts a CTA spill 8 to 48 bytes a thread (registers for four, or
+// two, CTAs a SM).
 #include "cluster.cuh"
 #include "common.cuh"
 #include "kvstore.cuh"
@@ -47,8 +53,8 @@ struct Cfg {
   // f16 weights, and with them the sums and the output before its division, are 2^7
   // times 2^(score - running maximum): scores pass the maximum by 2^8 at most
   // (kRescaleThreshold), so they stay below 2^15 of f16's 2^16, and what is far below
-  // the maximum keeps 7 bits more above f16's last one, 2^-24.  Weights from 2^-25 down
-  // were lost without it, though their keys counted in the sum.
+  // the maximum keeps 7 bits more above f16's last one, 2^-24.  (Without them weights
+  // from 2^-25 down would be lost, while their keys count in the sum.)
   static constexpr float kWeightLog2 = kF16 ? 7.f : 0.f;
   static constexpr int kStageKeys = KV == kKvBf16 ? 32 : 64;
   static constexpr int kStageWarps = kStageKeys / 16;  // consumer warps that read a stage

@@ -5,8 +5,8 @@
 // fraction of a turn t f / 2 pi mod 1.  f / 2 pi is kept as a fraction of
 // 2^64, so the product modulo one turn is a 64-bit integer product that
 // wraps: exact for the fraction as it is kept, at any position, where an angle in
-// float32 would have lost its low bits and one in float64 costs its slow sine.  The fraction is
-// taken to within an eighth of a turn of a quarter turn (its top bits) and
+// float32 would have lost its low bits and one in float64 costs its slow sine.  The
+// fraction is taken to within an eighth of a turn of a quarter turn (its top bits) and
 // only then rounded to float32.  Bound by the stores, 8 bytes an entry: 131,072
 // positions of 64 frequencies (67 MB) in 11.5 us, 5.8 TB/s, the integer pipe close
 // behind (five instructions an entry more, for the signs, cost 0.7 us).
@@ -20,7 +20,10 @@
 // its own, so that the stored codes are a function of the inputs alone.  Bound by a
 // warp's chain from its loads over the root to its stores, and by how many such
 // chains the registers of 16 warps a SM allow: 4,096 rows of 32, 8 and 8 heads over
-// bf16 (103 MB) in 25.5 us, 4.0 TB/s; eight rows in 2.8 us, two latencies.
+// bf16 (103 MB) in 25.6 us, 4.0 TB/s; over e4m3 (94 MB) and 4 bits (91 MB) in 29 us,
+// 3.2 TB/s, for a quarter and a third more instructions (issue 59 and 61 %); 2,044 rows
+// over 4 bits (45 MB, neighbouring dims, no norm) in 14.8 us; eight rows in 2.8 us (e4m3
+// and 4 bits 3.4), two latencies.
 // (No read-only loads in these kernels and the block kernels: they may start
 // while the kernel before them still writes what they will read.)
 #include <cuda_fp8.h>
